@@ -26,6 +26,10 @@ DG_DEBUG_DROP_ONE_LOAD = 1
 DG_DEBUG_PRINT_CONFIGS = 2
 DG_DEBUG_SINGLE_CTA = 4
 DG_DEBUG_WIDE_PAIR = 8
+DG_LOGITS_F32 = 0
+DG_LOGITS_BF16 = 1
+DG_SCORE_SOFTMAX = 0
+DG_SCORE_SIGMOID = 1
 
 # Every symbol include/dg.h declares.
 EXPORTS = (
@@ -37,6 +41,8 @@ EXPORTS = (
     "dg_m_grouped_fp8_gemm_nt_masked", "dg_get_mk_alignment_for_contiguous_layout",
     "dg_get_tma_aligned_size", "dg_packed_sf_words", "dg_set_num_sms", "dg_get_num_sms",
     "dg_set_wait_timeout_ms", "dg_set_debug_flags", "dg_status_string", "dg_get_last_config",
+    "dg_bf16_fp4_gemv_nt", "dg_bf16_fp8_gemv_nt", "dg_bf16_fp4_gemv_nt_f32", "dg_bf16_fp8_gemv_nt_f32",
+    "dg_moe_route", "dg_moe_layer_workspace_bytes", "dg_moe_fp4_layer", "dg_moe_fp8_layer",
 )
 
 
@@ -94,6 +100,19 @@ def lib():
                       "dg_fp8_gemm_tt", "dg_transform_sf",
                       "dg_m_grouped_fp8_gemm_nt_contiguous",
                       "dg_m_grouped_fp8_gemm_nt_contiguous_psum", "dg_m_grouped_fp8_gemm_nt_masked"):
+                getattr(L, f).restype = i32
+            f32 = ctypes.c_float
+            for f in ("dg_bf16_fp4_gemv_nt", "dg_bf16_fp8_gemv_nt", "dg_bf16_fp4_gemv_nt_f32",
+                      "dg_bf16_fp8_gemv_nt_f32"):
+                getattr(L, f).argtypes = [P, i64, P, i64, P, P, i64, P, i64, i32, i32, i32, P, P]
+                getattr(L, f).restype = i32
+            L.dg_moe_route.argtypes = [P, i64, i32, P, P, P, i32, i32, i32, i32, i32, f32, P]
+            L.dg_moe_route.restype = i32
+            L.dg_moe_layer_workspace_bytes.argtypes = [i32, i32, i32]
+            L.dg_moe_layer_workspace_bytes.restype = i64
+            for f in ("dg_moe_fp4_layer", "dg_moe_fp8_layer"):
+                getattr(L, f).argtypes = [P, i64, P, P, P, P, P, P, P, i64, P, i64, i32, i32, i32, i32, i32, P, i64,
+                                          P, P]
                 getattr(L, f).restype = i32
             L.dg_get_mk_alignment_for_contiguous_layout.restype = i32
             L.dg_get_mk_alignment_for_contiguous_layout.argtypes = []
@@ -412,3 +431,115 @@ def dg_m_grouped_fp8_gemm_nt_masked(a, sfa, b, sfb, d, masked_m, expected_m: int
         _p(a), _p(sfa), _sf_fmt(sfa), _p(b), _p(sfb), _sf_fmt(sfb), _p(d), _p(masked_m), E, max_m,
         expected_m, N, K, _p(status), _stream(stream)))
     return d
+
+
+# --------------------------------------------------------------------- decode: few rows, routing, the MoE layer
+
+def _ld(t) -> int:
+    """Row stride in elements; a single row's own length where its stride says nothing."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _gemv(fn: str, fp4: bool, dtype, a, b, sfb, d, c, status, stream):
+    m, k = a.shape
+    n = b.shape[0]
+    assert a.dtype == torch.bfloat16 and b.dtype == (torch.uint8 if fp4 else torch.float8_e4m3fn)
+    assert sfb.dtype == torch.int32 and sfb.is_contiguous()
+    assert b.shape[1] == (k // 2 if fp4 else k) and sfb.numel() >= (-(-k // (128 if fp4 else 512))) * ((n + 3) // 4 * 4)
+    assert d.dtype == dtype and d.shape == (m, n) and a.stride(1) == 1 and b.stride(1) == 1 and d.stride(1) == 1
+    assert c is None or (c.dtype == dtype and c.shape == d.shape and c.stride(1) == 1)
+    _check(fn, getattr(lib(), fn)(
+        _p(a), _ld(a), _p(b), _ld(b), _p(sfb), _p(c), 0 if c is None else _ld(c), _p(d), _ld(d),
+        m, n, k, _p(status), _stream(stream)))
+    return d
+
+
+def dg_bf16_fp4_gemv_nt(a, b, sfb, d, c=None, status=None, stream=None):
+    """D = C + A @ B^T for 1..64 rows: a bf16 [M, K]; b uint8 [N, K/2], two E2M1 codes
+    per byte (even k in the low nibble); sfb packed int32 [K/128, align4(N)] (4 x 32
+    K per word); d (and c) bf16 [M, N]."""
+    return _gemv("dg_bf16_fp4_gemv_nt", True, torch.bfloat16, a, b, sfb, d, c, status, stream)
+
+
+def dg_bf16_fp8_gemv_nt(a, b, sfb, d, c=None, status=None, stream=None):
+    """As dg_bf16_fp4_gemv_nt with b float8_e4m3fn [N, K] and sfb packed int32
+    [ceil(K/512), align4(N)] (4 x 128 K per word)."""
+    return _gemv("dg_bf16_fp8_gemv_nt", False, torch.bfloat16, a, b, sfb, d, c, status, stream)
+
+
+def dg_bf16_fp4_gemv_nt_f32(a, b, sfb, d, c=None, status=None, stream=None):
+    """dg_bf16_fp4_gemv_nt with FP32 d (and c)."""
+    return _gemv("dg_bf16_fp4_gemv_nt_f32", True, torch.float32, a, b, sfb, d, c, status, stream)
+
+
+def dg_bf16_fp8_gemv_nt_f32(a, b, sfb, d, c=None, status=None, stream=None):
+    """dg_bf16_fp8_gemv_nt with FP32 d (and c)."""
+    return _gemv("dg_bf16_fp8_gemv_nt_f32", False, torch.float32, a, b, sfb, d, c, status, stream)
+
+
+def dg_moe_route(logits, ids, weights, bias=None, scoring: str = "softmax", renormalize: bool = True,
+                 scale: float = 1.0, stream=None):
+    """Top-k routing: logits [T, E] float32 or bfloat16 (unit column stride) -> ids int32
+    [T, topk] and weights float32 [T, topk] (both contiguous); bias float32 [E]
+    shifts the choice only.  scoring "softmax" or "sigmoid"."""
+    t, e = logits.shape
+    topk = ids.shape[1]
+    assert logits.dtype in (torch.float32, torch.bfloat16) and (logits.stride(1) == 1 or e == 1)
+    assert ids.dtype == torch.int32 and ids.shape == (t, topk) and ids.is_contiguous()
+    assert weights.dtype == torch.float32 and weights.shape == ids.shape and weights.is_contiguous()
+    assert bias is None or (bias.dtype == torch.float32 and bias.shape == (e,) and bias.is_contiguous())
+    assert scoring in ("softmax", "sigmoid")
+    _check("dg_moe_route", lib().dg_moe_route(
+        _p(logits), _ld(logits), DG_LOGITS_F32 if logits.dtype == torch.float32 else DG_LOGITS_BF16,
+        _p(bias), _p(ids), _p(weights), t, e, topk, DG_SCORE_SIGMOID if scoring == "sigmoid" else DG_SCORE_SOFTMAX,
+        int(renormalize), scale, _stream(stream)))
+    return ids, weights
+
+
+def moe_layer_workspace_bytes(t: int, topk: int, i: int) -> int:
+    return int(lib().dg_moe_layer_workspace_bytes(t, topk, i))
+
+
+def _moe_layer(fn: str, fp4: bool, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream):
+    t, h = x.shape
+    topk = ids.shape[1]
+    e, i2 = w1.shape[0], w1.shape[1]
+    i = i2 // 2
+    code = torch.uint8 if fp4 else torch.float8_e4m3fn
+    per = 2 if fp4 else 1
+    assert x.dtype == torch.bfloat16 and x.stride(1) == 1
+    assert ids.dtype == torch.int32 and ids.shape == (t, topk) and ids.is_contiguous()
+    assert weights.dtype == torch.float32 and weights.shape == ids.shape and weights.is_contiguous()
+    assert w1.dtype == code and w1.is_contiguous() and w1.shape == (e, 2 * i, h // per)
+    assert w2.dtype == code and w2.is_contiguous() and w2.shape == (e, h, i // per)
+    sl = 128 if fp4 else 512
+    assert sf1.dtype == torch.int32 and sf1.is_contiguous() and sf1.numel() >= e * -(-h // sl) * 2 * i
+    assert sf2.dtype == torch.int32 and sf2.is_contiguous() and sf2.numel() >= e * -(-i // sl) * h
+    assert y.dtype == torch.bfloat16 and y.shape == (t, h) and y.stride(1) == 1
+    assert c is None or (c.dtype == torch.bfloat16 and c.shape == (t, h) and c.stride(1) == 1)
+    if workspace is None:
+        # allocated on the current stream; a caller's other stream is made known to the allocator
+        workspace = torch.empty(max(16, t * topk * i * 4), dtype=torch.uint8, device=y.device)
+        if stream is not None and y.is_cuda:
+            stream.wait_stream(torch.cuda.current_stream())
+            workspace.record_stream(stream)
+    _check(fn, getattr(lib(), fn)(
+        _p(x), _ld(x), _p(ids), _p(weights), _p(w1), _p(sf1), _p(w2), _p(sf2), _p(c),
+        0 if c is None else _ld(c), _p(y), _ld(y), t, h, i, e, topk, _p(workspace),
+        workspace.numel() * workspace.element_size(), _p(status), _stream(stream)))
+    return y
+
+
+def dg_moe_fp4_layer(x, ids, weights, w1, sf1, w2, sf2, y, c=None, workspace=None, status=None, stream=None):
+    """y = c + sum_j weights[:, j] * W2[e] (silu(W1g[e] x) * (W1u[e] x)), e = ids[:, j] (negative:
+    empty slot), for 1..64 tokens.  x bf16 [T, H]; ids int32 and weights float32 [T, topk];
+    w1 uint8 [E, 2I, H/2] (gate rows, then up rows) and w2 uint8 [E, H, I/2], packed E2M1;
+    sf1 packed int32 [E, H/128, 2I], sf2 [E, I/128, H]; y (and c) bf16 [T, H].  workspace:
+    a device buffer of moe_layer_workspace_bytes(T, topk, I) bytes (made here if not given)."""
+    return _moe_layer("dg_moe_fp4_layer", True, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream)
+
+
+def dg_moe_fp8_layer(x, ids, weights, w1, sf1, w2, sf2, y, c=None, workspace=None, status=None, stream=None):
+    """As dg_moe_fp4_layer with float8_e4m3fn w1 [E, 2I, H] and w2 [E, H, I], and scales packed
+    4 x 128 K per word: sf1 [E, ceil(H/512), 2I], sf2 [E, ceil(I/512), H]."""
+    return _moe_layer("dg_moe_fp8_layer", False, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream)

@@ -28,10 +28,7 @@ std::mutex g_dev_mutex;
 
 // cuTensorMapEncodeTiled, reached through the runtime so that the library does
 // not link libcuda directly.
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using EncodeTiledFn = TensorMapEncodeFn;
 EncodeTiledFn g_encode = nullptr;
 std::once_flag g_encode_once;
 
@@ -520,6 +517,32 @@ dg_status check_operand_rules(const void *a, int64_t lda, const void *b, int64_t
 }
 
 }  // namespace
+
+// ------------------------------------------------------------------ shared with the other host unit
+
+dg_status host_check_device(int *num_sms) { return check_device(num_sms); }
+TensorMapEncodeFn host_encode() { return get_encode(); }
+uint64_t host_timeout_ns() { return static_cast<uint64_t>(g_timeout_ms.load()) * 1000000ull; }
+uint32_t host_take_debug_flags() {
+    const uint32_t f = g_debug_flags.load();
+    if (f & DG_DEBUG_DROP_ONE_LOAD) g_debug_flags.fetch_and(~static_cast<uint32_t>(DG_DEBUG_DROP_ONE_LOAD));
+    return f;
+}
+void host_set_last_config(int block_m, int block_n, int stages, int grid, int kind, int launches) {
+    const int v[6] = {block_m, block_n, stages, grid, kind, launches};
+    std::memcpy(g_last_config, v, sizeof(v));
+}
+cudaError_t launch_fill_d(const void *c, int64_t ldc, void *d, int64_t ldd, int m, int n, bool f32, int num_sms,
+                          cudaStream_t stream) {
+    if (f32)
+        dg_fill_d_f32_kernel<<<num_sms * 4, 256, 0, stream>>>(static_cast<const float *>(c), ldc,
+                                                              static_cast<float *>(d), ldd, m, n);
+    else
+        dg_fill_d_kernel<<<num_sms * 4, 256, 0, stream>>>(static_cast<const uint16_t *>(c), ldc,
+                                                          static_cast<uint16_t *>(d), ldd, m, n);
+    return cudaGetLastError();
+}
+
 }  // namespace dg
 
 using namespace dg;

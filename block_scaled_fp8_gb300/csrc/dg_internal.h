@@ -111,4 +111,79 @@ cudaError_t launch_transform_sf(const float *sf, int batch, int mn_rows, int sf_
                                 int mn, int out_fmt, void *out, int32_t *status,
                                 cudaStream_t stream);
 
+// Host state and helpers of api.cu that the few-row entry points (api_few.cu) share.
+typedef CUresult (*TensorMapEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                      const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                                      CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                      CUtensorMapFloatOOBfill);
+dg_status host_check_device(int *num_sms);
+TensorMapEncodeFn host_encode();
+uint64_t host_timeout_ns();
+uint32_t host_take_debug_flags();   // clears DG_DEBUG_DROP_ONE_LOAD
+void host_set_last_config(int block_m, int block_n, int stages, int grid, int kind, int launches);
+cudaError_t launch_fill_d(const void *c, int64_t ldc, void *d, int64_t ldd, int m, int n, bool f32, int num_sms,
+                          cudaStream_t stream);
+
+// ---- few-row products, top-k routing and the MoE layer for few tokens
+
+constexpr int kMaxFewRows = 64;         // rows of a few-row product, tokens of a MoE layer call
+constexpr int kMaxLayerTopk = 16;
+constexpr int kMaxLayerExperts = 1024;
+constexpr int kMaxRouteExperts = 1024;
+constexpr int kMaxRouteTopk = 32;
+
+// One few-row product D = C + A @ B^T, bf16 A, FP4 or FP8 B with packed UE8M0 scales.
+struct FewParams {
+    const uint16_t *a;      // bf16 [m][lda]
+    int64_t lda;
+    const uint8_t *b;       // codes, row n at b + n * ldb bytes
+    int64_t ldb;
+    const uint32_t *sfb;    // [slices][align4(n)]
+    const void *c;          // D's type, or nullptr
+    int64_t ldc;
+    void *d;
+    int64_t ldd;
+    int m, n, k;
+    int fp4, f32;
+    int32_t *status;
+    uint64_t timeout_ns;
+    uint32_t debug_flags;
+};
+cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream);
+
+// The MoE layer for few tokens.
+struct LayerParams {
+    const uint16_t *x;      // bf16 [t][ldx]
+    int64_t ldx;
+    const int32_t *ids;     // [t][topk]
+    const float *weights;   // [t][topk]
+    const uint8_t *w1;      // [experts][2i][h] codes: gate rows, then up rows
+    const uint32_t *sf1;
+    const uint8_t *w2;      // [experts][h][i]
+    const uint32_t *sf2;
+    const uint16_t *c;      // bf16 [t][ldc] or nullptr
+    int64_t ldc;
+    uint16_t *y;            // bf16 [t][ldy]
+    int64_t ldy;
+    float *act;             // workspace: FP32 [t * topk][i]
+    int t, h, i, experts, topk;
+    int fp4;
+    int32_t *status;
+    uint64_t timeout_ns;
+    uint32_t debug_flags;
+};
+cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t stream);
+
+struct RouteParams {
+    const void *logits;
+    int64_t ld;
+    const float *bias;
+    int32_t *ids;
+    float *weights;
+    int t, experts, topk;
+    int bf16, sigmoid, renormalize;
+    float scale;
+};
+cudaError_t launch_moe_route(const RouteParams &p, cudaStream_t stream);
+
 }  // namespace dg

@@ -37,9 +37,10 @@
  *    16; N % 8 == 0 and ldc, ldd (bf16 elements) multiples of 8.  (FP4
  *    weights, M/N-contiguous operands and FP32 outputs have their own rules,
  *    given with their calls.)
- *  - No split-K: each output element is reduced by one CTA in a fixed K
- *    order, so a row's result does not depend on M or on the other rows of
- *    the batch (batch invariance, §13.1).
+ *  - No split-K in the GEMMs: each output element is reduced by one CTA in a
+ *    fixed K order, so a row's result does not depend on M or on the other rows of
+ *    the batch (batch invariance, §13.1).  (The few-row products split K by n
+ *    and k alone, in a fixed order, and keep that property.)
  */
 #ifndef DG_GB300_H
 #define DG_GB300_H
@@ -397,6 +398,105 @@ dg_status dg_transform_sf_k_grouped_k32(const float *sf, int mn, const int *ks, 
  * if ks is invalid (see dg_k_grouped_fp8_gemm_tn_contiguous) or the count
  * exceeds 65535. */
 int64_t dg_k_grouped_packed_sf_rows(const int *ks, int num_groups);
+
+/*
+ * dg_bf16_fp4_gemv_nt / dg_bf16_fp8_gemv_nt -- products of a few bf16 rows (one
+ * to 64 tokens of a decode step) with FP4 or FP8 weights, without quantising the
+ * activations:
+ *
+ *   D[m,n] = C[m,n] + sum_k A[m,k] * B[n,k] sb(n, k/g)      g = 32 (FP4), 128 (FP8)
+ *
+ *   a    bf16 [m, lda], K contiguous, 16-byte aligned, lda a multiple of 8.
+ *   b    fp4: E2M1 codes packed two per byte as for dg_fp8_fp4_gemm_nt (row n at
+ *        b + n*ldb BYTES; 32-byte aligned, ldb >= k/2 and a multiple of 32).
+ *        fp8: E4M3 [n, ldb] (16-byte aligned, ldb >= k and a multiple of 16).
+ *   sfb  packed UE8M0 int32, 16-byte aligned: fp4 [k/128][align4(n)], one byte per
+ *        32 K; fp8 [ceil(k/512)][align4(n)], one byte per 128 K (both as for
+ *        the GEMMs, from dg_transform_sf).
+ *   c    [m, ldc] of D's type or NULL; may equal d (in-place accumulate).
+ *   d    [m, ldd] bf16, or FP32 in the _f32 forms (no rounding after the sum).
+ *        c and d 16-byte aligned, ldc and ldd multiples of 8 (FP32: 4).
+ *   0 <= m <= 64 (else DG_ERR_UNSUPPORTED: use the GEMMs), n a multiple of 8, k a
+ *   multiple of 128.  m == 0 or n == 0 is a no-op; k == 0 gives D = C (or 0).
+ *   A row that holds an infinity or a NaN gives NaN in its row of D; other rows
+ *   are not affected.  Row i of D is the same bit for bit whatever m is.
+ */
+dg_status dg_bf16_fp4_gemv_nt(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
+                              const void *c, int64_t ldc, void *d, int64_t ldd, int m, int n, int k,
+                              int32_t *status_dev, void *stream);
+dg_status dg_bf16_fp8_gemv_nt(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
+                              const void *c, int64_t ldc, void *d, int64_t ldd, int m, int n, int k,
+                              int32_t *status_dev, void *stream);
+dg_status dg_bf16_fp4_gemv_nt_f32(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
+                                  const float *c, int64_t ldc, float *d, int64_t ldd, int m, int n, int k,
+                                  int32_t *status_dev, void *stream);
+dg_status dg_bf16_fp8_gemv_nt_f32(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
+                                  const float *c, int64_t ldc, float *d, int64_t ldd, int m, int n, int k,
+                                  int32_t *status_dev, void *stream);
+
+/*
+ * dg_moe_route -- top-k routing of tokens to experts.  For each token, with
+ * logits l and scores s = softmax(l) or sigmoid(l), the topk experts with the
+ * largest key are chosen, in the order of their keys, ties to the lowest index:
+ *
+ *   key = l (softmax, which has the order of s) or s (sigmoid), with a bias s + bias
+ *   weights[t][j] = scale * s[ids[t][j]]  ( / sum over the chosen s, if renormalize)
+ *
+ *   logits  [t, ld] FP32 (DG_LOGITS_F32) or bf16 (DG_LOGITS_BF16), experts contiguous.
+ *   bias    FP32 [experts] or NULL: shifts the choice only, never the weights.
+ *   ids, weights   int32 and FP32 [t][topk], as dg_moe_fp4_layer takes them.
+ *   A logit of -infinity or NaN (and a key that is NaN) is never chosen; where
+ *   fewer than topk experts are left, the remaining slots get id -1 and weight 0.
+ *   A sum of chosen scores below the smallest normal FP32 counts as that value.
+ *   1 <= experts <= 1024 and 1 <= topk <= min(experts, 32), else DG_ERR_UNSUPPORTED
+ *   (DG_ERR_INVALID_ARG below 1 or topk > experts); t == 0 is a no-op.
+ */
+typedef enum { DG_LOGITS_F32 = 0, DG_LOGITS_BF16 = 1 } dg_logits_format;
+typedef enum { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 } dg_score;
+dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const float *bias, int32_t *ids,
+                       float *weights, int t, int experts, int topk, int scoring, int renormalize, float scale,
+                       void *stream);
+
+/*
+ * dg_moe_fp4_layer / dg_moe_fp8_layer -- a whole mixture-of-experts layer for a
+ * few tokens (a decode step), from bf16 activations and the routing to bf16 output,
+ * in two kernels.  With e = ids[t][j]:
+ *
+ *   h(t,j)[i] = silu(sum_k W1[e][i][k] x[t][k]) * (sum_k W1[e][I + i][k] x[t][k])
+ *   y[t][n]   = c[t][n] + sum_j weights[t][j] * sum_i W2[e][n][i] h(t,j)[i]
+ *
+ *   x     bf16 [t, ldx], 16-byte aligned, ldx a multiple of 8.
+ *   ids   int32 [t][topk], weights FP32 [t][topk], both dense.  A negative id is an
+ *         empty slot (its weight is not read, so it may hold anything); an id >=
+ *         experts counts as empty and sets DG_DEV_BAD_GROUP.  A token that names an
+ *         expert twice gets it with the sum of the two weights; a token with
+ *         no expert left gets y = c (or 0).
+ *   w1, sf1   [experts][2*i][h] codes (rows 0..i-1 gate, i..2i-1 up) and their
+ *         packed scales [experts][slices][2*i]; w2, sf2  [experts][h][i] and
+ *         [experts][slices][h]; dense, laid out as for the grouped GEMMs: fp4
+ *         packed E2M1 with one scale per 32 K (slices = K/128; 32-byte aligned), fp8
+ *         E4M3 with one per 128 K (slices = ceil(K/512); 16-byte aligned).
+ *   c     bf16 [t, ldc] or NULL, may equal y; y bf16 [t, ldy]; 16-byte aligned,
+ *         strides multiples of 8.
+ *   workspace   device memory, 16-byte aligned, dg_moe_layer_workspace_bytes(t,
+ *         topk, i) bytes; its contents need no initialisation and do not outlive
+ *         the call.  Calls that may run at the same time need one each.
+ *   h and i multiples of 128 (DG_ERR_ALIGNMENT); t <= 64, topk <= 16 and experts <=
+ *   1024, else DG_ERR_UNSUPPORTED (more tokens: dg_m_grouped_*); t == 0 or h == 0
+ *   is a no-op, i == 0 gives y = c (or 0).
+ *   Only the rows of experts that some token names are read.  A token whose x
+ *   holds an infinity or a NaN gets NaN; the weights and scales of the named
+ *   experts must be finite (a NaN there may reach every token of the call).
+ */
+int64_t dg_moe_layer_workspace_bytes(int t, int topk, int i);
+dg_status dg_moe_fp4_layer(const void *x, int64_t ldx, const int32_t *ids, const float *weights, const void *w1,
+                           const void *sf1, const void *w2, const void *sf2, const void *c, int64_t ldc, void *y,
+                           int64_t ldy, int t, int h, int i, int experts, int topk, void *workspace,
+                           int64_t workspace_bytes, int32_t *status_dev, void *stream);
+dg_status dg_moe_fp8_layer(const void *x, int64_t ldx, const int32_t *ids, const float *weights, const void *w1,
+                           const void *sf1, const void *w2, const void *sf2, const void *c, int64_t ldc, void *y,
+                           int64_t ldy, int t, int h, int i, int experts, int topk, void *workspace,
+                           int64_t workspace_bytes, int32_t *status_dev, void *stream);
 
 /* Number of SMs the persistent kernels use (default: all SMs of the current
  * device).  n <= 0 restores the default. */
