@@ -1,155 +1,161 @@
-// Few-row products and the MoE layer for few tokens: plain CUDA-core kernels, one
-// warp per row of weights, FP32 sums.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
+// Launches of the few-row kernel (few_rows.cuh): tile and split choice, tensor maps.
+#include "few_rows.cuh"
 
-#include "dg_internal.h"
-#include "ptx.cuh"
+#include <cstdlib>
 
 namespace dg {
 namespace {
 
-constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr int kMaxSplit = 8;        // portable cluster size
+constexpr int kSmemOne = 232448 - 1024, kSmemTwo = 114000;   // bytes for one or two CTAs on an SM
 
-__device__ __forceinline__ float scale_of(uint32_t byte) {   // 2^(byte - 127)
-    return byte == 0 ? __uint_as_float(0x00400000u) : byte == 255 ? __uint_as_float(0x7FFFFFFFu)
-                                                                  : __uint_as_float(byte << 23);
+int cdiv(int a, int b) { return (a + b - 1) / b; }
+int pow2_at_least(int v) {
+    int p = 32;
+    while (p < v) p *= 2;
+    return p;
+}
+int env(const char *n, int d) { const char *e = std::getenv(n); return e ? std::atoi(e) : d; }
+
+// Rows of weights seen as [rows / 4][4]: weight row 4l + c lands in operand row 32c + l.
+bool encode_weights(CUtensorMap *map, bool fp4, const void *base, int64_t rows, int64_t ld_bytes, int k) {
+    const TensorMapEncodeFn enc = host_encode();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows / 4), 4};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(4 * ld_bytes), static_cast<cuuint64_t>(ld_bytes)};
+    const cuuint32_t box[3] = {128, 32, 4};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return enc(map, fp4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+               const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-__device__ __forceinline__ float e2m1(uint32_t c) {
-    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-    const float v = e == 0 ? 0.5f * m : __uint_as_float(((e + 126u) << 23) | (m << 22));
-    return c & 8u ? -v : v;
-}
-
-// Weights k..k+3 of one row, without their scale.
-template <bool FP4>
-__device__ __forceinline__ void load4(const uint8_t *row, int k, float (&w)[4]) {
-    if constexpr (FP4) {
-        const uint32_t c = *reinterpret_cast<const uint16_t *>(row + k / 2);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = e2m1((c >> (4 * j)) & 15u);
-    } else {
-        const uint32_t c = *reinterpret_cast<const uint32_t *>(row + k);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = __half2float(__half(__nv_cvt_fp8_to_halfraw((c >> (8 * j)) & 255u, __NV_E4M3)));
+// Cluster size for `tiles` CTA tiles of `kblocks` K-blocks each: the least number of
+// K-blocks on the busiest SM, where a CTA costs `fixed` K-blocks beside its own.
+int choose_split(int tiles, int kblocks, int num_sms, int fixed) {
+    int best = 1;
+    int64_t best_cost = -1;
+    for (int s = 1; s <= kMaxSplit && s <= kblocks; ++s) {
+        const int64_t cost = static_cast<int64_t>(cdiv(tiles * s, num_sms)) * (cdiv(kblocks, s) + fixed);
+        if (best_cost < 0 || cost < best_cost) { best = s; best_cost = cost; }
     }
+    return best;
 }
 
-// Scale of weights k.. of one row; sf points at the row's word of slice 0, ld words per slice.
-template <bool FP4>
-__device__ __forceinline__ float scale_at(const uint32_t *sf, int64_t ld, int k) {
-    const int g = FP4 ? k / 32 : k / 128;
-    return scale_of((sf[(g >> 2) * ld] >> (8 * (g & 3))) & 255u);
+template <bool FP4, int HALVES, int MODE>
+cudaError_t launch(const CUtensorMap &map, FewArgs &a, int tiles, int split, int gy, int gz, cudaStream_t stream) {
+    const int pairs = MODE == kGemv ? 0 : a.tokens * a.topk;
+    const int fixed = FewConfig::smem_bytes(HALVES, a.cap, 0, MODE, pairs);
+    const int stage = FewConfig::stage_bytes(HALVES, a.cap);
+    int stages = (kSmemTwo - fixed) / stage;
+    if (stages < env("DG_FEW_MIN2", 3)) stages = (kSmemOne - fixed) / stage;
+    if (stages > FewConfig::kMaxStages) stages = FewConfig::kMaxStages;
+    a.stages = stages;
+    a.tmem_cols = pow2_at_least(HALVES * 2 * a.cap + 2 * (4 * HALVES + 4));
+    const int smem = FewConfig::smem_bytes(HALVES, a.cap, stages, MODE, pairs);
+    auto kernel = dg_few_rows_kernel<FP4, HALVES, MODE>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(gy), static_cast<unsigned>(gz));
+    cfg.blockDim = dim3(FewConfig::kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    host_set_last_config(HALVES * 128, 2 * a.cap, stages, tiles * split * gy * gz, 3 + MODE, MODE == kDown ? 2 : 1);
+    return cudaLaunchKernelEx(&cfg, kernel, map, a);
 }
 
-// sum_k w[k] x[k] over the warp (x: bf16 or FP32)
-template <bool FP4, typename X>
-__device__ __forceinline__ float dot(const uint8_t *row, const uint32_t *sf, int64_t ld, const X *x, int k, int lane) {
-    float acc = 0.0f;
-    for (int i = lane * 4; i < k; i += 128) {
-        float w[4];
-        load4<FP4>(row, i, w);
-        float part = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float v = static_cast<float>(x[i + j]);
-            part += w[j] * v + (v - v);   // a non-finite activation gives NaN, whatever its weight
-        }
-        acc += part * scale_at<FP4>(sf, ld, i);
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) acc += __shfl_xor_sync(kFull, acc, s);
-    return acc;
+template <int HALVES, int MODE>
+cudaError_t launch_fmt(bool fp4, const CUtensorMap &map, FewArgs &a, int tiles, int split, int gy, int gz,
+                       cudaStream_t stream) {
+    return fp4 ? launch<true, HALVES, MODE>(map, a, tiles, split, gy, gz, stream)
+               : launch<false, HALVES, MODE>(map, a, tiles, split, gy, gz, stream);
 }
 
-template <bool FP4, bool F32>
-__global__ void __launch_bounds__(256) dg_few_gemv_kernel(const FewParams p) {
-    grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int n = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (n >= p.n) return;
-    for (int m = 0; m < p.m; ++m) {
-        float v = dot<FP4>(p.b + n * p.ldb, p.sfb + n, (p.n + 3) / 4 * 4,
-                           reinterpret_cast<const __nv_bfloat16 *>(p.a + m * p.lda), p.k, lane);
-        if (lane != 0) continue;
-        if constexpr (F32) {
-            if (p.c) v += static_cast<const float *>(p.c)[m * p.ldc + n];
-            static_cast<float *>(p.d)[m * p.ldd + n] = v;
-        } else {
-            if (p.c) v += static_cast<float>(static_cast<const __nv_bfloat16 *>(p.c)[m * p.ldc + n]);
-            static_cast<__nv_bfloat16 *>(p.d)[m * p.ldd + n] = __float2bfloat16_rn(v);
-        }
-    }
-}
-
-template <bool FP4>
-__global__ void __launch_bounds__(256) dg_moe_up_kernel(const LayerParams p) {
-    grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int j = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int pair = blockIdx.y;
-    const int e = p.ids[pair];
-    if (e >= p.experts && p.status && threadIdx.x == 0) atomicOr(p.status, DG_DEV_BAD_GROUP);
-    if (j >= p.i || e < 0 || e >= p.experts) return;
-    const int64_t row_bytes = FP4 ? p.h / 2 : p.h;
-    const int64_t slices = FP4 ? p.h / 128 : (p.h + 511) / 512;
-    const int64_t ld = 2 * p.i;
-    const uint8_t *w = p.w1 + e * ld * row_bytes;
-    const uint32_t *sf = p.sf1 + e * slices * ld;
-    const __nv_bfloat16 *x = reinterpret_cast<const __nv_bfloat16 *>(p.x + pair / p.topk * p.ldx);
-    const float g = dot<FP4>(w + j * row_bytes, sf + j, ld, x, p.h, lane);
-    const float u = dot<FP4>(w + (p.i + j) * row_bytes, sf + p.i + j, ld, x, p.h, lane);
-    if (lane == 0) p.act[static_cast<int64_t>(pair) * p.i + j] = g / (1.0f + expf(-g)) * u;
-}
-
-template <bool FP4>
-__global__ void __launch_bounds__(256) dg_moe_down_kernel(const LayerParams p) {
-    grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int n = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int t = blockIdx.y;
-    if (n >= p.h) return;
-    const int64_t row_bytes = FP4 ? p.i / 2 : p.i;
-    const int64_t slices = FP4 ? p.i / 128 : (p.i + 511) / 512;
-    float y = p.c ? static_cast<float>(reinterpret_cast<const __nv_bfloat16 *>(p.c)[t * p.ldc + n]) : 0.0f;
-    for (int j = 0; j < p.topk; ++j) {
-        const int pair = t * p.topk + j;
-        const int e = p.ids[pair];
-        if (e < 0 || e >= p.experts) continue;
-        y += p.weights[pair] * dot<FP4>(p.w2 + (static_cast<int64_t>(e) * p.h + n) * row_bytes,
-                                        p.sf2 + e * slices * p.h + n, p.h,
-                                        p.act + static_cast<int64_t>(pair) * p.i, p.i, lane);
-    }
-    if (lane == 0) reinterpret_cast<__nv_bfloat16 *>(p.y)[t * p.ldy + n] = __float2bfloat16_rn(y);
-}
+int capacity(int tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
 
 }  // namespace
 
 cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream) {
-    const dim3 grid((p.n + 7) / 8);
-    if (p.fp4)
-        p.f32 ? dg_few_gemv_kernel<true, true><<<grid, 256, 0, stream>>>(p)
-              : dg_few_gemv_kernel<true, false><<<grid, 256, 0, stream>>>(p);
-    else
-        p.f32 ? dg_few_gemv_kernel<false, true><<<grid, 256, 0, stream>>>(p)
-              : dg_few_gemv_kernel<false, false><<<grid, 256, 0, stream>>>(p);
-    host_set_last_config(1, 8, 1, static_cast<int>(grid.x), 3, 1);
-    return cudaGetLastError();
+    CUtensorMap map;
+    if (!encode_weights(&map, p.fp4, p.b, p.n, p.ldb, p.k)) return cudaErrorInvalidValue;
+    FewArgs a = {};
+    a.x = p.a;
+    a.ldx = p.lda;
+    a.sf = p.sfb;
+    a.sf_ld = cdiv(p.n, 4) * 4;
+    a.rows = p.n;
+    a.tokens = p.m;
+    a.kblocks = p.k / 128;
+    a.cap = capacity(p.m);
+    a.c = p.c;
+    a.ldc = p.ldc;
+    a.d = p.d;
+    a.ldd = p.ldd;
+    a.f32 = p.f32;
+    a.status = p.status;
+    a.timeout_ns = p.timeout_ns;
+    a.debug_flags = p.debug_flags;
+    const int split = env("DG_FEW_SPLIT", choose_split(cdiv(p.n, 128), a.kblocks, num_sms, env("DG_FEW_FIXED", 2)));
+    if (p.m <= env("DG_FEW_M1", 16)) return launch_fmt<1, kGemv>(p.fp4, map, a, cdiv(p.n, 128), split, 1, 1, stream);
+    return launch_fmt<2, kGemv>(p.fp4, map, a, cdiv(p.n, 256), split, 1, 1, stream);
 }
 
 cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t stream) {
-    const dim3 up((p.i + 7) / 8, p.t * p.topk), down((p.h + 7) / 8, p.t);
-    if (p.fp4) {
-        dg_moe_up_kernel<true><<<up, 256, 0, stream>>>(p);
-        dg_moe_down_kernel<true><<<down, 256, 0, stream>>>(p);
-    } else {
-        dg_moe_up_kernel<false><<<up, 256, 0, stream>>>(p);
-        dg_moe_down_kernel<false><<<down, 256, 0, stream>>>(p);
-    }
-    host_set_last_config(1, 8, 1, static_cast<int>(up.x * up.y), 4, 2);
-    return cudaGetLastError();
+    CUtensorMap map1, map2;
+    const int64_t per = p.fp4 ? 2 : 1;
+    if (!encode_weights(&map1, p.fp4, p.w1, static_cast<int64_t>(p.experts) * 2 * p.i, p.h / per, p.h) ||
+        !encode_weights(&map2, p.fp4, p.w2, static_cast<int64_t>(p.experts) * p.h, p.i / per, p.i))
+        return cudaErrorInvalidValue;
+    FewArgs a = {};
+    a.x = p.x;
+    a.ldx = p.ldx;
+    a.act = p.act;
+    a.tokens = p.t;
+    a.ids = p.ids;
+    a.weights = p.weights;
+    a.experts = p.experts;
+    a.topk = p.topk;
+    a.inner = p.i;
+    a.status = p.status;
+    a.timeout_ns = p.timeout_ns;
+    a.debug_flags = p.debug_flags;
+    // up: one grid row per expert that can be in use, one CTA tile per 128 columns of h
+    const int most = p.t * p.topk < p.experts ? p.t * p.topk : p.experts;
+    a.sf = p.sf1;
+    a.sf_ld = 2 * p.i;
+    a.sf_expert = static_cast<int64_t>(p.fp4 ? p.h / 128 : cdiv(p.h, 512)) * a.sf_ld;
+    a.rows = 2 * p.i;
+    a.kblocks = p.h / 128;
+    a.cap = capacity(p.t < 2 * p.t * p.topk / p.experts + 4 ? p.t : 2 * p.t * p.topk / p.experts + 4);
+    const int up_tiles = p.i / 128;
+    const int up_split = env("DG_UP_SPLIT", choose_split(up_tiles * most, a.kblocks, num_sms, 2));
+    cudaError_t e = launch_fmt<2, kUp>(p.fp4, map1, a, up_tiles, up_split, most, cdiv(p.t, a.cap), stream);
+    if (e != cudaSuccess) return e;
+    // down: K runs over the active experts
+    a.sf = p.sf2;
+    a.sf_ld = p.h;
+    a.sf_expert = static_cast<int64_t>(p.fp4 ? p.i / 128 : cdiv(p.i, 512)) * a.sf_ld;
+    a.rows = p.h;
+    a.kblocks = p.i / 128;
+    a.cap = capacity(p.t);
+    a.c = p.c;
+    a.ldc = p.ldc;
+    a.d = p.y;
+    a.ldd = p.ldy;
+    a.debug_flags = 0;
+    const int tiles = p.h / 128;
+    const int split = env("DG_DOWN_SPLIT", choose_split(tiles, a.kblocks * most, num_sms, 2));
+    return launch_fmt<1, kDown>(p.fp4, map2, a, tiles, split, 1, 1, stream);
 }
 
 }  // namespace dg

@@ -533,7 +533,7 @@ const char *dg_status_string(int status);
 /* Tile configuration the last GEMM call on this thread launched:
  * out[0]=BLOCK_M, out[1]=BLOCK_N, out[2]=stages, out[3]=grid size,
  * out[4]=kernel kind (0 block-scaled, 1 FP32-promotion, 2 block-scaled on
- * CTA pairs), out[5]=number of
+ * CTA pairs, 3 few-row product, 5 MoE layer for few tokens), out[5]=number of
  * kernel launches of that call. */
 void dg_get_last_config(int out[6]);
 
