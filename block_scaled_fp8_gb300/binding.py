@@ -42,7 +42,7 @@ EXPORTS = (
     "dg_get_tma_aligned_size", "dg_packed_sf_words", "dg_set_num_sms", "dg_get_num_sms",
     "dg_set_wait_timeout_ms", "dg_set_debug_flags", "dg_status_string", "dg_get_last_config",
     "dg_bf16_fp4_gemv_nt", "dg_bf16_fp8_gemv_nt", "dg_bf16_fp4_gemv_nt_f32", "dg_bf16_fp8_gemv_nt_f32",
-    "dg_moe_route", "dg_moe_layer_workspace_bytes", "dg_moe_fp4_layer", "dg_moe_fp8_layer",
+    "dg_bf16_gemv_workspace_bytes", "dg_moe_route", "dg_moe_layer_workspace_bytes", "dg_moe_fp4_layer", "dg_moe_fp8_layer",
 )
 
 
@@ -104,11 +104,13 @@ def lib():
             f32 = ctypes.c_float
             for f in ("dg_bf16_fp4_gemv_nt", "dg_bf16_fp8_gemv_nt", "dg_bf16_fp4_gemv_nt_f32",
                       "dg_bf16_fp8_gemv_nt_f32"):
-                getattr(L, f).argtypes = [P, i64, P, i64, P, P, i64, P, i64, i32, i32, i32, P, P]
+                getattr(L, f).argtypes = [P, i64, P, i64, P, P, i64, P, i64, i32, i32, i32, P, i64, P, P]
                 getattr(L, f).restype = i32
+            L.dg_bf16_gemv_workspace_bytes.argtypes = [i32, i32, i32]
+            L.dg_bf16_gemv_workspace_bytes.restype = i64
             L.dg_moe_route.argtypes = [P, i64, i32, P, P, P, i32, i32, i32, i32, i32, f32, P]
             L.dg_moe_route.restype = i32
-            L.dg_moe_layer_workspace_bytes.argtypes = [i32, i32, i32]
+            L.dg_moe_layer_workspace_bytes.argtypes = [i32, i32, i32, i32]
             L.dg_moe_layer_workspace_bytes.restype = i64
             for f in ("dg_moe_fp4_layer", "dg_moe_fp8_layer"):
                 getattr(L, f).argtypes = [P, i64, P, P, P, P, P, P, P, i64, P, i64, i32, i32, i32, i32, i32, P, i64,
@@ -252,7 +254,7 @@ def dg_fp8_gemm_nt_f32(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb:
     return d
 
 
-def _gemm_layout(fn: str, a_mn: bool, b_mn: bool, a, sfa, b, sfb, d, c, status, stream):
+def _gemm_layout(fn: str, a_mn: bool, b_mn: bool, a, sfa, b, sfb, d, c, workspace, status, stream):
     # a is [M, K] (K-contiguous) or [K, M] (M-contiguous); b is [N, K] or [K, N]
     M = a.shape[1] if a_mn else a.shape[0]
     K = a.shape[0] if a_mn else a.shape[1]
@@ -269,17 +271,17 @@ def _gemm_layout(fn: str, a_mn: bool, b_mn: bool, a, sfa, b, sfb, d, c, status, 
 
 def dg_fp8_gemm_nn(a, sfa, b, sfb, d, c=None, status=None, stream=None):
     """D = C + A @ B: a [M, K], b [K, N] (N contiguous); packed scales as for the NT call."""
-    return _gemm_layout("dg_fp8_gemm_nn", False, True, a, sfa, b, sfb, d, c, status, stream)
+    return _gemm_layout("dg_fp8_gemm_nn", False, True, a, sfa, b, sfb, d, c, workspace, status, stream)
 
 
 def dg_fp8_gemm_tn(a, sfa, b, sfb, d, c=None, status=None, stream=None):
     """D = C + A^T @ B: a [K, M] (M contiguous), b [K, N] (N contiguous)."""
-    return _gemm_layout("dg_fp8_gemm_tn", True, True, a, sfa, b, sfb, d, c, status, stream)
+    return _gemm_layout("dg_fp8_gemm_tn", True, True, a, sfa, b, sfb, d, c, workspace, status, stream)
 
 
 def dg_fp8_gemm_tt(a, sfa, b, sfb, d, c=None, status=None, stream=None):
     """D = C + A^T @ B^T: a [K, M] (M contiguous), b [N, K] (K contiguous)."""
-    return _gemm_layout("dg_fp8_gemm_tt", True, False, a, sfa, b, sfb, d, c, status, stream)
+    return _gemm_layout("dg_fp8_gemm_tt", True, False, a, sfa, b, sfb, d, c, workspace, status, stream)
 
 
 def dg_fp8_fp4_gemm_nt(a, sfa, b, sfb, d, c=None, status=None, stream=None):
@@ -440,7 +442,22 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
-def _gemv(fn: str, fp4: bool, dtype, a, b, sfb, d, c, status, stream):
+def gemv_workspace_bytes(m: int, n: int, k: int) -> int:
+    return int(lib().dg_bf16_gemv_workspace_bytes(m, n, k))
+
+
+def _workspace(nbytes: int, workspace, device, stream):
+    """The caller's workspace, or one allocated on the current stream; a caller's other
+    stream waits for that and is made known to the allocator."""
+    if workspace is None and nbytes > 0:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if stream is not None and workspace.is_cuda:
+            stream.wait_stream(torch.cuda.current_stream())
+            workspace.record_stream(stream)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _gemv(fn: str, fp4: bool, dtype, a, b, sfb, d, c, workspace, status, stream):
     m, k = a.shape
     n = b.shape[0]
     assert a.dtype == torch.bfloat16 and b.dtype == (torch.uint8 if fp4 else torch.float8_e4m3fn)
@@ -448,33 +465,36 @@ def _gemv(fn: str, fp4: bool, dtype, a, b, sfb, d, c, status, stream):
     assert b.shape[1] == (k // 2 if fp4 else k) and sfb.numel() >= (-(-k // (128 if fp4 else 512))) * ((n + 3) // 4 * 4)
     assert d.dtype == dtype and d.shape == (m, n) and a.stride(1) == 1 and b.stride(1) == 1 and d.stride(1) == 1
     assert c is None or (c.dtype == dtype and c.shape == d.shape and c.stride(1) == 1)
-    _check(fn, getattr(lib(), fn)(
-        _p(a), _ld(a), _p(b), _ld(b), _p(sfb), _p(c), 0 if c is None else _ld(c), _p(d), _ld(d),
-        m, n, k, _p(status), _stream(stream)))
+    L = lib()
+    ws, nbytes = _workspace(L.dg_bf16_gemv_workspace_bytes(m, n, k), workspace, d.device, stream)
+    _check(fn, getattr(L, fn)(
+        _p(a), _ld(a), _p(b), _ld(b), _p(sfb), _p(c), 0 if c is None else _ld(c), _p(d), _ld(d), m, n, k, _p(ws), nbytes,
+        _p(status), _stream(stream)))
     return d
 
 
-def dg_bf16_fp4_gemv_nt(a, b, sfb, d, c=None, status=None, stream=None):
+def dg_bf16_fp4_gemv_nt(a, b, sfb, d, c=None, workspace=None, status=None, stream=None):
     """D = C + A @ B^T for 1..64 rows: a bf16 [M, K]; b uint8 [N, K/2], two E2M1 codes
     per byte (even k in the low nibble); sfb packed int32 [K/128, align4(N)] (4 x 32
-    K per word); d (and c) bf16 [M, N]."""
-    return _gemv("dg_bf16_fp4_gemv_nt", True, torch.bfloat16, a, b, sfb, d, c, status, stream)
+    K per word); d (and c) bf16 [M, N].  workspace: a device buffer of
+    gemv_workspace_bytes(M, N, K) bytes (made here if not given)."""
+    return _gemv("dg_bf16_fp4_gemv_nt", True, torch.bfloat16, a, b, sfb, d, c, workspace, status, stream)
 
 
-def dg_bf16_fp8_gemv_nt(a, b, sfb, d, c=None, status=None, stream=None):
+def dg_bf16_fp8_gemv_nt(a, b, sfb, d, c=None, workspace=None, status=None, stream=None):
     """As dg_bf16_fp4_gemv_nt with b float8_e4m3fn [N, K] and sfb packed int32
     [ceil(K/512), align4(N)] (4 x 128 K per word)."""
-    return _gemv("dg_bf16_fp8_gemv_nt", False, torch.bfloat16, a, b, sfb, d, c, status, stream)
+    return _gemv("dg_bf16_fp8_gemv_nt", False, torch.bfloat16, a, b, sfb, d, c, workspace, status, stream)
 
 
-def dg_bf16_fp4_gemv_nt_f32(a, b, sfb, d, c=None, status=None, stream=None):
+def dg_bf16_fp4_gemv_nt_f32(a, b, sfb, d, c=None, workspace=None, status=None, stream=None):
     """dg_bf16_fp4_gemv_nt with FP32 d (and c)."""
-    return _gemv("dg_bf16_fp4_gemv_nt_f32", True, torch.float32, a, b, sfb, d, c, status, stream)
+    return _gemv("dg_bf16_fp4_gemv_nt_f32", True, torch.float32, a, b, sfb, d, c, workspace, status, stream)
 
 
-def dg_bf16_fp8_gemv_nt_f32(a, b, sfb, d, c=None, status=None, stream=None):
+def dg_bf16_fp8_gemv_nt_f32(a, b, sfb, d, c=None, workspace=None, status=None, stream=None):
     """dg_bf16_fp8_gemv_nt with FP32 d (and c)."""
-    return _gemv("dg_bf16_fp8_gemv_nt_f32", False, torch.float32, a, b, sfb, d, c, status, stream)
+    return _gemv("dg_bf16_fp8_gemv_nt_f32", False, torch.float32, a, b, sfb, d, c, workspace, status, stream)
 
 
 def dg_moe_route(logits, ids, weights, bias=None, scoring: str = "softmax", renormalize: bool = True,
@@ -496,8 +516,8 @@ def dg_moe_route(logits, ids, weights, bias=None, scoring: str = "softmax", reno
     return ids, weights
 
 
-def moe_layer_workspace_bytes(t: int, topk: int, i: int) -> int:
-    return int(lib().dg_moe_layer_workspace_bytes(t, topk, i))
+def moe_layer_workspace_bytes(t: int, topk: int, h: int, i: int) -> int:
+    return int(lib().dg_moe_layer_workspace_bytes(t, topk, h, i))
 
 
 def _moe_layer(fn: str, fp4: bool, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream):
@@ -517,16 +537,12 @@ def _moe_layer(fn: str, fp4: bool, x, ids, weights, w1, sf1, w2, sf2, y, c, work
     assert sf2.dtype == torch.int32 and sf2.is_contiguous() and sf2.numel() >= e * -(-i // sl) * h
     assert y.dtype == torch.bfloat16 and y.shape == (t, h) and y.stride(1) == 1
     assert c is None or (c.dtype == torch.bfloat16 and c.shape == (t, h) and c.stride(1) == 1)
-    if workspace is None:
-        # allocated on the current stream; a caller's other stream is made known to the allocator
-        workspace = torch.empty(max(16, t * topk * i * 4), dtype=torch.uint8, device=y.device)
-        if stream is not None and y.is_cuda:
-            stream.wait_stream(torch.cuda.current_stream())
-            workspace.record_stream(stream)
-    _check(fn, getattr(lib(), fn)(
+    L = lib()
+    ws, nbytes = _workspace(L.dg_moe_layer_workspace_bytes(t, topk, h, i), workspace, y.device, stream)
+    _check(fn, getattr(L, fn)(
         _p(x), _ld(x), _p(ids), _p(weights), _p(w1), _p(sf1), _p(w2), _p(sf2), _p(c),
-        0 if c is None else _ld(c), _p(y), _ld(y), t, h, i, e, topk, _p(workspace),
-        workspace.numel() * workspace.element_size(), _p(status), _stream(stream)))
+        0 if c is None else _ld(c), _p(y), _ld(y), t, h, i, e, topk, _p(ws), nbytes, _p(status),
+        _stream(stream)))
     return y
 
 
@@ -535,7 +551,7 @@ def dg_moe_fp4_layer(x, ids, weights, w1, sf1, w2, sf2, y, c=None, workspace=Non
     empty slot), for 1..64 tokens.  x bf16 [T, H]; ids int32 and weights float32 [T, topk];
     w1 uint8 [E, 2I, H/2] (gate rows, then up rows) and w2 uint8 [E, H, I/2], packed E2M1;
     sf1 packed int32 [E, H/128, 2I], sf2 [E, I/128, H]; y (and c) bf16 [T, H].  workspace:
-    a device buffer of moe_layer_workspace_bytes(T, topk, I) bytes (made here if not given)."""
+    a device buffer of moe_layer_workspace_bytes(T, topk, H, I) bytes (made here if not given)."""
     return _moe_layer("dg_moe_fp4_layer", True, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream)
 
 

@@ -9,8 +9,8 @@ namespace {
 bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 dg_status gemv(bool fp4, bool f32, const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
-               const void *c, int64_t ldc, void *d, int64_t ldd, int m, int n, int k, int32_t *status_dev,
-               void *stream) {
+               const void *c, int64_t ldc, void *d, int64_t ldd, int m, int n, int k, void *workspace,
+               int64_t workspace_bytes, int32_t *status_dev, void *stream) {
     if (m < 0 || n < 0 || k < 0) return DG_ERR_INVALID_ARG;
     if (m == 0 || n == 0) return DG_OK;
     if (m > kMaxFewRows) return DG_ERR_UNSUPPORTED;
@@ -28,6 +28,9 @@ dg_status gemv(bool fp4, bool f32, const void *a, int64_t lda, const void *b, in
         const unsigned row = fp4 ? 32 : 16;   // byte rule of B's rows
         if (!aligned(b, row) || ldb % row != 0) return DG_ERR_ALIGNMENT;
         if (lda < k || ldb < (fp4 ? k / 2 : k)) return DG_ERR_INVALID_ARG;
+        const int64_t need = few_workspace_bytes(m, n, k);
+        if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return DG_ERR_INVALID_ARG;
+        if (need > 0 && !aligned(workspace, 16)) return DG_ERR_ALIGNMENT;
     }
     dg_status st = host_check_device(&sms);
     if (st != DG_OK) return st;
@@ -50,6 +53,7 @@ dg_status gemv(bool fp4, bool f32, const void *a, int64_t lda, const void *b, in
         p.k = k;
         p.fp4 = fp4;
         p.f32 = f32;
+        p.workspace = static_cast<uint8_t *>(workspace);
         p.status = status_dev;
         p.timeout_ns = host_timeout_ns();
         p.debug_flags = host_take_debug_flags();
@@ -75,7 +79,7 @@ dg_status layer(bool fp4, const void *x, int64_t ldx, const int32_t *ids, const 
     if (i != 0) {
         if (!x || !ids || !weights || !w1 || !sf1 || !w2 || !sf2 || !workspace) return DG_ERR_INVALID_ARG;
         if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(ids, 4) || !aligned(weights, 4)) return DG_ERR_ALIGNMENT;
-        if (ldx < h || workspace_bytes < dg_moe_layer_workspace_bytes(t, topk, i)) return DG_ERR_INVALID_ARG;
+        if (ldx < h || workspace_bytes < layer_workspace_bytes(t, topk, h, i)) return DG_ERR_INVALID_ARG;
         const unsigned row = fp4 ? 32 : 16;
         if (!aligned(w1, row) || !aligned(w2, row) || !aligned(sf1, 16) || !aligned(sf2, 16) || !aligned(workspace, 16))
             return DG_ERR_ALIGNMENT;
@@ -100,7 +104,7 @@ dg_status layer(bool fp4, const void *x, int64_t ldx, const int32_t *ids, const 
         p.ldc = ldc;
         p.y = static_cast<uint16_t *>(y);
         p.ldy = ldy;
-        p.act = static_cast<float *>(workspace);
+        p.workspace = static_cast<uint8_t *>(workspace);
         p.t = t;
         p.h = h;
         p.i = i;
@@ -124,26 +128,26 @@ extern "C" {
 
 dg_status dg_bf16_fp4_gemv_nt(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
                               const void *c, int64_t ldc, void *d, int64_t ldd, int m, int n, int k,
-                              int32_t *status_dev, void *stream) {
-    return gemv(true, false, a, lda, b, ldb, sfb, c, ldc, d, ldd, m, n, k, status_dev, stream);
+                              void *workspace, int64_t workspace_bytes, int32_t *status_dev, void *stream) {
+    return gemv(true, false, a, lda, b, ldb, sfb, c, ldc, d, ldd, m, n, k, workspace, workspace_bytes, status_dev, stream);
 }
 
 dg_status dg_bf16_fp8_gemv_nt(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
                               const void *c, int64_t ldc, void *d, int64_t ldd, int m, int n, int k,
-                              int32_t *status_dev, void *stream) {
-    return gemv(false, false, a, lda, b, ldb, sfb, c, ldc, d, ldd, m, n, k, status_dev, stream);
+                              void *workspace, int64_t workspace_bytes, int32_t *status_dev, void *stream) {
+    return gemv(false, false, a, lda, b, ldb, sfb, c, ldc, d, ldd, m, n, k, workspace, workspace_bytes, status_dev, stream);
 }
 
 dg_status dg_bf16_fp4_gemv_nt_f32(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
                                   const float *c, int64_t ldc, float *d, int64_t ldd, int m, int n, int k,
-                                  int32_t *status_dev, void *stream) {
-    return gemv(true, true, a, lda, b, ldb, sfb, c, ldc, d, ldd, m, n, k, status_dev, stream);
+                                  void *workspace, int64_t workspace_bytes, int32_t *status_dev, void *stream) {
+    return gemv(true, true, a, lda, b, ldb, sfb, c, ldc, d, ldd, m, n, k, workspace, workspace_bytes, status_dev, stream);
 }
 
 dg_status dg_bf16_fp8_gemv_nt_f32(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
                                   const float *c, int64_t ldc, float *d, int64_t ldd, int m, int n, int k,
-                                  int32_t *status_dev, void *stream) {
-    return gemv(false, true, a, lda, b, ldb, sfb, c, ldc, d, ldd, m, n, k, status_dev, stream);
+                                  void *workspace, int64_t workspace_bytes, int32_t *status_dev, void *stream) {
+    return gemv(false, true, a, lda, b, ldb, sfb, c, ldc, d, ldd, m, n, k, workspace, workspace_bytes, status_dev, stream);
 }
 
 dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const float *bias, int32_t *ids,
@@ -166,9 +170,12 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
     return launch_moe_route(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
-int64_t dg_moe_layer_workspace_bytes(int t, int topk, int i) {
-    if (t < 0 || topk < 0 || i < 0) return -1;
-    return static_cast<int64_t>(t) * topk * i * 4;
+int64_t dg_bf16_gemv_workspace_bytes(int m, int n, int k) {
+    return m < 0 || n < 0 || k < 0 ? -1 : few_workspace_bytes(m, n, k);
+}
+
+int64_t dg_moe_layer_workspace_bytes(int t, int topk, int h, int i) {
+    return t < 0 || topk < 0 || h < 0 || i < 0 ? -1 : layer_workspace_bytes(t, topk, h, i);
 }
 
 dg_status dg_moe_fp4_layer(const void *x, int64_t ldx, const int32_t *ids, const float *weights, const void *w1,

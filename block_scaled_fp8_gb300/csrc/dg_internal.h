@@ -145,10 +145,12 @@ struct FewParams {
     int64_t ldd;
     int m, n, k;
     int fp4, f32;
+    uint8_t *workspace;     // few_workspace_bytes(m, n, k)
     int32_t *status;
     uint64_t timeout_ns;
     uint32_t debug_flags;
 };
+int64_t few_workspace_bytes(int64_t m, int64_t n, int64_t k);
 cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream);
 
 // The MoE layer for few tokens.
@@ -165,13 +167,14 @@ struct LayerParams {
     int64_t ldc;
     uint16_t *y;            // bf16 [t][ldy]
     int64_t ldy;
-    float *act;             // workspace: FP32 [t * topk][i]
+    uint8_t *workspace;     // layer_workspace_bytes(t, topk, h, i)
     int t, h, i, experts, topk;
     int fp4;
     int32_t *status;
     uint64_t timeout_ns;
     uint32_t debug_flags;
 };
+int64_t layer_workspace_bytes(int64_t t, int64_t topk, int64_t h, int64_t i);
 cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t stream);
 
 struct RouteParams {

@@ -31,6 +31,19 @@ bool encode_weights(CUtensorMap *map, bool fp4, const void *base, int64_t rows, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Split activation rows [rows][k] of codes; boxes of 128 K x all columns of the operand.
+bool encode_rows(CUtensorMap *map, const void *base, int rows, int k, int box_rows) {
+    const TensorMapEncodeFn enc = host_encode();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k)};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t step[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Cluster size for `tiles` CTA tiles of `kblocks` K-blocks each: the least number of
 // K-blocks on the busiest SM, where a CTA costs `fixed` K-blocks beside its own.
 int choose_split(int tiles, int kblocks, int num_sms, int fixed) {
@@ -44,8 +57,8 @@ int choose_split(int tiles, int kblocks, int num_sms, int fixed) {
 }
 
 template <bool FP4, int HALVES, int MODE>
-cudaError_t launch(const CUtensorMap &map, FewArgs &a, int tiles, int split, int gy, int gz, cudaStream_t stream) {
-    const int pairs = MODE == kGemv ? 0 : a.tokens * a.topk;
+cudaError_t launch(const CUtensorMap &map, const CUtensorMap &map_x, FewArgs &a, int tiles, int split, int gy, int gz, cudaStream_t stream) {
+    const int pairs = MODE < kUp ? 0 : a.tokens * a.topk;
     const int fixed = FewConfig::smem_bytes(HALVES, a.cap, 0, MODE, pairs);
     const int stage = FewConfig::stage_bytes(HALVES, a.cap);
     int stages = (kSmemTwo - fixed) / stage;
@@ -70,23 +83,47 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, int tiles, int split, int
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    host_set_last_config(HALVES * 128, 2 * a.cap, stages, tiles * split * gy * gz, 3 + MODE, MODE == kDown ? 2 : 1);
-    return cudaLaunchKernelEx(&cfg, kernel, map, a);
+    host_set_last_config(HALVES * 128, 2 * a.cap, stages, tiles * split * gy * gz, MODE < kUp ? 3 : 5, MODE == kGemv ? 1 : MODE == kGemvPre ? 2 : 3);
+    return cudaLaunchKernelEx(&cfg, kernel, map, map_x, a);
 }
 
 template <int HALVES, int MODE>
-cudaError_t launch_fmt(bool fp4, const CUtensorMap &map, FewArgs &a, int tiles, int split, int gy, int gz,
-                       cudaStream_t stream) {
-    return fp4 ? launch<true, HALVES, MODE>(map, a, tiles, split, gy, gz, stream)
-               : launch<false, HALVES, MODE>(map, a, tiles, split, gy, gz, stream);
+cudaError_t launch_fmt(bool fp4, const CUtensorMap &map, const CUtensorMap &map_x, FewArgs &a, int tiles, int split,
+                       int gy, int gz, cudaStream_t stream) {
+    return fp4 ? launch<true, HALVES, MODE>(map, map_x, a, tiles, split, gy, gz, stream)
+               : launch<false, HALVES, MODE>(map, map_x, a, tiles, split, gy, gz, stream);
 }
+
+cudaError_t launch_split(const uint16_t *x, int64_t ldx, int rows, int kblocks, uint8_t *codes, uint32_t *scales,
+                         bool cp_order, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(cdiv(rows * kblocks, 16)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, dg_few_split_kernel, x, ldx, rows, kblocks, codes, scales, cp_order ? 1 : 0);
+}
+
+// Rows that a product splits by itself (each CTA its own K range).
+bool direct(int64_t m) { return m <= env("DG_FEW_DIRECT", 4); }
 
 int capacity(int tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
 
 }  // namespace
 
+int64_t few_workspace_bytes(int64_t m, int64_t n, int64_t k) { return direct(m) ? 0 : 2 * m * k + 4 * k; }
+
+int64_t layer_workspace_bytes(int64_t t, int64_t topk, int64_t h, int64_t i) {
+    // split x and split h: codes, then scale words
+    return 2 * t * h + 2 * t * topk * i + t * h / 16 + t * topk * i / 16;
+}
+
 cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream) {
-    CUtensorMap map;
+    CUtensorMap map, map_x;
     if (!encode_weights(&map, p.fp4, p.b, p.n, p.ldb, p.k)) return cudaErrorInvalidValue;
     FewArgs a = {};
     a.x = p.a;
@@ -106,8 +143,18 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream
     a.timeout_ns = p.timeout_ns;
     a.debug_flags = p.debug_flags;
     const int split = env("DG_FEW_SPLIT", choose_split(cdiv(p.n, 128), a.kblocks, num_sms, env("DG_FEW_FIXED", 2)));
-    if (p.m <= env("DG_FEW_M1", 16)) return launch_fmt<1, kGemv>(p.fp4, map, a, cdiv(p.n, 128), split, 1, 1, stream);
-    return launch_fmt<2, kGemv>(p.fp4, map, a, cdiv(p.n, 256), split, 1, 1, stream);
+    const bool wide = p.m > env("DG_FEW_M1", 16);   // 256-row tiles
+    const int tiles = cdiv(p.n, wide ? 256 : 128);
+    if (direct(p.m))
+        return wide ? launch_fmt<2, kGemv>(p.fp4, map, map, a, tiles, split, 1, 1, stream)
+                    : launch_fmt<1, kGemv>(p.fp4, map, map, a, tiles, split, 1, 1, stream);
+    uint32_t *scales = reinterpret_cast<uint32_t *>(p.workspace + 2 * static_cast<int64_t>(p.m) * p.k);
+    if (!encode_rows(&map_x, p.workspace, 2 * p.m, p.k, 2 * a.cap)) return cudaErrorInvalidValue;
+    cudaError_t e = launch_split(p.a, p.lda, p.m, a.kblocks, p.workspace, scales, true, stream);
+    if (e != cudaSuccess) return e;
+    a.scales = scales;
+    return wide ? launch_fmt<2, kGemvPre>(p.fp4, map, map_x, a, tiles, split, 1, 1, stream)
+                : launch_fmt<1, kGemvPre>(p.fp4, map, map_x, a, tiles, split, 1, 1, stream);
 }
 
 cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t stream) {
@@ -116,10 +163,18 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     if (!encode_weights(&map1, p.fp4, p.w1, static_cast<int64_t>(p.experts) * 2 * p.i, p.h / per, p.h) ||
         !encode_weights(&map2, p.fp4, p.w2, static_cast<int64_t>(p.experts) * p.h, p.i / per, p.i))
         return cudaErrorInvalidValue;
+    const int64_t rows = static_cast<int64_t>(p.t) * p.topk;
+    uint8_t *x_codes = p.workspace, *h_codes = x_codes + 2 * static_cast<int64_t>(p.t) * p.h;
+    uint32_t *x_scales = reinterpret_cast<uint32_t *>(h_codes + 2 * rows * p.i);
+    uint32_t *h_scales = x_scales + p.h / 128 * 2 * p.t;
+    cudaError_t e = launch_split(p.x, p.ldx, p.t, p.h / 128, x_codes, x_scales, false, stream);
+    if (e != cudaSuccess) return e;
     FewArgs a = {};
-    a.x = p.x;
-    a.ldx = p.ldx;
-    a.act = p.act;
+    a.codes = x_codes;
+    a.scales = x_scales;
+    a.src_rows = p.t;
+    a.out_codes = h_codes;
+    a.out_scales = reinterpret_cast<uint8_t *>(h_scales);
     a.tokens = p.t;
     a.ids = p.ids;
     a.weights = p.weights;
@@ -139,9 +194,12 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.cap = capacity(p.t < 2 * p.t * p.topk / p.experts + 4 ? p.t : 2 * p.t * p.topk / p.experts + 4);
     const int up_tiles = p.i / 128;
     const int up_split = env("DG_UP_SPLIT", choose_split(up_tiles * most, a.kblocks, num_sms, 2));
-    cudaError_t e = launch_fmt<2, kUp>(p.fp4, map1, a, up_tiles, up_split, most, cdiv(p.t, a.cap), stream);
+    e = launch_fmt<2, kUp>(p.fp4, map1, map1, a, up_tiles, up_split, most, cdiv(p.t, a.cap), stream);
     if (e != cudaSuccess) return e;
     // down: K runs over the active experts
+    a.codes = h_codes;
+    a.scales = h_scales;
+    a.src_rows = static_cast<int>(rows);
     a.sf = p.sf2;
     a.sf_ld = p.h;
     a.sf_expert = static_cast<int64_t>(p.fp4 ? p.i / 128 : cdiv(p.i, 512)) * a.sf_ld;
@@ -155,7 +213,7 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.debug_flags = 0;
     const int tiles = p.h / 128;
     const int split = env("DG_DOWN_SPLIT", choose_split(tiles, a.kblocks * most, num_sms, 2));
-    return launch_fmt<1, kDown>(p.fp4, map2, a, tiles, split, 1, 1, stream);
+    return launch_fmt<1, kDown>(p.fp4, map2, map2, a, tiles, split, 1, 1, stream);
 }
 
 }  // namespace dg

@@ -21,16 +21,21 @@
 //               operand row 32c + l, so that 128 consecutive scale words are already in
 //               the order in which tcgen05.cp takes them to TMEM), scales by bulk copy.
 //   warp 1      TMEM owner, MMA issuer.
-//   warps 2..9  converters: teams of warps take the K-blocks in turn and write the
-//               pieces and their scales into the block's ring slot; then the epilogue.
+//   warps 2..9  the narrow operand, then the epilogue.
 // K is split over the CTAs of a cluster, which add their FP32 partial results in rank
 // order through distributed shared memory: no workspace, no atomics, a fixed order.
 //
-// Modes: kGemv; kUp, the gate and up rows of one expert for the tokens routed to it
-// (HALVES = 2: gate, up), whose epilogue is silu(g) u; kDown, where K runs over all
-// active experts, a column belongs to one token throughout and is zero for the
-// experts that the token does not use, so the sum over a token's experts is the
-// accumulation itself (the routing weight is multiplied into the activation).
+// Modes, by where the pieces come from:
+//   kGemv   teams of warps split the activations themselves, a K-block at a time.
+//   kGemvPre  dg_few_split_kernel has split them once, into rows [2m][K] of codes and
+//           per K-block a 512-byte block of scale words in tcgen05.cp order; one warp
+//           loads them by TMA.
+//   kUp     the gate and up rows of one expert (HALVES = 2) for the tokens routed to it;
+//           teams of warps gather the tokens' split rows.  The epilogue is w silu(g) u (w
+//           the routing weight), split again into pieces.
+//   kDown   K runs over all active experts; a column belongs to one token throughout
+//           and is zero for the experts that the token does not use, so the sum over a
+//           token's experts is the accumulation itself.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -41,17 +46,21 @@
 
 namespace dg {
 
-enum FewMode : int { kGemv = 0, kUp = 1, kDown = 2 };
+enum FewMode : int { kGemv = 0, kGemvPre = 1, kUp = 2, kDown = 3 };
 
 struct FewArgs {
-    const uint16_t *x;      // kGemv, kUp: bf16 activations
+    const uint16_t *x;      // kGemv: bf16 activations
     int64_t ldx;
-    float *act;             // kUp writes, kDown reads: FP32 [t * topk][i]
+    const uint8_t *codes;   // kUp, kDown: split rows, codes [2 rows][K] (row 2r hi, 2r + 1 lo)
+    const uint32_t *scales; // their scale words [K / 128][2 rows]; kGemvPre: [K / 128][128] in tcgen05.cp order
+    uint8_t *out_codes;     // kUp: the same of its output, rows = t * topk
+    uint8_t *out_scales;
     const uint32_t *sf;     // packed scale words of the weights
     int64_t sf_expert;      // words per expert
     int sf_ld;              // words per slice
     int rows;               // weight rows of one expert (kUp: 2 i)
     int tokens;             // rows of x
+    int src_rows;           // kUp, kDown: rows of the split source (t, t * topk)
     int kblocks;            // K-blocks of one expert
     int cap;                // token columns of the operand (8, 16, 32 or 64); N = 2 cap
     int stages;
@@ -79,29 +88,84 @@ struct FewConfig {
     static constexpr int kBarBytes = 512;
     static constexpr int kMaxStages = 24;
     static int stage_bytes(int halves, int cap) { return halves * 16384 + 2 * cap * 128 + halves * 512 + 512; }
-    static int table_bytes(int mode, int pairs) { return mode == kGemv ? 0 : (256 + 24 * pairs + 15) / 16 * 16; }
+    static int table_bytes(int mode, int pairs) { return mode < kUp ? 0 : (256 + 24 * pairs + 15) / 16 * 16; }
     static int smem_bytes(int halves, int cap, int stages, int mode, int pairs) {
         return kAlign + stages * stage_bytes(halves, cap) + kBarBytes + table_bytes(mode, pairs);
     }
 };
 
-// Eight scaled values of one token to their hi and lo pieces.
-__device__ __forceinline__ void split8(const float (&f)[8], uint2 &hi, uint2 &lo) {
-    uint32_t h[4], l[4];
+// Four scaled values to their hi and lo pieces.
+__device__ __forceinline__ void split4(float f0, float f1, float f2, float f3, uint32_t &hi, uint32_t &lo) {
+    const uint32_t h01 = cvt_e4m3x2(f0, f1), h23 = cvt_e4m3x2(f2, f3);
+    const uint32_t b01 = e4m3x2_to_f16x2(h01), b23 = e4m3x2_to_f16x2(h23);
+    const float2 g01 = __half22float2(*reinterpret_cast<const __half2 *>(&b01));
+    const float2 g23 = __half22float2(*reinterpret_cast<const __half2 *>(&b23));
+    hi = h01 | (h23 << 16);
+    lo = cvt_e4m3x2((f0 - g01.x) * 16.0f, (f1 - g01.y) * 16.0f) |
+         (cvt_e4m3x2((f2 - g23.x) * 16.0f, (f3 - g23.y) * 16.0f) << 16);
+}
+
+// Biased exponent of a group's largest magnitude, kept where both scales are representable;
+// 255 marks an infinity or a NaN in the group, whose scales become NaN.
+__device__ __forceinline__ uint32_t hi_scale(uint32_t e8) { return e8 == 255u ? 255u : e8 - 7u; }
+__device__ __forceinline__ uint32_t lo_scale(uint32_t e8) { return e8 == 255u ? 255u : e8 - 11u; }
+__device__ __forceinline__ float inverse_scale(uint32_t e8) { return __uint_as_float((261u - e8) << 23); }
+
+// Lane q16 of 16 holds values 8 q16 .. 8 q16 + 7 of one row's K-block (4 lanes to a group
+// of 32): their pieces, and the group's exponent.
+__device__ __forceinline__ uint32_t split_bf16(const uint4 &v, uint2 &hi, uint2 &lo) {
+    const uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                 __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    uint32_t m = max(m2 >> 16, m2 & 0xFFFFu);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    const uint32_t e8 = max(m >> 7, 11u);
+    const float inv = inverse_scale(e8);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float f[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        h[j] = cvt_e4m3x2(f[2 * j], f[2 * j + 1]);
-        const uint32_t back = e4m3x2_to_f16x2(h[j]);
-        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&back));
-        l[j] = cvt_e4m3x2((f[2 * j] - b.x) * 16.0f, (f[2 * j + 1] - b.y) * 16.0f);
+        f[2 * j] = __uint_as_float(w[j] << 16) * inv;
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
     }
-    hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-    lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+    split4(f[0], f[1], f[2], f[3], hi.x, lo.x);
+    split4(f[4], f[5], f[6], f[7], hi.y, lo.y);
+    return e8;
+}
+
+// Position of operand row n's scale word in a 512-byte block (tcgen05.cp order).
+__device__ __forceinline__ uint32_t sf_word(uint32_t n) { return (n & 31u) * 4u + (n >> 5); }
+
+// Splits bf16 rows once for all CTAs that read them: 16 lanes per row and K-block.
+__global__ void __launch_bounds__(256) dg_few_split_kernel(const uint16_t *x, int64_t ldx, int rows, int kblocks,
+                                                           uint8_t *codes, uint32_t *scales, int cp_order) {
+    grid_dependency_wait();
+    grid_launch_dependents();   // after the wait: the next kernel may read what was there before this one
+    const int unit = blockIdx.x * 16 + static_cast<int>(threadIdx.x >> 4);
+    const int q16 = threadIdx.x & 15;
+    const bool in = unit < rows * kblocks;
+    const int kb = in ? unit / rows : 0, t = in ? unit % rows : 0;
+    const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(x + t * ldx + kb * 128 + q16 * 8));
+    uint2 hi, lo;
+    const uint32_t e8 = split_bf16(v, hi, lo);
+    if (!in) return;
+    const int64_t k = static_cast<int64_t>(kblocks) * 128;
+    uint8_t *at = codes + 2 * t * k + kb * 128 + q16 * 8;
+    *reinterpret_cast<uint2 *>(at) = hi;
+    *reinterpret_cast<uint2 *>(at + k) = lo;
+    if ((q16 & 3) == 0) {
+        const uint32_t n = 2 * t;
+        uint8_t *s = reinterpret_cast<uint8_t *>(cp_order ? scales + kb * 128 + sf_word(n)
+                                                          : scales + static_cast<int64_t>(kb) * 2 * rows + n) + (q16 >> 2);
+        s[0] = static_cast<uint8_t>(hi_scale(e8));
+        s[cp_order ? 16 : 4] = static_cast<uint8_t>(lo_scale(e8));
+    }
 }
 
 template <bool FP4, int HALVES, int MODE>
 __global__ void __launch_bounds__(FewConfig::kThreads, 2)
-    dg_few_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ FewArgs p) {
+    dg_few_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                       const __grid_constant__ FewArgs p) {
     constexpr int ROWS = HALVES * 128;
     constexpr int NT = FewConfig::kThreads;
     extern __shared__ uint8_t smem_raw[];
@@ -132,32 +196,30 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
     // i - S tests one parity bit, which is unambiguous only if block i - 2S is known to be
     // done; the team's previous block i - teams implies that up to block i - teams - S.
     const int teams = S < FewConfig::kConvWarps ? S : FewConfig::kConvWarps;
-    const int team_size = FewConfig::kConvWarps / teams;
+    const int team_size = MODE == kGemvPre ? 1 : FewConfig::kConvWarps / teams;
 
     if (warp == 0) {
         for (int i = lane; i < 2 * S + 1; i += 32) mbar_init(bars + i, i < S ? 1 + team_size : 1);
         if (lane == 0) {
             *abort_flag = 0;
             tma_prefetch_desc(&tm_w);
+            if (MODE == kGemvPre) tma_prefetch_desc(&tm_x);
         }
         fence_mbar_init();
     }
-    if (warp == 1) {
-        tmem_alloc(tmem_holder, p.tmem_cols);
-        tmem_relinquish();
-    }
-    // kDown depends on kUp, which lets it start only after its own wait: everything
-    // before kUp is complete, so kDown may read ids and weights at once and only the
-    // readers of kUp's output wait.
-    if constexpr (MODE != kDown) grid_dependency_wait();
+    // The first kernel of a chain (kGemv; the split kernel before the others) waits for
+    // what precedes it and only then lets the next one start.  So the later kernels of
+    // the chain may read weights, ids and routing weights at once; only the warps that
+    // read the preceding kernel's output wait for it.
+    if constexpr (MODE == kGemv) grid_dependency_wait();
     grid_launch_dependents();
 
     // ---------------------------------------------------------------- routing tables
-    const int pairs = MODE == kGemv ? 0 : p.tokens * p.topk;
+    const int pairs = MODE < kUp ? 0 : p.tokens * p.topk;
     uint32_t *tab_mask = reinterpret_cast<uint32_t *>(tab);   // [32] experts in use
     int *tab_pre = tab + 32;                                  // [32] experts in use before this word
     int *s_ids = tab + 64;                                    // [pairs] id of a token's first slot with it, or -1
-    float *s_wsum = reinterpret_cast<float *>(s_ids + pairs); // kDown [pairs] weights by entry
+    float *s_wsum = reinterpret_cast<float *>(s_ids + pairs); // kUp: by entry, the weight (of all the token's slots)
     uint32_t *s_mask = reinterpret_cast<uint32_t *>(s_wsum + pairs);  // kDown [active][2] tokens of each expert
     uint16_t *s_ent = reinterpret_cast<uint16_t *>(s_mask + 2 * pairs);   // kUp: pairs of this CTA; kDown: by entry
     uint16_t *s_off = s_ent + pairs;                          // kDown [active] end of each expert's entries
@@ -166,7 +228,7 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
     int ntok = p.tokens;
     int expert = 0;
     int active = 1;
-    if constexpr (MODE != kGemv) {
+    if constexpr (MODE >= kUp) {
         if (warp == 0) tab_mask[lane] = 0u;
         if (threadIdx.x == 0) { sh_count = 0; sh_expert = 0; }
         __syncthreads();
@@ -215,15 +277,26 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
                     const bool hit = q0 + lane < pairs && s_ids[q0 + lane] == expert;
                     const uint32_t m = __ballot_sync(0xFFFFFFFFu, hit);
                     const int at = n + __popc(m & ((1u << lane) - 1)) - first;
-                    if (hit && at >= 0 && at < p.cap) s_ent[at] = static_cast<uint16_t>(q0 + lane);
+                    if (hit && at >= 0 && at < p.cap) {
+                        const int q = q0 + lane, token0 = q - q % p.topk;
+                        float w = 0.0f;
+                        for (int r = q; r < token0 + p.topk; ++r)
+                            if (__ldcg(p.ids + r) == expert) w += __ldcg(p.weights + r);
+                        s_ent[at] = static_cast<uint16_t>(q);
+                        s_wsum[at] = w;
+                    }
                     n += __popc(m);
                 }
                 if (lane == 0) sh_count = max(0, min(n - first, p.cap));
             }
             __syncthreads();
             ntok = sh_count;
+            if (ntok == 0) {   // no such expert or group of tokens; the same for the whole cluster
+                grid_dependency_wait();
+                return;
+            }
         } else {
-            // entries of all active experts: (pair, summed weight), grouped by expert
+            // entries of all active experts, grouped by expert
             for (int a = threadIdx.x; a < active; a += NT) {
                 s_off[a] = 0;
                 s_mask[2 * a] = s_mask[2 * a + 1] = 0u;
@@ -261,12 +334,8 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
                     const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
                     if (a >= 0) {
                         const int at = s_off[a] + __popc(same & ((1u << lane) - 1));
-                        float w = 0.0f;
-                        for (int r = q; r < q - q % p.topk + p.topk; ++r)
-                            if (__ldcg(p.ids + r) == e) w += __ldcg(p.weights + r);
                         s_ent[at] = static_cast<uint16_t>(q);
                         atomicOr(&s_mask[2 * a + (q / p.topk >> 5)], 1u << (q / p.topk & 31));
-                        s_wsum[at] = w;
                     }
                     __syncwarp();
                     if (a >= 0 && (same >> lane) == 1u) s_off[a] += static_cast<uint16_t>(__popc(same));
@@ -275,14 +344,17 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
             }
         }
     }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, p.tmem_cols);
+        tmem_relinquish();
+    }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_holder;
-    const bool idle = MODE == kUp && ntok == 0;     // the same for every CTA of a cluster
 
     // this CTA's K-blocks
-    const int total = idle ? 0 : (MODE == kDown ? active * p.kblocks : p.kblocks);
+    const int total = MODE == kDown ? active * p.kblocks : p.kblocks;
     const int k_begin = static_cast<int>(static_cast<int64_t>(total) * rank / nsplit);
     const int nblk = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / nsplit) - k_begin;
     const int row0 = tile * (MODE == kUp ? 128 : ROWS);   // first weight row (kUp: of the gate half)
@@ -384,124 +456,110 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
         __syncwarp();
         named_bar_sync(2, 64);
     } else {
-        // ------------------------------------------------------------ converters
+        // ------------------------------------------------------------ the narrow operand
         const int cw = warp - FewConfig::kFirstConv;
-        if constexpr (MODE == kDown) grid_dependency_wait();
-        const int team = cw / team_size, member = cw % team_size;
-        int a = 0, kb = k_begin + team;
-        if (MODE == kDown && total > 0) { a = kb / p.kblocks; kb -= a * p.kblocks; }
-        const int q16 = lane & 15, sub = lane >> 4;
-        for (int i = team < teams ? team : nblk; i < nblk; i += teams) {
-            const int slot = i % S;
-            if (!mbar_wait_warp(&empty_bar[slot], ((i / S) & 1) ^ 1, ctl, DG_DEV_TIMEOUT)) break;
-            uint8_t *tile_b = smem_b + slot * b_bytes;
-            uint8_t *tile_sf = smem_sfb + slot * 512;
-            // 8 values of token column col: pieces to rows 2 col and 2 col + 1 (128-byte swizzle), scales
-            auto put = [&](int col, const float (&f)[8], uint32_t e8) {
-                uint2 hi, lo;
-                split8(f, hi, lo);
-                const uint32_t n = 2 * col;
-                const uint32_t off = (q16 & 1) * 8;
-                *reinterpret_cast<uint2 *>(tile_b + n * 128 + (((q16 >> 1) ^ (n & 7)) << 4) + off) = hi;
-                *reinterpret_cast<uint2 *>(tile_b + (n + 1) * 128 + (((q16 >> 1) ^ ((n + 1) & 7)) << 4) + off) = lo;
-                if ((q16 & 3) == 0) {
-                    uint8_t *s = tile_sf + ((n & 31) * 4 + (n >> 5)) * 4 + (q16 >> 2);
-                    // e8 = 255 (infinity or NaN in the group): a NaN scale
-                    s[0] = static_cast<uint8_t>(e8 == 255 ? 255 : e8 - 7);
-                    s[16] = static_cast<uint8_t>(e8 == 255 ? 255 : e8 - 11);
-                }
-            };
-            if constexpr (MODE != kDown) {
-                for (int t0 = 8 * member; t0 < ntok; t0 += 8 * team_size) {
-                    uint4 v[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int t = t0 + 2 * u + sub;
-                        v[u] = make_uint4(0u, 0u, 0u, 0u);
-                        if (t < ntok) {
-                            const int row = MODE == kUp ? s_ent[t] / p.topk : t;
-                            v[u] = __ldcg(reinterpret_cast<const uint4 *>(p.x + row * p.ldx + kb * 128 + q16 * 8));
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        if (t0 + 2 * u >= ntok) break;
-                        const int t = t0 + 2 * u + sub;
-                        const uint32_t m2 = __vmaxu2(__vmaxu2(v[u].x & 0x7FFF7FFFu, v[u].y & 0x7FFF7FFFu),
-                                                     __vmaxu2(v[u].z & 0x7FFF7FFFu, v[u].w & 0x7FFF7FFFu));
-                        uint32_t m = max(m2 >> 16, m2 & 0xFFFFu);
-                        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                        const uint32_t e8 = max(m >> 7, 11u);
-                        const float inv = __uint_as_float((261u - e8) << 23);   // 1/s
-                        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-                        float f[8];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            f[2 * j] = __uint_as_float(w[j] << 16) * inv;
-                            f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
-                        }
-                        if (t < ntok) put(t, f, e8);
-                    }
-                }
-            } else {
-                // columns of tokens that do not use this expert are zero, codes and scales
-                for (int t = 2 * member + sub; t < p.cap; t += 2 * team_size) {
-                    if (s_mask[2 * a + (t >> 5)] >> (t & 31) & 1u) continue;
-                    reinterpret_cast<uint4 *>(tile_b + t * 256)[q16] = make_uint4(0u, 0u, 0u, 0u);
-                    const int n = 2 * t + q16;
-                    if (q16 < 2) reinterpret_cast<uint32_t *>(tile_sf)[(n & 31) * 4 + (n >> 5)] = 0u;
+        if constexpr (MODE != kGemv) grid_dependency_wait();
+        if constexpr (MODE == kGemvPre) {
+            for (int i = cw; i < nblk && cw == 0; ++i) {
+                const int slot = i % S;
+                if (!mbar_wait_warp(&empty_bar[slot], ((i / S) & 1) ^ 1, ctl, DG_DEV_TIMEOUT)) break;
+                if (elect_one()) {
+                    const int kb = k_begin + i;
+                    mbar_arrive_expect_tx(&full_bar[slot], b_bytes + 512);
+                    tma_load_2d(smem_b + slot * b_bytes, &tm_x, &full_bar[slot], kb * 128, 0);
+                    bulk_load(smem_sfb + slot * 512, p.scales + kb * 128, 512, &full_bar[slot]);
                 }
                 __syncwarp();
-                const int begin = a ? s_off[a - 1] : 0, end = s_off[a];
-                for (int t0 = begin + 4 * member; t0 < end; t0 += 4 * team_size) {
-                    float4 v[2][2];
-                    int col[2];
-                    float w[2];
+            }
+        } else {
+            const int team = cw / team_size, member = cw % team_size;
+            const int q16 = lane & 15, sub = lane >> 4;   // two tokens at a time, 16 lanes each
+            int a = 0, kb = k_begin + team;
+            if (MODE == kDown && total > 0) { a = kb / p.kblocks; kb -= a * p.kblocks; }
+            for (int i = team < teams ? team : nblk; i < nblk; i += teams) {
+                const int slot = i % S;
+                if (!mbar_wait_warp(&empty_bar[slot], ((i / S) & 1) ^ 1, ctl, DG_DEV_TIMEOUT)) break;
+                uint8_t *tile_b = smem_b + slot * b_bytes;
+                uint8_t *tile_sf = smem_sfb + slot * 512;
+                if constexpr (MODE == kGemv) {
+                    for (int t0 = 8 * member; t0 < ntok; t0 += 8 * team_size) {
+                        uint4 v[4];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int t = t0 + 2 * u + sub;
-                        v[u][0] = v[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        col[u] = 0;
-                        w[u] = 0.0f;
-                        if (t < end) {
-                            const int pair = s_ent[t];
-                            col[u] = pair / p.topk;
-                            w[u] = s_wsum[t];
-                            const float4 *src = reinterpret_cast<const float4 *>(
-                                p.act + static_cast<int64_t>(pair) * p.inner + kb * 128 + q16 * 8);
-                            v[u][0] = __ldcg(src);
-                            v[u][1] = __ldcg(src + 1);
+                        for (int u = 0; u < 4; ++u) {
+                            const int t = t0 + 2 * u + sub;
+                            v[u] = make_uint4(0u, 0u, 0u, 0u);
+                            if (t < ntok)
+                                v[u] = __ldcg(reinterpret_cast<const uint4 *>(p.x + t * p.ldx + kb * 128 + q16 * 8));
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            if (t0 + 2 * u >= ntok) break;
+                            const int t = t0 + 2 * u + sub;
+                            uint2 hi, lo;
+                            const uint32_t e8 = split_bf16(v[u], hi, lo);
+                            if (t >= ntok) continue;
+                            // columns 2t and 2t + 1 (rows of 128 bytes, 128-byte swizzle)
+                            const uint32_t n = 2 * t;
+                            const uint32_t off = (q16 & 1) * 8;
+                            *reinterpret_cast<uint2 *>(tile_b + n * 128 + (((q16 >> 1) ^ (n & 7)) << 4) + off) = hi;
+                            *reinterpret_cast<uint2 *>(tile_b + (n + 1) * 128 + (((q16 >> 1) ^ ((n + 1) & 7)) << 4) +
+                                                       off) = lo;
+                            if ((q16 & 3) == 0) {
+                                uint8_t *s = tile_sf + sf_word(n) * 4 + (q16 >> 2);
+                                s[0] = static_cast<uint8_t>(hi_scale(e8));
+                                s[16] = static_cast<uint8_t>(lo_scale(e8));
+                            }
                         }
                     }
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        if (t0 + 2 * u >= end) break;
-                        const int t = t0 + 2 * u + sub;
-                        float f[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w,
-                                      v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
-                        uint32_t m = 0;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            f[j] *= w[u];
-                            m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+                } else {
+                    int begin = 0, end = ntok;
+                    if constexpr (MODE == kDown) {
+                        // columns of tokens that do not use this expert are zero, codes and scales
+                        for (int t = 2 * member + sub; t < p.cap; t += 2 * team_size) {
+                            if (s_mask[2 * a + (t >> 5)] >> (t & 31) & 1u) continue;
+                            reinterpret_cast<uint4 *>(tile_b + t * 256)[q16] = make_uint4(0u, 0u, 0u, 0u);
+                            if (q16 < 2) reinterpret_cast<uint32_t *>(tile_sf)[sf_word(2 * t + q16)] = 0u;
                         }
-                        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                        const uint32_t e8 = max(m >> 23, 11u);
-                        const float inv = __uint_as_float((261u - e8) << 23);
+                        __syncwarp();
+                        begin = a ? s_off[a - 1] : 0;
+                        end = s_off[a];
+                    }
+                    const int64_t k = static_cast<int64_t>(p.kblocks) * 128;
+                    const uint8_t *src = p.codes + (q16 >> 3) * k + kb * 128 + (q16 & 7) * 16;
+                    const uint32_t *src_sf = p.scales + static_cast<int64_t>(kb) * 2 * p.src_rows + (q16 & 1);
+                    for (int t0 = begin + 8 * member; t0 < end; t0 += 8 * team_size) {
+                        uint4 v[4];
+                        uint32_t sf[4];
+                        int col[4];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) f[j] *= inv;
-                        if (t < end) put(col[u], f, e8);
+                        for (int u = 0; u < 4; ++u) {
+                            const int t = t0 + 2 * u + sub;
+                            if (t < end) {
+                                const int pair = s_ent[t];
+                                const int token = pair / p.topk;
+                                const int row = MODE == kUp ? token : pair;
+                                col[u] = MODE == kUp ? t : token;
+                                v[u] = __ldcg(reinterpret_cast<const uint4 *>(src + 2 * row * k));
+                                sf[u] = __ldcg(src_sf + 2 * row);
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            if (t0 + 2 * u + sub < end) {
+                                const uint32_t n = 2 * col[u] + (q16 >> 3);
+                                *reinterpret_cast<uint4 *>(tile_b + n * 128 + (((q16 & 7) ^ (n & 7)) << 4)) = v[u];
+                                if (q16 < 2) reinterpret_cast<uint32_t *>(tile_sf)[sf_word(2 * col[u] + q16)] = sf[u];
+                            }
+                        }
                     }
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full_bar[slot]);
+                kb += teams;
+                if constexpr (MODE == kDown)
+                    while (kb >= p.kblocks) { kb -= p.kblocks; ++a; }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full_bar[slot]);
-            kb += teams;
-            if constexpr (MODE == kDown)
-                while (kb >= p.kblocks) { kb -= p.kblocks; ++a; }
         }
 
         // ------------------------------------------------------------ accumulators -> shared memory
@@ -535,6 +593,8 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
         tc_fence_after_sync();
         tmem_dealloc(tmem_base, p.tmem_cols);
     }
+    // (the grid must not end before the one it depends on, whoever else waited)
+    if constexpr (MODE != kGemv) grid_dependency_wait();
     if (nsplit > 1) cluster_sync();
     // ---------------------------------------------------------------- sum over the cluster, output
     const uint32_t part0 = smem_u32(smem_a);
@@ -558,8 +618,28 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
                 const float u = load(base + 128 + 32 * c);
                 o[c] = o[c] / (1.0f + expf(-o[c])) * u;
             }
-            *reinterpret_cast<float4 *>(p.act + static_cast<int64_t>(s_ent[t]) * p.inner + n) =
-                make_float4(o[0], o[1], o[2], o[3]);
+            // a warp holds one token's 128 values; 8 lanes a group of 32
+            const float w = s_wsum[t];
+            uint32_t m = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                o[c] *= w;
+                m = max(m, __float_as_uint(o[c]) & 0x7FFFFFFFu);
+            }
+#pragma unroll
+            for (int s = 1; s < 8; s <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+            const uint32_t e8 = max(m >> 23, 11u);
+            const float inv = inverse_scale(e8);
+            uint32_t hi, lo;
+            split4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv, hi, lo);
+            const int64_t row = 2 * static_cast<int64_t>(s_ent[t]);
+            *reinterpret_cast<uint32_t *>(p.out_codes + row * p.inner + n) = hi;
+            *reinterpret_cast<uint32_t *>(p.out_codes + (row + 1) * p.inner + n) = lo;
+            if ((lane & 7) == 0) {
+                uint8_t *sf = p.out_scales + ((row0 >> 7) * 2 * static_cast<int64_t>(pairs) + row) * 4 + (lane >> 3);
+                sf[0] = static_cast<uint8_t>(hi_scale(e8));
+                sf[4] = static_cast<uint8_t>(lo_scale(e8));
+            }
         } else if (n < p.rows) {
             if (p.f32) {
                 if (p.c) {

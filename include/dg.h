@@ -418,21 +418,26 @@ int64_t dg_k_grouped_packed_sf_rows(const int *ks, int num_groups);
  *        c and d 16-byte aligned, ldc and ldd multiples of 8 (FP32: 4).
  *   0 <= m <= 64 (else DG_ERR_UNSUPPORTED: use the GEMMs), n a multiple of 8, k a
  *   multiple of 128.  m == 0 or n == 0 is a no-op; k == 0 gives D = C (or 0).
+ *   workspace   device memory, 16-byte aligned, of dg_bf16_gemv_workspace_bytes(m,
+ *        n, k) bytes (0 for the fewest rows: then it may be NULL); its contents need no
+ *        initialisation and do not outlive the call.  Calls that may run at the same
+ *        time need one each.
  *   A row that holds an infinity or a NaN gives NaN in its row of D; other rows
  *   are not affected.  Row i of D is the same bit for bit whatever m is.
  */
+int64_t dg_bf16_gemv_workspace_bytes(int m, int n, int k);
 dg_status dg_bf16_fp4_gemv_nt(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
                               const void *c, int64_t ldc, void *d, int64_t ldd, int m, int n, int k,
-                              int32_t *status_dev, void *stream);
+                              void *workspace, int64_t workspace_bytes, int32_t *status_dev, void *stream);
 dg_status dg_bf16_fp8_gemv_nt(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
                               const void *c, int64_t ldc, void *d, int64_t ldd, int m, int n, int k,
-                              int32_t *status_dev, void *stream);
+                              void *workspace, int64_t workspace_bytes, int32_t *status_dev, void *stream);
 dg_status dg_bf16_fp4_gemv_nt_f32(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
                                   const float *c, int64_t ldc, float *d, int64_t ldd, int m, int n, int k,
-                                  int32_t *status_dev, void *stream);
+                                  void *workspace, int64_t workspace_bytes, int32_t *status_dev, void *stream);
 dg_status dg_bf16_fp8_gemv_nt_f32(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
                                   const float *c, int64_t ldc, float *d, int64_t ldd, int m, int n, int k,
-                                  int32_t *status_dev, void *stream);
+                                  void *workspace, int64_t workspace_bytes, int32_t *status_dev, void *stream);
 
 /*
  * dg_moe_route -- top-k routing of tokens to experts.  For each token, with
@@ -460,7 +465,7 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
 /*
  * dg_moe_fp4_layer / dg_moe_fp8_layer -- a whole mixture-of-experts layer for a
  * few tokens (a decode step), from bf16 activations and the routing to bf16 output,
- * in two kernels.  With e = ids[t][j]:
+ * in three launches.  With e = ids[t][j]:
  *
  *   h(t,j)[i] = silu(sum_k W1[e][i][k] x[t][k]) * (sum_k W1[e][I + i][k] x[t][k])
  *   y[t][n]   = c[t][n] + sum_j weights[t][j] * sum_i W2[e][n][i] h(t,j)[i]
@@ -479,7 +484,7 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
  *   c     bf16 [t, ldc] or NULL, may equal y; y bf16 [t, ldy]; 16-byte aligned,
  *         strides multiples of 8.
  *   workspace   device memory, 16-byte aligned, dg_moe_layer_workspace_bytes(t,
- *         topk, i) bytes; its contents need no initialisation and do not outlive
+ *         topk, h, i) bytes; its contents need no initialisation and do not outlive
  *         the call.  Calls that may run at the same time need one each.
  *   h and i multiples of 128 (DG_ERR_ALIGNMENT); t <= 64, topk <= 16 and experts <=
  *   1024, else DG_ERR_UNSUPPORTED (more tokens: dg_m_grouped_*); t == 0 or h == 0
@@ -488,7 +493,7 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
  *   holds an infinity or a NaN gets NaN; the weights and scales of the named
  *   experts must be finite (a NaN there may reach every token of the call).
  */
-int64_t dg_moe_layer_workspace_bytes(int t, int topk, int i);
+int64_t dg_moe_layer_workspace_bytes(int t, int topk, int h, int i);
 dg_status dg_moe_fp4_layer(const void *x, int64_t ldx, const int32_t *ids, const float *weights, const void *w1,
                            const void *sf1, const void *w2, const void *sf2, const void *c, int64_t ldc, void *y,
                            int64_t ldy, int t, int h, int i, int experts, int topk, void *workspace,

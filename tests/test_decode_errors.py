@@ -22,8 +22,9 @@ def lib():
 def test_gemv_refusals(lib, fp4, f32):
     fn = getattr(lib, f"dg_bf16_{'fp4' if fp4 else 'fp8'}_gemv_nt" + ("_f32" if f32 else ""))
 
-    def call(a=16, lda=256, b=64, ldb=256, sfb=16, c=0, ldc=64, d=16, ldd=64, m=3, n=64, k=256):
-        return fn(P(a), lda, P(b), ldb, P(sfb), P(c), ldc, P(d), ldd, m, n, k, None, None)
+    def call(a=16, lda=256, b=64, ldb=256, sfb=16, c=0, ldc=64, d=16, ldd=64, m=3, n=64, k=256,
+             ws=16, nbytes=1 << 20):
+        return fn(P(a), lda, P(b), ldb, P(sfb), P(c), ldc, P(d), ldd, m, n, k, P(ws), nbytes, None, None)
     assert call(m=-1) == ARG and call(n=-8) == ARG and call(k=-128) == ARG
     assert call(m=0) == OK and call(n=0) == OK
     assert call(m=65) == UNSUP
@@ -34,6 +35,9 @@ def test_gemv_refusals(lib, fp4, f32):
     assert call(k=192) == ALIGN and call(lda=260) == ALIGN and call(lda=248) == ARG
     assert call(b=72) == ALIGN and call(ldb=264) == ALIGN
     assert call(ldb=96 if fp4 else 240) == ARG
+    need = lib.dg_bf16_gemv_workspace_bytes(64, 64, 256)
+    assert need > 0 and lib.dg_bf16_gemv_workspace_bytes(-1, 64, 256) == -1
+    assert call(m=64, ws=0, nbytes=need) == ARG and call(m=64, nbytes=need - 1) == ARG and call(m=64, ws=24) == ALIGN
     if fp4:
         assert call(b=48) == ALIGN and call(ldb=144) == ALIGN     # FP4 rows: 32 bytes
 
@@ -55,11 +59,11 @@ def test_layer_refusals(lib, fp4):
 
     def call(x=16, ldx=256, ids=16, w=16, w1=64, sf1=16, w2=64, sf2=16, c=0, ldc=256, y=16, ldy=256, t=3, h=256, i=128,
              e=4, topk=2, ws=16, nbytes=None):
-        nbytes = t * topk * i * 4 if nbytes is None else nbytes
+        nbytes = 1 << 24 if nbytes is None else nbytes
         return fn(P(x), ldx, P(ids), P(w), P(w1), P(sf1), P(w2), P(sf2), P(c), ldc, P(y), ldy, t, h, i, e, topk, P(ws),
                   nbytes, None, None)
-    assert lib.dg_moe_layer_workspace_bytes(3, 2, 128) == 3 * 2 * 128 * 4
-    assert lib.dg_moe_layer_workspace_bytes(-1, 2, 128) == -1
+    need = lib.dg_moe_layer_workspace_bytes(3, 2, 256, 128)
+    assert need > 0 and lib.dg_moe_layer_workspace_bytes(-1, 2, 256, 128) == -1
     assert call(t=-1) == ARG and call(h=-128) == ARG and call(i=-128) == ARG and call(e=0) == ARG and call(topk=0) == ARG
     assert call(t=0) == OK and call(h=0) == OK
     assert call(t=65) == UNSUP and call(topk=17) == UNSUP and call(e=1025) == UNSUP
@@ -71,6 +75,6 @@ def test_layer_refusals(lib, fp4):
     assert call(ids=18) == ALIGN and call(w=18) == ALIGN
     assert call(ldx=248) == ARG and call(ldy=248) == ARG and call(c=16, ldc=248) == ARG
     assert call(ldx=260) == ALIGN and call(ldy=260) == ALIGN and call(c=16, ldc=260) == ALIGN
-    assert call(nbytes=3 * 2 * 128 * 4 - 1) == ARG
+    assert call(nbytes=need - 1) == ARG
     if fp4:
         assert call(w1=48) == ALIGN and call(w2=48) == ALIGN
