@@ -44,29 +44,29 @@ bool encode_rows(CUtensorMap *map, const void *base, int rows, int k, int box_ro
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Cluster size for `tiles` CTA tiles of `kblocks` K-blocks each: the least number of
-// K-blocks on the busiest SM, where a CTA costs `fixed` K-blocks beside its own.
-int choose_split(int tiles, int kblocks, int num_sms, int fixed) {
-    int best = 1;
-    int64_t best_cost = -1;
-    for (int s = 1; s <= kMaxSplit && s <= kblocks; ++s) {
-        const int64_t cost = static_cast<int64_t>(cdiv(tiles * s, num_sms)) * (cdiv(kblocks, s) + fixed);
-        if (best_cost < 0 || cost < best_cost) { best = s; best_cost = cost; }
-    }
-    return best;
-}
+// How a launch fills the GPU: `occ` CTAs on an SM; `split` CTAs of a cluster share a
+// tile's K (1: persistent CTAs take the tiles in turn).
+struct Plan {
+    int halves, occ, split;
+};
 
 template <bool FP4, int HALVES, int MODE>
-cudaError_t launch(const CUtensorMap &map, const CUtensorMap &map_x, FewArgs &a, int tiles, int split, int gy, int gz, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap &map, const CUtensorMap &map_x, FewArgs &a, const Plan &plan, int max_tiles,
+                   int num_sms, cudaStream_t stream) {
     const int pairs = MODE < kUp ? 0 : a.tokens * a.topk;
-    const int fixed = FewConfig::smem_bytes(HALVES, a.cap, 0, MODE, pairs);
+    const int fixed = FewConfig::smem_bytes(HALVES, a.cap, 0, MODE, pairs, plan.split);
     const int stage = FewConfig::stage_bytes(HALVES, a.cap);
-    int stages = (kSmemTwo - fixed) / stage;
-    if (stages < env("DG_FEW_MIN2", 3)) stages = (kSmemOne - fixed) / stage;
+    const int limit = plan.occ == 2 ? kSmemTwo : kSmemOne;
+    int stages = (limit - fixed) / stage;
     if (stages > FewConfig::kMaxStages) stages = FewConfig::kMaxStages;
+    if (stages > env("DG_ST", 99)) stages = env("DG_ST", 99);
+    if (stages < 2) return cudaErrorInvalidConfiguration;
+    const int set = HALVES * 2 * a.cap, sf = 2 * (4 * HALVES + 4), most = plan.occ == 2 ? 256 : 512;
     a.stages = stages;
-    a.tmem_cols = pow2_at_least(HALVES * 2 * a.cap + 2 * (4 * HALVES + 4));
-    const int smem = FewConfig::smem_bytes(HALVES, a.cap, stages, MODE, pairs);
+    a.accs = plan.split == 1 && 2 * set + sf <= most ? 2 : 1;
+    a.tmem_cols = pow2_at_least(a.accs * set + sf);
+    if (a.tmem_cols > 512) return cudaErrorInvalidConfiguration;
+    const int smem = FewConfig::smem_bytes(HALVES, a.cap, stages, MODE, pairs, plan.split);
     auto kernel = dg_few_rows_kernel<FP4, HALVES, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
     if (e != cudaSuccess) return e;
@@ -75,23 +75,34 @@ cudaError_t launch(const CUtensorMap &map, const CUtensorMap &map_x, FewArgs &a,
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(plan.split);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(gy), static_cast<unsigned>(gz));
+    const int grid = plan.split > 1 ? max_tiles * plan.split
+                                    : (max_tiles < plan.occ * num_sms ? max_tiles : plan.occ * num_sms);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(FewConfig::kThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 2 : 1;
-    host_set_last_config(HALVES * 128, 2 * a.cap, stages, tiles * split * gy * gz, MODE < kUp ? 3 : 5, MODE == kGemv ? 1 : MODE == kGemvPre ? 2 : 3);
+    cfg.numAttrs = plan.split > 1 ? 2 : 1;
+    host_set_last_config(HALVES * 128, 2 * a.cap, stages, grid, MODE < kUp ? 3 : 5,
+                         MODE == kGemv ? 1 : MODE == kGemvPre ? 2 : 3);
     return cudaLaunchKernelEx(&cfg, kernel, map, map_x, a);
 }
 
 template <int HALVES, int MODE>
-cudaError_t launch_fmt(bool fp4, const CUtensorMap &map, const CUtensorMap &map_x, FewArgs &a, int tiles, int split,
-                       int gy, int gz, cudaStream_t stream) {
-    return fp4 ? launch<true, HALVES, MODE>(map, map_x, a, tiles, split, gy, gz, stream)
-               : launch<false, HALVES, MODE>(map, map_x, a, tiles, split, gy, gz, stream);
+cudaError_t launch_fmt(bool fp4, const CUtensorMap &map, const CUtensorMap &map_x, FewArgs &a, const Plan &plan,
+                       int max_tiles, int num_sms, cudaStream_t stream) {
+    return fp4 ? launch<true, HALVES, MODE>(map, map_x, a, plan, max_tiles, num_sms, stream)
+               : launch<false, HALVES, MODE>(map, map_x, a, plan, max_tiles, num_sms, stream);
+}
+
+// The largest cluster of at most kMaxSplit CTAs (and K-blocks) with all tiles resident at once.
+int resident_split(int tiles, int kblocks, int slots) {
+    int s = slots / tiles;
+    if (s > kMaxSplit) s = kMaxSplit;
+    if (s > kblocks) s = kblocks;
+    return s < 1 ? 1 : s;
 }
 
 cudaError_t launch_split(const uint16_t *x, int64_t ldx, int rows, int kblocks, uint8_t *codes, uint32_t *scales,
@@ -142,19 +153,22 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream
     a.status = p.status;
     a.timeout_ns = p.timeout_ns;
     a.debug_flags = p.debug_flags;
-    const int split = env("DG_FEW_SPLIT", choose_split(cdiv(p.n, 128), a.kblocks, num_sms, env("DG_FEW_FIXED", 2)));
-    const bool wide = p.m > env("DG_FEW_M1", 16);   // 256-row tiles
-    const int tiles = cdiv(p.n, wide ? 256 : 128);
+    Plan plan;
+    plan.halves = env("DG_H", p.m > 16 ? 2 : 1);
+    plan.occ = env("DG_OCC", plan.halves == 1 ? 2 : 1);
+    plan.split = env("DG_S", resident_split(cdiv(p.n, 128), a.kblocks, 2 * num_sms * 19 / 20));
+    const int tiles = cdiv(p.n, 128 * plan.halves);
+    a.row_tiles = tiles;
     if (direct(p.m))
-        return wide ? launch_fmt<2, kGemv>(p.fp4, map, map, a, tiles, split, 1, 1, stream)
-                    : launch_fmt<1, kGemv>(p.fp4, map, map, a, tiles, split, 1, 1, stream);
+        return plan.halves == 2 ? launch_fmt<2, kGemv>(p.fp4, map, map, a, plan, tiles, num_sms, stream)
+                                : launch_fmt<1, kGemv>(p.fp4, map, map, a, plan, tiles, num_sms, stream);
     uint32_t *scales = reinterpret_cast<uint32_t *>(p.workspace + 2 * static_cast<int64_t>(p.m) * p.k);
     if (!encode_rows(&map_x, p.workspace, 2 * p.m, p.k, 2 * a.cap)) return cudaErrorInvalidValue;
     cudaError_t e = launch_split(p.a, p.lda, p.m, a.kblocks, p.workspace, scales, true, stream);
     if (e != cudaSuccess) return e;
     a.scales = scales;
-    return wide ? launch_fmt<2, kGemvPre>(p.fp4, map, map_x, a, tiles, split, 1, 1, stream)
-                : launch_fmt<1, kGemvPre>(p.fp4, map, map_x, a, tiles, split, 1, 1, stream);
+    return plan.halves == 2 ? launch_fmt<2, kGemvPre>(p.fp4, map, map_x, a, plan, tiles, num_sms, stream)
+                            : launch_fmt<1, kGemvPre>(p.fp4, map, map_x, a, plan, tiles, num_sms, stream);
 }
 
 cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t stream) {
@@ -192,9 +206,14 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.rows = 2 * p.i;
     a.kblocks = p.h / 128;
     a.cap = capacity(p.t < 2 * p.t * p.topk / p.experts + 4 ? p.t : 2 * p.t * p.topk / p.experts + 4);
-    const int up_tiles = p.i / 128;
-    const int up_split = env("DG_UP_SPLIT", choose_split(up_tiles * most, a.kblocks, num_sms, 2));
-    e = launch_fmt<2, kUp>(p.fp4, map1, map1, a, up_tiles, up_split, most, cdiv(p.t, a.cap), stream);
+    a.chunks = cdiv(p.t, a.cap);
+    a.row_tiles = p.i / 128;
+    const int up_tiles = a.row_tiles * a.chunks * most;
+    Plan up;
+    up.halves = 2;
+    up.occ = env("DG_UP_OCC", 1);
+    up.split = env("DG_UP_S", resident_split(up_tiles, a.kblocks, up.occ * num_sms * 19 / 20));
+    e = launch_fmt<2, kUp>(p.fp4, map1, map1, a, up, up_tiles, num_sms, stream);
     if (e != cudaSuccess) return e;
     // down: K runs over the active experts
     a.codes = h_codes;
@@ -211,9 +230,13 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.d = p.y;
     a.ldd = p.ldy;
     a.debug_flags = 0;
-    const int tiles = p.h / 128;
-    const int split = env("DG_DOWN_SPLIT", choose_split(tiles, a.kblocks * most, num_sms, 2));
-    return launch_fmt<1, kDown>(p.fp4, map2, map2, a, tiles, split, 1, 1, stream);
+    Plan down;
+    down.halves = env("DG_DOWN_H", 1);
+    down.occ = env("DG_DOWN_OCC", 2);
+    a.row_tiles = cdiv(p.h, 128 * down.halves);
+    down.split = env("DG_DOWN_S", resident_split(a.row_tiles, a.kblocks * most, down.occ * num_sms * 19 / 20));
+    return down.halves == 2 ? launch_fmt<2, kDown>(p.fp4, map2, map2, a, down, a.row_tiles, num_sms, stream)
+                            : launch_fmt<1, kDown>(p.fp4, map2, map2, a, down, a.row_tiles, num_sms, stream);
 }
 
 }  // namespace dg

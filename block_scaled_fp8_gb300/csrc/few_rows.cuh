@@ -16,22 +16,24 @@
 // to be read from shared memory up to N = 64 columns (32 rows of activations), which is a
 // third of the time they take from HBM: the weight stream is the bound.
 //
-// A CTA computes HALVES x 128 weight rows over a range of K-blocks (128 K each):
+// A CTA computes tiles of HALVES x 128 weight rows, over K-blocks of 128 K:
 //   warp 0      producer: weights by TMA (a 3-D box that takes weight row 4l + c to
 //               operand row 32c + l, so that 128 consecutive scale words are already in
 //               the order in which tcgen05.cp takes them to TMEM), scales by bulk copy.
 //   warp 1      TMEM owner, MMA issuer.
-//   warps 2..9  the narrow operand, then the epilogue.
-// K is split over the CTAs of a cluster, which add their FP32 partial results in rank
-// order through distributed shared memory: no workspace, no atomics, a fixed order.
+//   warps 2..5  epilogue, one TMEM lane quadrant each.
+//   warps 6..9  the narrow operand, K-blocks in turn.
+// Many tiles: the CTAs are persistent and take tiles in turn, the ring of K-blocks running
+// on across them.  Few tiles: one tile per cluster, K split over its CTAs, which add
+// their FP32 partial results in rank order through distributed shared memory: no
+// workspace, no atomics, a fixed order.
 //
 // Modes, by where the pieces come from:
-//   kGemv   teams of warps split the activations themselves, a K-block at a time.
+//   kGemv   the warps split the activations themselves.
 //   kGemvPre  dg_few_split_kernel has split them once, into rows [2m][K] of codes and
-//           per K-block a 512-byte block of scale words in tcgen05.cp order; one warp
-//           loads them by TMA.
-//   kUp     the gate and up rows of one expert (HALVES = 2) for the tokens routed to it;
-//           teams of warps gather the tokens' split rows.  The epilogue is w silu(g) u (w
+//           per K-block a 512-byte block of scale words in tcgen05.cp order: TMA loads.
+//   kUp     the gate and up rows of one expert (HALVES = 2) for up to `cap` of the tokens
+//           routed to it, whose split rows are gathered.  The epilogue is w silu(g) u (w
 //           the routing weight), split again into pieces.
 //   kDown   K runs over all active experts; a column belongs to one token throughout
 //           and is zero for the experts that the token does not use, so the sum over a
@@ -64,7 +66,10 @@ struct FewArgs {
     int kblocks;            // K-blocks of one expert
     int cap;                // token columns of the operand (8, 16, 32 or 64); N = 2 cap
     int stages;
+    int accs;               // accumulator sets (1 or 2)
     int tmem_cols;
+    int row_tiles;          // tiles over the weight rows (kUp: of h's columns)
+    int chunks;             // kUp: groups of cap tokens that an expert may have
     // MoE
     const int32_t *ids;
     const float *weights;
@@ -82,15 +87,19 @@ struct FewArgs {
 
 struct FewConfig {
     static constexpr int kThreads = 320;
-    static constexpr int kConvWarps = 8;
-    static constexpr int kFirstConv = 2;
+    static constexpr int kFirstEpi = 2, kFirstB = 6, kBWarps = 4;
     static constexpr int kAlign = 1024;
     static constexpr int kBarBytes = 512;
     static constexpr int kMaxStages = 24;
     static int stage_bytes(int halves, int cap) { return halves * 16384 + 2 * cap * 128 + halves * 512 + 512; }
+    // two buffers of 8 tokens' FP32 results (split tiles leave theirs in the ring)
+    static int out_bytes(int halves, int mode, int split) {
+        return split > 1 ? 0 : 2 * 8 * (mode == kUp ? 128 : halves * 128) * 4;
+    }
     static int table_bytes(int mode, int pairs) { return mode < kUp ? 0 : (256 + 24 * pairs + 15) / 16 * 16; }
-    static int smem_bytes(int halves, int cap, int stages, int mode, int pairs) {
-        return kAlign + stages * stage_bytes(halves, cap) + kBarBytes + table_bytes(mode, pairs);
+    static int smem_bytes(int halves, int cap, int stages, int mode, int pairs, int split) {
+        return kAlign + stages * stage_bytes(halves, cap) + out_bytes(halves, mode, split) + kBarBytes +
+               table_bytes(mode, pairs);
     }
 };
 
@@ -162,11 +171,22 @@ __global__ void __launch_bounds__(256) dg_few_split_kernel(const uint16_t *x, in
     }
 }
 
+// One tile of work, the same for every role of a CTA.
+struct FewTile {
+    int expert;     // kUp
+    int row0;       // first weight row (kUp: column of h)
+    int ntok;       // token columns
+    int ent;        // kUp: first entry
+    int begin;      // first K-block (kDown: over the active experts)
+    int nblk;
+};
+
 template <bool FP4, int HALVES, int MODE>
 __global__ void __launch_bounds__(FewConfig::kThreads, 2)
     dg_few_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                        const __grid_constant__ FewArgs p) {
     constexpr int ROWS = HALVES * 128;
+    constexpr int OUT = MODE == kUp ? 128 : ROWS;     // results per token and tile
     constexpr int NT = FewConfig::kThreads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -178,12 +198,16 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
     uint8_t *smem_b = smem_a + S * HALVES * 16384;
     uint8_t *smem_sfa = smem_b + S * b_bytes;
     uint8_t *smem_sfb = smem_sfa + S * HALVES * 512;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_sfb + S * 512);
-    uint64_t *full_bar = bars;              // [S] weights and scales landed (transactions), pieces written by the team
+    float *smem_out = reinterpret_cast<float *>(smem_sfb + S * 512);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_out + (cluster_nctarank() > 1 ? 0 : 2 * 8 * OUT));
+    uint64_t *full_bar = bars;              // [S] weights and scales landed, pieces written
     uint64_t *empty_bar = bars + S;         // [S] the slot's MMAs are done
-    uint64_t *tfull_bar = bars + 2 * S;     // the accumulators are complete
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(tfull_bar + 1);
+    uint64_t *tfull_bar = bars + 2 * S;     // [2] accumulators complete
+    uint64_t *tempty_bar = tfull_bar + 2;   // [2] accumulators read
+    uint64_t *drain_bar = tempty_bar + 2;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    int *sh_active = reinterpret_cast<int *>(tmem_holder + 2);
     int *tab = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + FewConfig::kBarBytes);
 
     const int warp = threadIdx.x >> 5;
@@ -191,21 +215,21 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
     const WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
     const int rank = static_cast<int>(cluster_ctarank());
     const int nsplit = static_cast<int>(cluster_nctarank());
-    const int tile = blockIdx.x / nsplit;
-    // Converter teams: at most one per ring slot.  A team's wait for the MMAs of block
-    // i - S tests one parity bit, which is unambiguous only if block i - 2S is known to be
-    // done; the team's previous block i - teams implies that up to block i - teams - S.
-    const int teams = S < FewConfig::kConvWarps ? S : FewConfig::kConvWarps;
-    const int team_size = MODE == kGemvPre ? 1 : FewConfig::kConvWarps / teams;
+    const int first_tile = blockIdx.x / nsplit, tile_step = gridDim.x / nsplit;
 
     if (warp == 0) {
-        for (int i = lane; i < 2 * S + 1; i += 32) mbar_init(bars + i, i < S ? 1 + team_size : 1);
+        for (int i = lane; i < 2 * S + 5; i += 32)
+            mbar_init(bars + i, i < S ? 2 : i == 2 * S + 2 || i == 2 * S + 3 ? 4 : 1);
         if (lane == 0) {
             *abort_flag = 0;
             tma_prefetch_desc(&tm_w);
             if (MODE == kGemvPre) tma_prefetch_desc(&tm_x);
         }
         fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, p.tmem_cols);
+        tmem_relinquish();
     }
     // The first kernel of a chain (kGemv; the split kernel before the others) waits for
     // what precedes it and only then lets the next one start.  So the later kernels of
@@ -219,18 +243,14 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
     uint32_t *tab_mask = reinterpret_cast<uint32_t *>(tab);   // [32] experts in use
     int *tab_pre = tab + 32;                                  // [32] experts in use before this word
     int *s_ids = tab + 64;                                    // [pairs] id of a token's first slot with it, or -1
-    float *s_wsum = reinterpret_cast<float *>(s_ids + pairs); // kUp: by entry, the weight (of all the token's slots)
-    uint32_t *s_mask = reinterpret_cast<uint32_t *>(s_wsum + pairs);  // kDown [active][2] tokens of each expert
-    uint16_t *s_ent = reinterpret_cast<uint16_t *>(s_mask + 2 * pairs);   // kUp: pairs of this CTA; kDown: by entry
-    uint16_t *s_off = s_ent + pairs;                          // kDown [active] end of each expert's entries
-    uint16_t *s_exp = s_off + pairs;                          // kDown [active] expert
-    __shared__ int sh_active, sh_expert, sh_count;
-    int ntok = p.tokens;
-    int expert = 0;
+    float *s_wsum = reinterpret_cast<float *>(s_ids + pairs); // [pairs] by entry: weight (of all the token's slots)
+    uint32_t *s_mask = reinterpret_cast<uint32_t *>(s_wsum + pairs);     // [active][2] tokens of each expert
+    uint16_t *s_ent = reinterpret_cast<uint16_t *>(s_mask + 2 * pairs);  // [pairs] by entry: first slot (pair)
+    uint16_t *s_off = s_ent + pairs;                          // [active] end of each expert's entries
+    uint16_t *s_exp = s_off + pairs;                          // [active] expert
     int active = 1;
     if constexpr (MODE >= kUp) {
         if (warp == 0) tab_mask[lane] = 0u;
-        if (threadIdx.x == 0) { sh_count = 0; sh_expert = 0; }
         __syncthreads();
         for (int q = threadIdx.x; q < pairs; q += NT) {
             int e = __ldcg(p.ids + q);
@@ -245,160 +265,200 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
         }
         __syncthreads();
         if (warp == 0) {
-            const uint32_t word = tab_mask[lane];
-            const int cnt = __popc(word);
+            const int cnt = __popc(tab_mask[lane]);
             int inc = cnt;
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
                 const int v = __shfl_up_sync(0xFFFFFFFFu, inc, s);
                 if (lane >= s) inc += v;
             }
-            const int before = inc - cnt;
-            tab_pre[lane] = before;
-            if (lane == 31) sh_active = inc;
-            if constexpr (MODE == kUp) {
-                const int a = blockIdx.y;
-                if (a >= before && a < inc) {
-                    uint32_t w = word;
-                    for (int s = before; s < a; ++s) w &= w - 1;
-                    sh_expert = lane * 32 + __ffs(w) - 1;
-                }
-            }
-        }
-        __syncthreads();
-        active = sh_active;
-        if constexpr (MODE == kUp) {
-            // the tokens of this CTA's expert, in order, from the blockIdx.z-th group of cap
-            expert = sh_expert;
-            if (warp == 0 && static_cast<int>(blockIdx.y) < active) {
-                const int first = blockIdx.z * p.cap;
-                int n = 0;
-                for (int q0 = 0; q0 < pairs; q0 += 32) {
-                    const bool hit = q0 + lane < pairs && s_ids[q0 + lane] == expert;
-                    const uint32_t m = __ballot_sync(0xFFFFFFFFu, hit);
-                    const int at = n + __popc(m & ((1u << lane) - 1)) - first;
-                    if (hit && at >= 0 && at < p.cap) {
-                        const int q = q0 + lane, token0 = q - q % p.topk;
-                        float w = 0.0f;
-                        for (int r = q; r < token0 + p.topk; ++r)
-                            if (__ldcg(p.ids + r) == expert) w += __ldcg(p.weights + r);
-                        s_ent[at] = static_cast<uint16_t>(q);
-                        s_wsum[at] = w;
-                    }
-                    n += __popc(m);
-                }
-                if (lane == 0) sh_count = max(0, min(n - first, p.cap));
-            }
-            __syncthreads();
-            ntok = sh_count;
-            if (ntok == 0) {   // no such expert or group of tokens; the same for the whole cluster
-                grid_dependency_wait();
-                return;
-            }
-        } else {
-            // entries of all active experts, grouped by expert
-            for (int a = threadIdx.x; a < active; a += NT) {
+            tab_pre[lane] = inc - cnt;
+            if (lane == 31) *sh_active = inc;
+            const int used = __shfl_sync(0xFFFFFFFFu, inc, 31);
+            for (int a = lane; a < used; a += 32) {
                 s_off[a] = 0;
                 s_mask[2 * a] = s_mask[2 * a + 1] = 0u;
             }
-            __syncthreads();
-            if (warp == 0) {
-                // few hundred slots: one warp counts, scans and fills in slot order
-                for (int q0 = 0; q0 < pairs; q0 += 32) {
-                    const int e = q0 + lane < pairs ? s_ids[q0 + lane] : -1;
-                    const int a = e < 0 ? -1 - lane : tab_pre[e >> 5] + __popc(tab_mask[e >> 5] & ((1u << (e & 31)) - 1));
-                    const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
-                    if (a >= 0 && (same >> lane) == 1u) {   // the last holder of this expert
-                        s_off[a] += static_cast<uint16_t>(__popc(same));
-                        s_exp[a] = static_cast<uint16_t>(e);
-                    }
-                    __syncwarp();
+            __syncwarp();
+            // one warp counts, scans and fills, in slot order (the order is the same in every CTA)
+            auto rank_of = [&](int e) {
+                return e < 0 ? -1 - lane : tab_pre[e >> 5] + __popc(tab_mask[e >> 5] & ((1u << (e & 31)) - 1));
+            };
+            for (int q0 = 0; q0 < pairs; q0 += 32) {
+                const int e = q0 + lane < pairs ? s_ids[q0 + lane] : -1;
+                const int a = rank_of(e);
+                const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
+                if (a >= 0 && (same >> lane) == 1u) {   // the last holder of this expert
+                    s_off[a] += static_cast<uint16_t>(__popc(same));
+                    s_exp[a] = static_cast<uint16_t>(e);
                 }
-                int run = 0;
-                for (int a0 = 0; a0 < active; a0 += 32) {
-                    const int cnt = a0 + lane < active ? s_off[a0 + lane] : 0;
-                    int inc = cnt;
+                __syncwarp();
+            }
+            int run = 0;
+            for (int a0 = 0; a0 < used; a0 += 32) {
+                const int n = a0 + lane < used ? s_off[a0 + lane] : 0;
+                int sum = n;
 #pragma unroll
-                    for (int s = 1; s < 32; s <<= 1) {
-                        const int v = __shfl_up_sync(0xFFFFFFFFu, inc, s);
-                        if (lane >= s) inc += v;
-                    }
-                    if (a0 + lane < active) s_off[a0 + lane] = static_cast<uint16_t>(run + inc - cnt);
-                    run += __shfl_sync(0xFFFFFFFFu, inc, 31);
-                    __syncwarp();
+                for (int s = 1; s < 32; s <<= 1) {
+                    const int v = __shfl_up_sync(0xFFFFFFFFu, sum, s);
+                    if (lane >= s) sum += v;
                 }
-                for (int q0 = 0; q0 < pairs; q0 += 32) {
-                    const int q = q0 + lane;
-                    const int e = q < pairs ? s_ids[q] : -1;
-                    const int a = e < 0 ? -1 - lane : tab_pre[e >> 5] + __popc(tab_mask[e >> 5] & ((1u << (e & 31)) - 1));
-                    const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
-                    if (a >= 0) {
-                        const int at = s_off[a] + __popc(same & ((1u << lane) - 1));
-                        s_ent[at] = static_cast<uint16_t>(q);
-                        atomicOr(&s_mask[2 * a + (q / p.topk >> 5)], 1u << (q / p.topk & 31));
+                if (a0 + lane < used) s_off[a0 + lane] = static_cast<uint16_t>(run + sum - n);
+                run += __shfl_sync(0xFFFFFFFFu, sum, 31);
+            }
+            __syncwarp();
+            for (int q0 = 0; q0 < pairs; q0 += 32) {
+                const int q = q0 + lane;
+                const int e = q < pairs ? s_ids[q] : -1;
+                const int a = rank_of(e);
+                const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
+                if (a >= 0) {
+                    const int at = s_off[a] + __popc(same & ((1u << lane) - 1));
+                    const int token = q / p.topk;
+                    s_ent[at] = static_cast<uint16_t>(q);
+                    if constexpr (MODE == kUp) {
+                        float w = 0.0f;
+                        for (int r = q; r < (token + 1) * p.topk; ++r)
+                            if (__ldcg(p.ids + r) == e) w += __ldcg(p.weights + r);
+                        s_wsum[at] = w;
                     }
-                    __syncwarp();
-                    if (a >= 0 && (same >> lane) == 1u) s_off[a] += static_cast<uint16_t>(__popc(same));
-                    __syncwarp();
+                    atomicOr(&s_mask[2 * a + (token >> 5)], 1u << (token & 31));
                 }
+                __syncwarp();
+                if (a >= 0 && (same >> lane) == 1u) s_off[a] += static_cast<uint16_t>(__popc(same));
+                __syncwarp();
             }
         }
-    }
-    if (warp == 1) {
-        tmem_alloc(tmem_holder, p.tmem_cols);
-        tmem_relinquish();
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_holder;
-
-    // this CTA's K-blocks
-    const int total = MODE == kDown ? active * p.kblocks : p.kblocks;
+    if constexpr (MODE >= kUp) active = *sh_active;
+    const int total = MODE == kDown ? active * p.kblocks : p.kblocks;     // K-blocks of a tile
+    const int num_tiles = MODE == kUp ? active * p.row_tiles * p.chunks : p.row_tiles;
     const int k_begin = static_cast<int>(static_cast<int64_t>(total) * rank / nsplit);
-    const int nblk = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / nsplit) - k_begin;
-    const int row0 = tile * (MODE == kUp ? 128 : ROWS);   // first weight row (kUp: of the gate half)
+    const int k_count = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / nsplit) - k_begin;
+
+    // Tile w: kUp's go expert by expert, an expert's groups of tokens next to each other
+    // (they read the same weights).  False: no tokens.
+    auto get_tile = [&](int w, FewTile &t) -> bool {
+        t.begin = k_begin;
+        t.nblk = k_count;
+        t.ent = 0;
+        if constexpr (MODE == kUp) {
+            const int chunk = w % p.chunks, at = w / p.chunks;
+            const int a = at / p.row_tiles;
+            const int first = (a ? s_off[a - 1] : 0) + chunk * p.cap;
+            t.row0 = (at - a * p.row_tiles) * 128;
+            t.expert = s_exp[a];
+            t.ent = first;
+            t.ntok = min(static_cast<int>(s_off[a]) - first, p.cap);
+            return t.ntok > 0;
+        } else {
+            t.expert = 0;
+            t.row0 = w * ROWS;
+            t.ntok = p.tokens;
+            return true;
+        }
+    };
+    // Four results of one token at weight rows n .. n + 3 (kUp: a warp holds the token's 128).
+    auto store = [&](const FewTile &tile, int t, int n, float (&o)[4]) {
+        if constexpr (MODE == kUp) {
+            const float w = s_wsum[tile.ent + t];
+            uint32_t m = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                o[c] *= w;
+                m = max(m, __float_as_uint(o[c]) & 0x7FFFFFFFu);
+            }
+#pragma unroll
+            for (int s = 1; s < 8; s <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));   // a group of 32
+            const uint32_t e8 = max(m >> 23, 11u);
+            const float inv = inverse_scale(e8);
+            uint32_t hi, lo;
+            split4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv, hi, lo);
+            const int64_t row = 2 * static_cast<int64_t>(s_ent[tile.ent + t]);
+            *reinterpret_cast<uint32_t *>(p.out_codes + row * p.inner + n) = hi;
+            *reinterpret_cast<uint32_t *>(p.out_codes + (row + 1) * p.inner + n) = lo;
+            if ((lane & 7) == 0) {
+                uint8_t *sf = p.out_scales + ((tile.row0 >> 7) * 2 * static_cast<int64_t>(pairs) + row) * 4 + (lane >> 3);
+                sf[0] = static_cast<uint8_t>(hi_scale(e8));
+                sf[4] = static_cast<uint8_t>(lo_scale(e8));
+            }
+        } else if (n < p.rows) {
+            if (p.f32) {
+                if (p.c) {
+                    const float4 c =
+                        __ldcg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.c) + t * p.ldc + n));
+                    o[0] += c.x; o[1] += c.y; o[2] += c.z; o[3] += c.w;
+                }
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.d) + t * p.ldd + n) =
+                    make_float4(o[0], o[1], o[2], o[3]);
+            } else {
+                if (p.c) {
+                    const uint2 c =
+                        __ldcg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.c) + t * p.ldc + n));
+                    o[0] += __uint_as_float(c.x << 16);
+                    o[1] += __uint_as_float(c.x & 0xFFFF0000u);
+                    o[2] += __uint_as_float(c.y << 16);
+                    o[3] += __uint_as_float(c.y & 0xFFFF0000u);
+                }
+                const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.d) + t * p.ldd + n) =
+                    make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+            }
+        }
+    };
+    auto gated = [](float g, float u) { return g / (1.0f + expf(-g)) * u; };
+
+    FewTile tile;
+    float *part = reinterpret_cast<float *>(smem_a);   // nsplit > 1: [ntok][ROWS], in operand row order
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         int slot = 0;
         uint32_t phase = 0;
         uint32_t issued = 0;
-        bool drop = (p.debug_flags & DG_DEBUG_DROP_ONE_LOAD) && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
-        int a = MODE == kDown && total > 0 ? k_begin / p.kblocks : 0;
-        int kb = MODE == kDown && total > 0 ? k_begin - a * p.kblocks : k_begin;
-        for (int i = 0; i < nblk; ++i) {
-            if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) break;
-            if (drop) drop = false;   // diagnostic: this slot never fills
-            else issued |= 1u << slot;
-            if ((issued >> slot & 1u) && elect_one()) {
-                const int e = MODE == kDown ? s_exp[a] : expert;
-                const int slice = FP4 ? kb : kb >> 2;
-                const uint32_t *sf = p.sf + e * p.sf_expert + static_cast<int64_t>(slice) * p.sf_ld;
-                uint32_t sf_bytes[HALVES];
-                uint32_t bytes = HALVES * (FP4 ? 8192 : 16384);
+        bool drop = (p.debug_flags & DG_DEBUG_DROP_ONE_LOAD) && blockIdx.x == 0;
+        for (int w = first_tile; w < num_tiles; w += tile_step) {
+            if (!get_tile(w, tile)) continue;
+            int a = 0, kb = tile.begin;
+            if (MODE == kDown) { a = kb / p.kblocks; kb -= a * p.kblocks; }
+            for (int i = 0; i < tile.nblk; ++i) {
+                if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto producer_done;
+                if (drop) drop = false;   // diagnostic: this slot never fills
+                else issued |= 1u << slot;
+                if ((issued >> slot & 1u) && elect_one()) {
+                    const int e = MODE == kDown ? s_exp[a] : tile.expert;
+                    const int slice = FP4 ? kb : kb >> 2;
+                    const uint32_t *sf = p.sf + e * p.sf_expert + static_cast<int64_t>(slice) * p.sf_ld;
+                    uint32_t sf_bytes[HALVES];
+                    uint32_t bytes = HALVES * (FP4 ? 8192 : 16384);
 #pragma unroll
-                for (int h = 0; h < HALVES; ++h) {
-                    const int left = MODE == kUp ? 128 : p.sf_ld - (row0 + h * 128);
-                    sf_bytes[h] = left >= 128 ? 512u : left > 0 ? 4u * static_cast<uint32_t>(left) : 0u;
-                    bytes += sf_bytes[h];
-                }
-                mbar_arrive_expect_tx(&full_bar[slot], bytes);
+                    for (int h = 0; h < HALVES; ++h) {
+                        const int left = MODE == kUp ? 128 : p.sf_ld - (tile.row0 + h * 128);
+                        sf_bytes[h] = left >= 128 ? 512u : left > 0 ? 4u * static_cast<uint32_t>(left) : 0u;
+                        bytes += sf_bytes[h];
+                    }
+                    mbar_arrive_expect_tx(&full_bar[slot], bytes);
 #pragma unroll
-                for (int h = 0; h < HALVES; ++h) {
-                    const int r = MODE == kUp ? h * p.inner + row0 : row0 + h * 128;
-                    // (a half past the last row reads zeros)
-                    const int64_t r4 = (static_cast<int64_t>(e) * p.rows + r) >> 2;
-                    tma_load_3d(smem_a + (slot * HALVES + h) * 16384, &tm_w, &full_bar[slot], kb * 128,
-                                static_cast<int32_t>(r4), 0);
-                    if (sf_bytes[h])
-                        bulk_load(smem_sfa + (slot * HALVES + h) * 512, sf + r, sf_bytes[h], &full_bar[slot]);
+                    for (int h = 0; h < HALVES; ++h) {
+                        const int r = MODE == kUp ? h * p.inner + tile.row0 : tile.row0 + h * 128;
+                        // (a half past the last row reads zeros or the next expert's rows; unused)
+                        const int64_t r4 = (static_cast<int64_t>(e) * p.rows + r) >> 2;
+                        tma_load_3d(smem_a + (slot * HALVES + h) * 16384, &tm_w, &full_bar[slot], kb * 128,
+                                    static_cast<int32_t>(r4), 0);
+                        if (sf_bytes[h])
+                            bulk_load(smem_sfa + (slot * HALVES + h) * 512, sf + r, sf_bytes[h], &full_bar[slot]);
+                    }
                 }
+                __syncwarp();
+                if (++kb == p.kblocks && MODE == kDown) { kb = 0; ++a; }
+                if (++slot == S) { slot = 0; phase ^= 1; }
             }
-            __syncwarp();
-            if (++kb == p.kblocks && MODE == kDown) { kb = 0; ++a; }
-            if (++slot == S) { slot = 0; phase ^= 1; }
         }
+    producer_done:
         // Normally every load has landed once the MMAs are done.  After a wait that ran
         // out, never leave with loads in flight: give them the time limit once more.
         named_bar_sync(2, 64);   // the MMA warp is done with its waits
@@ -411,93 +471,105 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        int slot = 0;
-        uint32_t phase = 0;
+        int slot = 0, acc = 0, g = 0;
+        uint32_t phase = 0, acc_phase = 0;
         const uint64_t a_base = make_desc_kmajor_sw128(smem_u32(smem_a));
         const uint64_t b_base = make_desc_kmajor_sw128(smem_u32(smem_b));
-        const uint32_t sf_tmem = tmem_base + HALVES * ncols;   // two slots of 4 HALVES + 4 columns
-        // columns in use: the tokens', rounded up to the MMA's step of 16
-        const int n_used = MODE == kUp ? (2 * ntok + 15) / 16 * 16 : ncols;
-        const uint32_t idesc = make_idesc_mxf8(128, n_used, 0, 0) | (FP4 ? 5u << 7 : 0u);
-        int kb = MODE == kDown && total > 0 ? k_begin % p.kblocks : k_begin;
-        for (int i = 0; i < nblk; ++i) {
-            if (!mbar_wait_warp(&full_bar[slot], phase, ctl, DG_DEV_TIMEOUT)) break;
+        const uint32_t sf_tmem = tmem_base + p.accs * HALVES * ncols;   // two slots of 4 HALVES + 4 columns
+        for (int w = first_tile; w < num_tiles; w += tile_step) {
+            if (!get_tile(w, tile)) continue;
+            if (!mbar_wait_warp(&tempty_bar[acc], acc_phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto mma_done;
             tc_fence_after_sync();
-            if (elect_one()) {
-                const uint32_t sf = sf_tmem + (i & 1) * (4 * HALVES + 4);
-#pragma unroll
-                for (int h = 0; h < HALVES; ++h)
-                    tc_cp_32x128b_warpx4(sf + 4 * h,
-                                         make_desc_sf_32x128b(smem_u32(smem_sfa + (slot * HALVES + h) * 512)));
-                tc_cp_32x128b_warpx4(sf + 4 * HALVES, make_desc_sf_32x128b(smem_u32(smem_sfb + slot * 512)));
-                const uint64_t b_desc = b_base + static_cast<uint64_t>(slot * (b_bytes >> 4));
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    // scale byte: the activations' and FP4 weights' k-th 32 K, FP8 weights' 128-K block
-                    const uint32_t id = idesc | (static_cast<uint32_t>(k) << 4) |
-                                        (static_cast<uint32_t>(FP4 ? k : kb & 3) << 29);
+            const uint32_t d_tmem = tmem_base + acc * HALVES * ncols;
+            // columns in use: the tokens', rounded up to the MMA's step of 16
+            const int n_used = MODE == kUp ? (2 * tile.ntok + 15) / 16 * 16 : ncols;
+            const uint32_t idesc = make_idesc_mxf8(128, n_used, 0, 0) | (FP4 ? 5u << 7 : 0u);   // A: E2M1 or E4M3
+            int kb = MODE == kDown ? tile.begin % p.kblocks : tile.begin;
+            for (int i = 0; i < tile.nblk; ++i, ++g) {
+                if (!mbar_wait_warp(&full_bar[slot], phase, ctl, DG_DEV_TIMEOUT)) goto mma_done;
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    const uint32_t sf = sf_tmem + (g & 1) * (4 * HALVES + 4);
 #pragma unroll
                     for (int h = 0; h < HALVES; ++h)
-                        tc_mma_mxf8(tmem_base + h * ncols,
-                                    a_base + static_cast<uint64_t>((slot * HALVES + h) * 1024 + 2 * k), b_desc + 2 * k,
-                                    id, sf + 4 * h, sf + 4 * HALVES, (i | k) != 0);
+                        tc_cp_32x128b_warpx4(sf + 4 * h,
+                                             make_desc_sf_32x128b(smem_u32(smem_sfa + (slot * HALVES + h) * 512)));
+                    tc_cp_32x128b_warpx4(sf + 4 * HALVES, make_desc_sf_32x128b(smem_u32(smem_sfb + slot * 512)));
+                    const uint64_t b_desc = b_base + static_cast<uint64_t>(slot * (b_bytes >> 4));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // scale byte: the activations' and FP4 weights' k-th 32 K, FP8 weights' 128-K block
+                        const uint32_t id = idesc | (static_cast<uint32_t>(k) << 4) |
+                                            (static_cast<uint32_t>(FP4 ? k : kb & 3) << 29);
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h)
+                            tc_mma_mxf8(d_tmem + h * ncols,
+                                        a_base + static_cast<uint64_t>((slot * HALVES + h) * 1024 + 2 * k),
+                                        b_desc + 2 * k, id, sf + 4 * h, sf + 4 * HALVES, (i | k) != 0);
+                    }
+                    tc_commit(&empty_bar[slot]);
                 }
-                tc_commit(&empty_bar[slot]);
+                __syncwarp();
+                if (++kb == p.kblocks) kb = 0;
+                if (++slot == S) { slot = 0; phase ^= 1; }
             }
+            if (elect_one()) tc_commit(&tfull_bar[acc]);
             __syncwarp();
-            if (++kb == p.kblocks) kb = 0;
-            if (++slot == S) { slot = 0; phase ^= 1; }
+            if (++acc == p.accs) { acc = 0; acc_phase ^= 1; }
         }
-        // the accumulators are complete; TMEM is not freed before every MMA has finished
+    mma_done:
+        // TMEM is not freed before every MMA has finished
         if (elect_one()) {
-            tc_commit(tfull_bar);
-            mbar_wait_drain(tfull_bar, 0, ctl);
+            tc_commit(drain_bar);
+            mbar_wait_drain(drain_bar, 0, ctl);
         }
         __syncwarp();
         named_bar_sync(2, 64);
-    } else {
+    } else if (warp >= FewConfig::kFirstB) {
         // ------------------------------------------------------------ the narrow operand
-        const int cw = warp - FewConfig::kFirstConv;
+        // The warps take the K-blocks in turn, at most as many warps as ring slots: a
+        // wait for the MMAs of block g - S tests one parity bit, which is unambiguous only
+        // if block g - 2S is known to be done; a warp's previous block g - teams implies that
+        // up to block g - teams - S.
+        const int teams = S < FewConfig::kBWarps ? S : FewConfig::kBWarps;
+        const int bw = warp - FewConfig::kFirstB;
+        const int q16 = lane & 15, sub = lane >> 4;   // two tokens at a time, 16 lanes each
         if constexpr (MODE != kGemv) grid_dependency_wait();
-        if constexpr (MODE == kGemvPre) {
-            for (int i = cw; i < nblk && cw == 0; ++i) {
-                const int slot = i % S;
-                if (!mbar_wait_warp(&empty_bar[slot], ((i / S) & 1) ^ 1, ctl, DG_DEV_TIMEOUT)) break;
-                if (elect_one()) {
-                    const int kb = k_begin + i;
-                    mbar_arrive_expect_tx(&full_bar[slot], b_bytes + 512);
-                    tma_load_2d(smem_b + slot * b_bytes, &tm_x, &full_bar[slot], kb * 128, 0);
-                    bulk_load(smem_sfb + slot * 512, p.scales + kb * 128, 512, &full_bar[slot]);
-                }
-                __syncwarp();
-            }
-        } else {
-            const int team = cw / team_size, member = cw % team_size;
-            const int q16 = lane & 15, sub = lane >> 4;   // two tokens at a time, 16 lanes each
-            int a = 0, kb = k_begin + team;
-            if (MODE == kDown && total > 0) { a = kb / p.kblocks; kb -= a * p.kblocks; }
-            for (int i = team < teams ? team : nblk; i < nblk; i += teams) {
-                const int slot = i % S;
-                if (!mbar_wait_warp(&empty_bar[slot], ((i / S) & 1) ^ 1, ctl, DG_DEV_TIMEOUT)) break;
+        int g = 0;   // K-blocks of the tiles before
+        for (int w = first_tile; w < num_tiles && bw < teams; w += tile_step) {
+            if (!get_tile(w, tile)) continue;
+            for (int i = (bw + teams - g % teams) % teams; i < tile.nblk; i += teams) {
+                const int slot = (g + i) % S;
+                if (!mbar_wait_warp(&empty_bar[slot], (((g + i) / S) & 1) ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
                 uint8_t *tile_b = smem_b + slot * b_bytes;
                 uint8_t *tile_sf = smem_sfb + slot * 512;
-                if constexpr (MODE == kGemv) {
-                    for (int t0 = 8 * member; t0 < ntok; t0 += 8 * team_size) {
+                int kb = tile.begin + i, a = 0;
+                if (MODE == kDown) { a = kb / p.kblocks; kb -= a * p.kblocks; }
+                if constexpr (MODE == kGemvPre) {
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&full_bar[slot], b_bytes + 512);
+                        tma_load_2d(tile_b, &tm_x, &full_bar[slot], kb * 128, 0);
+                        bulk_load(tile_sf, p.scales + kb * 128, 512, &full_bar[slot]);
+                    }
+                    __syncwarp();
+                    continue;
+                } else if constexpr (MODE == kGemv) {
+                    for (int t0 = 0; t0 < tile.ntok; t0 += 8) {
                         uint4 v[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
                             const int t = t0 + 2 * u + sub;
                             v[u] = make_uint4(0u, 0u, 0u, 0u);
-                            if (t < ntok)
+                            if (t < tile.ntok)
                                 v[u] = __ldcg(reinterpret_cast<const uint4 *>(p.x + t * p.ldx + kb * 128 + q16 * 8));
                         }
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
-                            if (t0 + 2 * u >= ntok) break;
+                            if (t0 + 2 * u >= tile.ntok) break;
                             const int t = t0 + 2 * u + sub;
                             uint2 hi, lo;
                             const uint32_t e8 = split_bf16(v[u], hi, lo);
-                            if (t >= ntok) continue;
+                            if (t >= tile.ntok) continue;
                             // columns 2t and 2t + 1 (rows of 128 bytes, 128-byte swizzle)
                             const uint32_t n = 2 * t;
                             const uint32_t off = (q16 & 1) * 8;
@@ -510,12 +582,13 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
                                 s[16] = static_cast<uint8_t>(lo_scale(e8));
                             }
                         }
+                        __syncwarp();
                     }
                 } else {
-                    int begin = 0, end = ntok;
+                    int begin = tile.ent, end = tile.ent + tile.ntok;
                     if constexpr (MODE == kDown) {
                         // columns of tokens that do not use this expert are zero, codes and scales
-                        for (int t = 2 * member + sub; t < p.cap; t += 2 * team_size) {
+                        for (int t = sub; t < p.cap; t += 2) {
                             if (s_mask[2 * a + (t >> 5)] >> (t & 31) & 1u) continue;
                             reinterpret_cast<uint4 *>(tile_b + t * 256)[q16] = make_uint4(0u, 0u, 0u, 0u);
                             if (q16 < 2) reinterpret_cast<uint32_t *>(tile_sf)[sf_word(2 * t + q16)] = 0u;
@@ -527,7 +600,7 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
                     const int64_t k = static_cast<int64_t>(p.kblocks) * 128;
                     const uint8_t *src = p.codes + (q16 >> 3) * k + kb * 128 + (q16 & 7) * 16;
                     const uint32_t *src_sf = p.scales + static_cast<int64_t>(kb) * 2 * p.src_rows + (q16 & 1);
-                    for (int t0 = begin + 8 * member; t0 < end; t0 += 8 * team_size) {
+                    for (int t0 = begin; t0 < end; t0 += 8) {
                         uint4 v[4];
                         uint32_t sf[4];
                         int col[4];
@@ -538,7 +611,7 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
                                 const int pair = s_ent[t];
                                 const int token = pair / p.topk;
                                 const int row = MODE == kUp ? token : pair;
-                                col[u] = MODE == kUp ? t : token;
+                                col[u] = MODE == kUp ? t - begin : token;
                                 v[u] = __ldcg(reinterpret_cast<const uint4 *>(src + 2 * row * k));
                                 sf[u] = __ldcg(src_sf + 2 * row);
                             }
@@ -556,35 +629,71 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full_bar[slot]);
-                kb += teams;
-                if constexpr (MODE == kDown)
-                    while (kb >= p.kblocks) { kb -= p.kblocks; ++a; }
             }
+            g += tile.nblk;
         }
-
-        // ------------------------------------------------------------ accumulators -> shared memory
-        // (the ring is free: every load has landed and every MMA has read its slot)
-        float *part = reinterpret_cast<float *>(smem_a);      // [ntok][ROWS], in operand row order
+    b_done:
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ epilogue
         const uint32_t quad = warp & 3;
-        const int group = cw >> 2;
-        if (nblk > 0) {
-            __all_sync(0xFFFFFFFFu, mbar_wait(tfull_bar, 0, ctl, DG_DEV_TIMEOUT));
+        const int id = threadIdx.x - 32 * FewConfig::kFirstEpi;   // 0..127
+        int acc = 0, buf = 0;
+        uint32_t acc_phase = 0;
+        if constexpr (MODE != kGemv) grid_dependency_wait();       // C, and memory that the output may share
+        for (int w = first_tile; w < num_tiles; w += tile_step) {
+            if (!get_tile(w, tile)) continue;
+            // the four warps go on or give up together
+            const bool ok = mbar_wait_warp(&tfull_bar[acc], acc_phase, ctl, DG_DEV_TIMEOUT);
+            if (!named_bar_and(1, 128, ok)) break;
             tc_fence_after_sync();
-        }
-        const int half = HALVES == 2 ? group : 0;
-        for (int c = HALVES == 2 ? 0 : group; c * 8 < ntok; c += HALVES == 2 ? 1 : 2) {
-            uint32_t v[16] = {};
-            if (nblk > 0) {
-                tmem_ld_32x32b_x16(tmem_base + ((quad * 32) << 16) + half * ncols + c * 16, v);
-                tmem_ld_wait();
-                reg_fence16(v);
-            }
+            for (int t0 = 0; t0 < tile.ntok; t0 += 8) {
+                uint32_t v[HALVES][16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c * 8 + j < ntok)
-                    part[(c * 8 + j) * ROWS + half * 128 + quad * 32 + lane] =
-                        __uint_as_float(v[2 * j]) + __uint_as_float(v[2 * j + 1]);
+                for (int h = 0; h < HALVES; ++h) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[h][j] = 0u;
+                    if (tile.nblk > 0)
+                        tmem_ld_32x32b_x16(tmem_base + ((quad * 32) << 16) + (acc * HALVES + h) * ncols + 2 * t0, v[h]);
+                }
+                tmem_ld_wait();
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) reg_fence16(v[h]);
+                if (t0 + 8 >= tile.ntok) {   // the accumulators are read
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tempty_bar[acc]);
+                }
+                float *out = nsplit > 1 ? part + t0 * ROWS : smem_out + buf * 8 * OUT;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (t0 + j >= tile.ntok) break;
+                    float r[HALVES];
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h)
+                        r[h] = __uint_as_float(v[h][2 * j]) + __uint_as_float(v[h][2 * j + 1]);
+                    if (MODE == kUp && nsplit == 1) {
+                        out[j * OUT + quad * 32 + lane] = gated(r[0], r[HALVES - 1]);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h) out[j * ROWS + h * 128 + quad * 32 + lane] = r[h];
+                    }
+                }
+                if (nsplit > 1) continue;
+                named_bar_sync(1, 128);
+                const int n = min(8, tile.ntok - t0) * (OUT / 4);
+                for (int q = id; q < n; q += 128) {
+                    const int t = q / (OUT / 4), l = q % (OUT / 4);
+                    float o[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[c] = out[t * OUT + (l >> 5) * 128 + 32 * c + (l & 31)];
+                    store(tile, t0 + t, tile.row0 + 4 * l, o);
+                }
+                buf ^= 1;
+            }
+            if (++acc == p.accs) { acc = 0; acc_phase ^= 1; }
         }
+        __syncwarp();
     }
 
     tc_fence_before_sync();
@@ -593,76 +702,30 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
         tc_fence_after_sync();
         tmem_dealloc(tmem_base, p.tmem_cols);
     }
-    // (the grid must not end before the one it depends on, whoever else waited)
-    if constexpr (MODE != kGemv) grid_dependency_wait();
-    if (nsplit > 1) cluster_sync();
-    // ---------------------------------------------------------------- sum over the cluster, output
-    const uint32_t part0 = smem_u32(smem_a);
-    auto load = [&](int idx) {
-        float s = 0.0f;
-        if (nsplit == 1) return reinterpret_cast<const float *>(smem_a)[idx];
-        for (int r = 0; r < nsplit; ++r) s += ld_shared_cluster_f32(mapa_shared(part0 + 4u * idx, r));
-        return s;
-    };
-    constexpr int QUADS = MODE == kUp ? 32 : HALVES * 32;     // groups of 4 outputs per token
-    for (int q = rank * NT + threadIdx.x; q < ntok * QUADS; q += nsplit * NT) {
-        const int t = q / QUADS, l = q % QUADS;
-        const int base = t * ROWS + (l >> 5) * 128 + (l & 31);
-        float o[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] = load(base + 32 * c);
-        const int n = row0 + 4 * l;
-        if constexpr (MODE == kUp) {
+    if (nsplit == 1) return;
+    // ---------------------------------------------------------------- sum over the cluster (one tile)
+    cluster_sync();
+    if (first_tile < num_tiles && get_tile(first_tile, tile)) {
+        const uint32_t part0 = smem_u32(smem_a);
+        auto sum = [&](int idx) {
+            float s = 0.0f;
+            for (int r = 0; r < nsplit; ++r) s += ld_shared_cluster_f32(mapa_shared(part0 + 4u * idx, r));
+            return s;
+        };
+        for (int q = rank * NT + threadIdx.x; q < tile.ntok * (OUT / 4); q += nsplit * NT) {
+            const int t = q / (OUT / 4), l = q % (OUT / 4);
+            const int base = t * ROWS + (l >> 5) * 128 + (l & 31);
+            float o[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const float u = load(base + 128 + 32 * c);
-                o[c] = o[c] / (1.0f + expf(-o[c])) * u;
+                o[c] = sum(base + 32 * c);
+                if constexpr (MODE == kUp) o[c] = gated(o[c], sum(base + 128 + 32 * c));
             }
-            // a warp holds one token's 128 values; 8 lanes a group of 32
-            const float w = s_wsum[t];
-            uint32_t m = 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                o[c] *= w;
-                m = max(m, __float_as_uint(o[c]) & 0x7FFFFFFFu);
-            }
-#pragma unroll
-            for (int s = 1; s < 8; s <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-            const uint32_t e8 = max(m >> 23, 11u);
-            const float inv = inverse_scale(e8);
-            uint32_t hi, lo;
-            split4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv, hi, lo);
-            const int64_t row = 2 * static_cast<int64_t>(s_ent[t]);
-            *reinterpret_cast<uint32_t *>(p.out_codes + row * p.inner + n) = hi;
-            *reinterpret_cast<uint32_t *>(p.out_codes + (row + 1) * p.inner + n) = lo;
-            if ((lane & 7) == 0) {
-                uint8_t *sf = p.out_scales + ((row0 >> 7) * 2 * static_cast<int64_t>(pairs) + row) * 4 + (lane >> 3);
-                sf[0] = static_cast<uint8_t>(hi_scale(e8));
-                sf[4] = static_cast<uint8_t>(lo_scale(e8));
-            }
-        } else if (n < p.rows) {
-            if (p.f32) {
-                if (p.c) {
-                    const float4 c = __ldcg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.c) + t * p.ldc + n));
-                    o[0] += c.x; o[1] += c.y; o[2] += c.z; o[3] += c.w;
-                }
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.d) + t * p.ldd + n) =
-                    make_float4(o[0], o[1], o[2], o[3]);
-            } else {
-                if (p.c) {
-                    const uint2 c = __ldcg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.c) + t * p.ldc + n));
-                    o[0] += __uint_as_float(c.x << 16);
-                    o[1] += __uint_as_float(c.x & 0xFFFF0000u);
-                    o[2] += __uint_as_float(c.y << 16);
-                    o[3] += __uint_as_float(c.y & 0xFFFF0000u);
-                }
-                const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]), b = __floats2bfloat162_rn(o[2], o[3]);
-                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.d) + t * p.ldd + n) =
-                    make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-            }
+            store(tile, t, tile.row0 + 4 * l, o);
         }
     }
-    if (nsplit > 1) cluster_sync();   // peers may still read this CTA's partial results
+    __syncwarp();
+    cluster_sync();   // peers may still read this CTA's partial results
 }
 
 }  // namespace dg
