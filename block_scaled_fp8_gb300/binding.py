@@ -110,7 +110,7 @@ def lib():
             L.dg_bf16_gemv_workspace_bytes.restype = i64
             L.dg_moe_route.argtypes = [P, i64, i32, P, P, P, i32, i32, i32, i32, i32, f32, P]
             L.dg_moe_route.restype = i32
-            L.dg_moe_layer_workspace_bytes.argtypes = [i32, i32, i32, i32]
+            L.dg_moe_layer_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
             L.dg_moe_layer_workspace_bytes.restype = i64
             for f in ("dg_moe_fp4_layer", "dg_moe_fp8_layer"):
                 getattr(L, f).argtypes = [P, i64, P, P, P, P, P, P, P, i64, P, i64, i32, i32, i32, i32, i32, P, i64,
@@ -516,8 +516,8 @@ def dg_moe_route(logits, ids, weights, bias=None, scoring: str = "softmax", reno
     return ids, weights
 
 
-def moe_layer_workspace_bytes(t: int, topk: int, h: int, i: int) -> int:
-    return int(lib().dg_moe_layer_workspace_bytes(t, topk, h, i))
+def moe_layer_workspace_bytes(t: int, topk: int, h: int, i: int, experts: int) -> int:
+    return int(lib().dg_moe_layer_workspace_bytes(t, topk, h, i, experts))
 
 
 def _moe_layer(fn: str, fp4: bool, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream):
@@ -538,7 +538,7 @@ def _moe_layer(fn: str, fp4: bool, x, ids, weights, w1, sf1, w2, sf2, y, c, work
     assert y.dtype == torch.bfloat16 and y.shape == (t, h) and y.stride(1) == 1
     assert c is None or (c.dtype == torch.bfloat16 and c.shape == (t, h) and c.stride(1) == 1)
     L = lib()
-    ws, nbytes = _workspace(L.dg_moe_layer_workspace_bytes(t, topk, h, i), workspace, y.device, stream)
+    ws, nbytes = _workspace(L.dg_moe_layer_workspace_bytes(t, topk, h, i, e), workspace, y.device, stream)
     _check(fn, getattr(L, fn)(
         _p(x), _ld(x), _p(ids), _p(weights), _p(w1), _p(sf1), _p(w2), _p(sf2), _p(c),
         0 if c is None else _ld(c), _p(y), _ld(y), t, h, i, e, topk, _p(ws), nbytes, _p(status),
@@ -551,7 +551,7 @@ def dg_moe_fp4_layer(x, ids, weights, w1, sf1, w2, sf2, y, c=None, workspace=Non
     empty slot), for 1..64 tokens.  x bf16 [T, H]; ids int32 and weights float32 [T, topk];
     w1 uint8 [E, 2I, H/2] (gate rows, then up rows) and w2 uint8 [E, H, I/2], packed E2M1;
     sf1 packed int32 [E, H/128, 2I], sf2 [E, I/128, H]; y (and c) bf16 [T, H].  workspace:
-    a device buffer of moe_layer_workspace_bytes(T, topk, H, I) bytes (made here if not given)."""
+    a device buffer of moe_layer_workspace_bytes(T, topk, H, I, E) bytes (made here if not given)."""
     return _moe_layer("dg_moe_fp4_layer", True, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream)
 
 

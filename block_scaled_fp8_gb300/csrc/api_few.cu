@@ -79,7 +79,7 @@ dg_status layer(bool fp4, const void *x, int64_t ldx, const int32_t *ids, const 
     if (i != 0) {
         if (!x || !ids || !weights || !w1 || !sf1 || !w2 || !sf2 || !workspace) return DG_ERR_INVALID_ARG;
         if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(ids, 4) || !aligned(weights, 4)) return DG_ERR_ALIGNMENT;
-        if (ldx < h || workspace_bytes < layer_workspace_bytes(t, topk, h, i)) return DG_ERR_INVALID_ARG;
+        if (ldx < h || workspace_bytes < layer_workspace_bytes(t, topk, h, i, experts)) return DG_ERR_INVALID_ARG;
         const unsigned row = fp4 ? 32 : 16;
         if (!aligned(w1, row) || !aligned(w2, row) || !aligned(sf1, 16) || !aligned(sf2, 16) || !aligned(workspace, 16))
             return DG_ERR_ALIGNMENT;
@@ -174,8 +174,8 @@ int64_t dg_bf16_gemv_workspace_bytes(int m, int n, int k) {
     return m < 0 || n < 0 || k < 0 ? -1 : few_workspace_bytes(m, n, k);
 }
 
-int64_t dg_moe_layer_workspace_bytes(int t, int topk, int h, int i) {
-    return t < 0 || topk < 0 || h < 0 || i < 0 ? -1 : layer_workspace_bytes(t, topk, h, i);
+int64_t dg_moe_layer_workspace_bytes(int t, int topk, int h, int i, int experts) {
+    return t < 0 || topk < 0 || h < 0 || i < 0 || experts < 0 ? -1 : layer_workspace_bytes(t, topk, h, i, experts);
 }
 
 dg_status dg_moe_fp4_layer(const void *x, int64_t ldx, const int32_t *ids, const float *weights, const void *w1,

@@ -167,14 +167,14 @@ struct LayerParams {
     int64_t ldc;
     uint16_t *y;            // bf16 [t][ldy]
     int64_t ldy;
-    uint8_t *workspace;     // layer_workspace_bytes(t, topk, h, i)
+    uint8_t *workspace;     // layer_workspace_bytes(t, topk, h, i, experts)
     int t, h, i, experts, topk;
     int fp4;
     int32_t *status;
     uint64_t timeout_ns;
     uint32_t debug_flags;
 };
-int64_t layer_workspace_bytes(int64_t t, int64_t topk, int64_t h, int64_t i);
+int64_t layer_workspace_bytes(int64_t t, int64_t topk, int64_t h, int64_t i, int64_t experts);
 cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t stream);
 
 struct RouteParams {

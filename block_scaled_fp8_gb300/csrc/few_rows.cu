@@ -31,19 +31,6 @@ bool encode_weights(CUtensorMap *map, bool fp4, const void *base, int64_t rows, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Split activation rows [rows][k] of codes; boxes of 128 K x all columns of the operand.
-bool encode_rows(CUtensorMap *map, const void *base, int rows, int k, int box_rows) {
-    const TensorMapEncodeFn enc = host_encode();
-    if (enc == nullptr) return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k)};
-    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
-    const cuuint32_t step[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, step,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // How a launch fills the GPU: `occ` CTAs on an SM; `split` CTAs of a cluster share a
 // tile's K (1: persistent CTAs take the tiles in turn).
 struct Plan {
@@ -51,10 +38,9 @@ struct Plan {
 };
 
 template <bool FP4, int HALVES, int MODE>
-cudaError_t launch(const CUtensorMap &map, const CUtensorMap &map_x, FewArgs &a, const Plan &plan, int max_tiles,
+cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles,
                    int num_sms, cudaStream_t stream) {
-    const int pairs = MODE < kUp ? 0 : a.tokens * a.topk;
-    const int fixed = FewConfig::smem_bytes(HALVES, a.cap, 0, MODE, pairs, plan.split);
+    const int fixed = FewConfig::smem_bytes(HALVES, a.cap, 0, MODE, a.tokens, a.topk, plan.split);
     const int stage = FewConfig::stage_bytes(HALVES, a.cap);
     const int limit = plan.occ == 2 ? kSmemTwo : kSmemOne;
     int stages = (limit - fixed) / stage;
@@ -63,10 +49,10 @@ cudaError_t launch(const CUtensorMap &map, const CUtensorMap &map_x, FewArgs &a,
     if (stages < 2) return cudaErrorInvalidConfiguration;
     const int set = HALVES * 2 * a.cap, sf = 2 * (4 * HALVES + 4), most = plan.occ == 2 ? 256 : 512;
     a.stages = stages;
-    a.accs = plan.split == 1 && 2 * set + sf <= most ? 2 : 1;
+    a.accs = (plan.split == 1 || MODE == kDown) && 2 * set + sf <= most ? 2 : 1;
     a.tmem_cols = pow2_at_least(a.accs * set + sf);
     if (a.tmem_cols > 512) return cudaErrorInvalidConfiguration;
-    const int smem = FewConfig::smem_bytes(HALVES, a.cap, stages, MODE, pairs, plan.split);
+    const int smem = FewConfig::smem_bytes(HALVES, a.cap, stages, MODE, a.tokens, a.topk, plan.split);
     auto kernel = dg_few_rows_kernel<FP4, HALVES, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
     if (e != cudaSuccess) return e;
@@ -80,21 +66,28 @@ cudaError_t launch(const CUtensorMap &map, const CUtensorMap &map_x, FewArgs &a,
     const int grid = plan.split > 1 ? max_tiles * plan.split
                                     : (max_tiles < plan.occ * num_sms ? max_tiles : plan.occ * num_sms);
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(FewConfig::kThreads);
+    cfg.blockDim = dim3(FewConfig::threads(MODE));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = plan.split > 1 ? 2 : 1;
     host_set_last_config(HALVES * 128, 2 * a.cap, stages, grid, MODE < kUp ? 3 : 5,
                          MODE == kGemv ? 1 : MODE == kGemvPre ? 2 : 3);
-    return cudaLaunchKernelEx(&cfg, kernel, map, map_x, a);
+    return cudaLaunchKernelEx(&cfg, kernel, map, a);
 }
 
 template <int HALVES, int MODE>
-cudaError_t launch_fmt(bool fp4, const CUtensorMap &map, const CUtensorMap &map_x, FewArgs &a, const Plan &plan,
-                       int max_tiles, int num_sms, cudaStream_t stream) {
-    return fp4 ? launch<true, HALVES, MODE>(map, map_x, a, plan, max_tiles, num_sms, stream)
-               : launch<false, HALVES, MODE>(map, map_x, a, plan, max_tiles, num_sms, stream);
+cudaError_t launch_fmt(bool fp4, const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles, int num_sms,
+                       cudaStream_t stream) {
+    return fp4 ? launch<true, HALVES, MODE>(map, a, plan, max_tiles, num_sms, stream)
+               : launch<false, HALVES, MODE>(map, a, plan, max_tiles, num_sms, stream);
+}
+
+template <int MODE>
+cudaError_t launch_mode(bool fp4, const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles, int num_sms,
+                        cudaStream_t stream) {
+    return plan.halves == 2 ? launch_fmt<2, MODE>(fp4, map, a, plan, max_tiles, num_sms, stream)
+                            : launch_fmt<1, MODE>(fp4, map, a, plan, max_tiles, num_sms, stream);
 }
 
 // The largest cluster of at most kMaxSplit CTAs (and K-blocks) with all tiles resident at once.
@@ -105,36 +98,62 @@ int resident_split(int tiles, int kblocks, int slots) {
     return s < 1 ? 1 : s;
 }
 
-cudaError_t launch_split(const uint16_t *x, int64_t ldx, int rows, int kblocks, uint8_t *codes, uint32_t *scales,
-                         bool cp_order, cudaStream_t stream) {
+// A launch that may start before the stream's previous kernel ends.
+struct Dependent {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(cdiv(rows * kblocks, 16)));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dg_few_split_kernel, x, ldx, rows, kblocks, codes, scales, cp_order ? 1 : 0);
-}
+    Dependent(dim3 grid, int smem, cudaStream_t stream) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+};
 
 // Rows that a product splits by itself (each CTA its own K range).
 bool direct(int64_t m) { return m <= env("DG_FEW_DIRECT", 4); }
 
 int capacity(int tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
 
+// Tokens of a segment at most: room for twice the mean number of tokens of an expert (the
+// tokens beyond make another segment, which reads the expert's weights again).
+int segment_capacity(int64_t t, int64_t topk, int64_t experts) {
+    const int64_t most = 2 * t * topk / experts + 4;
+    return capacity(static_cast<int>(most < t ? most : t));
+}
+
+// Bounds of the layer's segments, and of their units of 8 image rows (4 tokens).
+struct SegmentBounds {
+    int64_t count, units;
+    SegmentBounds(int64_t t, int64_t topk, int64_t experts) {
+        const int64_t pairs = t * topk, used = pairs < experts ? pairs : experts;
+        const int cap = segment_capacity(t, topk, experts);
+        count = used + pairs / cap;
+        if (count > pairs) count = pairs;
+        units = (pairs + 3 * count) / 4;
+    }
+    int64_t image(int64_t k) const { return units * (k / 128) * 1024; }
+    int64_t scales(int64_t k) const { return count * (k / 128) * 512; }
+};
+
 }  // namespace
 
-int64_t few_workspace_bytes(int64_t m, int64_t n, int64_t k) { return direct(m) ? 0 : 2 * m * k + 4 * k; }
+int64_t few_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    return direct(m) ? 0 : k / 128 * ((m + 3) / 4 * 1024 + 512);
+}
 
-int64_t layer_workspace_bytes(int64_t t, int64_t topk, int64_t h, int64_t i) {
-    // split x and split h: codes, then scale words
-    return 2 * t * h + 2 * t * topk * i + t * h / 16 + t * topk * i / 16;
+int64_t layer_workspace_bytes(int64_t t, int64_t topk, int64_t h, int64_t i, int64_t experts) {
+    if (t == 0 || topk == 0 || experts == 0) return 0;
+    const SegmentBounds b(t, topk, experts);
+    return b.image(h) + b.image(i) + b.scales(h) + b.scales(i);
 }
 
 cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream) {
-    CUtensorMap map, map_x;
+    CUtensorMap map;
     if (!encode_weights(&map, p.fp4, p.b, p.n, p.ldb, p.k)) return cudaErrorInvalidValue;
     FewArgs a = {};
     a.x = p.a;
@@ -157,18 +176,15 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream
     plan.halves = env("DG_H", p.m > 16 ? 2 : 1);
     plan.occ = env("DG_OCC", plan.halves == 1 ? 2 : 1);
     plan.split = env("DG_S", resident_split(cdiv(p.n, 128), a.kblocks, 2 * num_sms * 19 / 20));
-    const int tiles = cdiv(p.n, 128 * plan.halves);
-    a.row_tiles = tiles;
-    if (direct(p.m))
-        return plan.halves == 2 ? launch_fmt<2, kGemv>(p.fp4, map, map, a, plan, tiles, num_sms, stream)
-                                : launch_fmt<1, kGemv>(p.fp4, map, map, a, plan, tiles, num_sms, stream);
-    uint32_t *scales = reinterpret_cast<uint32_t *>(p.workspace + 2 * static_cast<int64_t>(p.m) * p.k);
-    if (!encode_rows(&map_x, p.workspace, 2 * p.m, p.k, 2 * a.cap)) return cudaErrorInvalidValue;
-    cudaError_t e = launch_split(p.a, p.lda, p.m, a.kblocks, p.workspace, scales, true, stream);
+    a.row_tiles = cdiv(p.n, 128 * plan.halves);
+    if (direct(p.m)) return launch_mode<kGemv>(p.fp4, map, a, plan, a.row_tiles, num_sms, stream);
+    a.image = p.workspace;
+    a.image_sf = p.workspace + static_cast<int64_t>(a.kblocks) * ((p.m + 3) / 4) * 1024;
+    Dependent split(dim3(static_cast<unsigned>(cdiv(p.m * a.kblocks, 16))), 0, stream);
+    cudaError_t e = cudaLaunchKernelEx(&split.cfg, dg_few_split_kernel, a.x, a.ldx, p.m, a.kblocks,
+                                       const_cast<uint8_t *>(a.image), const_cast<uint8_t *>(a.image_sf));
     if (e != cudaSuccess) return e;
-    a.scales = scales;
-    return plan.halves == 2 ? launch_fmt<2, kGemvPre>(p.fp4, map, map_x, a, plan, tiles, num_sms, stream)
-                            : launch_fmt<1, kGemvPre>(p.fp4, map, map_x, a, plan, tiles, num_sms, stream);
+    return launch_mode<kGemvPre>(p.fp4, map, a, plan, a.row_tiles, num_sms, stream);
 }
 
 cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t stream) {
@@ -177,19 +193,19 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     if (!encode_weights(&map1, p.fp4, p.w1, static_cast<int64_t>(p.experts) * 2 * p.i, p.h / per, p.h) ||
         !encode_weights(&map2, p.fp4, p.w2, static_cast<int64_t>(p.experts) * p.h, p.i / per, p.i))
         return cudaErrorInvalidValue;
-    const int64_t rows = static_cast<int64_t>(p.t) * p.topk;
-    uint8_t *x_codes = p.workspace, *h_codes = x_codes + 2 * static_cast<int64_t>(p.t) * p.h;
-    uint32_t *x_scales = reinterpret_cast<uint32_t *>(h_codes + 2 * rows * p.i);
-    uint32_t *h_scales = x_scales + p.h / 128 * 2 * p.t;
-    cudaError_t e = launch_split(p.x, p.ldx, p.t, p.h / 128, x_codes, x_scales, false, stream);
+    const SegmentBounds bounds(p.t, p.topk, p.experts);
+    uint8_t *x_image = p.workspace, *h_image = x_image + bounds.image(p.h);
+    uint8_t *x_sf = h_image + bounds.image(p.i), *h_sf = x_sf + bounds.scales(p.h);
+    const int cap = segment_capacity(p.t, p.topk, p.experts), pairs = p.t * p.topk;
+    const int kh = p.h / 128, ki = p.i / 128;
+    Dependent split(dim3(static_cast<unsigned>(kh), static_cast<unsigned>(cdiv(pairs, 64))),
+                    FewConfig::table_bytes(kUp, pairs), stream);
+    cudaError_t e = cudaLaunchKernelEx(&split.cfg, dg_layer_split_kernel, p.x, p.ldx, p.ids, p.t, p.topk, p.experts,
+                                       cap, kh, x_image, x_sf);
     if (e != cudaSuccess) return e;
     FewArgs a = {};
-    a.codes = x_codes;
-    a.scales = x_scales;
-    a.src_rows = p.t;
-    a.out_codes = h_codes;
-    a.out_scales = reinterpret_cast<uint8_t *>(h_scales);
     a.tokens = p.t;
+    a.cap = cap;
     a.ids = p.ids;
     a.weights = p.weights;
     a.experts = p.experts;
@@ -198,33 +214,32 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.status = p.status;
     a.timeout_ns = p.timeout_ns;
     a.debug_flags = p.debug_flags;
-    // up: one grid row per expert that can be in use, one CTA tile per 128 columns of h
-    const int most = p.t * p.topk < p.experts ? p.t * p.topk : p.experts;
+    // up: a tile is 128 columns of h of one segment
+    a.image = x_image;
+    a.image_sf = x_sf;
+    a.out_image = h_image;
+    a.out_image_sf = h_sf;
     a.sf = p.sf1;
     a.sf_ld = 2 * p.i;
-    a.sf_expert = static_cast<int64_t>(p.fp4 ? p.h / 128 : cdiv(p.h, 512)) * a.sf_ld;
+    a.sf_expert = static_cast<int64_t>(p.fp4 ? kh : cdiv(kh, 4)) * a.sf_ld;
     a.rows = 2 * p.i;
-    a.kblocks = p.h / 128;
-    a.cap = capacity(p.t < 2 * p.t * p.topk / p.experts + 4 ? p.t : 2 * p.t * p.topk / p.experts + 4);
-    a.chunks = cdiv(p.t, a.cap);
-    a.row_tiles = p.i / 128;
-    const int up_tiles = a.row_tiles * a.chunks * most;
+    a.kblocks = kh;
+    a.row_tiles = ki;
+    const int up_tiles = static_cast<int>(bounds.count) * ki;
     Plan up;
     up.halves = 2;
     up.occ = env("DG_UP_OCC", 1);
-    up.split = env("DG_UP_S", resident_split(up_tiles, a.kblocks, up.occ * num_sms * 19 / 20));
-    e = launch_fmt<2, kUp>(p.fp4, map1, map1, a, up, up_tiles, num_sms, stream);
+    up.split = env("DG_UP_S", resident_split(up_tiles, kh, up.occ * num_sms * 19 / 20));
+    e = launch_fmt<2, kUp>(p.fp4, map1, a, up, up_tiles, num_sms, stream);
     if (e != cudaSuccess) return e;
-    // down: K runs over the active experts
-    a.codes = h_codes;
-    a.scales = h_scales;
-    a.src_rows = static_cast<int>(rows);
+    // down: K runs over the segments
+    a.image = h_image;
+    a.image_sf = h_sf;
     a.sf = p.sf2;
     a.sf_ld = p.h;
-    a.sf_expert = static_cast<int64_t>(p.fp4 ? p.i / 128 : cdiv(p.i, 512)) * a.sf_ld;
+    a.sf_expert = static_cast<int64_t>(p.fp4 ? ki : cdiv(ki, 4)) * a.sf_ld;
     a.rows = p.h;
-    a.kblocks = p.i / 128;
-    a.cap = capacity(p.t);
+    a.kblocks = ki;
     a.c = p.c;
     a.ldc = p.ldc;
     a.d = p.y;
@@ -232,11 +247,11 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.debug_flags = 0;
     Plan down;
     down.halves = env("DG_DOWN_H", 1);
-    down.occ = env("DG_DOWN_OCC", 2);
+    down.occ = env("DG_DOWN_OCC", p.t > 16 ? 1 : 2);
     a.row_tiles = cdiv(p.h, 128 * down.halves);
-    down.split = env("DG_DOWN_S", resident_split(a.row_tiles, a.kblocks * most, down.occ * num_sms * 19 / 20));
-    return down.halves == 2 ? launch_fmt<2, kDown>(p.fp4, map2, map2, a, down, a.row_tiles, num_sms, stream)
-                            : launch_fmt<1, kDown>(p.fp4, map2, map2, a, down, a.row_tiles, num_sms, stream);
+    down.split = env("DG_DOWN_S", resident_split(a.row_tiles, ki * static_cast<int>(bounds.count),
+                                                 down.occ * num_sms * 19 / 20));
+    return launch_mode<kDown>(p.fp4, map2, a, down, a.row_tiles, num_sms, stream);
 }
 
 }  // namespace dg

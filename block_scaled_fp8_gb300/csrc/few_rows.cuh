@@ -22,22 +22,24 @@
 //               the order in which tcgen05.cp takes them to TMEM), scales by bulk copy.
 //   warp 1      TMEM owner, MMA issuer.
 //   warps 2..5  epilogue, one TMEM lane quadrant each.
-//   warps 6..9  the narrow operand, K-blocks in turn.
+//   warp 6..    the narrow operand.
 // Many tiles: the CTAs are persistent and take tiles in turn, the ring of K-blocks running
 // on across them.  Few tiles: one tile per cluster, K split over its CTAs, which add
 // their FP32 partial results in rank order through distributed shared memory: no
 // workspace, no atomics, a fixed order.
 //
-// Modes, by where the pieces come from:
-//   kGemv   the warps split the activations themselves.
-//   kGemvPre  dg_few_split_kernel has split them once, into rows [2m][K] of codes and
-//           per K-block a 512-byte block of scale words in tcgen05.cp order: TMA loads.
-//   kUp     the gate and up rows of one expert (HALVES = 2) for up to `cap` of the tokens
-//           routed to it, whose split rows are gathered.  The epilogue is w silu(g) u (w
-//           the routing weight), split again into pieces.
-//   kDown   K runs over all active experts; a column belongs to one token throughout
-//           and is zero for the experts that the token does not use, so the sum over a
-//           token's experts is the accumulation itself.
+// Where the pieces come from: kGemv, for the fewest rows, splits the activations itself,
+// four warps taking K-blocks in turn.  The other modes read an image of the narrow
+// operand that is already in the shared-memory form of each K-block (rows of 128 bytes
+// in 128-byte swizzle, and the scale words in tcgen05.cp order), two bulk copies a block:
+//   kGemvPre  dg_few_split_kernel has written the image of all rows.
+//   kUp       the gate and up rows of one expert (HALVES = 2) for a segment, up to `cap`
+//           of the tokens routed to it; dg_layer_split_kernel has written the segments'
+//           images.  The epilogue is w silu(g) u (w the routing weight), split again
+//           and written as the image that kDown reads.
+//   kDown     K runs over all segments; the accumulators of a segment are added to the
+//           FP32 results of its tokens in shared memory while the next segment's
+//           products run.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -53,23 +55,21 @@ enum FewMode : int { kGemv = 0, kGemvPre = 1, kUp = 2, kDown = 3 };
 struct FewArgs {
     const uint16_t *x;      // kGemv: bf16 activations
     int64_t ldx;
-    const uint8_t *codes;   // kUp, kDown: split rows, codes [2 rows][K] (row 2r hi, 2r + 1 lo)
-    const uint32_t *scales; // their scale words [K / 128][2 rows]; kGemvPre: [K / 128][128] in tcgen05.cp order
-    uint8_t *out_codes;     // kUp: the same of its output, rows = t * topk
-    uint8_t *out_scales;
+    const uint8_t *image;   // the other modes: the narrow operand's image, and its scale blocks
+    const uint8_t *image_sf;
+    uint8_t *out_image;     // kUp
+    uint8_t *out_image_sf;
     const uint32_t *sf;     // packed scale words of the weights
     int64_t sf_expert;      // words per expert
     int sf_ld;              // words per slice
     int rows;               // weight rows of one expert (kUp: 2 i)
-    int tokens;             // rows of x
-    int src_rows;           // kUp, kDown: rows of the split source (t, t * topk)
+    int tokens;
     int kblocks;            // K-blocks of one expert
-    int cap;                // token columns of the operand (8, 16, 32 or 64); N = 2 cap
+    int cap;                // tokens of a segment at most (8, 16, 32 or 64); N = 2 cap
     int stages;
     int accs;               // accumulator sets (1 or 2)
     int tmem_cols;
     int row_tiles;          // tiles over the weight rows (kUp: of h's columns)
-    int chunks;             // kUp: groups of cap tokens that an expert may have
     // MoE
     const int32_t *ids;
     const float *weights;
@@ -86,20 +86,21 @@ struct FewArgs {
 };
 
 struct FewConfig {
-    static constexpr int kThreads = 320;
-    static constexpr int kFirstEpi = 2, kFirstB = 6, kBWarps = 4;
+    static constexpr int kFirstEpi = 2, kFirstB = 6;
+    static constexpr int b_warps(int mode) { return mode == kGemv ? 4 : 1; }
+    static constexpr int threads(int mode) { return 32 * (kFirstB + b_warps(mode)); }
     static constexpr int kAlign = 1024;
     static constexpr int kBarBytes = 512;
     static constexpr int kMaxStages = 24;
     static int stage_bytes(int halves, int cap) { return halves * 16384 + 2 * cap * 128 + halves * 512 + 512; }
-    // two buffers of 8 tokens' FP32 results (split tiles leave theirs in the ring)
-    static int out_bytes(int halves, int mode, int split) {
-        return split > 1 ? 0 : 2 * 8 * (mode == kUp ? 128 : halves * 128) * 4;
+    // kDown: the tokens' FP32 results; else two buffers of 8 tokens' (split tiles leave theirs in the ring)
+    static int out_bytes(int halves, int mode, int tokens, int split) {
+        return mode == kDown ? tokens * halves * 512 : split > 1 ? 0 : 2 * 8 * (mode == kUp ? 128 : halves * 128) * 4;
     }
     static int table_bytes(int mode, int pairs) { return mode < kUp ? 0 : (256 + 24 * pairs + 15) / 16 * 16; }
-    static int smem_bytes(int halves, int cap, int stages, int mode, int pairs, int split) {
-        return kAlign + stages * stage_bytes(halves, cap) + out_bytes(halves, mode, split) + kBarBytes +
-               table_bytes(mode, pairs);
+    static int smem_bytes(int halves, int cap, int stages, int mode, int tokens, int topk, int split) {
+        return kAlign + stages * stage_bytes(halves, cap) + out_bytes(halves, mode, tokens, split) + kBarBytes +
+               table_bytes(mode, tokens * topk);
     }
 };
 
@@ -145,9 +146,26 @@ __device__ __forceinline__ uint32_t split_bf16(const uint4 &v, uint2 &hi, uint2 
 // Position of operand row n's scale word in a 512-byte block (tcgen05.cp order).
 __device__ __forceinline__ uint32_t sf_word(uint32_t n) { return (n & 31u) * 4u + (n >> 5); }
 
-// Splits bf16 rows once for all CTAs that read them: 16 lanes per row and K-block.
+// Image of n tokens' K-block: their 2n rows in units of 8 (1024 bytes).
+__device__ __forceinline__ int image_units(int tokens) { return (tokens + 3) >> 2; }
+
+// Lane q16's pieces of token column col to the K-block's image, and its group's scales.
+__device__ __forceinline__ void put_pieces(uint8_t *image, uint8_t *sf, int col, int q16, const uint2 &hi,
+                                           const uint2 &lo, uint32_t e8) {
+    const uint32_t n = 2 * col;
+    const uint32_t off = (q16 & 1) * 8;
+    *reinterpret_cast<uint2 *>(image + n * 128 + (((q16 >> 1) ^ (n & 7)) << 4) + off) = hi;
+    *reinterpret_cast<uint2 *>(image + (n + 1) * 128 + (((q16 >> 1) ^ ((n + 1) & 7)) << 4) + off) = lo;
+    if ((q16 & 3) == 0) {
+        uint8_t *s = sf + sf_word(n) * 4 + (q16 >> 2);
+        s[0] = static_cast<uint8_t>(hi_scale(e8));
+        s[16] = static_cast<uint8_t>(lo_scale(e8));
+    }
+}
+
+// Splits all rows of a product once for all CTAs that read them: 16 lanes per row and K-block.
 __global__ void __launch_bounds__(256) dg_few_split_kernel(const uint16_t *x, int64_t ldx, int rows, int kblocks,
-                                                           uint8_t *codes, uint32_t *scales, int cp_order) {
+                                                           uint8_t *image, uint8_t *image_sf) {
     grid_dependency_wait();
     grid_launch_dependents();   // after the wait: the next kernel may read what was there before this one
     const int unit = blockIdx.x * 16 + static_cast<int>(threadIdx.x >> 4);
@@ -157,40 +175,170 @@ __global__ void __launch_bounds__(256) dg_few_split_kernel(const uint16_t *x, in
     const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(x + t * ldx + kb * 128 + q16 * 8));
     uint2 hi, lo;
     const uint32_t e8 = split_bf16(v, hi, lo);
-    if (!in) return;
-    const int64_t k = static_cast<int64_t>(kblocks) * 128;
-    uint8_t *at = codes + 2 * t * k + kb * 128 + q16 * 8;
-    *reinterpret_cast<uint2 *>(at) = hi;
-    *reinterpret_cast<uint2 *>(at + k) = lo;
-    if ((q16 & 3) == 0) {
-        const uint32_t n = 2 * t;
-        uint8_t *s = reinterpret_cast<uint8_t *>(cp_order ? scales + kb * 128 + sf_word(n)
-                                                          : scales + static_cast<int64_t>(kb) * 2 * rows + n) + (q16 >> 2);
-        s[0] = static_cast<uint8_t>(hi_scale(e8));
-        s[cp_order ? 16 : 4] = static_cast<uint8_t>(lo_scale(e8));
+    if (in)
+        put_pieces(image + static_cast<int64_t>(kb) * image_units(rows) * 1024, image_sf + kb * 512, t, q16, hi, lo, e8);
+}
+
+// The layer's routing, as every CTA of its kernels derives it from the ids (in shared
+// memory; the same in all of them): the slots of each expert in use form one segment
+// after another of up to `cap` tokens.
+struct Segments {
+    int count;
+    uint16_t *expert;   // [count]
+    uint16_t *first;    // [count] first entry
+    uint16_t *tokens;   // [count]
+    uint16_t *unit;     // [count] units of the segments before (image_units)
+    uint16_t *entry;    // [pairs] slot (token * topk + j), by expert, in slot order
+    uint16_t *of_entry; // [pairs] segment of each entry
+    int *ids;           // [pairs] id of a token's first slot with it, or -1
+};
+
+// Tables of 256 + 24 * pairs bytes at `tab`; called by all threads of a CTA.
+__device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids, int pairs, int topk, int experts,
+                                                   int cap, int32_t *status) {
+    uint32_t *mask = reinterpret_cast<uint32_t *>(tab);   // [32] experts in use
+    int *pre = tab + 32;                                  // [32] experts in use before this word; then the counts
+    Segments s;
+    s.ids = tab + 64;
+    uint16_t *off = reinterpret_cast<uint16_t *>(s.ids + pairs);   // [active] end of each expert's entries
+    uint16_t *exp = off + pairs;                                   // [active]
+    s.entry = exp + pairs;
+    s.of_entry = s.entry + pairs;
+    s.expert = s.of_entry + pairs;
+    s.first = s.expert + pairs;
+    s.tokens = s.first + pairs;
+    s.unit = s.tokens + pairs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) mask[lane] = 0u;
+    __syncthreads();
+    for (int q = threadIdx.x; q < pairs; q += blockDim.x) {
+        int e = __ldcg(ids + q);
+        if (e >= experts) {
+            if (status) atomicOr(status, DG_DEV_BAD_GROUP);
+            e = -1;
+        }
+        for (int r = q - q % topk; r < q && e >= 0; ++r)
+            if (__ldcg(ids + r) == e) e = -1;
+        s.ids[q] = e < 0 ? -1 : e;
+        if (e >= 0) atomicOr(&mask[e >> 5], 1u << (e & 31));
+    }
+    __syncthreads();
+    if (warp == 0) {
+        auto scan = [&](int v) {   // inclusive
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+                if (lane >= d) v += u;
+            }
+            return v;
+        };
+        const int cnt = __popc(mask[lane]);
+        const int inc = scan(cnt);
+        pre[lane] = inc - cnt;
+        const int used = __shfl_sync(0xFFFFFFFFu, inc, 31);
+        for (int a = lane; a < used; a += 32) off[a] = 0;
+        __syncwarp();
+        // one warp counts, scans and fills, in slot order
+        auto rank_of = [&](int e) {
+            return e < 0 ? -1 - lane : pre[e >> 5] + __popc(mask[e >> 5] & ((1u << (e & 31)) - 1));
+        };
+        for (int q0 = 0; q0 < pairs; q0 += 32) {
+            const int e = q0 + lane < pairs ? s.ids[q0 + lane] : -1;
+            const int a = rank_of(e);
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
+            if (a >= 0 && (same >> lane) == 1u) {   // the last holder of this expert
+                off[a] += static_cast<uint16_t>(__popc(same));
+                exp[a] = static_cast<uint16_t>(e);
+            }
+            __syncwarp();
+        }
+        int run = 0, seg = 0, unit = 0;
+        for (int a0 = 0; a0 < used; a0 += 32) {
+            const int n = a0 + lane < used ? off[a0 + lane] : 0;
+            const int mine = (n + cap - 1) / cap;
+            const int units = n / cap * image_units(cap) + image_units(n % cap);
+            const int in_n = scan(n), in_s = scan(mine), in_u = scan(units);
+            if (a0 + lane < used) {
+                int first = run + in_n - n, u = unit + in_u - units;
+                off[a0 + lane] = static_cast<uint16_t>(first);
+                int left = n;
+                for (int z = seg + in_s - mine; z < seg + in_s; ++z) {
+                    const int t = min(left, cap);
+                    s.expert[z] = exp[a0 + lane];
+                    s.first[z] = static_cast<uint16_t>(first);
+                    s.tokens[z] = static_cast<uint16_t>(t);
+                    s.unit[z] = static_cast<uint16_t>(u);
+                    for (int j = 0; j < t; ++j) s.of_entry[first + j] = static_cast<uint16_t>(z);
+                    first += t;
+                    left -= t;
+                    u += image_units(t);
+                }
+            }
+            run += __shfl_sync(0xFFFFFFFFu, in_n, 31);
+            seg += __shfl_sync(0xFFFFFFFFu, in_s, 31);
+            unit += __shfl_sync(0xFFFFFFFFu, in_u, 31);
+        }
+        __syncwarp();
+        for (int q0 = 0; q0 < pairs; q0 += 32) {
+            const int q = q0 + lane;
+            const int a = rank_of(q < pairs ? s.ids[q] : -1);
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
+            if (a >= 0) s.entry[off[a] + __popc(same & ((1u << lane) - 1))] = static_cast<uint16_t>(q);
+            __syncwarp();
+            if (a >= 0 && (same >> lane) == 1u) off[a] += static_cast<uint16_t>(__popc(same));
+            __syncwarp();
+        }
+        if (lane == 0) pre[0] = seg;
+    }
+    __syncthreads();
+    s.count = pre[0];
+    return s;
+}
+
+// Images of all segments' tokens.  Blocks of grid.y take entries in turn, one K-block each.
+__global__ void __launch_bounds__(256) dg_layer_split_kernel(const uint16_t *x, int64_t ldx, const int32_t *ids,
+                                                             int tokens, int topk, int experts, int cap, int kblocks,
+                                                             uint8_t *image, uint8_t *image_sf) {
+    extern __shared__ int split_tab[];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const Segments s = build_segments(split_tab, ids, tokens * topk, topk, experts, cap, nullptr);
+    const int entries = s.count ? s.first[s.count - 1] + s.tokens[s.count - 1] : 0;
+    const int q16 = threadIdx.x & 15, kb = blockIdx.x;
+    for (int at0 = blockIdx.y * 16; at0 < entries; at0 += gridDim.y * 16) {
+        const int at = at0 + static_cast<int>(threadIdx.x >> 4);
+        const bool in = at < entries;
+        const int row = in ? s.entry[at] / topk : 0;
+        const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(x + row * ldx + kb * 128 + q16 * 8));
+        uint2 hi, lo;
+        const uint32_t e8 = split_bf16(v, hi, lo);
+        if (in) {
+            const int z = s.of_entry[at];
+            put_pieces(image + (static_cast<int64_t>(s.unit[z]) * kblocks + kb * image_units(s.tokens[z])) * 1024,
+                       image_sf + (static_cast<int64_t>(z) * kblocks + kb) * 512, at - s.first[z], q16, hi, lo, e8);
+        }
     }
 }
 
 // One tile of work, the same for every role of a CTA.
 struct FewTile {
+    int seg;        // kUp
     int expert;     // kUp
     int row0;       // first weight row (kUp: column of h)
-    int ntok;       // token columns
-    int ent;        // kUp: first entry
-    int begin;      // first K-block (kDown: over the active experts)
-    int nblk;
+    int ntok;       // token columns (kDown: all tokens)
 };
 
 template <bool FP4, int HALVES, int MODE>
-__global__ void __launch_bounds__(FewConfig::kThreads, 2)
-    dg_few_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                       const __grid_constant__ FewArgs p) {
+__global__ void __launch_bounds__(FewConfig::threads(MODE), 2)
+    dg_few_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ FewArgs p) {
     constexpr int ROWS = HALVES * 128;
     constexpr int OUT = MODE == kUp ? 128 : ROWS;     // results per token and tile
-    constexpr int NT = FewConfig::kThreads;
+    constexpr int NT = FewConfig::threads(MODE);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int nsplit = static_cast<int>(cluster_nctarank());
     const int S = p.stages;
     const int ncols = 2 * p.cap;
     const int b_bytes = ncols * 128;
@@ -199,22 +347,20 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
     uint8_t *smem_sfa = smem_b + S * b_bytes;
     uint8_t *smem_sfb = smem_sfa + S * HALVES * 512;
     float *smem_out = reinterpret_cast<float *>(smem_sfb + S * 512);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_out + (cluster_nctarank() > 1 ? 0 : 2 * 8 * OUT));
-    uint64_t *full_bar = bars;              // [S] weights and scales landed, pieces written
+    uint64_t *bars = reinterpret_cast<uint64_t *>(
+        smem_out + (MODE == kDown ? p.tokens * ROWS : nsplit > 1 ? 0 : 2 * 8 * OUT));
+    uint64_t *full_bar = bars;              // [S] weights and scales landed, pieces landed or written
     uint64_t *empty_bar = bars + S;         // [S] the slot's MMAs are done
     uint64_t *tfull_bar = bars + 2 * S;     // [2] accumulators complete
     uint64_t *tempty_bar = tfull_bar + 2;   // [2] accumulators read
     uint64_t *drain_bar = tempty_bar + 2;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    int *sh_active = reinterpret_cast<int *>(tmem_holder + 2);
     int *tab = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + FewConfig::kBarBytes);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
-    const int rank = static_cast<int>(cluster_ctarank());
-    const int nsplit = static_cast<int>(cluster_nctarank());
     const int first_tile = blockIdx.x / nsplit, tile_step = gridDim.x / nsplit;
 
     if (warp == 0) {
@@ -223,7 +369,6 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
         if (lane == 0) {
             *abort_flag = 0;
             tma_prefetch_desc(&tm_w);
-            if (MODE == kGemvPre) tma_prefetch_desc(&tm_x);
         }
         fence_mbar_init();
     }
@@ -231,141 +376,44 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
         tmem_alloc(tmem_holder, p.tmem_cols);
         tmem_relinquish();
     }
-    // The first kernel of a chain (kGemv; the split kernel before the others) waits for
+    // The first kernel of a chain (kGemv; a split kernel before the others) waits for
     // what precedes it and only then lets the next one start.  So the later kernels of
     // the chain may read weights, ids and routing weights at once; only the warps that
     // read the preceding kernel's output wait for it.
     if constexpr (MODE == kGemv) grid_dependency_wait();
     grid_launch_dependents();
-
-    // ---------------------------------------------------------------- routing tables
     const int pairs = MODE < kUp ? 0 : p.tokens * p.topk;
-    uint32_t *tab_mask = reinterpret_cast<uint32_t *>(tab);   // [32] experts in use
-    int *tab_pre = tab + 32;                                  // [32] experts in use before this word
-    int *s_ids = tab + 64;                                    // [pairs] id of a token's first slot with it, or -1
-    float *s_wsum = reinterpret_cast<float *>(s_ids + pairs); // [pairs] by entry: weight (of all the token's slots)
-    uint32_t *s_mask = reinterpret_cast<uint32_t *>(s_wsum + pairs);     // [active][2] tokens of each expert
-    uint16_t *s_ent = reinterpret_cast<uint16_t *>(s_mask + 2 * pairs);  // [pairs] by entry: first slot (pair)
-    uint16_t *s_off = s_ent + pairs;                          // [active] end of each expert's entries
-    uint16_t *s_exp = s_off + pairs;                          // [active] expert
-    int active = 1;
-    if constexpr (MODE >= kUp) {
-        if (warp == 0) tab_mask[lane] = 0u;
-        __syncthreads();
-        for (int q = threadIdx.x; q < pairs; q += NT) {
-            int e = __ldcg(p.ids + q);
-            if (e >= p.experts) {
-                if (p.status) atomicOr(p.status, DG_DEV_BAD_GROUP);
-                e = -1;
-            }
-            for (int r = q - q % p.topk; r < q && e >= 0; ++r)
-                if (__ldcg(p.ids + r) == e) e = -1;
-            s_ids[q] = e < 0 ? -1 : e;
-            if (e >= 0) atomicOr(&tab_mask[e >> 5], 1u << (e & 31));
-        }
-        __syncthreads();
-        if (warp == 0) {
-            const int cnt = __popc(tab_mask[lane]);
-            int inc = cnt;
-#pragma unroll
-            for (int s = 1; s < 32; s <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, inc, s);
-                if (lane >= s) inc += v;
-            }
-            tab_pre[lane] = inc - cnt;
-            if (lane == 31) *sh_active = inc;
-            const int used = __shfl_sync(0xFFFFFFFFu, inc, 31);
-            for (int a = lane; a < used; a += 32) {
-                s_off[a] = 0;
-                s_mask[2 * a] = s_mask[2 * a + 1] = 0u;
-            }
-            __syncwarp();
-            // one warp counts, scans and fills, in slot order (the order is the same in every CTA)
-            auto rank_of = [&](int e) {
-                return e < 0 ? -1 - lane : tab_pre[e >> 5] + __popc(tab_mask[e >> 5] & ((1u << (e & 31)) - 1));
-            };
-            for (int q0 = 0; q0 < pairs; q0 += 32) {
-                const int e = q0 + lane < pairs ? s_ids[q0 + lane] : -1;
-                const int a = rank_of(e);
-                const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
-                if (a >= 0 && (same >> lane) == 1u) {   // the last holder of this expert
-                    s_off[a] += static_cast<uint16_t>(__popc(same));
-                    s_exp[a] = static_cast<uint16_t>(e);
-                }
-                __syncwarp();
-            }
-            int run = 0;
-            for (int a0 = 0; a0 < used; a0 += 32) {
-                const int n = a0 + lane < used ? s_off[a0 + lane] : 0;
-                int sum = n;
-#pragma unroll
-                for (int s = 1; s < 32; s <<= 1) {
-                    const int v = __shfl_up_sync(0xFFFFFFFFu, sum, s);
-                    if (lane >= s) sum += v;
-                }
-                if (a0 + lane < used) s_off[a0 + lane] = static_cast<uint16_t>(run + sum - n);
-                run += __shfl_sync(0xFFFFFFFFu, sum, 31);
-            }
-            __syncwarp();
-            for (int q0 = 0; q0 < pairs; q0 += 32) {
-                const int q = q0 + lane;
-                const int e = q < pairs ? s_ids[q] : -1;
-                const int a = rank_of(e);
-                const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
-                if (a >= 0) {
-                    const int at = s_off[a] + __popc(same & ((1u << lane) - 1));
-                    const int token = q / p.topk;
-                    s_ent[at] = static_cast<uint16_t>(q);
-                    if constexpr (MODE == kUp) {
-                        float w = 0.0f;
-                        for (int r = q; r < (token + 1) * p.topk; ++r)
-                            if (__ldcg(p.ids + r) == e) w += __ldcg(p.weights + r);
-                        s_wsum[at] = w;
-                    }
-                    atomicOr(&s_mask[2 * a + (token >> 5)], 1u << (token & 31));
-                }
-                __syncwarp();
-                if (a >= 0 && (same >> lane) == 1u) s_off[a] += static_cast<uint16_t>(__popc(same));
-                __syncwarp();
-            }
-        }
-    }
+    Segments seg = {};
+    if constexpr (MODE >= kUp) seg = build_segments(tab, p.ids, pairs, p.topk, p.experts, p.cap, p.status);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_holder;
-    if constexpr (MODE >= kUp) active = *sh_active;
-    const int total = MODE == kDown ? active * p.kblocks : p.kblocks;     // K-blocks of a tile
-    const int num_tiles = MODE == kUp ? active * p.row_tiles * p.chunks : p.row_tiles;
+    const int total = MODE == kDown ? seg.count * p.kblocks : p.kblocks;     // K-blocks of a tile
+    const int num_tiles = MODE == kUp ? seg.count * p.row_tiles : p.row_tiles;
+    // this CTA's share of each tile's K-blocks
     const int k_begin = static_cast<int>(static_cast<int64_t>(total) * rank / nsplit);
-    const int k_count = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / nsplit) - k_begin;
+    const int k_end = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / nsplit);
 
-    // Tile w: kUp's go expert by expert, an expert's groups of tokens next to each other
-    // (they read the same weights).  False: no tokens.
-    auto get_tile = [&](int w, FewTile &t) -> bool {
-        t.begin = k_begin;
-        t.nblk = k_count;
-        t.ent = 0;
+    auto get_tile = [&](int w) {
+        FewTile t = {0, 0, w * ROWS, p.tokens};
         if constexpr (MODE == kUp) {
-            const int chunk = w % p.chunks, at = w / p.chunks;
-            const int a = at / p.row_tiles;
-            const int first = (a ? s_off[a - 1] : 0) + chunk * p.cap;
-            t.row0 = (at - a * p.row_tiles) * 128;
-            t.expert = s_exp[a];
-            t.ent = first;
-            t.ntok = min(static_cast<int>(s_off[a]) - first, p.cap);
-            return t.ntok > 0;
-        } else {
-            t.expert = 0;
-            t.row0 = w * ROWS;
-            t.ntok = p.tokens;
-            return true;
+            t.seg = w / p.row_tiles;
+            t.row0 = (w - t.seg * p.row_tiles) * 128;
+            t.expert = seg.expert[t.seg];
+            t.ntok = seg.tokens[t.seg];
         }
+        return t;
     };
-    // Four results of one token at weight rows n .. n + 3 (kUp: a warp holds the token's 128).
+    // Four results of one token at weight rows n .. n + 3 (kUp: a warp holds the token's
+    // 128; o is already silu(g) u).
     auto store = [&](const FewTile &tile, int t, int n, float (&o)[4]) {
         if constexpr (MODE == kUp) {
-            const float w = s_wsum[tile.ent + t];
+            // the routing weight, summed over the token's slots that name this expert
+            const int slot = seg.entry[seg.first[tile.seg] + t] / p.topk * p.topk + lane;
+            float w = lane < p.topk && __ldcg(p.ids + slot) == tile.expert ? __ldcg(p.weights + slot) : 0.0f;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, s);
             uint32_t m = 0;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -378,13 +426,17 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
             const float inv = inverse_scale(e8);
             uint32_t hi, lo;
             split4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv, hi, lo);
-            const int64_t row = 2 * static_cast<int64_t>(s_ent[tile.ent + t]);
-            *reinterpret_cast<uint32_t *>(p.out_codes + row * p.inner + n) = hi;
-            *reinterpret_cast<uint32_t *>(p.out_codes + (row + 1) * p.inner + n) = lo;
+            const int kblocks = p.inner >> 7, kb = tile.row0 >> 7;   // this tile is one K-block of kDown
+            uint8_t *image = p.out_image +
+                (static_cast<int64_t>(seg.unit[tile.seg]) * kblocks + kb * image_units(tile.ntok)) * 1024;
+            const uint32_t r = 2 * t, at = (lane & 3) * 4;
+            *reinterpret_cast<uint32_t *>(image + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + at) = hi;
+            *reinterpret_cast<uint32_t *>(image + (r + 1) * 128 + (((lane >> 2) ^ ((r + 1) & 7)) << 4) + at) = lo;
             if ((lane & 7) == 0) {
-                uint8_t *sf = p.out_scales + ((tile.row0 >> 7) * 2 * static_cast<int64_t>(pairs) + row) * 4 + (lane >> 3);
+                uint8_t *sf = p.out_image_sf + (static_cast<int64_t>(tile.seg) * kblocks + kb) * 512 + sf_word(r) * 4 +
+                              (lane >> 3);
                 sf[0] = static_cast<uint8_t>(hi_scale(e8));
-                sf[4] = static_cast<uint8_t>(lo_scale(e8));
+                sf[16] = static_cast<uint8_t>(lo_scale(e8));
             }
         } else if (n < p.rows) {
             if (p.f32) {
@@ -412,8 +464,8 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
     };
     auto gated = [](float g, float u) { return g / (1.0f + expf(-g)) * u; };
 
-    FewTile tile;
-    float *part = reinterpret_cast<float *>(smem_a);   // nsplit > 1: [ntok][ROWS], in operand row order
+    // nsplit > 1: this CTA's partial results [ntok][ROWS], in operand row order
+    float *part = MODE == kDown ? smem_out : reinterpret_cast<float *>(smem_a);
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -422,15 +474,15 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
         uint32_t issued = 0;
         bool drop = (p.debug_flags & DG_DEBUG_DROP_ONE_LOAD) && blockIdx.x == 0;
         for (int w = first_tile; w < num_tiles; w += tile_step) {
-            if (!get_tile(w, tile)) continue;
-            int a = 0, kb = tile.begin;
-            if (MODE == kDown) { a = kb / p.kblocks; kb -= a * p.kblocks; }
-            for (int i = 0; i < tile.nblk; ++i) {
+            const FewTile tile = get_tile(w);
+            int z = MODE == kDown ? k_begin / p.kblocks : 0;
+            int kb = k_begin - z * p.kblocks;
+            for (int i = k_begin; i < k_end; ++i) {
                 if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto producer_done;
                 if (drop) drop = false;   // diagnostic: this slot never fills
                 else issued |= 1u << slot;
                 if ((issued >> slot & 1u) && elect_one()) {
-                    const int e = MODE == kDown ? s_exp[a] : tile.expert;
+                    const int e = MODE == kDown ? seg.expert[z] : tile.expert;
                     const int slice = FP4 ? kb : kb >> 2;
                     const uint32_t *sf = p.sf + e * p.sf_expert + static_cast<int64_t>(slice) * p.sf_ld;
                     uint32_t sf_bytes[HALVES];
@@ -454,7 +506,7 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
                     }
                 }
                 __syncwarp();
-                if (++kb == p.kblocks && MODE == kDown) { kb = 0; ++a; }
+                if (++kb == p.kblocks && MODE == kDown) { kb = 0; ++z; }
                 if (++slot == S) { slot = 0; phase ^= 1; }
             }
         }
@@ -477,15 +529,21 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
         const uint64_t b_base = make_desc_kmajor_sw128(smem_u32(smem_b));
         const uint32_t sf_tmem = tmem_base + p.accs * HALVES * ncols;   // two slots of 4 HALVES + 4 columns
         for (int w = first_tile; w < num_tiles; w += tile_step) {
-            if (!get_tile(w, tile)) continue;
-            if (!mbar_wait_warp(&tempty_bar[acc], acc_phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto mma_done;
-            tc_fence_after_sync();
-            const uint32_t d_tmem = tmem_base + acc * HALVES * ncols;
-            // columns in use: the tokens', rounded up to the MMA's step of 16
-            const int n_used = MODE == kUp ? (2 * tile.ntok + 15) / 16 * 16 : ncols;
-            const uint32_t idesc = make_idesc_mxf8(128, n_used, 0, 0) | (FP4 ? 5u << 7 : 0u);   // A: E2M1 or E4M3
-            int kb = MODE == kDown ? tile.begin % p.kblocks : tile.begin;
-            for (int i = 0; i < tile.nblk; ++i, ++g) {
+            const FewTile tile = get_tile(w);
+            int z = MODE == kDown ? k_begin / p.kblocks : tile.seg;
+            int kb = MODE == kDown ? k_begin - z * p.kblocks : k_begin;
+            uint32_t d_tmem = 0, idesc = 0;
+            for (int i = k_begin; i < k_end; ++i, ++g) {
+                const bool start = i == k_begin || (MODE == kDown && kb == 0);
+                const bool end = i == k_end - 1 || (MODE == kDown && kb == p.kblocks - 1);
+                if (start) {
+                    if (!mbar_wait_warp(&tempty_bar[acc], acc_phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto mma_done;
+                    tc_fence_after_sync();
+                    d_tmem = tmem_base + acc * HALVES * ncols;
+                    // columns in use: the tokens', rounded up to the MMA's step of 16
+                    const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
+                    idesc = make_idesc_mxf8(128, (2 * tok + 15) / 16 * 16, 0, 0) | (FP4 ? 5u << 7 : 0u);   // A: E2M1 or E4M3
+                }
                 if (!mbar_wait_warp(&full_bar[slot], phase, ctl, DG_DEV_TIMEOUT)) goto mma_done;
                 tc_fence_after_sync();
                 if (elect_one()) {
@@ -505,17 +563,16 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
                         for (int h = 0; h < HALVES; ++h)
                             tc_mma_mxf8(d_tmem + h * ncols,
                                         a_base + static_cast<uint64_t>((slot * HALVES + h) * 1024 + 2 * k),
-                                        b_desc + 2 * k, id, sf + 4 * h, sf + 4 * HALVES, (i | k) != 0);
+                                        b_desc + 2 * k, id, sf + 4 * h, sf + 4 * HALVES, !start || k != 0);
                     }
                     tc_commit(&empty_bar[slot]);
+                    if (end) tc_commit(&tfull_bar[acc]);
                 }
                 __syncwarp();
-                if (++kb == p.kblocks) kb = 0;
+                if (end && ++acc == p.accs) { acc = 0; acc_phase ^= 1; }
+                if (++kb == p.kblocks) { kb = 0; ++z; }
                 if (++slot == S) { slot = 0; phase ^= 1; }
             }
-            if (elect_one()) tc_commit(&tfull_bar[acc]);
-            __syncwarp();
-            if (++acc == p.accs) { acc = 0; acc_phase ^= 1; }
         }
     mma_done:
         // TMEM is not freed before every MMA has finished
@@ -527,110 +584,62 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
         named_bar_sync(2, 64);
     } else if (warp >= FewConfig::kFirstB) {
         // ------------------------------------------------------------ the narrow operand
-        // The warps take the K-blocks in turn, at most as many warps as ring slots: a
-        // wait for the MMAs of block g - S tests one parity bit, which is unambiguous only
-        // if block g - 2S is known to be done; a warp's previous block g - teams implies that
-        // up to block g - teams - S.
-        const int teams = S < FewConfig::kBWarps ? S : FewConfig::kBWarps;
-        const int bw = warp - FewConfig::kFirstB;
-        const int q16 = lane & 15, sub = lane >> 4;   // two tokens at a time, 16 lanes each
-        if constexpr (MODE != kGemv) grid_dependency_wait();
-        int g = 0;   // K-blocks of the tiles before
-        for (int w = first_tile; w < num_tiles && bw < teams; w += tile_step) {
-            if (!get_tile(w, tile)) continue;
-            for (int i = (bw + teams - g % teams) % teams; i < tile.nblk; i += teams) {
-                const int slot = (g + i) % S;
-                if (!mbar_wait_warp(&empty_bar[slot], (((g + i) / S) & 1) ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
-                uint8_t *tile_b = smem_b + slot * b_bytes;
-                uint8_t *tile_sf = smem_sfb + slot * 512;
-                int kb = tile.begin + i, a = 0;
-                if (MODE == kDown) { a = kb / p.kblocks; kb -= a * p.kblocks; }
-                if constexpr (MODE == kGemvPre) {
+        if constexpr (MODE == kGemv) {
+            // The warps take the K-blocks in turn, at most as many warps as ring slots: a
+            // wait for the MMAs of block g - S tests one parity bit, which is unambiguous
+            // only if block g - 2S is known to be done; a warp's previous block g - teams
+            // implies that up to block g - teams - S.
+            const int teams = S < FewConfig::b_warps(MODE) ? S : FewConfig::b_warps(MODE);
+            const int bw = warp - FewConfig::kFirstB;
+            const int q16 = lane & 15, sub = lane >> 4;   // two tokens at a time, 16 lanes each
+            int g = 0;   // K-blocks of the tiles before
+            for (int w = first_tile; w < num_tiles && bw < teams; w += tile_step, g += k_end - k_begin) {
+                for (int i = (bw + teams - g % teams) % teams; i < k_end - k_begin; i += teams) {
+                    const int slot = (g + i) % S;
+                    if (!mbar_wait_warp(&empty_bar[slot], (((g + i) / S) & 1) ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
+                    const int kb = k_begin + i;
+                    for (int t0 = 0; t0 < p.tokens; t0 += 2) {
+                        const int t = t0 + sub;
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (t < p.tokens)
+                            v = __ldcg(reinterpret_cast<const uint4 *>(p.x + t * p.ldx + kb * 128 + q16 * 8));
+                        uint2 hi, lo;
+                        const uint32_t e8 = split_bf16(v, hi, lo);
+                        if (t < p.tokens)
+                            put_pieces(smem_b + slot * b_bytes, smem_sfb + slot * 512, t, q16, hi, lo, e8);
+                        __syncwarp();
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full_bar[slot]);
+                }
+            }
+        } else {
+            int slot = 0;
+            uint32_t phase = 0;
+            grid_dependency_wait();
+            for (int w = first_tile; w < num_tiles; w += tile_step) {
+                const FewTile tile = get_tile(w);
+                int z = MODE == kDown ? k_begin / p.kblocks : tile.seg;
+                int kb = MODE == kDown ? k_begin - z * p.kblocks : k_begin;
+                for (int i = k_begin; i < k_end; ++i) {
+                    if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(&full_bar[slot], b_bytes + 512);
-                        tma_load_2d(tile_b, &tm_x, &full_bar[slot], kb * 128, 0);
-                        bulk_load(tile_sf, p.scales + kb * 128, 512, &full_bar[slot]);
+                        const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
+                        const int units = image_units(tok);
+                        const int64_t before = MODE >= kUp ? seg.unit[z] : 0;
+                        const uint32_t sf_bytes = tok < 16 ? 32u * tok : 512u;
+                        mbar_arrive_expect_tx(&full_bar[slot], units * 1024 + sf_bytes);
+                        bulk_load(smem_b + slot * b_bytes, p.image + (before * p.kblocks + kb * units) * 1024, units * 1024,
+                                  &full_bar[slot]);
+                        bulk_load(smem_sfb + slot * 512, p.image_sf + (static_cast<int64_t>(z) * p.kblocks + kb) * 512,
+                                  sf_bytes, &full_bar[slot]);
                     }
                     __syncwarp();
-                    continue;
-                } else if constexpr (MODE == kGemv) {
-                    for (int t0 = 0; t0 < tile.ntok; t0 += 8) {
-                        uint4 v[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int t = t0 + 2 * u + sub;
-                            v[u] = make_uint4(0u, 0u, 0u, 0u);
-                            if (t < tile.ntok)
-                                v[u] = __ldcg(reinterpret_cast<const uint4 *>(p.x + t * p.ldx + kb * 128 + q16 * 8));
-                        }
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            if (t0 + 2 * u >= tile.ntok) break;
-                            const int t = t0 + 2 * u + sub;
-                            uint2 hi, lo;
-                            const uint32_t e8 = split_bf16(v[u], hi, lo);
-                            if (t >= tile.ntok) continue;
-                            // columns 2t and 2t + 1 (rows of 128 bytes, 128-byte swizzle)
-                            const uint32_t n = 2 * t;
-                            const uint32_t off = (q16 & 1) * 8;
-                            *reinterpret_cast<uint2 *>(tile_b + n * 128 + (((q16 >> 1) ^ (n & 7)) << 4) + off) = hi;
-                            *reinterpret_cast<uint2 *>(tile_b + (n + 1) * 128 + (((q16 >> 1) ^ ((n + 1) & 7)) << 4) +
-                                                       off) = lo;
-                            if ((q16 & 3) == 0) {
-                                uint8_t *s = tile_sf + sf_word(n) * 4 + (q16 >> 2);
-                                s[0] = static_cast<uint8_t>(hi_scale(e8));
-                                s[16] = static_cast<uint8_t>(lo_scale(e8));
-                            }
-                        }
-                        __syncwarp();
-                    }
-                } else {
-                    int begin = tile.ent, end = tile.ent + tile.ntok;
-                    if constexpr (MODE == kDown) {
-                        // columns of tokens that do not use this expert are zero, codes and scales
-                        for (int t = sub; t < p.cap; t += 2) {
-                            if (s_mask[2 * a + (t >> 5)] >> (t & 31) & 1u) continue;
-                            reinterpret_cast<uint4 *>(tile_b + t * 256)[q16] = make_uint4(0u, 0u, 0u, 0u);
-                            if (q16 < 2) reinterpret_cast<uint32_t *>(tile_sf)[sf_word(2 * t + q16)] = 0u;
-                        }
-                        __syncwarp();
-                        begin = a ? s_off[a - 1] : 0;
-                        end = s_off[a];
-                    }
-                    const int64_t k = static_cast<int64_t>(p.kblocks) * 128;
-                    const uint8_t *src = p.codes + (q16 >> 3) * k + kb * 128 + (q16 & 7) * 16;
-                    const uint32_t *src_sf = p.scales + static_cast<int64_t>(kb) * 2 * p.src_rows + (q16 & 1);
-                    for (int t0 = begin; t0 < end; t0 += 8) {
-                        uint4 v[4];
-                        uint32_t sf[4];
-                        int col[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int t = t0 + 2 * u + sub;
-                            if (t < end) {
-                                const int pair = s_ent[t];
-                                const int token = pair / p.topk;
-                                const int row = MODE == kUp ? token : pair;
-                                col[u] = MODE == kUp ? t - begin : token;
-                                v[u] = __ldcg(reinterpret_cast<const uint4 *>(src + 2 * row * k));
-                                sf[u] = __ldcg(src_sf + 2 * row);
-                            }
-                        }
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            if (t0 + 2 * u + sub < end) {
-                                const uint32_t n = 2 * col[u] + (q16 >> 3);
-                                *reinterpret_cast<uint4 *>(tile_b + n * 128 + (((q16 & 7) ^ (n & 7)) << 4)) = v[u];
-                                if (q16 < 2) reinterpret_cast<uint32_t *>(tile_sf)[sf_word(2 * col[u] + q16)] = sf[u];
-                            }
-                        }
-                    }
+                    if (++kb == p.kblocks) { kb = 0; ++z; }
+                    if (++slot == S) { slot = 0; phase ^= 1; }
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full_bar[slot]);
             }
-            g += tile.nblk;
         }
     b_done:
         __syncwarp();
@@ -641,58 +650,98 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
         int acc = 0, buf = 0;
         uint32_t acc_phase = 0;
         if constexpr (MODE != kGemv) grid_dependency_wait();       // C, and memory that the output may share
-        for (int w = first_tile; w < num_tiles; w += tile_step) {
-            if (!get_tile(w, tile)) continue;
-            // the four warps go on or give up together
-            const bool ok = mbar_wait_warp(&tfull_bar[acc], acc_phase, ctl, DG_DEV_TIMEOUT);
-            if (!named_bar_and(1, 128, ok)) break;
-            tc_fence_after_sync();
-            for (int t0 = 0; t0 < tile.ntok; t0 += 8) {
-                uint32_t v[HALVES][16];
+        // Sums of columns 2 t0 .. 2 t0 + 15 in pairs: 8 tokens' results at this thread's operand rows
+        auto read8 = [&](int t0, float (&r)[HALVES][8]) {
+            uint32_t v[HALVES][16];
 #pragma unroll
-                for (int h = 0; h < HALVES; ++h) {
+            for (int h = 0; h < HALVES; ++h)
+                tmem_ld_32x32b_x16(tmem_base + ((quad * 32) << 16) + (acc * HALVES + h) * ncols + 2 * t0, v[h]);
+            tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[h][j] = 0u;
-                    if (tile.nblk > 0)
-                        tmem_ld_32x32b_x16(tmem_base + ((quad * 32) << 16) + (acc * HALVES + h) * ncols + 2 * t0, v[h]);
-                }
-                tmem_ld_wait();
+            for (int h = 0; h < HALVES; ++h) {
+                reg_fence16(v[h]);
 #pragma unroll
-                for (int h = 0; h < HALVES; ++h) reg_fence16(v[h]);
-                if (t0 + 8 >= tile.ntok) {   // the accumulators are read
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&tempty_bar[acc]);
-                }
-                float *out = nsplit > 1 ? part + t0 * ROWS : smem_out + buf * 8 * OUT;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (t0 + j >= tile.ntok) break;
-                    float r[HALVES];
-#pragma unroll
-                    for (int h = 0; h < HALVES; ++h)
-                        r[h] = __uint_as_float(v[h][2 * j]) + __uint_as_float(v[h][2 * j + 1]);
-                    if (MODE == kUp && nsplit == 1) {
-                        out[j * OUT + quad * 32 + lane] = gated(r[0], r[HALVES - 1]);
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < HALVES; ++h) out[j * ROWS + h * 128 + quad * 32 + lane] = r[h];
-                    }
-                }
-                if (nsplit > 1) continue;
-                named_bar_sync(1, 128);
-                const int n = min(8, tile.ntok - t0) * (OUT / 4);
-                for (int q = id; q < n; q += 128) {
-                    const int t = q / (OUT / 4), l = q % (OUT / 4);
-                    float o[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) o[c] = out[t * OUT + (l >> 5) * 128 + 32 * c + (l & 31)];
-                    store(tile, t0 + t, tile.row0 + 4 * l, o);
-                }
-                buf ^= 1;
+                for (int j = 0; j < 8; ++j)
+                    r[h][j] = __uint_as_float(v[h][2 * j]) + __uint_as_float(v[h][2 * j + 1]);
             }
+        };
+        auto release = [&] {   // the accumulators are read
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty_bar[acc]);
             if (++acc == p.accs) { acc = 0; acc_phase ^= 1; }
+        };
+        // the four warps go on or give up together
+        auto wait_acc = [&] {
+            const bool ok = named_bar_and(1, 128, mbar_wait_warp(&tfull_bar[acc], acc_phase, ctl, DG_DEV_TIMEOUT));
+            tc_fence_after_sync();
+            return ok;
+        };
+        auto write_out = [&](const FewTile &tile, const float *src, int t0, int n) {   // n tokens from t0
+            for (int q = id; q < n * (OUT / 4); q += 128) {
+                const int t = q / (OUT / 4), l = q % (OUT / 4);
+                float o[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[c] = src[t * OUT + (l >> 5) * 128 + 32 * c + (l & 31)];
+                store(tile, t0 + t, tile.row0 + 4 * l, o);
+            }
+        };
+        for (int w = first_tile; w < num_tiles; w += tile_step) {
+            const FewTile tile = get_tile(w);
+            const int mine = quad * 32 + lane;
+            if constexpr (MODE == kDown) {
+                // each thread adds up its operand rows' results, token by token
+                for (int t = 0; t < p.tokens; ++t)
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h) smem_out[t * ROWS + h * 128 + mine] = 0.0f;
+                for (int i = k_begin; i < k_end;) {
+                    const int z = i / p.kblocks;
+                    if (!wait_acc()) goto epi_done;
+                    for (int t0 = 0; t0 < seg.tokens[z]; t0 += 8) {
+                        float r[HALVES][8];
+                        read8(t0, r);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            if (t0 + j >= seg.tokens[z]) break;
+                            const int token = seg.entry[seg.first[z] + t0 + j] / p.topk;
+#pragma unroll
+                            for (int h = 0; h < HALVES; ++h) smem_out[token * ROWS + h * 128 + mine] += r[h][j];
+                        }
+                    }
+                    release();
+                    i = (z + 1) * p.kblocks;
+                }
+                if (nsplit == 1) {
+                    named_bar_sync(1, 128);
+                    write_out(tile, smem_out, 0, p.tokens);
+                    named_bar_sync(1, 128);
+                }
+            } else {
+                if (!wait_acc()) break;
+                for (int t0 = 0; t0 < tile.ntok; t0 += 8) {
+                    float r[HALVES][8];
+                    read8(t0, r);
+                    const int n = min(8, tile.ntok - t0);
+                    float *out = nsplit > 1 ? part + t0 * ROWS : smem_out + buf * 8 * OUT;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (j >= n) break;
+                        if (MODE == kUp && nsplit == 1) {
+                            out[j * OUT + mine] = gated(r[0][j], r[HALVES - 1][j]);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < HALVES; ++h) out[j * ROWS + h * 128 + mine] = r[h][j];
+                        }
+                    }
+                    if (nsplit > 1) continue;
+                    named_bar_sync(1, 128);
+                    write_out(tile, out, t0, n);
+                    buf ^= 1;
+                }
+                release();
+            }
         }
+    epi_done:
         __syncwarp();
     }
 
@@ -705,8 +754,9 @@ __global__ void __launch_bounds__(FewConfig::kThreads, 2)
     if (nsplit == 1) return;
     // ---------------------------------------------------------------- sum over the cluster (one tile)
     cluster_sync();
-    if (first_tile < num_tiles && get_tile(first_tile, tile)) {
-        const uint32_t part0 = smem_u32(smem_a);
+    if (first_tile < num_tiles) {
+        const FewTile tile = get_tile(first_tile);
+        const uint32_t part0 = smem_u32(part);
         auto sum = [&](int idx) {
             float s = 0.0f;
             for (int r = 0; r < nsplit; ++r) s += ld_shared_cluster_f32(mapa_shared(part0 + 4u * idx, r));

@@ -484,7 +484,7 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
  *   c     bf16 [t, ldc] or NULL, may equal y; y bf16 [t, ldy]; 16-byte aligned,
  *         strides multiples of 8.
  *   workspace   device memory, 16-byte aligned, dg_moe_layer_workspace_bytes(t,
- *         topk, h, i) bytes; its contents need no initialisation and do not outlive
+ *         topk, h, i, experts) bytes; its contents need no initialisation and do not outlive
  *         the call.  Calls that may run at the same time need one each.
  *   h and i multiples of 128 (DG_ERR_ALIGNMENT); t <= 64, topk <= 16 and experts <=
  *   1024, else DG_ERR_UNSUPPORTED (more tokens: dg_m_grouped_*); t == 0 or h == 0
@@ -493,7 +493,7 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
  *   holds an infinity or a NaN gets NaN; the weights and scales of the named
  *   experts must be finite (a NaN there may reach every token of the call).
  */
-int64_t dg_moe_layer_workspace_bytes(int t, int topk, int h, int i);
+int64_t dg_moe_layer_workspace_bytes(int t, int topk, int h, int i, int experts);
 dg_status dg_moe_fp4_layer(const void *x, int64_t ldx, const int32_t *ids, const float *weights, const void *w1,
                            const void *sf1, const void *w2, const void *sf2, const void *c, int64_t ldc, void *y,
                            int64_t ldy, int t, int h, int i, int experts, int topk, void *workspace,

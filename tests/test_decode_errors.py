@@ -62,8 +62,8 @@ def test_layer_refusals(lib, fp4):
         nbytes = 1 << 24 if nbytes is None else nbytes
         return fn(P(x), ldx, P(ids), P(w), P(w1), P(sf1), P(w2), P(sf2), P(c), ldc, P(y), ldy, t, h, i, e, topk, P(ws),
                   nbytes, None, None)
-    need = lib.dg_moe_layer_workspace_bytes(3, 2, 256, 128)
-    assert need > 0 and lib.dg_moe_layer_workspace_bytes(-1, 2, 256, 128) == -1
+    need = lib.dg_moe_layer_workspace_bytes(3, 2, 256, 128, 4)
+    assert need > 0 and lib.dg_moe_layer_workspace_bytes(-1, 2, 256, 128, 4) == -1
     assert call(t=-1) == ARG and call(h=-128) == ARG and call(i=-128) == ARG and call(e=0) == ARG and call(topk=0) == ARG
     assert call(t=0) == OK and call(h=0) == OK
     assert call(t=65) == UNSUP and call(topk=17) == UNSUP and call(e=1025) == UNSUP

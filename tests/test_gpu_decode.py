@@ -300,7 +300,7 @@ def test_layer_slots(fmt):
     c = torch.randn(5, 256, generator=_gen(2)).bfloat16()
     ref, tol = D.layer_plain(s["x"], s["ids"], s["weights"], s["d1"], s["d2"], c)
     y = c.cuda()
-    ws = torch.full((binding.moe_layer_workspace_bytes(5, 3, 256, 256) + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((binding.moe_layer_workspace_bytes(5, 3, 256, 256, 6) + 64,), 0xFF, dtype=torch.uint8, device="cuda")
     _layer(s, status_is=binding.DG_DEV_BAD_GROUP, y=y, c=y, workspace=ws)
     _check(y, ref, tol, fmt)
     s["ids"][:] = -1
@@ -335,7 +335,7 @@ def test_layer_other_stream_graph_and_chain(fmt):
     other.synchronize()
     assert torch.equal(y, want)
     graph = torch.cuda.CUDAGraph()
-    ws = torch.empty(binding.moe_layer_workspace_bytes(6, 4, 512, 256), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(binding.moe_layer_workspace_bytes(6, 4, 512, 256, 16), dtype=torch.uint8, device="cuda")
     g1, g2 = torch.zeros_like(want), torch.zeros_like(want)
     with torch.cuda.graph(graph):
         LAYER[fmt](x, ids, wt, *args, g1, workspace=ws)
