@@ -40,21 +40,25 @@ struct Plan {
 template <bool FP4, int HALVES, int MODE>
 cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles,
                    int num_sms, cudaStream_t stream) {
-    const int fixed = FewConfig::smem_bytes(HALVES, a.cap, 0, MODE, a.tokens, a.topk, plan.split);
+    const int tables = MODE < kUp ? 0 : segment_table_bytes(a.tokens * a.topk, a.experts);
+    const int fixed = FewConfig::smem_bytes(HALVES, a.cap, 0, MODE, plan.split, tables);
     const int stage = FewConfig::stage_bytes(HALVES, a.cap);
     const int limit = plan.occ == 2 ? kSmemTwo : kSmemOne;
     int stages = (limit - fixed) / stage;
     if (stages > FewConfig::kMaxStages) stages = FewConfig::kMaxStages;
     if (stages > env("DG_ST", 99)) stages = env("DG_ST", 99);
     if (stages < 2) return cudaErrorInvalidConfiguration;
-    const int set = HALVES * 2 * a.cap, sf = 2 * (4 * HALVES + 4), most = plan.occ == 2 ? 256 : 512;
+    const int set = HALVES * 2 * a.cap, most = plan.occ == 2 ? 256 : 512;
+    const int sf = 2 * HALVES * 8 + (MODE == kDown ? HALVES * ((a.tokens + 7) & ~7) : 0);
     a.stages = stages;
     a.accs = (plan.split == 1 || MODE == kDown) && 2 * set + sf <= most ? 2 : 1;
     a.tmem_cols = pow2_at_least(a.accs * set + sf);
     if (a.tmem_cols > 512) return cudaErrorInvalidConfiguration;
-    const int smem = FewConfig::smem_bytes(HALVES, a.cap, stages, MODE, a.tokens, a.topk, plan.split);
+    const int smem = FewConfig::smem_bytes(HALVES, a.cap, stages, MODE, plan.split, tables);
     auto kernel = dg_few_rows_kernel<FP4, HALVES, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -66,7 +70,7 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     const int grid = plan.split > 1 ? max_tiles * plan.split
                                     : (max_tiles < plan.occ * num_sms ? max_tiles : plan.occ * num_sms);
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(FewConfig::threads(MODE));
+    cfg.blockDim = dim3(FewConfig::threads(HALVES, MODE));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -199,7 +203,7 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     const int cap = segment_capacity(p.t, p.topk, p.experts), pairs = p.t * p.topk;
     const int kh = p.h / 128, ki = p.i / 128;
     Dependent split(dim3(static_cast<unsigned>(kh), static_cast<unsigned>(cdiv(pairs, 64))),
-                    FewConfig::table_bytes(kUp, pairs), stream);
+                    segment_table_bytes(pairs, p.experts), stream);
     cudaError_t e = cudaLaunchKernelEx(&split.cfg, dg_layer_split_kernel, p.x, p.ldx, p.ids, p.t, p.topk, p.experts,
                                        cap, kh, x_image, x_sf);
     if (e != cudaSuccess) return e;

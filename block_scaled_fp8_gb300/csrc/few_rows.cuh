@@ -20,9 +20,11 @@
 //   warp 0      producer: weights by TMA (a 3-D box that takes weight row 4l + c to
 //               operand row 32c + l, so that 128 consecutive scale words are already in
 //               the order in which tcgen05.cp takes them to TMEM), scales by bulk copy.
-//   warp 1      TMEM owner, MMA issuer.
+//   warp 1      TMEM owner, MMA issuer (of the first half; warp 6 of the second: waits,
+//               scale copies, MMAs and commits of a K-block take one warp about 490
+//               cycles, and two halves of FP4 weights arrive every 710).
 //   warps 2..5  epilogue, one TMEM lane quadrant each.
-//   warp 6..    the narrow operand.
+//   the rest    the narrow operand.
 // Many tiles: the CTAs are persistent and take tiles in turn, the ring of K-blocks running
 // on across them.  Few tiles: one tile per cluster, K split over its CTAs, which add
 // their FP32 partial results in rank order through distributed shared memory: no
@@ -38,8 +40,8 @@
 //           images.  The epilogue is w silu(g) u (w the routing weight), split again
 //           and written as the image that kDown reads.
 //   kDown     K runs over all segments; the accumulators of a segment are added to the
-//           FP32 results of its tokens in shared memory while the next segment's
-//           products run.
+//           FP32 results of its tokens, columns of their own in TMEM, while the next
+//           segment's products run.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -86,21 +88,20 @@ struct FewArgs {
 };
 
 struct FewConfig {
-    static constexpr int kFirstEpi = 2, kFirstB = 6;
+    static constexpr int kFirstEpi = 2;
+    static constexpr int first_b(int halves) { return halves == 2 ? 7 : 6; }
     static constexpr int b_warps(int mode) { return mode == kGemv ? 4 : 1; }
-    static constexpr int threads(int mode) { return 32 * (kFirstB + b_warps(mode)); }
+    static constexpr int threads(int halves, int mode) { return 32 * (first_b(halves) + b_warps(mode)); }
     static constexpr int kAlign = 1024;
     static constexpr int kBarBytes = 512;
     static constexpr int kMaxStages = 24;
     static int stage_bytes(int halves, int cap) { return halves * 16384 + 2 * cap * 128 + halves * 512 + 512; }
-    // kDown: the tokens' FP32 results; else two buffers of 8 tokens' (split tiles leave theirs in the ring)
-    static int out_bytes(int halves, int mode, int tokens, int split) {
-        return mode == kDown ? tokens * halves * 512 : split > 1 ? 0 : 2 * 8 * (mode == kUp ? 128 : halves * 128) * 4;
+    // two buffers of 8 tokens' FP32 results (split tiles leave theirs in the ring)
+    static int out_bytes(int halves, int mode, int split) {
+        return split > 1 ? 0 : 2 * 8 * (mode == kUp ? 128 : halves * 128) * 4;
     }
-    static int table_bytes(int mode, int pairs) { return mode < kUp ? 0 : (256 + 24 * pairs + 15) / 16 * 16; }
-    static int smem_bytes(int halves, int cap, int stages, int mode, int tokens, int topk, int split) {
-        return kAlign + stages * stage_bytes(halves, cap) + out_bytes(halves, mode, tokens, split) + kBarBytes +
-               table_bytes(mode, tokens * topk);
+    static int smem_bytes(int halves, int cap, int stages, int mode, int split, int tables) {
+        return kAlign + stages * stage_bytes(halves, cap) + out_bytes(halves, mode, split) + kBarBytes + tables;
     }
 };
 
@@ -180,50 +181,49 @@ __global__ void __launch_bounds__(256) dg_few_split_kernel(const uint16_t *x, in
 }
 
 // The layer's routing, as every CTA of its kernels derives it from the ids (in shared
-// memory; the same in all of them): the slots of each expert in use form one segment
+// memory; the same in all of them): the tokens of each expert in use form one segment
 // after another of up to `cap` tokens.
 struct Segments {
-    int count;
+    int count, entries;
     uint16_t *expert;   // [count]
     uint16_t *first;    // [count] first entry
     uint16_t *tokens;   // [count]
     uint16_t *unit;     // [count] units of the segments before (image_units)
-    uint16_t *entry;    // [pairs] slot (token * topk + j), by expert, in slot order
-    uint16_t *of_entry; // [pairs] segment of each entry
-    int *ids;           // [pairs] id of a token's first slot with it, or -1
+    uint16_t *token;    // [entries] by expert, ascending
+    uint16_t *of_entry; // [entries] segment
 };
 
-// Tables of 256 + 24 * pairs bytes at `tab`; called by all threads of a CTA.
+__host__ __device__ constexpr int segment_table_bytes(int pairs, int experts) {
+    return (16 + 12 * experts + 14 * pairs + 15) / 16 * 16;
+}
+
+// Tables of segment_table_bytes at `tab`; called by all threads of a CTA.
 __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids, int pairs, int topk, int experts,
                                                    int cap, int32_t *status) {
-    uint32_t *mask = reinterpret_cast<uint32_t *>(tab);   // [32] experts in use
-    int *pre = tab + 32;                                  // [32] experts in use before this word; then the counts
+    uint32_t *mask = reinterpret_cast<uint32_t *>(tab + 4);            // [experts][2] tokens of each expert
+    uint16_t *start = reinterpret_cast<uint16_t *>(mask + 2 * experts);   // [experts] first entry
+    uint16_t *seg0 = start + experts;                                     // [experts] first segment
+    uint16_t *s_ids = seg0 + experts;                                     // [pairs]
     Segments s;
-    s.ids = tab + 64;
-    uint16_t *off = reinterpret_cast<uint16_t *>(s.ids + pairs);   // [active] end of each expert's entries
-    uint16_t *exp = off + pairs;                                   // [active]
-    s.entry = exp + pairs;
-    s.of_entry = s.entry + pairs;
+    s.token = s_ids + pairs;
+    s.of_entry = s.token + pairs;
     s.expert = s.of_entry + pairs;
     s.first = s.expert + pairs;
     s.tokens = s.first + pairs;
     s.unit = s.tokens + pairs;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == 0) mask[lane] = 0u;
+    const int lane = threadIdx.x & 31;
+    for (int e = threadIdx.x; e < 2 * experts; e += blockDim.x) mask[e] = 0u;
     __syncthreads();
     for (int q = threadIdx.x; q < pairs; q += blockDim.x) {
-        int e = __ldcg(ids + q);
-        if (e >= experts) {
-            if (status) atomicOr(status, DG_DEV_BAD_GROUP);
-            e = -1;
-        }
-        for (int r = q - q % topk; r < q && e >= 0; ++r)
-            if (__ldcg(ids + r) == e) e = -1;
-        s.ids[q] = e < 0 ? -1 : e;
-        if (e >= 0) atomicOr(&mask[e >> 5], 1u << (e & 31));
+        const int e = __ldcg(ids + q);
+        const bool ok = e >= 0 && e < experts;
+        if (e >= experts && status) atomicOr(status, DG_DEV_BAD_GROUP);
+        s_ids[q] = ok ? static_cast<uint16_t>(e) : 0xFFFFu;
+        const int t = q / topk;
+        if (ok) atomicOr(&mask[2 * e + (t >> 5)], 1u << (t & 31));
     }
     __syncthreads();
-    if (warp == 0) {
+    if (threadIdx.x < 32) {
         auto scan = [&](int v) {   // inclusive
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -232,66 +232,47 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
             }
             return v;
         };
-        const int cnt = __popc(mask[lane]);
-        const int inc = scan(cnt);
-        pre[lane] = inc - cnt;
-        const int used = __shfl_sync(0xFFFFFFFFu, inc, 31);
-        for (int a = lane; a < used; a += 32) off[a] = 0;
-        __syncwarp();
-        // one warp counts, scans and fills, in slot order
-        auto rank_of = [&](int e) {
-            return e < 0 ? -1 - lane : pre[e >> 5] + __popc(mask[e >> 5] & ((1u << (e & 31)) - 1));
-        };
-        for (int q0 = 0; q0 < pairs; q0 += 32) {
-            const int e = q0 + lane < pairs ? s.ids[q0 + lane] : -1;
-            const int a = rank_of(e);
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
-            if (a >= 0 && (same >> lane) == 1u) {   // the last holder of this expert
-                off[a] += static_cast<uint16_t>(__popc(same));
-                exp[a] = static_cast<uint16_t>(e);
-            }
-            __syncwarp();
-        }
         int run = 0, seg = 0, unit = 0;
-        for (int a0 = 0; a0 < used; a0 += 32) {
-            const int n = a0 + lane < used ? off[a0 + lane] : 0;
-            const int mine = (n + cap - 1) / cap;
+        for (int e0 = 0; e0 < experts; e0 += 32) {
+            const int e = e0 + lane;
+            const int n = e < experts ? __popc(mask[2 * e]) + __popc(mask[2 * e + 1]) : 0;
+            const int segs = (n + cap - 1) / cap;
             const int units = n / cap * image_units(cap) + image_units(n % cap);
-            const int in_n = scan(n), in_s = scan(mine), in_u = scan(units);
-            if (a0 + lane < used) {
-                int first = run + in_n - n, u = unit + in_u - units;
-                off[a0 + lane] = static_cast<uint16_t>(first);
-                int left = n;
-                for (int z = seg + in_s - mine; z < seg + in_s; ++z) {
-                    const int t = min(left, cap);
-                    s.expert[z] = exp[a0 + lane];
-                    s.first[z] = static_cast<uint16_t>(first);
-                    s.tokens[z] = static_cast<uint16_t>(t);
-                    s.unit[z] = static_cast<uint16_t>(u);
-                    for (int j = 0; j < t; ++j) s.of_entry[first + j] = static_cast<uint16_t>(z);
-                    first += t;
-                    left -= t;
-                    u += image_units(t);
-                }
+            const int in_n = scan(n), in_su = scan(segs | units << 16);
+            int first = run + in_n - n, z = seg + (in_su & 0xFFFF) - segs, u = unit + (in_su >> 16) - units;
+            if (n > 0) {
+                start[e] = static_cast<uint16_t>(first);
+                seg0[e] = static_cast<uint16_t>(z);
+            }
+            for (int left = n; left > 0; left -= cap, ++z) {
+                const int t = min(left, cap);
+                s.expert[z] = static_cast<uint16_t>(e);
+                s.first[z] = static_cast<uint16_t>(first);
+                s.tokens[z] = static_cast<uint16_t>(t);
+                s.unit[z] = static_cast<uint16_t>(u);
+                first += t;
+                u += image_units(t);
             }
             run += __shfl_sync(0xFFFFFFFFu, in_n, 31);
-            seg += __shfl_sync(0xFFFFFFFFu, in_s, 31);
-            unit += __shfl_sync(0xFFFFFFFFu, in_u, 31);
+            const int all = __shfl_sync(0xFFFFFFFFu, in_su, 31);
+            seg += all & 0xFFFF;
+            unit += all >> 16;
         }
-        __syncwarp();
-        for (int q0 = 0; q0 < pairs; q0 += 32) {
-            const int q = q0 + lane;
-            const int a = rank_of(q < pairs ? s.ids[q] : -1);
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, a);
-            if (a >= 0) s.entry[off[a] + __popc(same & ((1u << lane) - 1))] = static_cast<uint16_t>(q);
-            __syncwarp();
-            if (a >= 0 && (same >> lane) == 1u) off[a] += static_cast<uint16_t>(__popc(same));
-            __syncwarp();
-        }
-        if (lane == 0) pre[0] = seg;
+        if (lane == 0) { tab[0] = seg; tab[1] = run; }
     }
     __syncthreads();
-    s.count = pre[0];
+    for (int q = threadIdx.x; q < pairs; q += blockDim.x) {
+        const int e = s_ids[q], t = q / topk;
+        if (e == 0xFFFF) continue;
+        // (a token that names an expert twice writes the same entry twice)
+        const uint32_t below = (1u << (t & 31)) - 1u;
+        const int at = t < 32 ? __popc(mask[2 * e] & below) : __popc(mask[2 * e]) + __popc(mask[2 * e + 1] & below);
+        s.token[start[e] + at] = static_cast<uint16_t>(t);
+        s.of_entry[start[e] + at] = static_cast<uint16_t>(seg0[e] + at / cap);
+    }
+    __syncthreads();
+    s.count = tab[0];
+    s.entries = tab[1];
     return s;
 }
 
@@ -303,12 +284,11 @@ __global__ void __launch_bounds__(256) dg_layer_split_kernel(const uint16_t *x, 
     grid_dependency_wait();
     grid_launch_dependents();
     const Segments s = build_segments(split_tab, ids, tokens * topk, topk, experts, cap, nullptr);
-    const int entries = s.count ? s.first[s.count - 1] + s.tokens[s.count - 1] : 0;
     const int q16 = threadIdx.x & 15, kb = blockIdx.x;
-    for (int at0 = blockIdx.y * 16; at0 < entries; at0 += gridDim.y * 16) {
+    for (int at0 = blockIdx.y * 16; at0 < s.entries; at0 += gridDim.y * 16) {
         const int at = at0 + static_cast<int>(threadIdx.x >> 4);
-        const bool in = at < entries;
-        const int row = in ? s.entry[at] / topk : 0;
+        const bool in = at < s.entries;
+        const int row = in ? s.token[at] : 0;
         const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(x + row * ldx + kb * 128 + q16 * 8));
         uint2 hi, lo;
         const uint32_t e8 = split_bf16(v, hi, lo);
@@ -329,11 +309,13 @@ struct FewTile {
 };
 
 template <bool FP4, int HALVES, int MODE>
-__global__ void __launch_bounds__(FewConfig::threads(MODE), 2)
+__global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     dg_few_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ FewArgs p) {
     constexpr int ROWS = HALVES * 128;
     constexpr int OUT = MODE == kUp ? 128 : ROWS;     // results per token and tile
-    constexpr int NT = FewConfig::threads(MODE);
+    constexpr int NT = FewConfig::threads(HALVES, MODE);
+    constexpr int FIRST_B = FewConfig::first_b(HALVES);
+    constexpr int SF = 4 + 4;                         // TMEM columns of a K-block's scales: weights', activations'
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -347,14 +329,13 @@ __global__ void __launch_bounds__(FewConfig::threads(MODE), 2)
     uint8_t *smem_sfa = smem_b + S * b_bytes;
     uint8_t *smem_sfb = smem_sfa + S * HALVES * 512;
     float *smem_out = reinterpret_cast<float *>(smem_sfb + S * 512);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(
-        smem_out + (MODE == kDown ? p.tokens * ROWS : nsplit > 1 ? 0 : 2 * 8 * OUT));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_out + (nsplit > 1 ? 0 : 2 * 8 * OUT));
     uint64_t *full_bar = bars;              // [S] weights and scales landed, pieces landed or written
     uint64_t *empty_bar = bars + S;         // [S] the slot's MMAs are done
     uint64_t *tfull_bar = bars + 2 * S;     // [2] accumulators complete
     uint64_t *tempty_bar = tfull_bar + 2;   // [2] accumulators read
-    uint64_t *drain_bar = tempty_bar + 2;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + 1);
+    uint64_t *drain_bar = tempty_bar + 2;   // [HALVES]
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + HALVES);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *tab = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + FewConfig::kBarBytes);
 
@@ -364,8 +345,9 @@ __global__ void __launch_bounds__(FewConfig::threads(MODE), 2)
     const int first_tile = blockIdx.x / nsplit, tile_step = gridDim.x / nsplit;
 
     if (warp == 0) {
-        for (int i = lane; i < 2 * S + 5; i += 32)
-            mbar_init(bars + i, i < S ? 2 : i == 2 * S + 2 || i == 2 * S + 3 ? 4 : 1);
+        // arrivals: full 2 (weights, pieces), empty and tfull one per issuer, tempty 4, drain 1
+        for (int i = lane; i < 2 * S + 4 + HALVES; i += 32)
+            mbar_init(bars + i, i < S ? 2 : i < 2 * S + 2 ? HALVES : i < 2 * S + 4 ? 4 : 1);
         if (lane == 0) {
             *abort_flag = 0;
             tma_prefetch_desc(&tm_w);
@@ -410,7 +392,7 @@ __global__ void __launch_bounds__(FewConfig::threads(MODE), 2)
     auto store = [&](const FewTile &tile, int t, int n, float (&o)[4]) {
         if constexpr (MODE == kUp) {
             // the routing weight, summed over the token's slots that name this expert
-            const int slot = seg.entry[seg.first[tile.seg] + t] / p.topk * p.topk + lane;
+            const int slot = seg.token[seg.first[tile.seg] + t] * p.topk + lane;
             float w = lane < p.topk && __ldcg(p.ids + slot) == tile.expert ? __ldcg(p.weights + slot) : 0.0f;
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, s);
@@ -464,8 +446,13 @@ __global__ void __launch_bounds__(FewConfig::threads(MODE), 2)
     };
     auto gated = [](float g, float u) { return g / (1.0f + expf(-g)) * u; };
 
+    // TMEM columns: accumulator sets, two scale slots for each issuer, kDown's results
+    const uint32_t sf_tmem = tmem_base + p.accs * HALVES * ncols;
+    const uint32_t y_tmem = sf_tmem + 2 * HALVES * SF;          // [HALVES][tokens, up to 8]
+    const int y_cols = (p.tokens + 7) & ~7;
+
     // nsplit > 1: this CTA's partial results [ntok][ROWS], in operand row order
-    float *part = MODE == kDown ? smem_out : reinterpret_cast<float *>(smem_a);
+    float *part = reinterpret_cast<float *>(smem_a);
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -513,7 +500,7 @@ __global__ void __launch_bounds__(FewConfig::threads(MODE), 2)
     producer_done:
         // Normally every load has landed once the MMAs are done.  After a wait that ran
         // out, never leave with loads in flight: give them the time limit once more.
-        named_bar_sync(2, 64);   // the MMA warp is done with its waits
+        named_bar_sync(2, 32 + 32 * HALVES);   // the issuers are done with their waits
         if (lane == 0 && *abort_flag) {
             const uint64_t t0 = global_timer_ns();
             for (int s = 0; s < S; ++s)
@@ -521,55 +508,53 @@ __global__ void __launch_bounds__(FewConfig::threads(MODE), 2)
                        !mbar_try_wait(smem_u32(&full_bar[s]), s < slot ? phase : phase ^ 1)) {}
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        int slot = 0, acc = 0, g = 0;
-        uint32_t phase = 0, acc_phase = 0;
-        const uint64_t a_base = make_desc_kmajor_sw128(smem_u32(smem_a));
+    } else if (warp == 1 || (HALVES == 2 && warp == FIRST_B - 1)) {
+        // ------------------------------------------------------------ MMA issuers
+        const int h = warp == 1 ? 0 : 1;
+        int slot = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0, sf = sf_tmem + 2 * h * SF, sf_flip = 0;
+        const uint64_t a_base = make_desc_kmajor_sw128(smem_u32(smem_a + h * 16384));
         const uint64_t b_base = make_desc_kmajor_sw128(smem_u32(smem_b));
-        const uint32_t sf_tmem = tmem_base + p.accs * HALVES * ncols;   // two slots of 4 HALVES + 4 columns
+        const uint64_t sfa_base = make_desc_sf_32x128b(smem_u32(smem_sfa + h * 512));
+        const uint64_t sfb_base = make_desc_sf_32x128b(smem_u32(smem_sfb));
         for (int w = first_tile; w < num_tiles; w += tile_step) {
             const FewTile tile = get_tile(w);
             int z = MODE == kDown ? k_begin / p.kblocks : tile.seg;
             int kb = MODE == kDown ? k_begin - z * p.kblocks : k_begin;
-            uint32_t d_tmem = 0, idesc = 0;
-            for (int i = k_begin; i < k_end; ++i, ++g) {
-                const bool start = i == k_begin || (MODE == kDown && kb == 0);
-                const bool end = i == k_end - 1 || (MODE == kDown && kb == p.kblocks - 1);
-                if (start) {
+            uint32_t d_tmem = 0, idesc = 0, more = 0;
+            for (int i = k_begin; i < k_end; ++i) {
+                if (more == 0) {   // a tile, or kDown's next segment
                     if (!mbar_wait_warp(&tempty_bar[acc], acc_phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto mma_done;
-                    tc_fence_after_sync();
-                    d_tmem = tmem_base + acc * HALVES * ncols;
+                    d_tmem = tmem_base + (acc * HALVES + h) * ncols;
                     // columns in use: the tokens', rounded up to the MMA's step of 16
                     const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
                     idesc = make_idesc_mxf8(128, (2 * tok + 15) / 16 * 16, 0, 0) | (FP4 ? 5u << 7 : 0u);   // A: E2M1 or E4M3
                 }
+                const bool end = i == k_end - 1 || (MODE == kDown && kb == p.kblocks - 1);
                 if (!mbar_wait_warp(&full_bar[slot], phase, ctl, DG_DEV_TIMEOUT)) goto mma_done;
                 tc_fence_after_sync();
                 if (elect_one()) {
-                    const uint32_t sf = sf_tmem + (g & 1) * (4 * HALVES + 4);
-#pragma unroll
-                    for (int h = 0; h < HALVES; ++h)
-                        tc_cp_32x128b_warpx4(sf + 4 * h,
-                                             make_desc_sf_32x128b(smem_u32(smem_sfa + (slot * HALVES + h) * 512)));
-                    tc_cp_32x128b_warpx4(sf + 4 * HALVES, make_desc_sf_32x128b(smem_u32(smem_sfb + slot * 512)));
+                    const uint32_t sf_now = sf + sf_flip;
+                    tc_cp_32x128b_warpx4(sf_now, sfa_base + static_cast<uint64_t>(slot * HALVES * 32));
+                    tc_cp_32x128b_warpx4(sf_now + 4, sfb_base + static_cast<uint64_t>(slot * 32));
+                    const uint64_t a_desc = a_base + static_cast<uint64_t>(slot * HALVES * 1024);
                     const uint64_t b_desc = b_base + static_cast<uint64_t>(slot * (b_bytes >> 4));
+                    // scale byte: the activations' and FP4 weights' k-th 32 K, FP8 weights' 128-K block
+                    const uint32_t id0 = idesc | (FP4 ? 0u : static_cast<uint32_t>(kb & 3) << 29);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        // scale byte: the activations' and FP4 weights' k-th 32 K, FP8 weights' 128-K block
-                        const uint32_t id = idesc | (static_cast<uint32_t>(k) << 4) |
-                                            (static_cast<uint32_t>(FP4 ? k : kb & 3) << 29);
-#pragma unroll
-                        for (int h = 0; h < HALVES; ++h)
-                            tc_mma_mxf8(d_tmem + h * ncols,
-                                        a_base + static_cast<uint64_t>((slot * HALVES + h) * 1024 + 2 * k),
-                                        b_desc + 2 * k, id, sf + 4 * h, sf + 4 * HALVES, !start || k != 0);
-                    }
+                    for (uint32_t k = 0; k < 4; ++k)
+                        tc_mma_mxf8(d_tmem, a_desc + 2 * k, b_desc + 2 * k, id0 | (k << 4) | (FP4 ? k << 29 : 0u), sf_now,
+                                    sf_now + 4, more | k);
                     tc_commit(&empty_bar[slot]);
                     if (end) tc_commit(&tfull_bar[acc]);
                 }
                 __syncwarp();
-                if (end && ++acc == p.accs) { acc = 0; acc_phase ^= 1; }
+                sf_flip ^= SF;
+                more = 1;
+                if (end) {
+                    more = 0;
+                    if (++acc == p.accs) { acc = 0; acc_phase ^= 1; }
+                }
                 if (++kb == p.kblocks) { kb = 0; ++z; }
                 if (++slot == S) { slot = 0; phase ^= 1; }
             }
@@ -577,12 +562,12 @@ __global__ void __launch_bounds__(FewConfig::threads(MODE), 2)
     mma_done:
         // TMEM is not freed before every MMA has finished
         if (elect_one()) {
-            tc_commit(drain_bar);
-            mbar_wait_drain(drain_bar, 0, ctl);
+            tc_commit(&drain_bar[h]);
+            mbar_wait_drain(&drain_bar[h], 0, ctl);
         }
         __syncwarp();
-        named_bar_sync(2, 64);
-    } else if (warp >= FewConfig::kFirstB) {
+        named_bar_sync(2, 32 + 32 * HALVES);
+    } else if (warp >= FIRST_B) {
         // ------------------------------------------------------------ the narrow operand
         if constexpr (MODE == kGemv) {
             // The warps take the K-blocks in turn, at most as many warps as ring slots: a
@@ -590,7 +575,7 @@ __global__ void __launch_bounds__(FewConfig::threads(MODE), 2)
             // only if block g - 2S is known to be done; a warp's previous block g - teams
             // implies that up to block g - teams - S.
             const int teams = S < FewConfig::b_warps(MODE) ? S : FewConfig::b_warps(MODE);
-            const int bw = warp - FewConfig::kFirstB;
+            const int bw = warp - FIRST_B;
             const int q16 = lane & 15, sub = lane >> 4;   // two tokens at a time, 16 lanes each
             int g = 0;   // K-blocks of the tiles before
             for (int w = first_tile; w < num_tiles && bw < teams; w += tile_step, g += k_end - k_begin) {
@@ -690,31 +675,60 @@ __global__ void __launch_bounds__(FewConfig::threads(MODE), 2)
             const FewTile tile = get_tile(w);
             const int mine = quad * 32 + lane;
             if constexpr (MODE == kDown) {
-                // each thread adds up its operand rows' results, token by token
-                for (int t = 0; t < p.tokens; ++t)
-#pragma unroll
-                    for (int h = 0; h < HALVES; ++h) smem_out[t * ROWS + h * 128 + mine] = 0.0f;
+                const uint32_t y0 = y_tmem + ((quad * 32) << 16);
+                for (int c = 0; c < HALVES * y_cols; ++c) tmem_st_32x32b_x1(y0 + c, 0u);
+                tmem_st_wait();
                 for (int i = k_begin; i < k_end;) {
                     const int z = i / p.kblocks;
                     if (!wait_acc()) goto epi_done;
-                    for (int t0 = 0; t0 < seg.tokens[z]; t0 += 8) {
+                    const int tok = seg.tokens[z];
+                    for (int t0 = 0; t0 < tok; t0 += 8) {
                         float r[HALVES][8];
+                        uint32_t y[HALVES][8], at[8];
                         read8(t0, r);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            if (t0 + j >= seg.tokens[z]) break;
-                            const int token = seg.entry[seg.first[z] + t0 + j] / p.topk;
+                            if (t0 + j >= tok) break;
+                            at[j] = y0 + seg.token[seg.first[z] + t0 + j];
 #pragma unroll
-                            for (int h = 0; h < HALVES; ++h) smem_out[token * ROWS + h * 128 + mine] += r[h][j];
+                            for (int h = 0; h < HALVES; ++h) y[h][j] = tmem_ld_32x32b_x1(at[j] + h * y_cols);
+                        }
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            if (t0 + j >= tok) break;
+#pragma unroll
+                            for (int h = 0; h < HALVES; ++h) {
+                                reg_fence1(y[h][j]);
+                                tmem_st_32x32b_x1(at[j] + h * y_cols, __float_as_uint(__uint_as_float(y[h][j]) + r[h][j]));
+                            }
                         }
                     }
+                    tmem_st_wait();
                     release();
                     i = (z + 1) * p.kblocks;
                 }
-                if (nsplit == 1) {
+                for (int t0 = 0; t0 < p.tokens; t0 += 8) {
+                    const int n = min(8, p.tokens - t0);
+                    float *out = nsplit > 1 ? part + t0 * ROWS : smem_out + buf * 8 * OUT;
+                    uint32_t y[HALVES][8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h) y[h][j] = tmem_ld_32x32b_x1(y0 + h * y_cols + t0 + j);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h) {
+                            reg_fence1(y[h][j]);
+                            if (j < n) out[j * ROWS + h * 128 + mine] = __uint_as_float(y[h][j]);
+                        }
+                    }
+                    if (nsplit > 1) continue;
                     named_bar_sync(1, 128);
-                    write_out(tile, smem_out, 0, p.tokens);
-                    named_bar_sync(1, 128);
+                    write_out(tile, out, t0, n);
+                    buf ^= 1;
                 }
             } else {
                 if (!wait_acc()) break;
