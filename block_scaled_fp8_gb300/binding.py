@@ -436,40 +436,61 @@ def dg_m_grouped_fp8_gemm_nt_masked(a, sfa, b, sfb, d, masked_m, expected_m: int
 
 
 # --------------------------------------------------------------------- decode: few rows, routing, the MoE layer
+#
+# Calls of a few microseconds: these marshal with as few Python steps as they can
+# (plain integers for the pointers, the raw handle of the current stream).
 
 def _ld(t) -> int:
     """Row stride in elements; a single row's own length where its stride says nothing."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return t.stride(0) if t.size(0) > 1 else max(t.stride(0), t.size(1))
+
+
+def _raw_stream(stream, t) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _fail(fn: str, status: int):
+    raise DGError(fn, status, lib().dg_status_string(status).decode())
+
+
+def _workspace(nbytes: int, t, stream):
+    """A workspace on t's device, allocated on the current stream; a caller's other
+    stream waits for that and is made known to the allocator."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+    if stream is not None and ws.is_cuda:
+        stream.wait_stream(torch.cuda.current_stream())
+        ws.record_stream(stream)
+    return ws
 
 
 def gemv_workspace_bytes(m: int, n: int, k: int) -> int:
     return int(lib().dg_bf16_gemv_workspace_bytes(m, n, k))
 
 
-def _workspace(nbytes: int, workspace, device, stream):
-    """The caller's workspace, or one allocated on the current stream; a caller's other
-    stream waits for that and is made known to the allocator."""
-    if workspace is None and nbytes > 0:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        if stream is not None and workspace.is_cuda:
-            stream.wait_stream(torch.cuda.current_stream())
-            workspace.record_stream(stream)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
-
-
 def _gemv(fn: str, fp4: bool, dtype, a, b, sfb, d, c, workspace, status, stream):
     m, k = a.shape
-    n = b.shape[0]
-    assert a.dtype == torch.bfloat16 and b.dtype == (torch.uint8 if fp4 else torch.float8_e4m3fn)
-    assert sfb.dtype == torch.int32 and sfb.is_contiguous()
-    assert b.shape[1] == (k // 2 if fp4 else k) and sfb.numel() >= (-(-k // (128 if fp4 else 512))) * ((n + 3) // 4 * 4)
-    assert d.dtype == dtype and d.shape == (m, n) and a.stride(1) == 1 and b.stride(1) == 1 and d.stride(1) == 1
-    assert c is None or (c.dtype == dtype and c.shape == d.shape and c.stride(1) == 1)
-    L = lib()
-    ws, nbytes = _workspace(L.dg_bf16_gemv_workspace_bytes(m, n, k), workspace, d.device, stream)
-    _check(fn, getattr(L, fn)(
-        _p(a), _ld(a), _p(b), _ld(b), _p(sfb), _p(c), 0 if c is None else _ld(c), _p(d), _ld(d), m, n, k, _p(ws), nbytes,
-        _p(status), _stream(stream)))
+    n, kb = b.shape
+    assert a.dtype is torch.bfloat16 and d.dtype is dtype and sfb.dtype is torch.int32
+    assert (b.dtype is torch.uint8 and kb * 2 == k) if fp4 else (b.dtype is torch.float8_e4m3fn and kb == k)
+    assert d.size(0) == m and d.size(1) == n and d.stride(1) == 1
+    assert (a.stride(1) == 1 and b.stride(1) == 1) or k == 0
+    assert sfb.is_contiguous() and sfb.numel() >= -(-k // (128 if fp4 else 512)) * ((n + 3) // 4 * 4)
+    assert c is None or (c.dtype is dtype and c.shape == d.shape and c.stride(1) == 1)
+    L = _lib or lib()
+    nbytes = 0
+    if workspace is not None:
+        nbytes = workspace.numel() * workspace.element_size()
+    elif m > 2:                          # the fewest rows need none
+        nbytes = L.dg_bf16_gemv_workspace_bytes(m, n, k)
+        workspace = _workspace(nbytes, d, stream)
+    st = getattr(L, fn)(
+        a.data_ptr(), _ld(a), b.data_ptr(), _ld(b), sfb.data_ptr(), None if c is None else c.data_ptr(),
+        0 if c is None else _ld(c), d.data_ptr(), _ld(d), m, n, k, None if workspace is None else workspace.data_ptr(),
+        nbytes, None if status is None else status.data_ptr(), _raw_stream(stream, d))
+    if st:
+        _fail(fn, st)
     return d
 
 
@@ -503,16 +524,21 @@ def dg_moe_route(logits, ids, weights, bias=None, scoring: str = "softmax", reno
     [T, topk] and weights float32 [T, topk] (both contiguous); bias float32 [E]
     shifts the choice only.  scoring "softmax" or "sigmoid"."""
     t, e = logits.shape
-    topk = ids.shape[1]
-    assert logits.dtype in (torch.float32, torch.bfloat16) and (logits.stride(1) == 1 or e == 1)
-    assert ids.dtype == torch.int32 and ids.shape == (t, topk) and ids.is_contiguous()
-    assert weights.dtype == torch.float32 and weights.shape == ids.shape and weights.is_contiguous()
-    assert bias is None or (bias.dtype == torch.float32 and bias.shape == (e,) and bias.is_contiguous())
-    assert scoring in ("softmax", "sigmoid")
-    _check("dg_moe_route", lib().dg_moe_route(
-        _p(logits), _ld(logits), DG_LOGITS_F32 if logits.dtype == torch.float32 else DG_LOGITS_BF16,
-        _p(bias), _p(ids), _p(weights), t, e, topk, DG_SCORE_SIGMOID if scoring == "sigmoid" else DG_SCORE_SOFTMAX,
-        int(renormalize), scale, _stream(stream)))
+    topk = ids.size(1)
+    f32 = logits.dtype is torch.float32
+    assert (f32 or logits.dtype is torch.bfloat16) and (logits.stride(1) == 1 or e == 1)
+    assert ids.dtype is torch.int32 and ids.size(0) == t and ids.is_contiguous()
+    assert weights.dtype is torch.float32 and weights.shape == ids.shape and weights.is_contiguous()
+    assert bias is None or (bias.dtype is torch.float32 and bias.shape == (e,) and bias.is_contiguous())
+    assert scoring == "softmax" or scoring == "sigmoid"
+    L = _lib or lib()
+    st = L.dg_moe_route(
+        logits.data_ptr(), _ld(logits), DG_LOGITS_F32 if f32 else DG_LOGITS_BF16,
+        None if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(), t, e, topk,
+        DG_SCORE_SIGMOID if scoring == "sigmoid" else DG_SCORE_SOFTMAX, renormalize, scale,
+        _raw_stream(stream, logits))
+    if st:
+        _fail("dg_moe_route", st)
     return ids, weights
 
 
@@ -522,27 +548,28 @@ def moe_layer_workspace_bytes(t: int, topk: int, h: int, i: int, experts: int) -
 
 def _moe_layer(fn: str, fp4: bool, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream):
     t, h = x.shape
-    topk = ids.shape[1]
-    e, i2 = w1.shape[0], w1.shape[1]
+    topk = ids.size(1)
+    e, i2, hp = w1.shape
     i = i2 // 2
-    code = torch.uint8 if fp4 else torch.float8_e4m3fn
-    per = 2 if fp4 else 1
-    assert x.dtype == torch.bfloat16 and x.stride(1) == 1
-    assert ids.dtype == torch.int32 and ids.shape == (t, topk) and ids.is_contiguous()
-    assert weights.dtype == torch.float32 and weights.shape == ids.shape and weights.is_contiguous()
-    assert w1.dtype == code and w1.is_contiguous() and w1.shape == (e, 2 * i, h // per)
-    assert w2.dtype == code and w2.is_contiguous() and w2.shape == (e, h, i // per)
-    sl = 128 if fp4 else 512
-    assert sf1.dtype == torch.int32 and sf1.is_contiguous() and sf1.numel() >= e * -(-h // sl) * 2 * i
-    assert sf2.dtype == torch.int32 and sf2.is_contiguous() and sf2.numel() >= e * -(-i // sl) * h
-    assert y.dtype == torch.bfloat16 and y.shape == (t, h) and y.stride(1) == 1
-    assert c is None or (c.dtype == torch.bfloat16 and c.shape == (t, h) and c.stride(1) == 1)
-    L = lib()
-    ws, nbytes = _workspace(L.dg_moe_layer_workspace_bytes(t, topk, h, i, e), workspace, y.device, stream)
-    _check(fn, getattr(L, fn)(
-        _p(x), _ld(x), _p(ids), _p(weights), _p(w1), _p(sf1), _p(w2), _p(sf2), _p(c),
-        0 if c is None else _ld(c), _p(y), _ld(y), t, h, i, e, topk, _p(ws), nbytes, _p(status),
-        _stream(stream)))
+    code, per, sl = (torch.uint8, 2, 128) if fp4 else (torch.float8_e4m3fn, 1, 512)
+    assert x.dtype is torch.bfloat16 and y.dtype is torch.bfloat16 and x.stride(1) == 1 and y.stride(1) == 1
+    assert ids.dtype is torch.int32 and ids.size(0) == t and ids.is_contiguous()
+    assert weights.dtype is torch.float32 and weights.shape == ids.shape and weights.is_contiguous()
+    assert w1.dtype is code and w1.is_contiguous() and i2 == 2 * i and hp * per == h
+    assert w2.dtype is code and w2.is_contiguous() and w2.shape == (e, h, i // per)
+    assert sf1.dtype is torch.int32 and sf1.is_contiguous() and sf1.numel() >= e * -(-h // sl) * 2 * i
+    assert sf2.dtype is torch.int32 and sf2.is_contiguous() and sf2.numel() >= e * -(-i // sl) * h
+    assert y.shape == x.shape and (c is None or (c.dtype is torch.bfloat16 and c.shape == x.shape and c.stride(1) == 1))
+    L = _lib or lib()
+    if workspace is None:
+        workspace = _workspace(max(16, L.dg_moe_layer_workspace_bytes(t, topk, h, i, e)), y, stream)
+    st = getattr(L, fn)(
+        x.data_ptr(), _ld(x), ids.data_ptr(), weights.data_ptr(), w1.data_ptr(), sf1.data_ptr(), w2.data_ptr(),
+        sf2.data_ptr(), None if c is None else c.data_ptr(), 0 if c is None else _ld(c), y.data_ptr(), _ld(y), t, h, i, e,
+        topk, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        None if status is None else status.data_ptr(), _raw_stream(stream, y))
+    if st:
+        _fail(fn, st)
     return y
 
 

@@ -1,7 +1,8 @@
 // Launches of the few-row kernel (few_rows.cuh): tile and split choice, tensor maps.
 #include "few_rows.cuh"
 
-#include <cstdlib>
+#include <atomic>
+#include <mutex>
 
 namespace dg {
 namespace {
@@ -15,7 +16,6 @@ int pow2_at_least(int v) {
     while (p < v) p *= 2;
     return p;
 }
-int env(const char *n, int d) { const char *e = std::getenv(n); return e ? std::atoi(e) : d; }
 
 // Rows of weights seen as [rows / 4][4]: weight row 4l + c lands in operand row 32c + l.
 bool encode_weights(CUtensorMap *map, bool fp4, const void *base, int64_t rows, int64_t ld_bytes, int k) {
@@ -46,7 +46,6 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     const int limit = plan.occ == 2 ? kSmemTwo : kSmemOne;
     int stages = (limit - fixed) / stage;
     if (stages > FewConfig::kMaxStages) stages = FewConfig::kMaxStages;
-    if (stages > env("DG_ST", 99)) stages = env("DG_ST", 99);
     if (stages < 2) return cudaErrorInvalidConfiguration;
     const int set = HALVES * 2 * a.cap, most = plan.occ == 2 ? 256 : 512;
     const int sf = 2 * HALVES * 8 + (MODE == kDown ? HALVES * ((a.tokens + 7) & ~7) : 0);
@@ -56,9 +55,16 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     if (a.tmem_cols > 512) return cudaErrorInvalidConfiguration;
     const int smem = FewConfig::smem_bytes(HALVES, a.cap, stages, MODE, plan.split, tables);
     auto kernel = dg_few_rows_kernel<FP4, HALVES, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    static std::atomic<uint64_t> ready{0};   // devices whose attributes are set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !(ready.load() >> (dev & 63) & 1)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
+        if (e == cudaSuccess) ready.fetch_or(uint64_t{1} << (dev & 63));
+    }
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -94,12 +100,56 @@ cudaError_t launch_mode(bool fp4, const CUtensorMap &map, FewArgs &a, const Plan
                             : launch_fmt<1, MODE>(fp4, map, a, plan, max_tiles, num_sms, stream);
 }
 
-// The largest cluster of at most kMaxSplit CTAs (and K-blocks) with all tiles resident at once.
-int resident_split(int tiles, int kblocks, int slots) {
-    int s = slots / tiles;
-    if (s > kMaxSplit) s = kMaxSplit;
-    if (s > kblocks) s = kblocks;
-    return s < 1 ? 1 : s;
+// Clusters of 1..kMaxSplit CTAs that are resident at once with one CTA on an SM (the SMs
+// of a cluster lie in one GPC, so the larger ones leave SMs over).
+const int *resident_clusters(int num_sms) {
+    static int count[64][kMaxSplit + 1];
+    static bool ready[64];
+    static std::mutex mutex;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+    dev &= 63;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (!ready[dev]) {
+        auto kernel = dg_few_rows_kernel<true, 1, kGemv>;
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
+        for (int c = 1; c <= kMaxSplit; ++c) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(static_cast<unsigned>(c * num_sms));
+            cfg.blockDim = dim3(FewConfig::threads(1, kGemv));
+            cfg.dynamicSmemBytes = kSmemOne;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+            count[dev][c] = n;
+        }
+        cudaGetLastError();   // a failed query means no clusters, not an error
+        ready[dev] = true;
+    }
+    return count[dev];
+}
+
+// Cluster size for `tiles` tiles of `kblocks` K-blocks: of those whose clusters are all
+// resident at once, the one with the least K-blocks on the busiest SM, the larger of equals
+// (more of the latency of a CTA's start and end overlaps).  A second wave of clusters costs
+// more than any split gains (24576 x 1536, 192 tiles: 7.4 us unsplit, 13 us in pairs).
+// `spare`: percent of that residence to leave free, for a kernel that starts while the
+// previous one's CTAs still hold SMs.
+int choose_split(int tiles, int kblocks, int occ, int num_sms, int spare) {
+    const int *clusters = resident_clusters(num_sms);
+    int best = 1;
+    int64_t best_cost = -1;
+    for (int s = 1; s <= kMaxSplit && s <= kblocks; ++s) {
+        if (s > 1 && (tiles * 100 > clusters[s] * occ * (100 - spare) || tiles * s > occ * num_sms)) continue;
+        const int64_t cost = static_cast<int64_t>(cdiv(tiles * s, num_sms)) * cdiv(kblocks, s);
+        if (best_cost < 0 || cost <= best_cost) { best = s; best_cost = cost; }
+    }
+    return best;
 }
 
 // A launch that may start before the stream's previous kernel ends.
@@ -118,8 +168,11 @@ struct Dependent {
     }
 };
 
-// Rows that a product splits by itself (each CTA its own K range).
-bool direct(int64_t m) { return m <= env("DG_FEW_DIRECT", 4); }
+// Rows that every CTA of a product splits by itself, without the split kernel's launch and
+// workspace: 1 x 2112 x 7168 takes 7.0 us so and 8.1 us with it; with 4 rows the CTAs' own
+// splitting is what bounds large products (1 x 131064 x 7168 FP4 85 us either way, 4 rows
+// 124 us so and 86 us with it).
+bool direct(int64_t m) { return m <= 2; }
 
 int capacity(int tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
 
@@ -176,10 +229,16 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream
     a.status = p.status;
     a.timeout_ns = p.timeout_ns;
     a.debug_flags = p.debug_flags;
-    Plan plan;
-    plan.halves = env("DG_H", p.m > 16 ? 2 : 1);
-    plan.occ = env("DG_OCC", plan.halves == 1 ? 2 : 1);
-    plan.split = env("DG_S", resident_split(cdiv(p.n, 128), a.kblocks, 2 * num_sms * 19 / 20));
+    // The split of K depends on n and k alone, so a row's result does not depend on m.
+    Plan plan = {1, 2, choose_split(cdiv(p.n, 128), a.kblocks, 2, num_sms, 0)};
+    if (plan.split == 1) {
+        // Many tiles.  Two CTAs of 128-row tiles on an SM, or one of 256-row tiles, which reads the
+        // activations' image half as often and keeps more loads in flight beside a wide one:
+        // 131064 x 7168 FP4, 8 rows 86 and 89 us, 16 rows 92 and 90, 32 rows 95 and 94; with 64 rows
+        // neither has room for its ring, and one CTA of 128-row tiles takes 111 us (122, 129).
+        if (p.m > 32) plan.occ = 1;
+        else if (p.m > 8) plan = {2, 1, 1};
+    }
     a.row_tiles = cdiv(p.n, 128 * plan.halves);
     if (direct(p.m)) return launch_mode<kGemv>(p.fp4, map, a, plan, a.row_tiles, num_sms, stream);
     a.image = p.workspace;
@@ -232,8 +291,8 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     const int up_tiles = static_cast<int>(bounds.count) * ki;
     Plan up;
     up.halves = 2;
-    up.occ = env("DG_UP_OCC", 1);
-    up.split = env("DG_UP_S", resident_split(up_tiles, kh, up.occ * num_sms * 19 / 20));
+    up.occ = 1;
+    up.split = choose_split(up_tiles, kh, up.occ, num_sms, 10);
     e = launch_fmt<2, kUp>(p.fp4, map1, a, up, up_tiles, num_sms, stream);
     if (e != cudaSuccess) return e;
     // down: K runs over the segments
@@ -250,11 +309,12 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.ldd = p.ldy;
     a.debug_flags = 0;
     Plan down;
-    down.halves = env("DG_DOWN_H", 1);
-    down.occ = env("DG_DOWN_OCC", p.t > 16 ? 1 : 2);
+    down.halves = 1;
+    down.occ = 2;
     a.row_tiles = cdiv(p.h, 128 * down.halves);
-    down.split = env("DG_DOWN_S", resident_split(a.row_tiles, ki * static_cast<int>(bounds.count),
-                                                 down.occ * num_sms * 19 / 20));
+    // (56 tiles in clusters of 5 fit the GPU exactly, and take 315 us in place of 264 with
+    // clusters of 4: h = 7168, i = 2048, 64 tokens, 64 experts)
+    down.split = choose_split(a.row_tiles, ki * static_cast<int>(bounds.count), down.occ, num_sms, 10);
     return launch_mode<kDown>(p.fp4, map2, a, down, a.row_tiles, num_sms, stream);
 }
 

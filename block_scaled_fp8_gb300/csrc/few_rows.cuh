@@ -511,52 +511,50 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     } else if (warp == 1 || (HALVES == 2 && warp == FIRST_B - 1)) {
         // ------------------------------------------------------------ MMA issuers
         const int h = warp == 1 ? 0 : 1;
-        int slot = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0, sf = sf_tmem + 2 * h * SF, sf_flip = 0;
+        int slot = 0, acc = 0, g = 0;
+        uint32_t phase = 0, acc_phase = 0;
         const uint64_t a_base = make_desc_kmajor_sw128(smem_u32(smem_a + h * 16384));
         const uint64_t b_base = make_desc_kmajor_sw128(smem_u32(smem_b));
         const uint64_t sfa_base = make_desc_sf_32x128b(smem_u32(smem_sfa + h * 512));
         const uint64_t sfb_base = make_desc_sf_32x128b(smem_u32(smem_sfb));
+        const uint32_t sf0 = sf_tmem + 2 * h * SF;
         for (int w = first_tile; w < num_tiles; w += tile_step) {
             const FewTile tile = get_tile(w);
-            int z = MODE == kDown ? k_begin / p.kblocks : tile.seg;
-            int kb = MODE == kDown ? k_begin - z * p.kblocks : k_begin;
-            uint32_t d_tmem = 0, idesc = 0, more = 0;
-            for (int i = k_begin; i < k_end; ++i) {
-                if (more == 0) {   // a tile, or kDown's next segment
-                    if (!mbar_wait_warp(&tempty_bar[acc], acc_phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto mma_done;
-                    d_tmem = tmem_base + (acc * HALVES + h) * ncols;
-                    // columns in use: the tokens', rounded up to the MMA's step of 16
-                    const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
-                    idesc = make_idesc_mxf8(128, (2 * tok + 15) / 16 * 16, 0, 0) | (FP4 ? 5u << 7 : 0u);   // A: E2M1 or E4M3
-                }
-                const bool end = i == k_end - 1 || (MODE == kDown && kb == p.kblocks - 1);
-                if (!mbar_wait_warp(&full_bar[slot], phase, ctl, DG_DEV_TIMEOUT)) goto mma_done;
+            // a run of K-blocks into one accumulator: the tile's, in kDown those of each segment
+            for (int i = k_begin; i < k_end;) {
+                const int z = MODE == kDown ? i / p.kblocks : tile.seg;
+                const int kb0 = MODE == kDown ? i - z * p.kblocks : i;
+                const int n = MODE == kDown ? min(k_end - i, p.kblocks - kb0) : k_end - k_begin;
+                i += n;
+                if (!mbar_wait_warp(&tempty_bar[acc], acc_phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto mma_done;
                 tc_fence_after_sync();
-                if (elect_one()) {
-                    const uint32_t sf_now = sf + sf_flip;
-                    tc_cp_32x128b_warpx4(sf_now, sfa_base + static_cast<uint64_t>(slot * HALVES * 32));
-                    tc_cp_32x128b_warpx4(sf_now + 4, sfb_base + static_cast<uint64_t>(slot * 32));
-                    const uint64_t a_desc = a_base + static_cast<uint64_t>(slot * HALVES * 1024);
-                    const uint64_t b_desc = b_base + static_cast<uint64_t>(slot * (b_bytes >> 4));
-                    // scale byte: the activations' and FP4 weights' k-th 32 K, FP8 weights' 128-K block
-                    const uint32_t id0 = idesc | (FP4 ? 0u : static_cast<uint32_t>(kb & 3) << 29);
+                const uint32_t d_tmem = tmem_base + (acc * HALVES + h) * ncols;
+                // columns in use: the tokens', rounded up to the MMA's step of 16
+                const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
+                const uint32_t idesc = make_idesc_mxf8(128, (2 * tok + 15) / 16 * 16, 0, 0) | (FP4 ? 5u << 7 : 0u);   // A: E2M1 or E4M3
+                for (int j = 0; j < n; ++j, ++g) {
+                    if (!mbar_wait_warp(&full_bar[slot], phase, ctl, DG_DEV_TIMEOUT)) goto mma_done;
+                    tc_fence_after_sync();
+                    if (elect_one()) {
+                        const uint32_t sf = sf0 + (g & 1) * SF;
+                        tc_cp_32x128b_warpx4(sf, sfa_base + static_cast<uint64_t>(slot * HALVES * 32));
+                        tc_cp_32x128b_warpx4(sf + 4, sfb_base + static_cast<uint64_t>(slot * 32));
+                        const uint64_t a_desc = a_base + static_cast<uint64_t>(slot * HALVES * 1024);
+                        const uint64_t b_desc = b_base + static_cast<uint64_t>(slot * (b_bytes >> 4));
 #pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k)
-                        tc_mma_mxf8(d_tmem, a_desc + 2 * k, b_desc + 2 * k, id0 | (k << 4) | (FP4 ? k << 29 : 0u), sf_now,
-                                    sf_now + 4, more | k);
-                    tc_commit(&empty_bar[slot]);
-                    if (end) tc_commit(&tfull_bar[acc]);
+                        for (uint32_t k = 0; k < 4; ++k) {
+                            // scale byte: the activations' and FP4 weights' k-th 32 K, FP8 weights' 128-K block
+                            const uint32_t id = idesc | (k << 4) | ((FP4 ? k : static_cast<uint32_t>((kb0 + j) & 3)) << 29);
+                            tc_mma_mxf8(d_tmem, a_desc + 2 * k, b_desc + 2 * k, id, sf, sf + 4, (j | k) != 0);
+                        }
+                        tc_commit(&empty_bar[slot]);
+                    }
+                    __syncwarp();
+                    if (++slot == S) { slot = 0; phase ^= 1; }
                 }
+                if (elect_one()) tc_commit(&tfull_bar[acc]);
                 __syncwarp();
-                sf_flip ^= SF;
-                more = 1;
-                if (end) {
-                    more = 0;
-                    if (++acc == p.accs) { acc = 0; acc_phase ^= 1; }
-                }
-                if (++kb == p.kblocks) { kb = 0; ++z; }
-                if (++slot == S) { slot = 0; phase ^= 1; }
+                if (++acc == p.accs) { acc = 0; acc_phase ^= 1; }
             }
         }
     mma_done:
