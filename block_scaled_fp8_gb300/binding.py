@@ -455,9 +455,21 @@ def _fail(fn: str, status: int):
     raise DGError(fn, status, lib().dg_status_string(status).decode())
 
 
+_workspaces: dict = {}
+
+
 def _workspace(nbytes: int, t, stream):
-    """A workspace on t's device, allocated on the current stream; a caller's other
-    stream waits for that and is made known to the allocator."""
+    """Device memory for a call whose caller gave none.  On the current stream: a buffer kept
+    for this stream and host thread (calls there run one after another).  In a graph capture,
+    or on a stream that the caller names: one of its own, which the allocator keeps from
+    other use as long as the capture or that stream needs it."""
+    if stream is None and not torch._C._cuda_isCurrentStreamCapturing():
+        i = t.get_device()
+        key = (i, torch._C._cuda_getCurrentRawStream(i), threading.get_ident())
+        ws = _workspaces.get(key)
+        if ws is None or ws.numel() < nbytes:
+            ws = _workspaces[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=t.device)
+        return ws
     ws = torch.empty(nbytes, dtype=torch.uint8, device=t.device)
     if stream is not None and ws.is_cuda:
         stream.wait_stream(torch.cuda.current_stream())
@@ -472,23 +484,29 @@ def gemv_workspace_bytes(m: int, n: int, k: int) -> int:
 def _gemv(fn: str, fp4: bool, dtype, a, b, sfb, d, c, workspace, status, stream):
     m, k = a.shape
     n, kb = b.shape
+    lda, sa = a.stride()
+    ldb, sb = b.stride()
+    ldd, sd = d.stride()
     assert a.dtype is torch.bfloat16 and d.dtype is dtype and sfb.dtype is torch.int32
     assert (b.dtype is torch.uint8 and kb * 2 == k) if fp4 else (b.dtype is torch.float8_e4m3fn and kb == k)
-    assert d.size(0) == m and d.size(1) == n and d.stride(1) == 1
-    assert (a.stride(1) == 1 and b.stride(1) == 1) or k == 0
+    assert d.shape == (m, n) and (sd == 1 or n <= 1) and ((sa == 1 and sb == 1) or k <= 1)
     assert sfb.is_contiguous() and sfb.numel() >= -(-k // (128 if fp4 else 512)) * ((n + 3) // 4 * 4)
     assert c is None or (c.dtype is dtype and c.shape == d.shape and c.stride(1) == 1)
+    if m == 1:   # (a single row's stride says nothing)
+        lda, ldd = max(lda, k), max(ldd, n)
+    if n == 1:
+        ldb = max(ldb, kb)
     L = _lib or lib()
-    nbytes = 0
+    ws, nbytes = None, 0
     if workspace is not None:
-        nbytes = workspace.numel() * workspace.element_size()
-    elif m > 2:                          # the fewest rows need none
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif m > 2:                          # (the fewest rows need none)
         nbytes = L.dg_bf16_gemv_workspace_bytes(m, n, k)
-        workspace = _workspace(nbytes, d, stream)
+        ws = (workspace := _workspace(nbytes, d, stream)).data_ptr()
     st = getattr(L, fn)(
-        a.data_ptr(), _ld(a), b.data_ptr(), _ld(b), sfb.data_ptr(), None if c is None else c.data_ptr(),
-        0 if c is None else _ld(c), d.data_ptr(), _ld(d), m, n, k, None if workspace is None else workspace.data_ptr(),
-        nbytes, None if status is None else status.data_ptr(), _raw_stream(stream, d))
+        a.data_ptr(), lda, b.data_ptr(), ldb, sfb.data_ptr(), None if c is None else c.data_ptr(),
+        0 if c is None else _ld(c), d.data_ptr(), ldd, m, n, k, ws, nbytes,
+        None if status is None else status.data_ptr(), _raw_stream(stream, d))
     if st:
         _fail(fn, st)
     return d

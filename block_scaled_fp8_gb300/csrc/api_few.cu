@@ -166,7 +166,7 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
     dg_status st = host_check_device(&sms);
     if (st != DG_OK) return st;
     RouteParams p = {logits, ld, bias, ids, weights, t, experts, topk, logits_fmt == DG_LOGITS_BF16,
-                     scoring == DG_SCORE_SIGMOID, renormalize != 0, scale};
+                     scoring == DG_SCORE_SIGMOID, renormalize != 0, scale, 0};
     return launch_moe_route(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 

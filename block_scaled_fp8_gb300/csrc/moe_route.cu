@@ -1,11 +1,15 @@
 // Top-k routing: scores of each token's logits, the topk largest keys, their weights.
 //
-// One warp per token; expert j sits in lane j % 32.  A key is an order-preserving
-// 32-bit integer (0: never chosen).  The topk-th largest of the 32 lanes' largest keys is a
-// lower bound of the topk-th largest key, so the keys below it are out; the few that
-// are left (about 1.5 topk) go to one lane each, which counts the candidates before its
-// own: that count is its place in the result.  More than 32 candidates (ties) are taken by
-// topk rounds of a warp maximum in place of that.
+// One warp per token.  Bound by the instructions that it issues (E logits are read
+// once, 4 E bytes a token), so no expert that cannot be chosen is worked on:
+//  - every lane takes the largest approximate key of its experts (the logit for softmax,
+//    else the score by approximate exponential and reciprocal, within kSlack);
+//  - the topk-th largest of the 32 lanes' values, less the slack, is a lower bound of the
+//    topk-th largest key; the experts not below it are candidates (about 1.2 topk);
+//  - each candidate goes to one lane, which computes its score and key in full and counts
+//    the candidates before it: its place in the result.
+// More than 32 candidates (ties) are taken by topk rounds of a warp maximum over all keys.
+// 32768 tokens x 256 experts, top 8 of sigmoid + bias, FP32 logits: see launch_moe_route.
 #include <cuda_bf16.h>
 
 #include "dg_internal.h"
@@ -15,6 +19,9 @@ namespace dg {
 namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
+// Twice the error of the approximate sigmoid: the exponential's argument is off by 2^-24 of
+// itself and exponential and reciprocal by 2^-22, which moves 1 / (1 + e) by at most 1e-6.
+constexpr float kSlack = 4e-6f;
 
 // Order-preserving map of a float to an unsigned integer; 0 for -infinity and NaN.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -23,144 +30,200 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-template <int PER>
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// Expert of a lane's i-th value: groups of VEC consecutive experts, one group a lane.
+template <int VEC>
+__device__ __forceinline__ int expert_of(int i, int lane) { return (i / VEC) * 32 * VEC + lane * VEC + i % VEC; }
+
+template <int PER, bool BF16, bool SIGMOID>
 __global__ void __launch_bounds__(256) dg_moe_route_kernel(const RouteParams p) {
+    constexpr int VEC = PER < 4 ? PER : 4;
     const int lane = threadIdx.x & 31;
-    const int token = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int w = threadIdx.x >> 5;
+    const int token = blockIdx.x * 8 + w;
     grid_launch_dependents();
     grid_dependency_wait();
     if (token >= p.t) return;
-    float score[PER];
-    uint32_t key[PER];
-    float top = -INFINITY;
+
+    float x[PER];      // logits; -infinity where none, and for NaN
+    const char *row = static_cast<const char *>(p.logits) + token * p.ld * (BF16 ? 2 : 4);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int j = i * 32 + lane;
-        float l = -INFINITY;
-        if (j < p.experts)
-            l = p.bf16 ? __uint_as_float(static_cast<uint32_t>(
-                             static_cast<const uint16_t *>(p.logits)[token * p.ld + j]) << 16)
-                       : static_cast<const float *>(p.logits)[token * p.ld + j];
-        score[i] = l;
-        if (l > top) top = l;
-    }
-    float denom = 1.0f;
-    // softmax weights that are normalised over the chosen need no other expert's score
-    const bool late = !p.sigmoid && p.renormalize && !p.bias;
-    if (p.sigmoid) {
+    for (int g = 0; g < PER / VEC; ++g) {
+        const int j0 = expert_of<VEC>(g * VEC, lane);
+        if (VEC == 4 && p.vec) {
+            if (j0 < p.experts) {
+                if constexpr (BF16) {
+                    const uint2 v = __ldcg(reinterpret_cast<const uint2 *>(row + 2 * j0));
+                    x[g * VEC] = __uint_as_float(v.x << 16);
+                    x[g * VEC + 1 % VEC] = __uint_as_float(v.x & 0xFFFF0000u);
+                    x[g * VEC + 2 % VEC] = __uint_as_float(v.y << 16);
+                    x[g * VEC + 3 % VEC] = __uint_as_float(v.y & 0xFFFF0000u);
+                } else {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(row + 4 * j0));
+                    x[g * VEC] = v.x;
+                    x[g * VEC + 1 % VEC] = v.y;
+                    x[g * VEC + 2 % VEC] = v.z;
+                    x[g * VEC + 3 % VEC] = v.w;
+                }
+            } else {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int j = i * 32 + lane;
-            const bool out = !(score[i] > -INFINITY);   // -infinity or NaN, and past the last expert
-            score[i] = __frcp_rn(1.0f + expf(-score[i]));   // 1 / x, correctly rounded
-            key[i] = out ? 0u : order_key(p.bias ? score[i] + p.bias[j] : score[i]);
+                for (int i = 0; i < VEC; ++i) x[g * VEC + i] = -INFINITY;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                x[g * VEC + i] = -INFINITY;
+                if (j0 + i < p.experts)
+                    x[g * VEC + i] =
+                        BF16 ? __uint_as_float(static_cast<uint32_t>(__ldcg(
+                                   reinterpret_cast<const uint16_t *>(row) + j0 + i)) << 16)
+                             : __ldcg(reinterpret_cast<const float *>(row) + j0 + i);
+            }
         }
-    } else {
+    }
+    float top = -INFINITY, denom = 1.0f;
+    // softmax weights that are normalised over the chosen need no other expert's score
+    const bool late = !SIGMOID && p.renormalize;
+    if constexpr (!SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) top = fmaxf(top, x[i]);
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, s));
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            key[i] = order_key(score[i]);
-            if (late) continue;
-            score[i] = key[i] ? expf(score[i] - top) : 0.0f;
-            sum += score[i];
-        }
-        if (!late) {
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
-        }
-        denom = sum;
-        if (p.bias) {
+        if (!late || p.bias) {
+            float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (key[i]) key[i] = order_key(score[i] / denom + p.bias[i * 32 + lane]);
+                if (x[i] > -INFINITY) sum += expf(x[i] - top);
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
+            denom = sum;
         }
     }
-    // the topk-th largest of the lanes' largest keys: a sort over the lanes, descending
-    uint32_t bound = 0;
+    // softmax with a bias takes the full score of every expert as its key
+    auto bias_of = [&](int j) { return p.bias ? __ldg(p.bias + j) : 0.0f; };
+    float approx[PER];
+    float best = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) bound = max(bound, key[i]);
+    for (int i = 0; i < PER; ++i) {
+        if constexpr (SIGMOID) {
+            approx[i] = __fdividef(1.0f, 1.0f + __expf(-x[i]));
+            if (x[i] < -80.0f) approx[i] = 0.0f;   // (where 1 + e leaves the fast division's range)
+        } else {
+            approx[i] = p.bias ? expf(x[i] - top) / denom : x[i];
+        }
+        const int j = expert_of<VEC>(i, lane);
+        if (p.bias && j < p.experts) approx[i] += __ldg(p.bias + j);
+        if (!(x[i] > -INFINITY)) approx[i] = -INFINITY;
+        best = fmaxf(best, approx[i]);
+    }
+    // the topk-th largest of the lanes' largest: a sort over the lanes, descending
+    float bound = best;
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
         for (int s = size >> 1; s > 0; s >>= 1) {
-            const uint32_t other = __shfl_xor_sync(kFull, bound, s);
+            const float other = __shfl_xor_sync(kFull, bound, s);
             const bool larger = ((lane & size) == 0) == ((lane & s) == 0);   // (lane & 32 is 0)
-            bound = larger ? max(bound, other) : min(bound, other);
+            bound = larger ? fmaxf(bound, other) : fminf(bound, other);
         }
-    bound = max(__shfl_sync(kFull, bound, p.topk - 1), 1u);
+    bound = __shfl_sync(kFull, bound, p.topk - 1);
+    if ((SIGMOID || p.bias) && fabsf(bound) < INFINITY)
+        bound -= kSlack + fabsf(bound) * 2.4e-7f;   // (and the key's own rounding)
 
+    __shared__ float s_x[8][32];
     __shared__ uint32_t s_key[8][32];
-    __shared__ float s_score[8][32];
     __shared__ int s_id[8][32];
-    const int w = threadIdx.x >> 5;
-    int count = 0;
+    int mine = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const bool in = key[i] >= bound;
-        const uint32_t m = __ballot_sync(kFull, in);
-        const int at = count + __popc(m & ((1u << lane) - 1u));
-        if (in && at < 32) {
-            s_key[w][at] = key[i];
-            s_score[w][at] = score[i];
-            s_id[w][at] = i * 32 + lane;
-        }
-        count += __popc(m);
+    for (int i = 0; i < PER; ++i) mine += approx[i] >= bound && approx[i] > -INFINITY;
+    int at = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const int v = __shfl_up_sync(kFull, at, s);
+        if (lane >= s) at += v;
     }
-    __syncwarp();
-    float chosen = 0.0f, mine = 0.0f;
-    int my_id = -1, place = lane;
+    const int count = __shfl_sync(kFull, at, 31);
+    float score = 0.0f, chosen = 0.0f;
+    int id = -1, place = lane;
     if (count <= 32) {
-        // candidates are in the order of their index
-        const uint32_t k = lane < count ? s_key[w][lane] : 0u;
+        at -= mine;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (approx[i] >= bound && approx[i] > -INFINITY) {
+                s_x[w][at] = x[i];
+                s_id[w][at] = expert_of<VEC>(i, lane);
+                ++at;
+            }
+        __syncwarp();
+        uint32_t key = 0;
+        if (lane < count) {
+            id = s_id[w][lane];
+            const float l = s_x[w][lane];
+            score = SIGMOID ? sigmoid(l) : expf(l - top);
+            if (!SIGMOID && !late) score /= denom;
+            if constexpr (SIGMOID) key = order_key(score + bias_of(id));
+            else key = order_key(p.bias ? expf(l - top) / denom + bias_of(id) : l);
+            s_key[w][lane] = key;
+        }
+        __syncwarp();
         int before = 0;
         for (int j = 0; j < count; ++j) {
             const uint32_t o = s_key[w][j];
-            before += o > k || (o == k && j < lane);
+            before += o > key || (o == key && s_id[w][j] < id);
         }
-        const bool in = lane < count && before < p.topk;
-        place = in ? before : 32;
-        if (in) {
-            my_id = s_id[w][lane];
-            mine = late ? expf(s_score[w][lane] - top) : s_score[w][lane];
+        // (a key that is NaN is 0; candidates beyond the topk have no place)
+        const bool in = lane < count && before < p.topk && key != 0u;
+        const uint32_t placed = __ballot_sync(kFull, in);
+        place = before;
+        if (!in) {   // the slots that no expert is left for go to the idle lanes
+            id = -1;
+            score = 0.0f;
+            place = __popc(placed) + __popc(~placed & ((1u << lane) - 1u));
         }
-        chosen = mine;
+        chosen = score;
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) chosen += __shfl_xor_sync(kFull, chosen, s);
-        // slots that no expert is left for
-        if (lane >= count && lane < p.topk) place = lane;
     } else {
-        for (int r = 0; r < p.topk; ++r) {
-            uint32_t best = 0;
+        uint32_t key[PER];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) best = max(best, key[i]);
-            const uint32_t m = __reduce_max_sync(kFull, best);
+        for (int i = 0; i < PER; ++i) {
+            const int j = expert_of<VEC>(i, lane);
+            key[i] = 0u;
+            if (!(x[i] > -INFINITY)) continue;
+            if constexpr (SIGMOID) key[i] = order_key(sigmoid(x[i]) + bias_of(j));
+            else key[i] = order_key(p.bias ? expf(x[i] - top) / denom + bias_of(j) : x[i]);
+        }
+        for (int r = 0; r < p.topk; ++r) {
+            uint32_t high = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) high = max(high, key[i]);
+            const uint32_t m = __reduce_max_sync(kFull, high);
             if (m == 0) break;
-            int at = 1 << 30;
-            float s = 0.0f;
+            int first = 1 << 30;
+            float l = 0.0f;
 #pragma unroll
             for (int i = PER - 1; i >= 0; --i)
-                if (key[i] == m) { at = i * 32 + lane; s = score[i]; }
-            const int win = __reduce_min_sync(kFull, at);
+                if (key[i] == m) { first = expert_of<VEC>(i, lane); l = x[i]; }
+            const int win = __reduce_min_sync(kFull, first);
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (i * 32 + lane == win) key[i] = 0u;
-            s = __shfl_sync(kFull, s, win & 31);
-            if (late) s = expf(s - top);
+                if (expert_of<VEC>(i, lane) == win) key[i] = 0u;
+            l = __shfl_sync(kFull, l, (win / VEC) & 31);
+            float s = SIGMOID ? sigmoid(l) : expf(l - top);
+            if (!SIGMOID && !late) s /= denom;
             chosen += s;
-            if (lane == r) { my_id = win; mine = s; }
+            if (lane == r) { id = win; score = s; }
         }
     }
     if (place < p.topk) {
-        if (p.renormalize) mine = mine / fmaxf(chosen, 1.17549435e-38f);
-        else if (!p.sigmoid) mine = mine / denom;
-        p.ids[static_cast<int64_t>(token) * p.topk + place] = my_id;
-        p.weights[static_cast<int64_t>(token) * p.topk + place] = my_id < 0 ? 0.0f : mine * p.scale;
+        if (p.renormalize) score /= fmaxf(chosen, 1.17549435e-38f);
+        p.ids[static_cast<int64_t>(token) * p.topk + place] = id;
+        p.weights[static_cast<int64_t>(token) * p.topk + place] = id < 0 ? 0.0f : score * p.scale;
     }
 }
 
-template <int PER>
+template <int PER, bool BF16, bool SIGMOID>
 cudaError_t launch(const RouteParams &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -171,18 +234,28 @@ cudaError_t launch(const RouteParams &p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dg_moe_route_kernel<PER>, p);
+    return cudaLaunchKernelEx(&cfg, dg_moe_route_kernel<PER, BF16, SIGMOID>, p);
+}
+
+template <int PER>
+cudaError_t launch_per(const RouteParams &p, cudaStream_t stream) {
+    if (p.bf16) return p.sigmoid ? launch<PER, true, true>(p, stream) : launch<PER, true, false>(p, stream);
+    return p.sigmoid ? launch<PER, false, true>(p, stream) : launch<PER, false, false>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_moe_route(const RouteParams &p, cudaStream_t stream) {
-    if (p.experts <= 32) return launch<1>(p, stream);
-    if (p.experts <= 64) return launch<2>(p, stream);
-    if (p.experts <= 128) return launch<4>(p, stream);
-    if (p.experts <= 256) return launch<8>(p, stream);
-    if (p.experts <= 512) return launch<16>(p, stream);
-    return launch<32>(p, stream);
+cudaError_t launch_moe_route(const RouteParams &params, cudaStream_t stream) {
+    RouteParams p = params;
+    // rows of whole aligned groups of 4 experts are read a group at a time
+    p.vec = p.experts % 4 == 0 && p.ld % 4 == 0 &&
+            reinterpret_cast<uintptr_t>(p.logits) % (p.bf16 ? 8 : 16) == 0;
+    if (p.experts <= 32) return launch_per<1>(p, stream);
+    if (p.experts <= 64) return launch_per<2>(p, stream);
+    if (p.experts <= 128) return launch_per<4>(p, stream);
+    if (p.experts <= 256) return launch_per<8>(p, stream);
+    if (p.experts <= 512) return launch_per<16>(p, stream);
+    return launch_per<32>(p, stream);
 }
 
 }  // namespace dg

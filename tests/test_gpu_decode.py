@@ -233,6 +233,37 @@ def test_route_masks_ties_and_special_values(scoring):
     assert ids[7].tolist() == [0, 1, 2, 3] and torch.isfinite(w[7]).all()
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e", [40, 64, 127, 256, 500])
+def test_route_many_candidates(scoring, dtype, e):
+    """Logits of a few values only: far more ties than lanes, on either side of the last slot;
+    saturated scores; biases of +-infinity and NaN; unaligned rows."""
+    topk = min(e, 9)
+    logits = torch.randint(-2, 3, (50, e), generator=_gen(e)).to(dtype)
+    logits[1] = 100.0                          # every sigmoid 1
+    logits[2] = -200.0                         # every sigmoid 0
+    logits[3, :5] = float("nan")
+    bias = torch.zeros(e)
+    bias[7], bias[8], bias[9] = float("inf"), float("-inf"), float("nan")
+    for b in (None, bias):
+        for shift in (0, 1):
+            wide = torch.zeros(50, e + 8, dtype=dtype, device="cuda")
+            wide[:, shift:shift + e] = logits.cuda()
+            ids, w = _route(wide[:, shift:shift + e], topk, bias=None if b is None else b.cuda(), scoring=scoring)
+            # 64-bit keys are as distinct as 32-bit ones here: the logits are small integers
+            x = torch.where(torch.isnan(logits.double()), float("-inf"), logits.double())
+            s = torch.softmax(x, -1) if scoring == "softmax" else torch.sigmoid(logits.float()).double()
+            key = s if b is None else s + torch.nan_to_num(b.double(), nan=float("-inf"), posinf=float("inf"),
+                                                           neginf=float("-inf"))
+            key = torch.where(x > float("-inf"), key, float("-inf"))
+            want = torch.sort(key, dim=-1, descending=True, stable=True)[1][:, :topk].int()
+            assert torch.equal(ids, want)
+            picked = s.gather(1, want.long())
+            picked = picked / picked.sum(1, keepdim=True).clamp_min(2.0 ** -126)
+            assert ((w.double() - picked).abs() <= 1e-6).all()
+
+
 # ------------------------------------------------------------------ the MoE layer
 
 LAYER = {"fp4": binding.dg_moe_fp4_layer, "fp8": binding.dg_moe_fp8_layer}
