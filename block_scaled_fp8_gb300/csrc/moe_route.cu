@@ -19,7 +19,7 @@ namespace dg {
 namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
-// Twice the error of the approximate sigmoid: the exponential's argument is off by 2^-24 of
+// Above twice the error of the approximate sigmoid: the exponential's argument is off by 2^-24 of
 // itself and exponential and reciprocal by 2^-22, which moves 1 / (1 + e) by at most 1e-6.
 constexpr float kSlack = 4e-6f;
 
@@ -32,56 +32,62 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// Expert of a lane's i-th value: groups of VEC consecutive experts, one group a lane.
-template <int VEC>
-__device__ __forceinline__ int expert_of(int i, int lane) { return (i / VEC) * 32 * VEC + lane * VEC + i % VEC; }
+__device__ __forceinline__ float sigmoid_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-x)));
+    return r;
+}
 
+// Lane l holds experts PER l .. PER l + PER - 1.
 template <int PER, bool BF16, bool SIGMOID>
 __global__ void __launch_bounds__(256) dg_moe_route_kernel(const RouteParams p) {
     constexpr int VEC = PER < 4 ? PER : 4;
     const int lane = threadIdx.x & 31;
     const int w = threadIdx.x >> 5;
     const int token = blockIdx.x * 8 + w;
+    __shared__ float s_x[8][32 * PER];
+    __shared__ uint32_t s_key[8][32];
+    __shared__ int s_id[8][32];
     grid_launch_dependents();
     grid_dependency_wait();
     if (token >= p.t) return;
 
-    float x[PER];      // logits; -infinity where none, and for NaN
+    float x[PER];      // logits; -infinity where none
     const char *row = static_cast<const char *>(p.logits) + token * p.ld * (BF16 ? 2 : 4);
 #pragma unroll
-    for (int g = 0; g < PER / VEC; ++g) {
-        const int j0 = expert_of<VEC>(g * VEC, lane);
+    for (int i0 = 0; i0 < PER; i0 += VEC) {
+        const int j0 = lane * PER + i0;
         if (VEC == 4 && p.vec) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) x[i0 + i] = -INFINITY;
             if (j0 < p.experts) {
                 if constexpr (BF16) {
                     const uint2 v = __ldcg(reinterpret_cast<const uint2 *>(row + 2 * j0));
-                    x[g * VEC] = __uint_as_float(v.x << 16);
-                    x[g * VEC + 1 % VEC] = __uint_as_float(v.x & 0xFFFF0000u);
-                    x[g * VEC + 2 % VEC] = __uint_as_float(v.y << 16);
-                    x[g * VEC + 3 % VEC] = __uint_as_float(v.y & 0xFFFF0000u);
+                    const uint32_t u[2] = {v.x, v.y};
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        x[i0 + i] = __uint_as_float(i & 1 ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
                 } else {
                     const float4 v = __ldcg(reinterpret_cast<const float4 *>(row + 4 * j0));
-                    x[g * VEC] = v.x;
-                    x[g * VEC + 1 % VEC] = v.y;
-                    x[g * VEC + 2 % VEC] = v.z;
-                    x[g * VEC + 3 % VEC] = v.w;
-                }
-            } else {
+                    const float u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) x[g * VEC + i] = -INFINITY;
+                    for (int i = 0; i < VEC; ++i) x[i0 + i] = u[i];
+                }
             }
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                x[g * VEC + i] = -INFINITY;
+                x[i0 + i] = -INFINITY;
                 if (j0 + i < p.experts)
-                    x[g * VEC + i] =
+                    x[i0 + i] =
                         BF16 ? __uint_as_float(static_cast<uint32_t>(__ldcg(
                                    reinterpret_cast<const uint16_t *>(row) + j0 + i)) << 16)
                              : __ldcg(reinterpret_cast<const float *>(row) + j0 + i);
             }
         }
     }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s_x[w][lane * PER + i] = x[i];
     float top = -INFINITY, denom = 1.0f;
     // softmax weights that are normalised over the chosen need no other expert's score
     const bool late = !SIGMOID && p.renormalize;
@@ -100,44 +106,38 @@ __global__ void __launch_bounds__(256) dg_moe_route_kernel(const RouteParams p) 
             denom = sum;
         }
     }
-    // softmax with a bias takes the full score of every expert as its key
     auto bias_of = [&](int j) { return p.bias ? __ldg(p.bias + j) : 0.0f; };
+    // approximate keys; -infinity for what is never chosen, NaN included
     float approx[PER];
     float best = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        if constexpr (SIGMOID) {
-            approx[i] = __fdividef(1.0f, 1.0f + __expf(-x[i]));
-            if (x[i] < -80.0f) approx[i] = 0.0f;   // (where 1 + e leaves the fast division's range)
-        } else {
-            approx[i] = p.bias ? expf(x[i] - top) / denom : x[i];
-        }
-        const int j = expert_of<VEC>(i, lane);
+        const int j = lane * PER + i;
+        approx[i] = SIGMOID ? sigmoid_approx(x[i]) : p.bias ? expf(x[i] - top) / denom : x[i];
         if (p.bias && j < p.experts) approx[i] += __ldg(p.bias + j);
         if (!(x[i] > -INFINITY)) approx[i] = -INFINITY;
         best = fmaxf(best, approx[i]);
     }
-    // the topk-th largest of the lanes' largest: a sort over the lanes, descending
+    // the topk-th largest of the lanes' largest: a bitonic sort over the lanes, descending,
+    // whose every step keeps the larger value in the lane with the step's bit clear
     float bound = best;
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
         for (int s = size >> 1; s > 0; s >>= 1) {
-            const float other = __shfl_xor_sync(kFull, bound, s);
-            const bool larger = ((lane & size) == 0) == ((lane & s) == 0);   // (lane & 32 is 0)
-            bound = larger ? fmaxf(bound, other) : fminf(bound, other);
+            const float other = __shfl_xor_sync(kFull, bound, s == size >> 1 ? size - 1 : s);
+            bound = lane & s ? fminf(bound, other) : fmaxf(bound, other);
         }
     bound = __shfl_sync(kFull, bound, p.topk - 1);
     if ((SIGMOID || p.bias) && fabsf(bound) < INFINITY)
         bound -= kSlack + fabsf(bound) * 2.4e-7f;   // (and the key's own rounding)
+    bound = fmaxf(bound, -3.402823466e38f);
 
-    __shared__ float s_x[8][32];
-    __shared__ uint32_t s_key[8][32];
-    __shared__ int s_id[8][32];
-    int mine = 0;
+    uint32_t hits = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) mine += approx[i] >= bound && approx[i] > -INFINITY;
-    int at = mine;
+    for (int i = 0; i < PER; ++i)
+        if (approx[i] >= bound) hits |= 1u << i;
+    int at = __popc(hits);
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
         const int v = __shfl_up_sync(kFull, at, s);
@@ -147,33 +147,31 @@ __global__ void __launch_bounds__(256) dg_moe_route_kernel(const RouteParams p) 
     float score = 0.0f, chosen = 0.0f;
     int id = -1, place = lane;
     if (count <= 32) {
-        at -= mine;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (approx[i] >= bound && approx[i] > -INFINITY) {
-                s_x[w][at] = x[i];
-                s_id[w][at] = expert_of<VEC>(i, lane);
-                ++at;
-            }
+        // the candidates, in the order of their index
+        for (at -= __popc(hits); hits; hits &= hits - 1u) s_id[w][at++] = lane * PER + __ffs(hits) - 1;
         __syncwarp();
         uint32_t key = 0;
         if (lane < count) {
             id = s_id[w][lane];
-            const float l = s_x[w][lane];
+            const float l = s_x[w][id];
             score = SIGMOID ? sigmoid(l) : expf(l - top);
             if (!SIGMOID && !late) score /= denom;
             if constexpr (SIGMOID) key = order_key(score + bias_of(id));
             else key = order_key(p.bias ? expf(l - top) / denom + bias_of(id) : l);
-            s_key[w][lane] = key;
         }
+        s_key[w][lane] = key;
         __syncwarp();
         int before = 0;
-        for (int j = 0; j < count; ++j) {
-            const uint32_t o = s_key[w][j];
-            before += o > key || (o == key && s_id[w][j] < id);
+        for (int j = 0; j < count; j += 4) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(&s_key[w][j]);
+            // (of equal keys the earlier candidate comes first)
+            before += o.x > key || (o.x == key && j < lane);
+            before += o.y > key || (o.y == key && j + 1 < lane);
+            before += o.z > key || (o.z == key && j + 2 < lane);
+            before += o.w > key || (o.w == key && j + 3 < lane);
         }
         // (a key that is NaN is 0; candidates beyond the topk have no place)
-        const bool in = lane < count && before < p.topk && key != 0u;
+        const bool in = key != 0u && before < p.topk;
         const uint32_t placed = __ballot_sync(kFull, in);
         place = before;
         if (!in) {   // the slots that no expert is left for go to the idle lanes
@@ -188,12 +186,12 @@ __global__ void __launch_bounds__(256) dg_moe_route_kernel(const RouteParams p) 
         uint32_t key[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int j = expert_of<VEC>(i, lane);
             key[i] = 0u;
             if (!(x[i] > -INFINITY)) continue;
-            if constexpr (SIGMOID) key[i] = order_key(sigmoid(x[i]) + bias_of(j));
-            else key[i] = order_key(p.bias ? expf(x[i] - top) / denom + bias_of(j) : x[i]);
+            if constexpr (SIGMOID) key[i] = order_key(sigmoid(x[i]) + bias_of(lane * PER + i));
+            else key[i] = order_key(p.bias ? expf(x[i] - top) / denom + bias_of(lane * PER + i) : x[i]);
         }
+        __syncwarp();
         for (int r = 0; r < p.topk; ++r) {
             uint32_t high = 0;
 #pragma unroll
@@ -201,15 +199,14 @@ __global__ void __launch_bounds__(256) dg_moe_route_kernel(const RouteParams p) 
             const uint32_t m = __reduce_max_sync(kFull, high);
             if (m == 0) break;
             int first = 1 << 30;
-            float l = 0.0f;
 #pragma unroll
             for (int i = PER - 1; i >= 0; --i)
-                if (key[i] == m) { first = expert_of<VEC>(i, lane); l = x[i]; }
+                if (key[i] == m) first = lane * PER + i;
             const int win = __reduce_min_sync(kFull, first);
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (expert_of<VEC>(i, lane) == win) key[i] = 0u;
-            l = __shfl_sync(kFull, l, (win / VEC) & 31);
+                if (lane * PER + i == win) key[i] = 0u;
+            const float l = s_x[w][win];
             float s = SIGMOID ? sigmoid(l) : expf(l - top);
             if (!SIGMOID && !late) s /= denom;
             chosen += s;
@@ -218,8 +215,9 @@ __global__ void __launch_bounds__(256) dg_moe_route_kernel(const RouteParams p) 
     }
     if (place < p.topk) {
         if (p.renormalize) score /= fmaxf(chosen, 1.17549435e-38f);
-        p.ids[static_cast<int64_t>(token) * p.topk + place] = id;
-        p.weights[static_cast<int64_t>(token) * p.topk + place] = id < 0 ? 0.0f : score * p.scale;
+        const int64_t out = static_cast<int64_t>(token) * p.topk + place;
+        p.ids[out] = id;
+        p.weights[out] = id < 0 ? 0.0f : score * p.scale;
     }
 }
 
