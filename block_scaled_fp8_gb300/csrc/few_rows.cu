@@ -10,6 +10,10 @@ namespace {
 constexpr int kMaxSplit = 8;        // portable cluster size
 constexpr int kSmemOne = 232448 - 1024, kSmemTwo = 114000;   // bytes for one or two CTAs on an SM
 
+// Bytes of weights an SM brings to L2 before it waits for the preceding kernel (1 x 2112 x 7168
+// in a row of calls 6.4 us without, 6.0 us with).
+constexpr int kAhead = 160 * 1024;
+
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 int pow2_at_least(int v) {
     int p = 32;
@@ -41,7 +45,11 @@ template <bool FP4, int HALVES, int MODE>
 cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles,
                    int num_sms, cudaStream_t stream) {
     const int tables = MODE < kUp ? 0 : segment_table_bytes(a.tokens * a.topk, a.experts);
-    const int fixed = FewConfig::smem_bytes(HALVES, a.cap, 0, MODE, plan.split, tables);
+    a.out_bytes = FewConfig::out_bytes(HALVES, MODE, MODE == kUp ? a.cap : a.tokens, plan.split);
+    // (split results of more than 8 KB go to the ring: one more wait, but no stage less)
+    if (plan.split > 1 && a.out_bytes > 8192) a.out_bytes = 0;
+    a.ahead = kAhead / (HALVES * (FP4 ? 8192 : 16384)) / plan.occ;
+    const int fixed = FewConfig::smem_bytes(HALVES, a.cap, 0, a.out_bytes, tables);
     const int stage = FewConfig::stage_bytes(HALVES, a.cap);
     const int limit = plan.occ == 2 ? kSmemTwo : kSmemOne;
     int stages = (limit - fixed) / stage;
@@ -53,7 +61,7 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     a.accs = (plan.split == 1 || MODE == kDown) && 2 * set + sf <= most ? 2 : 1;
     a.tmem_cols = pow2_at_least(a.accs * set + sf);
     if (a.tmem_cols > 512) return cudaErrorInvalidConfiguration;
-    const int smem = FewConfig::smem_bytes(HALVES, a.cap, stages, MODE, plan.split, tables);
+    const int smem = FewConfig::smem_bytes(HALVES, a.cap, stages, a.out_bytes, tables);
     auto kernel = dg_few_rows_kernel<FP4, HALVES, MODE>;
     static std::atomic<uint64_t> ready{0};   // devices whose attributes are set
     int dev = 0;
@@ -138,14 +146,17 @@ const int *resident_clusters(int num_sms) {
 // resident at once, the one with the least K-blocks on the busiest SM, the larger of equals
 // (more of the latency of a CTA's start and end overlaps).  A second wave of clusters costs
 // more than any split gains (24576 x 1536, 192 tiles: 7.4 us unsplit, 13 us in pairs).
-// `spare`: percent of that residence to leave free, for a kernel that starts while the
-// previous one's CTAs still hold SMs.
-int choose_split(int tiles, int kblocks, int occ, int num_sms, int spare) {
+// `tight`: whether clusters may take all of that residence.  A kernel starts while CTAs of
+// the ones around it still hold SMs, and clusters that find no room then make a second wave:
+// 56 tiles in clusters of 5 fit the GPU exactly, and 7168 x 2048 (3 K-blocks a CTA) takes 9.6 us
+// so and 5.6 us in clusters of 4, but 7168 x 16384 (26) 15.5 and 17.1 us.
+int choose_split(int tiles, int kblocks, int occ, int num_sms, bool tight) {
     const int *clusters = resident_clusters(num_sms);
     int best = 1;
     int64_t best_cost = -1;
     for (int s = 1; s <= kMaxSplit && s <= kblocks; ++s) {
-        if (s > 1 && (tiles * 100 > clusters[s] * occ * (100 - spare) || tiles * s > occ * num_sms)) continue;
+        const bool full = tight && kblocks >= 8 * s;
+        if (s > 1 && (tiles * 10 > clusters[s] * occ * (full ? 10 : 9) || tiles * s > occ * num_sms)) continue;
         const int64_t cost = static_cast<int64_t>(cdiv(tiles * s, num_sms)) * cdiv(kblocks, s);
         if (best_cost < 0 || cost <= best_cost) { best = s; best_cost = cost; }
     }
@@ -230,7 +241,7 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream
     a.timeout_ns = p.timeout_ns;
     a.debug_flags = p.debug_flags;
     // The split of K depends on n and k alone, so a row's result does not depend on m.
-    Plan plan = {1, 2, choose_split(cdiv(p.n, 128), a.kblocks, 2, num_sms, 0)};
+    Plan plan = {1, 2, choose_split(cdiv(p.n, 128), a.kblocks, 2, num_sms, true)};
     if (plan.split == 1) {
         // Many tiles.  Two CTAs of 128-row tiles on an SM, or one of 256-row tiles, which reads the
         // activations' image half as often and keeps more loads in flight beside a wide one:
@@ -277,6 +288,11 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.status = p.status;
     a.timeout_ns = p.timeout_ns;
     a.debug_flags = p.debug_flags;
+    Plan down;
+    down.halves = 1;
+    down.occ = 2;
+    const int down_tiles = cdiv(p.h, 128 * down.halves);
+    down.split = choose_split(down_tiles, ki * static_cast<int>(bounds.count), down.occ, num_sms, false);
     // up: a tile is 128 columns of h of one segment
     a.image = x_image;
     a.image_sf = x_sf;
@@ -292,10 +308,11 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     Plan up;
     up.halves = 2;
     up.occ = 1;
-    up.split = choose_split(up_tiles, kh, up.occ, num_sms, 10);
+    up.split = choose_split(up_tiles, kh, up.occ, num_sms, false);
     e = launch_fmt<2, kUp>(p.fp4, map1, a, up, up_tiles, num_sms, stream);
     if (e != cudaSuccess) return e;
     // down: K runs over the segments
+    a.row_tiles = down_tiles;
     a.image = h_image;
     a.image_sf = h_sf;
     a.sf = p.sf2;
@@ -308,13 +325,6 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.d = p.y;
     a.ldd = p.ldy;
     a.debug_flags = 0;
-    Plan down;
-    down.halves = 1;
-    down.occ = 2;
-    a.row_tiles = cdiv(p.h, 128 * down.halves);
-    // (56 tiles in clusters of 5 fit the GPU exactly, and take 315 us in place of 264 with
-    // clusters of 4: h = 7168, i = 2048, 64 tokens, 64 experts)
-    down.split = choose_split(a.row_tiles, ki * static_cast<int>(bounds.count), down.occ, num_sms, 10);
     return launch_mode<kDown>(p.fp4, map2, a, down, a.row_tiles, num_sms, stream);
 }
 

@@ -26,9 +26,9 @@
 //   warps 2..5  epilogue, one TMEM lane quadrant each.
 //   the rest    the narrow operand.
 // Many tiles: the CTAs are persistent and take tiles in turn, the ring of K-blocks running
-// on across them.  Few tiles: one tile per cluster, K split over its CTAs, which add
-// their FP32 partial results in rank order through distributed shared memory: no
-// workspace, no atomics, a fixed order.
+// on across them.  Few tiles: one tile per cluster, K split over its CTAs.  Each CTA writes its
+// FP32 partial results into the shared memory of the CTA that puts them out, which adds them
+// in rank order: no workspace, no atomics, a fixed order, and one cluster barrier.
 //
 // Where the pieces come from: kGemv, for the fewest rows, splits the activations itself,
 // four warps taking K-blocks in turn.  The other modes read an image of the narrow
@@ -69,6 +69,8 @@ struct FewArgs {
     int kblocks;            // K-blocks of one expert
     int cap;                // tokens of a segment at most (8, 16, 32 or 64); N = 2 cap
     int stages;
+    int out_bytes;          // room of its own for the results, or 0: split results go to the ring
+    int ahead;              // kGemv: K-blocks per CTA to bring to L2 before the wait
     int accs;               // accumulator sets (1 or 2)
     int tmem_cols;
     int row_tiles;          // tiles over the weight rows (kUp: of h's columns)
@@ -96,12 +98,15 @@ struct FewConfig {
     static constexpr int kBarBytes = 512;
     static constexpr int kMaxStages = 24;
     static int stage_bytes(int halves, int cap) { return halves * 16384 + 2 * cap * 128 + halves * 512 + 512; }
-    // two buffers of 8 tokens' FP32 results (split tiles leave theirs in the ring)
-    static int out_bytes(int halves, int mode, int split) {
-        return split > 1 ? 0 : 2 * 8 * (mode == kUp ? 128 : halves * 128) * 4;
+    // Two buffers of 8 tokens' FP32 results; of a split tile, what this CTA puts out (rows of
+    // 32 items of 4 results, shared out to the cluster's CTAs) from each of its CTAs.
+    static int out_bytes(int halves, int mode, int cols, int split) {
+        if (split == 1) return 2 * 8 * (mode == kUp ? 128 : halves * 128) * 4;
+        const int rows = cols * (mode == kUp ? 1 : halves);
+        return (rows + split - 1) / split * split * 32 * 4 * (mode == kUp ? 8 : 4);
     }
-    static int smem_bytes(int halves, int cap, int stages, int mode, int split, int tables) {
-        return kAlign + stages * stage_bytes(halves, cap) + out_bytes(halves, mode, split) + kBarBytes + tables;
+    static int smem_bytes(int halves, int cap, int stages, int out, int tables) {
+        return kAlign + stages * stage_bytes(halves, cap) + out + kBarBytes + tables;
     }
 };
 
@@ -197,9 +202,10 @@ __host__ __device__ constexpr int segment_table_bytes(int pairs, int experts) {
     return (16 + 12 * experts + 14 * pairs + 15) / 16 * 16;
 }
 
-// Tables of segment_table_bytes at `tab`; called by all threads of a CTA.
-__device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids, int pairs, int topk, int experts,
-                                                   int cap, int32_t *status) {
+// Tables of segment_table_bytes at `tab`; called by all threads of a CTA, after some work of
+// its own if it has any (`id`: load of thread q's slot q, issued before that).
+__device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids, int id, int pairs, int topk,
+                                                   int experts, int cap, int32_t *status) {
     uint32_t *mask = reinterpret_cast<uint32_t *>(tab + 4);            // [experts][2] tokens of each expert
     uint16_t *start = reinterpret_cast<uint16_t *>(mask + 2 * experts);   // [experts] first entry
     uint16_t *seg0 = start + experts;                                     // [experts] first segment
@@ -215,7 +221,7 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
     for (int e = threadIdx.x; e < 2 * experts; e += blockDim.x) mask[e] = 0u;
     __syncthreads();
     for (int q = threadIdx.x; q < pairs; q += blockDim.x) {
-        const int e = __ldcg(ids + q);
+        const int e = q == static_cast<int>(threadIdx.x) ? id : __ldcg(ids + q);
         const bool ok = e >= 0 && e < experts;
         if (e >= experts && status) atomicOr(status, DG_DEV_BAD_GROUP);
         s_ids[q] = ok ? static_cast<uint16_t>(e) : 0xFFFFu;
@@ -224,27 +230,26 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
     }
     __syncthreads();
     if (threadIdx.x < 32) {
-        auto scan = [&](int v) {   // inclusive
+        // lane l counts experts l * per .., one scan over the lanes, then it lays out its segments
+        const int per = (experts + 31) / 32;
+        int n = 0, segs = 0, units = 0;
+        for (int e = lane * per; e < min(experts, (lane + 1) * per); ++e) {
+            const int c = __popc(mask[2 * e]) + __popc(mask[2 * e + 1]);
+            n += c;
+            segs += (c + cap - 1) / cap;
+            units += c / cap * image_units(cap) + image_units(c % cap);
+        }
+        int in_n = n, in_su = segs | units << 16;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int u = __shfl_up_sync(0xFFFFFFFFu, v, d);
-                if (lane >= d) v += u;
-            }
-            return v;
-        };
-        int run = 0, seg = 0, unit = 0;
-        for (int e0 = 0; e0 < experts; e0 += 32) {
-            const int e = e0 + lane;
-            const int n = e < experts ? __popc(mask[2 * e]) + __popc(mask[2 * e + 1]) : 0;
-            const int segs = (n + cap - 1) / cap;
-            const int units = n / cap * image_units(cap) + image_units(n % cap);
-            const int in_n = scan(n), in_su = scan(segs | units << 16);
-            int first = run + in_n - n, z = seg + (in_su & 0xFFFF) - segs, u = unit + (in_su >> 16) - units;
-            if (n > 0) {
-                start[e] = static_cast<uint16_t>(first);
-                seg0[e] = static_cast<uint16_t>(z);
-            }
-            for (int left = n; left > 0; left -= cap, ++z) {
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, in_n, d), v = __shfl_up_sync(0xFFFFFFFFu, in_su, d);
+            if (lane >= d) { in_n += u; in_su += v; }
+        }
+        int first = in_n - n, z = (in_su & 0xFFFF) - segs, u = (in_su >> 16) - units;
+        for (int e = lane * per; e < min(experts, (lane + 1) * per); ++e) {
+            start[e] = static_cast<uint16_t>(first);
+            seg0[e] = static_cast<uint16_t>(z);
+            for (int left = __popc(mask[2 * e]) + __popc(mask[2 * e + 1]); left > 0; left -= cap, ++z) {
                 const int t = min(left, cap);
                 s.expert[z] = static_cast<uint16_t>(e);
                 s.first[z] = static_cast<uint16_t>(first);
@@ -253,12 +258,8 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
                 first += t;
                 u += image_units(t);
             }
-            run += __shfl_sync(0xFFFFFFFFu, in_n, 31);
-            const int all = __shfl_sync(0xFFFFFFFFu, in_su, 31);
-            seg += all & 0xFFFF;
-            unit += all >> 16;
         }
-        if (lane == 0) { tab[0] = seg; tab[1] = run; }
+        if (lane == 31) { tab[0] = in_su & 0xFFFF; tab[1] = in_n; }
     }
     __syncthreads();
     for (int q = threadIdx.x; q < pairs; q += blockDim.x) {
@@ -283,7 +284,8 @@ __global__ void __launch_bounds__(256) dg_layer_split_kernel(const uint16_t *x, 
     extern __shared__ int split_tab[];
     grid_dependency_wait();
     grid_launch_dependents();
-    const Segments s = build_segments(split_tab, ids, tokens * topk, topk, experts, cap, nullptr);
+    const int slot_id = threadIdx.x < tokens * topk ? __ldcg(ids + threadIdx.x) : -1;
+    const Segments s = build_segments(split_tab, ids, slot_id, tokens * topk, topk, experts, cap, nullptr);
     const int q16 = threadIdx.x & 15, kb = blockIdx.x;
     for (int at0 = blockIdx.y * 16; at0 < s.entries; at0 += gridDim.y * 16) {
         const int at = at0 + static_cast<int>(threadIdx.x >> 4);
@@ -328,8 +330,9 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     uint8_t *smem_b = smem_a + S * HALVES * 16384;
     uint8_t *smem_sfa = smem_b + S * b_bytes;
     uint8_t *smem_sfb = smem_sfa + S * HALVES * 512;
-    float *smem_out = reinterpret_cast<float *>(smem_sfb + S * 512);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_out + (nsplit > 1 ? 0 : 2 * 8 * OUT));
+    uint8_t *smem_end = smem_sfb + S * 512;
+    float *smem_out = reinterpret_cast<float *>(p.out_bytes ? smem_end : smem_a);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_end + p.out_bytes);
     uint64_t *full_bar = bars;              // [S] weights and scales landed, pieces landed or written
     uint64_t *empty_bar = bars + S;         // [S] the slot's MMAs are done
     uint64_t *tfull_bar = bars + 2 * S;     // [2] accumulators complete
@@ -344,6 +347,8 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     const WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
     const int first_tile = blockIdx.x / nsplit, tile_step = gridDim.x / nsplit;
 
+    const int pairs = MODE < kUp ? 0 : p.tokens * p.topk;
+    const int slot_id = MODE >= kUp && static_cast<int>(threadIdx.x) < pairs ? __ldcg(p.ids + threadIdx.x) : -1;
     if (warp == 0) {
         // arrivals: full 2 (weights, pieces), empty and tfull one per issuer, tempty 4, drain 1
         for (int i = lane; i < 2 * S + 4 + HALVES; i += 32)
@@ -358,15 +363,18 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         tmem_alloc(tmem_holder, p.tmem_cols);
         tmem_relinquish();
     }
-    // The first kernel of a chain (kGemv; a split kernel before the others) waits for
-    // what precedes it and only then lets the next one start.  So the later kernels of
-    // the chain may read weights, ids and routing weights at once; only the warps that
-    // read the preceding kernel's output wait for it.
-    if constexpr (MODE == kGemv) grid_dependency_wait();
+    __syncwarp();
+    // Split tiles: the CTAs may write to a peer's shared memory once it has started or, where
+    // the results go to the ring, once its ring is idle.
+    const bool early = p.out_bytes != 0;
+    if (nsplit > 1 && early) cluster_arrive_relaxed();
+    // The split kernel before kGemvPre, kUp and kDown waits for what precedes it and only then
+    // lets the next one start.  So these may read weights, ids and routing weights at once, and
+    // only the warps that read the preceding kernel's output wait for it.  In kGemv every warp
+    // waits that reads or writes memory.
     grid_launch_dependents();
-    const int pairs = MODE < kUp ? 0 : p.tokens * p.topk;
     Segments seg = {};
-    if constexpr (MODE >= kUp) seg = build_segments(tab, p.ids, pairs, p.topk, p.experts, p.cap, p.status);
+    if constexpr (MODE >= kUp) seg = build_segments(tab, p.ids, slot_id, pairs, p.topk, p.experts, p.cap, p.status);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -444,6 +452,11 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
             }
         }
     };
+    // All warps come by once: before they push results, or with nothing left to do.
+    auto ring_idle = [&] {
+        if (!early) cluster_arrive();
+        cluster_wait();
+    };
     auto gated = [](float g, float u) { return g / (1.0f + expf(-g)) * u; };
 
     // TMEM columns: accumulator sets, two scale slots for each issuer, kDown's results
@@ -451,8 +464,11 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     const uint32_t y_tmem = sf_tmem + 2 * HALVES * SF;          // [HALVES][tokens, up to 8]
     const int y_cols = (p.tokens + 7) & ~7;
 
-    // nsplit > 1: this CTA's partial results [ntok][ROWS], in operand row order
-    float *part = reinterpret_cast<float *>(smem_a);
+    // nsplit > 1.  A tile's results are rows of 32 items, item l the 4 results (kUp: and the 4
+    // of the up half) that lane l of the four epilogue warps hold: ROW_GROUPS rows a token.
+    // CTA r puts out rows r * share .. of them; smem_out is [CTA][share][component][32].
+    constexpr int ROW_GROUPS = OUT / 128, COMP = MODE == kUp ? 8 : 4;
+    auto share_of = [&](const FewTile &tile) { return (tile.ntok * ROW_GROUPS + nsplit - 1) / nsplit; };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -460,6 +476,22 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         uint32_t phase = 0;
         uint32_t issued = 0;
         bool drop = (p.debug_flags & DG_DEBUG_DROP_ONE_LOAD) && blockIdx.x == 0;
+        const auto box_row = [&](const FewTile &tile, int e, int h) {   // rows / 4 of a half's box
+            const int r = MODE == kUp ? h * p.inner + tile.row0 : tile.row0 + h * 128;
+            return static_cast<int32_t>((static_cast<int64_t>(e) * p.rows + r) >> 2);
+        };
+        if constexpr (MODE == kGemv) {
+            // The first K-blocks' weights to L2 while the preceding kernel ends (which makes no
+            // difference to what is read after the wait).
+            if (first_tile < num_tiles && elect_one()) {
+                const FewTile tile = get_tile(first_tile);
+                for (int i = k_begin; i < min(k_end, k_begin + p.ahead); ++i)
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h) tma_prefetch_3d(&tm_w, i * 128, box_row(tile, 0, h), 0);
+            }
+            __syncwarp();
+            grid_dependency_wait();
+        }
         for (int w = first_tile; w < num_tiles; w += tile_step) {
             const FewTile tile = get_tile(w);
             int z = MODE == kDown ? k_begin / p.kblocks : 0;
@@ -485,9 +517,8 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                     for (int h = 0; h < HALVES; ++h) {
                         const int r = MODE == kUp ? h * p.inner + tile.row0 : tile.row0 + h * 128;
                         // (a half past the last row reads zeros or the next expert's rows; unused)
-                        const int64_t r4 = (static_cast<int64_t>(e) * p.rows + r) >> 2;
                         tma_load_3d(smem_a + (slot * HALVES + h) * 16384, &tm_w, &full_bar[slot], kb * 128,
-                                    static_cast<int32_t>(r4), 0);
+                                    box_row(tile, e, h), 0);
                         if (sf_bytes[h])
                             bulk_load(smem_sfa + (slot * HALVES + h) * 512, sf + r, sf_bytes[h], &full_bar[slot]);
                     }
@@ -498,6 +529,8 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
             }
         }
     producer_done:
+        __syncwarp();
+        if (nsplit > 1) ring_idle();
         // Normally every load has landed once the MMAs are done.  After a wait that ran
         // out, never leave with loads in flight: give them the time limit once more.
         named_bar_sync(2, 32 + 32 * HALVES);   // the issuers are done with their waits
@@ -558,6 +591,8 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
             }
         }
     mma_done:
+        __syncwarp();
+        if (nsplit > 1) ring_idle();
         // TMEM is not freed before every MMA has finished
         if (elect_one()) {
             tc_commit(&drain_bar[h]);
@@ -567,6 +602,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         named_bar_sync(2, 32 + 32 * HALVES);
     } else if (warp >= FIRST_B) {
         // ------------------------------------------------------------ the narrow operand
+        grid_dependency_wait();
         if constexpr (MODE == kGemv) {
             // The warps take the K-blocks in turn, at most as many warps as ring slots: a
             // wait for the MMAs of block g - S tests one parity bit, which is unambiguous
@@ -600,7 +636,6 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         } else {
             int slot = 0;
             uint32_t phase = 0;
-            grid_dependency_wait();
             for (int w = first_tile; w < num_tiles; w += tile_step) {
                 const FewTile tile = get_tile(w);
                 int z = MODE == kDown ? k_begin / p.kblocks : tile.seg;
@@ -626,13 +661,34 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         }
     b_done:
         __syncwarp();
+        if (nsplit > 1) ring_idle();
     } else {
         // ------------------------------------------------------------ epilogue
         const uint32_t quad = warp & 3;
         const int id = threadIdx.x - 32 * FewConfig::kFirstEpi;   // 0..127
         int acc = 0, buf = 0;
+        bool pushed = false;
         uint32_t acc_phase = 0;
-        if constexpr (MODE != kGemv) grid_dependency_wait();       // C, and memory that the output may share
+        grid_dependency_wait();       // C, and memory that the output may share
+        // Results of this thread's operand row (of each half) for n tokens from t0, to the CTAs
+        // that put them out.
+        auto push = [&](const FewTile &tile, int t0, int n, const float (&r)[HALVES][8]) {
+            const int share = share_of(tile);
+            int row = t0 * ROW_GROUPS, owner = row / share;
+            row -= owner * share;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j >= n) break;
+#pragma unroll
+                for (int g = 0; g < ROW_GROUPS; ++g) {
+                    const uint32_t at = mapa_shared(
+                        smem_u32(smem_out + ((rank * share + row) * COMP + quad) * 32 + lane), owner);
+                    st_shared_cluster_f32(at, r[g][j]);
+                    if constexpr (MODE == kUp) st_shared_cluster_f32(at + 4 * 4 * 32, r[HALVES - 1][j]);
+                    if (++row == share) { row = 0; ++owner; }
+                }
+            }
+        };
         // Sums of columns 2 t0 .. 2 t0 + 15 in pairs: 8 tokens' results at this thread's operand rows
         auto read8 = [&](int t0, float (&r)[HALVES][8]) {
             uint32_t v[HALVES][16];
@@ -706,10 +762,13 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                     release();
                     i = (z + 1) * p.kblocks;
                 }
+                if (nsplit > 1) ring_idle();
+                pushed = true;
                 for (int t0 = 0; t0 < p.tokens; t0 += 8) {
                     const int n = min(8, p.tokens - t0);
-                    float *out = nsplit > 1 ? part + t0 * ROWS : smem_out + buf * 8 * OUT;
+                    float *out = smem_out + buf * 8 * OUT;
                     uint32_t y[HALVES][8];
+                    float r[HALVES][8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -720,32 +779,41 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
 #pragma unroll
                         for (int h = 0; h < HALVES; ++h) {
                             reg_fence1(y[h][j]);
-                            if (j < n) out[j * ROWS + h * 128 + mine] = __uint_as_float(y[h][j]);
+                            r[h][j] = __uint_as_float(y[h][j]);
+                            if (j < n && nsplit == 1) out[j * ROWS + h * 128 + mine] = r[h][j];
                         }
                     }
-                    if (nsplit > 1) continue;
+                    if (nsplit > 1) {
+                        push(tile, t0, n, r);
+                        continue;
+                    }
                     named_bar_sync(1, 128);
                     write_out(tile, out, t0, n);
                     buf ^= 1;
                 }
             } else {
                 if (!wait_acc()) break;
+                if (nsplit > 1) ring_idle();
+                pushed = true;
                 for (int t0 = 0; t0 < tile.ntok; t0 += 8) {
                     float r[HALVES][8];
                     read8(t0, r);
                     const int n = min(8, tile.ntok - t0);
-                    float *out = nsplit > 1 ? part + t0 * ROWS : smem_out + buf * 8 * OUT;
+                    float *out = smem_out + buf * 8 * OUT;
+                    if (nsplit > 1) {
+                        push(tile, t0, n, r);
+                        continue;
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         if (j >= n) break;
-                        if (MODE == kUp && nsplit == 1) {
+                        if (MODE == kUp) {
                             out[j * OUT + mine] = gated(r[0][j], r[HALVES - 1][j]);
                         } else {
 #pragma unroll
                             for (int h = 0; h < HALVES; ++h) out[j * ROWS + h * 128 + mine] = r[h][j];
                         }
                     }
-                    if (nsplit > 1) continue;
                     named_bar_sync(1, 128);
                     write_out(tile, out, t0, n);
                     buf ^= 1;
@@ -755,6 +823,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         }
     epi_done:
         __syncwarp();
+        if (nsplit > 1 && !pushed) ring_idle();
     }
 
     tc_fence_before_sync();
@@ -765,29 +834,26 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     }
     if (nsplit == 1) return;
     // ---------------------------------------------------------------- sum over the cluster (one tile)
-    cluster_sync();
+    cluster_sync();   // every CTA's results are here; nobody writes to or reads from a peer after this
     if (first_tile < num_tiles) {
         const FewTile tile = get_tile(first_tile);
-        const uint32_t part0 = smem_u32(part);
-        auto sum = [&](int idx) {
-            float s = 0.0f;
-            for (int r = 0; r < nsplit; ++r) s += ld_shared_cluster_f32(mapa_shared(part0 + 4u * idx, r));
-            return s;
-        };
-        for (int q = rank * NT + threadIdx.x; q < tile.ntok * (OUT / 4); q += nsplit * NT) {
-            const int t = q / (OUT / 4), l = q % (OUT / 4);
-            const int base = t * ROWS + (l >> 5) * 128 + (l & 31);
+        const int share = share_of(tile);
+        const int rows = min(share, tile.ntok * ROW_GROUPS - rank * share);
+        for (int row = warp; row < rows; row += NT / 32) {
             float o[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                o[c] = sum(base + 32 * c);
-                if constexpr (MODE == kUp) o[c] = gated(o[c], sum(base + 128 + 32 * c));
+                float s = 0.0f, u = 0.0f;
+                for (int r = 0; r < nsplit; ++r) {
+                    s += smem_out[((r * share + row) * COMP + c) * 32 + lane];
+                    if constexpr (MODE == kUp) u += smem_out[((r * share + row) * COMP + 4 + c) * 32 + lane];
+                }
+                o[c] = MODE == kUp ? gated(s, u) : s;
             }
-            store(tile, t, tile.row0 + 4 * l, o);
+            const int at = rank * share + row;
+            store(tile, at / ROW_GROUPS, tile.row0 + (at % ROW_GROUPS) * 128 + 4 * lane, o);
         }
     }
-    __syncwarp();
-    cluster_sync();   // peers may still read this CTA's partial results
 }
 
 }  // namespace dg

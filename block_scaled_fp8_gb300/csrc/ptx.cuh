@@ -211,6 +211,14 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The two halves of a cluster barrier; relaxed: without ordering this CTA's memory accesses
+// (enough to say that it has started, so that its shared memory may be written to).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 // ----------------------------------------------------------------- proxies
 
 // Make generic-proxy writes to shared memory visible to the async proxy
@@ -277,6 +285,14 @@ __device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *m
         : "memory");
 }
 
+// The box of tma_load_3d into L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 // As tma_load_3d, completing on an mbarrier given by its cluster address
 // (the leader CTA's barrier in a CTA pair).
 __device__ __forceinline__ void tma_load_3d_pair(void *smem_dst, const CUtensorMap *map,
@@ -331,11 +347,9 @@ __device__ __forceinline__ void bulk_load(void *smem_dst, const void *src, uint3
                  : "memory");
 }
 
-// FP32 word of another CTA's shared memory (cluster address from mapa_shared).
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr));
-    return v;
+// FP32 word to another CTA's shared memory (cluster address from mapa_shared).
+__device__ __forceinline__ void st_shared_cluster_f32(uint32_t cluster_addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
 // ----------------------------------------------------------------- E4M3 conversions
