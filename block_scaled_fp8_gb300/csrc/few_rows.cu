@@ -22,14 +22,14 @@ int pow2_at_least(int v) {
 }
 
 // Rows of weights seen as [rows / 4][4]: weight row 4l + c lands in operand row 32c + l.
-bool encode_weights(CUtensorMap *map, bool fp4, const void *base, int64_t rows, int64_t ld_bytes, int k) {
+bool encode_weights(CUtensorMap *map, int w, const void *base, int64_t rows, int64_t ld_bytes, int k) {
     const TensorMapEncodeFn enc = host_encode();
     if (enc == nullptr) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows / 4), 4};
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(w == kFp4Packed ? k / 2 : k), static_cast<cuuint64_t>(rows / 4), 4};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(4 * ld_bytes), static_cast<cuuint64_t>(ld_bytes)};
     const cuuint32_t box[3] = {128, 32, 4};
     const cuuint32_t step[3] = {1, 1, 1};
-    return enc(map, fp4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+    return enc(map, w == kFp4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
                const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -41,28 +41,28 @@ struct Plan {
     int halves, occ, split;
 };
 
-template <bool FP4, int HALVES, int MODE>
+template <int W, int HALVES, int MODE>
 cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles,
                    int num_sms, cudaStream_t stream) {
     const int tables = MODE < kUp ? 0 : segment_table_bytes(a.tokens * a.topk, a.experts);
     a.out_bytes = FewConfig::out_bytes(HALVES, MODE, MODE == kUp ? a.cap : a.tokens, plan.split);
     // (split results of more than 8 KB go to the ring: one more wait, but no stage less)
     if (plan.split > 1 && a.out_bytes > 8192) a.out_bytes = 0;
-    a.ahead = kAhead / (HALVES * (FP4 ? 8192 : 16384)) / plan.occ;
-    const int fixed = FewConfig::smem_bytes(HALVES, a.cap, 0, a.out_bytes, tables);
-    const int stage = FewConfig::stage_bytes(HALVES, a.cap);
+    a.ahead = kAhead / (HALVES * (W == kFp4 ? 8192 : 16384)) / plan.occ;
+    const int fixed = FewConfig::smem_bytes(W, HALVES, a.cap, 0, a.out_bytes, tables);
+    const int stage = FewConfig::stage_bytes(W, HALVES, a.cap);
     const int limit = plan.occ == 2 ? kSmemTwo : kSmemOne;
     int stages = (limit - fixed) / stage;
     if (stages > FewConfig::kMaxStages) stages = FewConfig::kMaxStages;
     if (stages < 2) return cudaErrorInvalidConfiguration;
-    const int set = HALVES * 2 * a.cap, most = plan.occ == 2 ? 256 : 512;
-    const int sf = 2 * HALVES * 8 + (MODE == kDown ? HALVES * ((a.tokens + 7) & ~7) : 0);
+    const int set = HALVES * pieces_of(W) * a.cap, most = plan.occ == 2 ? 256 : 512;
+    const int sf = 2 * HALVES * 8 * scale_blocks(W) + (MODE == kDown ? HALVES * ((a.tokens + 7) & ~7) : 0);
     a.stages = stages;
     a.accs = (plan.split == 1 || MODE == kDown) && 2 * set + sf <= most ? 2 : 1;
     a.tmem_cols = pow2_at_least(a.accs * set + sf);
     if (a.tmem_cols > 512) return cudaErrorInvalidConfiguration;
-    const int smem = FewConfig::smem_bytes(HALVES, a.cap, stages, a.out_bytes, tables);
-    auto kernel = dg_few_rows_kernel<FP4, HALVES, MODE>;
+    const int smem = FewConfig::smem_bytes(W, HALVES, a.cap, stages, a.out_bytes, tables);
+    auto kernel = dg_few_rows_kernel<W, HALVES, MODE>;
     static std::atomic<uint64_t> ready{0};   // devices whose attributes are set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -89,23 +89,26 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = plan.split > 1 ? 2 : 1;
-    host_set_last_config(HALVES * 128, 2 * a.cap, stages, grid, MODE < kUp ? 3 : 5,
+    host_set_last_config(HALVES * 128, pieces_of(W) * a.cap, stages, grid, MODE < kUp ? 3 : 5,
                          MODE == kGemv ? 1 : MODE == kGemvPre ? 2 : 3);
     return cudaLaunchKernelEx(&cfg, kernel, map, a);
 }
 
 template <int HALVES, int MODE>
-cudaError_t launch_fmt(bool fp4, const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles, int num_sms,
+cudaError_t launch_fmt(int w, const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles, int num_sms,
                        cudaStream_t stream) {
-    return fp4 ? launch<true, HALVES, MODE>(map, a, plan, max_tiles, num_sms, stream)
-               : launch<false, HALVES, MODE>(map, a, plan, max_tiles, num_sms, stream);
+    if (w == kFp8) return launch<kFp8, HALVES, MODE>(map, a, plan, max_tiles, num_sms, stream);
+    if (w == kFp4Packed) return launch<kFp4Packed, HALVES, MODE>(map, a, plan, max_tiles, num_sms, stream);
+    // (the fewest rows, kGemv, always have their FP4 weights packed)
+    if constexpr (MODE != kGemv) return launch<kFp4, HALVES, MODE>(map, a, plan, max_tiles, num_sms, stream);
+    return cudaErrorInvalidValue;
 }
 
 template <int MODE>
-cudaError_t launch_mode(bool fp4, const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles, int num_sms,
+cudaError_t launch_mode(int w, const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles, int num_sms,
                         cudaStream_t stream) {
-    return plan.halves == 2 ? launch_fmt<2, MODE>(fp4, map, a, plan, max_tiles, num_sms, stream)
-                            : launch_fmt<1, MODE>(fp4, map, a, plan, max_tiles, num_sms, stream);
+    return plan.halves == 2 ? launch_fmt<2, MODE>(w, map, a, plan, max_tiles, num_sms, stream)
+                            : launch_fmt<1, MODE>(w, map, a, plan, max_tiles, num_sms, stream);
 }
 
 // Clusters of 1..kMaxSplit CTAs that are resident at once with one CTA on an SM (the SMs
@@ -119,7 +122,7 @@ const int *resident_clusters(int num_sms) {
     dev &= 63;
     std::lock_guard<std::mutex> lock(mutex);
     if (!ready[dev]) {
-        auto kernel = dg_few_rows_kernel<true, 1, kGemv>;
+        auto kernel = dg_few_rows_kernel<kFp8, 1, kGemv>;
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne);
         for (int c = 1; c <= kMaxSplit; ++c) {
             cudaLaunchConfig_t cfg = {};
@@ -194,44 +197,65 @@ int segment_capacity(int64_t t, int64_t topk, int64_t experts) {
     return capacity(static_cast<int>(most < t ? most : t));
 }
 
-// Bounds of the layer's segments, and of their units of 8 image rows (4 tokens).
+// FP4 weights packed, where all activations fit the digits' 64 columns.
+int format_of(bool fp4, int cap) { return !fp4 ? kFp8 : cap == 8 ? kFp4Packed : kFp4; }
+
+// Bounds of the layer's segments and of their images.
 struct SegmentBounds {
+    int w, cap;
     int64_t count, units;
-    SegmentBounds(int64_t t, int64_t topk, int64_t experts) {
+    SegmentBounds(bool fp4, int64_t t, int64_t topk, int64_t experts) {
         const int64_t pairs = t * topk, used = pairs < experts ? pairs : experts;
-        const int cap = segment_capacity(t, topk, experts);
+        cap = segment_capacity(t, topk, experts);
+        w = format_of(fp4, cap);
         count = used + pairs / cap;
         if (count > pairs) count = pairs;
-        units = (pairs + 3 * count) / 4;
+        units = w == kFp4Packed ? pairs : (pairs + 3 * count) / 4;
     }
-    int64_t image(int64_t k) const { return units * (k / 128) * 1024; }
-    int64_t scales(int64_t k) const { return count * (k / 128) * 512; }
+    int64_t blocks(int64_t k) const { return (k + block_k(w) - 1) / block_k(w); }
+    int64_t image(int64_t k) const { return units * blocks(k) * 1024; }
+    int64_t scales(int64_t k) const { return count * blocks(k) * scale_blocks(w) * 512; }
 };
 
 }  // namespace
 
 int64_t few_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    return direct(m) ? 0 : k / 128 * ((m + 3) / 4 * 1024 + 512);
+    if (direct(m)) return 0;
+    int64_t most = 0;   // of either weight type
+    for (int w : {static_cast<int>(kFp8), format_of(true, capacity(static_cast<int>(m)))}) {
+        const int64_t blocks = (k + block_k(w) - 1) / block_k(w);
+        const int64_t bytes = blocks * (image_units(pieces_of(w), static_cast<int>(m)) * 1024 + scale_blocks(w) * 512);
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 int64_t layer_workspace_bytes(int64_t t, int64_t topk, int64_t h, int64_t i, int64_t experts) {
     if (t == 0 || topk == 0 || experts == 0) return 0;
-    const SegmentBounds b(t, topk, experts);
-    return b.image(h) + b.image(i) + b.scales(h) + b.scales(i);
+    int64_t most = 0;
+    for (bool fp4 : {false, true}) {
+        const SegmentBounds b(fp4, t, topk, experts);
+        const int64_t bytes = b.image(h) + b.image(i) + b.scales(h) + b.scales(i);
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream) {
-    CUtensorMap map;
-    if (!encode_weights(&map, p.fp4, p.b, p.n, p.ldb, p.k)) return cudaErrorInvalidValue;
     FewArgs a = {};
+    a.cap = capacity(p.m);
+    const int w = format_of(p.fp4, a.cap);
+    CUtensorMap map;
+    if (!encode_weights(&map, w, p.b, p.n, p.ldb, p.k)) return cudaErrorInvalidValue;
     a.x = p.a;
     a.ldx = p.lda;
     a.sf = p.sfb;
     a.sf_ld = cdiv(p.n, 4) * 4;
     a.rows = p.n;
     a.tokens = p.m;
-    a.kblocks = p.k / 128;
-    a.cap = capacity(p.m);
+    a.kblocks = cdiv(p.k, block_k(w));
+    a.slices = p.fp4 ? p.k / 128 : cdiv(p.k, 512);
+    a.last_mmas = p.k % 256 ? 2 : 4;
     a.c = p.c;
     a.ldc = p.ldc;
     a.d = p.d;
@@ -240,7 +264,8 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream
     a.status = p.status;
     a.timeout_ns = p.timeout_ns;
     a.debug_flags = p.debug_flags;
-    // The split of K depends on n and k alone, so a row's result does not depend on m.
+    // The split of K depends on n, k and the format alone, so a row's result does not depend on
+    // the other rows of the call.
     Plan plan = {1, 2, choose_split(cdiv(p.n, 128), a.kblocks, 2, num_sms, true)};
     if (plan.split == 1) {
         // Many tiles.  Two CTAs of 128-row tiles on an SM, or one of 256-row tiles, which reads the
@@ -251,31 +276,36 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream
         else if (p.m > 8) plan = {2, 1, 1};
     }
     a.row_tiles = cdiv(p.n, 128 * plan.halves);
-    if (direct(p.m)) return launch_mode<kGemv>(p.fp4, map, a, plan, a.row_tiles, num_sms, stream);
-    a.image = p.workspace;
-    a.image_sf = p.workspace + static_cast<int64_t>(a.kblocks) * ((p.m + 3) / 4) * 1024;
-    Dependent split(dim3(static_cast<unsigned>(cdiv(p.m * a.kblocks, 16))), 0, stream);
-    cudaError_t e = cudaLaunchKernelEx(&split.cfg, dg_few_split_kernel, a.x, a.ldx, p.m, a.kblocks,
-                                       const_cast<uint8_t *>(a.image), const_cast<uint8_t *>(a.image_sf));
+    if (direct(p.m)) return launch_mode<kGemv>(w, map, a, plan, a.row_tiles, num_sms, stream);
+    uint8_t *image = p.workspace;
+    uint8_t *image_sf = image + static_cast<int64_t>(a.kblocks) * image_units(pieces_of(w), p.m) * 1024;
+    const int rows = 256 * 8 / block_k(w);   // rows' K-blocks of a CTA
+    Dependent split(dim3(static_cast<unsigned>(cdiv(p.m * a.kblocks, rows))), 0, stream);
+    cudaError_t e = cudaLaunchKernelEx(&split.cfg, w == kFp4Packed ? dg_few_split_kernel<kFp4Packed> : dg_few_split_kernel<kFp8>,
+                                       a.x, a.ldx, p.m, p.k, image, image_sf);
     if (e != cudaSuccess) return e;
-    return launch_mode<kGemvPre>(p.fp4, map, a, plan, a.row_tiles, num_sms, stream);
+    a.image = image;
+    a.image_sf = image_sf;
+    return launch_mode<kGemvPre>(w, map, a, plan, a.row_tiles, num_sms, stream);
 }
 
 cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t stream) {
+    const SegmentBounds bounds(p.fp4, p.t, p.topk, p.experts);
+    const int w = bounds.w, cap = bounds.cap, pairs = p.t * p.topk;
     CUtensorMap map1, map2;
     const int64_t per = p.fp4 ? 2 : 1;
-    if (!encode_weights(&map1, p.fp4, p.w1, static_cast<int64_t>(p.experts) * 2 * p.i, p.h / per, p.h) ||
-        !encode_weights(&map2, p.fp4, p.w2, static_cast<int64_t>(p.experts) * p.h, p.i / per, p.i))
+    if (!encode_weights(&map1, w, p.w1, static_cast<int64_t>(p.experts) * 2 * p.i, p.h / per, p.h) ||
+        !encode_weights(&map2, w, p.w2, static_cast<int64_t>(p.experts) * p.h, p.i / per, p.i))
         return cudaErrorInvalidValue;
-    const SegmentBounds bounds(p.t, p.topk, p.experts);
     uint8_t *x_image = p.workspace, *h_image = x_image + bounds.image(p.h);
     uint8_t *x_sf = h_image + bounds.image(p.i), *h_sf = x_sf + bounds.scales(p.h);
-    const int cap = segment_capacity(p.t, p.topk, p.experts), pairs = p.t * p.topk;
-    const int kh = p.h / 128, ki = p.i / 128;
-    Dependent split(dim3(static_cast<unsigned>(kh), static_cast<unsigned>(cdiv(pairs, 64))),
+    const int kh = static_cast<int>(bounds.blocks(p.h)), ki = static_cast<int>(bounds.blocks(p.i));
+    const int rows = 256 * 8 / block_k(w);
+    Dependent split(dim3(static_cast<unsigned>(kh), static_cast<unsigned>(cdiv(pairs, 4 * rows))),
                     segment_table_bytes(pairs, p.experts), stream);
-    cudaError_t e = cudaLaunchKernelEx(&split.cfg, dg_layer_split_kernel, p.x, p.ldx, p.ids, p.t, p.topk, p.experts,
-                                       cap, kh, x_image, x_sf);
+    cudaError_t e = cudaLaunchKernelEx(&split.cfg,
+                                       w == kFp4Packed ? dg_layer_split_kernel<kFp4Packed> : dg_layer_split_kernel<kFp8>,
+                                       p.x, p.ldx, p.ids, p.t, p.topk, p.experts, cap, p.h, x_image, x_sf);
     if (e != cudaSuccess) return e;
     FewArgs a = {};
     a.tokens = p.t;
@@ -300,16 +330,18 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.out_image_sf = h_sf;
     a.sf = p.sf1;
     a.sf_ld = 2 * p.i;
-    a.sf_expert = static_cast<int64_t>(p.fp4 ? kh : cdiv(kh, 4)) * a.sf_ld;
+    a.slices = p.fp4 ? p.h / 128 : cdiv(p.h, 512);
+    a.last_mmas = p.h % 256 ? 2 : 4;
+    a.sf_expert = static_cast<int64_t>(a.slices) * a.sf_ld;
     a.rows = 2 * p.i;
     a.kblocks = kh;
-    a.row_tiles = ki;
-    const int up_tiles = static_cast<int>(bounds.count) * ki;
+    a.row_tiles = p.i / 128;
+    const int up_tiles = static_cast<int>(bounds.count) * a.row_tiles;
     Plan up;
     up.halves = 2;
     up.occ = 1;
     up.split = choose_split(up_tiles, kh, up.occ, num_sms, false);
-    e = launch_fmt<2, kUp>(p.fp4, map1, a, up, up_tiles, num_sms, stream);
+    e = launch_fmt<2, kUp>(w, map1, a, up, up_tiles, num_sms, stream);
     if (e != cudaSuccess) return e;
     // down: K runs over the segments
     a.row_tiles = down_tiles;
@@ -317,7 +349,9 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.image_sf = h_sf;
     a.sf = p.sf2;
     a.sf_ld = p.h;
-    a.sf_expert = static_cast<int64_t>(p.fp4 ? ki : cdiv(ki, 4)) * a.sf_ld;
+    a.slices = p.fp4 ? p.i / 128 : cdiv(p.i, 512);
+    a.last_mmas = p.i % 256 ? 2 : 4;
+    a.sf_expert = static_cast<int64_t>(a.slices) * a.sf_ld;
     a.rows = p.h;
     a.kblocks = ki;
     a.c = p.c;
@@ -325,7 +359,7 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.d = p.y;
     a.ldd = p.ldy;
     a.debug_flags = 0;
-    return launch_mode<kDown>(p.fp4, map2, a, down, a.row_tiles, num_sms, stream);
+    return launch_mode<kDown>(w, map2, a, down, a.row_tiles, num_sms, stream);
 }
 
 }  // namespace dg

@@ -1,22 +1,29 @@
 // Products of a few bf16 rows with FP4 or FP8 weights, and the two kernels of the MoE
 // layer for few tokens, on the block-scaled tensor cores.
 //
-// The weights are the MMA's 128-row operand, straight from their packed form (TMA
-// unpacks E2M1 to one code per byte of shared memory; their UE8M0 scales go to TMEM
-// as they are), so no instruction touches a weight.  The activations are the narrow
-// operand: each value x of a group of 32 along K is split into two E4M3 pieces
-//     x = s (hi + lo / 16),  s = 2^(floor(log2 max|x|) - 7),
-// which occupy two adjacent columns with the scales s and s/16.  hi holds 4 significant
-// bits and lo the 4 that follow (with its sign, 9 bits in all), so a bf16 value is
-// represented exactly down to 2^-13 of its group's largest, and to 2^-21 of the largest
-// below that.  An FP32 value (the layer's inner activations) is rounded to 9 bits, half
-// a bf16 unit.  Products and sums are FP32 in TMEM; the two columns are added at the end.
+// The weights are the MMA's 128-row operand, straight from their packed form, their UE8M0
+// scales going to TMEM as they are, so no instruction touches a weight.  The activations are
+// the narrow operand: each value x of a group of 32 along K is split into pieces of the
+// weights' width or less, which occupy adjacent columns and are added at the end:
+//  - two E4M3 pieces, x = s (hi + lo / 16), s = 2^(floor(log2 max|x|) - 7).  hi holds 4 significant
+//    bits and lo the 4 that follow (with its sign, 9 bits in all), so a bf16 value is
+//    represented exactly down to 2^-13 of its group's largest, and to 2^-21 of the largest
+//    below that.  An FP32 value (the layer's inner activations) is rounded to 9 bits, half a
+//    bf16 unit.
+//  - for FP4 weights and at most 8 rows, eight E2M1 digits, x = s sum_j d_j / 8^j with
+//    s = 2^(floor(log2 max|x|) - 1): |d| <= 4, each step leaves at most 1/8 of its range, and the
+//    whole is exact to 2^-23 of the group's largest (to 2^-128 absolute, for groups below 2^-105).
+// Products and sums are FP32 in TMEM.
 //
-// With M = 128 weight rows an MMA of K = 32 takes as long as its 4 KB of weights take
-// to be read from shared memory up to N = 64 columns (32 rows of activations), which is a
-// third of the time they take from HBM: the weight stream is the bound.
+// With M = 128 weight rows an MMA takes as long as its 4 KB of weights take to be read from
+// shared memory up to N = 64 columns, which is a third of the time they take from HBM: the
+// weight stream is the bound.  The digits exist for that stream: FP4 x FP4 takes the weights
+// packed, 128 bytes a row, and TMA brings them at the rate of bytes; beside E4M3 they have to
+// be unpacked to a byte a code, which TMA does at 38 GB/s an SM (214 ns for 128 rows of 64
+// bytes, measured with nothing but loads).
 //
-// A CTA computes tiles of HALVES x 128 weight rows, over K-blocks of 128 K:
+// A CTA computes tiles of HALVES x 128 weight rows, over K-blocks of 128 K (digits: 256 K, 128
+// bytes of a row in either case):
 //   warp 0      producer: weights by TMA (a 3-D box that takes weight row 4l + c to
 //               operand row 32c + l, so that 128 consecutive scale words are already in
 //               the order in which tcgen05.cp takes them to TMEM), scales by bulk copy.
@@ -54,6 +61,17 @@ namespace dg {
 
 enum FewMode : int { kGemv = 0, kGemvPre = 1, kUp = 2, kDown = 3 };
 
+// The weights' form.
+enum FewFormat : int {
+    kFp8 = 0,        // E4M3, activations in two E4M3 pieces
+    kFp4 = 1,        // E2M1 unpacked by TMA, activations in two E4M3 pieces
+    kFp4Packed = 2   // E2M1 packed, activations in eight E2M1 digits
+};
+// Columns of a token, and 512-byte blocks of scale words per K-block and 128 rows.
+__host__ __device__ constexpr int pieces_of(int w) { return w == kFp4Packed ? 8 : 2; }
+__host__ __device__ constexpr int scale_blocks(int w) { return w == kFp4Packed ? 2 : 1; }
+__host__ __device__ constexpr int block_k(int w) { return w == kFp4Packed ? 256 : 128; }
+
 struct FewArgs {
     const uint16_t *x;      // kGemv: bf16 activations
     int64_t ldx;
@@ -67,7 +85,9 @@ struct FewArgs {
     int rows;               // weight rows of one expert (kUp: 2 i)
     int tokens;
     int kblocks;            // K-blocks of one expert
-    int cap;                // tokens of a segment at most (8, 16, 32 or 64); N = 2 cap
+    int slices;             // scale slices of one expert's weights (packed FP4: K / 128)
+    int last_mmas;          // packed FP4: MMAs of K = 64 in the last K-block (4, or 2)
+    int cap;                // tokens of a segment at most (8, 16, 32 or 64); N = 2 cap (digits: 8 cap)
     int stages;
     int out_bytes;          // room of its own for the results, or 0: split results go to the ring
     int ahead;              // kGemv: K-blocks per CTA to bring to L2 before the wait
@@ -97,7 +117,9 @@ struct FewConfig {
     static constexpr int kAlign = 1024;
     static constexpr int kBarBytes = 512;
     static constexpr int kMaxStages = 24;
-    static int stage_bytes(int halves, int cap) { return halves * 16384 + 2 * cap * 128 + halves * 512 + 512; }
+    static int stage_bytes(int w, int halves, int cap) {
+        return halves * 16384 + pieces_of(w) * cap * 128 + (halves + 1) * 512 * scale_blocks(w);
+    }
     // Two buffers of 8 tokens' FP32 results; of a split tile, what this CTA puts out (rows of
     // 32 items of 4 results, shared out to the cluster's CTAs) from each of its CTAs.
     static int out_bytes(int halves, int mode, int cols, int split) {
@@ -105,8 +127,8 @@ struct FewConfig {
         const int rows = cols * (mode == kUp ? 1 : halves);
         return (rows + split - 1) / split * split * 32 * 4 * (mode == kUp ? 8 : 4);
     }
-    static int smem_bytes(int halves, int cap, int stages, int out, int tables) {
-        return kAlign + stages * stage_bytes(halves, cap) + out + kBarBytes + tables;
+    static int smem_bytes(int w, int halves, int cap, int stages, int out, int tables) {
+        return kAlign + stages * stage_bytes(w, halves, cap) + out + kBarBytes + tables;
     }
 };
 
@@ -127,62 +149,107 @@ __device__ __forceinline__ uint32_t hi_scale(uint32_t e8) { return e8 == 255u ? 
 __device__ __forceinline__ uint32_t lo_scale(uint32_t e8) { return e8 == 255u ? 255u : e8 - 11u; }
 __device__ __forceinline__ float inverse_scale(uint32_t e8) { return __uint_as_float((261u - e8) << 23); }
 
-// Lane q16 of 16 holds values 8 q16 .. 8 q16 + 7 of one row's K-block (4 lanes to a group
-// of 32): their pieces, and the group's exponent.
-__device__ __forceinline__ uint32_t split_bf16(const uint4 &v, uint2 &hi, uint2 &lo) {
+// Biased exponent of the largest of a group of 32, 8 bf16 values in each of 4 lanes.
+__device__ __forceinline__ uint32_t group_exponent(const uint4 &v) {
     const uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                                  __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
     uint32_t m = max(m2 >> 16, m2 & 0xFFFFu);
     m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const uint32_t e8 = max(m >> 7, 11u);
-    const float inv = inverse_scale(e8);
+    return m >> 7;
+}
+__device__ __forceinline__ void scaled(const uint4 &v, float by, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float f[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16) * inv;
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
+        f[2 * j] = __uint_as_float(w[j] << 16) * by;
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * by;
     }
+}
+
+// A lane's 8 bf16 values to their pieces; returns the group's exponent.
+__device__ __forceinline__ uint32_t split_bf16(const uint4 &v, uint2 &hi, uint2 &lo) {
+    const uint32_t e8 = max(group_exponent(v), 11u);
+    float f[8];
+    scaled(v, inverse_scale(e8), f);
     split4(f[0], f[1], f[2], f[3], hi.x, lo.x);
     split4(f[4], f[5], f[6], f[7], hi.y, lo.y);
     return e8;
 }
 
+// N scaled values (|f| < 4) to their j-th digits, N codes of 4 bits; what is left of them, times 8.
+template <int N>
+__device__ __forceinline__ uint32_t next_digits(float (&f)[N]) {
+    uint32_t code = 0;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const uint32_t c = cvt_e2m1x2(f[i], f[i + 1]);
+        const uint32_t back = e2m1x2_to_f16x2(c);
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+        code |= c << (4 * i);
+        f[i] = (f[i] - v.x) * 8.0f;
+        f[i + 1] = (f[i + 1] - v.y) * 8.0f;
+    }
+    return code;
+}
+__device__ __forceinline__ uint32_t digit_scale(uint32_t e8, int j) { return e8 == 255u ? 255u : e8 - 1u - 3u * j; }
+__device__ __forceinline__ float inverse_digit_scale(uint32_t e8) { return __uint_as_float((255u - e8) << 23); }
+constexpr uint32_t kLeastDigitExponent = 22;   // the last digit's scale is representable
+
 // Position of operand row n's scale word in a 512-byte block (tcgen05.cp order).
 __device__ __forceinline__ uint32_t sf_word(uint32_t n) { return (n & 31u) * 4u + (n >> 5); }
 
-// Image of n tokens' K-block: their 2n rows in units of 8 (1024 bytes).
-__device__ __forceinline__ int image_units(int tokens) { return (tokens + 3) >> 2; }
+// Image of n tokens' K-block: their rows in units of 8 (1024 bytes).
+__host__ __device__ constexpr int image_units(int pieces, int tokens) { return (pieces * tokens + 7) >> 3; }
 
-// Lane q16's pieces of token column col to the K-block's image, and its group's scales.
-__device__ __forceinline__ void put_pieces(uint8_t *image, uint8_t *sf, int col, int q16, const uint2 &hi,
-                                           const uint2 &lo, uint32_t e8) {
-    const uint32_t n = 2 * col;
-    const uint32_t off = (q16 & 1) * 8;
-    *reinterpret_cast<uint2 *>(image + n * 128 + (((q16 >> 1) ^ (n & 7)) << 4) + off) = hi;
-    *reinterpret_cast<uint2 *>(image + (n + 1) * 128 + (((q16 >> 1) ^ ((n + 1) & 7)) << 4) + off) = lo;
-    if ((q16 & 3) == 0) {
-        uint8_t *s = sf + sf_word(n) * 4 + (q16 >> 2);
-        s[0] = static_cast<uint8_t>(hi_scale(e8));
-        s[16] = static_cast<uint8_t>(lo_scale(e8));
+// The lanes of one row's K-block (16, digits: 32; lane q holds values 8 q ..) write token column
+// col of the K-block's image and its scales.  All lanes of a warp come here; `in`: to write.
+template <int W>
+__device__ __forceinline__ void split_row(const uint4 &v, uint8_t *image, uint8_t *sf, int col, int q, bool in) {
+    if constexpr (W != kFp4Packed) {
+        uint2 hi, lo;
+        const uint32_t e8 = split_bf16(v, hi, lo);
+        if (!in) return;
+        const uint32_t n = 2 * col;
+        const uint32_t off = (q & 1) * 8;
+        *reinterpret_cast<uint2 *>(image + n * 128 + (((q >> 1) ^ (n & 7)) << 4) + off) = hi;
+        *reinterpret_cast<uint2 *>(image + (n + 1) * 128 + (((q >> 1) ^ ((n + 1) & 7)) << 4) + off) = lo;
+        if ((q & 3) == 0) {
+            uint8_t *s = sf + sf_word(n) * 4 + (q >> 2);
+            s[0] = static_cast<uint8_t>(hi_scale(e8));
+            s[16] = static_cast<uint8_t>(lo_scale(e8));
+        }
+    } else {
+        const uint32_t e8 = max(group_exponent(v), kLeastDigitExponent);
+        float f[8];
+        scaled(v, inverse_digit_scale(e8), f);
+        uint8_t *s = sf + (q >> 4) * 512 + sf_word(8 * col) * 4 + ((q >> 2) & 3);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t code = next_digits(f);
+            if (!in) continue;
+            *reinterpret_cast<uint32_t *>(image + (8 * col + j) * 128 + (((q >> 2) ^ j) << 4) + (q & 3) * 4) = code;
+            if ((q & 3) == 0) s[16 * j] = static_cast<uint8_t>(digit_scale(e8, j));
+        }
     }
 }
 
-// Splits all rows of a product once for all CTAs that read them: 16 lanes per row and K-block.
-__global__ void __launch_bounds__(256) dg_few_split_kernel(const uint16_t *x, int64_t ldx, int rows, int kblocks,
+// Splits all rows of a product once for all CTAs that read them.
+template <int W>
+__global__ void __launch_bounds__(256) dg_few_split_kernel(const uint16_t *x, int64_t ldx, int rows, int k,
                                                            uint8_t *image, uint8_t *image_sf) {
+    constexpr int LANES = block_k(W) / 8;
     grid_dependency_wait();
     grid_launch_dependents();   // after the wait: the next kernel may read what was there before this one
-    const int unit = blockIdx.x * 16 + static_cast<int>(threadIdx.x >> 4);
-    const int q16 = threadIdx.x & 15;
-    const bool in = unit < rows * kblocks;
+    const int unit = blockIdx.x * (256 / LANES) + static_cast<int>(threadIdx.x) / LANES;
+    const int q = threadIdx.x % LANES;
+    const bool in = unit < rows * ((k + block_k(W) - 1) / block_k(W));
     const int kb = in ? unit / rows : 0, t = in ? unit % rows : 0;
-    const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(x + t * ldx + kb * 128 + q16 * 8));
-    uint2 hi, lo;
-    const uint32_t e8 = split_bf16(v, hi, lo);
-    if (in)
-        put_pieces(image + static_cast<int64_t>(kb) * image_units(rows) * 1024, image_sf + kb * 512, t, q16, hi, lo, e8);
+    const int at = kb * block_k(W) + q * 8;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (at < k) v = __ldcg(reinterpret_cast<const uint4 *>(x + t * ldx + at));
+    split_row<W>(v, image + static_cast<int64_t>(kb) * image_units(pieces_of(W), rows) * 1024,
+                 image_sf + static_cast<int64_t>(kb) * scale_blocks(W) * 512, t, q, in);
 }
 
 // The layer's routing, as every CTA of its kernels derives it from the ids (in shared
@@ -205,7 +272,7 @@ __host__ __device__ constexpr int segment_table_bytes(int pairs, int experts) {
 // Tables of segment_table_bytes at `tab`; called by all threads of a CTA, after some work of
 // its own if it has any (`id`: load of thread q's slot q, issued before that).
 __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids, int id, int pairs, int topk,
-                                                   int experts, int cap, int32_t *status) {
+                                                   int experts, int cap, int pieces, int32_t *status) {
     uint32_t *mask = reinterpret_cast<uint32_t *>(tab + 4);            // [experts][2] tokens of each expert
     uint16_t *start = reinterpret_cast<uint16_t *>(mask + 2 * experts);   // [experts] first entry
     uint16_t *seg0 = start + experts;                                     // [experts] first segment
@@ -237,7 +304,7 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
             const int c = __popc(mask[2 * e]) + __popc(mask[2 * e + 1]);
             n += c;
             segs += (c + cap - 1) / cap;
-            units += c / cap * image_units(cap) + image_units(c % cap);
+            units += c / cap * image_units(pieces, cap) + image_units(pieces, c % cap);
         }
         int in_n = n, in_su = segs | units << 16;
 #pragma unroll
@@ -256,7 +323,7 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
                 s.tokens[z] = static_cast<uint16_t>(t);
                 s.unit[z] = static_cast<uint16_t>(u);
                 first += t;
-                u += image_units(t);
+                u += image_units(pieces, t);
             }
         }
         if (lane == 31) { tab[0] = in_su & 0xFFFF; tab[1] = in_n; }
@@ -278,27 +345,27 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
 }
 
 // Images of all segments' tokens.  Blocks of grid.y take entries in turn, one K-block each.
+template <int W>
 __global__ void __launch_bounds__(256) dg_layer_split_kernel(const uint16_t *x, int64_t ldx, const int32_t *ids,
-                                                             int tokens, int topk, int experts, int cap, int kblocks,
+                                                             int tokens, int topk, int experts, int cap, int k,
                                                              uint8_t *image, uint8_t *image_sf) {
+    constexpr int LANES = block_k(W) / 8, ROWS = 256 / LANES;
     extern __shared__ int split_tab[];
     grid_dependency_wait();
     grid_launch_dependents();
     const int slot_id = threadIdx.x < tokens * topk ? __ldcg(ids + threadIdx.x) : -1;
-    const Segments s = build_segments(split_tab, ids, slot_id, tokens * topk, topk, experts, cap, nullptr);
-    const int q16 = threadIdx.x & 15, kb = blockIdx.x;
-    for (int at0 = blockIdx.y * 16; at0 < s.entries; at0 += gridDim.y * 16) {
-        const int at = at0 + static_cast<int>(threadIdx.x >> 4);
+    const Segments s = build_segments(split_tab, ids, slot_id, tokens * topk, topk, experts, cap, pieces_of(W), nullptr);
+    const int q = threadIdx.x % LANES, kb = blockIdx.x, kblocks = gridDim.x;
+    const int col = kb * block_k(W) + q * 8;
+    for (int at0 = blockIdx.y * ROWS; at0 < s.entries; at0 += gridDim.y * ROWS) {
+        const int at = at0 + static_cast<int>(threadIdx.x) / LANES;
         const bool in = at < s.entries;
-        const int row = in ? s.token[at] : 0;
-        const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(x + row * ldx + kb * 128 + q16 * 8));
-        uint2 hi, lo;
-        const uint32_t e8 = split_bf16(v, hi, lo);
-        if (in) {
-            const int z = s.of_entry[at];
-            put_pieces(image + (static_cast<int64_t>(s.unit[z]) * kblocks + kb * image_units(s.tokens[z])) * 1024,
-                       image_sf + (static_cast<int64_t>(z) * kblocks + kb) * 512, at - s.first[z], q16, hi, lo, e8);
-        }
+        const int row = in ? s.token[at] : 0, z = in ? s.of_entry[at] : 0;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (col < k) v = __ldcg(reinterpret_cast<const uint4 *>(x + row * ldx + col));
+        const int units = image_units(pieces_of(W), s.tokens[z]);
+        split_row<W>(v, image + (static_cast<int64_t>(s.unit[z]) * kblocks + kb * units) * 1024,
+                     image_sf + (static_cast<int64_t>(z) * kblocks + kb) * scale_blocks(W) * 512, at - s.first[z], q, in);
     }
 }
 
@@ -310,27 +377,29 @@ struct FewTile {
     int ntok;       // token columns (kDown: all tokens)
 };
 
-template <bool FP4, int HALVES, int MODE>
+template <int W, int HALVES, int MODE>
 __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     dg_few_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ FewArgs p) {
     constexpr int ROWS = HALVES * 128;
     constexpr int OUT = MODE == kUp ? 128 : ROWS;     // results per token and tile
     constexpr int NT = FewConfig::threads(HALVES, MODE);
     constexpr int FIRST_B = FewConfig::first_b(HALVES);
-    constexpr int SF = 4 + 4;                         // TMEM columns of a K-block's scales: weights', activations'
+    constexpr bool DIGITS = W == kFp4Packed;
+    constexpr int PIECES = pieces_of(W), SB = scale_blocks(W), BLOCK_K = block_k(W);
+    constexpr int SF = 4 * SB + 4 * SB;               // TMEM columns of a K-block's scales: weights', activations'
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     const int rank = static_cast<int>(cluster_ctarank());
     const int nsplit = static_cast<int>(cluster_nctarank());
     const int S = p.stages;
-    const int ncols = 2 * p.cap;
+    const int ncols = PIECES * p.cap;
     const int b_bytes = ncols * 128;
     uint8_t *smem_a = smem;
     uint8_t *smem_b = smem_a + S * HALVES * 16384;
     uint8_t *smem_sfa = smem_b + S * b_bytes;
-    uint8_t *smem_sfb = smem_sfa + S * HALVES * 512;
-    uint8_t *smem_end = smem_sfb + S * 512;
+    uint8_t *smem_sfb = smem_sfa + S * HALVES * SB * 512;
+    uint8_t *smem_end = smem_sfb + S * SB * 512;
     float *smem_out = reinterpret_cast<float *>(p.out_bytes ? smem_end : smem_a);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem_end + p.out_bytes);
     uint64_t *full_bar = bars;              // [S] weights and scales landed, pieces landed or written
@@ -374,7 +443,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     // waits that reads or writes memory.
     grid_launch_dependents();
     Segments seg = {};
-    if constexpr (MODE >= kUp) seg = build_segments(tab, p.ids, slot_id, pairs, p.topk, p.experts, p.cap, p.status);
+    if constexpr (MODE >= kUp) seg = build_segments(tab, p.ids, slot_id, pairs, p.topk, p.experts, p.cap, PIECES, p.status);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -412,21 +481,38 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
             }
 #pragma unroll
             for (int s = 1; s < 8; s <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));   // a group of 32
-            const uint32_t e8 = max(m >> 23, 11u);
-            const float inv = inverse_scale(e8);
-            uint32_t hi, lo;
-            split4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv, hi, lo);
-            const int kblocks = p.inner >> 7, kb = tile.row0 >> 7;   // this tile is one K-block of kDown
-            uint8_t *image = p.out_image +
-                (static_cast<int64_t>(seg.unit[tile.seg]) * kblocks + kb * image_units(tile.ntok)) * 1024;
-            const uint32_t r = 2 * t, at = (lane & 3) * 4;
-            *reinterpret_cast<uint32_t *>(image + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + at) = hi;
-            *reinterpret_cast<uint32_t *>(image + (r + 1) * 128 + (((lane >> 2) ^ ((r + 1) & 7)) << 4) + at) = lo;
-            if ((lane & 7) == 0) {
-                uint8_t *sf = p.out_image_sf + (static_cast<int64_t>(tile.seg) * kblocks + kb) * 512 + sf_word(r) * 4 +
-                              (lane >> 3);
-                sf[0] = static_cast<uint8_t>(hi_scale(e8));
-                sf[16] = static_cast<uint8_t>(lo_scale(e8));
+            // this tile is a K-block of kDown, or half of one
+            const int kblocks = (p.inner + BLOCK_K - 1) / BLOCK_K, kb = tile.row0 / BLOCK_K, k0 = tile.row0 % BLOCK_K;
+            uint8_t *image = p.out_image + (static_cast<int64_t>(seg.unit[tile.seg]) * kblocks +
+                                            kb * image_units(PIECES, tile.ntok)) * 1024;
+            uint8_t *sf = p.out_image_sf + ((static_cast<int64_t>(tile.seg) * kblocks + kb) * SB + k0 / 128) * 512 +
+                          sf_word(PIECES * t) * 4 + (lane >> 3);
+            const uint32_t r = PIECES * t;
+            if constexpr (DIGITS) {
+                const uint32_t e8 = max(m >> 23, kLeastDigitExponent);
+                const float inv = inverse_digit_scale(e8);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[c] *= inv;
+                const uint32_t at = k0 / 2 + lane * 2;   // byte of the row
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t code = next_digits(o);
+                    *reinterpret_cast<uint16_t *>(image + (r + j) * 128 + (((at >> 4) ^ j) << 4) + (at & 15)) =
+                        static_cast<uint16_t>(code);
+                    if ((lane & 7) == 0) sf[16 * j] = static_cast<uint8_t>(digit_scale(e8, j));
+                }
+            } else {
+                const uint32_t e8 = max(m >> 23, 11u);
+                const float inv = inverse_scale(e8);
+                uint32_t hi, lo;
+                split4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv, hi, lo);
+                const uint32_t at = (lane & 3) * 4;
+                *reinterpret_cast<uint32_t *>(image + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + at) = hi;
+                *reinterpret_cast<uint32_t *>(image + (r + 1) * 128 + (((lane >> 2) ^ ((r + 1) & 7)) << 4) + at) = lo;
+                if ((lane & 7) == 0) {
+                    sf[0] = static_cast<uint8_t>(hi_scale(e8));
+                    sf[16] = static_cast<uint8_t>(lo_scale(e8));
+                }
             }
         } else if (n < p.rows) {
             if (p.f32) {
@@ -502,15 +588,16 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                 else issued |= 1u << slot;
                 if ((issued >> slot & 1u) && elect_one()) {
                     const int e = MODE == kDown ? seg.expert[z] : tile.expert;
-                    const int slice = FP4 ? kb : kb >> 2;
+                    const int slice = W == kFp8 ? kb >> 2 : kb * SB;
+                    const int slices = min(SB, p.slices - slice);
                     const uint32_t *sf = p.sf + e * p.sf_expert + static_cast<int64_t>(slice) * p.sf_ld;
                     uint32_t sf_bytes[HALVES];
-                    uint32_t bytes = HALVES * (FP4 ? 8192 : 16384);
+                    uint32_t bytes = HALVES * (W == kFp4 ? 8192 : 16384);
 #pragma unroll
                     for (int h = 0; h < HALVES; ++h) {
                         const int left = MODE == kUp ? 128 : p.sf_ld - (tile.row0 + h * 128);
                         sf_bytes[h] = left >= 128 ? 512u : left > 0 ? 4u * static_cast<uint32_t>(left) : 0u;
-                        bytes += sf_bytes[h];
+                        bytes += sf_bytes[h] * slices;
                     }
                     mbar_arrive_expect_tx(&full_bar[slot], bytes);
 #pragma unroll
@@ -519,8 +606,11 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                         // (a half past the last row reads zeros or the next expert's rows; unused)
                         tma_load_3d(smem_a + (slot * HALVES + h) * 16384, &tm_w, &full_bar[slot], kb * 128,
                                     box_row(tile, e, h), 0);
-                        if (sf_bytes[h])
-                            bulk_load(smem_sfa + (slot * HALVES + h) * 512, sf + r, sf_bytes[h], &full_bar[slot]);
+#pragma unroll
+                        for (int b = 0; b < SB; ++b)
+                            if (sf_bytes[h] && b < slices)
+                                bulk_load(smem_sfa + ((slot * HALVES + h) * SB + b) * 512,
+                                          sf + static_cast<int64_t>(b) * p.sf_ld + r, sf_bytes[h], &full_bar[slot]);
                     }
                 }
                 __syncwarp();
@@ -548,7 +638,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         uint32_t phase = 0, acc_phase = 0;
         const uint64_t a_base = make_desc_kmajor_sw128(smem_u32(smem_a + h * 16384));
         const uint64_t b_base = make_desc_kmajor_sw128(smem_u32(smem_b));
-        const uint64_t sfa_base = make_desc_sf_32x128b(smem_u32(smem_sfa + h * 512));
+        const uint64_t sfa_base = make_desc_sf_32x128b(smem_u32(smem_sfa + h * SB * 512));
         const uint64_t sfb_base = make_desc_sf_32x128b(smem_u32(smem_sfb));
         const uint32_t sf0 = sf_tmem + 2 * h * SF;
         for (int w = first_tile; w < num_tiles; w += tile_step) {
@@ -564,21 +654,38 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                 const uint32_t d_tmem = tmem_base + (acc * HALVES + h) * ncols;
                 // columns in use: the tokens', rounded up to the MMA's step of 16
                 const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
-                const uint32_t idesc = make_idesc_mxf8(128, (2 * tok + 15) / 16 * 16, 0, 0) | (FP4 ? 5u << 7 : 0u);   // A: E2M1 or E4M3
+                const uint32_t cols = (PIECES * tok + 15) / 16 * 16;
+                const uint32_t idesc = DIGITS ? make_idesc_mxf4(128, cols, 0, 0)
+                                              : make_idesc_mxf8(128, cols, 0, 0) | (W == kFp4 ? 5u << 7 : 0u);   // A: E2M1
                 for (int j = 0; j < n; ++j, ++g) {
                     if (!mbar_wait_warp(&full_bar[slot], phase, ctl, DG_DEV_TIMEOUT)) goto mma_done;
                     tc_fence_after_sync();
                     if (elect_one()) {
                         const uint32_t sf = sf0 + (g & 1) * SF;
-                        tc_cp_32x128b_warpx4(sf, sfa_base + static_cast<uint64_t>(slot * HALVES * 32));
-                        tc_cp_32x128b_warpx4(sf + 4, sfb_base + static_cast<uint64_t>(slot * 32));
+#pragma unroll
+                        for (int b = 0; b < SB; ++b) {
+                            tc_cp_32x128b_warpx4(sf + 4 * b, sfa_base + static_cast<uint64_t>((slot * HALVES * SB + b) * 32));
+                            tc_cp_32x128b_warpx4(sf + 4 * SB + 4 * b, sfb_base + static_cast<uint64_t>((slot * SB + b) * 32));
+                        }
                         const uint64_t a_desc = a_base + static_cast<uint64_t>(slot * HALVES * 1024);
                         const uint64_t b_desc = b_base + static_cast<uint64_t>(slot * (b_bytes >> 4));
+                        if constexpr (DIGITS) {
+                            const int mmas = kb0 + j == p.kblocks - 1 ? p.last_mmas : 4;
 #pragma unroll
-                        for (uint32_t k = 0; k < 4; ++k) {
-                            // scale byte: the activations' and FP4 weights' k-th 32 K, FP8 weights' 128-K block
-                            const uint32_t id = idesc | (k << 4) | ((FP4 ? k : static_cast<uint32_t>((kb0 + j) & 3)) << 29);
-                            tc_mma_mxf8(d_tmem, a_desc + 2 * k, b_desc + 2 * k, id, sf, sf + 4, (j | k) != 0);
+                            for (uint32_t k = 0; k < 4; ++k) {
+                                const uint32_t byte = (k & 1) * 2;   // of the slice's scale words
+                                if (k < 2 || mmas == 4)
+                                    tc_mma_mxf4(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc | (byte << 4) | (byte << 29),
+                                                sf + 4 * (k >> 1), sf + 4 * SB + 4 * (k >> 1), (j | k) != 0);
+                            }
+                        } else {
+#pragma unroll
+                            for (uint32_t k = 0; k < 4; ++k) {
+                                // scale byte: the activations' and FP4 weights' k-th 32 K, FP8 weights' 128-K block
+                                const uint32_t id =
+                                    idesc | (k << 4) | ((W == kFp4 ? k : static_cast<uint32_t>((kb0 + j) & 3)) << 29);
+                                tc_mma_mxf8(d_tmem, a_desc + 2 * k, b_desc + 2 * k, id, sf, sf + 4, (j | k) != 0);
+                            }
                         }
                         tc_commit(&empty_bar[slot]);
                     }
@@ -610,22 +717,20 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
             // implies that up to block g - teams - S.
             const int teams = S < FewConfig::b_warps(MODE) ? S : FewConfig::b_warps(MODE);
             const int bw = warp - FIRST_B;
-            const int q16 = lane & 15, sub = lane >> 4;   // two tokens at a time, 16 lanes each
+            constexpr int LANES = BLOCK_K / 8, AT_ONCE = 32 / LANES;   // of a row, and rows of a warp
+            const int q = lane % LANES;
             int g = 0;   // K-blocks of the tiles before
             for (int w = first_tile; w < num_tiles && bw < teams; w += tile_step, g += k_end - k_begin) {
                 for (int i = (bw + teams - g % teams) % teams; i < k_end - k_begin; i += teams) {
                     const int slot = (g + i) % S;
                     if (!mbar_wait_warp(&empty_bar[slot], (((g + i) / S) & 1) ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
-                    const int kb = k_begin + i;
-                    for (int t0 = 0; t0 < p.tokens; t0 += 2) {
-                        const int t = t0 + sub;
+                    const int at = (k_begin + i) * BLOCK_K + q * 8;
+                    for (int t0 = 0; t0 < p.tokens; t0 += AT_ONCE) {
+                        const int t = t0 + lane / LANES;
                         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (t < p.tokens)
-                            v = __ldcg(reinterpret_cast<const uint4 *>(p.x + t * p.ldx + kb * 128 + q16 * 8));
-                        uint2 hi, lo;
-                        const uint32_t e8 = split_bf16(v, hi, lo);
-                        if (t < p.tokens)
-                            put_pieces(smem_b + slot * b_bytes, smem_sfb + slot * 512, t, q16, hi, lo, e8);
+                        if (t < p.tokens && (!DIGITS || at < p.slices * 128))
+                            v = __ldcg(reinterpret_cast<const uint4 *>(p.x + t * p.ldx + at));
+                        split_row<W>(v, smem_b + slot * b_bytes, smem_sfb + slot * SB * 512, t, q, t < p.tokens);
                         __syncwarp();
                     }
                     fence_proxy_async_smem();
@@ -644,14 +749,15 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                     if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
                     if (elect_one()) {
                         const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
-                        const int units = image_units(tok);
+                        const int units = image_units(PIECES, tok);
                         const int64_t before = MODE >= kUp ? seg.unit[z] : 0;
-                        const uint32_t sf_bytes = tok < 16 ? 32u * tok : 512u;
+                        const uint32_t sf_bytes = DIGITS ? 1024u : tok < 16 ? 32u * tok : 512u;
                         mbar_arrive_expect_tx(&full_bar[slot], units * 1024 + sf_bytes);
                         bulk_load(smem_b + slot * b_bytes, p.image + (before * p.kblocks + kb * units) * 1024, units * 1024,
                                   &full_bar[slot]);
-                        bulk_load(smem_sfb + slot * 512, p.image_sf + (static_cast<int64_t>(z) * p.kblocks + kb) * 512,
-                                  sf_bytes, &full_bar[slot]);
+                        bulk_load(smem_sfb + slot * SB * 512,
+                                  p.image_sf + (static_cast<int64_t>(z) * p.kblocks + kb) * SB * 512, sf_bytes,
+                                  &full_bar[slot]);
                     }
                     __syncwarp();
                     if (++kb == p.kblocks) { kb = 0; ++z; }
@@ -689,19 +795,29 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                 }
             }
         };
-        // Sums of columns 2 t0 .. 2 t0 + 15 in pairs: 8 tokens' results at this thread's operand rows
-        auto read8 = [&](int t0, float (&r)[HALVES][8]) {
-            uint32_t v[HALVES][16];
+        // 8 tokens' results from t0 at this thread's operand rows: the sums of their columns
+        auto read8 = [&](int t0, int n, float (&r)[HALVES][8]) {
+            constexpr int AT_ONCE = 16 / PIECES;   // tokens of 16 columns
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h)
-                tmem_ld_32x32b_x16(tmem_base + ((quad * 32) << 16) + (acc * HALVES + h) * ncols + 2 * t0, v[h]);
-            tmem_ld_wait();
+            for (int j0 = 0; j0 < 8; j0 += AT_ONCE) {
+                if (j0 >= n) break;
+                uint32_t v[HALVES][16];
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h) {
-                reg_fence16(v[h]);
+                for (int h = 0; h < HALVES; ++h)
+                    tmem_ld_32x32b_x16(tmem_base + ((quad * 32) << 16) + (acc * HALVES + h) * ncols + PIECES * (t0 + j0),
+                                       v[h]);
+                tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    r[h][j] = __uint_as_float(v[h][2 * j]) + __uint_as_float(v[h][2 * j + 1]);
+                for (int h = 0; h < HALVES; ++h) {
+                    reg_fence16(v[h]);
+#pragma unroll
+                    for (int j = 0; j < AT_ONCE; ++j) {
+                        float sum = __uint_as_float(v[h][PIECES * j + PIECES - 1]);   // the smallest first
+#pragma unroll
+                        for (int c = PIECES - 2; c >= 0; --c) sum += __uint_as_float(v[h][PIECES * j + c]);
+                        r[h][j0 + j] = sum;
+                    }
+                }
             }
         };
         auto release = [&] {   // the accumulators are read
@@ -739,7 +855,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                     for (int t0 = 0; t0 < tok; t0 += 8) {
                         float r[HALVES][8];
                         uint32_t y[HALVES][8], at[8];
-                        read8(t0, r);
+                        read8(t0, tok - t0, r);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             if (t0 + j >= tok) break;
@@ -797,8 +913,8 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                 pushed = true;
                 for (int t0 = 0; t0 < tile.ntok; t0 += 8) {
                     float r[HALVES][8];
-                    read8(t0, r);
                     const int n = min(8, tile.ntok - t0);
+                    read8(t0, n, r);
                     float *out = smem_out + buf * 8 * OUT;
                     if (nsplit > 1) {
                         push(tile, t0, n, r);

@@ -352,7 +352,29 @@ __device__ __forceinline__ void st_shared_cluster_f32(uint32_t cluster_addr, flo
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
-// ----------------------------------------------------------------- E4M3 conversions
+// ----------------------------------------------------------------- E4M3 and E2M1 conversions
+
+// Two floats to E2M1, round to nearest even (a in the low nibble).
+__device__ __forceinline__ uint32_t cvt_e2m1x2(float a, float b) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 t;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
+        "cvt.u32.u8 %0, t;\n\t}"
+        : "=r"(r)
+        : "f"(b), "f"(a));
+    return r;
+}
+
+// Two E2M1 codes to the f16 pair of the same values (exact).
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t codes) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 t;\n\t"
+        "cvt.u8.u32 t, %1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+        : "=r"(r)
+        : "r"(codes));
+    return r;
+}
 
 // Two floats to E4M3, round to nearest even (a in the low byte).
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float a, float b) {
@@ -506,6 +528,20 @@ __device__ __forceinline__ void tc_mma_mxf8(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
+// The same for packed FP4 (E2M1) operands, K = 64 a step: rows of two codes a byte, two scales
+// (bytes 0, 1 or 2, 3 of the TMEM words, by the scale-factor ids 0 or 2).
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
+
 // D(tmem) (+)= A(smem) * B(smem)^T without scales (FP8 inputs, FP32 accumulate).
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                           uint32_t idesc, uint32_t accumulate) {
@@ -602,6 +638,11 @@ __host__ __device__ constexpr uint32_t make_idesc_mxf8(uint32_t m, uint32_t n, u
            | (1u << 23)               // scale format: UE8M0
            | ((m >> 4) << 24)         // M / 16
            | ((sf_id_a & 3u) << 29);  // A scale-factor byte
+}
+
+// Instruction descriptor, packed FP4 x FP4 (E2M1 both, K = 64), UE8M0 scales.
+__host__ __device__ constexpr uint32_t make_idesc_mxf4(uint32_t m, uint32_t n, uint32_t sf_id_a, uint32_t sf_id_b) {
+    return make_idesc_mxf8(m, n, sf_id_a, sf_id_b) | (1u << 7) | (1u << 10);   // A and B format: E2M1
 }
 
 // Instruction descriptor, FP8 x FP8 (E4M3 both) without scales, FP32 accumulate.

@@ -423,7 +423,10 @@ int64_t dg_k_grouped_packed_sf_rows(const int *ks, int num_groups);
  *        initialisation and do not outlive the call.  Calls that may run at the same
  *        time need one each.
  *   A row that holds an infinity or a NaN gives NaN in its row of D; other rows
- *   are not affected.  Row i of D is the same bit for bit whatever m is.
+ *   are not affected.  Row i of D is the same bit for bit whatever the other rows
+ *   and (FP4: up to 8, and above 8) their number are.  Activations below 2^-20 of
+ *   the largest of their 32 along K (and, in FP4 calls of up to 8 rows, below 2^-128) may
+ *   count as zero.
  */
 int64_t dg_bf16_gemv_workspace_bytes(int m, int n, int k);
 dg_status dg_bf16_fp4_gemv_nt(const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,

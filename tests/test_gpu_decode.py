@@ -89,13 +89,18 @@ def test_gemv_rows_do_not_depend_on_the_batch(fmt):
     codes, s, _ = D.quantize(torch.randn(n, k, generator=g), fmt)
     codes, sf = codes.cuda(), D.pack_scales(s)
     full = _gemv(fmt, a, codes, sf, True)
-    for m in (1, 2, 8, 9, 16, 17, 32, 33, 63):
-        assert torch.equal(_gemv(fmt, a[:m], codes, sf, True), full[:m]), m
-        assert torch.equal(_gemv(fmt, a[64 - m:], codes, sf, True), full[64 - m:]), m
+    few = full
+    if fmt == "fp4":                                # up to 8 rows: other pieces
+        few = torch.cat([_gemv(fmt, a[i:i + 8], codes, sf, True) for i in range(0, 64, 8)])
+    for m in (1, 2, 3, 7, 8, 9, 16, 17, 32, 33, 63):
+        want = few if m <= 8 else full
+        assert torch.equal(_gemv(fmt, a[:m], codes, sf, True), want[:m]), m
+        assert torch.equal(_gemv(fmt, a[64 - m:], codes, sf, True), want[64 - m:]), m
 
 
 @pytest.mark.parametrize("fmt", ["fp4", "fp8"])
-def test_gemv_extreme_values(fmt):
+@pytest.mark.parametrize("few", [False, True])
+def test_gemv_extreme_values(fmt, few):
     """Zero rows, groups of very different magnitude, the ends of the scale range, and
     non-finite rows, which stay alone."""
     m, n, k = 10, 256, 512
@@ -109,6 +114,9 @@ def test_gemv_extreme_values(fmt):
     a[6, 7] = 3e4          # one large channel in its group
     a[7] = 2.0 ** -133       # the smallest bf16
     a = a.bfloat16()
+    run = (lambda x: torch.cat([_gemv(fmt, x[:5].cuda(), codes.cuda(), sf, True),      # 5 rows at a time
+                                _gemv(fmt, x[5:].cuda(), codes.cuda(), sf, True)]).cpu().double()) if few else \
+        (lambda x: _gemv(fmt, x.cuda(), codes.cuda(), sf, True).cpu().double())
     codes, s, gran = D.quantize(torch.randn(n, k, generator=g), fmt)
     s[::4] *= 2.0 ** -100
     s[1::4] *= 2.0 ** 90
@@ -116,7 +124,10 @@ def test_gemv_extreme_values(fmt):
     # rows whose results leave the FP32 range are kept out of the comparison
     ref, tol = a.double() @ w.t(), D.product_bound(a.double(), w)
     sane = (ref.abs() < 1e37) & (a.double().abs() @ w.abs().t() < 1e38)
-    d = _gemv(fmt, a.cuda(), codes.cuda(), D.pack_scales(s), True).cpu().double()
+    if few and fmt == "fp4":
+        tol = tol + 2.0 ** -128 * w.abs().sum(1)      # the digits' absolute bound, an element
+    sf = D.pack_scales(s)
+    d = run(a)
     # sums below the normal range may lose their last bits
     over = (d - ref).abs() - tol - 2.0 ** -22 * ref.abs() - 2.0 ** -126
     assert (over[sane] <= 0).all()
@@ -125,7 +136,7 @@ def test_gemv_extreme_values(fmt):
     bad[0, 3] = float("nan")
     bad[8, 100] = float("inf")
     bad[9, 511] = float("-inf")
-    e = _gemv(fmt, bad.cuda(), codes.cuda(), D.pack_scales(s), True).cpu().double()
+    e = run(bad)
     assert torch.isnan(e[[0, 8, 9]]).all()
     assert torch.allclose(e[1:8], d[1:8], rtol=0.0, atol=0.0, equal_nan=True)   # row 2 overflows in places
 
