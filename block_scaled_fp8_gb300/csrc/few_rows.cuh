@@ -269,6 +269,8 @@ __host__ __device__ constexpr int segment_table_bytes(int pairs, int experts) {
     return (16 + 12 * experts + 14 * pairs + 15) / 16 * 16;
 }
 
+// (The loops are not unrolled: a kernel's first pass over its code waits for the code, from
+// HBM where the weights have pushed it out of L2.)
 // Tables of segment_table_bytes at `tab`; called by all threads of a CTA, after some work of
 // its own if it has any (`id`: load of thread q's slot q, issued before that).
 __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids, int id, int pairs, int topk,
@@ -285,8 +287,11 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
     s.tokens = s.first + pairs;
     s.unit = s.tokens + pairs;
     const int lane = threadIdx.x & 31;
+    const int shift = __ffs(cap) - 1;   // (a power of two; runtime divisions would cost over a microsecond here)
+#pragma unroll 1
     for (int e = threadIdx.x; e < 2 * experts; e += blockDim.x) mask[e] = 0u;
     __syncthreads();
+#pragma unroll 1
     for (int q = threadIdx.x; q < pairs; q += blockDim.x) {
         const int e = q == static_cast<int>(threadIdx.x) ? id : __ldcg(ids + q);
         const bool ok = e >= 0 && e < experts;
@@ -298,13 +303,14 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
     __syncthreads();
     if (threadIdx.x < 32) {
         // lane l counts experts l * per .., one scan over the lanes, then it lays out its segments
-        const int per = (experts + 31) / 32;
+        const int per = (experts + 31) / 32, full = image_units(pieces, cap);
         int n = 0, segs = 0, units = 0;
+#pragma unroll 1
         for (int e = lane * per; e < min(experts, (lane + 1) * per); ++e) {
             const int c = __popc(mask[2 * e]) + __popc(mask[2 * e + 1]);
             n += c;
-            segs += (c + cap - 1) / cap;
-            units += c / cap * image_units(pieces, cap) + image_units(pieces, c % cap);
+            segs += (c + cap - 1) >> shift;
+            units += (c >> shift) * full + image_units(pieces, c & (cap - 1));
         }
         int in_n = n, in_su = segs | units << 16;
 #pragma unroll
@@ -313,9 +319,11 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
             if (lane >= d) { in_n += u; in_su += v; }
         }
         int first = in_n - n, z = (in_su & 0xFFFF) - segs, u = (in_su >> 16) - units;
+#pragma unroll 1
         for (int e = lane * per; e < min(experts, (lane + 1) * per); ++e) {
             start[e] = static_cast<uint16_t>(first);
             seg0[e] = static_cast<uint16_t>(z);
+#pragma unroll 1
             for (int left = __popc(mask[2 * e]) + __popc(mask[2 * e + 1]); left > 0; left -= cap, ++z) {
                 const int t = min(left, cap);
                 s.expert[z] = static_cast<uint16_t>(e);
@@ -329,6 +337,7 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
         if (lane == 31) { tab[0] = in_su & 0xFFFF; tab[1] = in_n; }
     }
     __syncthreads();
+#pragma unroll 1
     for (int q = threadIdx.x; q < pairs; q += blockDim.x) {
         const int e = s_ids[q], t = q / topk;
         if (e == 0xFFFF) continue;
@@ -336,7 +345,7 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
         const uint32_t below = (1u << (t & 31)) - 1u;
         const int at = t < 32 ? __popc(mask[2 * e] & below) : __popc(mask[2 * e]) + __popc(mask[2 * e + 1] & below);
         s.token[start[e] + at] = static_cast<uint16_t>(t);
-        s.of_entry[start[e] + at] = static_cast<uint16_t>(seg0[e] + at / cap);
+        s.of_entry[start[e] + at] = static_cast<uint16_t>(seg0[e] + (at >> shift));
     }
     __syncthreads();
     s.count = tab[0];
@@ -351,6 +360,10 @@ __global__ void __launch_bounds__(256) dg_layer_split_kernel(const uint16_t *x, 
                                                              uint8_t *image, uint8_t *image_sf) {
     constexpr int LANES = block_k(W) / 8, ROWS = 256 / LANES;
     extern __shared__ int split_tab[];
+    // x's part to L2 meanwhile (which makes no difference to what is read later)
+    if (blockIdx.y == 0 && static_cast<int>(threadIdx.x) < tokens)
+        prefetch_l2_bulk(x + threadIdx.x * ldx + blockIdx.x * block_k(W),
+                         2 * min(block_k(W), k - static_cast<int>(blockIdx.x) * block_k(W)));
     grid_dependency_wait();
     grid_launch_dependents();
     const int slot_id = threadIdx.x < tokens * topk ? __ldcg(ids + threadIdx.x) : -1;
