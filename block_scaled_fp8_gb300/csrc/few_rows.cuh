@@ -304,23 +304,30 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
     if (threadIdx.x < 32) {
         // lane l counts experts l * per .., one scan over the lanes, then it lays out its segments
         const int per = (experts + 31) / 32, full = image_units(pieces, cap);
+        // (trip counts are the same in all lanes: shuffles after a loop that could diverge take
+        // 270 cycles each)
         int n = 0, segs = 0, units = 0;
 #pragma unroll 1
-        for (int e = lane * per; e < min(experts, (lane + 1) * per); ++e) {
-            const int c = __popc(mask[2 * e]) + __popc(mask[2 * e + 1]);
+        for (int i = 0; i < per; ++i) {
+            const int e = lane * per + i;
+            const int c = e < experts ? __popc(mask[2 * e]) + __popc(mask[2 * e + 1]) : 0;
             n += c;
             segs += (c + cap - 1) >> shift;
             units += (c >> shift) * full + image_units(pieces, c & (cap - 1));
         }
+        __syncwarp();
         int in_n = n, in_su = segs | units << 16;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int u = __shfl_up_sync(0xFFFFFFFFu, in_n, d), v = __shfl_up_sync(0xFFFFFFFFu, in_su, d);
-            if (lane >= d) { in_n += u; in_su += v; }
+            in_n += lane >= d ? u : 0;
+            in_su += lane >= d ? v : 0;
         }
         int first = in_n - n, z = (in_su & 0xFFFF) - segs, u = (in_su >> 16) - units;
 #pragma unroll 1
-        for (int e = lane * per; e < min(experts, (lane + 1) * per); ++e) {
+        for (int i = 0; i < per; ++i) {
+            const int e = lane * per + i;
+            if (e >= experts) continue;
             start[e] = static_cast<uint16_t>(first);
             seg0[e] = static_cast<uint16_t>(z);
 #pragma unroll 1
