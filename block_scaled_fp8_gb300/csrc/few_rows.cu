@@ -45,7 +45,7 @@ template <int W, int HALVES, int MODE>
 cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles,
                    int num_sms, cudaStream_t stream) {
     const int tables = MODE < kUp ? 0 : segment_table_bytes(a.tokens * a.topk, a.experts);
-    a.out_bytes = FewConfig::out_bytes(HALVES, MODE, MODE == kUp ? a.cap : a.tokens, plan.split);
+    a.out_bytes = FewConfig::out_bytes(HALVES, MODE, is_up(MODE) ? a.cap : a.tokens, plan.split);
     // (split results of more than 8 KB go to the ring: one more wait, but no stage less)
     if (plan.split > 1 && a.out_bytes > 8192) a.out_bytes = 0;
     a.ahead = kAhead / (HALVES * (W == kFp4 ? 8192 : 16384)) / plan.occ;
@@ -90,7 +90,7 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     cfg.attrs = attr;
     cfg.numAttrs = plan.split > 1 ? 2 : 1;
     host_set_last_config(HALVES * 128, pieces_of(W) * a.cap, stages, grid, MODE < kUp ? 3 : 5,
-                         MODE == kGemv ? 1 : MODE == kGemvPre ? 2 : 3);
+                         MODE == kGemv ? 1 : MODE < kDown ? 2 : a.launches);
     return cudaLaunchKernelEx(&cfg, kernel, map, a);
 }
 
@@ -99,8 +99,8 @@ cudaError_t launch_fmt(int w, const CUtensorMap &map, FewArgs &a, const Plan &pl
                        cudaStream_t stream) {
     if (w == kFp8) return launch<kFp8, HALVES, MODE>(map, a, plan, max_tiles, num_sms, stream);
     if (w == kFp4Packed) return launch<kFp4Packed, HALVES, MODE>(map, a, plan, max_tiles, num_sms, stream);
-    // (the fewest rows, kGemv, always have their FP4 weights packed)
-    if constexpr (MODE != kGemv) return launch<kFp4, HALVES, MODE>(map, a, plan, max_tiles, num_sms, stream);
+    // (rows few enough for a kernel to split them itself have their FP4 weights packed)
+    if constexpr (!splits_itself(MODE)) return launch<kFp4, HALVES, MODE>(map, a, plan, max_tiles, num_sms, stream);
     return cudaErrorInvalidValue;
 }
 
@@ -300,13 +300,6 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     uint8_t *x_image = p.workspace, *h_image = x_image + bounds.image(p.h);
     uint8_t *x_sf = h_image + bounds.image(p.i), *h_sf = x_sf + bounds.scales(p.h);
     const int kh = static_cast<int>(bounds.blocks(p.h)), ki = static_cast<int>(bounds.blocks(p.i));
-    const int rows = 256 * 8 / block_k(w);
-    Dependent split(dim3(static_cast<unsigned>(kh), static_cast<unsigned>(cdiv(pairs, 4 * rows))),
-                    segment_table_bytes(pairs, p.experts), stream);
-    cudaError_t e = cudaLaunchKernelEx(&split.cfg,
-                                       w == kFp4Packed ? dg_layer_split_kernel<kFp4Packed> : dg_layer_split_kernel<kFp8>,
-                                       p.x, p.ldx, p.ids, p.t, p.topk, p.experts, cap, p.h, x_image, x_sf);
-    if (e != cudaSuccess) return e;
     FewArgs a = {};
     a.tokens = p.t;
     a.cap = cap;
@@ -341,7 +334,28 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     up.halves = 2;
     up.occ = 1;
     up.split = choose_split(up_tiles, kh, up.occ, num_sms, false);
-    e = launch_fmt<2, kUp>(w, map1, a, up, up_tiles, num_sms, stream);
+    // With no more tokens than experts, counting a token once per slot, the up kernel splits x
+    // itself, a launch less: 1 token, top 8 of 64 experts, 7168 x 2048 FP4 40.6 us so and 40.8 us
+    // with the split kernel, FP8 (of 32) 61.8 and 63.2 us, 2 tokens, top 2 of 8, 1024 x 512 12.8
+    // and 13.3 us.  With more its own splitting bounds it: 8 tokens, top 4 of 16 experts, 7168 x
+    // 2048 FP4 71 us so and 66 us with the split kernel.
+    cudaError_t e;
+    if (pairs <= p.experts) {
+        a.x = p.x;
+        a.ldx = p.ldx;
+        a.launches = 2;
+        e = launch_fmt<2, kUpSelf>(w, map1, a, up, up_tiles, num_sms, stream);
+    } else {
+        const int rows = 256 * 8 / block_k(w);
+        Dependent split(dim3(static_cast<unsigned>(kh), static_cast<unsigned>(cdiv(pairs, 4 * rows))),
+                        segment_table_bytes(pairs, p.experts), stream);
+        e = cudaLaunchKernelEx(&split.cfg,
+                               w == kFp4Packed ? dg_layer_split_kernel<kFp4Packed> : dg_layer_split_kernel<kFp8>,
+                               p.x, p.ldx, p.ids, p.t, p.topk, p.experts, cap, p.h, x_image, x_sf);
+        if (e != cudaSuccess) return e;
+        a.launches = 3;
+        e = launch_fmt<2, kUp>(w, map1, a, up, up_tiles, num_sms, stream);
+    }
     if (e != cudaSuccess) return e;
     // down: K runs over the segments
     a.row_tiles = down_tiles;

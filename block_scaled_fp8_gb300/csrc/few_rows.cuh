@@ -37,15 +37,15 @@
 // FP32 partial results into the shared memory of the CTA that puts them out, which adds them
 // in rank order: no workspace, no atomics, a fixed order, and one cluster barrier.
 //
-// Where the pieces come from: kGemv, for the fewest rows, splits the activations itself,
-// four warps taking K-blocks in turn.  The other modes read an image of the narrow
+// Where the pieces come from: kGemv and kUpSelf, for the fewest rows, split the activations
+// themselves, four warps taking K-blocks in turn.  The other modes read an image of the narrow
 // operand that is already in the shared-memory form of each K-block (rows of 128 bytes
 // in 128-byte swizzle, and the scale words in tcgen05.cp order), two bulk copies a block:
 //   kGemvPre  dg_few_split_kernel has written the image of all rows.
 //   kUp       the gate and up rows of one expert (HALVES = 2) for a segment, up to `cap`
 //           of the tokens routed to it; dg_layer_split_kernel has written the segments'
 //           images.  The epilogue is w silu(g) u (w the routing weight), split again
-//           and written as the image that kDown reads.
+//           and written as the image that kDown reads.  kUpSelf: the same without an image.
 //   kDown     K runs over all segments; the accumulators of a segment are added to the
 //           FP32 results of its tokens, columns of their own in TMEM, while the next
 //           segment's products run.
@@ -59,7 +59,10 @@
 
 namespace dg {
 
-enum FewMode : int { kGemv = 0, kGemvPre = 1, kUp = 2, kDown = 3 };
+enum FewMode : int { kGemv = 0, kGemvPre = 1, kUp = 2, kUpSelf = 3, kDown = 4 };
+// Modes whose CTAs split the activations themselves.
+__host__ __device__ constexpr bool splits_itself(int mode) { return mode == kGemv || mode == kUpSelf; }
+__host__ __device__ constexpr bool is_up(int mode) { return mode == kUp || mode == kUpSelf; }
 
 // The weights' form.
 enum FewFormat : int {
@@ -73,7 +76,7 @@ __host__ __device__ constexpr int scale_blocks(int w) { return w == kFp4Packed ?
 __host__ __device__ constexpr int block_k(int w) { return w == kFp4Packed ? 256 : 128; }
 
 struct FewArgs {
-    const uint16_t *x;      // kGemv: bf16 activations
+    const uint16_t *x;      // kGemv, kUpSelf: bf16 activations
     int64_t ldx;
     const uint8_t *image;   // the other modes: the narrow operand's image, and its scale blocks
     const uint8_t *image_sf;
@@ -107,12 +110,13 @@ struct FewArgs {
     int32_t *status;
     uint64_t timeout_ns;
     uint32_t debug_flags;
+    int launches;           // kernels of the call (host only)
 };
 
 struct FewConfig {
     static constexpr int kFirstEpi = 2;
     static constexpr int first_b(int halves) { return halves == 2 ? 7 : 6; }
-    static constexpr int b_warps(int mode) { return mode == kGemv ? 4 : 1; }
+    static constexpr int b_warps(int mode) { return splits_itself(mode) ? 4 : 1; }
     static constexpr int threads(int halves, int mode) { return 32 * (first_b(halves) + b_warps(mode)); }
     static constexpr int kAlign = 1024;
     static constexpr int kBarBytes = 512;
@@ -123,9 +127,9 @@ struct FewConfig {
     // Two buffers of 8 tokens' FP32 results; of a split tile, what this CTA puts out (rows of
     // 32 items of 4 results, shared out to the cluster's CTAs) from each of its CTAs.
     static int out_bytes(int halves, int mode, int cols, int split) {
-        if (split == 1) return 2 * 8 * (mode == kUp ? 128 : halves * 128) * 4;
-        const int rows = cols * (mode == kUp ? 1 : halves);
-        return (rows + split - 1) / split * split * 32 * 4 * (mode == kUp ? 8 : 4);
+        if (split == 1) return 2 * 8 * (is_up(mode) ? 128 : halves * 128) * 4;
+        const int rows = cols * (is_up(mode) ? 1 : halves);
+        return (rows + split - 1) / split * split * 32 * 4 * (is_up(mode) ? 8 : 4);
     }
     static int smem_bytes(int w, int halves, int cap, int stages, int out, int tables) {
         return kAlign + stages * stage_bytes(w, halves, cap) + out + kBarBytes + tables;
@@ -248,6 +252,7 @@ __global__ void __launch_bounds__(256) dg_few_split_kernel(const uint16_t *x, in
     const int at = kb * block_k(W) + q * 8;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (at < k) v = __ldcg(reinterpret_cast<const uint4 *>(x + t * ldx + at));
+    __syncwarp();
     split_row<W>(v, image + static_cast<int64_t>(kb) * image_units(pieces_of(W), rows) * 1024,
                  image_sf + static_cast<int64_t>(kb) * scale_blocks(W) * 512, t, q, in);
 }
@@ -384,6 +389,7 @@ __global__ void __launch_bounds__(256) dg_layer_split_kernel(const uint16_t *x, 
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (col < k) v = __ldcg(reinterpret_cast<const uint4 *>(x + row * ldx + col));
         const int units = image_units(pieces_of(W), s.tokens[z]);
+        __syncwarp();
         split_row<W>(v, image + (static_cast<int64_t>(s.unit[z]) * kblocks + kb * units) * 1024,
                      image_sf + (static_cast<int64_t>(z) * kblocks + kb) * scale_blocks(W) * 512, at - s.first[z], q, in);
     }
@@ -400,8 +406,9 @@ struct FewTile {
 template <int W, int HALVES, int MODE>
 __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     dg_few_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ FewArgs p) {
+    constexpr bool UP = is_up(MODE), SELF = splits_itself(MODE);
     constexpr int ROWS = HALVES * 128;
-    constexpr int OUT = MODE == kUp ? 128 : ROWS;     // results per token and tile
+    constexpr int OUT = UP ? 128 : ROWS;     // results per token and tile
     constexpr int NT = FewConfig::threads(HALVES, MODE);
     constexpr int FIRST_B = FewConfig::first_b(HALVES);
     constexpr bool DIGITS = W == kFp4Packed;
@@ -437,7 +444,9 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     const int first_tile = blockIdx.x / nsplit, tile_step = gridDim.x / nsplit;
 
     const int pairs = MODE < kUp ? 0 : p.tokens * p.topk;
-    const int slot_id = MODE >= kUp && static_cast<int>(threadIdx.x) < pairs ? __ldcg(p.ids + threadIdx.x) : -1;
+    // (kUpSelf is the first kernel of its call: its ids may be the preceding kernel's)
+    int slot_id = -1;
+    if (MODE >= kUp && MODE != kUpSelf && static_cast<int>(threadIdx.x) < pairs) slot_id = __ldcg(p.ids + threadIdx.x);
     if (warp == 0) {
         // arrivals: full 2 (weights, pieces), empty and tfull one per issuer, tempty 4, drain 1
         for (int i = lane; i < 2 * S + 4 + HALVES; i += 32)
@@ -457,10 +466,14 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     // the results go to the ring, once its ring is idle.
     const bool early = p.out_bytes != 0;
     if (nsplit > 1 && early) cluster_arrive_relaxed();
-    // The split kernel before kGemvPre, kUp and kDown waits for what precedes it and only then
-    // lets the next one start.  So these may read weights, ids and routing weights at once, and
-    // only the warps that read the preceding kernel's output wait for it.  In kGemv every warp
-    // waits that reads or writes memory.
+    // The kernel before kGemvPre, kUp and kDown (a split kernel or kUpSelf) waits for what
+    // precedes it and only then lets the next one start.  So these may read weights, ids and
+    // routing weights at once, and only the warps that read the preceding kernel's output wait
+    // for it.  In kGemv every warp waits that reads or writes memory, in kUpSelf all do here.
+    if constexpr (MODE == kUpSelf) {
+        grid_dependency_wait();
+        if (static_cast<int>(threadIdx.x) < pairs) slot_id = __ldcg(p.ids + threadIdx.x);
+    }
     grid_launch_dependents();
     Segments seg = {};
     if constexpr (MODE >= kUp) seg = build_segments(tab, p.ids, slot_id, pairs, p.topk, p.experts, p.cap, PIECES, p.status);
@@ -469,14 +482,14 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_holder;
     const int total = MODE == kDown ? seg.count * p.kblocks : p.kblocks;     // K-blocks of a tile
-    const int num_tiles = MODE == kUp ? seg.count * p.row_tiles : p.row_tiles;
+    const int num_tiles = UP ? seg.count * p.row_tiles : p.row_tiles;
     // this CTA's share of each tile's K-blocks
     const int k_begin = static_cast<int>(static_cast<int64_t>(total) * rank / nsplit);
     const int k_end = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / nsplit);
 
     auto get_tile = [&](int w) {
         FewTile t = {0, 0, w * ROWS, p.tokens};
-        if constexpr (MODE == kUp) {
+        if constexpr (UP) {
             t.seg = w / p.row_tiles;
             t.row0 = (w - t.seg * p.row_tiles) * 128;
             t.expert = seg.expert[t.seg];
@@ -487,10 +500,11 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     // Four results of one token at weight rows n .. n + 3 (kUp: a warp holds the token's
     // 128; o is already silu(g) u).
     auto store = [&](const FewTile &tile, int t, int n, float (&o)[4]) {
-        if constexpr (MODE == kUp) {
+        if constexpr (UP) {
             // the routing weight, summed over the token's slots that name this expert
             const int slot = seg.token[seg.first[tile.seg] + t] * p.topk + lane;
             float w = lane < p.topk && __ldcg(p.ids + slot) == tile.expert ? __ldcg(p.weights + slot) : 0.0f;
+            __syncwarp();
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, s);
             uint32_t m = 0;
@@ -573,7 +587,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     // nsplit > 1.  A tile's results are rows of 32 items, item l the 4 results (kUp: and the 4
     // of the up half) that lane l of the four epilogue warps hold: ROW_GROUPS rows a token.
     // CTA r puts out rows r * share .. of them; smem_out is [CTA][share][component][32].
-    constexpr int ROW_GROUPS = OUT / 128, COMP = MODE == kUp ? 8 : 4;
+    constexpr int ROW_GROUPS = OUT / 128, COMP = UP ? 8 : 4;
     auto share_of = [&](const FewTile &tile) { return (tile.ntok * ROW_GROUPS + nsplit - 1) / nsplit; };
 
     if (warp == 0) {
@@ -583,7 +597,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         uint32_t issued = 0;
         bool drop = (p.debug_flags & DG_DEBUG_DROP_ONE_LOAD) && blockIdx.x == 0;
         const auto box_row = [&](const FewTile &tile, int e, int h) {   // rows / 4 of a half's box
-            const int r = MODE == kUp ? h * p.inner + tile.row0 : tile.row0 + h * 128;
+            const int r = UP ? h * p.inner + tile.row0 : tile.row0 + h * 128;
             return static_cast<int32_t>((static_cast<int64_t>(e) * p.rows + r) >> 2);
         };
         if constexpr (MODE == kGemv) {
@@ -615,14 +629,14 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                     uint32_t bytes = HALVES * (W == kFp4 ? 8192 : 16384);
 #pragma unroll
                     for (int h = 0; h < HALVES; ++h) {
-                        const int left = MODE == kUp ? 128 : p.sf_ld - (tile.row0 + h * 128);
+                        const int left = UP ? 128 : p.sf_ld - (tile.row0 + h * 128);
                         sf_bytes[h] = left >= 128 ? 512u : left > 0 ? 4u * static_cast<uint32_t>(left) : 0u;
                         bytes += sf_bytes[h] * slices;
                     }
                     mbar_arrive_expect_tx(&full_bar[slot], bytes);
 #pragma unroll
                     for (int h = 0; h < HALVES; ++h) {
-                        const int r = MODE == kUp ? h * p.inner + tile.row0 : tile.row0 + h * 128;
+                        const int r = UP ? h * p.inner + tile.row0 : tile.row0 + h * 128;
                         // (a half past the last row reads zeros or the next expert's rows; unused)
                         tma_load_3d(smem_a + (slot * HALVES + h) * 16384, &tm_w, &full_bar[slot], kb * 128,
                                     box_row(tile, e, h), 0);
@@ -730,7 +744,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     } else if (warp >= FIRST_B) {
         // ------------------------------------------------------------ the narrow operand
         grid_dependency_wait();
-        if constexpr (MODE == kGemv) {
+        if constexpr (SELF) {
             // The warps take the K-blocks in turn, at most as many warps as ring slots: a
             // wait for the MMAs of block g - S tests one parity bit, which is unambiguous
             // only if block g - 2S is known to be done; a warp's previous block g - teams
@@ -741,16 +755,20 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
             const int q = lane % LANES;
             int g = 0;   // K-blocks of the tiles before
             for (int w = first_tile; w < num_tiles && bw < teams; w += tile_step, g += k_end - k_begin) {
+                const FewTile tile = get_tile(w);
                 for (int i = (bw + teams - g % teams) % teams; i < k_end - k_begin; i += teams) {
                     const int slot = (g + i) % S;
                     if (!mbar_wait_warp(&empty_bar[slot], (((g + i) / S) & 1) ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
                     const int at = (k_begin + i) * BLOCK_K + q * 8;
-                    for (int t0 = 0; t0 < p.tokens; t0 += AT_ONCE) {
+                    for (int t0 = 0; t0 < tile.ntok; t0 += AT_ONCE) {
                         const int t = t0 + lane / LANES;
                         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (t < p.tokens && (!DIGITS || at < p.slices * 128))
-                            v = __ldcg(reinterpret_cast<const uint4 *>(p.x + t * p.ldx + at));
-                        split_row<W>(v, smem_b + slot * b_bytes, smem_sfb + slot * SB * 512, t, q, t < p.tokens);
+                        if (t < tile.ntok && (!DIGITS || at < p.slices * 128)) {
+                            const int row = UP ? seg.token[seg.first[tile.seg] + t] : t;
+                            v = __ldcg(reinterpret_cast<const uint4 *>(p.x + row * p.ldx + at));
+                        }
+                        __syncwarp();
+                        split_row<W>(v, smem_b + slot * b_bytes, smem_sfb + slot * SB * 512, t, q, t < tile.ntok);
                         __syncwarp();
                     }
                     fence_proxy_async_smem();
@@ -810,7 +828,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                     const uint32_t at = mapa_shared(
                         smem_u32(smem_out + ((rank * share + row) * COMP + quad) * 32 + lane), owner);
                     st_shared_cluster_f32(at, r[g][j]);
-                    if constexpr (MODE == kUp) st_shared_cluster_f32(at + 4 * 4 * 32, r[HALVES - 1][j]);
+                    if constexpr (UP) st_shared_cluster_f32(at + 4 * 4 * 32, r[HALVES - 1][j]);
                     if (++row == share) { row = 0; ++owner; }
                 }
             }
@@ -943,7 +961,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         if (j >= n) break;
-                        if (MODE == kUp) {
+                        if (UP) {
                             out[j * OUT + mine] = gated(r[0][j], r[HALVES - 1][j]);
                         } else {
 #pragma unroll
@@ -982,9 +1000,9 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                 float s = 0.0f, u = 0.0f;
                 for (int r = 0; r < nsplit; ++r) {
                     s += smem_out[((r * share + row) * COMP + c) * 32 + lane];
-                    if constexpr (MODE == kUp) u += smem_out[((r * share + row) * COMP + 4 + c) * 32 + lane];
+                    if constexpr (UP) u += smem_out[((r * share + row) * COMP + 4 + c) * 32 + lane];
                 }
-                o[c] = MODE == kUp ? gated(s, u) : s;
+                o[c] = UP ? gated(s, u) : s;
             }
             const int at = rank * share + row;
             store(tile, at / ROW_GROUPS, tile.row0 + (at % ROW_GROUPS) * 128 + 4 * lane, o);
