@@ -186,7 +186,7 @@ struct RouteParams {
     int t, experts, topk;
     int bf16, sigmoid, renormalize;
     float scale;
-    int vec;                // set by the launch: rows may be read 4 experts at a time
+    int vec, vec_bias;      // set by the launch: rows, the bias may be read 4 experts at a time
 };
 cudaError_t launch_moe_route(const RouteParams &p, cudaStream_t stream);
 

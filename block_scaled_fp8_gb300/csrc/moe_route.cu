@@ -3,13 +3,15 @@
 // One warp per token.  Bound by the instructions that it issues (E logits are read
 // once, 4 E bytes a token), so no expert that cannot be chosen is worked on:
 //  - every lane takes the largest approximate key of its experts (the logit for softmax,
-//    else the score by approximate exponential and reciprocal, within kSlack);
-//  - the topk-th largest of the 32 lanes' values, less the slack, is a lower bound of the
-//    topk-th largest key; the experts not below it are candidates (about 1.2 topk);
+//    else the score by one approximate tanh, within kCoarse);
+//  - the topk-th largest of the 32 lanes' values (topk rounds of a maximum over the lanes),
+//    less twice the error, is a lower bound of the topk-th largest key; the experts not
+//    below it are candidates (about 1.2 topk);
 //  - each candidate goes to one lane, which computes its score and key in full and counts
 //    the candidates before it: its place in the result.
-// More than 32 candidates (ties) are taken by topk rounds of a warp maximum over all keys.
-// 32768 tokens x 256 experts, top 8 of sigmoid + bias, FP32 logits: see launch_moe_route.
+// More than 32 candidates of a sigmoid (scores close to 1) are looked for once more with its
+// approximation by exponential and reciprocal, within kFine; where they are still more (ties),
+// topk rounds of a maximum over all keys take them.
 #include <cuda_bf16.h>
 
 #include "dg_internal.h"
@@ -19,9 +21,10 @@ namespace dg {
 namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
-// Above twice the error of the approximate sigmoid: the exponential's argument is off by 2^-24 of
-// itself and exponential and reciprocal by 2^-22, which moves 1 / (1 + e) by at most 1e-6.
-constexpr float kSlack = 4e-6f;
+// Above twice the errors of the approximate sigmoids.  1/2 + tanh(x / 2) / 2: tanh.approx is
+// within 2^-11 of its value.  1 / (1 + e): the exponential's argument is off by 2^-24 of
+// itself and exponential and reciprocal by 2^-22, which moves it by at most 1e-6.
+constexpr float kCoarse = 6e-4f, kFine = 4e-6f;
 
 // Order-preserving map of a float to an unsigned integer; 0 for -infinity and NaN.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -31,6 +34,29 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+__device__ __forceinline__ float tanh_approx(float x) {
+    float r;
+    asm("tanh.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float max_over_lanes(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// x of the lane `d` below added, in lanes that have one
+__device__ __forceinline__ int add_from_below(int x, int d) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 v;\n\t"
+        "shfl.sync.up.b32 v|p, %0, %1, 0, 0xffffffff;\n\t"
+        "@p add.s32 %0, %0, v;\n\t}"
+        : "+r"(x)
+        : "r"(d));
+    return x;
+}
 
 __device__ __forceinline__ float sigmoid_approx(float x) {
     float r;
@@ -45,8 +71,8 @@ __global__ void __launch_bounds__(256) dg_moe_route_kernel(const RouteParams p) 
     const int lane = threadIdx.x & 31;
     const int w = threadIdx.x >> 5;
     const int token = blockIdx.x * 8 + w;
-    __shared__ float s_x[8][32 * PER];
-    __shared__ uint32_t s_key[8][32];
+    __shared__ __align__(16) float s_x[8][32 * PER];
+    __shared__ __align__(16) uint32_t s_key[8][32];
     __shared__ int s_id[8][32];
     grid_launch_dependents();
     grid_dependency_wait();
@@ -86,8 +112,14 @@ __global__ void __launch_bounds__(256) dg_moe_route_kernel(const RouteParams p) 
             }
         }
     }
+    if constexpr (VEC == 4) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) s_x[w][lane * PER + i] = x[i];
+        for (int i = 0; i < PER; i += 4)
+            *reinterpret_cast<float4 *>(&s_x[w][lane * PER + i]) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) s_x[w][lane * PER + i] = x[i];
+    }
     float top = -INFINITY, denom = 1.0f;
     // softmax weights that are normalised over the chosen need no other expert's score
     const bool late = !SIGMOID && p.renormalize;
@@ -107,43 +139,70 @@ __global__ void __launch_bounds__(256) dg_moe_route_kernel(const RouteParams p) 
         }
     }
     auto bias_of = [&](int j) { return p.bias ? __ldg(p.bias + j) : 0.0f; };
-    // approximate keys; -infinity for what is never chosen, NaN included
-    float approx[PER];
-    float best = -INFINITY;
+    // approximate keys; -infinity or NaN for what is never chosen
+    float approx[PER], low = x[0];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int j = lane * PER + i;
-        approx[i] = SIGMOID ? sigmoid_approx(x[i]) : p.bias ? expf(x[i] - top) / denom : x[i];
-        if (p.bias && j < p.experts) approx[i] += __ldg(p.bias + j);
-        if (!(x[i] > -INFINITY)) approx[i] = -INFINITY;
-        best = fmaxf(best, approx[i]);
+        if (SIGMOID) approx[i] = 0.5f;
+        else approx[i] = p.bias ? expf(x[i] - top) / denom : x[i];
+        low = fminf(low, x[i]);
     }
-    // the topk-th largest of the lanes' largest: a bitonic sort over the lanes, descending,
-    // whose every step keeps the larger value in the lane with the step's bit clear
-    float bound = best;
+    if (p.bias) {
+        const float *bias = p.bias + lane * PER;
 #pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
+        for (int i0 = 0; i0 < PER; i0 += VEC) {
+            if (VEC == 4 && p.vec_bias) {
+                if (lane * PER + i0 >= p.experts) break;
+                const float4 v = __ldg(reinterpret_cast<const float4 *>(bias + i0));
+                const float u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int s = size >> 1; s > 0; s >>= 1) {
-            const float other = __shfl_xor_sync(kFull, bound, s == size >> 1 ? size - 1 : s);
-            bound = lane & s ? fminf(bound, other) : fmaxf(bound, other);
+                for (int i = 0; i < VEC; ++i) approx[i0 + i] += u[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (lane * PER + i0 + i < p.experts) approx[i0 + i] += __ldg(bias + i0 + i);
+            }
         }
-    bound = __shfl_sync(kFull, bound, p.topk - 1);
-    if ((SIGMOID || p.bias) && fabsf(bound) < INFINITY)
-        bound -= kSlack + fabsf(bound) * 2.4e-7f;   // (and the key's own rounding)
-    bound = fmaxf(bound, -3.402823466e38f);
-
-    uint32_t hits = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (approx[i] >= bound) hits |= 1u << i;
-    int at = __popc(hits);
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-        const int v = __shfl_up_sync(kFull, at, s);
-        if (lane >= s) at += v;
     }
-    const int count = __shfl_sync(kFull, at, 31);
+    if constexpr (SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) approx[i] = fmaf(0.5f, tanh_approx(0.5f * x[i]), approx[i]);
+    }
+    float slack = SIGMOID ? kCoarse : p.bias ? kFine : 0.0f;
+    uint32_t hits;
+    int at, count;
+    while (true) {
+        if (low == -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (x[i] == -INFINITY) approx[i] = -INFINITY;
+        }
+        __syncwarp();
+        float best = -INFINITY, bound = INFINITY;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) best = fmaxf(best, approx[i]);
+        // the topk-th largest of the lanes' largest (lower where some are equal)
+        for (int r = 0; r < p.topk; ++r) {
+            bound = max_over_lanes(best);
+            if (best == bound) best = -INFINITY;
+        }
+        if (slack != 0.0f && fabsf(bound) < INFINITY)
+            bound -= slack + fabsf(bound) * 2.4e-7f;   // (and the key's own rounding)
+        bound = fmaxf(bound, -3.402823466e38f);
+        hits = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (approx[i] >= bound) hits |= 1u << i;
+        at = __popc(hits);
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) at = add_from_below(at, s);
+        count = __shfl_sync(kFull, at, 31);
+        if (!SIGMOID || count <= 32 || slack == kFine) break;
+        slack = kFine;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            approx[i] = sigmoid_approx(x[i]) + (lane * PER + i < p.experts ? bias_of(lane * PER + i) : 0.0f);
+    }
     float score = 0.0f, chosen = 0.0f;
     int id = -1, place = lane;
     if (count <= 32) {
@@ -164,20 +223,27 @@ __global__ void __launch_bounds__(256) dg_moe_route_kernel(const RouteParams p) 
         int before = 0;
         for (int j = 0; j < count; j += 4) {
             const uint4 o = *reinterpret_cast<const uint4 *>(&s_key[w][j]);
-            // (of equal keys the earlier candidate comes first)
-            before += o.x > key || (o.x == key && j < lane);
-            before += o.y > key || (o.y == key && j + 1 < lane);
-            before += o.z > key || (o.z == key && j + 2 < lane);
-            before += o.w > key || (o.w == key && j + 3 < lane);
+            before += o.x > key;
+            before += o.y > key;
+            before += o.z > key;
+            before += o.w > key;
         }
         // (a key that is NaN is 0; candidates beyond the topk have no place)
-        const bool in = key != 0u && before < p.topk;
-        const uint32_t placed = __ballot_sync(kFull, in);
-        place = before;
-        if (!in) {   // the slots that no expert is left for go to the idle lanes
+        const bool valid = key != 0u;
+        const int valids = __popc(__ballot_sync(kFull, valid));
+        if (__popc(__reduce_or_sync(kFull, valid ? 1u << before : 0u)) != valids) {
+            for (int j = 0; j < lane; ++j) before += s_key[w][j] == key;   // of equal keys the earlier comes first
+            __syncwarp();
+        }
+        const bool in = valid && before < p.topk;
+        place = in ? before : 32;
+        if (!in) {
             id = -1;
             score = 0.0f;
-            place = __popc(placed) + __popc(~placed & ((1u << lane) - 1u));
+        }
+        if (valids < p.topk) {   // the slots that no expert is left for go to the idle lanes
+            const uint32_t placed = __ballot_sync(kFull, in);
+            if (!in) place = __popc(placed) + __popc(~placed & ((1u << lane) - 1u));
         }
         chosen = score;
 #pragma unroll
@@ -248,6 +314,7 @@ cudaError_t launch_moe_route(const RouteParams &params, cudaStream_t stream) {
     // rows of whole aligned groups of 4 experts are read a group at a time
     p.vec = p.experts % 4 == 0 && p.ld % 4 == 0 &&
             reinterpret_cast<uintptr_t>(p.logits) % (p.bf16 ? 8 : 16) == 0;
+    p.vec_bias = p.experts % 4 == 0 && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0;
     if (p.experts <= 32) return launch_per<1>(p, stream);
     if (p.experts <= 64) return launch_per<2>(p, stream);
     if (p.experts <= 128) return launch_per<4>(p, stream);
