@@ -210,7 +210,9 @@ struct SegmentBounds {
         w = format_of(fp4, cap);
         count = used + pairs / cap;
         if (count > pairs) count = pairs;
-        units = w == kFp4Packed ? pairs : (pairs + 3 * count) / 4;
+        // (up to 8 tokens: a segment takes the room of all tokens)
+        units = w == kFp4Packed ? pairs : t <= 8 ? count * image_units(pieces_of(w), static_cast<int>(t))
+                                                 : (pairs + 3 * count) / 4;
     }
     int64_t blocks(int64_t k) const { return (k + block_k(w) - 1) / block_k(w); }
     int64_t image(int64_t k) const { return units * blocks(k) * 1024; }

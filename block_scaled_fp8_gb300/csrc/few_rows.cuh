@@ -271,15 +271,84 @@ struct Segments {
 };
 
 __host__ __device__ constexpr int segment_table_bytes(int pairs, int experts) {
-    return (16 + 12 * experts + 14 * pairs + 15) / 16 * 16;
+    const int masks = experts < 3 ? 32 : 12 * experts;   // either form's tables by expert
+    return (16 + masks + 14 * pairs + 15) / 16 * 16;
 }
 
 // (The loops are not unrolled: a kernel's first pass over its code waits for the code, from
 // HBM where the weights have pushed it out of L2.)
+// Tables for up to 8 tokens, where an expert's tokens are one segment: a bit for each token
+// and expert, from which every slot counts the entries and segments before its own.
+__device__ __forceinline__ Segments build_short_segments(int *tab, const int32_t *ids, int id, int tokens, int topk,
+                                                         int experts, int pieces, int32_t *status) {
+    const int words = (experts + 31) / 32, pairs = tokens * topk;
+    uint32_t *mask = reinterpret_cast<uint32_t *>(tab + 4);   // [words][8 tokens]
+    Segments s;
+    s.token = reinterpret_cast<uint16_t *>(mask + 8 * words);
+    s.of_entry = s.token + pairs;
+    s.expert = s.of_entry + pairs;
+    s.first = s.expert + pairs;
+    s.tokens = s.first + pairs;
+    s.unit = s.tokens + pairs;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < 8 * words; i += blockDim.x) mask[i] = 0u;
+    __syncthreads();
+#pragma unroll 1
+    for (int q = threadIdx.x; q < pairs; q += blockDim.x) {
+        const int t = q / topk, e = q == static_cast<int>(threadIdx.x) ? id : __ldcg(ids + q);
+        if (e >= 0 && e < experts) atomicOr(&mask[(e >> 5) * 8 + t], 1u << (e & 31));
+        else if (e >= experts && status) atomicOr(status, DG_DEV_BAD_GROUP);
+    }
+    __syncthreads();
+    // (the last thread counts all of them)
+#pragma unroll 1
+    for (int q = threadIdx.x; q < pairs || threadIdx.x == blockDim.x - 1; q += blockDim.x) {
+        const int t = q / topk, e = q >= pairs ? 32 * words : q == static_cast<int>(threadIdx.x) ? id : __ldcg(ids + q);
+        if (q < pairs && !(e >= 0 && e < experts)) continue;
+        int first = 0, z = 0;
+        uint32_t have = 0;   // the tokens that name e
+#pragma unroll 1
+        for (int w = 0; w <= min(e >> 5, words - 1); ++w) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(mask + 8 * w), b = *reinterpret_cast<const uint4 *>(mask + 8 * w + 4);
+            const uint32_t m[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            const uint32_t before = w == e >> 5 ? (1u << (e & 31)) - 1u : ~0u;
+            uint32_t any = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                any |= m[i];
+                first += __popc(m[i] & before);
+                have = (have & ~(1u << i)) | (m[i] >> (e & 31) & 1u) << i;
+            }
+            z += __popc(any & before);
+        }
+        if (q >= pairs) {
+            tab[0] = z;
+            tab[1] = first;
+            break;
+        }
+        // (a token that names an expert twice writes the same entry twice)
+        const int at = __popc(have & ((1u << t) - 1u));
+        s.token[first + at] = static_cast<uint16_t>(t);
+        s.of_entry[first + at] = static_cast<uint16_t>(z);
+        if (at == 0) {
+            s.expert[z] = static_cast<uint16_t>(e);
+            s.first[z] = static_cast<uint16_t>(first);
+            s.tokens[z] = static_cast<uint16_t>(__popc(have));
+            s.unit[z] = static_cast<uint16_t>(pieces == 8 ? first : z * image_units(pieces, tokens));
+        }
+    }
+    __syncthreads();
+    s.count = tab[0];
+    s.entries = tab[1];
+    return s;
+}
+
 // Tables of segment_table_bytes at `tab`; called by all threads of a CTA, after some work of
 // its own if it has any (`id`: load of thread q's slot q, issued before that).
-__device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids, int id, int pairs, int topk,
+__device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids, int id, int tokens, int topk,
                                                    int experts, int cap, int pieces, int32_t *status) {
+    if (tokens <= 8) return build_short_segments(tab, ids, id, tokens, topk, experts, pieces, status);
+    const int pairs = tokens * topk;
     uint32_t *mask = reinterpret_cast<uint32_t *>(tab + 4);            // [experts][2] tokens of each expert
     uint16_t *start = reinterpret_cast<uint16_t *>(mask + 2 * experts);   // [experts] first entry
     uint16_t *seg0 = start + experts;                                     // [experts] first segment
@@ -379,7 +448,7 @@ __global__ void __launch_bounds__(256) dg_layer_split_kernel(const uint16_t *x, 
     grid_dependency_wait();
     grid_launch_dependents();
     const int slot_id = threadIdx.x < tokens * topk ? __ldcg(ids + threadIdx.x) : -1;
-    const Segments s = build_segments(split_tab, ids, slot_id, tokens * topk, topk, experts, cap, pieces_of(W), nullptr);
+    const Segments s = build_segments(split_tab, ids, slot_id, tokens, topk, experts, cap, pieces_of(W), nullptr);
     const int q = threadIdx.x % LANES, kb = blockIdx.x, kblocks = gridDim.x;
     const int col = kb * block_k(W) + q * 8;
     for (int at0 = blockIdx.y * ROWS; at0 < s.entries; at0 += gridDim.y * ROWS) {
@@ -476,7 +545,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     }
     grid_launch_dependents();
     Segments seg = {};
-    if constexpr (MODE >= kUp) seg = build_segments(tab, p.ids, slot_id, pairs, p.topk, p.experts, p.cap, PIECES, p.status);
+    if constexpr (MODE >= kUp) seg = build_segments(tab, p.ids, slot_id, p.tokens, p.topk, p.experts, p.cap, PIECES, p.status);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
