@@ -268,23 +268,28 @@ struct Segments {
     uint16_t *unit;     // [count] units of the segments before (image_units)
     uint16_t *token;    // [entries] by expert, ascending
     uint16_t *of_entry; // [entries] segment
+    uint16_t *id;       // [pairs] expert of a slot, 0xFFFF where none
+    float *weight;      // [pairs] its routing weight, where asked for
 };
 
 __host__ __device__ constexpr int segment_table_bytes(int pairs, int experts) {
     const int masks = experts < 3 ? 32 : 12 * experts;   // either form's tables by expert
-    return (16 + masks + 14 * pairs + 15) / 16 * 16;
+    return (16 + masks + 18 * pairs + 15) / 16 * 16;
 }
 
 // (The loops are not unrolled: a kernel's first pass over its code waits for the code, from
 // HBM where the weights have pushed it out of L2.)
 // Tables for up to 8 tokens, where an expert's tokens are one segment: a bit for each token
 // and expert, from which every slot counts the entries and segments before its own.
-__device__ __forceinline__ Segments build_short_segments(int *tab, const int32_t *ids, int id, int tokens, int topk,
-                                                         int experts, int pieces, int32_t *status) {
+__device__ __forceinline__ Segments build_short_segments(int *tab, const int32_t *ids, const float *weights, int id,
+                                                         float weight, int tokens, int topk, int experts, int pieces,
+                                                         int32_t *status) {
     const int words = (experts + 31) / 32, pairs = tokens * topk;
     uint32_t *mask = reinterpret_cast<uint32_t *>(tab + 4);   // [words][8 tokens]
     Segments s;
-    s.token = reinterpret_cast<uint16_t *>(mask + 8 * words);
+    s.weight = reinterpret_cast<float *>(mask + 8 * words);
+    s.id = reinterpret_cast<uint16_t *>(s.weight + pairs);
+    s.token = s.id + pairs;
     s.of_entry = s.token + pairs;
     s.expert = s.of_entry + pairs;
     s.first = s.expert + pairs;
@@ -295,16 +300,20 @@ __device__ __forceinline__ Segments build_short_segments(int *tab, const int32_t
     __syncthreads();
 #pragma unroll 1
     for (int q = threadIdx.x; q < pairs; q += blockDim.x) {
-        const int t = q / topk, e = q == static_cast<int>(threadIdx.x) ? id : __ldcg(ids + q);
-        if (e >= 0 && e < experts) atomicOr(&mask[(e >> 5) * 8 + t], 1u << (e & 31));
+        const bool mine = q == static_cast<int>(threadIdx.x);
+        const int t = q / topk, e = mine ? id : __ldcg(ids + q);
+        const bool ok = e >= 0 && e < experts;
+        if (ok) atomicOr(&mask[(e >> 5) * 8 + t], 1u << (e & 31));
         else if (e >= experts && status) atomicOr(status, DG_DEV_BAD_GROUP);
+        s.id[q] = ok ? static_cast<uint16_t>(e) : 0xFFFFu;
+        if (weights) s.weight[q] = mine ? weight : __ldcg(weights + q);
     }
     __syncthreads();
     // (the last thread counts all of them)
 #pragma unroll 1
     for (int q = threadIdx.x; q < pairs || threadIdx.x == blockDim.x - 1; q += blockDim.x) {
-        const int t = q / topk, e = q >= pairs ? 32 * words : q == static_cast<int>(threadIdx.x) ? id : __ldcg(ids + q);
-        if (q < pairs && !(e >= 0 && e < experts)) continue;
+        const int t = q / topk, e = q < pairs ? s.id[q] : 32 * words;
+        if (e == 0xFFFF) continue;
         int first = 0, z = 0;
         uint32_t have = 0;   // the tokens that name e
 #pragma unroll 1
@@ -344,17 +353,20 @@ __device__ __forceinline__ Segments build_short_segments(int *tab, const int32_t
 }
 
 // Tables of segment_table_bytes at `tab`; called by all threads of a CTA, after some work of
-// its own if it has any (`id`: load of thread q's slot q, issued before that).
-__device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids, int id, int tokens, int topk,
-                                                   int experts, int cap, int pieces, int32_t *status) {
-    if (tokens <= 8) return build_short_segments(tab, ids, id, tokens, topk, experts, pieces, status);
+// its own if it has any (`id`, `weight`: loads of thread q's slot q, issued before that).
+__device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids, const float *weights, int id, float weight,
+                                                   int tokens, int topk, int experts, int cap, int pieces,
+                                                   int32_t *status) {
+    if (tokens <= 8)
+        return build_short_segments(tab, ids, weights, id, weight, tokens, topk, experts, pieces, status);
     const int pairs = tokens * topk;
     uint32_t *mask = reinterpret_cast<uint32_t *>(tab + 4);            // [experts][2] tokens of each expert
     uint16_t *start = reinterpret_cast<uint16_t *>(mask + 2 * experts);   // [experts] first entry
     uint16_t *seg0 = start + experts;                                     // [experts] first segment
-    uint16_t *s_ids = seg0 + experts;                                     // [pairs]
     Segments s;
-    s.token = s_ids + pairs;
+    s.weight = reinterpret_cast<float *>(seg0 + experts);
+    s.id = reinterpret_cast<uint16_t *>(s.weight + pairs);
+    s.token = s.id + pairs;
     s.of_entry = s.token + pairs;
     s.expert = s.of_entry + pairs;
     s.first = s.expert + pairs;
@@ -367,10 +379,12 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
     __syncthreads();
 #pragma unroll 1
     for (int q = threadIdx.x; q < pairs; q += blockDim.x) {
-        const int e = q == static_cast<int>(threadIdx.x) ? id : __ldcg(ids + q);
+        const bool mine = q == static_cast<int>(threadIdx.x);
+        const int e = mine ? id : __ldcg(ids + q);
         const bool ok = e >= 0 && e < experts;
         if (e >= experts && status) atomicOr(status, DG_DEV_BAD_GROUP);
-        s_ids[q] = ok ? static_cast<uint16_t>(e) : 0xFFFFu;
+        s.id[q] = ok ? static_cast<uint16_t>(e) : 0xFFFFu;
+        if (weights) s.weight[q] = mine ? weight : __ldcg(weights + q);
         const int t = q / topk;
         if (ok) atomicOr(&mask[2 * e + (t >> 5)], 1u << (t & 31));
     }
@@ -420,7 +434,7 @@ __device__ __forceinline__ Segments build_segments(int *tab, const int32_t *ids,
     __syncthreads();
 #pragma unroll 1
     for (int q = threadIdx.x; q < pairs; q += blockDim.x) {
-        const int e = s_ids[q], t = q / topk;
+        const int e = s.id[q], t = q / topk;
         if (e == 0xFFFF) continue;
         // (a token that names an expert twice writes the same entry twice)
         const uint32_t below = (1u << (t & 31)) - 1u;
@@ -448,7 +462,7 @@ __global__ void __launch_bounds__(256) dg_layer_split_kernel(const uint16_t *x, 
     grid_dependency_wait();
     grid_launch_dependents();
     const int slot_id = threadIdx.x < tokens * topk ? __ldcg(ids + threadIdx.x) : -1;
-    const Segments s = build_segments(split_tab, ids, slot_id, tokens, topk, experts, cap, pieces_of(W), nullptr);
+    const Segments s = build_segments(split_tab, ids, nullptr, slot_id, 0.0f, tokens, topk, experts, cap, pieces_of(W), nullptr);
     const int q = threadIdx.x % LANES, kb = blockIdx.x, kblocks = gridDim.x;
     const int col = kb * block_k(W) + q * 8;
     for (int at0 = blockIdx.y * ROWS; at0 < s.entries; at0 += gridDim.y * ROWS) {
@@ -515,7 +529,13 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     const int pairs = MODE < kUp ? 0 : p.tokens * p.topk;
     // (kUpSelf is the first kernel of its call: its ids may be the preceding kernel's)
     int slot_id = -1;
-    if (MODE >= kUp && MODE != kUpSelf && static_cast<int>(threadIdx.x) < pairs) slot_id = __ldcg(p.ids + threadIdx.x);
+    float slot_weight = 0.0f;
+    auto load_slot = [&] {
+        if (static_cast<int>(threadIdx.x) >= pairs) return;
+        slot_id = __ldcg(p.ids + threadIdx.x);
+        if constexpr (UP) slot_weight = __ldcg(p.weights + threadIdx.x);
+    };
+    if constexpr (MODE == kUp || MODE == kDown) load_slot();
     if (warp == 0) {
         // arrivals: full 2 (weights, pieces), empty and tfull one per issuer, tempty 4, drain 1
         for (int i = lane; i < 2 * S + 4 + HALVES; i += 32)
@@ -541,11 +561,13 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     // for it.  In kGemv every warp waits that reads or writes memory, in kUpSelf all do here.
     if constexpr (MODE == kUpSelf) {
         grid_dependency_wait();
-        if (static_cast<int>(threadIdx.x) < pairs) slot_id = __ldcg(p.ids + threadIdx.x);
+        load_slot();
     }
     grid_launch_dependents();
     Segments seg = {};
-    if constexpr (MODE >= kUp) seg = build_segments(tab, p.ids, slot_id, p.tokens, p.topk, p.experts, p.cap, PIECES, p.status);
+    if constexpr (MODE >= kUp)
+        seg = build_segments(tab, p.ids, UP ? p.weights : nullptr, slot_id, slot_weight, p.tokens, p.topk, p.experts,
+                             p.cap, PIECES, p.status);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -572,7 +594,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         if constexpr (UP) {
             // the routing weight, summed over the token's slots that name this expert
             const int slot = seg.token[seg.first[tile.seg] + t] * p.topk + lane;
-            float w = lane < p.topk && __ldcg(p.ids + slot) == tile.expert ? __ldcg(p.weights + slot) : 0.0f;
+            float w = lane < p.topk && seg.id[slot] == tile.expert ? seg.weight[slot] : 0.0f;
             __syncwarp();
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, s);
