@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *tab = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + FewConfig::kBarBytes);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x) >> 5, 0);   // (known to be the same in a warp)
     const int lane = threadIdx.x & 31;
     const WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
     const int first_tile = blockIdx.x / nsplit, tile_step = gridDim.x / nsplit;
@@ -686,6 +686,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         int slot = 0;
         uint32_t phase = 0;
         uint32_t issued = 0;
+        const bool one = elect_one();
         bool drop = (p.debug_flags & DG_DEBUG_DROP_ONE_LOAD) && blockIdx.x == 0;
         const auto box_row = [&](const FewTile &tile, int e, int h) {   // rows / 4 of a half's box
             const int r = UP ? h * p.inner + tile.row0 : tile.row0 + h * 128;
@@ -711,34 +712,31 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                 if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto producer_done;
                 if (drop) drop = false;   // diagnostic: this slot never fills
                 else issued |= 1u << slot;
-                if ((issued >> slot & 1u) && elect_one()) {
-                    const int e = MODE == kDown ? seg.expert[z] : tile.expert;
-                    const int slice = W == kFp8 ? kb >> 2 : kb * SB;
-                    const int slices = min(SB, p.slices - slice);
-                    const uint32_t *sf = p.sf + e * p.sf_expert + static_cast<int64_t>(slice) * p.sf_ld;
-                    uint32_t sf_bytes[HALVES];
-                    uint32_t bytes = HALVES * (W == kFp4 ? 8192 : 16384);
+                const bool on = one && (issued >> slot & 1u);
+                const int e = MODE == kDown ? seg.expert[z] : tile.expert;
+                const int slice = W == kFp8 ? kb >> 2 : kb * SB;
+                const int slices = min(SB, p.slices - slice);
+                const uint32_t *sf = p.sf + e * p.sf_expert + static_cast<int64_t>(slice) * p.sf_ld;
+                uint32_t sf_bytes[HALVES];
+                uint32_t bytes = HALVES * (W == kFp4 ? 8192 : 16384);
 #pragma unroll
-                    for (int h = 0; h < HALVES; ++h) {
-                        const int left = UP ? 128 : p.sf_ld - (tile.row0 + h * 128);
-                        sf_bytes[h] = left >= 128 ? 512u : left > 0 ? 4u * static_cast<uint32_t>(left) : 0u;
-                        bytes += sf_bytes[h] * slices;
-                    }
-                    mbar_arrive_expect_tx(&full_bar[slot], bytes);
-#pragma unroll
-                    for (int h = 0; h < HALVES; ++h) {
-                        const int r = UP ? h * p.inner + tile.row0 : tile.row0 + h * 128;
-                        // (a half past the last row reads zeros or the next expert's rows; unused)
-                        tma_load_3d(smem_a + (slot * HALVES + h) * 16384, &tm_w, &full_bar[slot], kb * 128,
-                                    box_row(tile, e, h), 0);
-#pragma unroll
-                        for (int b = 0; b < SB; ++b)
-                            if (sf_bytes[h] && b < slices)
-                                bulk_load(smem_sfa + ((slot * HALVES + h) * SB + b) * 512,
-                                          sf + static_cast<int64_t>(b) * p.sf_ld + r, sf_bytes[h], &full_bar[slot]);
-                    }
+                for (int h = 0; h < HALVES; ++h) {
+                    const int left = UP ? 128 : p.sf_ld - (tile.row0 + h * 128);
+                    sf_bytes[h] = left >= 128 ? 512u : left > 0 ? 4u * static_cast<uint32_t>(left) : 0u;
+                    bytes += sf_bytes[h] * slices;
                 }
-                __syncwarp();
+                mbar_arrive_expect_tx_if(on, &full_bar[slot], bytes);
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+                    const int r = UP ? h * p.inner + tile.row0 : tile.row0 + h * 128;
+                    // (a half past the last row reads zeros or the next expert's rows; unused)
+                    tma_load_3d_if(on, smem_a + (slot * HALVES + h) * 16384, &tm_w, &full_bar[slot], kb * 128,
+                                   box_row(tile, e, h), 0);
+#pragma unroll
+                    for (int b = 0; b < SB; ++b)
+                        bulk_load_if(on && sf_bytes[h] && b < slices, smem_sfa + ((slot * HALVES + h) * SB + b) * 512,
+                                     sf + static_cast<int64_t>(b) * p.sf_ld + r, sf_bytes[h], &full_bar[slot]);
+                }
                 if (++kb == p.kblocks && MODE == kDown) { kb = 0; ++z; }
                 if (++slot == S) { slot = 0; phase ^= 1; }
             }
@@ -766,6 +764,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         const uint64_t sfa_base = make_desc_sf_32x128b(smem_u32(smem_sfa + h * SB * 512));
         const uint64_t sfb_base = make_desc_sf_32x128b(smem_u32(smem_sfb));
         const uint32_t sf0 = sf_tmem + 2 * h * SF;
+        const bool one = elect_one();
         for (int w = first_tile; w < num_tiles; w += tile_step) {
             const FewTile tile = get_tile(w);
             // a run of K-blocks into one accumulator: the tile's, in kDown those of each segment
@@ -778,47 +777,48 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                 tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_base + (acc * HALVES + h) * ncols;
                 // columns in use: the tokens', rounded up to the MMA's step of 16
-                const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
+                const int tok = MODE >= kUp ? __shfl_sync(0xFFFFFFFFu, static_cast<int>(seg.tokens[z]), 0) : tile.ntok;
                 const uint32_t cols = (PIECES * tok + 15) / 16 * 16;
                 const uint32_t idesc = DIGITS ? make_idesc_mxf4(128, cols, 0, 0)
                                               : make_idesc_mxf8(128, cols, 0, 0) | (W == kFp4 ? 5u << 7 : 0u);   // A: E2M1
+                // (nothing here diverges: a branch for the issuing lane costs 200 cycles a K-block)
                 for (int j = 0; j < n; ++j, ++g) {
                     if (!mbar_wait_warp(&full_bar[slot], phase, ctl, DG_DEV_TIMEOUT)) goto mma_done;
                     tc_fence_after_sync();
-                    if (elect_one()) {
-                        const uint32_t sf = sf0 + (g & 1) * SF;
+                    const int next = slot + 1 == S ? 0 : slot + 1;
+                    const uint32_t sf = sf0 + (g & 1) * SF;
 #pragma unroll
-                        for (int b = 0; b < SB; ++b) {
-                            tc_cp_32x128b_warpx4(sf + 4 * b, sfa_base + static_cast<uint64_t>((slot * HALVES * SB + b) * 32));
-                            tc_cp_32x128b_warpx4(sf + 4 * SB + 4 * b, sfb_base + static_cast<uint64_t>((slot * SB + b) * 32));
-                        }
-                        const uint64_t a_desc = a_base + static_cast<uint64_t>(slot * HALVES * 1024);
-                        const uint64_t b_desc = b_base + static_cast<uint64_t>(slot * (b_bytes >> 4));
-                        if constexpr (DIGITS) {
-                            const int mmas = kb0 + j == p.kblocks - 1 ? p.last_mmas : 4;
-#pragma unroll
-                            for (uint32_t k = 0; k < 4; ++k) {
-                                const uint32_t byte = (k & 1) * 2;   // of the slice's scale words
-                                if (k < 2 || mmas == 4)
-                                    tc_mma_mxf4(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc | (byte << 4) | (byte << 29),
-                                                sf + 4 * (k >> 1), sf + 4 * SB + 4 * (k >> 1), (j | k) != 0);
-                            }
-                        } else {
-#pragma unroll
-                            for (uint32_t k = 0; k < 4; ++k) {
-                                // scale byte: the activations' and FP4 weights' k-th 32 K, FP8 weights' 128-K block
-                                const uint32_t id =
-                                    idesc | (k << 4) | ((W == kFp4 ? k : static_cast<uint32_t>((kb0 + j) & 3)) << 29);
-                                tc_mma_mxf8(d_tmem, a_desc + 2 * k, b_desc + 2 * k, id, sf, sf + 4, (j | k) != 0);
-                            }
-                        }
-                        tc_commit(&empty_bar[slot]);
+                    for (int b = 0; b < SB; ++b) {
+                        tc_cp_32x128b_warpx4_if(one, sf + 4 * b,
+                                                sfa_base + static_cast<uint64_t>((slot * HALVES * SB + b) * 32));
+                        tc_cp_32x128b_warpx4_if(one, sf + 4 * SB + 4 * b,
+                                                sfb_base + static_cast<uint64_t>((slot * SB + b) * 32));
                     }
-                    __syncwarp();
-                    if (++slot == S) { slot = 0; phase ^= 1; }
+                    const uint64_t a_desc = a_base + static_cast<uint64_t>(slot * HALVES * 1024);
+                    const uint64_t b_desc = b_base + static_cast<uint64_t>(slot * (b_bytes >> 4));
+                    if constexpr (DIGITS) {
+                        const bool all = one && (kb0 + j != p.kblocks - 1 || p.last_mmas == 4);
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k) {
+                            const uint32_t byte = (k & 1) * 2;   // of the slice's scale words
+                            tc_mma_mxf4_if(k < 2 ? one : all, d_tmem, a_desc + 2 * k, b_desc + 2 * k,
+                                           idesc | (byte << 4) | (byte << 29), sf + 4 * (k >> 1),
+                                           sf + 4 * SB + 4 * (k >> 1), (j | k) != 0);
+                        }
+                    } else {
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k) {
+                            // scale byte: the activations' and FP4 weights' k-th 32 K, FP8 weights' 128-K block
+                            const uint32_t id =
+                                idesc | (k << 4) | ((W == kFp4 ? k : static_cast<uint32_t>((kb0 + j) & 3)) << 29);
+                            tc_mma_mxf8_if(one, d_tmem, a_desc + 2 * k, b_desc + 2 * k, id, sf, sf + 4, (j | k) != 0);
+                        }
+                    }
+                    tc_commit_if(one, &empty_bar[slot]);
+                    slot = next;
+                    phase ^= next == 0;
                 }
-                if (elect_one()) tc_commit(&tfull_bar[acc]);
-                __syncwarp();
+                tc_commit_if(one, &tfull_bar[acc]);
                 if (++acc == p.accs) { acc = 0; acc_phase ^= 1; }
             }
         }
@@ -826,8 +826,8 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         __syncwarp();
         if (nsplit > 1) ring_idle();
         // TMEM is not freed before every MMA has finished
-        if (elect_one()) {
-            tc_commit(&drain_bar[h]);
+        tc_commit_if(one, &drain_bar[h]);
+        if (one) {
             mbar_wait_drain(&drain_bar[h], 0, ctl);
         }
         __syncwarp();
@@ -870,25 +870,23 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         } else {
             int slot = 0;
             uint32_t phase = 0;
+            const bool one = elect_one();
             for (int w = first_tile; w < num_tiles; w += tile_step) {
                 const FewTile tile = get_tile(w);
                 int z = MODE == kDown ? k_begin / p.kblocks : tile.seg;
                 int kb = MODE == kDown ? k_begin - z * p.kblocks : k_begin;
                 for (int i = k_begin; i < k_end; ++i) {
                     if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
-                    if (elect_one()) {
-                        const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
-                        const int units = image_units(PIECES, tok);
-                        const int64_t before = MODE >= kUp ? seg.unit[z] : 0;
-                        const uint32_t sf_bytes = DIGITS ? 1024u : tok < 16 ? 32u * tok : 512u;
-                        mbar_arrive_expect_tx(&full_bar[slot], units * 1024 + sf_bytes);
-                        bulk_load(smem_b + slot * b_bytes, p.image + (before * p.kblocks + kb * units) * 1024, units * 1024,
-                                  &full_bar[slot]);
-                        bulk_load(smem_sfb + slot * SB * 512,
-                                  p.image_sf + (static_cast<int64_t>(z) * p.kblocks + kb) * SB * 512, sf_bytes,
-                                  &full_bar[slot]);
-                    }
-                    __syncwarp();
+                    const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
+                    const int units = image_units(PIECES, tok);
+                    const int64_t before = MODE >= kUp ? seg.unit[z] : 0;
+                    const uint32_t sf_bytes = DIGITS ? 1024u : tok < 16 ? 32u * tok : 512u;
+                    mbar_arrive_expect_tx_if(one, &full_bar[slot], units * 1024 + sf_bytes);
+                    bulk_load_if(one, smem_b + slot * b_bytes, p.image + (before * p.kblocks + kb * units) * 1024,
+                                 units * 1024, &full_bar[slot]);
+                    bulk_load_if(one, smem_sfb + slot * SB * 512,
+                                 p.image_sf + (static_cast<int64_t>(z) * p.kblocks + kb) * SB * 512, sf_bytes,
+                                 &full_bar[slot]);
                     if (++kb == p.kblocks) { kb = 0; ++z; }
                     if (++slot == S) { slot = 0; phase ^= 1; }
                 }
