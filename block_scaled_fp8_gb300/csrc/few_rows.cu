@@ -49,8 +49,9 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     // (split results of more than 8 KB go to the ring: one more wait, but no stage less)
     if (plan.split > 1 && a.out_bytes > 8192) a.out_bytes = 0;
     a.ahead = kAhead / (HALVES * (W == kFp4 ? 8192 : 16384)) / plan.occ;
-    const int fixed = FewConfig::smem_bytes(W, HALVES, a.cap, 0, a.out_bytes, tables);
-    const int stage = FewConfig::stage_bytes(W, HALVES, a.cap);
+    const int tokens = a.tokens < a.cap ? a.tokens : a.cap;   // of a tile, at most
+    const int fixed = FewConfig::smem_bytes(W, HALVES, tokens, 0, a.out_bytes, tables);
+    const int stage = FewConfig::stage_bytes(W, HALVES, tokens);
     const int limit = plan.occ == 2 ? kSmemTwo : kSmemOne;
     int stages = (limit - fixed) / stage;
     if (stages > FewConfig::kMaxStages) stages = FewConfig::kMaxStages;
@@ -58,10 +59,11 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     const int set = HALVES * pieces_of(W) * a.cap, most = plan.occ == 2 ? 256 : 512;
     const int sf = 2 * HALVES * 8 * scale_blocks(W) + (MODE == kDown ? HALVES * ((a.tokens + 7) & ~7) : 0);
     a.stages = stages;
+    a.b_rows = FewConfig::b_rows(W, tokens);
     a.accs = (plan.split == 1 || MODE == kDown) && 2 * set + sf <= most ? 2 : 1;
     a.tmem_cols = pow2_at_least(a.accs * set + sf);
     if (a.tmem_cols > 512) return cudaErrorInvalidConfiguration;
-    const int smem = FewConfig::smem_bytes(W, HALVES, a.cap, stages, a.out_bytes, tables);
+    const int smem = FewConfig::smem_bytes(W, HALVES, tokens, stages, a.out_bytes, tables);
     auto kernel = dg_few_rows_kernel<W, HALVES, MODE>;
     static std::atomic<uint64_t> ready{0};   // devices whose attributes are set
     int dev = 0;
@@ -89,7 +91,7 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = plan.split > 1 ? 2 : 1;
-    host_set_last_config(HALVES * 128, pieces_of(W) * a.cap, stages, grid, MODE < kUp ? 3 : 5,
+    host_set_last_config(HALVES * 128, a.b_rows, stages, grid, MODE < kUp ? 3 : 5,
                          MODE == kGemv ? 1 : MODE < kDown ? 2 : a.launches);
     return cudaLaunchKernelEx(&cfg, kernel, map, a);
 }
@@ -191,9 +193,13 @@ bool direct(int64_t m) { return m <= 2; }
 int capacity(int tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
 
 // Tokens of a segment at most: room for twice the mean number of tokens of an expert (the
-// tokens beyond make another segment, which reads the expert's weights again).
+// tokens beyond make another segment, which reads the expert's weights again).  Less room
+// leaves more of the ring to the weights, and up to 8 tokens their packed form.  FP4, top 8 of
+// 64 experts, 64 tokens (mean 8), 7168 x 2048: routed evenly 253 us with room for 16, 266 us
+// for 32 and 269 us for 8; with some experts at 57 tokens 266, 264 and 277 us; all tokens to
+// the same 8 experts 112, 89 and 141 us.  32 tokens: 239 us with room for 8, 243 us for 16.
 int segment_capacity(int64_t t, int64_t topk, int64_t experts) {
-    const int64_t most = 2 * t * topk / experts + 4;
+    const int64_t most = 2 * t * topk / experts;
     return capacity(static_cast<int>(most < t ? most : t));
 }
 

@@ -110,6 +110,7 @@ struct FewArgs {
     int32_t *status;
     uint64_t timeout_ns;
     uint32_t debug_flags;
+    int b_rows;             // of the narrow operand, in shared memory
     int launches;           // kernels of the call (host only)
 };
 
@@ -121,8 +122,10 @@ struct FewConfig {
     static constexpr int kAlign = 1024;
     static constexpr int kBarBytes = 512;
     static constexpr int kMaxStages = 24;
-    static int stage_bytes(int w, int halves, int cap) {
-        return halves * 16384 + pieces_of(w) * cap * 128 + (halves + 1) * 512 * scale_blocks(w);
+    // Rows of the narrow operand for up to `tokens` tokens: whole MMA column steps.
+    static int b_rows(int w, int tokens) { return (pieces_of(w) * tokens + 15) / 16 * 16; }
+    static int stage_bytes(int w, int halves, int tokens) {
+        return halves * 16384 + b_rows(w, tokens) * 128 + (halves + 1) * 512 * scale_blocks(w);
     }
     // Two buffers of 8 tokens' FP32 results; of a split tile, what this CTA puts out (rows of
     // 32 items of 4 results, shared out to the cluster's CTAs) from each of its CTAs.
@@ -131,8 +134,8 @@ struct FewConfig {
         const int rows = cols * (is_up(mode) ? 1 : halves);
         return (rows + split - 1) / split * split * 32 * 4 * (is_up(mode) ? 8 : 4);
     }
-    static int smem_bytes(int w, int halves, int cap, int stages, int out, int tables) {
-        return kAlign + stages * stage_bytes(w, halves, cap) + out + kBarBytes + tables;
+    static int smem_bytes(int w, int halves, int tokens, int stages, int out, int tables) {
+        return kAlign + stages * stage_bytes(w, halves, tokens) + out + kBarBytes + tables;
     }
 };
 
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     const int nsplit = static_cast<int>(cluster_nctarank());
     const int S = p.stages;
     const int ncols = PIECES * p.cap;
-    const int b_bytes = ncols * 128;
+    const int b_bytes = p.b_rows * 128;
     uint8_t *smem_a = smem;
     uint8_t *smem_b = smem_a + S * HALVES * 16384;
     uint8_t *smem_sfa = smem_b + S * b_bytes;
