@@ -185,10 +185,10 @@ struct Dependent {
 };
 
 // Rows that every CTA of a product splits by itself, without the split kernel's launch and
-// workspace: 1 x 2112 x 7168 takes 7.0 us so and 8.1 us with it; with 4 rows the CTAs' own
-// splitting is what bounds large products (1 x 131064 x 7168 FP4 85 us either way, 4 rows
-// 124 us so and 86 us with it).
-bool direct(int64_t m) { return m <= 2; }
+// workspace.  FP8, 3 rows, 2112 x 7168: 6.7 us so and 8.2 us with it, 8 rows 7.8 and 8.6 us (4096
+// x 7168 10.8 and 10.9, 65536 x 7168 75.7 and 75.4, 12 rows 100 and 77 us).  The eight digits of
+// FP4's take longer: 2 rows, 4096 x 7168 7.7 us so, 3 rows 9.3 and 8.6 us, 8 rows 14.2 and 8.9 us.
+bool direct(int w, int64_t m) { return m <= (w == kFp4Packed ? 2 : 8); }
 
 int capacity(int tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
 
@@ -228,9 +228,9 @@ struct SegmentBounds {
 }  // namespace
 
 int64_t few_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    if (direct(m)) return 0;
     int64_t most = 0;   // of either weight type
     for (int w : {static_cast<int>(kFp8), format_of(true, capacity(static_cast<int>(m)))}) {
+        if (direct(w, m)) continue;
         const int64_t blocks = (k + block_k(w) - 1) / block_k(w);
         const int64_t bytes = blocks * (image_units(pieces_of(w), static_cast<int>(m)) * 1024 + scale_blocks(w) * 512);
         if (bytes > most) most = bytes;
@@ -284,7 +284,7 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream
         else if (p.m > 8) plan = {2, 1, 1};
     }
     a.row_tiles = cdiv(p.n, 128 * plan.halves);
-    if (direct(p.m)) return launch_mode<kGemv>(w, map, a, plan, a.row_tiles, num_sms, stream);
+    if (direct(w, p.m)) return launch_mode<kGemv>(w, map, a, plan, a.row_tiles, num_sms, stream);
     uint8_t *image = p.workspace;
     uint8_t *image_sf = image + static_cast<int64_t>(a.kblocks) * image_units(pieces_of(w), p.m) * 1024;
     const int rows = 256 * 8 / block_k(w);   // rows' K-blocks of a CTA

@@ -846,6 +846,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
             const int teams = S < FewConfig::b_warps(MODE) ? S : FewConfig::b_warps(MODE);
             const int bw = warp - FIRST_B;
             constexpr int LANES = BLOCK_K / 8, AT_ONCE = 32 / LANES;   // of a row, and rows of a warp
+            constexpr int STEPS = !DIGITS ? 4 : MODE == kGemv ? 2 : 1;
             const int q = lane % LANES;
             int g = 0;   // K-blocks of the tiles before
             for (int w = first_tile; w < num_tiles && bw < teams; w += tile_step, g += k_end - k_begin) {
@@ -854,16 +855,25 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                     const int slot = (g + i) % S;
                     if (!mbar_wait_warp(&empty_bar[slot], (((g + i) / S) & 1) ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
                     const int at = (k_begin + i) * BLOCK_K + q * 8;
-                    for (int t0 = 0; t0 < tile.ntok; t0 += AT_ONCE) {
-                        const int t = t0 + lane / LANES;
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (t < tile.ntok && (!DIGITS || at < p.slices * 128)) {
-                            const int row = UP ? seg.token[seg.first[tile.seg] + t] : t;
-                            v = __ldcg(reinterpret_cast<const uint4 *>(p.x + row * p.ldx + at));
+                    for (int t0 = 0; t0 < tile.ntok; t0 += STEPS * AT_ONCE) {
+                        uint4 v[STEPS];   // the loads of some steps, then their splitting
+#pragma unroll
+                        for (int r = 0; r < STEPS; ++r) {
+                            const int t = t0 + r * AT_ONCE + lane / LANES;
+                            v[r] = make_uint4(0u, 0u, 0u, 0u);
+                            if (t < tile.ntok && (!DIGITS || at < p.slices * 128)) {
+                                const int row = UP ? seg.token[seg.first[tile.seg] + t] : t;
+                                v[r] = __ldcg(reinterpret_cast<const uint4 *>(p.x + row * p.ldx + at));
+                            }
                         }
                         __syncwarp();
-                        split_row<W>(v, smem_b + slot * b_bytes, smem_sfb + slot * SB * 512, t, q, t < tile.ntok);
-                        __syncwarp();
+#pragma unroll
+                        for (int r = 0; r < STEPS; ++r) {
+                            const int t = t0 + r * AT_ONCE + lane / LANES;
+                            if (t0 + r * AT_ONCE >= tile.ntok) break;
+                            split_row<W>(v[r], smem_b + slot * b_bytes, smem_sfb + slot * SB * 512, t, q, t < tile.ntok);
+                            __syncwarp();
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
