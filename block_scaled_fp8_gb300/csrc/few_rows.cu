@@ -152,16 +152,20 @@ const int *resident_clusters(int num_sms) {
 // (more of the latency of a CTA's start and end overlaps).  A second wave of clusters costs
 // more than any split gains (24576 x 1536, 192 tiles: 7.4 us unsplit, 13 us in pairs).
 // `tight`: whether clusters may take all of that residence.  A kernel starts while CTAs of
-// the ones around it still hold SMs, and clusters that find no room then make a second wave:
-// 56 tiles in clusters of 5 fit the GPU exactly, and 7168 x 2048 (3 K-blocks a CTA) takes 9.6 us
-// so and 5.6 us in clusters of 4, but 7168 x 16384 (26) 15.5 and 17.1 us.
+// the ones around it still hold SMs, and clusters that find no room then make a second wave,
+// which costs most where a CTA has little to do (7168 x 2048, 56 tiles in clusters of 5, 3 K-blocks
+// a CTA: 9.6 us, 5.6 us in clusters of 4).  With more to do, clusters of up to 4 find their room:
+// 72 tiles of 16 x 9216 x 4096 FP4 take 9.7 us in clusters of 4 and 11.8 us of 3; larger ones need
+// that many free SMs of one GPC at once and often do not: 1 x 7168 x 16384 18.5 us in clusters of
+// 5 and 13.3 us of 4 (FP8 28.1 and 21.8; 16 rows 16.7 and 17.7).
 int choose_split(int tiles, int kblocks, int occ, int num_sms, bool tight) {
     const int *clusters = resident_clusters(num_sms);
     int best = 1;
     int64_t best_cost = -1;
     for (int s = 1; s <= kMaxSplit && s <= kblocks; ++s) {
         const bool full = tight && kblocks >= 8 * s;
-        if (s > 1 && (tiles * 10 > clusters[s] * occ * (full ? 10 : 9) || tiles * s > occ * num_sms)) continue;
+        const bool fits = full ? tiles < clusters[s] * occ + (s <= 4) : tiles * 10 <= clusters[s] * occ * 9;
+        if (s > 1 && (!fits || tiles * s > occ * num_sms)) continue;
         const int64_t cost = static_cast<int64_t>(cdiv(tiles * s, num_sms)) * cdiv(kblocks, s);
         if (best_cost < 0 || cost <= best_cost) { best = s; best_cost = cost; }
     }
