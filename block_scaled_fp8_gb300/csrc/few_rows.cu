@@ -86,7 +86,7 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     const int grid = plan.split > 1 ? max_tiles * plan.split
                                     : (max_tiles < plan.occ * num_sms ? max_tiles : plan.occ * num_sms);
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(FewConfig::threads(HALVES, MODE));
+    cfg.blockDim = dim3(FewConfig::threads(W, HALVES, MODE, a.tokens));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -133,7 +133,7 @@ const int *resident_clusters(int num_sms) {
             attr[0].val.clusterDim.x = static_cast<unsigned>(c);
             attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
             cfg.gridDim = dim3(static_cast<unsigned>(c * num_sms));
-            cfg.blockDim = dim3(FewConfig::threads(1, kGemv));
+            cfg.blockDim = dim3(FewConfig::threads(kFp8, 1, kGemv));
             cfg.dynamicSmemBytes = kSmemOne;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
@@ -189,9 +189,9 @@ struct Dependent {
 };
 
 // Rows that every CTA of a product splits by itself, without the split kernel's launch and
-// workspace.  FP8, 3 rows, 2112 x 7168: 6.7 us so and 8.2 us with it, 8 rows 7.8 and 8.6 us (4096
-// x 7168 10.8 and 10.9, 65536 x 7168 75.7 and 75.4, 12 rows 100 and 77 us).  The eight digits of
-// FP4's take longer: 2 rows, 4096 x 7168 7.7 us so, 3 rows 9.3 and 8.6 us, 8 rows 14.2 and 8.9 us.
+// workspace.  FP8, 3 rows, 2112 x 7168: 6.6 us so and 8.2 us with it, 8 rows 7.5 and 8.6 us (4096
+// x 7168 10.1 and 10.9, 65536 x 7168 75.1 and 75.4, 12 rows 100 and 77 us).  The eight digits of
+// FP4's take longer: 2 rows, 4096 x 7168 7.3 us so, 3 rows 8.8 and 8.6 us, 8 rows 13.8 and 8.9 us.
 bool direct(int w, int64_t m) { return m <= (w == kFp4Packed ? 2 : 8); }
 
 int capacity(int tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }

@@ -117,8 +117,17 @@ struct FewArgs {
 struct FewConfig {
     static constexpr int kFirstEpi = 2;
     static constexpr int first_b(int halves) { return halves == 2 ? 7 : 6; }
-    static constexpr int b_warps(int mode) { return splits_itself(mode) ? 4 : 1; }
-    static constexpr int threads(int halves, int mode) { return 32 * (first_b(halves) + b_warps(mode)); }
+    // kGemv: with rows for more than one, two warps share a K-block's between them (8 x 4096 x
+    // 7168 FP8 10.8 -> 10.2 us, 2 x 7168 x 16384 FP4 14.1 -> 13.7).
+    static constexpr int members(int w, int mode, int tokens) {
+        return mode == kGemv && tokens > 256 / block_k(w) ? 2 : 1;
+    }
+    static constexpr int b_warps(int w, int mode, int tokens) {
+        return splits_itself(mode) ? 4 * members(w, mode, tokens) : 1;
+    }
+    static constexpr int threads(int w, int halves, int mode, int tokens = kMaxFewRows) {
+        return 32 * (first_b(halves) + b_warps(w, mode, tokens));
+    }
     static constexpr int kAlign = 1024;
     static constexpr int kBarBytes = 512;
     static constexpr int kMaxStages = 24;
@@ -490,14 +499,14 @@ struct FewTile {
 };
 
 template <int W, int HALVES, int MODE>
-__global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
+__global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
     dg_few_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ FewArgs p) {
     constexpr bool UP = is_up(MODE), SELF = splits_itself(MODE);
     constexpr int ROWS = HALVES * 128;
     constexpr int OUT = UP ? 128 : ROWS;     // results per token and tile
-    constexpr int NT = FewConfig::threads(HALVES, MODE);
     constexpr int FIRST_B = FewConfig::first_b(HALVES);
     constexpr bool DIGITS = W == kFp4Packed;
+    const int members = FewConfig::members(W, MODE, p.tokens);
     constexpr int PIECES = pieces_of(W), SB = scale_blocks(W), BLOCK_K = block_k(W);
     constexpr int SF = 4 * SB + 4 * SB;               // TMEM columns of a K-block's scales: weights', activations'
     extern __shared__ uint8_t smem_raw[];
@@ -540,9 +549,9 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
     };
     if constexpr (MODE == kUp || MODE == kDown) load_slot();
     if (warp == 0) {
-        // arrivals: full 2 (weights, pieces), empty and tfull one per issuer, tempty 4, drain 1
+        // arrivals: full one for weights and `members` for pieces, empty and tfull one per issuer, tempty 4, drain 1
         for (int i = lane; i < 2 * S + 4 + HALVES; i += 32)
-            mbar_init(bars + i, i < S ? 2 : i < 2 * S + 2 ? HALVES : i < 2 * S + 4 ? 4 : 1);
+            mbar_init(bars + i, i < S ? 1 + members : i < 2 * S + 2 ? HALVES : i < 2 * S + 4 ? 4 : 1);
         if (lane == 0) {
             *abort_flag = 0;
             tma_prefetch_desc(&tm_w);
@@ -843,10 +852,10 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
             // wait for the MMAs of block g - S tests one parity bit, which is unambiguous
             // only if block g - 2S is known to be done; a warp's previous block g - teams
             // implies that up to block g - teams - S.
-            const int teams = S < FewConfig::b_warps(MODE) ? S : FewConfig::b_warps(MODE);
-            const int bw = warp - FIRST_B;
+            const int teams = S < 4 ? S : 4;
+            const int bw = (warp - FIRST_B) >> (members - 1), member = (warp - FIRST_B) & (members - 1);
             constexpr int LANES = BLOCK_K / 8, AT_ONCE = 32 / LANES;   // of a row, and rows of a warp
-            constexpr int STEPS = !DIGITS ? 4 : MODE == kGemv ? 2 : 1;
+            constexpr int STEPS = MODE == kGemv ? 2 : DIGITS ? 1 : 4;
             const int q = lane % LANES;
             int g = 0;   // K-blocks of the tiles before
             for (int w = first_tile; w < num_tiles && bw < teams; w += tile_step, g += k_end - k_begin) {
@@ -855,11 +864,11 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                     const int slot = (g + i) % S;
                     if (!mbar_wait_warp(&empty_bar[slot], (((g + i) / S) & 1) ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
                     const int at = (k_begin + i) * BLOCK_K + q * 8;
-                    for (int t0 = 0; t0 < tile.ntok; t0 += STEPS * AT_ONCE) {
+                    for (int t0 = member * AT_ONCE; t0 < tile.ntok; t0 += STEPS * members * AT_ONCE) {
                         uint4 v[STEPS];   // the loads of some steps, then their splitting
 #pragma unroll
                         for (int r = 0; r < STEPS; ++r) {
-                            const int t = t0 + r * AT_ONCE + lane / LANES;
+                            const int t = t0 + r * members * AT_ONCE + lane / LANES;
                             v[r] = make_uint4(0u, 0u, 0u, 0u);
                             if (t < tile.ntok && (!DIGITS || at < p.slices * 128)) {
                                 const int row = UP ? seg.token[seg.first[tile.seg] + t] : t;
@@ -869,8 +878,8 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
                         __syncwarp();
 #pragma unroll
                         for (int r = 0; r < STEPS; ++r) {
-                            const int t = t0 + r * AT_ONCE + lane / LANES;
-                            if (t0 + r * AT_ONCE >= tile.ntok) break;
+                            const int t = t0 + r * members * AT_ONCE + lane / LANES;
+                            if (t0 + r * members * AT_ONCE >= tile.ntok) break;
                             split_row<W>(v[r], smem_b + slot * b_bytes, smem_sfb + slot * SB * 512, t, q, t < tile.ntok);
                             __syncwarp();
                         }
@@ -1095,7 +1104,7 @@ __global__ void __launch_bounds__(FewConfig::threads(HALVES, MODE), 2)
         const FewTile tile = get_tile(first_tile);
         const int share = share_of(tile);
         const int rows = min(share, tile.ntok * ROW_GROUPS - rank * share);
-        for (int row = warp; row < rows; row += NT / 32) {
+        for (int row = warp; row < rows; row += blockDim.x / 32) {
             float o[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
