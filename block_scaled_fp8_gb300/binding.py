@@ -9,6 +9,8 @@ been built (block_scaled_fp8_gb300.build) -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -437,18 +439,32 @@ def dg_m_grouped_fp8_gemm_nt_masked(a, sfa, b, sfb, d, masked_m, expected_m: int
 
 # --------------------------------------------------------------------- decode: few rows, routing, the MoE layer
 #
-# Calls of a few microseconds: these marshal with as few Python steps as they can
-# (plain integers for the pointers, the raw handle of the current stream).
+# Calls of a few microseconds: their arguments are checked and marshalled in C
+# (csrc/marshal.c), through the tensors' own methods.  A wrong dtype, shape or layout raises
+# AssertionError, what the library refuses DGError.
 
-def _ld(t) -> int:
-    """Row stride in elements; a single row's own length where its stride says nothing."""
-    return t.stride(0) if t.size(0) > 1 else max(t.stride(0), t.size(1))
+_marshal = None
 
 
-def _raw_stream(stream, t) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _load_marshal():
+    global _marshal
+    L = lib()
+    with _lock:
+        if _marshal is None:
+            from .build import MARSHAL
+            if not os.path.exists(MARSHAL):
+                raise RuntimeError(f"{MARSHAL} is missing (run block_scaled_fp8_gb300.build.build())")
+            loader = importlib.machinery.ExtensionFileLoader("dg_marshal", MARSHAL)
+            m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("dg_marshal", MARSHAL, loader=loader))
+            loader.exec_module(m)
+            fns = ("dg_bf16_fp4_gemv_nt", "dg_bf16_fp8_gemv_nt", "dg_bf16_fp4_gemv_nt_f32", "dg_bf16_fp8_gemv_nt_f32",
+                   "dg_moe_route", "dg_moe_fp4_layer", "dg_moe_fp8_layer", "dg_bf16_gemv_workspace_bytes",
+                   "dg_moe_layer_workspace_bytes")
+            m.setup(tuple(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in fns),
+                    (torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.uint8, torch.int32),
+                    torch._C._cuda_getCurrentRawStream, _workspace)
+            _marshal = m
+    return _marshal
 
 
 def _fail(fn: str, status: int):
@@ -481,59 +497,40 @@ def gemv_workspace_bytes(m: int, n: int, k: int) -> int:
     return int(lib().dg_bf16_gemv_workspace_bytes(m, n, k))
 
 
-def _gemv(fn: str, fp4: bool, dtype, a, b, sfb, d, c, workspace, status, stream):
-    m, k = a.shape
-    n, kb = b.shape
-    lda, sa = a.stride()
-    ldb, sb = b.stride()
-    ldd, sd = d.stride()
-    assert a.dtype is torch.bfloat16 and d.dtype is dtype and sfb.dtype is torch.int32
-    assert (b.dtype is torch.uint8 and kb * 2 == k) if fp4 else (b.dtype is torch.float8_e4m3fn and kb == k)
-    assert d.shape == (m, n) and (sd == 1 or n <= 1) and ((sa == 1 and sb == 1) or k <= 1)
-    assert sfb.is_contiguous() and sfb.numel() >= -(-k // (128 if fp4 else 512)) * ((n + 3) // 4 * 4)
-    assert c is None or (c.dtype is dtype and c.shape == d.shape and c.stride(1) == 1)
-    if m == 1:   # (a single row's stride says nothing)
-        lda, ldd = max(lda, k), max(ldd, n)
-    if n == 1:
-        ldb = max(ldb, kb)
-    L = _lib or lib()
-    ws, nbytes = None, 0
-    if workspace is not None:
-        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    elif m > 2:                          # (the fewest rows need none)
-        nbytes = L.dg_bf16_gemv_workspace_bytes(m, n, k)
-        ws = (workspace := _workspace(nbytes, d, stream)).data_ptr()
-    st = getattr(L, fn)(
-        a.data_ptr(), lda, b.data_ptr(), ldb, sfb.data_ptr(), None if c is None else c.data_ptr(),
-        0 if c is None else _ld(c), d.data_ptr(), ldd, m, n, k, ws, nbytes,
-        None if status is None else status.data_ptr(), _raw_stream(stream, d))
-    if st:
-        _fail(fn, st)
-    return d
-
-
 def dg_bf16_fp4_gemv_nt(a, b, sfb, d, c=None, workspace=None, status=None, stream=None):
     """D = C + A @ B^T for 1..64 rows: a bf16 [M, K]; b uint8 [N, K/2], two E2M1 codes
     per byte (even k in the low nibble); sfb packed int32 [K/128, align4(N)] (4 x 32
     K per word); d (and c) bf16 [M, N].  workspace: a device buffer of
     gemv_workspace_bytes(M, N, K) bytes (made here if not given)."""
-    return _gemv("dg_bf16_fp4_gemv_nt", True, torch.bfloat16, a, b, sfb, d, c, workspace, status, stream)
+    st = (_marshal or _load_marshal()).gemv(0, a, b, sfb, d, c, workspace, status, stream)
+    if st:
+        _fail("dg_bf16_fp4_gemv_nt", st)
+    return d
 
 
 def dg_bf16_fp8_gemv_nt(a, b, sfb, d, c=None, workspace=None, status=None, stream=None):
     """As dg_bf16_fp4_gemv_nt with b float8_e4m3fn [N, K] and sfb packed int32
     [ceil(K/512), align4(N)] (4 x 128 K per word)."""
-    return _gemv("dg_bf16_fp8_gemv_nt", False, torch.bfloat16, a, b, sfb, d, c, workspace, status, stream)
+    st = (_marshal or _load_marshal()).gemv(1, a, b, sfb, d, c, workspace, status, stream)
+    if st:
+        _fail("dg_bf16_fp8_gemv_nt", st)
+    return d
 
 
 def dg_bf16_fp4_gemv_nt_f32(a, b, sfb, d, c=None, workspace=None, status=None, stream=None):
     """dg_bf16_fp4_gemv_nt with FP32 d (and c)."""
-    return _gemv("dg_bf16_fp4_gemv_nt_f32", True, torch.float32, a, b, sfb, d, c, workspace, status, stream)
+    st = (_marshal or _load_marshal()).gemv(2, a, b, sfb, d, c, workspace, status, stream)
+    if st:
+        _fail("dg_bf16_fp4_gemv_nt_f32", st)
+    return d
 
 
 def dg_bf16_fp8_gemv_nt_f32(a, b, sfb, d, c=None, workspace=None, status=None, stream=None):
     """dg_bf16_fp8_gemv_nt with FP32 d (and c)."""
-    return _gemv("dg_bf16_fp8_gemv_nt_f32", False, torch.float32, a, b, sfb, d, c, workspace, status, stream)
+    st = (_marshal or _load_marshal()).gemv(3, a, b, sfb, d, c, workspace, status, stream)
+    if st:
+        _fail("dg_bf16_fp8_gemv_nt_f32", st)
+    return d
 
 
 def dg_moe_route(logits, ids, weights, bias=None, scoring: str = "softmax", renormalize: bool = True,
@@ -541,20 +538,8 @@ def dg_moe_route(logits, ids, weights, bias=None, scoring: str = "softmax", reno
     """Top-k routing: logits [T, E] float32 or bfloat16 (unit column stride) -> ids int32
     [T, topk] and weights float32 [T, topk] (both contiguous); bias float32 [E]
     shifts the choice only.  scoring "softmax" or "sigmoid"."""
-    t, e = logits.shape
-    topk = ids.size(1)
-    f32 = logits.dtype is torch.float32
-    assert (f32 or logits.dtype is torch.bfloat16) and (logits.stride(1) == 1 or e == 1)
-    assert ids.dtype is torch.int32 and ids.size(0) == t and ids.is_contiguous()
-    assert weights.dtype is torch.float32 and weights.shape == ids.shape and weights.is_contiguous()
-    assert bias is None or (bias.dtype is torch.float32 and bias.shape == (e,) and bias.is_contiguous())
     assert scoring == "softmax" or scoring == "sigmoid"
-    L = _lib or lib()
-    st = L.dg_moe_route(
-        logits.data_ptr(), _ld(logits), DG_LOGITS_F32 if f32 else DG_LOGITS_BF16,
-        None if bias is None else bias.data_ptr(), ids.data_ptr(), weights.data_ptr(), t, e, topk,
-        DG_SCORE_SIGMOID if scoring == "sigmoid" else DG_SCORE_SOFTMAX, renormalize, scale,
-        _raw_stream(stream, logits))
+    st = (_marshal or _load_marshal()).route(logits, ids, weights, bias, scoring == "sigmoid", renormalize, scale, stream)
     if st:
         _fail("dg_moe_route", st)
     return ids, weights
@@ -564,43 +549,22 @@ def moe_layer_workspace_bytes(t: int, topk: int, h: int, i: int, experts: int) -
     return int(lib().dg_moe_layer_workspace_bytes(t, topk, h, i, experts))
 
 
-def _moe_layer(fn: str, fp4: bool, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream):
-    t, h = x.shape
-    topk = ids.size(1)
-    e, i2, hp = w1.shape
-    i = i2 // 2
-    code, per, sl = (torch.uint8, 2, 128) if fp4 else (torch.float8_e4m3fn, 1, 512)
-    assert x.dtype is torch.bfloat16 and y.dtype is torch.bfloat16 and x.stride(1) == 1 and y.stride(1) == 1
-    assert ids.dtype is torch.int32 and ids.size(0) == t and ids.is_contiguous()
-    assert weights.dtype is torch.float32 and weights.shape == ids.shape and weights.is_contiguous()
-    assert w1.dtype is code and w1.is_contiguous() and i2 == 2 * i and hp * per == h
-    assert w2.dtype is code and w2.is_contiguous() and w2.shape == (e, h, i // per)
-    assert sf1.dtype is torch.int32 and sf1.is_contiguous() and sf1.numel() >= e * -(-h // sl) * 2 * i
-    assert sf2.dtype is torch.int32 and sf2.is_contiguous() and sf2.numel() >= e * -(-i // sl) * h
-    assert y.shape == x.shape and (c is None or (c.dtype is torch.bfloat16 and c.shape == x.shape and c.stride(1) == 1))
-    L = _lib or lib()
-    if workspace is None:
-        workspace = _workspace(max(16, L.dg_moe_layer_workspace_bytes(t, topk, h, i, e)), y, stream)
-    st = getattr(L, fn)(
-        x.data_ptr(), _ld(x), ids.data_ptr(), weights.data_ptr(), w1.data_ptr(), sf1.data_ptr(), w2.data_ptr(),
-        sf2.data_ptr(), None if c is None else c.data_ptr(), 0 if c is None else _ld(c), y.data_ptr(), _ld(y), t, h, i, e,
-        topk, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        None if status is None else status.data_ptr(), _raw_stream(stream, y))
-    if st:
-        _fail(fn, st)
-    return y
-
-
 def dg_moe_fp4_layer(x, ids, weights, w1, sf1, w2, sf2, y, c=None, workspace=None, status=None, stream=None):
     """y = c + sum_j weights[:, j] * W2[e] (silu(W1g[e] x) * (W1u[e] x)), e = ids[:, j] (negative:
     empty slot), for 1..64 tokens.  x bf16 [T, H]; ids int32 and weights float32 [T, topk];
     w1 uint8 [E, 2I, H/2] (gate rows, then up rows) and w2 uint8 [E, H, I/2], packed E2M1;
     sf1 packed int32 [E, H/128, 2I], sf2 [E, I/128, H]; y (and c) bf16 [T, H].  workspace:
     a device buffer of moe_layer_workspace_bytes(T, topk, H, I, E) bytes (made here if not given)."""
-    return _moe_layer("dg_moe_fp4_layer", True, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream)
+    st = (_marshal or _load_marshal()).layer(True, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream)
+    if st:
+        _fail("dg_moe_fp4_layer", st)
+    return y
 
 
 def dg_moe_fp8_layer(x, ids, weights, w1, sf1, w2, sf2, y, c=None, workspace=None, status=None, stream=None):
     """As dg_moe_fp4_layer with float8_e4m3fn w1 [E, 2I, H] and w2 [E, H, I], and scales packed
     4 x 128 K per word: sf1 [E, ceil(H/512), 2I], sf2 [E, ceil(I/512), H]."""
-    return _moe_layer("dg_moe_fp8_layer", False, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream)
+    st = (_marshal or _load_marshal()).layer(False, x, ids, weights, w1, sf1, w2, sf2, y, c, workspace, status, stream)
+    if st:
+        _fail("dg_moe_fp8_layer", st)
+    return y

@@ -1,7 +1,9 @@
 """Builds the CUDA library in-tree: block_scaled_fp8_gb300/_build/libdg_gb300.so.
 
 Every translation unit under csrc/ is compiled for sm_103a only, in parallel,
-then linked into one shared library against the shared CUDA runtime.
+then linked into one shared library against the shared CUDA runtime.  The
+marshalling of the binding's decode calls (csrc/marshal.c, a Python extension
+without CUDA) is built beside it.
 """
 from __future__ import annotations
 
@@ -11,11 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libdg_gb300.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.c")
+MARSHAL = os.path.join(BUILD, "dg_marshal" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr"]
@@ -34,7 +39,7 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(CSRC, "*.h")) + [os.path.join(HERE, "..", "include", "dg.h"), __file__]
+        os.path.join(CSRC, "*.h")) + [MARSHAL_SRC, os.path.join(HERE, "..", "include", "dg.h"), __file__]
 
 
 def strip_comments(src: str) -> str:
@@ -87,9 +92,9 @@ def source_digest() -> str:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(MARSHAL)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -109,9 +114,20 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
+    def compile_marshal():
+        tmp = MARSHAL + f".tmp{os.getpid()}"
+        cmd = [os.environ.get("CC") or "gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", sysconfig.get_paths()["include"],
+               "-I", os.path.join(HERE, "..", "include"), MARSHAL_SRC, "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, MARSHAL)
+
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+        marshal = ex.submit(compile_marshal)
         results = list(ex.map(compile_one, srcs))
+        marshal.result()
     if verbose or ptxas_verbose:
         for _, log in results:
             if log.strip():
