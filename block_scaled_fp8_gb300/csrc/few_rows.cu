@@ -38,7 +38,7 @@ bool encode_weights(CUtensorMap *map, int w, const void *base, int64_t rows, int
 // How a launch fills the GPU: `occ` CTAs on an SM; `split` CTAs of a cluster share a
 // tile's K (1: persistent CTAs take the tiles in turn).
 struct Plan {
-    int halves, occ, split;
+    int occ, split;
 };
 
 template <int W, int HALVES, int MODE>
@@ -104,13 +104,6 @@ cudaError_t launch_fmt(int w, const CUtensorMap &map, FewArgs &a, const Plan &pl
     // (rows few enough for a kernel to split them itself have their FP4 weights packed)
     if constexpr (!splits_itself(MODE)) return launch<kFp4, HALVES, MODE>(map, a, plan, max_tiles, num_sms, stream);
     return cudaErrorInvalidValue;
-}
-
-template <int MODE>
-cudaError_t launch_mode(int w, const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles, int num_sms,
-                        cudaStream_t stream) {
-    return plan.halves == 2 ? launch_fmt<2, MODE>(w, map, a, plan, max_tiles, num_sms, stream)
-                            : launch_fmt<1, MODE>(w, map, a, plan, max_tiles, num_sms, stream);
 }
 
 // Clusters of 1..kMaxSplit CTAs that are resident at once with one CTA on an SM (the SMs
@@ -278,17 +271,19 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream
     a.debug_flags = p.debug_flags;
     // The split of K depends on n, k and the format alone, so a row's result does not depend on
     // the other rows of the call.
-    Plan plan = {1, 2, choose_split(cdiv(p.n, 128), a.kblocks, 2, num_sms, true)};
-    if (plan.split == 1) {
-        // Many tiles.  Two CTAs of 128-row tiles on an SM, or one of 256-row tiles, which reads the
-        // activations' image half as often and keeps more loads in flight beside a wide one:
-        // 131064 x 7168 FP4, 8 rows 86 and 89 us, 16 rows 92 and 90, 32 rows 95 and 94; with 64 rows
-        // neither has room for its ring, and one CTA of 128-row tiles takes 111 us (122, 129).
-        if (p.m > 32) plan.occ = 1;
-        else if (p.m > 8) plan = {2, 1, 1};
-    }
-    a.row_tiles = cdiv(p.n, 128 * plan.halves);
-    if (direct(w, p.m)) return launch_mode<kGemv>(w, map, a, plan, a.row_tiles, num_sms, stream);
+    a.row_tiles = cdiv(p.n, 128);
+    Plan plan = {2, choose_split(a.row_tiles, a.kblocks, 2, num_sms, true)};
+    // Many tiles: two CTAs on an SM, except where, after whole rounds of them, so few tiles are left
+    // that an SM has one, and its ring is half as deep as one CTA's.  1024 tiles (131064 x 7168
+    // FP4, 112 left): two CTAs 82.4 and one 79.7 us at 8 rows, 90.6 and 85.4 at 16; 512 (208 left): 48.2
+    // and 50.6 at 16 rows; 352 (48 left) 43.8 and 39.0.  Rings of two CTAs are too short beside more
+    // than 32 rows: 64 rows, 1024 tiles 123 and 106 us, 512 tiles 64.2 and 61.9.  With one round
+    // (192 tiles) two CTAs are better all the same: 13.8 and 15.5 us at 64 rows; and where CTAs split
+    // the rows themselves: 62 and 67 us at 8 rows of FP8, 352 tiles.
+    const int left = a.row_tiles % (2 * num_sms);
+    if (plan.split == 1 && a.row_tiles > 2 * num_sms && !direct(w, p.m) && (p.m > 32 || (left > 0 && left <= num_sms)))
+        plan.occ = 1;
+    if (direct(w, p.m)) return launch_fmt<1, kGemv>(w, map, a, plan, a.row_tiles, num_sms, stream);
     uint8_t *image = p.workspace;
     uint8_t *image_sf = image + static_cast<int64_t>(a.kblocks) * image_units(pieces_of(w), p.m) * 1024;
     const int rows = 256 * 8 / block_k(w);   // rows' K-blocks of a CTA
@@ -298,7 +293,7 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream
     if (e != cudaSuccess) return e;
     a.image = image;
     a.image_sf = image_sf;
-    return launch_mode<kGemvPre>(w, map, a, plan, a.row_tiles, num_sms, stream);
+    return launch_fmt<1, kGemvPre>(w, map, a, plan, a.row_tiles, num_sms, stream);
 }
 
 cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t stream) {
@@ -323,11 +318,8 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.status = p.status;
     a.timeout_ns = p.timeout_ns;
     a.debug_flags = p.debug_flags;
-    Plan down;
-    down.halves = 1;
-    down.occ = 2;
-    const int down_tiles = cdiv(p.h, 128 * down.halves);
-    down.split = choose_split(down_tiles, ki * static_cast<int>(bounds.count), down.occ, num_sms, false);
+    const int down_tiles = cdiv(p.h, 128);
+    const Plan down = {2, choose_split(down_tiles, ki * static_cast<int>(bounds.count), 2, num_sms, false)};
     // up: a tile is 128 columns of h of one segment
     a.image = x_image;
     a.image_sf = x_sf;
@@ -342,10 +334,7 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.kblocks = kh;
     a.row_tiles = p.i / 128;
     const int up_tiles = static_cast<int>(bounds.count) * a.row_tiles;
-    Plan up;
-    up.halves = 2;
-    up.occ = 1;
-    up.split = choose_split(up_tiles, kh, up.occ, num_sms, false);
+    const Plan up = {1, choose_split(up_tiles, kh, 1, num_sms, false)};
     // With no more tokens than experts, counting a token once per slot, the up kernel splits x
     // itself, a launch less: 1 token, top 8 of 64 experts, 7168 x 2048 FP4 40.6 us so and 40.8 us
     // with the split kernel, FP8 (of 32) 61.8 and 63.2 us, 2 tokens, top 2 of 8, 1024 x 512 12.8
@@ -385,7 +374,7 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.d = p.y;
     a.ldd = p.ldy;
     a.debug_flags = 0;
-    return launch_mode<kDown>(w, map2, a, down, a.row_tiles, num_sms, stream);
+    return launch_fmt<1, kDown>(w, map2, a, down, a.row_tiles, num_sms, stream);
 }
 
 }  // namespace dg
