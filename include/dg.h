@@ -468,14 +468,14 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
 /*
  * dg_moe_fp4_layer / dg_moe_fp8_layer -- a whole mixture-of-experts layer for a
  * few tokens (a decode step), from bf16 activations and the routing to bf16 output,
- * in three launches.  With e = ids[t][j]:
+ * in two launches, or three.  With e = ids[t][j]:
  *
  *   h(t,j)[i] = silu(sum_k W1[e][i][k] x[t][k]) * (sum_k W1[e][I + i][k] x[t][k])
  *   y[t][n]   = c[t][n] + sum_j weights[t][j] * sum_i W2[e][n][i] h(t,j)[i]
  *
  *   x     bf16 [t, ldx], 16-byte aligned, ldx a multiple of 8.
  *   ids   int32 [t][topk], weights FP32 [t][topk], both dense.  A negative id is an
- *         empty slot (its weight is not read, so it may hold anything); an id >=
+ *         empty slot (its weight does not count, it may hold anything); an id >=
  *         experts counts as empty and sets DG_DEV_BAD_GROUP.  A token that names an
  *         expert twice gets it with the sum of the two weights; a token with
  *         no expert left gets y = c (or 0).
