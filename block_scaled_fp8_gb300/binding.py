@@ -256,7 +256,7 @@ def dg_fp8_gemm_nt_f32(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb:
     return d
 
 
-def _gemm_layout(fn: str, a_mn: bool, b_mn: bool, a, sfa, b, sfb, d, c, workspace, status, stream):
+def _gemm_layout(fn: str, a_mn: bool, b_mn: bool, a, sfa, b, sfb, d, c, status, stream):
     # a is [M, K] (K-contiguous) or [K, M] (M-contiguous); b is [N, K] or [K, N]
     M = a.shape[1] if a_mn else a.shape[0]
     K = a.shape[0] if a_mn else a.shape[1]
@@ -273,17 +273,17 @@ def _gemm_layout(fn: str, a_mn: bool, b_mn: bool, a, sfa, b, sfb, d, c, workspac
 
 def dg_fp8_gemm_nn(a, sfa, b, sfb, d, c=None, status=None, stream=None):
     """D = C + A @ B: a [M, K], b [K, N] (N contiguous); packed scales as for the NT call."""
-    return _gemm_layout("dg_fp8_gemm_nn", False, True, a, sfa, b, sfb, d, c, workspace, status, stream)
+    return _gemm_layout("dg_fp8_gemm_nn", False, True, a, sfa, b, sfb, d, c, status, stream)
 
 
 def dg_fp8_gemm_tn(a, sfa, b, sfb, d, c=None, status=None, stream=None):
     """D = C + A^T @ B: a [K, M] (M contiguous), b [K, N] (N contiguous)."""
-    return _gemm_layout("dg_fp8_gemm_tn", True, True, a, sfa, b, sfb, d, c, workspace, status, stream)
+    return _gemm_layout("dg_fp8_gemm_tn", True, True, a, sfa, b, sfb, d, c, status, stream)
 
 
 def dg_fp8_gemm_tt(a, sfa, b, sfb, d, c=None, status=None, stream=None):
     """D = C + A^T @ B^T: a [K, M] (M contiguous), b [N, K] (K contiguous)."""
-    return _gemm_layout("dg_fp8_gemm_tt", True, False, a, sfa, b, sfb, d, c, workspace, status, stream)
+    return _gemm_layout("dg_fp8_gemm_tt", True, False, a, sfa, b, sfb, d, c, status, stream)
 
 
 def dg_fp8_fp4_gemm_nt(a, sfa, b, sfb, d, c=None, status=None, stream=None):
