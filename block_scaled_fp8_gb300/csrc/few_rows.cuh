@@ -34,8 +34,9 @@
 //   the rest    the narrow operand.
 // Many tiles: the CTAs are persistent and take tiles in turn, the ring of K-blocks running
 // on across them.  Few tiles: one tile per cluster, K split over its CTAs.  Each CTA writes its
-// FP32 partial results into the shared memory of the CTA that puts them out, which adds them
-// in rank order: no workspace, no atomics, a fixed order, and one cluster barrier.
+// FP32 partial results into the shared memory of the CTA that puts them out, whose barrier
+// counts their bytes (a cluster barrier in its place: 1 x 2112 x 7168 5.6 us instead of 5.2),
+// and which adds them in rank order: no workspace, no atomics, a fixed order.
 //
 // Where the pieces come from: kGemv and kUpSelf, for the fewest rows, split the activations
 // themselves, four warps taking K-blocks in turn.  The other modes read an image of the narrow
@@ -55,8 +56,8 @@
 //   FP4 131064 x 7168: 1 row 76 us (6.6 TB/s), 8 rows 78, 16 rows 84, 64 rows 105 us; the DRAM
 //   traffic is the weights' and the output's alone.  FP8 65536 x 7168: 1 row 72, 16 rows 76 us.
 //   Small products are bound by the chain of latencies from the end of one kernel to the next
-//   one's last store: 1 x 1024 x 1024 4.4 us, 1 x 2112 x 7168 FP4 5.5 us.
-//   MoE layer, top 8 of 64 experts, 7168 x 2048 FP4: 1 token 38.5 us (187 MB), 16 tokens 213,
+//   one's last store: 1 x 1024 x 1024 4.2 us, 1 x 2112 x 7168 FP4 5.2 us.
+//   MoE layer, top 8 of 64 experts, 7168 x 2048 FP4: 1 token 37.7 us (187 MB), 16 tokens 213,
 //   64 tokens 250 us (1.5 GB, 6.0 TB/s).
 #pragma once
 
@@ -538,7 +539,8 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
     uint64_t *tfull_bar = bars + 2 * S;     // [2] accumulators complete
     uint64_t *tempty_bar = tfull_bar + 2;   // [2] accumulators read
     uint64_t *drain_bar = tempty_bar + 2;   // [HALVES]
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + HALVES);
+    uint64_t *join_bar = drain_bar + HALVES;   // split tiles: the results that this CTA puts out are here
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(join_bar + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *tab = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + FewConfig::kBarBytes);
 
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
     if constexpr (MODE == kUp || MODE == kDown) load_slot();
     if (warp == 0) {
         // arrivals: full one for weights and `members` for pieces, empty and tfull one per issuer, tempty 4, drain 1
-        for (int i = lane; i < 2 * S + 4 + HALVES; i += 32)
+        for (int i = lane; i < 2 * S + 4 + HALVES + 1; i += 32)
             mbar_init(bars + i, i < S ? 1 + members : i < 2 * S + 2 ? HALVES : i < 2 * S + 4 ? 4 : 1);
         if (lane == 0) {
             *abort_flag = 0;
@@ -947,8 +949,9 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
                 for (int g = 0; g < ROW_GROUPS; ++g) {
                     const uint32_t at = mapa_shared(
                         smem_u32(smem_out + ((rank * share + row) * COMP + quad) * 32 + lane), owner);
-                    st_shared_cluster_f32(at, r[g][j]);
-                    if constexpr (UP) st_shared_cluster_f32(at + 4 * 4 * 32, r[HALVES - 1][j]);
+                    const uint32_t bar = mapa_shared(smem_u32(join_bar), owner);
+                    st_async_cluster_f32(at, r[g][j], bar);
+                    if constexpr (UP) st_async_cluster_f32(at + 4 * 4 * 32, r[HALVES - 1][j], bar);
                     if (++row == share) { row = 0; ++owner; }
                 }
             }
@@ -1108,11 +1111,18 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
     }
     if (nsplit == 1) return;
     // ---------------------------------------------------------------- sum over the cluster (one tile)
-    cluster_sync();   // every CTA's results are here; nobody writes to or reads from a peer after this
     if (first_tile < num_tiles) {
         const FewTile tile = get_tile(first_tile);
         const int share = share_of(tile);
         const int rows = min(share, tile.ntok * ROW_GROUPS - rank * share);
+        if (rows <= 0) return;   // (nobody writes here)
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(join_bar, nsplit * rows * COMP * 128);
+        if (!mbar_wait_cluster_warp(join_bar, 0, ctl, DG_DEV_TIMEOUT)) {
+            // A peer may still write here: leave with it (threads that have left count as arrived).
+            cluster_arrive();
+            cluster_wait();
+            return;
+        }
         for (int row = warp; row < rows; row += blockDim.x / 32) {
             float o[4];
 #pragma unroll

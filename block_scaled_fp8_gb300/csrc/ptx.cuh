@@ -360,9 +360,12 @@ __device__ __forceinline__ void bulk_load(void *smem_dst, const void *src, uint3
                  : "memory");
 }
 
-// FP32 word to another CTA's shared memory (cluster address from mapa_shared).
-__device__ __forceinline__ void st_shared_cluster_f32(uint32_t cluster_addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+// FP32 word to another CTA's shared memory, and its 4 bytes to the transaction count of a
+// barrier there (cluster addresses from mapa_shared).
+__device__ __forceinline__ void st_async_cluster_f32(uint32_t cluster_addr, float v, uint32_t cluster_bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr),
+                 "r"(__float_as_uint(v)), "r"(cluster_bar)
+                 : "memory");
 }
 
 // ----------------------------------------------------------------- E4M3 and E2M1 conversions
