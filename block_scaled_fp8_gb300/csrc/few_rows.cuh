@@ -1124,16 +1124,13 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
             return;
         }
         for (int row = warp; row < rows; row += blockDim.x / 32) {
-            float o[4];
+            float sum[COMP] = {}, o[4];
+#pragma unroll 4
+            for (int r = 0; r < nsplit; ++r)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float s = 0.0f, u = 0.0f;
-                for (int r = 0; r < nsplit; ++r) {
-                    s += smem_out[((r * share + row) * COMP + c) * 32 + lane];
-                    if constexpr (UP) u += smem_out[((r * share + row) * COMP + 4 + c) * 32 + lane];
-                }
-                o[c] = UP ? gated(s, u) : s;
-            }
+                for (int c = 0; c < COMP; ++c) sum[c] += smem_out[((r * share + row) * COMP + c) * 32 + lane];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[c] = UP ? gated(sum[c], sum[COMP - 4 + c]) : sum[c];
             const int at = rank * share + row;
             store(tile, at / ROW_GROUPS, tile.row0 + (at % ROW_GROUPS) * 128 + 4 * lane, o);
         }
