@@ -702,7 +702,8 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
     // of the up half) that lane l of the four epilogue warps hold: ROW_GROUPS rows a token.
     // CTA r puts out rows r * share .. of them; smem_out is [CTA][share][component][32].
     constexpr int ROW_GROUPS = OUT / 128, COMP = UP ? 8 : 4;
-    auto share_of = [&](const FewTile &tile) { return (tile.ntok * ROW_GROUPS + nsplit - 1) / nsplit; };
+    const int share = nsplit > 1 && first_tile < num_tiles
+                          ? (get_tile(first_tile).ntok * ROW_GROUPS + nsplit - 1) / nsplit : 0;
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -936,12 +937,20 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
         bool pushed = false;
         uint32_t acc_phase = 0;
         grid_dependency_wait();       // C, and memory that the output may share
+        if (!UP && p.c && first_tile < num_tiles) {   // the first tile's C to L2
+            const int size = p.f32 ? 4 : 2, lines = ROWS * size / 128;
+            const int row0 = first_tile * ROWS;
+            for (int i = id; i < p.tokens * lines; i += 128) {
+                const int t = i / lines, at = i % lines * (128 / size);
+                if (row0 + at < p.rows)
+                    prefetch_l2_line(static_cast<const char *>(p.c) + (t * p.ldc + row0 + at) * size);
+            }
+        }
         // Results of this thread's operand row (of each half) for n tokens from t0, to the CTAs
         // that put them out.
         auto push = [&](const FewTile &tile, int t0, int n, const float (&r)[HALVES][8]) {
-            const int share = share_of(tile);
-            int row = t0 * ROW_GROUPS, owner = row / share;
-            row -= owner * share;
+            int row = t0 * ROW_GROUPS, owner = 0;
+            for (; row >= share; row -= share) ++owner;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 if (j >= n) break;
@@ -958,27 +967,33 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
         };
         // 8 tokens' results from t0 at this thread's operand rows: the sums of their columns
         auto read8 = [&](int t0, int n, float (&r)[HALVES][8]) {
-            constexpr int AT_ONCE = 16 / PIECES;   // tokens of 16 columns
+            constexpr int AT_ONCE = 16 / PIECES, LOADS = AT_ONCE < 8 && HALVES == 1 ? 2 : 1;   // tokens of 16 columns, loads in flight
 #pragma unroll
-            for (int j0 = 0; j0 < 8; j0 += AT_ONCE) {
+            for (int j0 = 0; j0 < 8; j0 += LOADS * AT_ONCE) {
                 if (j0 >= n) break;
-                uint32_t v[HALVES][16];
+                uint32_t v[LOADS][HALVES][16];
 #pragma unroll
-                for (int h = 0; h < HALVES; ++h)
-                    tmem_ld_32x32b_x16(tmem_base + ((quad * 32) << 16) + (acc * HALVES + h) * ncols + PIECES * (t0 + j0),
-                                       v[h]);
+                for (int l = 0; l < LOADS; ++l)
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h)
+                        if (l == 0 || j0 + l * AT_ONCE < n)
+                            tmem_ld_32x32b_x16(tmem_base + ((quad * 32) << 16) + (acc * HALVES + h) * ncols +
+                                                   PIECES * (t0 + j0 + l * AT_ONCE),
+                                               v[l][h]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int h = 0; h < HALVES; ++h) {
-                    reg_fence16(v[h]);
+                for (int l = 0; l < LOADS; ++l)
 #pragma unroll
-                    for (int j = 0; j < AT_ONCE; ++j) {
-                        float sum = __uint_as_float(v[h][PIECES * j + PIECES - 1]);   // the smallest first
+                    for (int h = 0; h < HALVES; ++h) {
+                        reg_fence16(v[l][h]);
 #pragma unroll
-                        for (int c = PIECES - 2; c >= 0; --c) sum += __uint_as_float(v[h][PIECES * j + c]);
-                        r[h][j0 + j] = sum;
+                        for (int j = 0; j < AT_ONCE; ++j) {
+                            float sum = __uint_as_float(v[l][h][PIECES * j + PIECES - 1]);   // the smallest first
+#pragma unroll
+                            for (int c = PIECES - 2; c >= 0; --c) sum += __uint_as_float(v[l][h][PIECES * j + c]);
+                            r[h][j0 + l * AT_ONCE + j] = sum;
+                        }
                     }
-                }
             }
         };
         auto release = [&] {   // the accumulators are read
@@ -1113,7 +1128,6 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
     // ---------------------------------------------------------------- sum over the cluster (one tile)
     if (first_tile < num_tiles) {
         const FewTile tile = get_tile(first_tile);
-        const int share = share_of(tile);
         const int rows = min(share, tile.ntok * ROW_GROUPS - rank * share);
         if (rows <= 0) return;   // (nobody writes here)
         if (threadIdx.x == 0) mbar_arrive_expect_tx(join_bar, nsplit * rows * COMP * 128);
