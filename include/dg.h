@@ -539,7 +539,8 @@ void dg_set_debug_flags(uint32_t flags);
 const char *dg_status_string(int status);
 
 /* Tile configuration the last GEMM call on this thread launched:
- * out[0]=BLOCK_M, out[1]=BLOCK_N, out[2]=stages, out[3]=grid size,
+ * out[0]=BLOCK_M, out[1]=BLOCK_N (kinds 3 and 5: rows of the narrow operand in
+ * shared memory), out[2]=stages, out[3]=grid size,
  * out[4]=kernel kind (0 block-scaled, 1 FP32-promotion, 2 block-scaled on
  * CTA pairs, 3 few-row product, 5 MoE layer for few tokens), out[5]=number of
  * kernel launches of that call. */
