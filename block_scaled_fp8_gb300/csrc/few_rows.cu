@@ -143,8 +143,11 @@ const int *resident_clusters(int num_sms) {
 
 // Cluster size for `tiles` tiles of `kblocks` K-blocks: of those whose clusters are all
 // resident at once, the one with the least K-blocks on the busiest SM, the larger of equals
-// (more of the latency of a CTA's start and end overlaps).  A second wave of clusters costs
-// more than any split gains (24576 x 1536, 192 tiles: 7.4 us unsplit, 13 us in pairs).
+// (more of the latency of a CTA's start and end overlaps).  Where an SM would have one CTA in the
+// room of two, its K-blocks count 1.6 times, for it has half a ring: 17 x 6144 x 8192 FP4 12.1 us in
+// clusters of 3 (144 CTAs) and 10.5 us of 5 (240), 1 x 4096 x 7168 5.6 us of 4 and 5.2 of 6 (64 x 4096 x
+// 2048 9.0 and 9.6); the layer's down kernel, 64 tokens, h = 6400: 255 us of 3 and 227 of 5.  A second wave
+// of clusters costs more than any split gains (24576 x 1536, 192 tiles: 7.4 us unsplit, 13 us in pairs).
 // `tight`: whether clusters may take all of that residence.  A kernel starts while CTAs of
 // the ones around it still hold SMs, and clusters that find no room then make a second wave,
 // which costs most where a CTA has little to do (7168 x 2048, 56 tiles in clusters of 5, 3 K-blocks
@@ -160,7 +163,8 @@ int choose_split(int tiles, int kblocks, int occ, int num_sms, bool tight) {
         const bool full = tight && kblocks >= 8 * s;
         const bool fits = full ? tiles < clusters[s] * occ + (s <= 4) : tiles * 10 <= clusters[s] * occ * 9;
         if (s > 1 && (!fits || tiles * s > occ * num_sms)) continue;
-        const int64_t cost = static_cast<int64_t>(cdiv(tiles * s, num_sms)) * cdiv(kblocks, s);
+        const int on_sm = cdiv(tiles * s, num_sms);
+        const int64_t cost = static_cast<int64_t>(on_sm < occ ? 8 : 5 * on_sm) * cdiv(kblocks, s);
         if (best_cost < 0 || cost <= best_cost) { best = s; best_cost = cost; }
     }
     return best;
