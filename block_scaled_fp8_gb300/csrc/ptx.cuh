@@ -50,19 +50,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar_addr, uint32_t parity
     return ok != 0;
 }
 
-// As mbar_try_wait, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // As mbar_try_wait, with cluster-scope acquire: for barriers that the other CTA
 // of a cluster arrives on after its own writes.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar_addr, uint32_t parity) {
@@ -352,14 +339,6 @@ __device__ __forceinline__ void bulk_wait_group() {
     asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Untiled bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned).
-__device__ __forceinline__ void bulk_load(void *smem_dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(smem_dst)),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
 // FP32 word to another CTA's shared memory, and its 4 bytes to the transaction count of a
 // barrier there (cluster addresses from mapa_shared).
 __device__ __forceinline__ void st_async_cluster_f32(uint32_t cluster_addr, float v, uint32_t cluster_bar) {
@@ -544,20 +523,6 @@ __device__ __forceinline__ void tc_mma_mxf8(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
-// The same for packed FP4 (E2M1) operands, K = 64 a step: rows of two codes a byte, two scales
-// (bytes 0, 1 or 2, 3 of the TMEM words, by the scale-factor ids 0 or 2).
-__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}\n" ::"r"(
-            d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
-        : "memory");
-}
-
 // D(tmem) (+)= A(smem) * B(smem)^T without scales (FP8 inputs, FP32 accumulate).
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                           uint32_t idesc, uint32_t accumulate) {
@@ -598,6 +563,7 @@ __device__ __forceinline__ void tma_load_3d_if(bool on, void *smem_dst, const CU
         : "memory");
 }
 
+// Untiled bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned).
 __device__ __forceinline__ void bulk_load_if(bool on, void *smem_dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"
@@ -639,6 +605,8 @@ __device__ __forceinline__ void tc_mma_mxf8_if(bool on, uint32_t d_tmem, uint64_
         : "memory");
 }
 
+// As tc_mma_mxf8_if for packed FP4 (E2M1) operands, K = 64 a step: rows of two codes a byte, two
+// scales (bytes 0, 1 or 2, 3 of the TMEM words, by the scale-factor ids 0 or 2).
 __device__ __forceinline__ void tc_mma_mxf4_if(bool on, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                                uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
                                                uint32_t accumulate) {
