@@ -8,7 +8,13 @@ namespace dg {
 namespace {
 
 constexpr int kMaxSplit = 8;        // portable cluster size
-constexpr int kSmemOne = 232448 - 1024, kSmemTwo = 114000;   // bytes for one or two CTAs on an SM
+// Shared memory of a CTA, alone on an SM or one of two.  It also keeps CTAs apart that would want
+// more TMEM than there is: of a kernel and the one that starts beside its end, the later CTA
+// could take the columns that the earlier one has yet to allocate, and then wait for it.  Two CTAs
+// take up to 256 columns each and leave no room for a third, nor for one of the GEMM kernels,
+// which take all 512 and over 116 KB.
+constexpr int kSmemOne = 232448 - 1024, kSmemTwo = 114000;
+static_assert(kSmemTwo + 116 * 1024 + 2 * 1024 > 228 * 1024, "no room beside a kernel that takes all of TMEM");
 
 // Bytes of weights an SM brings to L2 before it waits for the preceding kernel (1 x 2112 x 7168
 // in a row of calls 6.4 us without, 6.0 us with).
@@ -63,8 +69,8 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     a.b_rows = FewConfig::b_rows(W, tokens);
     a.accs = (plan.split == 1 || MODE == kDown) && 2 * set + sf <= most ? 2 : 1;
     a.tmem_cols = pow2_at_least(a.accs * set + sf);
-    if (a.tmem_cols > 512) return cudaErrorInvalidConfiguration;
-    const int smem = FewConfig::smem_bytes(W, HALVES, tokens, stages, a.out_bytes, tables);
+    if (a.tmem_cols > (plan.occ == 2 ? 256 : 512)) return cudaErrorInvalidConfiguration;
+    const int smem = limit;   // (all of it, whatever the stages take: see kSmemTwo)
     auto kernel = dg_few_rows_kernel<W, HALVES, MODE>;
     static std::atomic<uint64_t> ready{0};   // devices whose attributes are set
     int dev = 0;

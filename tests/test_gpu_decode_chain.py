@@ -88,3 +88,34 @@ def test_dropped_load_times_out_and_context_survives(make, args):
         binding.set_debug_flags(0)
         binding.set_wait_timeout_ms(2000)
     assert torch.equal(first, again)
+
+
+def test_calls_in_a_row_with_gemms():
+    """GEMMs, few-row products and layers back to back on one stream, each starting beside the
+    end of the one before (all of them allocate TMEM): every call gives the bits that it gives alone."""
+    from block_scaled_fp8_gb300 import inputs
+    calls = []
+    for M, N, K in ((128, 512, 1024), (512, 768, 512)):
+        case = inputs.dense_case(M, N, K, seed=5)
+        a, b = case.a.cuda(), case.b.cuda()
+        sfa, sfb = binding.transform_sf(case.sfa.cuda(), 1, M), binding.transform_sf(case.sfb.cuda(), 128, N)
+        calls.append((lambda d, status, a=a, b=b, sfa=sfa, sfb=sfb: binding.dg_fp8_gemm_nt(a, sfa, b, sfb, d, status=status),
+                      (M, N)))
+    calls += [_gemv("fp4", 1, 1024, 2048), _gemv("fp8", 12, 2048, 1024), _gemv("fp4", 40, 20480, 512),
+              _layer("fp4", 3, 8, 2, 512, 256), _layer("fp8", 24, 8, 2, 512, 256)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    alone = []
+    for call, shape in calls:
+        d = torch.full(shape, 9.0, dtype=torch.bfloat16, device="cuda")
+        call(d, status)
+        torch.cuda.synchronize()
+        alone.append(d)
+    order = [i for first in range(len(calls)) for second in range(len(calls)) for i in (first, second)]
+    outs = [torch.full(calls[i][1], 9.0, dtype=torch.bfloat16, device="cuda") for i in order]
+    torch.cuda.synchronize()
+    for i, d in zip(order, outs):
+        calls[i][0](d, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for i, d in zip(order, outs):
+        assert torch.equal(d, alone[i]), i
