@@ -39,7 +39,7 @@
 // and which adds them in rank order: no workspace, no atomics, a fixed order.
 //
 // Where the pieces come from: kGemv and kUpSelf, for the fewest rows, split the activations
-// themselves, four warps taking K-blocks in turn.  The other modes read an image of the narrow
+// themselves, four warps (kGemv with more rows: pairs) taking K-blocks in turn.  The other modes read an image of the narrow
 // operand that is already in the shared-memory form of each K-block (rows of 128 bytes
 // in 128-byte swizzle, and the scale words in tcgen05.cp order), two bulk copies a block:
 //   kGemvPre  dg_few_split_kernel has written the image of all rows.
