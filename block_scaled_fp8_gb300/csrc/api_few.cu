@@ -62,16 +62,19 @@ dg_status gemv(bool fp4, bool f32, const void *a, int64_t lda, const void *b, in
     return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
+bool layer_unsupported(int t, int topk, int h, int i, int experts) {
+    return t > kMaxFewRows || topk > kMaxLayerTopk || experts > kMaxLayerExperts || h > kMaxLayerWidth || i > kMaxLayerWidth;
+}
+
 dg_status layer(bool fp4, const void *x, int64_t ldx, const int32_t *ids, const float *weights, const void *w1,
                 const void *sf1, const void *w2, const void *sf2, const void *c, int64_t ldc, void *y, int64_t ldy,
                 int t, int h, int i, int experts, int topk, void *workspace, int64_t workspace_bytes,
                 int32_t *status_dev, void *stream) {
     if (t < 0 || h < 0 || i < 0 || experts < 1 || topk < 1) return DG_ERR_INVALID_ARG;
     if (t == 0 || h == 0) return DG_OK;
-    if (t > kMaxFewRows || topk > kMaxLayerTopk || experts > kMaxLayerExperts) return DG_ERR_UNSUPPORTED;
+    if (layer_unsupported(t, topk, h, i, experts)) return DG_ERR_UNSUPPORTED;
     if (y == nullptr) return DG_ERR_INVALID_ARG;
     if (h % kBlockK != 0 || i % kBlockK != 0) return DG_ERR_ALIGNMENT;
-    if (i > 1 << 24 || h > 1 << 24) return DG_ERR_UNSUPPORTED;
     if (!aligned(y, 16) || ldy % 8 != 0) return DG_ERR_ALIGNMENT;
     if (ldy < h) return DG_ERR_INVALID_ARG;
     if (c != nullptr && (!aligned(c, 16) || ldc % 8 != 0)) return DG_ERR_ALIGNMENT;
@@ -171,11 +174,13 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
 }
 
 int64_t dg_bf16_gemv_workspace_bytes(int m, int n, int k) {
-    return m < 0 || n < 0 || k < 0 ? -1 : few_workspace_bytes(m, n, k);
+    if (m < 0 || n < 0 || k < 0 || m > kMaxFewRows) return -1;
+    return few_workspace_bytes(m, n, k);
 }
 
 int64_t dg_moe_layer_workspace_bytes(int t, int topk, int h, int i, int experts) {
-    return t < 0 || topk < 0 || h < 0 || i < 0 || experts < 0 ? -1 : layer_workspace_bytes(t, topk, h, i, experts);
+    if (t < 0 || topk < 0 || h < 0 || i < 0 || experts < 0 || layer_unsupported(t, topk, h, i, experts)) return -1;
+    return layer_workspace_bytes(t, topk, h, i, experts);
 }
 
 dg_status dg_moe_fp4_layer(const void *x, int64_t ldx, const int32_t *ids, const float *weights, const void *w1,

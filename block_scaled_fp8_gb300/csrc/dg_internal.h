@@ -129,6 +129,7 @@ cudaError_t launch_fill_d(const void *c, int64_t ldc, void *d, int64_t ldd, int 
 constexpr int kMaxFewRows = 64;         // rows of a few-row product, tokens of a MoE layer call
 constexpr int kMaxLayerTopk = 16;
 constexpr int kMaxLayerExperts = 1024;
+constexpr int kMaxLayerWidth = 1 << 24;
 constexpr int kMaxRouteExperts = 1024;
 constexpr int kMaxRouteTopk = 32;
 

@@ -111,7 +111,8 @@ static int stream_of(PyObject *stream, PyObject *on, void **out) {
     return *out || !PyErr_Occurred();
 }
 
-/* The caller's workspace, or one of `need` bytes (a new reference in *hold). */
+/* The caller's workspace, or one of `need` bytes (a new reference in *hold).  None is made for
+ * sizes that the library does not take (`need` negative): it refuses them. */
 static int workspace_of(PyObject *given, int64_t need, PyObject *on, PyObject *stream, PyObject **hold, void **p,
                         int64_t *bytes) {
     *p = NULL;
@@ -241,7 +242,7 @@ static PyObject *layer(PyObject *self, PyObject *const *arg, Py_ssize_t nargs) {
         CHECK(pointer_of(s1, &sf1) && pointer_of(s2, &sf2) && optional_pointer(arg[11], &status));
         CHECK(stream_of(arg[12], ty, &stream));
         need = ((LayerBytesFn)fns[LAYER_BYTES])((int)t, (int)topk, (int)h, (int)i, (int)e);
-        CHECK(workspace_of(arg[10], need > 16 ? need : 16, ty, arg[12], &hold, &ws, &ws_bytes));
+        CHECK(workspace_of(arg[10], need, ty, arg[12], &hold, &ws, &ws_bytes));
     }
     Py_BEGIN_ALLOW_THREADS
     st = ((LayerFn)fns[fp4 ? LAYER_FP4 : LAYER_FP8])(

@@ -419,7 +419,8 @@ int64_t dg_k_grouped_packed_sf_rows(const int *ks, int num_groups);
  *   0 <= m <= 64 (else DG_ERR_UNSUPPORTED: use the GEMMs), n a multiple of 8, k a
  *   multiple of 128.  m == 0 or n == 0 is a no-op; k == 0 gives D = C (or 0).
  *   workspace   device memory, 16-byte aligned, of dg_bf16_gemv_workspace_bytes(m,
- *        n, k) bytes (0 for the fewest rows: then it may be NULL); its contents need no
+ *        n, k) bytes (0 for the fewest rows: then it may be NULL; -1 for sizes that the
+ *        call refuses as negative or unsupported); its contents need no
  *        initialisation and do not outlive the call.  Calls that may run at the same
  *        time need one each.
  *   A row that holds an infinity or a NaN gives NaN in its row of D; other rows
@@ -487,10 +488,11 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
  *   c     bf16 [t, ldc] or NULL, may equal y; y bf16 [t, ldy]; 16-byte aligned,
  *         strides multiples of 8.
  *   workspace   device memory, 16-byte aligned, dg_moe_layer_workspace_bytes(t,
- *         topk, h, i, experts) bytes; its contents need no initialisation and do not outlive
+ *         topk, h, i, experts) bytes (-1 for sizes that the call refuses as negative or
+ *         unsupported); its contents need no initialisation and do not outlive
  *         the call.  Calls that may run at the same time need one each.
- *   h and i multiples of 128 (DG_ERR_ALIGNMENT); t <= 64, topk <= 16 and experts <=
- *   1024, else DG_ERR_UNSUPPORTED (more tokens: dg_m_grouped_*); t == 0 or h == 0
+ *   h and i multiples of 128 (DG_ERR_ALIGNMENT); t <= 64, topk <= 16, experts <=
+ *   1024, h and i <= 2^24, else DG_ERR_UNSUPPORTED (more tokens: dg_m_grouped_*); t == 0 or h == 0
  *   is a no-op, i == 0 gives y = c (or 0).
  *   Only the rows of experts that some token names are read.  A token whose x
  *   holds an infinity or a NaN gets NaN; the weights and scales of the named
