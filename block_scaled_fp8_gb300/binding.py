@@ -462,7 +462,9 @@ def _load_marshal():
                    "dg_moe_layer_workspace_bytes")
             m.setup(tuple(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in fns),
                     (torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.uint8, torch.int32),
-                    torch._C._cuda_getCurrentRawStream, _workspace)
+                    torch._C._cuda_getCurrentRawStream,
+                    torch._C._cuda_getDevice if torch.cuda.is_available() else lambda: -2,   # (no tensor is there)
+                    _workspace)
             _marshal = m
     return _marshal
 

@@ -249,7 +249,7 @@ int64_t few_workspace_bytes(int64_t m, int64_t n, int64_t k) {
 }
 
 int64_t layer_workspace_bytes(int64_t t, int64_t topk, int64_t h, int64_t i, int64_t experts) {
-    if (t == 0 || topk == 0 || experts == 0) return 0;
+    if (t == 0 || topk == 0 || experts == 0 || h == 0 || i == 0) return 0;   // nothing to split
     int64_t most = 0;
     for (bool fp4 : {false, true}) {
         const SegmentBounds b(fp4, t, topk, experts);

@@ -23,7 +23,7 @@ enum { GEMV_FP4, GEMV_FP8, GEMV_FP4_F32, GEMV_FP8_F32, ROUTE, LAYER_FP4, LAYER_F
 enum { BF16, F32, FP8, U8, I32, DTYPES };
 
 static void *fns[FNS];
-static PyObject *dtypes[DTYPES], *raw_stream, *make_workspace;
+static PyObject *dtypes[DTYPES], *raw_stream, *current_device, *make_workspace;
 static PyObject *s_data_ptr, *s_stride, *s_shape, *s_dtype, *s_is_contiguous, *s_get_device, *s_nbytes, *s_cuda_stream;
 
 #define CHECK(cond)                                                       \
@@ -96,6 +96,31 @@ static int64_t row_stride(const Tensor *t) {
     return t->n[0] > 1 || t->stride[0] > t->n[1] ? t->stride[0] : t->n[1];
 }
 
+/* Whether all tensors (NULL or None: not given) are on the current CUDA device, the one that the
+ * library launches on: its kernels would fault on the pointer of any other. */
+static int placed(PyObject *const *tensors, int n) {
+    PyObject *d = PyObject_CallNoArgs(current_device), *r;
+    long device, at;
+    int i;
+    if (!d) return 0;
+    device = PyLong_AsLong(d);
+    Py_DECREF(d);
+    if (device == -1 && PyErr_Occurred()) return 0;
+    for (i = 0; i < n; ++i) {
+        if (!tensors[i] || tensors[i] == Py_None) continue;
+        r = PyObject_CallMethodNoArgs(tensors[i], s_get_device);   /* (-1 on the host) */
+        if (!r) return 0;
+        at = PyLong_AsLong(r);
+        Py_DECREF(r);
+        if (at != device) {
+            if (!PyErr_Occurred())
+                PyErr_Format(PyExc_AssertionError, "operand on device %ld (-1: host), current device %ld", at, device);
+            return 0;
+        }
+    }
+    return 1;
+}
+
 static int stream_of(PyObject *stream, PyObject *on, void **out) {
     PyObject *d, *r;
     if (stream != Py_None) {
@@ -111,15 +136,23 @@ static int stream_of(PyObject *stream, PyObject *on, void **out) {
     return *out || !PyErr_Occurred();
 }
 
-/* The caller's workspace, or one of `need` bytes (a new reference in *hold).  None is made for
- * sizes that the library does not take (`need` negative): it refuses them. */
-static int workspace_of(PyObject *given, int64_t need, PyObject *on, PyObject *stream, PyObject **hold, void **p,
-                        int64_t *bytes) {
-    *p = NULL;
+/* The stream and the workspace of a call on `tensors`, which all have to be on the current device:
+ * the caller's workspace, or one of `need` bytes (a new reference in *hold).  Where the library does
+ * not take the sizes (`need` negative) or the workspace is too small, it refuses the call before
+ * any device access: then no tensor's place counts, and no workspace is made. */
+static int device_side(PyObject *const *tensors, int count, PyObject *given, int64_t need, PyObject *on, PyObject *stream,
+                       PyObject **hold, void **p, int64_t *bytes, void **stream_out) {
+    *p = *stream_out = NULL;
     *bytes = 0;
+    if (given != Py_None) {
+        *bytes = bytes_of(given);
+        if (*bytes < 0 || !pointer_of(given, p)) return 0;
+    }
+    if (need < 0 || (given != Py_None && *bytes < need)) return 1;
+    if (!placed(tensors, count) || !placed(&given, 1) || !stream_of(stream, on, stream_out)) return 0;
     if (given == Py_None) {
         PyObject *n, *args[3];
-        if (need <= 0) return 1;
+        if (need == 0) return 1;
         n = PyLong_FromLongLong(need);
         if (!n) return 0;
         args[0] = n;
@@ -128,9 +161,10 @@ static int workspace_of(PyObject *given, int64_t need, PyObject *on, PyObject *s
         given = *hold = PyObject_Vectorcall(make_workspace, args, 3, NULL);
         Py_DECREF(n);
         if (!given) return 0;
+        *bytes = bytes_of(given);
+        return *bytes >= 0 && pointer_of(given, p);
     }
-    *bytes = bytes_of(given);
-    return *bytes >= 0 && pointer_of(given, p);
+    return 1;
 }
 
 static PyObject *gemv(PyObject *self, PyObject *const *arg, Py_ssize_t nargs) {
@@ -159,9 +193,10 @@ static PyObject *gemv(PyObject *self, PyObject *const *arg, Py_ssize_t nargs) {
         CHECK(is_contiguous(sfb) && bytes_of(sfb) >= (fp4 ? (k + 127) / 128 : (k + 511) / 512) * ((n + 3) / 4 * 4) * 4);
         CHECK(tc == Py_None ||
               (is_dtype(tc, dtype) && strided(tc, 2, &c) && c.n[0] == m && c.n[1] == n && (c.stride[1] == 1 || n <= 1)));
-        CHECK(pointer_of(sfb, &sf) && optional_pointer(arg[7], &status) && stream_of(arg[8], td, &stream));
-        CHECK(workspace_of(arg[6], ((GemvBytesFn)fns[GEMV_BYTES])((int)m, (int)n, (int)k), td, arg[8], &hold, &ws,
-                           &ws_bytes));
+        CHECK(pointer_of(sfb, &sf) && optional_pointer(arg[7], &status));
+        PyObject *const on_device[] = {ta, tb, sfb, td, tc, arg[7]};
+        CHECK(device_side(on_device, 6, arg[6], ((GemvBytesFn)fns[GEMV_BYTES])((int)m, (int)n, (int)k), td, arg[8], &hold,
+                          &ws, &ws_bytes, &stream));
     }
     Py_BEGIN_ALLOW_THREADS
     st = ((GemvFn)fns[which])(a.p, row_stride(&a), b.p, row_stride(&b), sf, c.p, c.p ? row_stride(&c) : 0, d.p,
@@ -193,7 +228,7 @@ static PyObject *route(PyObject *self, PyObject *const *arg, Py_ssize_t nargs) {
     sigmoid = PyObject_IsTrue(arg[4]);
     renormalize = PyObject_IsTrue(arg[5]);
     scale = PyFloat_AsDouble(arg[6]);
-    CHECK(!PyErr_Occurred() && stream_of(arg[7], arg[0], &stream));
+    CHECK(!PyErr_Occurred() && placed(arg, 4) && stream_of(arg[7], arg[0], &stream));
     Py_BEGIN_ALLOW_THREADS
     st = ((RouteFn)fns[ROUTE])(logits.p, row_stride(&logits), f32 ? DG_LOGITS_F32 : DG_LOGITS_BF16, (const float *)bias.p,
                                (int32_t *)ids.p, (float *)weights.p, (int)logits.n[0], (int)logits.n[1], (int)ids.n[1],
@@ -240,9 +275,9 @@ static PyObject *layer(PyObject *self, PyObject *const *arg, Py_ssize_t nargs) {
                                 (c.stride[1] == 1 || h <= 1)));
         CHECK(t <= INT32_MAX && h <= INT32_MAX && w1.n[1] <= INT32_MAX && e <= INT32_MAX && topk <= INT32_MAX);
         CHECK(pointer_of(s1, &sf1) && pointer_of(s2, &sf2) && optional_pointer(arg[11], &status));
-        CHECK(stream_of(arg[12], ty, &stream));
         need = ((LayerBytesFn)fns[LAYER_BYTES])((int)t, (int)topk, (int)h, (int)i, (int)e);
-        CHECK(workspace_of(arg[10], need, ty, arg[12], &hold, &ws, &ws_bytes));
+        PyObject *const on_device[] = {tx, tids, tw, t1, s1, t2, s2, ty, tc, arg[11]};
+        CHECK(device_side(on_device, 10, arg[10], need, ty, arg[12], &hold, &ws, &ws_bytes, &stream));
     }
     Py_BEGIN_ALLOW_THREADS
     st = ((LayerFn)fns[fp4 ? LAYER_FP4 : LAYER_FP8])(
@@ -257,11 +292,12 @@ fail:
     return NULL;
 }
 
-/* setup(addresses of the entry points, dtypes, raw stream of a device, workspace maker) */
+/* setup(addresses of the entry points, dtypes, raw stream of a device, current device, workspace maker) */
 static PyObject *setup(PyObject *self, PyObject *args) {
     PyObject *addresses, *types;
     int i;
-    if (!PyArg_ParseTuple(args, "O!O!OO", &PyTuple_Type, &addresses, &PyTuple_Type, &types, &raw_stream, &make_workspace))
+    if (!PyArg_ParseTuple(args, "O!O!OOO", &PyTuple_Type, &addresses, &PyTuple_Type, &types, &raw_stream, &current_device,
+                          &make_workspace))
         return NULL;
     CHECK(PyTuple_GET_SIZE(addresses) == FNS && PyTuple_GET_SIZE(types) == DTYPES);
     for (i = 0; i < FNS; ++i) {
@@ -270,6 +306,7 @@ static PyObject *setup(PyObject *self, PyObject *args) {
     }
     for (i = 0; i < DTYPES; ++i) Py_INCREF(dtypes[i] = PyTuple_GET_ITEM(types, i));
     Py_INCREF(raw_stream);
+    Py_INCREF(current_device);
     Py_INCREF(make_workspace);
     Py_RETURN_NONE;
 fail:
