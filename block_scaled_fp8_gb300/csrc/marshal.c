@@ -58,11 +58,6 @@ static int pointer_of(PyObject *t, void **out) {
     return *out || !PyErr_Occurred();
 }
 
-static int optional_pointer(PyObject *t, void **out) {
-    *out = NULL;
-    return t == Py_None || pointer_of(t, out);
-}
-
 static int is_dtype(PyObject *t, PyObject *dtype) {
     PyObject *r = PyObject_GetAttr(t, s_dtype);
     Py_XDECREF(r);   /* (the dtypes are held here) */
@@ -89,6 +84,12 @@ static int64_t bytes_of(PyObject *t) {
     const int64_t n = r ? PyLong_AsLongLong(r) : -1;
     Py_XDECREF(r);
     return n;
+}
+
+/* The status word, or NULL: the kernels OR into 4 bytes. */
+static int status_of(PyObject *t, void **out) {
+    *out = NULL;
+    return t == Py_None || (is_dtype(t, dtypes[I32]) && is_contiguous(t) && bytes_of(t) >= 4 && pointer_of(t, out));
 }
 
 /* Row stride in elements; a single row's own length where its stride says nothing. */
@@ -145,6 +146,7 @@ static int device_side(PyObject *const *tensors, int count, PyObject *given, int
     *p = *stream_out = NULL;
     *bytes = 0;
     if (given != Py_None) {
+        if (!is_contiguous(given)) return 0;   /* its bytes would not be one range */
         *bytes = bytes_of(given);
         if (*bytes < 0 || !pointer_of(given, p)) return 0;
     }
@@ -193,7 +195,7 @@ static PyObject *gemv(PyObject *self, PyObject *const *arg, Py_ssize_t nargs) {
         CHECK(is_contiguous(sfb) && bytes_of(sfb) >= (fp4 ? (k + 127) / 128 : (k + 511) / 512) * ((n + 3) / 4 * 4) * 4);
         CHECK(tc == Py_None ||
               (is_dtype(tc, dtype) && strided(tc, 2, &c) && c.n[0] == m && c.n[1] == n && (c.stride[1] == 1 || n <= 1)));
-        CHECK(pointer_of(sfb, &sf) && optional_pointer(arg[7], &status));
+        CHECK(pointer_of(sfb, &sf) && status_of(arg[7], &status));
         PyObject *const on_device[] = {ta, tb, sfb, td, tc, arg[7]};
         CHECK(device_side(on_device, 6, arg[6], ((GemvBytesFn)fns[GEMV_BYTES])((int)m, (int)n, (int)k), td, arg[8], &hold,
                           &ws, &ws_bytes, &stream));
@@ -274,7 +276,7 @@ static PyObject *layer(PyObject *self, PyObject *const *arg, Py_ssize_t nargs) {
         CHECK(tc == Py_None || (is_dtype(tc, dtypes[BF16]) && strided(tc, 2, &c) && c.n[0] == t && c.n[1] == h &&
                                 (c.stride[1] == 1 || h <= 1)));
         CHECK(t <= INT32_MAX && h <= INT32_MAX && w1.n[1] <= INT32_MAX && e <= INT32_MAX && topk <= INT32_MAX);
-        CHECK(pointer_of(s1, &sf1) && pointer_of(s2, &sf2) && optional_pointer(arg[11], &status));
+        CHECK(pointer_of(s1, &sf1) && pointer_of(s2, &sf2) && status_of(arg[11], &status));
         need = ((LayerBytesFn)fns[LAYER_BYTES])((int)t, (int)topk, (int)h, (int)i, (int)e);
         PyObject *const on_device[] = {tx, tids, tw, t1, s1, t2, s2, ty, tc, arg[11]};
         CHECK(device_side(on_device, 10, arg[10], need, ty, arg[12], &hold, &ws, &ws_bytes, &stream));
