@@ -580,8 +580,10 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
     if (nsplit > 1 && early) cluster_arrive_relaxed();
     // The kernel before kGemvPre, kUp and kDown (a split kernel or kUpSelf) waits for what
     // precedes it and only then lets the next one start.  So these may read weights, ids and
-    // routing weights at once, and only the warps that read the preceding kernel's output wait
+    // routing weights at once, and the warps that read the preceding kernel's output wait
     // for it.  In kGemv every warp waits that reads or writes memory, in kUpSelf all do here.
+    // No timed wait begins before the preceding kernel's end, whose time is none of this one's: the
+    // issuers wait for it first, the producer before it waits for a slot of the ring to be free.
     if constexpr (MODE == kUpSelf) {
         grid_dependency_wait();
         load_slot();
@@ -710,6 +712,7 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
         int slot = 0;
         uint32_t phase = 0;
         uint32_t issued = 0;
+        bool waited = MODE == kGemv || MODE == kUpSelf;
         const bool one = elect_one();
         bool drop = (p.debug_flags & DG_DEBUG_DROP_ONE_LOAD) && blockIdx.x == 0;
         const auto box_row = [&](const FewTile &tile, int e, int h) {   // rows / 4 of a half's box
@@ -762,7 +765,12 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
                                      sf + static_cast<int64_t>(b) * p.sf_ld + r, sf_bytes[h], &full_bar[slot]);
                 }
                 if (++kb == p.kblocks && MODE == kDown) { kb = 0; ++z; }
-                if (++slot == S) { slot = 0; phase ^= 1; }
+                if (++slot == S) {
+                    slot = 0;
+                    phase ^= 1;
+                    if (!waited) grid_dependency_wait();
+                    waited = true;
+                }
             }
         }
     producer_done:
@@ -789,6 +797,7 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
         const uint64_t sfb_base = make_desc_sf_32x128b(smem_u32(smem_sfb));
         const uint32_t sf0 = sf_tmem + 2 * h * SF;
         const bool one = elect_one();
+        if constexpr (MODE != kUpSelf) grid_dependency_wait();   // (the narrow operand comes after it anyway)
         for (int w = first_tile; w < num_tiles; w += tile_step) {
             const FewTile tile = get_tile(w);
             // a run of K-blocks into one accumulator: the tile's, in kDown those of each segment
