@@ -44,8 +44,8 @@ EncodeTiledFn get_encode() {
     return g_encode;
 }
 
-// Current device must be an sm_103 GPU; fills its SM count.
-dg_status check_device(int *num_sms) {
+// Current device must be an sm_103 GPU; fills the SMs to use, and whether that is less than it has.
+dg_status check_device(int *num_sms, bool *limited = nullptr) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return DG_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_dev_mutex);
@@ -62,6 +62,7 @@ dg_status check_device(int *num_sms) {
     if (di.checked < 0) return DG_ERR_UNSUPPORTED;
     int ov = g_num_sms_override.load();
     *num_sms = (ov > 0 && ov < di.num_sms) ? ov : di.num_sms;
+    if (limited) *limited = *num_sms < di.num_sms;
     return DG_OK;
 }
 
@@ -520,7 +521,7 @@ dg_status check_operand_rules(const void *a, int64_t lda, const void *b, int64_t
 
 // ------------------------------------------------------------------ shared with the other host unit
 
-dg_status host_check_device(int *num_sms) { return check_device(num_sms); }
+dg_status host_check_device(int *num_sms, bool *limited) { return check_device(num_sms, limited); }
 TensorMapEncodeFn host_encode() { return get_encode(); }
 uint64_t host_timeout_ns() { return static_cast<uint64_t>(g_timeout_ms.load()) * 1000000ull; }
 uint32_t host_take_debug_flags() {

@@ -6,6 +6,10 @@
 namespace dg {
 namespace {
 
+// The hardware lays CTAs out one to an SM before it puts a second on any, so a grid of two CTAs on each
+// of `num_sms` SMs would take twice as many: where dg_set_num_sms leaves SMs out, an SM has one.
+int max_occ(bool limited) { return limited ? 1 : 2; }
+
 bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 dg_status gemv(bool fp4, bool f32, const void *a, int64_t lda, const void *b, int64_t ldb, const void *sfb,
@@ -32,7 +36,8 @@ dg_status gemv(bool fp4, bool f32, const void *a, int64_t lda, const void *b, in
         if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return DG_ERR_INVALID_ARG;
         if (need > 0 && !aligned(workspace, 16)) return DG_ERR_ALIGNMENT;
     }
-    dg_status st = host_check_device(&sms);
+    bool limited = false;
+    dg_status st = host_check_device(&sms, &limited);
     if (st != DG_OK) return st;
     cudaError_t e;
     if (k == 0) {
@@ -57,7 +62,7 @@ dg_status gemv(bool fp4, bool f32, const void *a, int64_t lda, const void *b, in
         p.status = status_dev;
         p.timeout_ns = host_timeout_ns();
         p.debug_flags = host_take_debug_flags();
-        e = launch_few_gemv(p, sms, static_cast<cudaStream_t>(stream));
+        e = launch_few_gemv(p, sms, max_occ(limited), static_cast<cudaStream_t>(stream));
     }
     return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
@@ -88,7 +93,8 @@ dg_status layer(bool fp4, const void *x, int64_t ldx, const int32_t *ids, const 
             return DG_ERR_ALIGNMENT;
     }
     int sms = 0;
-    dg_status st = host_check_device(&sms);
+    bool limited = false;
+    dg_status st = host_check_device(&sms, &limited);
     if (st != DG_OK) return st;
     cudaError_t e;
     if (i == 0) {
@@ -117,7 +123,7 @@ dg_status layer(bool fp4, const void *x, int64_t ldx, const int32_t *ids, const 
         p.status = status_dev;
         p.timeout_ns = host_timeout_ns();
         p.debug_flags = host_take_debug_flags();
-        e = launch_moe_layer(p, sms, static_cast<cudaStream_t>(stream));
+        e = launch_moe_layer(p, sms, max_occ(limited), static_cast<cudaStream_t>(stream));
     }
     return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
@@ -166,7 +172,8 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
         !aligned(bias, 4))
         return DG_ERR_ALIGNMENT;
     int sms = 0;
-    dg_status st = host_check_device(&sms);
+    bool limited = false;
+    dg_status st = host_check_device(&sms, &limited);
     if (st != DG_OK) return st;
     RouteParams p = {logits, ld, bias, ids, weights, t, experts, topk, logits_fmt == DG_LOGITS_BF16,
                      scoring == DG_SCORE_SIGMOID, renormalize != 0, scale, 0};

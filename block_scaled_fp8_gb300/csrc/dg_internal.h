@@ -116,7 +116,7 @@ typedef CUresult (*TensorMapEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint
                                       const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
                                       CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                                       CUtensorMapFloatOOBfill);
-dg_status host_check_device(int *num_sms);
+dg_status host_check_device(int *num_sms, bool *limited);   // limited: dg_set_num_sms leaves some out
 TensorMapEncodeFn host_encode();
 uint64_t host_timeout_ns();
 uint32_t host_take_debug_flags();   // clears DG_DEBUG_DROP_ONE_LOAD
@@ -152,7 +152,8 @@ struct FewParams {
     uint32_t debug_flags;
 };
 int64_t few_workspace_bytes(int64_t m, int64_t n, int64_t k);
-cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream);
+// max_occ (here and below): CTAs on an SM of the kernels that may have two
+cudaError_t launch_few_gemv(const FewParams &p, int num_sms, int max_occ, cudaStream_t stream);
 
 // The MoE layer for few tokens.
 struct LayerParams {
@@ -176,7 +177,7 @@ struct LayerParams {
     uint32_t debug_flags;
 };
 int64_t layer_workspace_bytes(int64_t t, int64_t topk, int64_t h, int64_t i, int64_t experts);
-cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, int max_occ, cudaStream_t stream);
 
 struct RouteParams {
     const void *logits;

@@ -259,7 +259,7 @@ int64_t layer_workspace_bytes(int64_t t, int64_t topk, int64_t h, int64_t i, int
     return most;
 }
 
-cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_few_gemv(const FewParams &p, int num_sms, int max_occ, cudaStream_t stream) {
     FewArgs a = {};
     a.cap = capacity(p.m);
     const int w = format_of(p.fp4, a.cap);
@@ -282,10 +282,10 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream
     a.status = p.status;
     a.timeout_ns = p.timeout_ns;
     a.debug_flags = p.debug_flags;
-    // The split of K depends on n, k and the format alone, so a row's result does not depend on
-    // the other rows of the call.
+    // The split of K depends on n, k, the format and dg_set_num_sms alone, so a row's result does not
+    // depend on the other rows of the call.
     a.row_tiles = cdiv(p.n, 128);
-    Plan plan = {2, choose_split(a.row_tiles, a.kblocks, 2, num_sms, true)};
+    Plan plan = {max_occ, choose_split(a.row_tiles, a.kblocks, max_occ, num_sms, true)};
     // Many tiles: two CTAs on an SM, except where, after whole rounds of them, so few tiles are left
     // that an SM has one, and its ring is half as deep as one CTA's.  1024 tiles (131064 x 7168
     // FP4, 112 left): two CTAs 82.4 and one 79.7 us at 8 rows, 90.6 and 85.4 at 16; 512 (208 left): 48.2
@@ -309,7 +309,7 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, cudaStream_t stream
     return launch_fmt<1, kGemvPre>(w, map, a, plan, a.row_tiles, num_sms, stream);
 }
 
-cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, int max_occ, cudaStream_t stream) {
     const SegmentBounds bounds(p.fp4, p.t, p.topk, p.experts);
     const int w = bounds.w, cap = bounds.cap, pairs = p.t * p.topk;
     CUtensorMap map1, map2;
@@ -332,7 +332,7 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, cudaStream_t str
     a.timeout_ns = p.timeout_ns;
     a.debug_flags = p.debug_flags;
     const int down_tiles = cdiv(p.h, 128);
-    const Plan down = {2, choose_split(down_tiles, ki * static_cast<int>(bounds.count), 2, num_sms, false)};
+    const Plan down = {max_occ, choose_split(down_tiles, ki * static_cast<int>(bounds.count), max_occ, num_sms, false)};
     // up: a tile is 128 columns of h of one segment
     a.image = x_image;
     a.image_sf = x_sf;

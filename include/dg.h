@@ -39,8 +39,8 @@
  *    given with their calls.)
  *  - No split-K in the GEMMs: each output element is reduced by one CTA in a
  *    fixed K order, so a row's result does not depend on M or on the other rows of
- *    the batch (batch invariance, §13.1).  (The few-row products split K by n
- *    and k alone, in a fixed order, and keep that property.)
+ *    the batch (batch invariance, §13.1).  (The few-row products split K by n,
+ *    k and dg_set_num_sms alone, in a fixed order, and keep that property.)
  */
 #ifndef DG_GB300_H
 #define DG_GB300_H
@@ -509,7 +509,11 @@ dg_status dg_moe_fp8_layer(const void *x, int64_t ldx, const int32_t *ids, const
                            int64_t workspace_bytes, int32_t *status_dev, void *stream);
 
 /* Number of SMs the persistent kernels use (default: all SMs of the current
- * device).  n <= 0 restores the default. */
+ * device).  n <= 0 restores the default.  (The kernels that only rearrange data,
+ * scale packing, the splitting of a decode call's rows, routing, are not
+ * persistent and not limited.)  The few-row products and the MoE layer for few
+ * tokens divide K by it: their results may differ in the last bits from one
+ * setting to another. */
 void dg_set_num_sms(int n);
 int dg_get_num_sms(void);
 
