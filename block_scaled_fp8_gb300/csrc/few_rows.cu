@@ -51,7 +51,7 @@ template <int W, int HALVES, int MODE>
 cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max_tiles,
                    int num_sms, cudaStream_t stream) {
     const int tables = MODE < kUp ? 0 : segment_table_bytes(a.tokens * a.topk, a.experts);
-    a.out_bytes = FewConfig::out_bytes(HALVES, MODE, is_up(MODE) ? a.cap : a.tokens, plan.split);
+    a.out_bytes = FewConfig::out_bytes(HALVES, MODE, a.tokens, plan.split);
     a.ahead = kAhead / (HALVES * (W == kFp4 ? 8192 : 16384)) / plan.occ;
     const int tokens = a.tokens < a.cap ? a.tokens : a.cap;   // of a tile, at most
     const int stage = FewConfig::stage_bytes(W, HALVES, tokens), limit = plan.occ == 2 ? kSmemTwo : kSmemOne;
@@ -161,7 +161,7 @@ const int *resident_clusters(int num_sms) {
 // 72 tiles of 16 x 9216 x 4096 FP4 take 9.7 us in clusters of 4 and 11.8 us of 3; larger ones need
 // that many free SMs of one GPC at once and often do not: 1 x 7168 x 16384 18.5 us in clusters of
 // 5 and 13.3 us of 4 (FP8 28.1 and 21.8; 16 rows 16.7 and 17.7).
-int choose_split(int tiles, int kblocks, int occ, int num_sms, bool tight) {
+int choose_split(int tiles, int64_t kblocks, int occ, int num_sms, bool tight) {
     const int *clusters = resident_clusters(num_sms);
     int best = 1;
     int64_t best_cost = -1;
@@ -170,7 +170,7 @@ int choose_split(int tiles, int kblocks, int occ, int num_sms, bool tight) {
         const bool fits = full ? tiles < clusters[s] * occ + (s <= 4) : tiles * 10 <= clusters[s] * occ * 9;
         if (s > 1 && (!fits || tiles * s > occ * num_sms)) continue;
         const int on_sm = cdiv(tiles * s, num_sms);
-        const int64_t cost = static_cast<int64_t>(on_sm < occ ? 8 : 5 * on_sm) * cdiv(kblocks, s);
+        const int64_t cost = (on_sm < occ ? 8 : 5 * on_sm) * ((kblocks + s - 1) / s);
         if (best_cost < 0 || cost <= best_cost) { best = s; best_cost = cost; }
     }
     return best;
@@ -209,6 +209,17 @@ int capacity(int tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <
 int segment_capacity(int64_t t, int64_t topk, int64_t experts) {
     const int64_t most = 2 * t * topk / experts;
     return capacity(static_cast<int>(most < t ? most : t));
+}
+
+// Parts of an expert's K-blocks in the down kernel, each for one CTA of a cluster.  A CTA spends 0.3 us
+// more on each segment that it has a part of (its accumulators change hands), so parts are of
+// 3 K-blocks at least; with fewer parts the CTAs' shares are less even.  7 tokens, top 6 of 64 experts,
+// 2048 x 1408 FP4 (6 K-blocks, clusters of 8): 38.7 us in one part, 37.8 in 2, 38.6 in 3, 40.5 in 6;
+// FP8 (11): 56.9 in one, 54.6 in 3, 56.5 in 6; 64 tokens, top 8 of 256, 4096 x 1024 FP4 (4 of 6): 254 in
+// one, 248 in 2, 261 in 4; 24 tokens, top 5 of 48, 3584 x 640 (3 of 5): 47 in one, 52 in 3.
+int down_parts(int kblocks, int split) {
+    const int parts = kblocks / 3;
+    return parts < 1 ? 1 : parts < split ? parts : split;
 }
 
 // FP4 weights packed, where all activations fit the digits' 64 columns: 8 x 131064 x 7168 82 us,
@@ -332,7 +343,9 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, int max_occ, cud
     a.timeout_ns = p.timeout_ns;
     a.debug_flags = p.debug_flags;
     const int down_tiles = cdiv(p.h, 128);
-    const Plan down = {max_occ, choose_split(down_tiles, ki * static_cast<int>(bounds.count), max_occ, num_sms, false)};
+    // The split of K depends on h, i, the number of experts, the weights' form and dg_set_num_sms
+    // alone, and the up kernel does not split it, so a token's result does not depend on the other tokens.
+    const Plan down = {max_occ, choose_split(down_tiles, static_cast<int64_t>(ki) * p.experts, max_occ, num_sms, false)};
     // up: a tile is 128 columns of h of one segment
     a.image = x_image;
     a.image_sf = x_sf;
@@ -346,8 +359,12 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, int max_occ, cud
     a.rows = 2 * p.i;
     a.kblocks = kh;
     a.row_tiles = p.i / 128;
+    // K is not split: a token alone would then have its sums split otherwise than among many.  (It gains
+    // only where tiles are few and K is long: 1 token, top 1, 5120 x 2048 FP8 20.5 us so and 15.6 us in
+    // clusters of 6, top 2, 7168 x 2048 FP4 19.3 and 17.2; top 8 of 128, 2048 x 768 13.9 and 15.3, top 6
+    // of 64, 2048 x 1408 15.1 and 16.5.)
     const int up_tiles = static_cast<int>(bounds.count) * a.row_tiles;
-    const Plan up = {1, choose_split(up_tiles, kh, 1, num_sms, false)};
+    const Plan up = {1, 1};
     // With no more tokens than experts, counting a token once per slot, the up kernel splits x
     // itself, a launch less: 1 token, top 8 of 64 experts, 7168 x 2048 FP4 40.6 us so and 40.8 us
     // with the split kernel, FP8 (of 32) 61.8 and 63.2 us, 2 tokens, top 2 of 8, 1024 x 512 12.8
@@ -382,6 +399,7 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, int max_occ, cud
     a.sf_expert = static_cast<int64_t>(a.slices) * a.sf_ld;
     a.rows = p.h;
     a.kblocks = ki;
+    a.parts = down_parts(ki, down.split);
     a.c = p.c;
     a.ldc = p.ldc;
     a.d = p.y;

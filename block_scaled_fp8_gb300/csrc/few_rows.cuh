@@ -32,8 +32,8 @@
 //               cycles, 490 with a branch around what one lane issues).
 //   warps 2..5  epilogue, one TMEM lane quadrant each.
 //   the rest    the narrow operand.
-// Many tiles: the CTAs are persistent and take tiles in turn, the ring of K-blocks running
-// on across them.  Few tiles: one tile per cluster, K split over its CTAs.  Each CTA writes its
+// Many tiles, and the layer's up kernel: the CTAs are persistent and take tiles in turn, the
+// ring of K-blocks running on across them.  Few tiles: one tile per cluster, K split over its CTAs.  Each CTA writes its
 // FP32 partial results into the shared memory of the CTA that puts them out, whose barrier
 // counts their bytes (a cluster barrier in its place: 1 x 2112 x 7168 5.6 us instead of 5.2),
 // and which adds them in rank order: no workspace, no atomics, a fixed order.
@@ -105,6 +105,7 @@ struct FewArgs {
     int out_bytes;          // room of its own for the results, or 0: split results go to the ring
     int ahead;              // kGemv: K-blocks per CTA to bring to L2 before the wait
     int accs;               // accumulator sets (1 or 2)
+    int parts;              // kDown: parts of an expert's K-blocks that different CTAs of a cluster take
     int tmem_cols;
     int row_tiles;          // tiles over the weight rows (kUp: of h's columns)
     // MoE
@@ -150,8 +151,7 @@ struct FewConfig {
     // 32 items of 4 results, shared out to the cluster's CTAs) from each of its CTAs.
     static int out_bytes(int halves, int mode, int cols, int split) {
         if (split == 1) return 2 * 8 * (is_up(mode) ? 128 : halves * 128) * 4;
-        const int rows = cols * (is_up(mode) ? 1 : halves);
-        return (rows + split - 1) / split * split * 32 * 4 * (is_up(mode) ? 8 : 4);
+        return (cols * halves + split - 1) / split * split * 32 * 4 * 4;
     }
     static int smem_bytes(int w, int halves, int tokens, int stages, int out, int tables) {
         return kAlign + stages * stage_bytes(w, halves, tokens) + out + kBarBytes + tables;
@@ -508,8 +508,13 @@ struct FewTile {
     int ntok;       // token columns (kDown: all tokens)
 };
 
+// A CTA's K-blocks of a run: kb, kb + 1, ..
+struct FewRun {
+    int kb, n;
+};
+
 template <int W, int HALVES, int MODE>
-__global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
+__global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MODE) ? 1 : 2)
     dg_few_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ FewArgs p) {
     constexpr bool UP = is_up(MODE), SELF = splits_itself(MODE);
     constexpr int ROWS = HALVES * 128;
@@ -522,8 +527,8 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    const int rank = static_cast<int>(cluster_ctarank());
-    const int nsplit = static_cast<int>(cluster_nctarank());
+    const int rank = UP ? 0 : static_cast<int>(cluster_ctarank());
+    const int nsplit = UP ? 1 : static_cast<int>(cluster_nctarank());
     const int S = p.stages;
     const int ncols = PIECES * p.cap;
     const int b_bytes = p.b_rows * 128;
@@ -597,11 +602,25 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_holder;
-    const int total = MODE == kDown ? seg.count * p.kblocks : p.kblocks;     // K-blocks of a tile
     const int num_tiles = UP ? seg.count * p.row_tiles : p.row_tiles;
-    // this CTA's share of each tile's K-blocks
-    const int k_begin = static_cast<int>(static_cast<int64_t>(total) * rank / nsplit);
-    const int k_end = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / nsplit);
+    // A tile's K-blocks are one run, of which each CTA of a cluster has a share; in kDown a run for
+    // each segment, cut into p.parts parts that fall to CTAs by the expert alone.  (Equal
+    // shares of all segments' K-blocks would make the order in which a token's products are summed
+    // depend on the other tokens' experts.)
+    const int runs = MODE == kDown ? seg.count : 1;
+    const int k_begin = static_cast<int>(static_cast<int64_t>(p.kblocks) * rank / nsplit);
+    const int k_end = static_cast<int>(static_cast<int64_t>(p.kblocks) * (rank + 1) / nsplit);
+    const int part_base = MODE == kDown ? p.kblocks / p.parts : 0, part_odd = MODE == kDown ? p.kblocks % p.parts : 0;
+    const uint32_t split_inv = 65536u / nsplit + 1u;
+    auto run_of = [&](int z) {
+        if constexpr (MODE != kDown) return FewRun{k_begin, k_end - k_begin};
+        const auto mod = [&](uint32_t v) { return v - (v * split_inv >> 16) * nsplit; };   // (v below 1024)
+        // part j of expert e falls to CTA e * parts + j
+        int j = rank - static_cast<int>(mod(mod(seg.expert[z]) * p.parts));
+        if (j < 0) j += nsplit;
+        if (j >= p.parts) return FewRun{0, 0};
+        return FewRun{part_base * j + min(j, part_odd), part_base + (j < part_odd ? 1 : 0)};
+    };
 
     auto get_tile = [&](int w) {
         FewTile t = {0, 0, w * ROWS, p.tokens};
@@ -700,10 +719,10 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
     const uint32_t y_tmem = sf_tmem + 2 * HALVES * SF;          // [HALVES][tokens, up to 8]
     const int y_cols = (p.tokens + 7) & ~7;
 
-    // nsplit > 1.  A tile's results are rows of 32 items, item l the 4 results (kUp: and the 4
-    // of the up half) that lane l of the four epilogue warps hold: ROW_GROUPS rows a token.
+    // nsplit > 1.  A tile's results are rows of 32 items, item l the 4 results
+    // that lane l of the four epilogue warps hold: ROW_GROUPS rows a token.
     // CTA r puts out rows r * share .. of them; smem_out is [CTA][share][component][32].
-    constexpr int ROW_GROUPS = OUT / 128, COMP = UP ? 8 : 4;
+    constexpr int ROW_GROUPS = OUT / 128, COMP = 4;
     const int share = nsplit > 1 && first_tile < num_tiles
                           ? (get_tile(first_tile).ntok * ROW_GROUPS + nsplit - 1) / nsplit : 0;
 
@@ -733,9 +752,9 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
         }
         for (int w = first_tile; w < num_tiles; w += tile_step) {
             const FewTile tile = get_tile(w);
-            int z = MODE == kDown ? k_begin / p.kblocks : 0;
-            int kb = k_begin - z * p.kblocks;
-            for (int i = k_begin; i < k_end; ++i) {
+            for (int z = 0; z < runs; ++z)
+            for (FewRun run = run_of(z); run.n > 0; ++run.kb, --run.n) {
+                const int kb = run.kb;
                 if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto producer_done;
                 if (drop) drop = false;   // diagnostic: this slot never fills
                 else issued |= 1u << slot;
@@ -764,7 +783,6 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
                         bulk_load_if(on && sf_bytes[h] && b < slices, smem_sfa + ((slot * HALVES + h) * SB + b) * 512,
                                      sf + static_cast<int64_t>(b) * p.sf_ld + r, sf_bytes[h], &full_bar[slot]);
                 }
-                if (++kb == p.kblocks && MODE == kDown) { kb = 0; ++z; }
                 if (++slot == S) {
                     slot = 0;
                     phase ^= 1;
@@ -800,12 +818,11 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
         if constexpr (MODE != kUpSelf) grid_dependency_wait();   // (the narrow operand comes after it anyway)
         for (int w = first_tile; w < num_tiles; w += tile_step) {
             const FewTile tile = get_tile(w);
-            // a run of K-blocks into one accumulator: the tile's, in kDown those of each segment
-            for (int i = k_begin; i < k_end;) {
-                const int z = MODE == kDown ? i / p.kblocks : tile.seg;
-                const int kb0 = MODE == kDown ? i - z * p.kblocks : i;
-                const int n = MODE == kDown ? min(k_end - i, p.kblocks - kb0) : k_end - k_begin;
-                i += n;
+            // each run into one accumulator
+            for (int i = 0; i < runs; ++i) {
+                const FewRun run = run_of(i);
+                const int z = MODE == kDown ? i : tile.seg, kb0 = run.kb, n = run.n;
+                if (MODE == kDown && n == 0) continue;
                 if (!mbar_wait_warp(&tempty_bar[acc], acc_phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto mma_done;
                 tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_base + (acc * HALVES + h) * ncols;
@@ -916,9 +933,9 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
             const bool one = elect_one();
             for (int w = first_tile; w < num_tiles; w += tile_step) {
                 const FewTile tile = get_tile(w);
-                int z = MODE == kDown ? k_begin / p.kblocks : tile.seg;
-                int kb = MODE == kDown ? k_begin - z * p.kblocks : k_begin;
-                for (int i = k_begin; i < k_end; ++i) {
+                for (int i = 0; i < runs; ++i)
+                for (FewRun run = run_of(i); run.n > 0; ++run.kb, --run.n) {
+                    const int z = MODE == kDown ? i : tile.seg, kb = run.kb;
                     if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
                     const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
                     const int units = image_units(PIECES, tok);
@@ -930,7 +947,6 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
                     bulk_load_if(one, smem_sfb + slot * SB * 512,
                                  p.image_sf + (static_cast<int64_t>(z) * p.kblocks + kb) * SB * 512, sf_bytes,
                                  &full_bar[slot]);
-                    if (++kb == p.kblocks) { kb = 0; ++z; }
                     if (++slot == S) { slot = 0; phase ^= 1; }
                 }
             }
@@ -969,7 +985,6 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
                         smem_u32(smem_out + ((rank * share + row) * COMP + quad) * 32 + lane), owner);
                     const uint32_t bar = mapa_shared(smem_u32(join_bar), owner);
                     st_async_cluster_f32(at, r[g][j], bar);
-                    if constexpr (UP) st_async_cluster_f32(at + 4 * 4 * 32, r[HALVES - 1][j], bar);
                     if (++row == share) { row = 0; ++owner; }
                 }
             }
@@ -1033,8 +1048,8 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
                 const uint32_t y0 = y_tmem + ((quad * 32) << 16);
                 for (int c = 0; c < HALVES * y_cols; ++c) tmem_st_32x32b_x1(y0 + c, 0u);
                 tmem_st_wait();
-                for (int i = k_begin; i < k_end;) {
-                    const int z = i / p.kblocks;
+                for (int z = 0; z < runs; ++z) {
+                    if (run_of(z).n == 0) continue;
                     if (!wait_acc()) goto epi_done;
                     const int tok = seg.tokens[z];
                     for (int t0 = 0; t0 < tok; t0 += 8) {
@@ -1061,7 +1076,6 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
                     }
                     tmem_st_wait();
                     release();
-                    i = (z + 1) * p.kblocks;
                 }
                 if (nsplit > 1) ring_idle();
                 pushed = true;
@@ -1133,7 +1147,7 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
         tc_fence_after_sync();
         tmem_dealloc(tmem_base, p.tmem_cols);
     }
-    if (nsplit == 1) return;
+    if (UP || nsplit == 1) return;
     // ---------------------------------------------------------------- sum over the cluster (one tile)
     if (first_tile < num_tiles) {
         const FewTile tile = get_tile(first_tile);
@@ -1153,7 +1167,7 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), 2)
 #pragma unroll
                 for (int c = 0; c < COMP; ++c) sum[c] += smem_out[((r * share + row) * COMP + c) * 32 + lane];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = UP ? gated(sum[c], sum[COMP - 4 + c]) : sum[c];
+            for (int c = 0; c < 4; ++c) o[c] = sum[c];
             const int at = rank * share + row;
             store(tile, at / ROW_GROUPS, tile.row0 + (at % ROW_GROUPS) * 128 + 4 * lane, o);
         }
