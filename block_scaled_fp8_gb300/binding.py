@@ -478,20 +478,22 @@ _workspaces: dict = {}
 
 def _workspace(nbytes: int, t, stream):
     """Device memory for a call whose caller gave none.  On the current stream: a buffer kept
-    for this stream and host thread (calls there run one after another).  In a graph capture,
-    or on a stream that the caller names: one of its own, which the allocator keeps from
-    other use as long as the capture or that stream needs it."""
-    if stream is None and not torch._C._cuda_isCurrentStreamCapturing():
-        i = t.get_device()
-        key = (i, torch._C._cuda_getCurrentRawStream(i), threading.get_ident())
-        ws = _workspaces.get(key)
-        if ws is None or ws.numel() < nbytes:
-            ws = _workspaces[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=t.device)
-        return ws
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=t.device)
-    if stream is not None and ws.is_cuda:
-        stream.wait_stream(torch.cuda.current_stream())
-        ws.record_stream(stream)
+    for this stream and host thread (calls there run one after another).  In a graph capture:
+    one of its own, which the allocator keeps from other use as long as the capture needs it.
+    On a stream that the caller names: the same there, so that the call waits for nothing on the
+    current stream."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=t.device)
+        with torch.cuda.stream(stream):
+            return _workspace(nbytes, t, None)
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+    i = t.get_device()
+    key = (i, torch._C._cuda_getCurrentRawStream(i), threading.get_ident())
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _workspaces[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=t.device)
     return ws
 
 
