@@ -473,12 +473,14 @@ def _fail(fn: str, status: int):
     raise DGError(fn, status, lib().dg_status_string(status).decode())
 
 
-_workspaces: dict = {}
+_kept = threading.local()   # .workspaces: {(device, stream): buffer}
+_MAX_KEPT = 8
 
 
 def _workspace(nbytes: int, t, stream):
     """Device memory for a call whose caller gave none.  On the current stream: a buffer kept
-    for this stream and host thread (calls there run one after another).  In a graph capture:
+    for this stream by this host thread (calls there run one after another), as long as the thread
+    lives and uses no more than _MAX_KEPT streams after it.  In a graph capture:
     one of its own, which the allocator keeps from other use as long as the capture needs it.
     On a stream that the caller names: the same there, so that the call waits for nothing on the
     current stream."""
@@ -490,10 +492,17 @@ def _workspace(nbytes: int, t, stream):
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
     i = t.get_device()
-    key = (i, torch._C._cuda_getCurrentRawStream(i), threading.get_ident())
-    ws = _workspaces.get(key)
+    key = (i, torch._C._cuda_getCurrentRawStream(i))
+    try:
+        kept = _kept.workspaces
+    except AttributeError:
+        kept = _kept.workspaces = {}
+    ws = kept.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = _workspaces[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=t.device)
+        kept.pop(key, None)
+        while len(kept) >= _MAX_KEPT:
+            del kept[next(iter(kept))]   # the longest there
+        ws = kept[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=t.device)
     return ws
 
 
