@@ -453,7 +453,8 @@ def _load_marshal():
         if _marshal is None:
             from .build import MARSHAL
             if not os.path.exists(MARSHAL):
-                raise RuntimeError(f"{MARSHAL} is missing (run block_scaled_fp8_gb300.build.build())")
+                raise RuntimeError(f"{MARSHAL} is missing (run block_scaled_fp8_gb300.build.build(), with "
+                                   "Python's headers installed)")
             loader = importlib.machinery.ExtensionFileLoader("dg_marshal", MARSHAL)
             m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("dg_marshal", MARSHAL, loader=loader))
             loader.exec_module(m)

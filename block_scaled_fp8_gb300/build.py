@@ -3,7 +3,8 @@
 Every translation unit under csrc/ is compiled for sm_103a only, in parallel,
 then linked into one shared library against the shared CUDA runtime.  The
 marshalling of the binding's decode calls (csrc/marshal.c, a Python extension
-without CUDA) is built beside it.
+without CUDA) is built beside it where Python's headers are installed; without
+them the library is whole, and only the binding's decode calls are missing.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -91,11 +93,31 @@ def source_digest() -> str:
     return h.hexdigest()[:16]
 
 
+def _have_python_headers() -> bool:
+    return os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(MARSHAL)):
+    made = [LIB, MARSHAL] if _have_python_headers() else [LIB]
+    if not all(os.path.exists(f) for f in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
+    t = min(os.path.getmtime(f) for f in made)
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _compile_marshal():
+    if not _have_python_headers():
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)   # (of other sources)
+        warnings.warn("Python.h is not installed: the binding's decode calls are not built")
+        return
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CC") or "gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(HERE, "..", "include"), MARSHAL_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
@@ -114,20 +136,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    def compile_marshal():
-        tmp = MARSHAL + f".tmp{os.getpid()}"
-        cmd = [os.environ.get("CC") or "gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", sysconfig.get_paths()["include"],
-               "-I", os.path.join(HERE, "..", "include"), MARSHAL_SRC, "-o", tmp]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{cmd[0]} failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, MARSHAL)
-
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
-        marshal = ex.submit(compile_marshal)
         results = list(ex.map(compile_one, srcs))
-        marshal.result()
     if verbose or ptxas_verbose:
         for _, log in results:
             if log.strip():
@@ -136,6 +147,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *[o for o, _ in results]]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    _compile_marshal()
     return LIB
 
 
