@@ -17,7 +17,7 @@ dg_status gemv(bool fp4, bool f32, const void *a, int64_t lda, const void *b, in
                int64_t workspace_bytes, int32_t *status_dev, void *stream) {
     if (m < 0 || n < 0 || k < 0) return DG_ERR_INVALID_ARG;
     if (m == 0 || n == 0) return DG_OK;
-    if (m > kMaxFewRows) return DG_ERR_UNSUPPORTED;
+    if (m > kMaxFewRows || n > kMaxFewSize || k > kMaxFewSize) return DG_ERR_UNSUPPORTED;
     if (d == nullptr) return DG_ERR_INVALID_ARG;
     const int step = f32 ? 4 : 8;
     if (!aligned(d, 16) || ldd % step != 0 || n % 8 != 0) return DG_ERR_ALIGNMENT;
@@ -165,7 +165,7 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
     if (t < 0 || experts < 1 || topk < 1 || topk > experts) return DG_ERR_INVALID_ARG;
     if (logits_fmt != DG_LOGITS_F32 && logits_fmt != DG_LOGITS_BF16) return DG_ERR_INVALID_ARG;
     if (scoring != DG_SCORE_SOFTMAX && scoring != DG_SCORE_SIGMOID) return DG_ERR_INVALID_ARG;
-    if (experts > kMaxRouteExperts || topk > kMaxRouteTopk) return DG_ERR_UNSUPPORTED;
+    if (t > kMaxFewSize || experts > kMaxRouteExperts || topk > kMaxRouteTopk) return DG_ERR_UNSUPPORTED;
     if (t == 0) return DG_OK;
     if (logits == nullptr || ids == nullptr || weights == nullptr || ld < experts) return DG_ERR_INVALID_ARG;
     if (!aligned(logits, logits_fmt == DG_LOGITS_F32 ? 4 : 2) || !aligned(ids, 4) || !aligned(weights, 4) ||
@@ -181,7 +181,7 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
 }
 
 int64_t dg_bf16_gemv_workspace_bytes(int m, int n, int k) {
-    if (m < 0 || n < 0 || k < 0 || m > kMaxFewRows) return -1;
+    if (m < 0 || n < 0 || k < 0 || m > kMaxFewRows || n > kMaxFewSize || k > kMaxFewSize) return -1;
     return few_workspace_bytes(m, n, k);
 }
 

@@ -127,6 +127,7 @@ cudaError_t launch_fill_d(const void *c, int64_t ldc, void *d, int64_t ldd, int 
 // ---- few-row products, top-k routing and the MoE layer for few tokens
 
 constexpr int kMaxFewRows = 64;         // rows of a few-row product, tokens of a MoE layer call
+constexpr int kMaxFewSize = 0x7FFFFFFF - 255;   // n and k of a product, tokens to route: rounded up to tiles they fit an int
 constexpr int kMaxLayerTopk = 16;
 constexpr int kMaxLayerExperts = 1024;
 constexpr int kMaxLayerWidth = 1 << 24;

@@ -417,7 +417,7 @@ int64_t dg_k_grouped_packed_sf_rows(const int *ks, int num_groups);
  *   d    [m, ldd] bf16, or FP32 in the _f32 forms (no rounding after the sum).
  *        c and d 16-byte aligned, ldc and ldd multiples of 8 (FP32: 4).
  *   0 <= m <= 64 (else DG_ERR_UNSUPPORTED: use the GEMMs), n a multiple of 8, k a
- *   multiple of 128.  m == 0 or n == 0 is a no-op; k == 0 gives D = C (or 0).
+ *   multiple of 128, both at most 2^31 - 256 (DG_ERR_UNSUPPORTED).  m == 0 or n == 0 is a no-op; k == 0 gives D = C (or 0).
  *   workspace   device memory, 16-byte aligned, of dg_bf16_gemv_workspace_bytes(m,
  *        n, k) bytes (0 for the fewest rows: then it may be NULL; -1 for sizes that the
  *        call refuses as negative or unsupported); its contents need no
@@ -457,7 +457,7 @@ dg_status dg_bf16_fp8_gemv_nt_f32(const void *a, int64_t lda, const void *b, int
  *   A logit of -infinity or NaN (and a key that is NaN) is never chosen; where
  *   fewer than topk experts are left, the remaining slots get id -1 and weight 0.
  *   A sum of chosen scores below the smallest normal FP32 counts as that value.
- *   1 <= experts <= 1024 and 1 <= topk <= min(experts, 32), else DG_ERR_UNSUPPORTED
+ *   t <= 2^31 - 256, 1 <= experts <= 1024 and 1 <= topk <= min(experts, 32), else DG_ERR_UNSUPPORTED
  *   (DG_ERR_INVALID_ARG below 1 or topk > experts); t == 0 is a no-op.
  */
 typedef enum { DG_LOGITS_F32 = 0, DG_LOGITS_BF16 = 1 } dg_logits_format;
