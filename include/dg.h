@@ -454,8 +454,9 @@ dg_status dg_bf16_fp8_gemv_nt_f32(const void *a, int64_t lda, const void *b, int
  *   logits  [t, ld] FP32 (DG_LOGITS_F32) or bf16 (DG_LOGITS_BF16), experts contiguous.
  *   bias    FP32 [experts] or NULL: shifts the choice only, never the weights.
  *   ids, weights   int32 and FP32 [t][topk], as dg_moe_fp4_layer takes them.
- *   A logit of -infinity or NaN (and a key that is NaN) is never chosen; where
- *   fewer than topk experts are left, the remaining slots get id -1 and weight 0.
+ *   An expert whose logit or key is -infinity or NaN (a bias of -infinity or NaN
+ *   among the causes) is never chosen; where fewer than topk experts are left, the
+ *   remaining slots get id -1 and weight 0.
  *   A sum of chosen scores below the smallest normal FP32 counts as that value.
  *   t <= 2^31 - 256, 1 <= experts <= 1024 and 1 <= topk <= min(experts, 32), else DG_ERR_UNSUPPORTED
  *   (DG_ERR_INVALID_ARG below 1 or topk > experts); t == 0 is a no-op.
