@@ -92,10 +92,9 @@ static int status_of(PyObject *t, void **out) {
     return t == Py_None || (is_dtype(t, dtypes[I32]) && is_contiguous(t) && bytes_of(t) >= 4 && pointer_of(t, out));
 }
 
-/* Row stride in elements; a single row's own length where its stride says nothing. */
-static int64_t row_stride(const Tensor *t) {
-    return t->n[0] > 1 || t->stride[0] > t->n[1] ? t->stride[0] : t->n[1];
-}
+/* Row stride in elements; a single row's own length, for its stride says nothing (and need not
+ * be one that rows may have). */
+static int64_t row_stride(const Tensor *t) { return t->n[0] > 1 ? t->stride[0] : t->n[1]; }
 
 /* Whether all tensors (NULL or None: not given) are on the current CUDA device, the one that the
  * library launches on: its kernels would fault on the pointer of any other. */
