@@ -1,4 +1,8 @@
 // Launches of the few-row kernel (few_rows.cuh): tile and split choice, tensor maps.
+//
+// The times beside the rules are of these kernels, both sides of a rule in one run: microseconds a call
+// over calls in a row in a CUDA graph, on weights that are not in L2, the median of three graphs' medians.
+// They repeat within 1.5 %.
 #include "few_rows.cuh"
 
 #include <atomic>
@@ -16,8 +20,8 @@ constexpr int kMaxSplit = 8;        // portable cluster size
 constexpr int kSmemOne = 232448 - 1024, kSmemTwo = 114000;
 static_assert(kSmemTwo + 116 * 1024 + 2 * 1024 > 228 * 1024, "no room beside a kernel that takes all of TMEM");
 
-// Bytes of weights an SM brings to L2 before it waits for the preceding kernel (1 x 2112 x 7168
-// in a row of calls 6.4 us without, 6.0 us with).
+// Bytes of weights an SM brings to L2 before it waits for the preceding kernel (FP4, 1 x 2112 x 7168
+// 4.75 us without, 4.42 us with; 1 x 24576 x 1536 6.32 and 6.01).
 constexpr int kAhead = 160 * 1024;
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
@@ -57,8 +61,8 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     const int stage = FewConfig::stage_bytes(W, HALVES, tokens), limit = plan.occ == 2 ? kSmemTwo : kSmemOne;
     const int ring = limit - FewConfig::smem_bytes(W, HALVES, tokens, 0, 0, tables);
     // Split results of more than 8 KB go to the ring where they would cost a stage: one more wait
-    // instead (17 x 4096 x 7168 FP8 11.8 us so, 11.4 beside the ring at no stage; 32 x 4096 x 7168
-    // FP4 11.6 so and 12.0 with a stage less).
+    // instead (17 x 4096 x 7168 FP8, at no stage, 10.8 us so and 10.4 us beside the ring; MoE layer of 64 tokens,
+    // top 8 of 64 experts, 7168 x 2048 FP4, down kernel with a ring of 4 253 us so and 268 us beside one of 3).
     if (plan.split > 1 && a.out_bytes > 8192 && (ring - a.out_bytes) / stage < ring / stage) a.out_bytes = 0;
     int stages = (ring - a.out_bytes) / stage;
     if (stages > FewConfig::kMaxStages) stages = FewConfig::kMaxStages;
@@ -151,16 +155,16 @@ const int *resident_clusters(int num_sms) {
 // resident at once, the one with the least K-blocks on the busiest SM, the larger of equals
 // (more of the latency of a CTA's start and end overlaps).  Where an SM would have one CTA in the
 // room of two, its K-blocks count 1.6 times, for it has half a ring: 17 x 6144 x 8192 FP4 12.1 us in
-// clusters of 3 (144 CTAs) and 10.5 us of 5 (240), 1 x 4096 x 7168 5.6 us of 4 and 5.2 of 6 (64 x 4096 x
-// 2048 9.0 and 9.6); the layer's down kernel, 64 tokens, h = 6400: 255 us of 3 and 227 of 5.  A second wave
-// of clusters costs more than any split gains (24576 x 1536, 192 tiles: 7.4 us unsplit, 13 us in pairs).
+// clusters of 3 (144 CTAs) and 10.6 us of 5 (240), 1 x 4096 x 7168 5.6 us of 4 and 5.2 of 6 (64 x 4096 x
+// 2048 9.1 and 9.5); the layer's down kernel, 64 tokens, h = 6400: 272 us of 3 and 241 of 5.  A second wave
+// of clusters costs more than any split gains (24576 x 1536, 192 tiles: 5.9 us unsplit, 8.7 us in pairs).
 // `tight`: whether clusters may take all of that residence.  A kernel starts while CTAs of
 // the ones around it still hold SMs, and clusters that find no room then make a second wave,
-// which costs most where a CTA has little to do (7168 x 2048, 56 tiles in clusters of 5, 3 K-blocks
-// a CTA: 9.6 us, 5.6 us in clusters of 4).  With more to do, clusters of up to 4 find their room:
-// 72 tiles of 16 x 9216 x 4096 FP4 take 9.7 us in clusters of 4 and 11.8 us of 3; larger ones need
-// that many free SMs of one GPC at once and often do not: 1 x 7168 x 16384 18.5 us in clusters of
-// 5 and 13.3 us of 4 (FP8 28.1 and 21.8; 16 rows 16.7 and 17.7).
+// which costs most where a CTA has little to do (1 x 7168 x 2048, 56 tiles in clusters of 5, 2 K-blocks
+// a CTA: 5.2 us, 4.3 us in clusters of 4; the layer's down kernel, h = 7168: 325 and 254 us).  With more to
+// do, clusters of up to 4 find their room: 72 tiles of 16 x 9216 x 4096 FP4 take 8.9 us in clusters of 4 and
+// 9.3 us of 3; larger ones need that many free SMs of one GPC at once and often do not: 1 x 7168 x 16384
+// 14.4 us in clusters of 5 and 12.4 us of 4 (FP8 24.9 and 20.9; 16 rows 16.5 and 17.1).
 int choose_split(int tiles, int64_t kblocks, int occ, int num_sms, bool tight) {
     const int *clusters = resident_clusters(num_sms);
     int best = 1;
@@ -193,19 +197,19 @@ struct Dependent {
 };
 
 // Rows that every CTA of a product splits by itself, without the split kernel's launch and
-// workspace.  FP8, 3 rows, 2112 x 7168: 6.6 us so and 8.2 us with it, 8 rows 7.5 and 8.6 us (4096
-// x 7168 10.1 and 10.9, 65536 x 7168 75.1 and 75.4, 12 rows 100 and 77 us).  The eight digits of
-// FP4's take longer: 2 rows, 4096 x 7168 7.3 us so, 3 rows 8.8 and 8.6 us, 8 rows 13.8 and 8.9 us.
+// workspace.  FP8, 3 rows, 2112 x 7168: 5.6 us so and 7.4 us with it, 8 rows 6.3 and 7.6 us (4096
+// x 7168 8.3 and 9.6, 65536 x 7168 74.8 and 75.3, 12 rows 94 and 77 us).  The eight digits of
+// FP4's take longer: 2 rows, 4096 x 7168 5.7 us so and 7.4 with it, 65536 x 7168 40.2 and 41.3; 3 rows
+// 7.3 and 7.6, 46.1 and 41.2; 8 rows, 4096 x 7168 10.6 and 7.9 us.
 bool direct(int w, int64_t m) { return m <= (w == kFp4Packed ? 2 : 8); }
 
 int capacity(int tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64; }
 
 // Tokens of a segment at most: room for twice the mean number of tokens of an expert (the
 // tokens beyond make another segment, which reads the expert's weights again).  Less room
-// leaves more of the ring to the weights, and up to 8 tokens their packed form.  FP4, top 8 of
-// 64 experts, 64 tokens (mean 8), 7168 x 2048: routed evenly 253 us with room for 16, 266 us
-// for 32 and 269 us for 8; with some experts at 57 tokens 266, 264 and 277 us; all tokens to
-// the same 8 experts 112, 89 and 141 us.  32 tokens: 239 us with room for 8, 243 us for 16.
+// leaves more of the ring to the weights, and up to 8 tokens their packed form.  Top 8 of 64 experts,
+// routed evenly, 64 tokens (mean 8), 7168 x 2048 FP4: 254 us with room for 16, 266 us for 32 and 273 us
+// for 8; 4096 x 1024 FP8 139, 142 and 148 us; 32 tokens, 7168 x 2048 FP4: 235 us with room for 8, 241 for 16.
 int segment_capacity(int64_t t, int64_t topk, int64_t experts) {
     const int64_t most = 2 * t * topk / experts;
     return capacity(static_cast<int>(most < t ? most : t));
@@ -222,9 +226,9 @@ int down_parts(int kblocks, int split) {
     return parts < 1 ? 1 : parts < split ? parts : split;
 }
 
-// FP4 weights packed, where all activations fit the digits' 64 columns: 8 x 131064 x 7168 82 us,
-// 86 us unpacked; MoE layer of 32 tokens, top 8 of 64 experts, 7168 x 2048, 239 us packed and 243 us
-// unpacked, of 64 tokens and 256 experts, 4096 x 1024, 260 and 288 us.
+// FP4 weights packed, where all activations fit the digits' 64 columns: 8 x 131064 x 7168 79.2 us,
+// 83.5 us unpacked; one row 77.1 and 82.8; MoE layer of one token, top 8 of 64 experts, 7168 x 2048, 37.0 us
+// packed and 38.1 us unpacked, of 64 tokens and 256 experts, 4096 x 1024, 253 and 260 us.
 int format_of(bool fp4, int cap) { return !fp4 ? kFp8 : cap == 8 ? kFp4Packed : kFp4; }
 
 // Bounds of the layer's segments and of their images.
@@ -299,11 +303,11 @@ cudaError_t launch_few_gemv(const FewParams &p, int num_sms, int max_occ, cudaSt
     Plan plan = {max_occ, choose_split(a.row_tiles, a.kblocks, max_occ, num_sms, true)};
     // Many tiles: two CTAs on an SM, except where, after whole rounds of them, so few tiles are left
     // that an SM has one, and its ring is half as deep as one CTA's.  1024 tiles (131064 x 7168
-    // FP4, 112 left): two CTAs 82.4 and one 79.7 us at 8 rows, 90.6 and 85.4 at 16; 512 (208 left): 48.2
-    // and 50.6 at 16 rows; 352 (48 left) 43.8 and 39.0.  Rings of two CTAs are too short beside more
-    // than 32 rows: 64 rows, 1024 tiles 123 and 106 us, 512 tiles 64.2 and 61.9.  With one round
-    // (192 tiles) two CTAs are better all the same: 13.8 and 15.5 us at 64 rows; and where CTAs split
-    // the rows themselves: 62 and 67 us at 8 rows of FP8, 352 tiles.
+    // FP4, 112 left): two CTAs 82.3 and one 79.0 us at 8 rows, 91.1 and 85.3 at 16; 512 (208 left): 48.2
+    // and 50.8 at 16 rows; 352 (48 left) 43.5 and 39.2.  Rings of two CTAs are too short beside more
+    // than 32 rows: 64 rows, 1024 tiles 120 and 105 us, 512 tiles 64.2 and 61.8.  With one round
+    // (192 tiles) two CTAs are better all the same: 32.3 and 33.8 us at 64 rows; and where CTAs split
+    // the rows themselves: 61.6 and 67.8 us at 8 rows of FP8, 352 tiles.
     const int left = a.row_tiles % (2 * num_sms);
     if (plan.split == 1 && a.row_tiles > 2 * num_sms && !direct(w, p.m) && (p.m > 32 || (left > 0 && left <= num_sms)))
         plan.occ = 1;
@@ -366,10 +370,11 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, int max_occ, cud
     const int up_tiles = static_cast<int>(bounds.count) * a.row_tiles;
     const Plan up = {1, 1};
     // With no more tokens than experts, counting a token once per slot, the up kernel splits x
-    // itself, a launch less: 1 token, top 8 of 64 experts, 7168 x 2048 FP4 40.6 us so and 40.8 us
-    // with the split kernel, FP8 (of 32) 61.8 and 63.2 us, 2 tokens, top 2 of 8, 1024 x 512 12.8
-    // and 13.3 us.  With more its own splitting bounds it: 8 tokens, top 4 of 16 experts, 7168 x
-    // 2048 FP4 71 us so and 66 us with the split kernel.
+    // itself, a launch less: 1 token, top 8 of 64 experts, 7168 x 2048 FP4 37.0 us so and 39.2 us
+    // with the split kernel, FP8 (of 32) 58.9 and 60.3 us, 2 tokens, top 2 of 8, 1024 x 512 9.1
+    // and 9.8 us, 7 tokens, top 6 of 64, 2048 x 1408 36.5 and 38.6.  With more its own splitting bounds
+    // it: 8 tokens, top 4 of 8 experts, 7168 x 2048 FP4 46 us so and 43 us with the split kernel, 16
+    // tokens, top 4 of 16 87 and 72 us (FP8, whose pieces take less, 16 tokens, top 8 of 32: 207 and 210).
     cudaError_t e;
     if (pairs <= p.experts) {
         a.x = p.x;

@@ -35,7 +35,7 @@
 // Many tiles, and the layer's up kernel: the CTAs are persistent and take tiles in turn, the
 // ring of K-blocks running on across them.  Few tiles: one tile per cluster, K split over its CTAs.  Each CTA writes its
 // FP32 partial results into the shared memory of the CTA that puts them out, whose barrier
-// counts their bytes (a cluster barrier in its place: 1 x 2112 x 7168 5.6 us instead of 5.2),
+// counts their bytes (a cluster barrier in its place took 0.4 us more at 1 x 2112 x 7168),
 // and which adds them in rank order: no workspace, no atomics, a fixed order.
 //
 // Where the pieces come from: kGemv and kUpSelf, for the fewest rows, split the activations
@@ -56,9 +56,9 @@
 //   FP4 131064 x 7168: 1 row 76 us (6.6 TB/s), 8 rows 78, 16 rows 84, 64 rows 105 us; the DRAM
 //   traffic is the weights' and the output's alone.  FP8 65536 x 7168: 1 row 72, 16 rows 76 us.
 //   Small products are bound by the chain of latencies from the end of one kernel to the next
-//   one's last store: 1 x 1024 x 1024 4.2 us, 1 x 2112 x 7168 FP4 5.2 us.
-//   MoE layer, top 8 of 64 experts, 7168 x 2048 FP4: 1 token 37.7 us (187 MB), 16 tokens 213,
-//   64 tokens 250 us (1.5 GB, 6.0 TB/s).
+//   one's last store: 1 x 1024 x 1024 3.3 us, 1 x 2112 x 7168 FP4 4.4 us.
+//   MoE layer, top 8 of 64 experts, 7168 x 2048 FP4: 1 token 36.4 us (187 MB), 16 tokens 209,
+//   64 tokens 251 us (1.5 GB, 6.0 TB/s).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -129,7 +129,7 @@ struct FewConfig {
     static constexpr int kFirstEpi = 2;
     static constexpr int first_b(int halves) { return halves == 2 ? 7 : 6; }
     // kGemv: with rows for more than one, two warps share a K-block's between them (8 x 4096 x
-    // 7168 FP8 10.8 -> 10.2 us, 2 x 7168 x 16384 FP4 14.1 -> 13.7).
+    // 7168 FP8 10.2 us with one, 8.3 with two; 2 x 7168 x 16384 FP4 13.3 and 12.8).
     static constexpr int members(int w, int mode, int tokens) {
         return mode == kGemv && tokens > 256 / block_k(w) ? 2 : 1;
     }

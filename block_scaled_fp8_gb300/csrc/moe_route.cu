@@ -13,9 +13,9 @@
 // approximation by exponential and reciprocal, within kFine; where they are still more (ties),
 // topk rounds of a maximum over all keys take them.
 //
-// Measured, calls in a row in a graph: 32768 x 256, top 8 of sigmoid + bias, FP32 18.8 us (33.5 MB
-// of logits take 5.0 us; 500 instructions a token fill 81 % of the issue slots), softmax
-// without bias 16.1 us, 4099 x 128, top 6 of softmax, bf16 4.9 us, one token 3.1 us (a launch).
+// Measured, calls in a row in a graph: 32768 x 256, top 8 of sigmoid + bias, FP32 17.9 us (33.5 MB
+// of logits take 5.0 us; 500 instructions a token fill 79 % of the issue slots), softmax
+// without bias 15.4 us, 4099 x 128, top 6 of softmax, bf16 4.7 us, one token 2.2 us (a launch).
 #include <cuda_bf16.h>
 
 #include "dg_internal.h"
