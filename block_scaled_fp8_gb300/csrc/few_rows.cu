@@ -215,9 +215,9 @@ int segment_capacity(int64_t t, int64_t topk, int64_t experts) {
     return capacity(static_cast<int>(most < t ? most : t));
 }
 
-// Parts of an expert's K-blocks in the down kernel, each for one CTA of a cluster.  A CTA spends 0.3 us
-// more on each segment that it has a part of (its accumulators change hands), so parts are of
-// 3 K-blocks at least; with fewer parts the CTAs' shares are less even.  7 tokens, top 6 of 64 experts,
+// Parts of an expert's K-blocks in the down kernel, each for one CTA of a cluster.  Short parts are narrow
+// strips of many weight rows, and take longer a K-block (413 ns with parts of 6 on 128 CTAs, 458 ns of
+// 3, 625 ns of one), so parts are of 3 at least; with fewer parts the CTAs' shares are less even.  7 tokens, top 6 of 64 experts,
 // 2048 x 1408 FP4 (6 K-blocks, clusters of 8): 38.7 us in one part, 37.8 in 2, 38.6 in 3, 40.5 in 6;
 // FP8 (11): 56.9 in one, 54.6 in 3, 56.5 in 6; 64 tokens, top 8 of 256, 4096 x 1024 FP4 (4 of 6): 254 in
 // one, 248 in 2, 261 in 4; 24 tokens, top 5 of 48, 3584 x 640 (3 of 5): 47 in one, 52 in 3.

@@ -101,6 +101,8 @@ def main(argv=None):
     p.add_argument("--vocab", type=int, default=8192)
     p.add_argument("--seed", type=int, default=0)
     a = p.parse_args(argv)
+    if not 1 <= a.tokens <= 64:
+        p.error("1 to 64 tokens (more go through the grouped GEMMs)")
     block = Block(a.tokens, a.hidden, a.inner, a.experts, a.topk, a.vocab, a.seed)
     block.step()   # sizes are checked, kernels loaded
     torch.cuda.synchronize()

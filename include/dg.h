@@ -423,6 +423,8 @@ int64_t dg_k_grouped_packed_sf_rows(const int *ks, int num_groups);
  *        call refuses as negative or unsupported); its contents need no
  *        initialisation and do not outlive the call.  Calls that may run at the same
  *        time need one each.
+ *   Sums are the tensor cores' FP32 sums, each step truncated, not rounded: within (k/32 +
+ *   16) 2^-23 of the sum of the products' magnitudes.
  *   A row that holds an infinity or a NaN gives NaN in its row of D; other rows
  *   are not affected.  Row i of D is the same bit for bit whatever the other rows
  *   and (FP4: up to 8, and above 8) their number are.  Activations below 2^-20 of
@@ -498,7 +500,7 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
  *   A token's row of y is the same bit for bit whatever the other tokens, their
  *   routing and their number are, for the same h, i, experts, topk and dg_set_num_sms
  *   (FP4: among calls with t <= 8 or 2*t*topk < 9*experts, and among the others, whose
- *   activations take another form).  Sums are FP32.  w silu(g) u is rounded once, to
+ *   activations take another form).  Sums are as in the products.  w silu(g) u is rounded once, to
  *   the form in which the second product takes it: to 9 significant bits (bf16 has 8) for
  *   values down to 2^-13 of the largest of their 32 along i and to 2^-21 of that largest
  *   below; FP4 in calls of the first kind: to 2^-23 of that largest.
