@@ -12,6 +12,9 @@ namespace dg {
 namespace {
 
 constexpr int kMaxSplit = 8;        // portable cluster size
+// Tokens of a layer's segment: 64 in three pieces, their scales and 64 tokens' results would take 272
+// columns of TMEM, and two CTAs have 256 each.
+constexpr int kMaxSegment = 32;
 // Shared memory of a CTA, alone on an SM or one of two.  It also keeps CTAs apart that would want
 // more TMEM than there is: of a kernel and the one that starts beside its end, the later CTA
 // could take the columns that the earlier one has yet to allocate, and then wait for it.  Two CTAs
@@ -58,8 +61,10 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     a.out_bytes = FewConfig::out_bytes(HALVES, MODE, a.tokens, plan.split);
     a.ahead = kAhead / (HALVES * (W == kFp4 ? 8192 : 16384)) / plan.occ;
     const int tokens = a.tokens < a.cap ? a.tokens : a.cap;   // of a tile, at most
-    const int stage = FewConfig::stage_bytes(W, HALVES, tokens), limit = plan.occ == 2 ? kSmemTwo : kSmemOne;
-    const int ring = limit - FewConfig::smem_bytes(W, HALVES, tokens, 0, 0, tables);
+    constexpr int pieces = MODE == kDown ? inner_pieces(W) : pieces_of(W);
+    a.b_rows = FewConfig::b_rows(pieces, tokens);
+    const int stage = FewConfig::stage_bytes(W, HALVES, a.b_rows), limit = plan.occ == 2 ? kSmemTwo : kSmemOne;
+    const int ring = limit - FewConfig::fixed_bytes(tables);
     // Split results of more than 8 KB go to the ring where they would cost a stage: one more wait
     // instead (17 x 4096 x 7168 FP8, at no stage, 10.8 us so and 10.4 us beside the ring; MoE layer of 64 tokens,
     // top 8 of 64 experts, 7168 x 2048 FP4, down kernel with a ring of 4 253 us so and 268 us beside one of 3).
@@ -67,10 +72,9 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     int stages = (ring - a.out_bytes) / stage;
     if (stages > FewConfig::kMaxStages) stages = FewConfig::kMaxStages;
     if (stages < 2) return cudaErrorInvalidConfiguration;
-    const int set = HALVES * pieces_of(W) * a.cap, most = plan.occ == 2 ? 256 : 512;
+    const int set = HALVES * FewConfig::b_rows(pieces, a.cap), most = plan.occ == 2 ? 256 : 512;
     const int sf = 2 * HALVES * 8 * scale_blocks(W) + (MODE == kDown ? HALVES * ((a.tokens + 7) & ~7) : 0);
     a.stages = stages;
-    a.b_rows = FewConfig::b_rows(W, tokens);
     a.accs = (plan.split == 1 || MODE == kDown) && 2 * set + sf <= most ? 2 : 1;
     a.tmem_cols = pow2_at_least(a.accs * set + sf);
     if (a.tmem_cols > (plan.occ == 2 ? 256 : 512)) return cudaErrorInvalidConfiguration;
@@ -212,7 +216,8 @@ int capacity(int tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <
 // for 8; 4096 x 1024 FP8 139, 142 and 148 us; 32 tokens, 7168 x 2048 FP4: 235 us with room for 8, 241 for 16.
 int segment_capacity(int64_t t, int64_t topk, int64_t experts) {
     const int64_t most = 2 * t * topk / experts;
-    return capacity(static_cast<int>(most < t ? most : t));
+    const int cap = capacity(static_cast<int>(most < t ? most : t));
+    return cap < kMaxSegment ? cap : kMaxSegment;
 }
 
 // Parts of an expert's K-blocks in the down kernel, each for one CTA of a cluster.  Short parts are narrow
@@ -234,7 +239,7 @@ int format_of(bool fp4, int cap) { return !fp4 ? kFp8 : cap == 8 ? kFp4Packed : 
 // Bounds of the layer's segments and of their images.
 struct SegmentBounds {
     int w, cap;
-    int64_t count, units;
+    int64_t count, units, inner_units;
     SegmentBounds(bool fp4, int64_t t, int64_t topk, int64_t experts) {
         const int64_t pairs = t * topk, used = pairs < experts ? pairs : experts;
         cap = segment_capacity(t, topk, experts);
@@ -244,9 +249,11 @@ struct SegmentBounds {
         // (up to 8 tokens: a segment takes the room of all tokens)
         units = w == kFp4Packed ? pairs : t <= 8 ? count * image_units(pieces_of(w), static_cast<int>(t))
                                                  : (pairs + 3 * count) / 4;
+        inner_units = inner_units_before(w, static_cast<int>(pairs), static_cast<int>(count));
     }
     int64_t blocks(int64_t k) const { return (k + block_k(w) - 1) / block_k(w); }
     int64_t image(int64_t k) const { return units * blocks(k) * 1024; }
+    int64_t inner_image(int64_t k) const { return inner_units * blocks(k) * 1024; }
     int64_t scales(int64_t k) const { return count * blocks(k) * scale_blocks(w) * 512; }
 };
 
@@ -268,7 +275,7 @@ int64_t layer_workspace_bytes(int64_t t, int64_t topk, int64_t h, int64_t i, int
     int64_t most = 0;
     for (bool fp4 : {false, true}) {
         const SegmentBounds b(fp4, t, topk, experts);
-        const int64_t bytes = b.image(h) + b.image(i) + b.scales(h) + b.scales(i);
+        const int64_t bytes = b.image(h) + b.inner_image(i) + b.scales(h) + b.scales(i);
         if (bytes > most) most = bytes;
     }
     return most;
@@ -333,7 +340,7 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, int max_occ, cud
         !encode_weights(&map2, w, p.w2, static_cast<int64_t>(p.experts) * p.h, p.i / per, p.i))
         return cudaErrorInvalidValue;
     uint8_t *x_image = p.workspace, *h_image = x_image + bounds.image(p.h);
-    uint8_t *x_sf = h_image + bounds.image(p.i), *h_sf = x_sf + bounds.scales(p.h);
+    uint8_t *x_sf = h_image + bounds.inner_image(p.i), *h_sf = x_sf + bounds.scales(p.h);
     const int kh = static_cast<int>(bounds.blocks(p.h)), ki = static_cast<int>(bounds.blocks(p.i));
     FewArgs a = {};
     a.tokens = p.t;

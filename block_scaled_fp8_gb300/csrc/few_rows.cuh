@@ -8,8 +8,10 @@
 //  - two E4M3 pieces, x = s (hi + lo / 16), s = 2^(floor(log2 max|x|) - 7).  hi holds 4 significant
 //    bits and lo the 4 that follow (with its sign, 9 bits in all), so a bf16 value is
 //    represented exactly down to 2^-13 of its group's largest, and to 2^-21 of the largest
-//    below that.  An FP32 value (the layer's inner activations) is rounded to 9 bits, half a
-//    bf16 unit.
+//    below that.  An FP32 value (the layer's inner activations) has a third piece, lo2 / 256: it
+//    is rounded to 14 bits down to 2^-13 of its group's largest, to 2^-25 of the largest below (rounded to
+//    the 9 bits of two pieces, a layer's bf16 outputs differ from the FP32 form's by 7e-4 of their
+//    size with FP8 weights and 1.5e-3 with FP4's; with 14 bits by 1e-4 and 2e-4).
 //  - for FP4 weights and at most 8 rows, eight E2M1 digits, x = s sum_j d_j / 8^j with
 //    s = 2^(floor(log2 max|x|) - 1): |d| <= 4, each step leaves at most 1/8 of its range, and the
 //    whole is exact to 2^-23 of the group's largest (to 2^-128 absolute, for groups below 2^-105).
@@ -82,6 +84,7 @@ enum FewFormat : int {
 };
 // Columns of a token, and 512-byte blocks of scale words per K-block and 128 rows.
 __host__ __device__ constexpr int pieces_of(int w) { return w == kFp4Packed ? 8 : 2; }
+__host__ __device__ constexpr int inner_pieces(int w) { return w == kFp4Packed ? 8 : 3; }   // of the layer's inner activations
 __host__ __device__ constexpr int scale_blocks(int w) { return w == kFp4Packed ? 2 : 1; }
 __host__ __device__ constexpr int block_k(int w) { return w == kFp4Packed ? 256 : 128; }
 
@@ -100,7 +103,7 @@ struct FewArgs {
     int kblocks;            // K-blocks of one expert
     int slices;             // scale slices of one expert's weights (packed FP4: K / 128)
     int last_mmas;          // packed FP4: MMAs of K = 64 in the last K-block (4, or 2)
-    int cap;                // tokens of a segment at most (8, 16, 32 or 64); N = 2 cap (digits: 8 cap)
+    int cap;                // tokens of a segment at most (8, 16, 32; rows of a product: or 64)
     int stages;
     int out_bytes;          // room of its own for the results, or 0: split results go to the ring
     int ahead;              // kGemv: K-blocks per CTA to bring to L2 before the wait
@@ -143,9 +146,9 @@ struct FewConfig {
     static constexpr int kBarBytes = 512;
     static constexpr int kMaxStages = 24;
     // Rows of the narrow operand for up to `tokens` tokens: whole MMA column steps.
-    static int b_rows(int w, int tokens) { return (pieces_of(w) * tokens + 15) / 16 * 16; }
-    static int stage_bytes(int w, int halves, int tokens) {
-        return halves * 16384 + b_rows(w, tokens) * 128 + (halves + 1) * 512 * scale_blocks(w);
+    static int b_rows(int pieces, int tokens) { return (pieces * tokens + 15) / 16 * 16; }
+    static int stage_bytes(int w, int halves, int b_rows) {
+        return halves * 16384 + b_rows * 128 + (halves + 1) * 512 * scale_blocks(w);
     }
     // Two buffers of 8 tokens' FP32 results; of a split tile, what this CTA puts out (rows of
     // 32 items of 4 results, shared out to the cluster's CTAs) from each of its CTAs.
@@ -153,26 +156,26 @@ struct FewConfig {
         if (split == 1) return 2 * 8 * (is_up(mode) ? 128 : halves * 128) * 4;
         return (cols * halves + split - 1) / split * split * 32 * 4 * 4;
     }
-    static int smem_bytes(int w, int halves, int tokens, int stages, int out, int tables) {
-        return kAlign + stages * stage_bytes(w, halves, tokens) + out + kBarBytes + tables;
-    }
+    static int fixed_bytes(int tables) { return kAlign + kBarBytes + tables; }   // beside the ring and the results
 };
 
-// Four scaled values to their hi and lo pieces.
-__device__ __forceinline__ void split4(float f0, float f1, float f2, float f3, uint32_t &hi, uint32_t &lo) {
+// Four scaled values to their E4M3 codes; what is left of them, times 16.
+__device__ __forceinline__ uint32_t next_piece4(float &f0, float &f1, float &f2, float &f3) {
     const uint32_t h01 = cvt_e4m3x2(f0, f1), h23 = cvt_e4m3x2(f2, f3);
     const uint32_t b01 = e4m3x2_to_f16x2(h01), b23 = e4m3x2_to_f16x2(h23);
     const float2 g01 = __half22float2(*reinterpret_cast<const __half2 *>(&b01));
     const float2 g23 = __half22float2(*reinterpret_cast<const __half2 *>(&b23));
-    hi = h01 | (h23 << 16);
-    lo = cvt_e4m3x2((f0 - g01.x) * 16.0f, (f1 - g01.y) * 16.0f) |
-         (cvt_e4m3x2((f2 - g23.x) * 16.0f, (f3 - g23.y) * 16.0f) << 16);
+    f0 = (f0 - g01.x) * 16.0f;
+    f1 = (f1 - g01.y) * 16.0f;
+    f2 = (f2 - g23.x) * 16.0f;
+    f3 = (f3 - g23.y) * 16.0f;
+    return h01 | (h23 << 16);
 }
 
-// Biased exponent of a group's largest magnitude, kept where both scales are representable;
-// 255 marks an infinity or a NaN in the group, whose scales become NaN.
-__device__ __forceinline__ uint32_t hi_scale(uint32_t e8) { return e8 == 255u ? 255u : e8 - 7u; }
-__device__ __forceinline__ uint32_t lo_scale(uint32_t e8) { return e8 == 255u ? 255u : e8 - 11u; }
+// Scale of the j-th piece.  e8: biased exponent of a group's largest magnitude, kept where the scales
+// are representable; 255 marks an infinity or a NaN in the group, whose scales become NaN.
+__device__ __forceinline__ uint32_t piece_scale(uint32_t e8, int j) { return e8 == 255u ? 255u : e8 - 7u - 4u * j; }
+constexpr uint32_t least_piece_exponent(int pieces) { return 7u + 4u * (pieces - 1); }
 __device__ __forceinline__ float inverse_scale(uint32_t e8) { return __uint_as_float((261u - e8) << 23); }
 
 // Biased exponent of the largest of a group of 32, 8 bf16 values in each of 4 lanes.
@@ -195,11 +198,11 @@ __device__ __forceinline__ void scaled(const uint4 &v, float by, float (&f)[8]) 
 
 // A lane's 8 bf16 values to their pieces; returns the group's exponent.
 __device__ __forceinline__ uint32_t split_bf16(const uint4 &v, uint2 &hi, uint2 &lo) {
-    const uint32_t e8 = max(group_exponent(v), 11u);
+    const uint32_t e8 = max(group_exponent(v), least_piece_exponent(2));
     float f[8];
     scaled(v, inverse_scale(e8), f);
-    split4(f[0], f[1], f[2], f[3], hi.x, lo.x);
-    split4(f[4], f[5], f[6], f[7], hi.y, lo.y);
+    hi = make_uint2(next_piece4(f[0], f[1], f[2], f[3]), next_piece4(f[4], f[5], f[6], f[7]));
+    lo = make_uint2(next_piece4(f[0], f[1], f[2], f[3]), next_piece4(f[4], f[5], f[6], f[7]));
     return e8;
 }
 
@@ -227,6 +230,11 @@ __device__ __forceinline__ uint32_t sf_word(uint32_t n) { return (n & 31u) * 4u 
 
 // Image of n tokens' K-block: their rows in units of 8 (1024 bytes).
 __host__ __device__ constexpr int image_units(int pieces, int tokens) { return (pieces * tokens + 7) >> 3; }
+// Units of the inner activations before segment z, whose first entry is `first` (a bound of the sum of
+// the segments' own units, each of which may be rounded up).
+__host__ __device__ constexpr int inner_units_before(int w, int first, int z) {
+    return w == kFp4Packed ? first : inner_pieces(w) * first / 8 + z;
+}
 
 // The lanes of one row's K-block (16, digits: 32; lane q holds values 8 q ..) write token column
 // col of the K-block's image and its scales.  All lanes of a warp come here; `in`: to write.
@@ -242,8 +250,8 @@ __device__ __forceinline__ void split_row(const uint4 &v, uint8_t *image, uint8_
         *reinterpret_cast<uint2 *>(image + (n + 1) * 128 + (((q >> 1) ^ ((n + 1) & 7)) << 4) + off) = lo;
         if ((q & 3) == 0) {
             uint8_t *s = sf + sf_word(n) * 4 + (q >> 2);
-            s[0] = static_cast<uint8_t>(hi_scale(e8));
-            s[16] = static_cast<uint8_t>(lo_scale(e8));
+            s[0] = static_cast<uint8_t>(piece_scale(e8, 0));
+            s[16] = static_cast<uint8_t>(piece_scale(e8, 1));
         }
     } else {
         const uint32_t e8 = max(group_exponent(v), kLeastDigitExponent);
@@ -522,7 +530,8 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MOD
     constexpr int FIRST_B = FewConfig::first_b(HALVES);
     constexpr bool DIGITS = W == kFp4Packed;
     const int members = FewConfig::members(W, MODE, p.tokens);
-    constexpr int PIECES = pieces_of(W), SB = scale_blocks(W), BLOCK_K = block_k(W);
+    constexpr int INNER = inner_pieces(W), PIECES = MODE == kDown ? INNER : pieces_of(W);
+    constexpr int SB = scale_blocks(W), BLOCK_K = block_k(W);
     constexpr int SF = 4 * SB + 4 * SB;               // TMEM columns of a K-block's scales: weights', activations'
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -530,7 +539,7 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MOD
     const int rank = UP ? 0 : static_cast<int>(cluster_ctarank());
     const int nsplit = UP ? 1 : static_cast<int>(cluster_nctarank());
     const int S = p.stages;
-    const int ncols = PIECES * p.cap;
+    const int ncols = (PIECES * p.cap + 15) & ~15;
     const int b_bytes = p.b_rows * 128;
     uint8_t *smem_a = smem;
     uint8_t *smem_b = smem_a + S * HALVES * 16384;
@@ -597,7 +606,7 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MOD
     Segments seg = {};
     if constexpr (MODE >= kUp)
         seg = build_segments(tab, p.ids, UP ? p.weights : nullptr, slot_id, slot_weight, p.tokens, p.topk, p.experts,
-                             p.cap, PIECES, p.status);
+                             p.cap, pieces_of(W), p.status);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -652,11 +661,9 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MOD
             for (int s = 1; s < 8; s <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));   // a group of 32
             // this tile is a K-block of kDown, or half of one
             const int kblocks = (p.inner + BLOCK_K - 1) / BLOCK_K, kb = tile.row0 / BLOCK_K, k0 = tile.row0 % BLOCK_K;
-            uint8_t *image = p.out_image + (static_cast<int64_t>(seg.unit[tile.seg]) * kblocks +
-                                            kb * image_units(PIECES, tile.ntok)) * 1024;
-            uint8_t *sf = p.out_image_sf + ((static_cast<int64_t>(tile.seg) * kblocks + kb) * SB + k0 / 128) * 512 +
-                          sf_word(PIECES * t) * 4 + (lane >> 3);
-            const uint32_t r = PIECES * t;
+            uint8_t *image = p.out_image + (static_cast<int64_t>(inner_units_before(W, seg.first[tile.seg], tile.seg)) * kblocks +
+                                            kb * image_units(INNER, tile.ntok)) * 1024;
+            uint8_t *sf = p.out_image_sf + ((static_cast<int64_t>(tile.seg) * kblocks + kb) * SB + k0 / 128) * 512 + (lane >> 3);
             if constexpr (DIGITS) {
                 const uint32_t e8 = max(m >> 23, kLeastDigitExponent);
                 const float inv = inverse_digit_scale(e8);
@@ -664,23 +671,22 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MOD
                 for (int c = 0; c < 4; ++c) o[c] *= inv;
                 const uint32_t at = k0 / 2 + lane * 2;   // byte of the row
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < INNER; ++j) {
                     const uint32_t code = next_digits(o);
-                    *reinterpret_cast<uint16_t *>(image + (r + j) * 128 + (((at >> 4) ^ j) << 4) + (at & 15)) =
+                    *reinterpret_cast<uint16_t *>(image + (INNER * t + j) * 128 + (((at >> 4) ^ j) << 4) + (at & 15)) =
                         static_cast<uint16_t>(code);
-                    if ((lane & 7) == 0) sf[16 * j] = static_cast<uint8_t>(digit_scale(e8, j));
+                    if ((lane & 7) == 0) sf[sf_word(INNER * t + j) * 4] = static_cast<uint8_t>(digit_scale(e8, j));
                 }
             } else {
-                const uint32_t e8 = max(m >> 23, 11u);
+                const uint32_t e8 = max(m >> 23, least_piece_exponent(INNER));
                 const float inv = inverse_scale(e8);
-                uint32_t hi, lo;
-                split4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv, hi, lo);
-                const uint32_t at = (lane & 3) * 4;
-                *reinterpret_cast<uint32_t *>(image + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + at) = hi;
-                *reinterpret_cast<uint32_t *>(image + (r + 1) * 128 + (((lane >> 2) ^ ((r + 1) & 7)) << 4) + at) = lo;
-                if ((lane & 7) == 0) {
-                    sf[0] = static_cast<uint8_t>(hi_scale(e8));
-                    sf[16] = static_cast<uint8_t>(lo_scale(e8));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[c] *= inv;
+#pragma unroll
+                for (int j = 0; j < INNER; ++j) {
+                    const uint32_t r = INNER * t + j, code = next_piece4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint32_t *>(image + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = code;
+                    if ((lane & 7) == 0) sf[sf_word(r) * 4] = static_cast<uint8_t>(piece_scale(e8, j));
                 }
             }
         } else if (n < p.rows) {
@@ -939,8 +945,8 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MOD
                     if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
                     const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
                     const int units = image_units(PIECES, tok);
-                    const int64_t before = MODE >= kUp ? seg.unit[z] : 0;
-                    const uint32_t sf_bytes = DIGITS ? 1024u : tok < 16 ? 32u * tok : 512u;
+                    const int64_t before = MODE == kDown ? inner_units_before(W, seg.first[z], z) : MODE >= kUp ? seg.unit[z] : 0;
+                    const uint32_t sf_bytes = DIGITS ? 1024u : PIECES * tok < 32 ? 16u * PIECES * tok : 512u;
                     mbar_arrive_expect_tx_if(one, &full_bar[slot], units * 1024 + sf_bytes);
                     bulk_load_if(one, smem_b + slot * b_bytes, p.image + (before * p.kblocks + kb * units) * 1024,
                                  units * 1024, &full_bar[slot]);
@@ -989,8 +995,26 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MOD
                 }
             }
         };
-        // 8 tokens' results from t0 at this thread's operand rows: the sums of their columns
+        // 8 tokens' results from t0 at this thread's operand rows: the sums of their columns, the smallest first
         auto read8 = [&](int t0, int n, float (&r)[HALVES][8]) {
+            const uint32_t col = tmem_base + ((quad * 32) << 16) + acc * HALVES * ncols + PIECES * t0;
+            if constexpr (PIECES == 3) {   // (kDown) 24 columns
+                uint32_t v[HALVES][3][8];
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+                    for (int l = 0; l < 3; ++l) tmem_ld_32x32b_x8(col + h * ncols + 8 * l, v[h][l]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+#pragma unroll
+                    for (int l = 0; l < 3; ++l) reg_fence8(v[h][l]);
+                    const auto at = [&](int c) { return __uint_as_float(v[h][c >> 3][c & 7]); };
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) r[h][j] = (at(3 * j + 2) + at(3 * j + 1)) + at(3 * j);
+                }
+                return;
+            }
             constexpr int AT_ONCE = 16 / PIECES, LOADS = AT_ONCE < 8 && HALVES == 1 ? 2 : 1;   // tokens of 16 columns, loads in flight
 #pragma unroll
             for (int j0 = 0; j0 < 8; j0 += LOADS * AT_ONCE) {
@@ -1001,9 +1025,7 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MOD
 #pragma unroll
                     for (int h = 0; h < HALVES; ++h)
                         if (l == 0 || j0 + l * AT_ONCE < n)
-                            tmem_ld_32x32b_x16(tmem_base + ((quad * 32) << 16) + (acc * HALVES + h) * ncols +
-                                                   PIECES * (t0 + j0 + l * AT_ONCE),
-                                               v[l][h]);
+                            tmem_ld_32x32b_x16(col + h * ncols + PIECES * (j0 + l * AT_ONCE), v[l][h]);
                 tmem_ld_wait();
 #pragma unroll
                 for (int l = 0; l < LOADS; ++l)
@@ -1012,7 +1034,7 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MOD
                         reg_fence16(v[l][h]);
 #pragma unroll
                         for (int j = 0; j < AT_ONCE; ++j) {
-                            float sum = __uint_as_float(v[l][h][PIECES * j + PIECES - 1]);   // the smallest first
+                            float sum = __uint_as_float(v[l][h][PIECES * j + PIECES - 1]);
 #pragma unroll
                             for (int c = PIECES - 2; c >= 0; --c) sum += __uint_as_float(v[l][h][PIECES * j + c]);
                             r[h][j0 + l * AT_ONCE + j] = sum;

@@ -501,8 +501,8 @@ dg_status dg_moe_route(const void *logits, int64_t ld, int logits_fmt, const flo
  *   routing and their number are, for the same h, i, experts, topk and dg_set_num_sms
  *   (FP4: among calls with t <= 8 or 2*t*topk < 9*experts, and among the others, whose
  *   activations take another form).  Sums are as in the products.  w silu(g) u is rounded once, to
- *   the form in which the second product takes it: to 9 significant bits (bf16 has 8) for
- *   values down to 2^-13 of the largest of their 32 along i and to 2^-21 of that largest
+ *   the form in which the second product takes it: to 14 significant bits (bf16 has 8) for
+ *   values down to 2^-13 of the largest of their 32 along i and to 2^-25 of that largest
  *   below; FP4 in calls of the first kind: to 2^-23 of that largest.
  *   Only the rows of experts that some token names are read.  A token whose x
  *   holds an infinity or a NaN gets NaN; the weights and scales of the named
