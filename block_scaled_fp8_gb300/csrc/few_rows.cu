@@ -2,7 +2,7 @@
 //
 // The times beside the rules are of these kernels, both sides of a rule in one run: microseconds a call
 // over calls in a row in a CUDA graph, on weights that are not in L2, the median of three graphs' medians.
-// They repeat within 1.5 %.
+// They repeat within 1.5 % on one GPU, and between GPUs within 3 %.
 #include "few_rows.cuh"
 
 #include <atomic>
@@ -67,7 +67,7 @@ cudaError_t launch(const CUtensorMap &map, FewArgs &a, const Plan &plan, int max
     const int ring = limit - FewConfig::fixed_bytes(tables);
     // Split results of more than 8 KB go to the ring where they would cost a stage: one more wait
     // instead (17 x 4096 x 7168 FP8, at no stage, 10.8 us so and 10.4 us beside the ring; MoE layer of 64 tokens,
-    // top 8 of 64 experts, 7168 x 2048 FP4, down kernel with a ring of 4 253 us so and 268 us beside one of 3).
+    // top 8 of 64 experts, 7168 x 2048 FP4, down kernel with a ring of 3 256 us so and 298 us beside one of 2).
     if (plan.split > 1 && a.out_bytes > 8192 && (ring - a.out_bytes) / stage < ring / stage) a.out_bytes = 0;
     int stages = (ring - a.out_bytes) / stage;
     if (stages > FewConfig::kMaxStages) stages = FewConfig::kMaxStages;
@@ -160,12 +160,12 @@ const int *resident_clusters(int num_sms) {
 // (more of the latency of a CTA's start and end overlaps).  Where an SM would have one CTA in the
 // room of two, its K-blocks count 1.6 times, for it has half a ring: 17 x 6144 x 8192 FP4 12.1 us in
 // clusters of 3 (144 CTAs) and 10.6 us of 5 (240), 1 x 4096 x 7168 5.6 us of 4 and 5.2 of 6 (64 x 4096 x
-// 2048 9.1 and 9.5); the layer's down kernel, 64 tokens, h = 6400: 272 us of 3 and 241 of 5.  A second wave
+// 2048 9.1 and 9.5); the layer's down kernel, 64 tokens, h = 6400: 275 us of 3 and 244 of 5.  A second wave
 // of clusters costs more than any split gains (24576 x 1536, 192 tiles: 5.9 us unsplit, 8.7 us in pairs).
 // `tight`: whether clusters may take all of that residence.  A kernel starts while CTAs of
 // the ones around it still hold SMs, and clusters that find no room then make a second wave,
 // which costs most where a CTA has little to do (1 x 7168 x 2048, 56 tiles in clusters of 5, 2 K-blocks
-// a CTA: 5.2 us, 4.3 us in clusters of 4; the layer's down kernel, h = 7168: 325 and 254 us).  With more to
+// a CTA: 5.2 us, 4.3 us in clusters of 4; the layer's down kernel, h = 7168: 326 and 256 us).  With more to
 // do, clusters of up to 4 find their room: 72 tiles of 16 x 9216 x 4096 FP4 take 8.9 us in clusters of 4 and
 // 9.3 us of 3; larger ones need that many free SMs of one GPC at once and often do not: 1 x 7168 x 16384
 // 14.4 us in clusters of 5 and 12.4 us of 4 (FP8 24.9 and 20.9; 16 rows 16.5 and 17.1).
@@ -212,8 +212,8 @@ int capacity(int tokens) { return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <
 // Tokens of a segment at most: room for twice the mean number of tokens of an expert (the
 // tokens beyond make another segment, which reads the expert's weights again).  Less room
 // leaves more of the ring to the weights, and up to 8 tokens their packed form.  Top 8 of 64 experts,
-// routed evenly, 64 tokens (mean 8), 7168 x 2048 FP4: 254 us with room for 16, 266 us for 32 and 273 us
-// for 8; 4096 x 1024 FP8 139, 142 and 148 us; 32 tokens, 7168 x 2048 FP4: 235 us with room for 8, 241 for 16.
+// routed evenly, 64 tokens (mean 8), 7168 x 2048 FP4: 256 us with room for 16, 305 us for 32 and 273 us
+// for 8; 4096 x 1024 FP8 140, 147 and 149 us; 32 tokens, 7168 x 2048 FP4: 235 us with room for 8, 243 for 16.
 int segment_capacity(int64_t t, int64_t topk, int64_t experts) {
     const int64_t most = 2 * t * topk / experts;
     const int cap = capacity(static_cast<int>(most < t ? most : t));
@@ -223,17 +223,17 @@ int segment_capacity(int64_t t, int64_t topk, int64_t experts) {
 // Parts of an expert's K-blocks in the down kernel, each for one CTA of a cluster.  Short parts are narrow
 // strips of many weight rows, and take longer a K-block (413 ns with parts of 6 on 128 CTAs, 458 ns of
 // 3, 625 ns of one), so parts are of 3 at least; with fewer parts the CTAs' shares are less even.  7 tokens, top 6 of 64 experts,
-// 2048 x 1408 FP4 (6 K-blocks, clusters of 8): 38.7 us in one part, 37.8 in 2, 38.6 in 3, 40.5 in 6;
-// FP8 (11): 56.9 in one, 54.6 in 3, 56.5 in 6; 64 tokens, top 8 of 256, 4096 x 1024 FP4 (4 of 6): 254 in
-// one, 248 in 2, 261 in 4; 24 tokens, top 5 of 48, 3584 x 640 (3 of 5): 47 in one, 52 in 3.
+// 2048 x 1408 FP4 (6 K-blocks, clusters of 8): 38.6 us in one part, 37.1 in 2, 38.3 in 3, 40.0 in 6;
+// FP8 (11): 59.3 in one, 55.7 in 3, 57.4 in 6; 64 tokens, top 8 of 256, 4096 x 1024 FP4 (4 of 6): 254 in
+// one, 248 in 2, 262 in 4; 24 tokens, top 5 of 48, 3584 x 640 (3 of 5): 47 in one, 52 in 3.
 int down_parts(int kblocks, int split) {
     const int parts = kblocks / 3;
     return parts < 1 ? 1 : parts < split ? parts : split;
 }
 
 // FP4 weights packed, where all activations fit the digits' 64 columns: 8 x 131064 x 7168 79.2 us,
-// 83.5 us unpacked; one row 77.1 and 82.8; MoE layer of one token, top 8 of 64 experts, 7168 x 2048, 37.0 us
-// packed and 38.1 us unpacked, of 64 tokens and 256 experts, 4096 x 1024, 253 and 260 us.
+// 83.5 us unpacked; one row 77.1 and 82.8; MoE layer of one token, top 8 of 64 experts, 7168 x 2048, 37.2 us
+// packed and 38.3 us unpacked, of 64 tokens and 256 experts, 4096 x 1024, 254 and 263 us.
 int format_of(bool fp4, int cap) { return !fp4 ? kFp8 : cap == 8 ? kFp4Packed : kFp4; }
 
 // Bounds of the layer's segments and of their images.
@@ -370,18 +370,18 @@ cudaError_t launch_moe_layer(const LayerParams &p, int num_sms, int max_occ, cud
     a.rows = 2 * p.i;
     a.kblocks = kh;
     a.row_tiles = p.i / 128;
-    // K is not split: a token alone would then have its sums split otherwise than among many.  (It gains
-    // only where tiles are few and K is long: 1 token, top 1, 5120 x 2048 FP8 20.5 us so and 15.6 us in
+    // K is not split: a token alone would then have its sums split otherwise than among many.  (Measured
+    // before that form was taken out, it gains only where tiles are few and K is long: 1 token, top 1, 5120 x 2048 FP8 20.5 us so and 15.6 us in
     // clusters of 6, top 2, 7168 x 2048 FP4 19.3 and 17.2; top 8 of 128, 2048 x 768 13.9 and 15.3, top 6
     // of 64, 2048 x 1408 15.1 and 16.5.)
     const int up_tiles = static_cast<int>(bounds.count) * a.row_tiles;
     const Plan up = {1, 1};
     // With no more tokens than experts, counting a token once per slot, the up kernel splits x
-    // itself, a launch less: 1 token, top 8 of 64 experts, 7168 x 2048 FP4 37.0 us so and 39.2 us
-    // with the split kernel, FP8 (of 32) 58.9 and 60.3 us, 2 tokens, top 2 of 8, 1024 x 512 9.1
-    // and 9.8 us, 7 tokens, top 6 of 64, 2048 x 1408 36.5 and 38.6.  With more its own splitting bounds
-    // it: 8 tokens, top 4 of 8 experts, 7168 x 2048 FP4 46 us so and 43 us with the split kernel, 16
-    // tokens, top 4 of 16 87 and 72 us (FP8, whose pieces take less, 16 tokens, top 8 of 32: 207 and 210).
+    // itself, a launch less: 1 token, top 8 of 64 experts, 7168 x 2048 FP4 37.3 us so and 39.7 us
+    // with the split kernel, FP8 (of 32) 59.1 and 60.3 us, 2 tokens, top 2 of 8, 1024 x 512 9.3
+    // and 10.0 us, 7 tokens, top 6 of 64, 2048 x 1408 37.3 and 39.1.  With more its own splitting bounds
+    // it: 8 tokens, top 4 of 8 experts, 7168 x 2048 FP4 47 us so and 43 us with the split kernel, 16
+    // tokens, top 4 of 16 89 and 73 us (FP8, whose pieces take less, 16 tokens, top 8 of 32: 211 and 215).
     cudaError_t e;
     if (pairs <= p.experts) {
         a.x = p.x;

@@ -59,8 +59,8 @@
 //   traffic is the weights' and the output's alone.  FP8 65536 x 7168: 1 row 72, 16 rows 76 us.
 //   Small products are bound by the chain of latencies from the end of one kernel to the next
 //   one's last store: 1 x 1024 x 1024 3.3 us, 1 x 2112 x 7168 FP4 4.4 us.
-//   MoE layer, top 8 of 64 experts, 7168 x 2048 FP4: 1 token 36.4 us (187 MB), 16 tokens 209,
-//   64 tokens 251 us (1.5 GB, 6.0 TB/s).
+//   MoE layer, top 8 of 64 experts, 7168 x 2048 FP4: 1 token 37.3 us (187 MB), 16 tokens 213,
+//   64 tokens 256 us (1.5 GB, 5.8 TB/s).
 #pragma once
 
 #include <cuda_bf16.h>
