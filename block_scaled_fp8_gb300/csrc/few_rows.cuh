@@ -758,8 +758,7 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MOD
         }
         for (int w = first_tile; w < num_tiles; w += tile_step) {
             const FewTile tile = get_tile(w);
-            for (int z = 0; z < runs; ++z)
-            for (FewRun run = run_of(z); run.n > 0; ++run.kb, --run.n) {
+            for (int z = 0; z < runs; ++z) for (FewRun run = run_of(z); run.n > 0; ++run.kb, --run.n) {
                 const int kb = run.kb;
                 if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto producer_done;
                 if (drop) drop = false;   // diagnostic: this slot never fills
@@ -939,8 +938,7 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MOD
             const bool one = elect_one();
             for (int w = first_tile; w < num_tiles; w += tile_step) {
                 const FewTile tile = get_tile(w);
-                for (int i = 0; i < runs; ++i)
-                for (FewRun run = run_of(i); run.n > 0; ++run.kb, --run.n) {
+                for (int i = 0; i < runs; ++i) for (FewRun run = run_of(i); run.n > 0; ++run.kb, --run.n) {
                     const int z = MODE == kDown ? i : tile.seg, kb = run.kb;
                     if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto b_done;
                     const int tok = MODE >= kUp ? seg.tokens[z] : tile.ntok;
@@ -1013,33 +1011,33 @@ __global__ void __launch_bounds__(FewConfig::threads(W, HALVES, MODE), is_up(MOD
 #pragma unroll
                     for (int j = 0; j < 8; ++j) r[h][j] = (at(3 * j + 2) + at(3 * j + 1)) + at(3 * j);
                 }
-                return;
-            }
-            constexpr int AT_ONCE = 16 / PIECES, LOADS = AT_ONCE < 8 && HALVES == 1 ? 2 : 1;   // tokens of 16 columns, loads in flight
+            } else {
+                constexpr int AT_ONCE = 16 / PIECES, LOADS = AT_ONCE < 8 && HALVES == 1 ? 2 : 1;   // tokens of 16 columns, loads in flight
 #pragma unroll
-            for (int j0 = 0; j0 < 8; j0 += LOADS * AT_ONCE) {
-                if (j0 >= n) break;
-                uint32_t v[LOADS][HALVES][16];
+                for (int j0 = 0; j0 < 8; j0 += LOADS * AT_ONCE) {
+                    if (j0 >= n) break;
+                    uint32_t v[LOADS][HALVES][16];
 #pragma unroll
-                for (int l = 0; l < LOADS; ++l)
+                    for (int l = 0; l < LOADS; ++l)
 #pragma unroll
-                    for (int h = 0; h < HALVES; ++h)
-                        if (l == 0 || j0 + l * AT_ONCE < n)
-                            tmem_ld_32x32b_x16(col + h * ncols + PIECES * (j0 + l * AT_ONCE), v[l][h]);
-                tmem_ld_wait();
+                        for (int h = 0; h < HALVES; ++h)
+                            if (l == 0 || j0 + l * AT_ONCE < n)
+                                tmem_ld_32x32b_x16(col + h * ncols + PIECES * (j0 + l * AT_ONCE), v[l][h]);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int l = 0; l < LOADS; ++l)
+                    for (int l = 0; l < LOADS; ++l)
 #pragma unroll
-                    for (int h = 0; h < HALVES; ++h) {
-                        reg_fence16(v[l][h]);
+                        for (int h = 0; h < HALVES; ++h) {
+                            reg_fence16(v[l][h]);
 #pragma unroll
-                        for (int j = 0; j < AT_ONCE; ++j) {
-                            float sum = __uint_as_float(v[l][h][PIECES * j + PIECES - 1]);
+                            for (int j = 0; j < AT_ONCE; ++j) {
+                                float sum = __uint_as_float(v[l][h][PIECES * j + PIECES - 1]);
 #pragma unroll
-                            for (int c = PIECES - 2; c >= 0; --c) sum += __uint_as_float(v[l][h][PIECES * j + c]);
-                            r[h][j0 + l * AT_ONCE + j] = sum;
+                                for (int c = PIECES - 2; c >= 0; --c) sum += __uint_as_float(v[l][h][PIECES * j + c]);
+                                r[h][j0 + l * AT_ONCE + j] = sum;
+                            }
                         }
-                    }
+                }
             }
         };
         auto release = [&] {   // the accumulators are read
