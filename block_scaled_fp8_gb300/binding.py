@@ -45,6 +45,8 @@ EXPORTS = (
     "dg_set_wait_timeout_ms", "dg_set_debug_flags", "dg_status_string", "dg_get_last_config",
     "dg_bf16_fp4_gemv_nt", "dg_bf16_fp8_gemv_nt", "dg_bf16_fp4_gemv_nt_f32", "dg_bf16_fp8_gemv_nt_f32",
     "dg_bf16_gemv_workspace_bytes", "dg_moe_route", "dg_moe_layer_workspace_bytes", "dg_moe_fp4_layer", "dg_moe_fp8_layer",
+    "dg_fp8_gated_gemm_nt", "dg_m_grouped_fp8_gated_gemm_nt_contiguous", "dg_fp8_gated_gemm_nn_backward",
+    "dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous",
 )
 
 
@@ -117,6 +119,15 @@ def lib():
             for f in ("dg_moe_fp4_layer", "dg_moe_fp8_layer"):
                 getattr(L, f).argtypes = [P, i64, P, P, P, P, P, P, P, i64, P, i64, i32, i32, i32, i32, i32, P, i64,
                                           P, P]
+                getattr(L, f).restype = i32
+            gated = [P, i64, P, P, i64, P, P, i64, P, i64, P, i64, P]
+            L.dg_fp8_gated_gemm_nt.argtypes = gated + [i32, i32, i32, P, P]
+            L.dg_m_grouped_fp8_gated_gemm_nt_contiguous.argtypes = gated + [P, i32, i32, i32, i32, P, P]
+            gated = [P, i64, P, P, i64, P, P, i64, P, i64, P, i64]
+            L.dg_fp8_gated_gemm_nn_backward.argtypes = gated + [i32, i32, i32, P, P]
+            L.dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous.argtypes = gated + [P, i32, i32, i32, i32, P, P]
+            for f in ("dg_fp8_gated_gemm_nt", "dg_m_grouped_fp8_gated_gemm_nt_contiguous",
+                      "dg_fp8_gated_gemm_nn_backward", "dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous"):
                 getattr(L, f).restype = i32
             L.dg_get_mk_alignment_for_contiguous_layout.restype = i32
             L.dg_get_mk_alignment_for_contiguous_layout.argtypes = []
@@ -582,3 +593,130 @@ def dg_moe_fp8_layer(x, ids, weights, w1, sf1, w2, sf2, y, c=None, workspace=Non
     if st:
         _fail("dg_moe_fp8_layer", st)
     return y
+
+
+# --------------------------------------------------------------------- feed-forward training: gated block, quantiser, update
+#
+# A wrong dtype, shape, layout or device raises AssertionError, what the library refuses DGError.
+
+_E4M3 = torch.float8_e4m3fn
+_BF16 = torch.bfloat16
+
+
+def _here(*tensors):
+    """All of them (None aside) are on the current CUDA device."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+    for t in tensors:
+        assert t is None or t.get_device() == dev, "tensors have to be on the current CUDA device"
+
+
+def _matrix(t, dtype, shape):
+    """t is a matrix of this dtype and shape with unit column stride; its row stride."""
+    assert t.dtype == dtype and t.shape == shape and (t.stride(-1) == 1 or t.shape[-1] <= 1), \
+        f"expected {dtype} {tuple(shape)} with unit column stride, got {t.dtype} {tuple(t.shape)} {t.stride()}"
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+
+
+def _words(t, *shape):
+    """t holds packed scale words of this shape, dense."""
+    assert t.dtype == torch.int32 and tuple(t.shape) == shape and t.is_contiguous(), \
+        f"expected dense int32 {shape}, got {t.dtype} {tuple(t.shape)}"
+    return t
+
+
+def _align4(n):
+    return (n + 3) // 4 * 4
+
+
+def _status_word(status):
+    assert status is None or (status.dtype == torch.int32 and status.numel() >= 1)
+
+
+def _gated_forward(fn, a, sfa, b, sfb, layout, h, hq, sfh, gu, status, stream):
+    M, K = a.shape
+    grouped = layout is not None
+    I = b.shape[-2] // 2
+    E = b.shape[0] if grouped else 1
+    lda = _matrix(a, _E4M3, (M, K))
+    ldb = _matrix(b, _E4M3, (E, 2 * I, K) if grouped else (2 * I, K))
+    assert not grouped or E == 1 or b.stride(0) == 2 * I * ldb, "experts have to follow one another"
+    slices = (K + 511) // 512
+    _words(sfa, slices, _align4(M))
+    _words(sfb, *((E,) if grouped else ()), slices, _align4(2 * I))
+    assert (h is None) != (hq is None), "exactly one of h and hq"
+    ldgu = 0 if gu is None else _matrix(gu, _BF16, (M, 2 * I))
+    ldh = 0 if h is None else _matrix(h, _BF16, (M, I))
+    ldhq = 0
+    if hq is not None:
+        ldhq = _matrix(hq, _E4M3, (M, I))
+        _words(sfh, (I + 511) // 512, _align4(M))
+    _status_word(status)
+    _here(a, sfa, b, sfb, layout, h, hq, sfh, gu, status)
+    more = ()
+    if grouped:
+        assert layout.dtype == torch.int32 and layout.shape == (M,) and layout.is_contiguous()
+        more = (_p(layout),)
+    _check(fn, getattr(lib(), fn)(
+        _p(a), lda, _p(sfa), _p(b), ldb, _p(sfb), _p(gu), ldgu, _p(h), ldh, _p(hq), ldhq,
+        _p(sfh if hq is not None else None), *more, M, I, K, *((E,) if grouped else ()), _p(status), _stream(stream)))
+    return h if hq is None else hq
+
+
+def dg_fp8_gated_gemm_nt(a, sfa, b, sfb, h=None, hq=None, sfh=None, gu=None, status=None, stream=None):
+    """silu(A Wg^T) * (A Wu^T) with Wg, Wu the first and second half of b's rows.  a
+    float8_e4m3fn [M, K], sfa packed int32 [ceil(K/512), align4(M)]; b float8_e4m3fn
+    [2I, K], sfb [ceil(K/512), align4(2I)].  The result goes to h bf16 [M, I], or,
+    quantised, to hq float8_e4m3fn [M, I] with sfh packed int32 [ceil(I/512), align4(M)]
+    (the down product's A).  gu bf16 [M, 2I], if given, gets gate and up for the
+    backward pass.  Returns h or hq."""
+    return _gated_forward("dg_fp8_gated_gemm_nt", a, sfa, b, sfb, None, h, hq, sfh, gu, status, stream)
+
+
+def dg_m_grouped_fp8_gated_gemm_nt_contiguous(a, sfa, b, sfb, grouped_layout, h=None, hq=None, sfh=None, gu=None,
+                                              status=None, stream=None):
+    """As dg_fp8_gated_gemm_nt with an expert for each 128 rows: b [E, 2I, K], sfb
+    [E, ceil(K/512), align4(2I)], grouped_layout int32 [M] (-1: not computed)."""
+    assert grouped_layout is not None
+    return _gated_forward("dg_m_grouped_fp8_gated_gemm_nt_contiguous", a, sfa, b, sfb, grouped_layout, h, hq, sfh, gu,
+                          status, stream)
+
+
+def _gated_backward(fn, dy, sfdy, w2, sfw2, layout, gu, dgu, h, status, stream):
+    M, K = dy.shape
+    grouped = layout is not None
+    E, I = (w2.shape[0] if grouped else 1), w2.shape[-1]
+    lddy = _matrix(dy, _E4M3, (M, K))
+    ldw2 = _matrix(w2, _E4M3, (E, K, I) if grouped else (K, I))
+    assert not grouped or E == 1 or w2.stride(0) == K * ldw2, "experts have to follow one another"
+    slices = (K + 511) // 512
+    _words(sfdy, slices, _align4(M))
+    _words(sfw2, *((E,) if grouped else ()), slices, _align4(I))
+    ldgu, lddgu = _matrix(gu, _BF16, (M, 2 * I)), _matrix(dgu, _BF16, (M, 2 * I))
+    ldh = 0 if h is None else _matrix(h, _BF16, (M, I))
+    _status_word(status)
+    _here(dy, sfdy, w2, sfw2, layout, gu, dgu, h, status)
+    more = ()
+    if grouped:
+        assert layout.dtype == torch.int32 and layout.shape == (M,) and layout.is_contiguous()
+        more = (_p(layout),)
+    _check(fn, getattr(lib(), fn)(
+        _p(dy), lddy, _p(sfdy), _p(w2), ldw2, _p(sfw2), _p(gu), ldgu, _p(dgu), lddgu, _p(h), ldh, *more, M, I, K,
+        *((E,) if grouped else ()), _p(status), _stream(stream)))
+    return dgu
+
+
+def dg_fp8_gated_gemm_nn_backward(dy, sfdy, w2, sfw2, gu, dgu, h=None, status=None, stream=None):
+    """Gradient of gate and up: dh = dY @ W2, dgu = [dh * up * silu'(gate), dh * silu(gate)].
+    dy float8_e4m3fn [M, K], sfdy packed int32 [ceil(K/512), align4(M)]; w2 float8_e4m3fn
+    [K, I] (I contiguous), sfw2 [ceil(K/512), align4(I)]; gu and dgu bf16 [M, 2I] (may be one
+    buffer); h bf16 [M, I], if given, gets silu(gate) * up again.  Returns dgu."""
+    return _gated_backward("dg_fp8_gated_gemm_nn_backward", dy, sfdy, w2, sfw2, None, gu, dgu, h, status, stream)
+
+
+def dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(dy, sfdy, w2, sfw2, grouped_layout, gu, dgu, h=None,
+                                                       status=None, stream=None):
+    """As dg_fp8_gated_gemm_nn_backward with an expert for each 128 rows: w2 [E, K, I], sfw2
+    [E, ceil(K/512), align4(I)], grouped_layout int32 [M] (-1: not computed)."""
+    assert grouped_layout is not None
+    return _gated_backward("dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous", dy, sfdy, w2, sfw2, grouped_layout,
+                           gu, dgu, h, status, stream)

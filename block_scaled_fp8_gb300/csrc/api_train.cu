@@ -1,0 +1,231 @@
+// Host side of the feed-forward training entry points of include/dg.h: the gated
+// block and its backward pass, the FP8 quantiser, Newton-Schulz orthogonalisation.
+// Validation order as in api.cu: sizes, pointers, alignment, then the device.
+#include <cstring>
+#include <mutex>
+
+#include "dg_internal.h"
+
+namespace dg {
+namespace {
+
+bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t align4(int64_t x) { return (x + 3) / 4 * 4; }
+
+// 2-D tensor map; true if it was encoded.
+bool encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t dim0, uint64_t dim1,
+            uint64_t stride_bytes, uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle,
+            CUtensorMapL2promotion promo) {
+    TensorMapEncodeFn fn = host_encode();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {dim0, dim1};
+    const cuuint64_t strides[1] = {stride_bytes};
+    const cuuint32_t box[2] = {box0, box1};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              promo, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// FP8 operand: boxes of 128 bytes x `rows`, 128-byte swizzle.
+bool encode_fp8(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t rows) {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, inner, outer, ld, 128, rows, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// bf16 output: boxes of 32 columns x 32 rows, 64-byte swizzle.
+bool encode_out(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, int64_t ld) {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, static_cast<uint64_t>(ld) * 2, 32, 32,
+                  CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
+// Co-resident CTA pairs of a gated kernel on the current device.
+int gated_pairs(int lay, int num_sms) {
+    static std::mutex mu;
+    static int cache[64][2];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    int &v = cache[dev][lay == kLayGated ? 0 : 1];
+    if (v == 0) v = bs2_max_active_pairs(256, false, 256, false, lay);
+    return v * 2 > num_sms ? num_sms / 2 : v;
+}
+
+struct GatedArgs {
+    const void *a;       // x, or dy
+    int64_t lda;
+    const void *sfa;
+    const void *b;       // W1 [groups][2 inner][ldb], or W2 [groups][k][ldb]
+    int64_t ldb;
+    const void *sfb;
+    const int32_t *layout;   // grouped: expert of each row; nullptr: dense
+    void *gu;
+    int64_t ldgu;
+    void *h;
+    int64_t ldh;
+    void *hq;
+    int64_t ldhq;
+    void *sfh;
+    void *dgu;
+    int64_t lddgu;
+    int m, inner, k, groups;
+    bool grouped, backward;
+    int32_t *status;
+    void *stream;
+};
+
+bool bad_out(const void *p, int64_t ld) { return !aligned(p, 16) || ld % 8 != 0; }
+
+dg_status gated(const GatedArgs &g) {
+    const int m = g.m, inner = g.inner, k = g.k;
+    if (m < 0 || inner < 0 || k < 0 || g.groups < 1) return DG_ERR_INVALID_ARG;
+    if (g.grouped && m % kBlockM != 0) return DG_ERR_LAYOUT;
+    if (m == 0 || inner == 0) return DG_OK;
+    if (k == 0 || m > kMaxFewSize || inner > kMaxFewSize / 2 || k > kMaxFewSize) return DG_ERR_UNSUPPORTED;
+    const int64_t units = cdiv(m, 2 * kBlockM);
+    const int cols = g.backward ? 256 : 128;   // output columns of a tile
+    const int64_t tiles = (g.grouped ? m / kBlockM : units) * cdiv(inner, cols);
+    const int64_t b_rows = static_cast<int64_t>(g.groups) * (g.backward ? k : 2 * inner);
+    if (tiles > INT32_MAX / 2 || b_rows > INT32_MAX) return DG_ERR_UNSUPPORTED;
+    if (g.grouped && (units > kMaxPairPrefix || g.groups >= 32768)) return DG_ERR_UNSUPPORTED;
+    // pointers
+    if (!g.a || !g.b || !g.sfa || !g.sfb || (g.grouped && !g.layout)) return DG_ERR_INVALID_ARG;
+    if (g.backward ? (!g.gu || !g.dgu) : (!g.h == !g.hq || (g.hq && !g.sfh))) return DG_ERR_INVALID_ARG;
+    if (g.lda < k || g.ldb < (g.backward ? inner : k) || (g.gu && g.ldgu < 2 * static_cast<int64_t>(inner)) ||
+        (g.h && g.ldh < inner) || (g.hq && g.ldhq < inner) ||
+        (g.dgu && g.lddgu < 2 * static_cast<int64_t>(inner)))
+        return DG_ERR_INVALID_ARG;
+    // alignment: 16-byte rows; whole 16-column chunks of the inner width; whole K-blocks where
+    // an expert's rows of B follow another's along K
+    if (!aligned(g.a, 16) || !aligned(g.b, 16) || !aligned(g.sfa, 16) || !aligned(g.sfb, 16) || !aligned(g.layout, 4))
+        return DG_ERR_ALIGNMENT;
+    if (inner % 16 != 0 || k % 16 != 0 || (g.backward && g.grouped && k % kBlockK != 0) || g.lda % 16 != 0 ||
+        g.ldb % 16 != 0)
+        return DG_ERR_ALIGNMENT;
+    if ((g.gu && bad_out(g.gu, g.ldgu)) || (g.h && bad_out(g.h, g.ldh)) || (g.dgu && bad_out(g.dgu, g.lddgu)) ||
+        (g.hq && (!aligned(g.hq, 16) || g.ldhq % 16 != 0 || !aligned(g.sfh, 16))))
+        return DG_ERR_ALIGNMENT;
+    int sms = 0;
+    dg_status st = host_check_device(&sms, nullptr);
+    if (st != DG_OK) return st;
+
+    GemmParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.mode = g.grouped ? kModeContiguous : kModeDense;
+    p.rows = m;
+    p.n = inner;
+    p.k = k;
+    p.num_groups = g.groups;
+    p.grouped_layout = g.layout;
+    p.status = g.status;
+    p.layout = g.backward ? (kLayGatedBwd | 2) : kLayGated;
+    p.num_m_blocks = static_cast<int>(units);
+    p.num_n_blocks = static_cast<int>(cdiv(inner, cols));
+    p.num_k_blocks = static_cast<int>(cdiv(k, kBlockK));
+    p.group_m = 8;
+    p.timeout_ns = host_timeout_ns();
+    p.debug_flags = host_take_debug_flags();
+    const int64_t psf_k = cdiv(p.num_k_blocks, 4);
+    p.sfa_words = static_cast<const uint32_t *>(g.sfa);
+    p.sfb_words = static_cast<const uint32_t *>(g.sfb);
+    p.sfa_ld = static_cast<int>(align4(m));
+    p.sfb_ld = static_cast<int>(align4(g.backward ? inner : 2 * static_cast<int64_t>(inner)));
+    p.sfa_slices = static_cast<int>(psf_k);
+    p.sfb_slices = static_cast<int>(psf_k * g.groups);
+    p.gu = static_cast<uint16_t *>(g.gu);
+    p.ldgu = g.ldgu;
+    TensorMaps maps;
+    bool ok = encode_fp8(&maps.a, g.a, k, m, g.lda, kBlockM);
+    if (g.backward) {
+        p.d = static_cast<uint16_t *>(g.dgu);
+        p.ldd = g.lddgu;
+        p.h = static_cast<uint16_t *>(g.h);
+        p.ldh = g.ldh;
+        ok &= encode_fp8(&maps.b, g.b, inner, b_rows, g.ldb, kBlockK);
+        ok &= encode_out(&maps.d, g.dgu, 2 * static_cast<uint64_t>(inner), m, g.lddgu);
+        if (g.h) ok &= encode_out(&maps.c, g.h, inner, m, g.ldh);
+        else maps.c = maps.d;   // not used
+    } else {
+        p.d = static_cast<uint16_t *>(g.h);
+        p.ldd = g.ldh;
+        p.hq = static_cast<uint8_t *>(g.hq);
+        p.ldhq = g.ldhq;
+        p.sfh = static_cast<uint8_t *>(g.sfh);
+        p.sfh_ld = static_cast<int>(align4(m));
+        ok &= encode_fp8(&maps.b, g.b, k, b_rows, g.ldb, kBlockM);
+        if (g.h) ok &= encode_out(&maps.d, g.h, inner, m, g.ldh);
+        if (g.gu) ok &= encode_out(&maps.c, g.gu, 2 * static_cast<uint64_t>(inner), m, g.ldgu);
+        if (!g.h) maps.d = g.gu ? maps.c : maps.a;   // not used
+        if (!g.gu) maps.c = maps.d;
+    }
+    maps.b2 = maps.b;   // not used
+    if (!ok) return DG_ERR_CUDA;
+    KernelInfo info;
+    const int pairs = gated_pairs(p.layout, sms);
+    if (pairs <= 0 || !get_bs2_kernel_info(256, false, 256, &info, false, p.layout)) return DG_ERR_UNSUPPORTED;
+    const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
+    host_set_last_config(256, 256, info.stages, grid, 2, 1);
+    const cudaError_t e = launch_bs2_gemm(256, 256, maps, p, grid, static_cast<cudaStream_t>(g.stream));
+    return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" {
+
+dg_status dg_fp8_gated_gemm_nt(const void *a, int64_t lda, const void *sfa, const void *b, int64_t ldb, const void *sfb,
+                               void *gu, int64_t ldgu, void *h, int64_t ldh, void *hq, int64_t ldhq, void *sfh, int m,
+                               int inner, int k, int32_t *status_dev, void *stream) {
+    GatedArgs g = {};
+    g.a = a; g.lda = lda; g.sfa = sfa; g.b = b; g.ldb = ldb; g.sfb = sfb;
+    g.gu = gu; g.ldgu = ldgu; g.h = h; g.ldh = ldh; g.hq = hq; g.ldhq = ldhq; g.sfh = sfh;
+    g.m = m; g.inner = inner; g.k = k; g.groups = 1;
+    g.status = status_dev; g.stream = stream;
+    return gated(g);
+}
+
+dg_status dg_m_grouped_fp8_gated_gemm_nt_contiguous(const void *a, int64_t lda, const void *sfa, const void *b,
+                                                    int64_t ldb, const void *sfb, void *gu, int64_t ldgu, void *h,
+                                                    int64_t ldh, void *hq, int64_t ldhq, void *sfh,
+                                                    const int32_t *grouped_layout, int m_total, int inner, int k,
+                                                    int num_groups, int32_t *status_dev, void *stream) {
+    GatedArgs g = {};
+    g.a = a; g.lda = lda; g.sfa = sfa; g.b = b; g.ldb = ldb; g.sfb = sfb;
+    g.gu = gu; g.ldgu = ldgu; g.h = h; g.ldh = ldh; g.hq = hq; g.ldhq = ldhq; g.sfh = sfh;
+    g.layout = grouped_layout; g.grouped = true;
+    g.m = m_total; g.inner = inner; g.k = k; g.groups = num_groups;
+    g.status = status_dev; g.stream = stream;
+    return gated(g);
+}
+
+dg_status dg_fp8_gated_gemm_nn_backward(const void *dy, int64_t lddy, const void *sfdy, const void *w2, int64_t ldw2,
+                                        const void *sfw2, const void *gu, int64_t ldgu, void *dgu, int64_t lddgu,
+                                        void *h, int64_t ldh, int m, int inner, int k, int32_t *status_dev,
+                                        void *stream) {
+    GatedArgs g = {};
+    g.a = dy; g.lda = lddy; g.sfa = sfdy; g.b = w2; g.ldb = ldw2; g.sfb = sfw2;
+    g.gu = const_cast<void *>(gu); g.ldgu = ldgu; g.dgu = dgu; g.lddgu = lddgu; g.h = h; g.ldh = ldh;
+    g.m = m; g.inner = inner; g.k = k; g.groups = 1; g.backward = true;
+    g.status = status_dev; g.stream = stream;
+    return gated(g);
+}
+
+dg_status dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(const void *dy, int64_t lddy, const void *sfdy,
+                                                             const void *w2, int64_t ldw2, const void *sfw2,
+                                                             const void *gu, int64_t ldgu, void *dgu, int64_t lddgu,
+                                                             void *h, int64_t ldh, const int32_t *grouped_layout,
+                                                             int m_total, int inner, int k, int num_groups,
+                                                             int32_t *status_dev, void *stream) {
+    GatedArgs g = {};
+    g.a = dy; g.lda = lddy; g.sfa = sfdy; g.b = w2; g.ldb = ldw2; g.sfb = sfw2;
+    g.gu = const_cast<void *>(gu); g.ldgu = ldgu; g.dgu = dgu; g.lddgu = lddgu; g.h = h; g.ldh = ldh;
+    g.layout = grouped_layout; g.grouped = true; g.backward = true;
+    g.m = m_total; g.inner = inner; g.k = k; g.groups = num_groups;
+    g.status = status_dev; g.stream = stream;
+    return gated(g);
+}
+
+}  // extern "C"

@@ -18,6 +18,11 @@ constexpr int kMaxPairPrefix = 512;
 // Experts of the PSUM contiguous layout (8-bit ids in the pair kernel's unit info).
 constexpr int kMaxPsumGroups = 255;
 
+// Operand and epilogue layouts of the pair kernel (GemmParams::layout), beside bits 0-3: B is an
+// expert's gate rows and up rows and D = silu(gate) up; D is the gradient of gate and up.
+constexpr int kLayGated = 16;
+constexpr int kLayGatedBwd = 32;
+
 enum GemmMode : int { kModeDense = 0, kModeContiguous = 1, kModeMasked = 2, kModeKGrouped = 3 };
 
 // Runtime parameters of one GEMM launch (passed by value).
@@ -49,7 +54,18 @@ struct GemmParams {
     int c_in_place;      // FP32 C is D itself (same pointer and stride): D is accumulated into at L2
     int c_tma;           // bf16 C goes through shared memory by TMA (dense pair GEMMs, 16-byte aligned rows)
     int layout;          // operand layouts: bit 0 A MN-major ([K][M]), bit 1 B MN-major ([K][N]),
-                         // bit 2 B FP4 (E2M1, one scale per 32 K)
+                         // bit 2 B FP4 (E2M1, one scale per 32 K); kLayGated, kLayGatedBwd
+    // gated forward and backward: n is the inner width I (multiple of 16); gate and up bf16
+    // [rows][2 I] (written forward, read backward; nullable forward), E4M3 h and its packed scale
+    // bytes (forward, instead of d), recomputed bf16 h (backward, nullable)
+    uint16_t *gu;
+    int64_t ldgu;
+    uint8_t *hq;
+    int64_t ldhq;
+    uint8_t *sfh;        // [ceil(I/512)][sfh_ld] words
+    int sfh_ld;
+    uint16_t *h;
+    int64_t ldh;
     // packed UE8M0 scale words, [slices][ld] int32 with ld = align4(mn); the
     // block-scaled kernels' scale warps read them with cp.async
     const uint32_t *sfa_words;
@@ -116,7 +132,7 @@ typedef CUresult (*TensorMapEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint
                                       const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
                                       CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                                       CUtensorMapFloatOOBfill);
-dg_status host_check_device(int *num_sms, bool *limited);   // limited: dg_set_num_sms leaves some out
+dg_status host_check_device(int *num_sms, bool *limited);   // limited (nullable): dg_set_num_sms leaves some out
 TensorMapEncodeFn host_encode();
 uint64_t host_timeout_ns();
 uint32_t host_take_debug_flags();   // clears DG_DEBUG_DROP_ONE_LOAD

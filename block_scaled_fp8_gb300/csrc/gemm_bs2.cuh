@@ -35,6 +35,7 @@
 #include "dg_internal.h"
 #include "gemm_bs.cuh"
 #include "ptx.cuh"
+#include "quant.cuh"
 
 namespace dg {
 
@@ -206,6 +207,7 @@ struct PairTile {
     int d_row0;      // this CTA's first row of D (and C): a_row0 except for the K-grouped layout
     int kb0;         // first 128-K block of the tile's K range
     int nkb;         // 128-K blocks in the tile's K range (K-grouped: 0 for an empty group)
+    int b_kb0;       // gated backward: first 128-K block of the tile's expert in B
 };
 
 // Pair units.  A unit is the row range of one pair tile; the tiles are the
@@ -388,7 +390,7 @@ __device__ __forceinline__ int pair_units(const GemmParams &p, const int *prefix
 
 // Pair tile t (< units * n-blocks) for cluster rank `rank`; units are grouped
 // along M in runs of group_m so that pairs running at the same time share B.
-template <int BN, int MP>
+template <int BN, int MP, int LAY = 0>
 __device__ __forceinline__ void get_pair_tile(const GemmParams &p, const int *prefix, const int *info,
                                               int num_units, int psf_k, int t, int rank, PairTile &tile) {
     const int per_group = p.group_m * p.num_n_blocks;
@@ -399,10 +401,12 @@ __device__ __forceinline__ void get_pair_tile(const GemmParams &p, const int *pr
     const int r = t - g * per_group;
     const int u = first + r % gsize;
     const int nb = r / gsize;
-    tile.n0 = nb * BN;
+    // (gated: a tile is BN/2 output columns, the gate rows of B and then the up rows)
+    tile.n0 = nb * ((LAY & kLayGated) ? BN / 2 : BN);
     int group = 0;
     tile.zero_tail = 0;
     tile.kb0 = 0;
+    tile.b_kb0 = 0;
     tile.nkb = p.num_k_blocks;
     if (MP == 128 || p.mode == kModeDense) {
         tile.a_row0 = u * MP + rank * (MP / 2);
@@ -459,6 +463,21 @@ __device__ __forceinline__ void get_pair_tile(const GemmParams &p, const int *pr
         tile.sfa_y0 = e * psf_k;
         tile.valid_rows = v <= 0 ? 0 : (v < kBlockM ? v : kBlockM);
     }
+    if constexpr ((LAY & kLayGated) != 0) {
+        // the leader's half of B: gate rows of the expert; the peer's: its up rows
+        tile.b_row0 = (2 * group + rank) * p.n + tile.n0;
+        tile.sfb_y0 = group * ((LAY & 4) ? p.num_k_blocks : psf_k);
+        tile.d_row0 = tile.a_row0;
+        return;
+    }
+    if constexpr ((LAY & kLayGatedBwd) != 0) {
+        // B is [experts * K][N]: the expert's K rows
+        tile.b_row0 = tile.n0 + rank * Bs2Config<BN, MP>::kB1Rows;
+        tile.b_kb0 = group * p.num_k_blocks;
+        tile.sfb_y0 = group * psf_k;
+        tile.d_row0 = tile.a_row0;
+        return;
+    }
     tile.b_row0 = group * p.n + tile.n0 + rank * Bs2Config<BN, MP>::kB1Rows;
     tile.b2_row0 = group * p.n + tile.n0 + Bs2Config<BN, MP>::kBN1 + rank * Bs2Config<BN, MP>::kB2Rows;
     // (FP4 B: one packed scale row per K-block, so an expert's rows start at e * K-blocks)
@@ -474,6 +493,27 @@ __device__ __forceinline__ void get_pair_tile(const GemmParams &p, const int *pr
 // the rest of the atom unread), 8-row groups 1024 bytes apart, and a 32-K step
 // of the MMA 4096 bytes on; the instruction descriptor's transpose bits (15:
 // A, 16: B) select the layout.
+// Two chunks of 16 FP32 values as 32 bf16, and two values as one word.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b2);
+}
+__device__ __forceinline__ void pack_bf16_32(const uint32_t (&a)[16], const uint32_t (&b)[16], uint32_t (&o)[16]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        o[i] = pack_bf16(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+        o[8 + i] = pack_bf16(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+    }
+}
+
+// 1 / (1 + e^-x) by the hardware's 2^x and 1/x: within 2^-21 + 2^-23 |x| of the value
+// (e^-x = inf gives 0), far below the bf16 or E4M3 rounding of what it enters.
+__device__ __forceinline__ float sigmoid_approx(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-x)));
+    return r;
+}
+
 template <int BN, bool WITH_C, int MP, bool F32 = false, int LAY = 0>
 __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims__(2, 1, 1)
     dg_bs2_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
@@ -495,6 +535,10 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
     constexpr int MMA_M = MP;
     constexpr int ACC = Cfg::kAccCols;
 
+    // gated forward: two tiles' half-row scales (0: zeros) of each epilogue warp's rows, and the
+    // quadrants' barriers
+    __shared__ uint8_t s_scale[(LAY & kLayGated) ? 512 : 1];
+    __shared__ uint64_t s_xbar[(LAY & kLayGated) ? 4 : 1];
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -536,6 +580,8 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
             uint64_t *b = bars + i;
             mbar_init(b, b >= tempty_bar && b < tempty_bar + NUM_ACC ? 2 * Cfg::kEpiWarps : 1);
         }
+        if constexpr ((LAY & kLayGated) != 0)
+            if (lane < 4) mbar_init(&s_xbar[lane], 2);
         if (lane == 0) *abort_flag = 0;
         fence_mbar_init();
     }
@@ -579,7 +625,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
         bool drop = (p.debug_flags & DG_DEBUG_DROP_ONE_LOAD) && pair_id == 0;
         for (int t = pair_id; t < num_tiles; t += num_pairs) {
             PairTile tile;
-            get_pair_tile<BN, MP>(p, prefix, pinfo, num_units, psf_k, t, rank, tile);
+            get_pair_tile<BN, MP, LAY>(p, prefix, pinfo, num_units, psf_k, t, rank, tile);
             for (int kb0 = 0; kb0 < tile.nkb; kb0 += G) {
                 const int nk = tile.nkb - kb0 < G ? tile.nkb - kb0 : G;
                 const int kg0 = tile.kb0 + kb0;   // the slot's first 128-K block in the operands
@@ -605,7 +651,8 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                                                      tile.a_row0);
                             }
                             if constexpr (B_MN) {
-                                tma_load_2d_pair(b_slot, &tm_b, fb, tile.b_row0, kg0 * kBlockK);
+                                tma_load_2d_pair(b_slot, &tm_b, fb, tile.b_row0,
+                                                 (kg0 + ((LAY & kLayGatedBwd) ? tile.b_kb0 : 0)) * kBlockK);
                             } else {
 #pragma unroll
                                 for (int j = 0; j < G; ++j)
@@ -682,7 +729,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                 int nkb = p.num_k_blocks;
                 if (p.mode == kModeKGrouped) {
                     PairTile tl;
-                    get_pair_tile<BN, MP>(p, prefix, pinfo, num_units, psf_k, t, rank, tl);
+                    get_pair_tile<BN, MP, LAY>(p, prefix, pinfo, num_units, psf_k, t, rank, tl);
                     nkb = tl.nkb;
                 }
                 if (!mbar_wait_cluster_warp(&tempty_bar[acc], acc_phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto mma_done;
@@ -781,7 +828,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
         auto tile_groups = [&](int t) -> int {
             if (p.mode != kModeKGrouped) return groups_per_tile;
             PairTile tl;
-            get_pair_tile<BN, MP>(p, prefix, pinfo, num_units, psf_k, t, rank, tl);
+            get_pair_tile<BN, MP, LAY>(p, prefix, pinfo, num_units, psf_k, t, rank, tl);
             return (tl.nkb + 3) >> 2;
         };
         // this pair's groups: those of tiles pair_id, pair_id + num_pairs, ...
@@ -815,7 +862,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                     !mbar_wait_warp(&sf_sfree_bar[slot], ((gl / NSF) & 1) ^ 1, ctl, DG_DEV_TIMEOUT))
                     return false;
                 if (st_t != lt) {
-                    get_pair_tile<BN, MP>(p, prefix, pinfo, num_units, psf_k, lt, rank, st);
+                    get_pair_tile<BN, MP, LAY>(p, prefix, pinfo, num_units, psf_k, lt, rank, st);
                     st_t = lt;
                 }
                 const uint32_t dst0 = smem_u32(smem_sf + slot * Cfg::kSfSlotBytes);
@@ -840,8 +887,10 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                         for (int c = 0; c < Cfg::kSfbChunks; ++c)
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
+                                // (gated: chunk 0 is the gate rows, chunk 1 the up rows, p.n on)
                                 copy_word(p.sfb_words, p.sfb_ld, p.sfb_slices,
-                                          st.n0 + 128 * c + 32 * q + static_cast<int>(lane),
+                                          st.n0 + ((LAY & kLayGated) ? c * p.n : 128 * c) + 32 * q +
+                                              static_cast<int>(lane),
                                           (B4 || S32) ? st.sfb_y0 + 4 * lj + jj : yb,
                                           128 * Cfg::kSfaKb + 128 * (jj * Cfg::kSfbChunks + c) + 4 * lane + q);
                 } else {
@@ -1033,11 +1082,35 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
             __syncwarp();
             c_pending = true;
         };
+        // gated backward: 32 columns of this thread's row of gate (off 0) or up (off p.n); zero
+        // outside the matrix
+        auto load_gu = [&](uint32_t (&dst)[16], int row, int col, int off) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (row < p.rows && col + 8 * h < p.n)
+                    v = __ldcg(reinterpret_cast<const uint4 *>(p.gu + static_cast<int64_t>(row) * p.ldgu + off + col + 8 * h));
+                dst[4 * h + 0] = v.x;
+                dst[4 * h + 1] = v.y;
+                dst[4 * h + 2] = v.z;
+                dst[4 * h + 3] = v.w;
+            }
+        };
+        // this tile's rows of gate (first warp of a quadrant) or up (second) to L2
+        auto prefetch_gu = [&](const PairTile &tl) {
+            const int row = tl.d_row0 + row_off + static_cast<int>(lane);
+            const int cols = p.n - tl.n0 < BN ? p.n - tl.n0 : BN;
+            if (tl.valid_rows > 0 && row < p.rows && cols > 0)
+                prefetch_l2_bulk(p.gu + static_cast<int64_t>(row) * p.ldgu + (half ? p.n : 0) + tl.n0,
+                                 static_cast<uint32_t>(cols) * 2u);
+        };
+        uint32_t xphase = 0;   // gated forward: the exchange of the halves' amax
         PairTile tile;
         if (pair_id < num_tiles) {
-            get_pair_tile<BN, MP>(p, prefix, pinfo, num_units, psf_k, pair_id, rank, tile);
+            get_pair_tile<BN, MP, LAY>(p, prefix, pinfo, num_units, psf_k, pair_id, rank, tile);
             if constexpr (WITH_C && !F32) prefetch_c(tile);
             if (c_tma) load_ctile(tile);
+            if constexpr ((LAY & kLayGatedBwd) != 0) prefetch_gu(tile);
             if constexpr (WITH_C && F32) {
                 prefetch_d32(tile);
                 if (!p.c_in_place) {
@@ -1049,7 +1122,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
         for (int t = pair_id; t < num_tiles; t += num_pairs) {
             const bool has_next = t + num_pairs < num_tiles;
             PairTile next_tile = tile;
-            if (has_next) get_pair_tile<BN, MP>(p, prefix, pinfo, num_units, psf_k, t + num_pairs, rank, next_tile);
+            if (has_next) get_pair_tile<BN, MP, LAY>(p, prefix, pinfo, num_units, psf_k, t + num_pairs, rank, next_tile);
             // bf16 chunk (16 columns of this thread's row) -> swizzled staging -> TMA store
             // valid_rows: all (MP/2) -> TMA store (clipped at the tensor's edge); 0 -> this
             // CTA's rows belong to no unit of the tile; otherwise (masked edge) direct stores
@@ -1101,6 +1174,41 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                     bulk_commit_group();
                 }
                 buf = buf + 1 == Cfg::kStageBufs ? 0 : buf + 1;
+            };
+            // gated epilogues: 32 columns of this warp's rows (two chunks), 64-byte rows, one TMA
+            // box.  `off` is the column offset of the plane (gate 0, up p.n); where the plane ends
+            // inside the box (p.n is whole 16-column chunks) the first chunk goes out directly, so
+            // that the box does not reach into the next plane.
+            auto store_pair = [&](const CUtensorMap *map, uint16_t *base, int64_t ld, const uint32_t (&o)[16],
+                                  int col, int off) {
+                if (col >= p.n) return;
+                if (col + 32 > p.n) {
+                    const int drow = tile.d_row0 + row_off + static_cast<int>(lane);
+                    if (drow < p.rows) {
+                        uint4 *dp = reinterpret_cast<uint4 *>(base + static_cast<int64_t>(drow) * ld + off + col);
+                        dp[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                        dp[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                    return;
+                }
+                constexpr int NB2 = Cfg::kStageBufs / 2 > 0 ? Cfg::kStageBufs / 2 : 1;
+                uint8_t *sbuf = stage_out + buf * 2 * Cfg::kStageBufBytes;
+                if (lane == 0) bulk_wait_group_read<NB2 - 1>();
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    // 64-byte swizzle: 16-byte unit h of row r sits at unit h ^ ((r >> 1) & 3)
+                    const uint32_t at = lane * 64 + ((h ^ ((lane >> 1) & 3)) * 16);
+                    *reinterpret_cast<uint4 *>(sbuf + at) =
+                        make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(map, sbuf, off + col, tile.d_row0 + row_off);
+                    bulk_commit_group();
+                }
+                buf = buf + 1 == NB2 ? 0 : buf + 1;
             };
             // bf16 C of this tile into registers (the first tile's once its accumulator is
             // complete, so that its loads do not compete with the first operand loads)
@@ -1179,7 +1287,150 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                     continue;
                 }
             }
-            if constexpr (F32) {
+            if constexpr ((LAY & kLayGated) != 0) {
+                // gated forward: this warp's 64 gate and 64 up columns of its 32 rows, in the
+                // two halves of the accumulator, to registers; the accumulator is released
+                // before any arithmetic, so that the next tile's MMAs wait for the reads alone
+                constexpr int HC = BN / 4;
+                uint32_t g[HC / 16][16], u[HC / 16][16];
+                const uint32_t tcol = tmem_base + ((quad * 32) << 16) + acc * ACC + half * HC;
+#pragma unroll
+                for (int j = 0; j < HC / 16; ++j) {
+                    tmem_ld_32x32b_x16(tcol + 16 * j, g[j]);
+                    tmem_ld_32x32b_x16(tcol + BN / 2 + 16 * j, u[j]);
+                }
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < HC / 16; ++j) {
+                    reg_fence16(g[j]);
+                    reg_fence16(u[j]);
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(leader_tempty + acc * 8);
+                if (++acc == NUM_ACC) { acc = 0; acc_phase ^= 1; }
+                const int col0 = tile.n0 + static_cast<int>(half) * HC;
+                const bool stores = tile.valid_rows > 0;   // (all rows of a block, or none)
+                if (p.gu != nullptr && stores) {
+#pragma unroll
+                    for (int j = 0; j < HC / 16; j += 2) {
+                        uint32_t o[16];
+                        pack_bf16_32(g[j], g[j + 1], o);
+                        store_pair(&tm_c, p.gu, p.ldgu, o, col0 + 16 * j, 0);
+                        pack_bf16_32(u[j], u[j + 1], o);
+                        store_pair(&tm_c, p.gu, p.ldgu, o, col0 + 16 * j, p.n);
+                    }
+                }
+                // h = silu(gate) up, in place of gate
+                uint32_t amax = 0u;
+#pragma unroll
+                for (int j = 0; j < HC / 16; ++j)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float gv = __uint_as_float(g[j][i]);
+                        const float h = gv * sigmoid_approx(gv) * __uint_as_float(u[j][i]);
+                        g[j][i] = __float_as_uint(h);
+                        const uint32_t b = col0 + 16 * j < p.n ? amax_bits(h) : 0u;   // (p.n is whole chunks)
+                        amax = b > amax ? b : amax;
+                    }
+                if (p.hq != nullptr) {
+                    // a row's group of 128 columns is this thread's 64 and its partner's (the other
+                    // warp of the quadrant): its scale is the larger of the halves', which meet in
+                    // shared memory, in slots that alternate by tile, so that one arrival a warp and
+                    // tile is enough
+                    const uint32_t slot = xphase * 256u;
+                    const uint32_t mine = amax == 0u ? 0u : ue8m0_of_amax(amax);
+                    s_scale[slot + ew * 32u + lane] = static_cast<uint8_t>(mine);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_xbar[quad]);
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s_xbar[quad], xphase, ctl, DG_DEV_TIMEOUT))) break;
+                    const uint32_t other = s_scale[slot + (ew ^ 4u) * 32u + lane];
+                    xphase ^= 1u;
+                    const uint32_t larger = mine > other ? mine : other;
+                    const uint32_t byte = larger == 0u ? 127u : larger;
+                    const float inv = inv_scale(byte);
+                    const int row = tile.d_row0 + row_off + static_cast<int>(lane);
+                    if (stores && row < p.rows) {
+                        uint8_t *qrow = p.hq + static_cast<int64_t>(row) * p.ldhq + col0;
+#pragma unroll
+                        for (int j = 0; j < HC / 16; ++j) {
+                            if (col0 + 16 * j >= p.n) break;
+                            uint32_t o[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                o[q] = e4m3x4(__uint_as_float(g[j][4 * q]), __uint_as_float(g[j][4 * q + 1]),
+                                              __uint_as_float(g[j][4 * q + 2]), __uint_as_float(g[j][4 * q + 3]), inv);
+                            *reinterpret_cast<uint4 *>(qrow + 16 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                    // the group's byte of the row's scale word; the last tile's threads also clear the
+                    // word's unused bytes, and those of the rows that pad the words to a multiple of 4
+                    if (half == 0 && stores && row < p.sfh_ld) {
+                        const int gi = tile.n0 / kGran;
+                        uint8_t *w = p.sfh + (static_cast<int64_t>(gi >> 2) * p.sfh_ld + row) * 4;
+                        w[gi & 3] = row < p.rows ? static_cast<uint8_t>(byte) : 0;
+                        if (tile.n0 + BN / 2 >= p.n)
+                            for (int b = (gi & 3) + 1; b < 4; ++b) w[b] = 0;
+                    }
+                } else if (stores) {
+#pragma unroll
+                    for (int j = 0; j < HC / 16; j += 2) {
+                        uint32_t o[16];
+                        pack_bf16_32(g[j], g[j + 1], o);
+                        store_pair(&tm_d, p.d, p.ldd, o, col0 + 16 * j, 0);
+                    }
+                }
+            } else if constexpr ((LAY & kLayGatedBwd) != 0) {
+                // gated backward: the accumulator is dh.  This warp's 128 columns of its 32 rows go
+                // to registers and the accumulator is released; gate and up are read 32 columns at a
+                // time (their lines were fetched to L2 a tile ahead)
+                constexpr int HC = BN / 2;
+                uint32_t dh[HC / 16][16];
+                const uint32_t tcol = tmem_base + ((quad * 32) << 16) + acc * ACC + half * HC;
+                if (has_next) prefetch_gu(next_tile);
+#pragma unroll
+                for (int j = 0; j < HC / 16; ++j) tmem_ld_32x32b_x16(tcol + 16 * j, dh[j]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < HC / 16; ++j) reg_fence16(dh[j]);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(leader_tempty + acc * 8);
+                if (++acc == NUM_ACC) { acc = 0; acc_phase ^= 1; }
+                const int row = tile.d_row0 + row_off + static_cast<int>(lane);
+                if (tile.valid_rows > 0) {
+#pragma unroll
+                    for (int j = 0; j < HC / 16; j += 2) {
+                        const int col0 = tile.n0 + static_cast<int>(half) * HC + 16 * j;
+                        uint32_t gv[16], uv[16], og[16], ou[16], oh[16];
+                        load_gu(gv, row, col0, 0);
+                        load_gu(uv, row, col0, p.n);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint32_t *d2 = dh[j + i / 8] + 2 * (i & 7);
+                            float r[2][3];
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const float gt = __uint_as_float(q ? gv[i] & 0xFFFF0000u : gv[i] << 16);
+                                const float up = __uint_as_float(q ? uv[i] & 0xFFFF0000u : uv[i] << 16);
+                                const float d = __uint_as_float(d2[q]);
+                                // s = sigmoid(g), silu = g s, silu' = s + silu (1 - s)
+                                const float sg = sigmoid_approx(gt);
+                                const float si = gt * sg;
+                                r[q][0] = d * up * fmaf(si, 1.0f - sg, sg);
+                                r[q][1] = d * si;
+                                r[q][2] = si * up;
+                            }
+                            og[i] = pack_bf16(r[0][0], r[1][0]);
+                            ou[i] = pack_bf16(r[0][1], r[1][1]);
+                            oh[i] = pack_bf16(r[0][2], r[1][2]);
+                        }
+                        store_pair(&tm_d, p.d, p.ldd, og, col0, 0);
+                        store_pair(&tm_d, p.d, p.ldd, ou, col0, p.n);
+                        if (p.h != nullptr) store_pair(&tm_c, p.h, p.ldh, oh, col0, 0);
+                    }
+                }
+            } else if constexpr (F32) {
                 // FP32 D (and FP32 C): each chunk goes TMEM -> registers (+ C) -> one
                 // 16-column FP32 box through a pair of staging buffers; the accumulator is
                 // released after its last chunk is read

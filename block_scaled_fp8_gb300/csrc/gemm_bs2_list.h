@@ -2,7 +2,8 @@
 // pair tile, FP32 D, operand layouts: bit 0 A MN-major, bit 1 B MN-major, bit 2
 // B FP4, bit 3 A and B scales every 32 K).  The bf16-output NT ones are instantiated in gemm_bs2_inst.cu, the
 // FP32-output ones in gemm_bs2_inst_f32.cu, the NN/TN/TT and K-grouped ones in
-// gemm_bs2_inst_mn.cu, the FP8 x FP4 ones in gemm_bs2_inst_fp4.cu.
+// gemm_bs2_inst_mn.cu, the FP8 x FP4 ones in gemm_bs2_inst_fp4.cu, the gated ones in
+// gemm_bs2_inst_gated.cu.
 #pragma once
 
 #define DG_BS2_LIST_BF16(X)                                                                        \
@@ -31,4 +32,8 @@
     X(256, false, 256, false, 4) X(128, false, 256, false, 4) X(128, true, 256, false, 4)          \
     X(32, false, 128, false, 4) X(96, false, 128, false, 4) X(128, false, 128, false, 4)
 
-#define DG_BS2_LIST(X) DG_BS2_LIST_BF16(X) DG_BS2_LIST_F32(X) DG_BS2_LIST_MN(X) DG_BS2_LIST_FP4(X)
+// Gated feed-forward: forward (layout bit 4, NT), backward (bit 5, NN)
+#define DG_BS2_LIST_GATED(X) X(256, false, 256, false, 16) X(256, false, 256, false, 34)
+
+#define DG_BS2_LIST(X) \
+    DG_BS2_LIST_BF16(X) DG_BS2_LIST_F32(X) DG_BS2_LIST_MN(X) DG_BS2_LIST_FP4(X) DG_BS2_LIST_GATED(X)

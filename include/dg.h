@@ -518,6 +518,74 @@ dg_status dg_moe_fp8_layer(const void *x, int64_t ldx, const int32_t *ids, const
                            int64_t ldy, int t, int h, int i, int experts, int topk, void *workspace,
                            int64_t workspace_bytes, int32_t *status_dev, void *stream);
 
+/*
+ * dg_fp8_gated_gemm_nt -- the gated half of a feed-forward block in one launch: both
+ * projections, the activation and the product.  With W1 = b, its gate rows [0, I)
+ * and its up rows [I, 2I) (as the MoE layer's w1),
+ *
+ *   g[t][i] = sum_k x[t][k] W1[i][k]      u[t][i] = sum_k x[t][k] W1[I + i][k]
+ *   h[t][i] = silu(g) u,  silu(g) = g / (1 + exp(-g))
+ *
+ *   a, sfa  x: E4M3 [m][lda] with packed UE8M0 scales [ceil(k/512)][align4(m)].
+ *   b, sfb  W1: E4M3 [2I][ldb], packed scales [ceil(k/512)][align4(2I)].
+ *   Results, of which exactly one of h and hq:
+ *     h    bf16 [m][ldh].
+ *     hq   E4M3 [m][ldhq] and sfh, its packed scales int32 [ceil(I/512)][align4(m)]:
+ *          the A operand of the down product, quantised from the FP32 h by the rule of
+ *          dg_quantize_fp8, one scale per 1x128; the words' unused bytes are 0.
+ *     gu   NULL, or bf16 [m][ldgu]: g in columns [0, I), u in [I, 2I), as the backward
+ *          pass takes them (h itself comes from the FP32 g and u).
+ *   I (inner) and k multiples of 16; lda, ldb, ldhq multiples of 16, ldh, ldgu of 8; 16-byte
+ *   aligned pointers.  m == 0 or inner == 0 is a no-op, k == 0 DG_ERR_UNSUPPORTED.
+ *   Sums over k are the tensor cores' FP32 sums, in one CTA pair in a fixed order: a row's
+ *   results do not depend on m or on the other rows.  A row of x that holds a NaN gets NaN.
+ * dg_m_grouped_fp8_gated_gemm_nt_contiguous -- the same with one W1 an expert: b
+ *   [num_groups][2I][ldb], sfb [num_groups][ceil(k/512)][align4(2I)]; grouped_layout and its rows
+ *   as for dg_m_grouped_fp8_gemm_nt_contiguous (rows of skipped blocks are left unwritten in all
+ *   results); m_total <= 131072, num_groups < 32768, num_groups * 2I < 2^31.
+ */
+dg_status dg_fp8_gated_gemm_nt(const void *a, int64_t lda, const void *sfa, const void *b, int64_t ldb, const void *sfb,
+                               void *gu, int64_t ldgu, void *h, int64_t ldh, void *hq, int64_t ldhq, void *sfh, int m,
+                               int inner, int k, int32_t *status_dev, void *stream);
+dg_status dg_m_grouped_fp8_gated_gemm_nt_contiguous(const void *a, int64_t lda, const void *sfa, const void *b,
+                                                    int64_t ldb, const void *sfb, void *gu, int64_t ldgu, void *h,
+                                                    int64_t ldh, void *hq, int64_t ldhq, void *sfh,
+                                                    const int32_t *grouped_layout, int m_total, int inner, int k,
+                                                    int num_groups, int32_t *status_dev, void *stream);
+
+/*
+ * dg_fp8_gated_gemm_nn_backward -- the backward pass of that block up to its two projections,
+ * in one launch: the input gradient of the down product y = h W2^T with the activation's
+ * derivative in the epilogue.  With s = 1 / (1 + exp(-g)):
+ *
+ *   dh[t][i] = sum_k dy[t][k] W2[k][i]
+ *   dg = dh u s (1 + g (1 - s))      du = dh g s      h = g s u
+ *
+ *   dy, sfdy   E4M3 [m][lddy] with packed scales [ceil(k/512)][align4(m)]; k is the model width.
+ *   w2, sfw2   E4M3 [k][ldw2], I contiguous (the down product's B as it lies there), packed
+ *        scales [ceil(k/512)][align4(I)]: one per 128 rows of k for each i (dg_quantize_fp8_blocks
+ *        writes this form too).
+ *   gu    bf16 [m][ldgu], gate then up, as the forward call wrote it.
+ *   dgu   bf16 [m][lddgu]: dg in columns [0, I), du in [I, 2I); may be gu itself (same stride).
+ *   h     NULL, or bf16 [m][ldh]: h again, for the gradient of W2.
+ *   The gradients of x and of the weights are products of dgu, h, x and dy: quantise them with
+ *   dg_quantize_fp8 and call dg_fp8_gemm_nn, dg_k_grouped_fp8_gemm_tn_contiguous.
+ *   Size and alignment rules as for dg_fp8_gated_gemm_nt.
+ * dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous -- the same with one W2 an expert: w2
+ *   [num_groups][k][ldw2], sfw2 [num_groups][ceil(k/512)][align4(I)]; k a multiple of 128;
+ *   num_groups * k < 2^31, rows as for the grouped forward call.
+ */
+dg_status dg_fp8_gated_gemm_nn_backward(const void *dy, int64_t lddy, const void *sfdy, const void *w2, int64_t ldw2,
+                                        const void *sfw2, const void *gu, int64_t ldgu, void *dgu, int64_t lddgu,
+                                        void *h, int64_t ldh, int m, int inner, int k, int32_t *status_dev,
+                                        void *stream);
+dg_status dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(const void *dy, int64_t lddy, const void *sfdy,
+                                                             const void *w2, int64_t ldw2, const void *sfw2,
+                                                             const void *gu, int64_t ldgu, void *dgu, int64_t lddgu,
+                                                             void *h, int64_t ldh, const int32_t *grouped_layout,
+                                                             int m_total, int inner, int k, int num_groups,
+                                                             int32_t *status_dev, void *stream);
+
 /* Number of SMs the persistent kernels use (default: all SMs of the current
  * device).  n <= 0 restores the default.  (The kernels that only rearrange data,
  * scale packing, the splitting of a decode call's rows, routing, are not
