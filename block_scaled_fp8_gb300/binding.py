@@ -30,6 +30,8 @@ DG_DEBUG_SINGLE_CTA = 4
 DG_DEBUG_WIDE_PAIR = 8
 DG_LOGITS_F32 = 0
 DG_LOGITS_BF16 = 1
+DG_VALUES_F32 = 0
+DG_VALUES_BF16 = 1
 DG_SCORE_SOFTMAX = 0
 DG_SCORE_SIGMOID = 1
 
@@ -46,7 +48,7 @@ EXPORTS = (
     "dg_bf16_fp4_gemv_nt", "dg_bf16_fp8_gemv_nt", "dg_bf16_fp4_gemv_nt_f32", "dg_bf16_fp8_gemv_nt_f32",
     "dg_bf16_gemv_workspace_bytes", "dg_moe_route", "dg_moe_layer_workspace_bytes", "dg_moe_fp4_layer", "dg_moe_fp8_layer",
     "dg_fp8_gated_gemm_nt", "dg_m_grouped_fp8_gated_gemm_nt_contiguous", "dg_fp8_gated_gemm_nn_backward",
-    "dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous",
+    "dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous", "dg_quantize_fp8", "dg_quantize_fp8_blocks",
 )
 
 
@@ -126,6 +128,9 @@ def lib():
             gated = [P, i64, P, P, i64, P, P, i64, P, i64, P, i64]
             L.dg_fp8_gated_gemm_nn_backward.argtypes = gated + [i32, i32, i32, P, P]
             L.dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous.argtypes = gated + [P, i32, i32, i32, i32, P, P]
+            L.dg_quantize_fp8.argtypes = [P, i32, i64, P, i64, P, P, i64, P, i32, i32, P, i32, P]
+            L.dg_quantize_fp8_blocks.argtypes = [P, i32, i64, i64, P, i64, i64, P, P, i32, i32, i32, P]
+            L.dg_quantize_fp8.restype = L.dg_quantize_fp8_blocks.restype = i32
             for f in ("dg_fp8_gated_gemm_nt", "dg_m_grouped_fp8_gated_gemm_nt_contiguous",
                       "dg_fp8_gated_gemm_nn_backward", "dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous"):
                 getattr(L, f).restype = i32
@@ -720,3 +725,55 @@ def dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(dy, sfdy, w2, sfw2, group
     assert grouped_layout is not None
     return _gated_backward("dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous", dy, sfdy, w2, sfw2, grouped_layout,
                            gu, dgu, h, status, stream)
+
+
+def _values(x):
+    """x's dg_values_format."""
+    assert x.dtype == torch.float32 or x.dtype == _BF16, f"expected float32 or bfloat16 values, got {x.dtype}"
+    return DG_VALUES_F32 if x.dtype == torch.float32 else DG_VALUES_BF16
+
+
+def dg_quantize_fp8(x, q=None, sf=None, qk=None, sfk=None, ks=None, stream=None):
+    """E4M3 codes and packed scales of x [R, C] (float32 or bfloat16): q float8_e4m3fn [R, C]
+    and sf int32 [ceil(C/512), align4(R)] with a scale for each 1x128, qk [R, C] and sfk with one
+    for each 128x1 (either pair may be left out).  sfk is int32 [ceil(R/512), align4(C)], or with
+    group sizes ks (host list, multiples of 128, in sum R) [k_grouped_packed_sf_rows(ks), C], as
+    the K-grouped call takes it.  Returns (q, sf, qk, sfk)."""
+    R, C = x.shape
+    ldx = _matrix(x, x.dtype, (R, C))
+    assert q is not None or qk is not None, "q or qk"
+    ldq = ldqk = 0
+    if q is not None:
+        ldq = _matrix(q, _E4M3, (R, C))
+        _words(sf, (C + 511) // 512, _align4(R))
+    if qk is not None:
+        ldqk = _matrix(qk, _E4M3, (R, C))
+        if ks is None:
+            _words(sfk, (R + 511) // 512, _align4(C))
+        else:
+            _words(sfk, max(0, k_grouped_packed_sf_rows(ks)), C)
+    _here(x, q, qk, sf if q is not None else None, sfk if qk is not None else None)
+    _check("dg_quantize_fp8", lib().dg_quantize_fp8(
+        _p(x), _values(x), ldx, _p(q), ldq, _p(sf), _p(qk), ldqk, _p(sfk), R, C, None if ks is None else _ks_host(ks),
+        0 if ks is None else len(ks), _stream(stream)))
+    return q, sf, qk, sfk
+
+
+def dg_quantize_fp8_blocks(x, q, sf=None, sft=None, stream=None):
+    """E4M3 codes q and packed scales of x [R, C] or [B, R, C] (float32 or bfloat16) with a scale for
+    each 128x128: sf int32 [B, ceil(C/512), align4(R)] for x as B of the NT calls, sft
+    [B, ceil(R/512), align4(C)] for x as B of the NN calls (one may be left out).  Returns (q, sf, sft)."""
+    R, C = x.shape[-2:]
+    B = x.shape[0] if x.dim() == 3 else 1
+    lead = (B,) if x.dim() == 3 else ()
+    ldx, ldq = _matrix(x, x.dtype, (*lead, R, C)), _matrix(q, _E4M3, (*lead, R, C))
+    assert sf is not None or sft is not None, "sf or sft"
+    if sf is not None:
+        _words(sf, *lead, (C + 511) // 512, _align4(R))
+    if sft is not None:
+        _words(sft, *lead, (R + 511) // 512, _align4(C))
+    _here(x, q, sf, sft)
+    _check("dg_quantize_fp8_blocks", lib().dg_quantize_fp8_blocks(
+        _p(x), _values(x), ldx, x.stride(0) if lead else 0, _p(q), ldq, q.stride(0) if lead else 0, _p(sf), _p(sft), B,
+        R, C, _stream(stream)))
+    return q, sf, sft

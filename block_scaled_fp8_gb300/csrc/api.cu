@@ -1071,6 +1071,10 @@ static int64_t k_grouped_rows(const int *ks, int num_groups, KGroupRows *t, int 
     return prow;
 }
 
+extern "C++" int64_t dg::host_k_grouped_rows(const int *ks, int num_groups, KGroupRows *t) {
+    return k_grouped_rows(ks, num_groups, t);
+}
+
 int64_t dg_k_grouped_packed_sf_rows(const int *ks, int num_groups) {
     return k_grouped_rows(ks, num_groups, nullptr);
 }

@@ -169,6 +169,10 @@ dg_status gated(const GatedArgs &g) {
     return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
+bool bad_values(const void *x, int64_t ldx, int fmt) {
+    return !aligned(x, 16) || ldx % (fmt == DG_VALUES_BF16 ? 8 : 4) != 0;
+}
+
 }  // namespace
 }  // namespace dg
 
@@ -226,6 +230,80 @@ dg_status dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(const void *dy, int
     g.m = m_total; g.inner = inner; g.k = k; g.groups = num_groups;
     g.status = status_dev; g.stream = stream;
     return gated(g);
+}
+
+dg_status dg_quantize_fp8(const void *x, int x_fmt, int64_t ldx, void *q, int64_t ldq, void *sf, void *qk, int64_t ldqk,
+                          void *sfk, int rows, int cols, const int *ks, int num_groups, void *stream) {
+    if (rows < 0 || cols < 0 || num_groups < 0) return DG_ERR_INVALID_ARG;
+    if (x_fmt != DG_VALUES_F32 && x_fmt != DG_VALUES_BF16) return DG_ERR_INVALID_ARG;
+    if (!q && !qk) return DG_ERR_INVALID_ARG;
+    KGroupRows t;
+    t.num_groups = 0;
+    if (ks != nullptr) {
+        if (!qk) return DG_ERR_INVALID_ARG;
+        if (host_k_grouped_rows(ks, num_groups, &t) < 0) return DG_ERR_INVALID_ARG;
+        if (cols % 4 != 0 || static_cast<int64_t>(t.srow[num_groups]) * kBlockK != rows) return DG_ERR_LAYOUT;
+    }
+    if (rows == 0 || cols == 0) return DG_OK;
+    if (rows > kMaxFewSize || cols > kMaxFewSize) return DG_ERR_UNSUPPORTED;
+    if (!x || (q && !sf) || (qk && !sfk)) return DG_ERR_INVALID_ARG;
+    if (ldx < cols || (q && ldq < cols) || (qk && ldqk < cols)) return DG_ERR_INVALID_ARG;
+    if (bad_values(x, ldx, x_fmt) || (q && (!aligned(q, 16) || ldq % 16 != 0 || !aligned(sf, 16))) ||
+        (qk && (!aligned(qk, 16) || ldqk % 16 != 0 || !aligned(sfk, 16))))
+        return DG_ERR_ALIGNMENT;
+    int sms = 0;
+    dg_status st = host_check_device(&sms, nullptr);
+    if (st != DG_OK) return st;
+    QuantParams p = {};
+    p.x = x;
+    p.ldx = ldx;
+    p.rows = rows;
+    p.cols = cols;
+    p.q = static_cast<uint8_t *>(q);
+    p.ldq = ldq;
+    p.sf = static_cast<uint8_t *>(sf);
+    p.sf_ld = static_cast<int>(align4(rows));
+    p.qk = static_cast<uint8_t *>(qk);
+    p.ldqk = ldqk;
+    p.sfk = static_cast<uint8_t *>(sfk);
+    p.sfk_ld = static_cast<int>(align4(cols));
+    const cudaError_t e = launch_quantize(p, t, 1, (q ? 1 : 0) | (qk ? 2 : 0), x_fmt == DG_VALUES_BF16, sms,
+                                          static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+dg_status dg_quantize_fp8_blocks(const void *x, int x_fmt, int64_t ldx, int64_t x_batch, void *q, int64_t ldq,
+                                 int64_t q_batch, void *sf, void *sft, int batch, int rows, int cols, void *stream) {
+    if (batch < 0 || rows < 0 || cols < 0) return DG_ERR_INVALID_ARG;
+    if (x_fmt != DG_VALUES_F32 && x_fmt != DG_VALUES_BF16) return DG_ERR_INVALID_ARG;
+    if (batch == 0 || rows == 0 || cols == 0) return DG_OK;
+    if (rows > kMaxFewSize || cols > kMaxFewSize || batch > 65535) return DG_ERR_UNSUPPORTED;
+    if (!x || !q || (!sf && !sft)) return DG_ERR_INVALID_ARG;
+    if (ldx < cols || ldq < cols || x_batch < 0) return DG_ERR_INVALID_ARG;
+    if (batch > 1 && q_batch < (rows - 1) * ldq + cols) return DG_ERR_INVALID_ARG;   // (the matrices' codes are apart)
+    if (batch > 1 && (x_batch % (x_fmt == DG_VALUES_BF16 ? 8 : 4) != 0 || q_batch % 16 != 0)) return DG_ERR_ALIGNMENT;
+    if (bad_values(x, ldx, x_fmt) || !aligned(q, 16) || ldq % 16 != 0 || !aligned(sf, 16) || !aligned(sft, 16))
+        return DG_ERR_ALIGNMENT;
+    int sms = 0;
+    dg_status st = host_check_device(&sms, nullptr);
+    if (st != DG_OK) return st;
+    QuantParams p = {};
+    KGroupRows t;
+    t.num_groups = 0;
+    p.x = x;
+    p.ldx = ldx;
+    p.x_batch = x_batch;
+    p.q_batch = q_batch;
+    p.rows = rows;
+    p.cols = cols;
+    p.q = static_cast<uint8_t *>(q);
+    p.ldq = ldq;
+    p.sf = static_cast<uint8_t *>(sf);
+    p.sf_ld = static_cast<int>(align4(rows));
+    p.sfk = static_cast<uint8_t *>(sft);
+    p.sfk_ld = static_cast<int>(align4(cols));
+    const cudaError_t e = launch_quantize(p, t, batch, 4, x_fmt == DG_VALUES_BF16, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -127,6 +127,26 @@ cudaError_t launch_transform_sf(const float *sf, int batch, int mn_rows, int sf_
                                 int mn, int out_fmt, void *out, int32_t *status,
                                 cudaStream_t stream);
 
+// FP8 quantiser.  sf: a byte a row and 128 columns, words [ceil(cols/512)][sf_ld]; sfk: a byte a
+// column and 128 rows, words [packed rows][sfk_ld].
+struct QuantParams {
+    const void *x;
+    int64_t ldx;
+    int64_t x_batch, q_batch;   // elements from one matrix to the next (blocks)
+    int rows, cols;
+    uint8_t *q;
+    int64_t ldq;
+    uint8_t *sf;
+    int sf_ld;
+    uint8_t *qk;
+    int64_t ldqk;
+    uint8_t *sfk;
+    int sfk_ld;
+};
+// mode: 1 rows, 2 columns, 3 both, 4 blocks (sf and sfk nullable)
+cudaError_t launch_quantize(const QuantParams &p, const KGroupRows &t, int batch, int mode, bool bf16, int num_sms,
+                            cudaStream_t stream);
+
 // Host state and helpers of api.cu that the few-row entry points (api_few.cu) share.
 typedef CUresult (*TensorMapEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                       const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
@@ -135,6 +155,8 @@ typedef CUresult (*TensorMapEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint
 dg_status host_check_device(int *num_sms, bool *limited);   // limited (nullable): dg_set_num_sms leaves some out
 TensorMapEncodeFn host_encode();
 uint64_t host_timeout_ns();
+// Scale rows of the K-grouped layout for host sizes ks; the packed rows, or -1 for invalid sizes.
+int64_t host_k_grouped_rows(const int *ks, int num_groups, KGroupRows *t);
 uint32_t host_take_debug_flags();   // clears DG_DEBUG_DROP_ONE_LOAD
 void host_set_last_config(int block_m, int block_n, int stages, int grid, int kind, int launches);
 cudaError_t launch_fill_d(const void *c, int64_t ldc, void *d, int64_t ldd, int m, int n, bool f32, int num_sms,

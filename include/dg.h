@@ -519,6 +519,39 @@ dg_status dg_moe_fp8_layer(const void *x, int64_t ldx, const int32_t *ids, const
                            int64_t workspace_bytes, int32_t *status_dev, void *stream);
 
 /*
+ * dg_quantize_fp8 -- values to the FP8 operands of the products: E4M3 codes with a scale for
+ * each 1x128 of a row, each 128x1 of a column, or both from one read of the values.
+ *
+ *   s = 2^ceil(log2(amax / 448)) over the group's finite values, 1 for a group of zeros (and at
+ *       least 2^-126);  code = E4M3(x / s), to nearest even
+ *
+ *   x     values [rows][ldx], FP32 or bf16 (dg_values_format), columns contiguous.
+ *   q, sf     E4M3 [rows][ldq] and packed words int32 [ceil(cols/512)][align4(rows)], scales of
+ *         1x128: the operand [rows] of a product along the columns (A or B of the NT call).
+ *         NULL: not wanted.
+ *   qk, sfk   E4M3 [rows][ldqk] and packed words, scales of 128x1: an operand of a product along
+ *         the rows (dg_fp8_gemm_tn; the K-grouped weight gradient), as it lies there.
+ *         ks NULL: sfk is int32 [ceil(rows/512)][align4(cols)].
+ *         ks given (HOST, num_groups sizes as in dg_k_grouped_fp8_gemm_tn_contiguous, in sum
+ *         rows): sfk is int32 [dg_k_grouped_packed_sf_rows(ks, num_groups)][cols], cols % 4 == 0
+ *         (else DG_ERR_LAYOUT).
+ *   Unused bytes of a word and words that pad a row of them are 0.  A NaN or infinite value
+ *   becomes the NaN code and does not count for its group's scale.
+ *   Pointers 16-byte aligned; ldx a multiple of 4 (FP32) or 8 (bf16), ldq and ldqk of 16.
+ *   rows == 0 or cols == 0 is a no-op.  No output may overlap x.
+ * dg_quantize_fp8_blocks -- the same with a scale for each 128x128 block of each of `batch`
+ *   matrices (weights): x at x + b * x_batch elements, q at q + b * q_batch (multiples of 16
+ *   bytes; the matrices' codes apart from one another).  sf: words int32 [batch][ceil(cols/512)][align4(rows)], for the matrix as B of the NT
+ *   calls; sft: [batch][ceil(rows/512)][align4(cols)], for the matrix as it lies there as B of
+ *   the NN calls (products along its rows).  Either may be NULL.  batch <= 65535.
+ */
+typedef enum { DG_VALUES_F32 = 0, DG_VALUES_BF16 = 1 } dg_values_format;
+dg_status dg_quantize_fp8(const void *x, int x_fmt, int64_t ldx, void *q, int64_t ldq, void *sf, void *qk, int64_t ldqk,
+                          void *sfk, int rows, int cols, const int *ks, int num_groups, void *stream);
+dg_status dg_quantize_fp8_blocks(const void *x, int x_fmt, int64_t ldx, int64_t x_batch, void *q, int64_t ldq,
+                                 int64_t q_batch, void *sf, void *sft, int batch, int rows, int cols, void *stream);
+
+/*
  * dg_fp8_gated_gemm_nt -- the gated half of a feed-forward block in one launch: both
  * projections, the activation and the product.  With W1 = b, its gate rows [0, I)
  * and its up rows [I, 2I) (as the MoE layer's w1),
