@@ -49,6 +49,7 @@ EXPORTS = (
     "dg_bf16_gemv_workspace_bytes", "dg_moe_route", "dg_moe_layer_workspace_bytes", "dg_moe_fp4_layer", "dg_moe_fp8_layer",
     "dg_fp8_gated_gemm_nt", "dg_m_grouped_fp8_gated_gemm_nt_contiguous", "dg_fp8_gated_gemm_nn_backward",
     "dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous", "dg_quantize_fp8", "dg_quantize_fp8_blocks",
+    "dg_newton_schulz", "dg_newton_schulz_workspace_bytes",
 )
 
 
@@ -130,6 +131,11 @@ def lib():
             L.dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous.argtypes = gated + [P, i32, i32, i32, i32, P, P]
             L.dg_quantize_fp8.argtypes = [P, i32, i64, P, i64, P, P, i64, P, i32, i32, P, i32, P]
             L.dg_quantize_fp8_blocks.argtypes = [P, i32, i64, i64, P, i64, i64, P, P, i32, i32, i32, P]
+            L.dg_newton_schulz.argtypes = [P, i32, i64, i64, P, i64, i64, i32, i32, i32, i32, f32, f32, f32, f32, P, i64,
+                                           P, P]
+            L.dg_newton_schulz.restype = i32
+            L.dg_newton_schulz_workspace_bytes.argtypes = [i32, i32, i32]
+            L.dg_newton_schulz_workspace_bytes.restype = i64
             L.dg_quantize_fp8.restype = L.dg_quantize_fp8_blocks.restype = i32
             for f in ("dg_fp8_gated_gemm_nt", "dg_m_grouped_fp8_gated_gemm_nt_contiguous",
                       "dg_fp8_gated_gemm_nn_backward", "dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous"):
@@ -777,3 +783,33 @@ def dg_quantize_fp8_blocks(x, q, sf=None, sft=None, stream=None):
         _p(x), _values(x), ldx, x.stride(0) if lead else 0, _p(q), ldq, q.stride(0) if lead else 0, _p(sf), _p(sft), B,
         R, C, _stream(stream)))
     return q, sf, sft
+
+
+def newton_schulz_workspace_bytes(batch: int, rows: int, cols: int) -> int:
+    return int(lib().dg_newton_schulz_workspace_bytes(batch, rows, cols))
+
+
+def dg_newton_schulz(g, out, steps: int = 5, coef=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, workspace=None,
+                     status=None, stream=None):
+    """Orthogonalises g [R, C] or [B, R, C] (float32 or bfloat16) into out (bfloat16, same shape): X = g /
+    (|g| + eps), then `steps` times X <- a X + (b A + c A A) X with A = X X^T and (a, b, c) = coef
+    (X^T X on the right where R > C).  workspace: a device buffer of
+    newton_schulz_workspace_bytes(B, R, C) bytes (made here if not given)."""
+    R, C = g.shape[-2:]
+    B = g.shape[0] if g.dim() == 3 else 1
+    lead = (B,) if g.dim() == 3 else ()
+    ldg, ldo = _matrix(g, g.dtype, (*lead, R, C)), _matrix(out, _BF16, (*lead, R, C))
+    a, b, c = coef
+    _status_word(status)
+    _here(g, out, workspace, status)
+    if workspace is None:
+        need = newton_schulz_workspace_bytes(B, R, C)
+        if need > 0 and steps >= 1:   # (what is refused makes no workspace)
+            workspace = _workspace(need, g, stream)
+    else:
+        assert workspace.is_contiguous()
+    _check("dg_newton_schulz", lib().dg_newton_schulz(
+        _p(g), _values(g), ldg, g.stride(0) if lead else 0, _p(out), ldo, out.stride(0) if lead else 0, B, R, C,
+        steps, a, b, c, eps, _p(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _p(status), _stream(stream)))
+    return out

@@ -169,6 +169,10 @@ dg_status gated(const GatedArgs &g) {
     return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
+bool ns_unsupported(int batch, int rows, int cols) {
+    return batch > 4096 || rows > kMaxNsSide || cols > kMaxNsSide || static_cast<int64_t>(rows) * cols > kMaxNsElements;
+}
+
 bool bad_values(const void *x, int64_t ldx, int fmt) {
     return !aligned(x, 16) || ldx % (fmt == DG_VALUES_BF16 ? 8 : 4) != 0;
 }
@@ -303,6 +307,51 @@ dg_status dg_quantize_fp8_blocks(const void *x, int x_fmt, int64_t ldx, int64_t 
     p.sfk = static_cast<uint8_t *>(sft);
     p.sfk_ld = static_cast<int>(align4(cols));
     const cudaError_t e = launch_quantize(p, t, batch, 4, x_fmt == DG_VALUES_BF16, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+int64_t dg_newton_schulz_workspace_bytes(int batch, int rows, int cols) {
+    if (batch < 0 || rows < 0 || cols < 0 || ns_unsupported(batch, rows, cols)) return -1;
+    return ns_workspace_bytes(batch, rows, cols);
+}
+
+dg_status dg_newton_schulz(const void *g, int g_fmt, int64_t ldg, int64_t g_batch, void *out, int64_t ldo,
+                           int64_t out_batch, int batch, int rows, int cols, int steps, float a, float b, float c,
+                           float eps, void *workspace, int64_t workspace_bytes, int32_t *status_dev, void *stream) {
+    if (batch < 0 || rows < 0 || cols < 0 || steps < 1 || !(eps >= 0.0f)) return DG_ERR_INVALID_ARG;
+    if (g_fmt != DG_VALUES_F32 && g_fmt != DG_VALUES_BF16) return DG_ERR_INVALID_ARG;
+    if (batch == 0 || rows == 0 || cols == 0) return DG_OK;
+    if (ns_unsupported(batch, rows, cols)) return DG_ERR_UNSUPPORTED;
+    if (!g || !out || !workspace || ldg < cols || ldo < cols) return DG_ERR_INVALID_ARG;
+    if (g_batch < 0 || (batch > 1 && out_batch < (rows - 1) * ldo + cols)) return DG_ERR_INVALID_ARG;
+    if (workspace_bytes < ns_workspace_bytes(batch, rows, cols)) return DG_ERR_INVALID_ARG;
+    if (!aligned(g, g_fmt == DG_VALUES_F32 ? 4 : 2) || !aligned(out, 2) || !aligned(workspace, 128)) return DG_ERR_ALIGNMENT;
+    int sms = 0;
+    dg_status st = host_check_device(&sms, nullptr);
+    if (st != DG_OK) return st;
+    if (sms < 2) return DG_ERR_UNSUPPORTED;   // (CTA pairs)
+    NsParams p = {};
+    p.g = g;
+    p.ldg = ldg;
+    p.g_batch = g_batch;
+    p.out = static_cast<uint16_t *>(out);
+    p.ldo = ldo;
+    p.out_batch = out_batch;
+    p.batch = batch;
+    p.rows = rows;
+    p.cols = cols;
+    p.ca = a;
+    p.cb = b;
+    p.cc = c;
+    p.eps = eps;
+    p.workspace = workspace;
+    p.status = status_dev;
+    p.timeout_ns = host_timeout_ns();
+    p.debug_flags = host_take_debug_flags();
+    int launches = 0;
+    const cudaError_t e = launch_newton_schulz(p, steps, g_fmt == DG_VALUES_BF16, sms, static_cast<cudaStream_t>(stream),
+                                               &launches);
+    host_set_last_config(256, 256, 0, 0, 6, launches);
     return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 

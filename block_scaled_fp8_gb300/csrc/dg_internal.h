@@ -147,6 +147,31 @@ struct QuantParams {
 cudaError_t launch_quantize(const QuantParams &p, const KGroupRows &t, int batch, int mode, bool bf16, int num_sms,
                             cudaStream_t stream);
 
+// Newton-Schulz orthogonalisation.  The caller sets what is above the line.
+struct NsParams {
+    const void *g;          // [batch][rows][ldg], FP32 or bf16
+    int64_t ldg, g_batch;
+    uint16_t *out;          // bf16 [batch][rows][ldo]
+    int64_t ldo, out_batch;
+    int batch, rows, cols;
+    float ca, cb, cc, eps;
+    void *workspace;        // ns_workspace_bytes(batch, rows, cols)
+    int32_t *status;
+    uint64_t timeout_ns;
+    uint32_t debug_flags;
+    // ----
+    int lo, hi;             // short and long side: X is [lo][hi]
+    int64_t ldx, lda;
+    uint16_t *xh[2];        // FP16 high planes of X: this step's, the next's
+    uint16_t *xl;           // low plane
+    uint16_t *a, *b;        // FP16 [batch][lo][lda]
+    double *partial;        // [batch][num_partial] sums of squares
+    int num_partial;
+    int dense;              // a matrix's rows of G follow one another
+};
+int64_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, cudaStream_t stream, int *launches);
+
 // Host state and helpers of api.cu that the few-row entry points (api_few.cu) share.
 typedef CUresult (*TensorMapEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                       const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
@@ -169,6 +194,8 @@ constexpr int kMaxFewSize = 0x7FFFFFFF - 255;   // n and k of a product, tokens 
 constexpr int kMaxLayerTopk = 16;
 constexpr int kMaxLayerExperts = 1024;
 constexpr int kMaxLayerWidth = 1 << 24;
+constexpr int kMaxNsSide = 1 << 20;             // sides and elements of a matrix to orthogonalise
+constexpr int64_t kMaxNsElements = 1ll << 31;
 constexpr int kMaxRouteExperts = 1024;
 constexpr int kMaxRouteTopk = 32;
 

@@ -619,6 +619,35 @@ dg_status dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(const void *dy, int
                                                              int m_total, int inner, int k, int num_groups,
                                                              int32_t *status_dev, void *stream);
 
+/*
+ * dg_newton_schulz -- orthogonalises each of `batch` matrices by Newton-Schulz products (the
+ * update that an orthogonalising optimiser makes of a weight gradient).  With G a matrix, X its
+ * form with the short side as rows (G, or its transpose where rows > cols):
+ *
+ *   X = X / (|G|_F + eps);  steps times: A = X X^T, X <- a X + (b A + c A A) X;  out = X (transposed back)
+ *
+ *   g     FP32 or bf16 (dg_values_format) [rows][ldg] at g + i * g_batch elements.
+ *   out   bf16 [rows][ldo] at out + i * out_batch elements (matrices apart from one another);
+ *         may be g itself where g is bf16 of the same strides.
+ *   steps >= 1; a, b, c the polynomial (3.4445, -4.7750, 2.0315 brings singular values from
+ *         above 0.003 to 0.7 .. 1.2 in five steps); eps >= 0.  A polynomial or a G that
+ *         makes an element of X or A or of b A + c A A 16 or more gives infinities or NaN.
+ *   The operands of the products are rounded to 11 bits, X itself is kept to 22; sums are FP32.  The result
+ *   differs from the definition's by about 1e-3 of its RMS before its rounding to bf16.
+ *   A zero matrix gives zeros; a NaN or infinite value makes its matrix NaN, no other.
+ *   A matrix's result does not depend on the others, nor on batch.
+ *   No alignment beyond the elements' own; rows, cols <= 2^20 and rows * cols <= 2^31, batch <=
+ *   4096 (DG_ERR_UNSUPPORTED).  batch, rows or cols 0 is a no-op.
+ *   workspace   device memory, 128-byte aligned, dg_newton_schulz_workspace_bytes(batch, rows,
+ *         cols) bytes (-1 for sizes that the call refuses); needs no initialisation and
+ *         does not outlive the call.  Calls that may run at the same time need one each.
+ *   2 + 3 steps launches.
+ */
+int64_t dg_newton_schulz_workspace_bytes(int batch, int rows, int cols);
+dg_status dg_newton_schulz(const void *g, int g_fmt, int64_t ldg, int64_t g_batch, void *out, int64_t ldo,
+                           int64_t out_batch, int batch, int rows, int cols, int steps, float a, float b, float c,
+                           float eps, void *workspace, int64_t workspace_bytes, int32_t *status_dev, void *stream);
+
 /* Number of SMs the persistent kernels use (default: all SMs of the current
  * device).  n <= 0 restores the default.  (The kernels that only rearrange data,
  * scale packing, the splitting of a decode call's rows, routing, are not
@@ -659,7 +688,7 @@ const char *dg_status_string(int status);
  * out[0]=BLOCK_M, out[1]=BLOCK_N (kinds 3 and 5: rows of the narrow operand in
  * shared memory), out[2]=stages, out[3]=grid size,
  * out[4]=kernel kind (0 block-scaled, 1 FP32-promotion, 2 block-scaled on
- * CTA pairs, 3 few-row product, 5 MoE layer for few tokens), out[5]=number of
+ * CTA pairs, 3 few-row product, 5 MoE layer for few tokens, 6 Newton-Schulz products), out[5]=number of
  * kernel launches of that call. */
 void dg_get_last_config(int out[6]);
 

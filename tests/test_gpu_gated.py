@@ -303,3 +303,38 @@ def test_last_config():
     dg.dg_fp8_gated_gemm_nt(a, sfa, b, sfb, h=torch.empty(300, 256, dtype=BF16, device="cuda"))
     cfg = dg.last_config()
     assert cfg["kind"] == 2 and cfg["launches"] == 1 and cfg["block_m"] == 256
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_lost_load_is_reported(backward):
+    """A load that never comes ends in a time-out and a status; the next call is whole."""
+    torch.manual_seed(17)
+    m, i, k = 512, 384, 640
+    a, sfa, _ = rows_operand(torch.randn(m, k))
+    b, sfb, _ = block_operand(torch.randn(2 * i, k) * k ** -0.5)
+    c, sfc, _ = block_operand(torch.randn(k, i), along_rows=True)
+    a, sfa, b, sfb, c, sfc = cuda(a, sfa, b, sfb, c, sfc)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gu = torch.randn(m, 2 * i, device="cuda").to(BF16)
+
+    def call():
+        if backward:
+            out = torch.empty_like(gu)
+            dg.dg_fp8_gated_gemm_nn_backward(a, sfa, c, sfc, gu, out, status=status)
+            return out
+        out = torch.empty(m, i, dtype=E4M3, device="cuda")
+        dg.dg_fp8_gated_gemm_nt(a, sfa, b, sfb, hq=out, sfh=torch.empty(1, m, dtype=torch.int32, device="cuda"),
+                                status=status)
+        return out.view(torch.uint8)
+    want = call()
+    dg.set_wait_timeout_ms(20)
+    dg.set_debug_flags(dg.DG_DEBUG_DROP_ONE_LOAD)
+    try:
+        call()
+        torch.cuda.synchronize()
+    finally:
+        dg.set_wait_timeout_ms(0)
+        dg.set_debug_flags(0)
+    assert int(status) == dg.DG_DEV_TIMEOUT
+    status.zero_()
+    assert torch.equal(call(), want) and int(status) == 0
