@@ -164,7 +164,9 @@ struct NsParams {
     int64_t ldx, lda;
     uint16_t *xh[2];        // FP16 high planes of X: this step's, the next's
     uint16_t *xl;           // low plane
-    uint16_t *a, *b;        // FP16 [batch][lo][lda]
+    uint16_t *a, *b;        // FP16 [batch][lo][lda], 0 on the diagonal
+    float *da, *db;         // their diagonals, FP32 [batch][lo]
+    int out_tma;            // the output's rows can be stored by TMA
     double *partial;        // [batch][num_partial] sums of squares
     int num_partial;
     int dense;              // a matrix's rows of G follow one another

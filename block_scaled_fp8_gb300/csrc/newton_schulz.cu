@@ -29,11 +29,16 @@ namespace {
 constexpr float kScale = 4096.0f;          // of all FP16 planes
 constexpr int kTile = 256;                 // rows and columns of a pair tile
 constexpr int kKBlock = 64;                // K of a stage: 128 bytes
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kStageBytes = 2 * 128 * 128; // A and B: 128 rows of 128 bytes each
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
-constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
+// Epilogue: an epilogue warp's 32 rows x 128 columns of a tile in chunks of 32 columns; a chunk
+// passes through one of two slots of two boxes (32 rows of 64 bytes, 64-byte swizzle)
+constexpr int kBoxBytes = 32 * 64;
+constexpr int kSlotBytes = 2 * kBoxBytes;
+constexpr int kEpiBytes = kEpiWarps * 2 * kSlotBytes;
+constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiBytes + 512;
 
 // ------------------------------------------------------------------ norm and split
 
@@ -104,15 +109,10 @@ __global__ void __launch_bounds__(256) dg_ns_norm_kernel(const __grid_constant__
     }
 }
 
-// X0 as high and low planes [lo][ld], transposed where G is tall; tiles of 64x64 through shared memory.
-template <bool BF16>
-__global__ void __launch_bounds__(256) dg_ns_split_kernel(const __grid_constant__ NsParams p) {
-    __shared__ float tile[64][65];
+// 2^12 / (norm + eps) in two factors, so that neither leaves FP32's range.  Every CTA adds the
+// partial sums in the same order.
+__device__ __forceinline__ void norm_factors(const NsParams &p, int64_t batch, float &f1, float &f2) {
     __shared__ double sum;
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const int64_t batch = blockIdx.z;
-    // every CTA adds the partial sums in the same order
     if (threadIdx.x < 32) {
         double s = 0.0;
         for (int i = threadIdx.x; i < p.num_partial; i += 32) s += p.partial[batch * p.num_partial + i];
@@ -120,36 +120,100 @@ __global__ void __launch_bounds__(256) dg_ns_split_kernel(const __grid_constant_
         if (threadIdx.x == 0) sum = s;
     }
     __syncthreads();
-    // 2^12 / (norm + eps) in two factors, so that neither leaves FP32's range
     const double norm = sqrt(sum) + static_cast<double>(p.eps);
     int e = 0;
-    const double mant = norm > 0.0 ? frexp(static_cast<double>(kScale) / norm, &e) : 0.0;
+    // (not norm > 0: a NaN stays one)
+    const double mant = norm == 0.0 ? 0.0 : frexp(static_cast<double>(kScale) / norm, &e);
     const int e1 = e / 2;
-    const float f1 = static_cast<float>(ldexp(1.0, e1)), f2 = static_cast<float>(ldexp(mant, e - e1));
+    f1 = static_cast<float>(ldexp(1.0, e1));
+    f2 = static_cast<float>(ldexp(mant, e - e1));
+}
+
+// Two values as high and low FP16 pairs.
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const __half2 l = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+template <bool BF16>
+__device__ __forceinline__ float g_value(const char *g, int64_t at) {
+    return BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(g)[at]) << 16)
+                : reinterpret_cast<const float *>(g)[at];
+}
+
+// X0 as high and low planes [lo][ldx].  A wide G row by row, 8 values a thread (16-byte loads where
+// the rows allow them); a tall G transposed through 64x64 tiles in shared memory.
+template <bool BF16, bool TALL>
+__global__ void __launch_bounds__(256) dg_ns_split_kernel(const __grid_constant__ NsParams p) {
+    __shared__ float tile[TALL ? 64 : 1][65];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int64_t batch = blockIdx.z;
+    float f1, f2;
+    norm_factors(p, batch, f1, f2);
     const char *g = static_cast<const char *>(p.g) + batch * p.g_batch * (BF16 ? 2 : 4);
-    const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;   // of G
-    for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-        const int r = r0 + i / 64, c = c0 + i % 64;
-        float v = 0.f;
-        if (r < p.rows && c < p.cols) {
+    if constexpr (!TALL) {
+        constexpr int kRows = 8;   // of G, 2048 columns each
+        const int c = static_cast<int>(blockIdx.x) * 2048 + static_cast<int>(threadIdx.x) * 8;
+        const bool vec = (reinterpret_cast<uintptr_t>(g) & 15u) == 0 && p.ldg % (BF16 ? 8 : 4) == 0 && c + 8 <= p.cols;
+        if (c >= p.cols) return;
+#pragma unroll 4
+        for (int i = 0; i < kRows; ++i) {
+            const int r = static_cast<int>(blockIdx.y) * kRows + i;
+            if (r >= p.rows) break;
             const int64_t at = static_cast<int64_t>(r) * p.ldg + c;
-            v = BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(g)[at]) << 16)
-                     : reinterpret_cast<const float *>(g)[at];
+            float v[8];
+            if (vec) {
+                const uint4 *q = reinterpret_cast<const uint4 *>(g + at * (BF16 ? 2 : 4));
+                const uint4 a = __ldg(q);
+                const uint32_t x[4] = {a.x, a.y, a.z, a.w};
+                if constexpr (BF16) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[2 * j] = __uint_as_float(x[j] << 16);
+                        v[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+                    }
+                } else {
+                    const uint4 b = __ldg(q + 1);
+                    const uint32_t y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[j] = __uint_as_float(x[j]);
+                        v[4 + j] = __uint_as_float(y[j]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = c + j < p.cols ? g_value<BF16>(g, at + j) : 0.f;
+            }
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split2(v[2 * j] * f1 * f2, v[2 * j + 1] * f1 * f2, h[j], l[j]);
+            const int64_t to = (batch * p.lo + r) * p.ldx + c;   // (rows are padded to whole 64s)
+            *reinterpret_cast<uint4 *>(p.xh[0] + to) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(p.xl + to) = make_uint4(l[0], l[1], l[2], l[3]);
         }
-        tile[i / 64][i % 64] = v * f1 * f2;
-    }
-    __syncthreads();
-    const bool tall = p.rows > p.cols;
-    const int x0 = tall ? c0 : r0, y0 = tall ? r0 : c0;     // of X
-    for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-        const int r = i / 32, c = 2 * (i % 32);
-        if (x0 + r >= p.lo || y0 + c >= p.hi) continue;
-        const float a = tall ? tile[c][r] : tile[r][c], b = tall ? tile[c + 1][r] : tile[r][c + 1];
-        const __half2 h = __floats2half2_rn(a, b);
-        const __half2 l = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
-        const int64_t at = (batch * p.lo + x0 + r) * p.ldx + y0 + c;
-        *reinterpret_cast<__half2 *>(p.xh[0] + at) = h;      // (ld is even: the pair past the end is padding)
-        *reinterpret_cast<__half2 *>(p.xl + at) = l;
+    } else {
+        const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;   // of G
+#pragma unroll 8
+        for (int i = threadIdx.x; i < 64 * 64; i += 256) {
+            const int r = r0 + i / 64, c = c0 + i % 64;
+            tile[i / 64][i % 64] =
+                r < p.rows && c < p.cols ? g_value<BF16>(g, static_cast<int64_t>(r) * p.ldg + c) * f1 * f2 : 0.f;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 64 * 8; i += 256) {
+            const int r = i / 8, c = 8 * (i % 8);               // of X's tile
+            if (c0 + r >= p.lo || r0 + c >= p.hi) continue;
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split2(tile[c + 2 * j][r], tile[c + 2 * j + 1][r], h[j], l[j]);
+            const int64_t to = (batch * p.lo + c0 + r) * p.ldx + r0 + c;
+            *reinterpret_cast<uint4 *>(p.xh[0] + to) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(p.xl + to) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
     }
 }
 
@@ -173,32 +237,40 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 }
 __device__ __forceinline__ float2 half2_values(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
 
-// 16 consecutive FP16 values (rows are padded to whole chunks of 16).
-__device__ __forceinline__ void load16(const uint16_t *at, uint32_t (&w)[8]) {
-    const uint4 a = __ldcg(reinterpret_cast<const uint4 *>(at)), b = __ldcg(reinterpret_cast<const uint4 *>(at) + 1);
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-}
-
 // MODE kNsGram: D = A; kNsPoly: D = b A + c A A; kNsUpdate: X planes of a X + B X; kNsLast: the same
-// to the bf16 output.  The first two are [lo][lo] products of K-major operands; the others take X as
-// the MN-major operand ([K][N], N contiguous).
+// to the bf16 output.  The first two are [lo][lo] products of K-major operands and symmetric: the
+// tiles on and above the diagonal are computed, and those above it stored twice, once transposed.
+// The others take X as the MN-major operand ([K][N], N contiguous).
+//
+// The diagonals of A and B are kept apart in FP32 and are 0 in the FP16 matrices: with A = D + R,
+// A A = D D + D R + R D + R R, and B X = diag(B) X + (rest) X.  Near convergence X X^T is close to
+// the identity, so that the diagonal holds most of A and B, and its rounding to 11 bits most of the error: with it
+// in FP32 the result's error is about half (noise 512x512: 7e-4 against 1.5e-3 of its norm).
+//
+// The epilogue's own operands (A; the planes of X) come by TMA into the boxes that the results go
+// out from, two chunks ahead.
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     dg_ns_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                      const __grid_constant__ CUtensorMap tm_in0, const __grid_constant__ CUtensorMap tm_in1,
+                      const __grid_constant__ CUtensorMap tm_out0, const __grid_constant__ CUtensorMap tm_out1,
                       const __grid_constant__ NsParams p, const int k) {
     constexpr bool B_MN = MODE >= kNsUpdate;
+    constexpr bool SYM = MODE < kNsUpdate;
+    constexpr int kLoads = MODE == kNsGram ? 0 : MODE == kNsPoly ? 1 : 2;   // boxes a chunk reads
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     uint8_t *smem_a = smem, *smem_b = smem + kStages * 16384;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes);
+    uint8_t *smem_epi = smem + kStages * kStageBytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_epi + kEpiBytes);
     uint64_t *full_bar = bars;                   // [kStages] leader: both CTAs' stages landed
     uint64_t *empty_bar = full_bar + kStages;    // [kStages] both: MMAs done with the stage
     uint64_t *tfull_bar = empty_bar + kStages;   // [2] both: accumulator complete
     uint64_t *tempty_bar = tfull_bar + 2;        // [2] leader: both epilogues drained
     uint64_t *drain_bar = tempty_bar + 2;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain_bar + 1);
+    uint64_t *in_bar = drain_bar + 1;            // [kEpiWarps][2] an epilogue warp's boxes landed
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(in_bar + 2 * kEpiWarps);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -208,11 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const int pair_id = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
     const int rows = p.lo, cols = MODE >= kNsUpdate ? p.hi : p.lo;
     const int tm = (rows + kTile - 1) / kTile, tn = (cols + kTile - 1) / kTile;
-    const int per = tm * tn, num_tiles = per * p.batch;
+    const int per = SYM ? tm * (tm + 1) / 2 : tm * tn, num_tiles = per * p.batch;
     const int nkb = (k + kKBlock - 1) / kKBlock;
 
     if (warp == 0) {
-        if (lane < 2 * kStages + 5) mbar_init(bars + lane, bars + lane >= tempty_bar && bars + lane < tempty_bar + 2 ? 2 * kEpiWarps : 1);
+        for (uint64_t *b = bars + lane; b < in_bar + 2 * kEpiWarps; b += 32)
+            mbar_init(b, b >= tempty_bar && b < tempty_bar + 2 ? 2 * kEpiWarps : 1);
         if (lane == 0) *abort_flag = 0;
         fence_mbar_init();
         if (lane == 0) {
@@ -233,12 +306,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_holder;
 
-    // tile t: (batch, m, n), the m tiles of a column of tiles first
+    // tile t: (batch, m, n), the m tiles of a column of tiles first; symmetric: column n has tiles 0..n
     auto locate = [&](int t, int &b, int &m0, int &n0) {
         b = t / per;
         const int r = t - b * per;
-        m0 = (r % tm) * kTile;
-        n0 = (r / tm) * kTile;
+        if constexpr (SYM) {
+            int n = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
+            while (n * (n + 1) / 2 > r) --n;
+            while ((n + 1) * (n + 2) / 2 <= r) ++n;
+            m0 = (r - n * (n + 1) / 2) * kTile;
+            n0 = n * kTile;
+        } else {
+            m0 = (r % tm) * kTile;
+            n0 = (r / tm) * kTile;
+        }
     };
 
     if (warp == 0) {
@@ -318,87 +399,215 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     } else {
         const uint32_t ew = warp - 2, quad = warp & 3, half = ew >> 2;
         const uint32_t leader_tempty = mapa_shared(smem_u32(tempty_bar), 0);
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        for (int t = pair_id; t < num_tiles; t += num_pairs) {
+        uint8_t *const slots = smem_epi + ew * 2 * kSlotBytes;
+        uint64_t *const landed = in_bar + 2 * ew;
+        const int row_off = rank * 128 + static_cast<int>(quad) * 32, col_off = static_cast<int>(half) * 128;
+        // 16-byte unit h of row r of a box (64-byte swizzle)
+        auto unit = [](uint8_t *box, int r, int h) { return reinterpret_cast<uint4 *>(box + r * 64 + ((h ^ ((r >> 1) & 3)) << 4)); };
+        // chunk j of tile t: the epilogue's operands, into slot j & 1 (j counts on over the tiles)
+        auto load_chunk = [&](int t, int j) {
+            if constexpr (kLoads > 0) {
+                if (t >= num_tiles) return;
+                int b, m0, n0;
+                locate(t, b, m0, n0);
+                uint8_t *box = slots + (j & 1) * kSlotBytes;
+                const int x = n0 + col_off + 32 * (j & 3), y = m0 + row_off;
+                mbar_arrive_expect_tx(&landed[j & 1], kLoads * kBoxBytes);
+                tma_load_3d(box, &tm_in0, &landed[j & 1], x, y, b);
+                if constexpr (kLoads > 1) tma_load_3d(box + kBoxBytes, &tm_in1, &landed[j & 1], x, y, b);
+            }
+        };
+        int acc = 0, pending = 0;   // pending: slots (bits) whose loads have not been waited for
+        uint32_t acc_phase = 0, in_phase = 0;
+        if (kLoads > 0 && pair_id < num_tiles) {
+            if (lane == 0) {
+                load_chunk(pair_id, 0);
+                load_chunk(pair_id, 1);
+            }
+            pending = 3;
+        }
+        bool alive = true;
+        for (int t = pair_id; t < num_tiles && alive; t += num_pairs) {
             int b, m0, n0;
             locate(t, b, m0, n0);
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull_bar[acc], acc_phase, ctl, DG_DEV_TIMEOUT))) break;
             tc_fence_after_sync();
-            const int row = m0 + rank * 128 + static_cast<int>(quad) * 32 + static_cast<int>(lane);
-            const int col0 = n0 + static_cast<int>(half) * 128;
+            const int row0 = m0 + row_off, row = row0 + static_cast<int>(lane);
+            const bool mirror = SYM && m0 != n0;
+            // the row's entry of A's or B's diagonal
+            float diag = 0.f;
+            if (MODE != kNsGram && row < rows) diag = __ldcg((MODE == kNsPoly ? p.da : p.db) + static_cast<int64_t>(b) * p.lo + row);
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 16) {
-                uint32_t v[16];
-                tmem_ld_32x32b_x16(tmem_base + ((quad * 32) << 16) + acc * kTile + half * 128 + c, v);
-                tmem_ld_wait();
-                reg_fence16(v);
-                const int col = col0 + c;
-                if (row >= rows || col >= cols) continue;
-                float f[16];
-                if constexpr (MODE == kNsGram) {
-                    // 2^24 X X^T -> 2^12 A
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]) * (1.0f / kScale);
-                } else if constexpr (MODE == kNsPoly) {
-                    uint32_t a[8];
-                    load16(p.a + (static_cast<int64_t>(b) * p.lo + row) * p.lda + col, a);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 x = half2_values(a[i]);
-                        f[2 * i] = fmaf(p.cb, x.x, p.cc * (1.0f / kScale) * __uint_as_float(v[2 * i]));
-                        f[2 * i + 1] = fmaf(p.cb, x.y, p.cc * (1.0f / kScale) * __uint_as_float(v[2 * i + 1]));
+            for (int j = 0; j < 4; ++j) {
+                const int s = j & 1, col = n0 + col_off + 32 * j;
+                uint8_t *box0 = slots + s * kSlotBytes, *box1 = box0 + kBoxBytes;
+                uint32_t v[2][16];
+                const uint32_t at = tmem_base + ((quad * 32) << 16) + acc * kTile + half * 128 + 32 * j;
+                tmem_ld_32x32b_x16(at, v[0]);
+                tmem_ld_32x32b_x16(at + 16, v[1]);
+                if constexpr (kLoads > 0) {
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&landed[s], (in_phase >> s) & 1u, ctl, DG_DEV_TIMEOUT))) {
+                        alive = false;
+                        break;
                     }
-                } else {
-                    const int64_t at = (static_cast<int64_t>(b) * p.lo + row) * p.ldx + col;
-                    uint32_t xh[8], xl[8];
-                    load16(p.xh[0] + at, xh);
-                    load16(p.xl + at, xl);
+                    in_phase ^= 1u << s;
+                    pending &= ~(1 << s);
+                }
+                tmem_ld_wait();
+                reg_fence16(v[0]);
+                reg_fence16(v[1]);
+                if (j == 3) {   // the accumulator has been read
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(leader_tempty + acc * 8);
+                }
+                const bool in = row0 < rows && col < cols;   // (else nothing of the chunk is stored)
+                if constexpr (kLoads == 0) {
+                    // the slot's stores have read it (the other slot's may still run)
+                    if (lane == 0) bulk_wait_group_read<1>();
+                    __syncwarp();
+                }
+                // 8 columns at a time, in place: f in units of 2^-12
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 h = half2_values(xh[i]), l = half2_values(xl[i]);
-                        f[2 * i] = fmaf(p.ca, h.x + l.x, (1.0f / kScale) * __uint_as_float(v[2 * i]));
-                        f[2 * i + 1] = fmaf(p.ca, h.y + l.y, (1.0f / kScale) * __uint_as_float(v[2 * i + 1]));
+                for (int h = 0; h < 4; ++h) {
+                    const uint32_t *x = v[h >> 1] + 8 * (h & 1);
+                    float f[8];
+                    uint32_t w0[4], w1[4];
+                    if constexpr (kLoads > 0) {
+                        const uint4 q = *unit(box0, lane, h);
+                        w0[0] = q.x; w0[1] = q.y; w0[2] = q.z; w0[3] = q.w;
+                    }
+                    if constexpr (kLoads > 1) {
+                        const uint4 q = *unit(box1, lane, h);
+                        w1[0] = q.x; w1[1] = q.y; w1[2] = q.z; w1[3] = q.w;
+                    }
+                    if constexpr (MODE == kNsGram) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(x[i]) * (1.0f / kScale);
+                    } else if constexpr (MODE == kNsPoly) {
+                        float dc[8];
+                        const float *d = p.da + static_cast<int64_t>(b) * p.lo + col + 8 * h;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dc[i] = col + 8 * h + i < cols ? __ldcg(d + i) : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 r = half2_values(w0[i]);
+                            f[2 * i] = fmaf(fmaf(p.cc, diag + dc[2 * i], p.cb), r.x, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i]));
+                            f[2 * i + 1] = fmaf(fmaf(p.cc, diag + dc[2 * i + 1], p.cb), r.y, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 hi = half2_values(w0[i]), lo = half2_values(w1[i]);
+                            f[2 * i] = fmaf(p.ca + diag, hi.x + lo.x, (1.0f / kScale) * __uint_as_float(x[2 * i]));
+                            f[2 * i + 1] = fmaf(p.ca + diag, hi.y + lo.y, (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
+                        }
+                    }
+                    if constexpr (SYM) {
+                        // the diagonal goes out in FP32 (as it is, not scaled)
+                        const int on = row - (col + 8 * h);
+                        if (m0 == n0 && on >= 0 && on < 8) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (i == on) {
+                                    const float dv = f[i] * (1.0f / kScale);
+                                    if (row < rows)
+                                        (MODE == kNsGram ? p.da : p.db)[static_cast<int64_t>(b) * p.lo + row] =
+                                            MODE == kNsGram ? dv : fmaf(diag, fmaf(p.cc, diag, p.cb), dv);
+                                    f[i] = 0.f;
+                                }
+                        }
+                    }
+                    if constexpr (MODE == kNsLast) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] *= 1.0f / kScale;
+                        if (!p.out_tma) {
+                            // rows that TMA cannot address: element by element
+                            uint16_t *out = p.out + b * p.out_batch;
+                            const bool tall = p.rows > p.cols;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int c = col + 8 * h + i;
+                                if (row >= rows || c >= cols) continue;
+                                const __nv_bfloat16 o = __float2bfloat16_rn(f[i]);
+                                out[tall ? static_cast<int64_t>(c) * p.ldo + row : static_cast<int64_t>(row) * p.ldo + c] =
+                                    *reinterpret_cast<const uint16_t *>(&o);
+                            }
+                        } else if (p.rows > p.cols) {
+                            // (box1: every lane has read its own unit h of the low plane, the others not;
+                            // the transposed box is written once all have, below)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[h >> 1][8 * (h & 1) + i] = __float_as_uint(f[i]);
+                        } else {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                                o[i] = *reinterpret_cast<const uint32_t *>(&b2);
+                            }
+                            *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                    } else if constexpr (MODE == kNsUpdate) {
+                        uint32_t o[4], l[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) split2(f[2 * i], f[2 * i + 1], o[i], l[i]);
+                        *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *unit(box1, lane, h) = make_uint4(l[0], l[1], l[2], l[3]);
+                    } else {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = half2_bits(f[2 * i], f[2 * i + 1]);
+                        *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (mirror) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const uint16_t e = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+                                *reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(unit(box1, 8 * h + i, lane >> 3)) + 2 * (lane & 7)) = e;
+                            }
+                        }
                     }
                 }
                 if constexpr (MODE == kNsLast) {
-                    uint16_t *out = p.out + b * p.out_batch;
-                    const bool tall = p.rows > p.cols;
+                    if (p.out_tma && p.rows > p.cols) {
+                        __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (col + i >= cols) break;
-                        const __nv_bfloat16 o = __float2bfloat16_rn(f[i] * (1.0f / kScale));
-                        out[tall ? static_cast<int64_t>(col + i) * p.ldo + row : static_cast<int64_t>(row) * p.ldo + col + i] =
-                            *reinterpret_cast<const uint16_t *>(&o);
-                    }
-                } else {
-                    uint32_t o[8], l[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        o[i] = half2_bits(f[2 * i], f[2 * i + 1]);
-                        if constexpr (MODE == kNsUpdate) {
-                            const float2 h = half2_values(o[i]);
-                            l[i] = half2_bits(f[2 * i] - h.x, f[2 * i + 1] - h.y);
+                        for (int c = 0; c < 32; ++c) {
+                            const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(v[c >> 4][c & 15]));
+                            *reinterpret_cast<__nv_bfloat16 *>(reinterpret_cast<uint8_t *>(unit(box0, c, lane >> 3)) + 2 * (lane & 7)) = o;
                         }
                     }
-                    const int64_t ld = MODE == kNsUpdate ? p.ldx : p.lda;
-                    const int64_t at = (static_cast<int64_t>(b) * p.lo + row) * ld + col;
-                    uint16_t *dst = MODE == kNsGram ? p.a : MODE == kNsPoly ? p.b : p.xh[1];
-                    uint4 *d = reinterpret_cast<uint4 *>(dst + at);
-                    d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                    d[1] = make_uint4(o[4], o[5], o[6], o[7]);
-                    if constexpr (MODE == kNsUpdate) {
-                        d = reinterpret_cast<uint4 *>(p.xl + at);
-                        d[0] = make_uint4(l[0], l[1], l[2], l[3]);
-                        d[1] = make_uint4(l[4], l[5], l[6], l[7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (in && (MODE != kNsLast || p.out_tma)) {
+                        if (MODE == kNsLast && p.rows > p.cols) {
+                            tma_store_3d(&tm_out0, box0, row0, col, b);
+                        } else {
+                            tma_store_3d(&tm_out0, box0, col, row0, b);
+                            if (MODE == kNsUpdate) tma_store_3d(&tm_out1, box1, col, row0, b);
+                            if (mirror) tma_store_3d(&tm_out0, box1, row0, col, b);
+                        }
+                    }
+                    bulk_commit_group();
+                    if constexpr (kLoads > 0) {
+                        bulk_wait_group_read<0>();
+                        // two chunks on: of this tile, or of this pair's next
+                        load_chunk(j < 2 ? t : t + num_pairs, j < 2 ? j + 2 : j - 2);
                     }
                 }
+                if (kLoads > 0 && (j < 2 || t + num_pairs < num_tiles)) pending |= 1 << s;
+                __syncwarp();
             }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(leader_tempty + acc * 8);
             if (++acc == 2) { acc = 0; acc_phase ^= 1; }
         }
+        // (an aborted loop leaves no load landing in shared memory after the CTA is gone)
+        if (lane == 0) {
+            for (int s = 0; s < 2; ++s)
+                if (pending & (1 << s)) mbar_wait_drain(&landed[s], (in_phase >> s) & 1u, ctl);
+            bulk_wait_group<0>();
+        }
+        __syncwarp();
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -411,17 +620,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// 3-D map of planes [batch][rows][ld] of FP16: boxes of 64 elements (128 bytes) x box_rows.
-bool encode_plane(CUtensorMap *map, const uint16_t *base, int64_t cols, int64_t rows, int64_t ld, int64_t batch,
-                  uint32_t box_rows) {
+// 3-D map of planes [batch][rows][ld] of 16-bit values: boxes of 64 elements (128 bytes) x box_rows as
+// operands, of 32 x 32 elements for the epilogue.
+bool encode_plane(CUtensorMap *map, const uint16_t *base, int64_t cols, int64_t rows, int64_t ld, int64_t batch_stride,
+                  int64_t batch, uint32_t box_rows) {
     TensorMapEncodeFn fn = host_encode();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld * rows) * 2};
-    const cuuint32_t box[3] = {kKBlock, box_rows, 1};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(batch_stride) * 2};
+    const bool epi = box_rows == 32;
+    const cuuint32_t box[3] = {epi ? 32u : kKBlock, box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<uint16_t *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, epi ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              epi ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -452,11 +664,13 @@ int max_pairs(int num_sms) {
 }
 
 template <int MODE>
-cudaError_t launch_product(const NsParams &p, const CUtensorMap &a, const CUtensorMap &b, int k, int num_sms,
+cudaError_t launch_product(const NsParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &in0,
+                           const CUtensorMap &in1, const CUtensorMap &out0, const CUtensorMap &out1, int k, int num_sms,
                            cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(dg_ns_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = up(p.lo, kTile) / kTile * (up(MODE >= kNsUpdate ? p.hi : p.lo, kTile) / kTile) * p.batch;
+    const int64_t tm = up(p.lo, kTile) / kTile, tn = up(p.hi, kTile) / kTile;
+    const int64_t tiles = (MODE >= kNsUpdate ? tm * tn : tm * (tm + 1) / 2) * p.batch;
     const int pairs = max_pairs<MODE>(num_sms);
     if (pairs <= 0) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
@@ -469,7 +683,7 @@ cudaError_t launch_product(const NsParams &p, const CUtensorMap &a, const CUtens
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dg_ns_gemm_kernel<MODE>, a, b, p, k);
+    return cudaLaunchKernelEx(&cfg, dg_ns_gemm_kernel<MODE>, a, b, in0, in1, out0, out1, p, k);
 }
 
 cudaError_t launch_simple(void (*kernel)(NsParams), dim3 grid, const NsParams &p, cudaStream_t stream) {
@@ -489,11 +703,11 @@ constexpr int kMaxPartial = 304;
 
 }  // namespace
 
-// Two high planes, the low plane, A and B, and the norm's partial sums; rows of whole 64-element
+// Two high planes, the low plane, A and B, their diagonals, the norm's partial sums; rows of whole 64-element
 // (128-byte) lines.
 int64_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
     const int64_t lo = rows < cols ? rows : cols, hi = rows < cols ? cols : rows;
-    return batch * (2 * lo * (3 * up(hi, 64) + 2 * up(lo, 64)) + 8 * kMaxPartial);
+    return batch * (2 * lo * (3 * up(hi, 64) + 2 * up(lo, 64)) + 8 * kMaxPartial + 8 * up(lo, 4));
 }
 
 cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, cudaStream_t stream, int *launches) {
@@ -509,32 +723,51 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
     p.xl = take(plane);
     p.a = take(square);
     p.b = take(square);
-    p.partial = reinterpret_cast<double *>(w);
+    p.partial = reinterpret_cast<double *>(take(8ll * kMaxPartial * p.batch));
+    p.da = reinterpret_cast<float *>(take(4 * up(p.lo, 4) * p.batch));
+    p.db = reinterpret_cast<float *>(w);
     p.dense = p.ldg == p.cols;
     const int64_t segs = p.dense ? (static_cast<int64_t>(p.rows) * p.cols + 8191) / 8192 : p.rows * ((p.cols + 8191ll) / 8192);
     p.num_partial = static_cast<int>(segs < kMaxPartial ? segs : kMaxPartial);   // (by the matrix alone, as its sum's order)
     cudaError_t e = launch_simple(bf16 ? dg_ns_norm_kernel<true> : dg_ns_norm_kernel<false>, dim3(p.num_partial, p.batch), p, stream);
     if (e != cudaSuccess) return e;
-    e = launch_simple(bf16 ? dg_ns_split_kernel<true> : dg_ns_split_kernel<false>,
-                      dim3((p.cols + 63) / 64, (p.rows + 63) / 64, p.batch), p, stream);
+    const bool tall = p.rows > p.cols;
+    if (tall)
+        e = launch_simple(bf16 ? dg_ns_split_kernel<true, true> : dg_ns_split_kernel<false, true>,
+                          dim3((p.cols + 63) / 64, (p.rows + 63) / 64, p.batch), p, stream);
+    else
+        e = launch_simple(bf16 ? dg_ns_split_kernel<true, false> : dg_ns_split_kernel<false, false>,
+                          dim3((p.cols + 2047) / 2048, (p.rows + 7) / 8, p.batch), p, stream);
     *launches = 2 + 3 * steps;
-    CUtensorMap ma, mb, mx[2], mxn[2];
+    // operands: X along K (Gram), X as [K][N], A and B; epilogue boxes of the planes, A, B and the output
+    CUtensorMap xk[2], xn[2], a, b, xh[2], xl, ea, eb, eo;
+    const int64_t px = p.lo * p.ldx, pa = p.lo * p.lda;
+    bool ok = true;
     for (int i = 0; i < 2; ++i)
-        if (!encode_plane(&mx[i], p.xh[i], p.hi, p.lo, p.ldx, p.batch, 128) ||
-            !encode_plane(&mxn[i], p.xh[i], p.hi, p.lo, p.ldx, p.batch, kKBlock))
-            return cudaErrorInvalidValue;
-    if (!encode_plane(&ma, p.a, p.lo, p.lo, p.lda, p.batch, 128) || !encode_plane(&mb, p.b, p.lo, p.lo, p.lda, p.batch, 128))
-        return cudaErrorInvalidValue;
+        ok &= encode_plane(&xk[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, 128) &&
+              encode_plane(&xn[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, kKBlock) &&
+              encode_plane(&xh[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, 32);
+    ok &= encode_plane(&xl, p.xl, p.hi, p.lo, p.ldx, px, p.batch, 32) &&
+          encode_plane(&a, p.a, p.lo, p.lo, p.lda, pa, p.batch, 128) &&
+          encode_plane(&b, p.b, p.lo, p.lo, p.lda, pa, p.batch, 128) &&
+          encode_plane(&ea, p.a, p.lo, p.lo, p.lda, pa, p.batch, 32) &&
+          encode_plane(&eb, p.b, p.lo, p.lo, p.lda, pa, p.batch, 32);
+    if (!ok) return cudaErrorInvalidValue;
+    // the output by TMA where its rows (and matrices) start on 16 bytes
+    p.out_tma = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && p.ldo % 8 == 0 && (p.batch == 1 || p.out_batch % 8 == 0) &&
+                encode_plane(&eo, p.out, p.cols, p.rows, p.ldo, p.batch == 1 ? p.ldo * p.rows : p.out_batch, p.batch, 32);
+    if (!p.out_tma) eo = ea;   // not used
     int cur = 0;
     uint16_t *planes[2] = {p.xh[0], p.xh[1]};
     for (int s = 0; s < steps && e == cudaSuccess; ++s) {
         p.xh[0] = planes[cur];
         p.xh[1] = planes[cur ^ 1];
-        e = launch_product<kNsGram>(p, mx[cur], mx[cur], p.hi, num_sms, stream);
-        if (e == cudaSuccess) e = launch_product<kNsPoly>(p, ma, ma, p.lo, num_sms, stream);
+        e = launch_product<kNsGram>(p, xk[cur], xk[cur], ea, ea, ea, ea, p.hi, num_sms, stream);
+        if (e == cudaSuccess) e = launch_product<kNsPoly>(p, a, a, ea, ea, eb, eb, p.lo, num_sms, stream);
         if (e == cudaSuccess)
-            e = s + 1 < steps ? launch_product<kNsUpdate>(p, mb, mxn[cur], p.lo, num_sms, stream)
-                              : launch_product<kNsLast>(p, mb, mxn[cur], p.lo, num_sms, stream);
+            e = s + 1 < steps
+                    ? launch_product<kNsUpdate>(p, b, xn[cur], xh[cur], xl, xh[cur ^ 1], xl, p.lo, num_sms, stream)
+                    : launch_product<kNsLast>(p, b, xn[cur], xh[cur], xl, eo, eo, p.lo, num_sms, stream);
         p.debug_flags = 0;
         cur ^= 1;
     }

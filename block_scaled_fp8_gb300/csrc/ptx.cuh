@@ -313,6 +313,15 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void 
         : "memory");
 }
 
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *smem_src, int32_t x, int32_t y,
+                                             int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(x), "r"(y), "r"(z), "r"(smem_u32(smem_src))
+        : "memory");
+}
+
 // TMA reduce: the box in shared memory is added element-wise to the tensor in
 // global memory (the addition is done at L2, in the tensor map's type; FP32
 // adds round to nearest even).
