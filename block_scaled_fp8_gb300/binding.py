@@ -482,7 +482,10 @@ def _load_marshal():
             loader.exec_module(m)
             fns = ("dg_bf16_fp4_gemv_nt", "dg_bf16_fp8_gemv_nt", "dg_bf16_fp4_gemv_nt_f32", "dg_bf16_fp8_gemv_nt_f32",
                    "dg_moe_route", "dg_moe_fp4_layer", "dg_moe_fp8_layer", "dg_bf16_gemv_workspace_bytes",
-                   "dg_moe_layer_workspace_bytes")
+                   "dg_moe_layer_workspace_bytes", "dg_fp8_gated_gemm_nt", "dg_m_grouped_fp8_gated_gemm_nt_contiguous",
+                   "dg_fp8_gated_gemm_nn_backward", "dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous", "dg_quantize_fp8",
+                   "dg_quantize_fp8_blocks", "dg_newton_schulz", "dg_newton_schulz_workspace_bytes",
+                   "dg_k_grouped_packed_sf_rows")
             m.setup(tuple(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in fns),
                     (torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.uint8, torch.int32),
                     torch._C._cuda_getCurrentRawStream,
@@ -608,70 +611,8 @@ def dg_moe_fp8_layer(x, ids, weights, w1, sf1, w2, sf2, y, c=None, workspace=Non
 
 # --------------------------------------------------------------------- feed-forward training: gated block, quantiser, update
 #
-# A wrong dtype, shape, layout or device raises AssertionError, what the library refuses DGError.
-
-_E4M3 = torch.float8_e4m3fn
-_BF16 = torch.bfloat16
-
-
-def _here(*tensors):
-    """All of them (None aside) are on the current CUDA device."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
-    for t in tensors:
-        assert t is None or t.get_device() == dev, "tensors have to be on the current CUDA device"
-
-
-def _matrix(t, dtype, shape):
-    """t is a matrix of this dtype and shape with unit column stride; its row stride."""
-    assert t.dtype == dtype and t.shape == shape and (t.stride(-1) == 1 or t.shape[-1] <= 1), \
-        f"expected {dtype} {tuple(shape)} with unit column stride, got {t.dtype} {tuple(t.shape)} {t.stride()}"
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
-
-
-def _words(t, *shape):
-    """t holds packed scale words of this shape, dense."""
-    assert t.dtype == torch.int32 and tuple(t.shape) == shape and t.is_contiguous(), \
-        f"expected dense int32 {shape}, got {t.dtype} {tuple(t.shape)}"
-    return t
-
-
-def _align4(n):
-    return (n + 3) // 4 * 4
-
-
-def _status_word(status):
-    assert status is None or (status.dtype == torch.int32 and status.numel() >= 1)
-
-
-def _gated_forward(fn, a, sfa, b, sfb, layout, h, hq, sfh, gu, status, stream):
-    M, K = a.shape
-    grouped = layout is not None
-    I = b.shape[-2] // 2
-    E = b.shape[0] if grouped else 1
-    lda = _matrix(a, _E4M3, (M, K))
-    ldb = _matrix(b, _E4M3, (E, 2 * I, K) if grouped else (2 * I, K))
-    assert not grouped or E == 1 or b.stride(0) == 2 * I * ldb, "experts have to follow one another"
-    slices = (K + 511) // 512
-    _words(sfa, slices, _align4(M))
-    _words(sfb, *((E,) if grouped else ()), slices, _align4(2 * I))
-    assert (h is None) != (hq is None), "exactly one of h and hq"
-    ldgu = 0 if gu is None else _matrix(gu, _BF16, (M, 2 * I))
-    ldh = 0 if h is None else _matrix(h, _BF16, (M, I))
-    ldhq = 0
-    if hq is not None:
-        ldhq = _matrix(hq, _E4M3, (M, I))
-        _words(sfh, (I + 511) // 512, _align4(M))
-    _status_word(status)
-    _here(a, sfa, b, sfb, layout, h, hq, sfh, gu, status)
-    more = ()
-    if grouped:
-        assert layout.dtype == torch.int32 and layout.shape == (M,) and layout.is_contiguous()
-        more = (_p(layout),)
-    _check(fn, getattr(lib(), fn)(
-        _p(a), lda, _p(sfa), _p(b), ldb, _p(sfb), _p(gu), ldgu, _p(h), ldh, _p(hq), ldhq,
-        _p(sfh if hq is not None else None), *more, M, I, K, *((E,) if grouped else ()), _p(status), _stream(stream)))
-    return h if hq is None else hq
-
+# Marshalled in C as the decode calls are: a wrong dtype, shape, layout or device raises
+# AssertionError, what the library refuses DGError.
 
 def dg_fp8_gated_gemm_nt(a, sfa, b, sfb, h=None, hq=None, sfh=None, gu=None, status=None, stream=None):
     """silu(A Wg^T) * (A Wu^T) with Wg, Wu the first and second half of b's rows.  a
@@ -680,7 +621,10 @@ def dg_fp8_gated_gemm_nt(a, sfa, b, sfb, h=None, hq=None, sfh=None, gu=None, sta
     quantised, to hq float8_e4m3fn [M, I] with sfh packed int32 [ceil(I/512), align4(M)]
     (the down product's A).  gu bf16 [M, 2I], if given, gets gate and up for the
     backward pass.  Returns h or hq."""
-    return _gated_forward("dg_fp8_gated_gemm_nt", a, sfa, b, sfb, None, h, hq, sfh, gu, status, stream)
+    st = (_marshal or _load_marshal()).gated(a, sfa, b, sfb, None, h, hq, sfh, gu, status, stream)
+    if st:
+        _fail("dg_fp8_gated_gemm_nt", st)
+    return h if hq is None else hq
 
 
 def dg_m_grouped_fp8_gated_gemm_nt_contiguous(a, sfa, b, sfb, grouped_layout, h=None, hq=None, sfh=None, gu=None,
@@ -688,32 +632,10 @@ def dg_m_grouped_fp8_gated_gemm_nt_contiguous(a, sfa, b, sfb, grouped_layout, h=
     """As dg_fp8_gated_gemm_nt with an expert for each 128 rows: b [E, 2I, K], sfb
     [E, ceil(K/512), align4(2I)], grouped_layout int32 [M] (-1: not computed)."""
     assert grouped_layout is not None
-    return _gated_forward("dg_m_grouped_fp8_gated_gemm_nt_contiguous", a, sfa, b, sfb, grouped_layout, h, hq, sfh, gu,
-                          status, stream)
-
-
-def _gated_backward(fn, dy, sfdy, w2, sfw2, layout, gu, dgu, h, status, stream):
-    M, K = dy.shape
-    grouped = layout is not None
-    E, I = (w2.shape[0] if grouped else 1), w2.shape[-1]
-    lddy = _matrix(dy, _E4M3, (M, K))
-    ldw2 = _matrix(w2, _E4M3, (E, K, I) if grouped else (K, I))
-    assert not grouped or E == 1 or w2.stride(0) == K * ldw2, "experts have to follow one another"
-    slices = (K + 511) // 512
-    _words(sfdy, slices, _align4(M))
-    _words(sfw2, *((E,) if grouped else ()), slices, _align4(I))
-    ldgu, lddgu = _matrix(gu, _BF16, (M, 2 * I)), _matrix(dgu, _BF16, (M, 2 * I))
-    ldh = 0 if h is None else _matrix(h, _BF16, (M, I))
-    _status_word(status)
-    _here(dy, sfdy, w2, sfw2, layout, gu, dgu, h, status)
-    more = ()
-    if grouped:
-        assert layout.dtype == torch.int32 and layout.shape == (M,) and layout.is_contiguous()
-        more = (_p(layout),)
-    _check(fn, getattr(lib(), fn)(
-        _p(dy), lddy, _p(sfdy), _p(w2), ldw2, _p(sfw2), _p(gu), ldgu, _p(dgu), lddgu, _p(h), ldh, *more, M, I, K,
-        *((E,) if grouped else ()), _p(status), _stream(stream)))
-    return dgu
+    st = (_marshal or _load_marshal()).gated(a, sfa, b, sfb, grouped_layout, h, hq, sfh, gu, status, stream)
+    if st:
+        _fail("dg_m_grouped_fp8_gated_gemm_nt_contiguous", st)
+    return h if hq is None else hq
 
 
 def dg_fp8_gated_gemm_nn_backward(dy, sfdy, w2, sfw2, gu, dgu, h=None, status=None, stream=None):
@@ -721,7 +643,10 @@ def dg_fp8_gated_gemm_nn_backward(dy, sfdy, w2, sfw2, gu, dgu, h=None, status=No
     dy float8_e4m3fn [M, K], sfdy packed int32 [ceil(K/512), align4(M)]; w2 float8_e4m3fn
     [K, I] (I contiguous), sfw2 [ceil(K/512), align4(I)]; gu and dgu bf16 [M, 2I] (may be one
     buffer); h bf16 [M, I], if given, gets silu(gate) * up again.  Returns dgu."""
-    return _gated_backward("dg_fp8_gated_gemm_nn_backward", dy, sfdy, w2, sfw2, None, gu, dgu, h, status, stream)
+    st = (_marshal or _load_marshal()).gated_backward(dy, sfdy, w2, sfw2, None, gu, dgu, h, status, stream)
+    if st:
+        _fail("dg_fp8_gated_gemm_nn_backward", st)
+    return dgu
 
 
 def dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(dy, sfdy, w2, sfw2, grouped_layout, gu, dgu, h=None,
@@ -729,14 +654,10 @@ def dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(dy, sfdy, w2, sfw2, group
     """As dg_fp8_gated_gemm_nn_backward with an expert for each 128 rows: w2 [E, K, I], sfw2
     [E, ceil(K/512), align4(I)], grouped_layout int32 [M] (-1: not computed)."""
     assert grouped_layout is not None
-    return _gated_backward("dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous", dy, sfdy, w2, sfw2, grouped_layout,
-                           gu, dgu, h, status, stream)
-
-
-def _values(x):
-    """x's dg_values_format."""
-    assert x.dtype == torch.float32 or x.dtype == _BF16, f"expected float32 or bfloat16 values, got {x.dtype}"
-    return DG_VALUES_F32 if x.dtype == torch.float32 else DG_VALUES_BF16
+    st = (_marshal or _load_marshal()).gated_backward(dy, sfdy, w2, sfw2, grouped_layout, gu, dgu, h, status, stream)
+    if st:
+        _fail("dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous", st)
+    return dgu
 
 
 def dg_quantize_fp8(x, q=None, sf=None, qk=None, sfk=None, ks=None, stream=None):
@@ -745,23 +666,9 @@ def dg_quantize_fp8(x, q=None, sf=None, qk=None, sfk=None, ks=None, stream=None)
     for each 128x1 (either pair may be left out).  sfk is int32 [ceil(R/512), align4(C)], or with
     group sizes ks (host list, multiples of 128, in sum R) [k_grouped_packed_sf_rows(ks), C], as
     the K-grouped call takes it.  Returns (q, sf, qk, sfk)."""
-    R, C = x.shape
-    ldx = _matrix(x, x.dtype, (R, C))
-    assert q is not None or qk is not None, "q or qk"
-    ldq = ldqk = 0
-    if q is not None:
-        ldq = _matrix(q, _E4M3, (R, C))
-        _words(sf, (C + 511) // 512, _align4(R))
-    if qk is not None:
-        ldqk = _matrix(qk, _E4M3, (R, C))
-        if ks is None:
-            _words(sfk, (R + 511) // 512, _align4(C))
-        else:
-            _words(sfk, max(0, k_grouped_packed_sf_rows(ks)), C)
-    _here(x, q, qk, sf if q is not None else None, sfk if qk is not None else None)
-    _check("dg_quantize_fp8", lib().dg_quantize_fp8(
-        _p(x), _values(x), ldx, _p(q), ldq, _p(sf), _p(qk), ldqk, _p(sfk), R, C, None if ks is None else _ks_host(ks),
-        0 if ks is None else len(ks), _stream(stream)))
+    st = (_marshal or _load_marshal()).quantize(x, q, sf, qk, sfk, ks, stream)
+    if st:
+        _fail("dg_quantize_fp8", st)
     return q, sf, qk, sfk
 
 
@@ -769,19 +676,9 @@ def dg_quantize_fp8_blocks(x, q, sf=None, sft=None, stream=None):
     """E4M3 codes q and packed scales of x [R, C] or [B, R, C] (float32 or bfloat16) with a scale for
     each 128x128: sf int32 [B, ceil(C/512), align4(R)] for x as B of the NT calls, sft
     [B, ceil(R/512), align4(C)] for x as B of the NN calls (one may be left out).  Returns (q, sf, sft)."""
-    R, C = x.shape[-2:]
-    B = x.shape[0] if x.dim() == 3 else 1
-    lead = (B,) if x.dim() == 3 else ()
-    ldx, ldq = _matrix(x, x.dtype, (*lead, R, C)), _matrix(q, _E4M3, (*lead, R, C))
-    assert sf is not None or sft is not None, "sf or sft"
-    if sf is not None:
-        _words(sf, *lead, (C + 511) // 512, _align4(R))
-    if sft is not None:
-        _words(sft, *lead, (R + 511) // 512, _align4(C))
-    _here(x, q, sf, sft)
-    _check("dg_quantize_fp8_blocks", lib().dg_quantize_fp8_blocks(
-        _p(x), _values(x), ldx, x.stride(0) if lead else 0, _p(q), ldq, q.stride(0) if lead else 0, _p(sf), _p(sft), B,
-        R, C, _stream(stream)))
+    st = (_marshal or _load_marshal()).quantize_blocks(x, q, sf, sft, stream)
+    if st:
+        _fail("dg_quantize_fp8_blocks", st)
     return q, sf, sft
 
 
@@ -794,22 +691,9 @@ def dg_newton_schulz(g, out, steps: int = 5, coef=(3.4445, -4.7750, 2.0315), eps
     """Orthogonalises g [R, C] or [B, R, C] (float32 or bfloat16) into out (bfloat16, same shape): X = g /
     (|g| + eps), then `steps` times X <- a X + (b A + c A A) X with A = X X^T and (a, b, c) = coef
     (X^T X on the right where R > C).  workspace: a device buffer of
-    newton_schulz_workspace_bytes(B, R, C) bytes (made here if not given)."""
-    R, C = g.shape[-2:]
-    B = g.shape[0] if g.dim() == 3 else 1
-    lead = (B,) if g.dim() == 3 else ()
-    ldg, ldo = _matrix(g, g.dtype, (*lead, R, C)), _matrix(out, _BF16, (*lead, R, C))
+    newton_schulz_workspace_bytes(B, R, C) bytes (made here if not given).  Returns out."""
     a, b, c = coef
-    _status_word(status)
-    _here(g, out, workspace, status)
-    if workspace is None:
-        need = newton_schulz_workspace_bytes(B, R, C)
-        if need > 0 and steps >= 1:   # (what is refused makes no workspace)
-            workspace = _workspace(need, g, stream)
-    else:
-        assert workspace.is_contiguous()
-    _check("dg_newton_schulz", lib().dg_newton_schulz(
-        _p(g), _values(g), ldg, g.stride(0) if lead else 0, _p(out), ldo, out.stride(0) if lead else 0, B, R, C,
-        steps, a, b, c, eps, _p(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _p(status), _stream(stream)))
+    st = (_marshal or _load_marshal()).newton_schulz(g, out, steps, a, b, c, eps, workspace, status, stream)
+    if st:
+        _fail("dg_newton_schulz", st)
     return out

@@ -1,5 +1,6 @@
-/* Marshalling of the decode calls (few-row products, routing, the MoE layer) from torch tensors
- * to the C ABI, for binding.py.  Such a call takes a few microseconds on the device, and its
+/* Marshalling of the decode calls (few-row products, routing, the MoE layer) and of the feed-forward
+ * training calls (gated block, quantiser, Newton-Schulz) from torch tensors to the C ABI, for
+ * binding.py.  Such a call takes a few microseconds on the device, and its
  * arguments cost as much through ctypes and Python attribute lookups (1 x 256 routing: 6.1 us a
  * call, of which the launch is 1.9).  Only Python's C API is used: tensors are asked through
  * their own methods.  A failed check raises AssertionError; the calls return the dg_status. */
@@ -18,8 +19,27 @@ typedef dg_status (*LayerFn)(const void *, int64_t, const int32_t *, const float
                              int, void *, int64_t, int32_t *, void *);
 typedef int64_t (*GemvBytesFn)(int, int, int);
 typedef int64_t (*LayerBytesFn)(int, int, int, int, int);
+typedef dg_status (*GatedFn)(const void *, int64_t, const void *, const void *, int64_t, const void *, void *, int64_t,
+                             void *, int64_t, void *, int64_t, void *, int, int, int, int32_t *, void *);
+typedef dg_status (*GatedGroupedFn)(const void *, int64_t, const void *, const void *, int64_t, const void *, void *,
+                                    int64_t, void *, int64_t, void *, int64_t, void *, const int32_t *, int, int, int,
+                                    int, int32_t *, void *);
+typedef dg_status (*BackwardFn)(const void *, int64_t, const void *, const void *, int64_t, const void *, const void *,
+                                int64_t, void *, int64_t, void *, int64_t, int, int, int, int32_t *, void *);
+typedef dg_status (*BackwardGroupedFn)(const void *, int64_t, const void *, const void *, int64_t, const void *,
+                                       const void *, int64_t, void *, int64_t, void *, int64_t, const int32_t *, int,
+                                       int, int, int, int32_t *, void *);
+typedef dg_status (*QuantizeFn)(const void *, int, int64_t, void *, int64_t, void *, void *, int64_t, void *, int, int,
+                                const int *, int, void *);
+typedef dg_status (*BlocksFn)(const void *, int, int64_t, int64_t, void *, int64_t, int64_t, void *, void *, int, int,
+                              int, void *);
+typedef dg_status (*SchulzFn)(const void *, int, int64_t, int64_t, void *, int64_t, int64_t, int, int, int, int, float,
+                              float, float, float, void *, int64_t, int32_t *, void *);
+typedef int64_t (*SchulzBytesFn)(int, int, int);
+typedef int64_t (*PackedRowsFn)(const int *, int);
 
-enum { GEMV_FP4, GEMV_FP8, GEMV_FP4_F32, GEMV_FP8_F32, ROUTE, LAYER_FP4, LAYER_FP8, GEMV_BYTES, LAYER_BYTES, FNS };
+enum { GEMV_FP4, GEMV_FP8, GEMV_FP4_F32, GEMV_FP8_F32, ROUTE, LAYER_FP4, LAYER_FP8, GEMV_BYTES, LAYER_BYTES,
+       GATED, GATED_GROUPED, BACKWARD, BACKWARD_GROUPED, QUANTIZE, BLOCKS, SCHULZ, SCHULZ_BYTES, PACKED_ROWS, FNS };
 enum { BF16, F32, FP8, U8, I32, DTYPES };
 
 static void *fns[FNS];
@@ -293,6 +313,224 @@ fail:
     return NULL;
 }
 
+/* A matrix, or (lead >= 0) `lead` of them, of this dtype and these sizes, with unit column stride: its
+ * pointer and row stride in elements (of a single row: its length in whole 16s), the stride
+ * from one matrix to the next. */
+typedef struct {
+    void *p;
+    int64_t ld, batch;
+} Matrix;
+
+static int matrix_of(PyObject *t, PyObject *dtype, int64_t lead, int64_t rows, int64_t cols, Matrix *out) {
+    Tensor x;
+    const int d = lead >= 0 ? 1 : 0;
+    out->p = NULL;
+    out->ld = out->batch = 0;
+    if (!is_dtype(t, dtype) || !strided(t, 2 + d, &x)) return 0;
+    if ((d && x.n[0] != lead) || x.n[d] != rows || x.n[d + 1] != cols || (x.stride[d + 1] != 1 && cols > 1)) return 0;
+    out->p = x.p;
+    out->ld = rows > 1 ? x.stride[d] : (cols + 15) / 16 * 16;
+    out->batch = d && lead > 1 ? x.stride[0] : 0;
+    return 1;
+}
+
+/* Not given, or a matrix. */
+static int matrix_or_none(PyObject *t, PyObject *dtype, int64_t lead, int64_t rows, int64_t cols, Matrix *out) {
+    out->p = NULL;
+    out->ld = out->batch = 0;
+    return t == Py_None || matrix_of(t, dtype, lead, rows, cols, out);
+}
+
+/* Dense int32 words, this many. */
+static int words_of(PyObject *t, int64_t count, void **out) {
+    return is_dtype(t, dtypes[I32]) && is_contiguous(t) && bytes_of(t) == 4 * count && pointer_of(t, out);
+}
+
+static int64_t slices_of(int64_t k) { return (k + 511) / 512; }
+static int64_t align4_of(int64_t n) { return (n + 3) / 4 * 4; }
+
+/* The last dimensions of a 2-D or 3-D tensor; lead is -1 where it is 2-D. */
+static int sizes_of(PyObject *t, int64_t *lead, int64_t *rows, int64_t *cols) {
+    PyObject *shape = PyObject_GetAttr(t, s_shape);
+    int64_t n[3];
+    int d;
+    if (!shape || !PyTuple_Check(shape)) {
+        Py_XDECREF(shape);
+        return 0;
+    }
+    d = PyTuple_GET_SIZE(shape) == 3;
+    if (!dims_of(shape, 2 + d, n)) return 0;
+    *lead = d ? n[0] : -1;
+    *rows = n[d];
+    *cols = n[d + 1];
+    return *lead <= INT32_MAX && *rows <= INT32_MAX && *cols <= INT32_MAX;
+}
+
+/* gated(a, sfa, b, sfb, layout or None, h, hq, sfh, gu, status, stream) */
+static PyObject *gated(PyObject *self, PyObject *const *arg, Py_ssize_t nargs) {
+    Matrix a, b, h, hq, gu;
+    void *sfa, *sfb, *sfh = NULL, *layout = NULL, *status, *stream;
+    int64_t m, k, i, e, none;
+    int grouped;
+    dg_status st;
+    CHECK(nargs == 11);
+    grouped = arg[4] != Py_None;
+    CHECK(sizes_of(arg[0], &none, &m, &k) && none < 0 && sizes_of(arg[2], &e, &i, &none) && (e >= 0) == grouped);
+    CHECK(i % 2 == 0);
+    i /= 2;
+    CHECK(matrix_of(arg[0], dtypes[FP8], -1, m, k, &a) && matrix_of(arg[2], dtypes[FP8], e, 2 * i, k, &b));
+    CHECK(e <= 1 || b.batch == 2 * i * b.ld);   /* experts follow one another */
+    CHECK(words_of(arg[1], slices_of(k) * align4_of(m), &sfa));
+    CHECK(words_of(arg[3], (grouped ? e : 1) * slices_of(k) * align4_of(2 * i), &sfb));
+    CHECK((arg[5] == Py_None) != (arg[6] == Py_None));   /* exactly one of h and hq */
+    CHECK(matrix_or_none(arg[5], dtypes[BF16], -1, m, i, &h) && matrix_or_none(arg[6], dtypes[FP8], -1, m, i, &hq));
+    CHECK(matrix_or_none(arg[8], dtypes[BF16], -1, m, 2 * i, &gu));
+    CHECK(arg[6] == Py_None || words_of(arg[7], slices_of(i) * align4_of(m), &sfh));
+    CHECK(!grouped || words_of(arg[4], m, &layout));
+    CHECK(status_of(arg[9], &status) && placed(arg, 7) && placed(arg + 8, 2));
+    CHECK((arg[6] == Py_None || placed(arg + 7, 1)) && stream_of(arg[10], arg[0], &stream));
+    Py_BEGIN_ALLOW_THREADS
+    st = grouped ? ((GatedGroupedFn)fns[GATED_GROUPED])(a.p, a.ld, sfa, b.p, b.ld, sfb, gu.p, gu.ld, h.p, h.ld, hq.p,
+                                                        hq.ld, sfh, (const int32_t *)layout, (int)m, (int)i, (int)k,
+                                                        (int)e, (int32_t *)status, stream)
+                 : ((GatedFn)fns[GATED])(a.p, a.ld, sfa, b.p, b.ld, sfb, gu.p, gu.ld, h.p, h.ld, hq.p, hq.ld, sfh,
+                                         (int)m, (int)i, (int)k, (int32_t *)status, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+fail:
+    return NULL;
+}
+
+/* gated_backward(dy, sfdy, w2, sfw2, layout or None, gu, dgu, h, status, stream) */
+static PyObject *gated_backward(PyObject *self, PyObject *const *arg, Py_ssize_t nargs) {
+    Matrix dy, w2, gu, dgu, h;
+    void *sfdy, *sfw2, *layout = NULL, *status, *stream;
+    int64_t m, k, i, e, rows, none;
+    int grouped;
+    dg_status st;
+    CHECK(nargs == 10);
+    grouped = arg[4] != Py_None;
+    CHECK(sizes_of(arg[0], &none, &m, &k) && none < 0 && sizes_of(arg[2], &e, &rows, &i) && (e >= 0) == grouped);
+    CHECK(rows == k && i <= INT32_MAX / 2);
+    CHECK(matrix_of(arg[0], dtypes[FP8], -1, m, k, &dy) && matrix_of(arg[2], dtypes[FP8], e, k, i, &w2));
+    CHECK(e <= 1 || w2.batch == k * w2.ld);   /* experts follow one another */
+    CHECK(words_of(arg[1], slices_of(k) * align4_of(m), &sfdy));
+    CHECK(words_of(arg[3], (grouped ? e : 1) * slices_of(k) * align4_of(i), &sfw2));
+    CHECK(matrix_of(arg[5], dtypes[BF16], -1, m, 2 * i, &gu) && matrix_of(arg[6], dtypes[BF16], -1, m, 2 * i, &dgu));
+    CHECK(matrix_or_none(arg[7], dtypes[BF16], -1, m, i, &h));
+    CHECK(!grouped || words_of(arg[4], m, &layout));
+    CHECK(status_of(arg[8], &status) && placed(arg, 9) && stream_of(arg[9], arg[0], &stream));
+    Py_BEGIN_ALLOW_THREADS
+    st = grouped ? ((BackwardGroupedFn)fns[BACKWARD_GROUPED])(dy.p, dy.ld, sfdy, w2.p, w2.ld, sfw2, gu.p, gu.ld, dgu.p,
+                                                              dgu.ld, h.p, h.ld, (const int32_t *)layout, (int)m, (int)i,
+                                                              (int)k, (int)e, (int32_t *)status, stream)
+                 : ((BackwardFn)fns[BACKWARD])(dy.p, dy.ld, sfdy, w2.p, w2.ld, sfw2, gu.p, gu.ld, dgu.p, dgu.ld, h.p,
+                                               h.ld, (int)m, (int)i, (int)k, (int32_t *)status, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+fail:
+    return NULL;
+}
+
+/* quantize(x, q, sf, qk, sfk, ks or None, stream) */
+static PyObject *quantize(PyObject *self, PyObject *const *arg, Py_ssize_t nargs) {
+    Matrix x, q, qk;
+    PyObject *list = NULL;
+    void *sf = NULL, *sfk = NULL, *stream;
+    int64_t r, c, none, packed;
+    int ks[256], groups = 0, f32, j;
+    dg_status st;
+    CHECK(nargs == 7);
+    f32 = is_dtype(arg[0], dtypes[F32]);
+    CHECK(sizes_of(arg[0], &none, &r, &c) && none < 0 && matrix_of(arg[0], dtypes[f32 ? F32 : BF16], -1, r, c, &x));
+    CHECK(arg[1] != Py_None || arg[3] != Py_None);   /* q or qk */
+    CHECK(matrix_or_none(arg[1], dtypes[FP8], -1, r, c, &q) && matrix_or_none(arg[3], dtypes[FP8], -1, r, c, &qk));
+    CHECK(arg[1] == Py_None || words_of(arg[2], slices_of(c) * align4_of(r), &sf));
+    packed = slices_of(r) * align4_of(c);
+    if (arg[5] != Py_None) {
+        list = PySequence_Fast(arg[5], "ks is a list of group sizes");
+        CHECK(list && PySequence_Fast_GET_SIZE(list) <= 255);
+        groups = (int)PySequence_Fast_GET_SIZE(list);
+        for (j = 0; j < groups; ++j) {
+            const int64_t k = PyLong_AsLongLong(PySequence_Fast_GET_ITEM(list, j));
+            CHECK(!(k == -1 && PyErr_Occurred()) && k >= 0 && k <= INT32_MAX && k % 128 == 0);
+            ks[j] = (int)k;
+        }
+        packed = ((PackedRowsFn)fns[PACKED_ROWS])(ks, groups) * c;
+        CHECK(packed >= 0);
+    }
+    CHECK(arg[3] == Py_None || words_of(arg[4], packed, &sfk));
+    CHECK(placed(arg, 2) && placed(arg + 3, 1) && (!sf || placed(arg + 2, 1)) && (!sfk || placed(arg + 4, 1)));
+    CHECK(stream_of(arg[6], arg[0], &stream));
+    Py_BEGIN_ALLOW_THREADS
+    st = ((QuantizeFn)fns[QUANTIZE])(x.p, f32 ? DG_VALUES_F32 : DG_VALUES_BF16, x.ld, q.p, q.ld, sf, qk.p, qk.ld, sfk,
+                                     (int)r, (int)c, list ? ks : NULL, groups, stream);
+    Py_END_ALLOW_THREADS
+    Py_XDECREF(list);
+    return PyLong_FromLong(st);
+fail:
+    Py_XDECREF(list);
+    return NULL;
+}
+
+/* quantize_blocks(x, q, sf, sft, stream) */
+static PyObject *quantize_blocks(PyObject *self, PyObject *const *arg, Py_ssize_t nargs) {
+    Matrix x, q;
+    void *sf = NULL, *sft = NULL, *stream;
+    int64_t lead, r, c, b;
+    int f32;
+    dg_status st;
+    CHECK(nargs == 5);
+    f32 = is_dtype(arg[0], dtypes[F32]);
+    CHECK(sizes_of(arg[0], &lead, &r, &c) && matrix_of(arg[0], dtypes[f32 ? F32 : BF16], lead, r, c, &x));
+    CHECK(matrix_of(arg[1], dtypes[FP8], lead, r, c, &q) && (arg[2] != Py_None || arg[3] != Py_None));   /* sf or sft */
+    b = lead < 0 ? 1 : lead;
+    CHECK(arg[2] == Py_None || words_of(arg[2], b * slices_of(c) * align4_of(r), &sf));
+    CHECK(arg[3] == Py_None || words_of(arg[3], b * slices_of(r) * align4_of(c), &sft));
+    CHECK(placed(arg, 4) && stream_of(arg[4], arg[0], &stream));
+    Py_BEGIN_ALLOW_THREADS
+    st = ((BlocksFn)fns[BLOCKS])(x.p, f32 ? DG_VALUES_F32 : DG_VALUES_BF16, x.ld, x.batch, q.p, q.ld, q.batch, sf, sft,
+                                 (int)b, (int)r, (int)c, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+fail:
+    return NULL;
+}
+
+/* newton_schulz(g, out, steps, a, b, c, eps, workspace, status, stream) */
+static PyObject *newton_schulz(PyObject *self, PyObject *const *arg, Py_ssize_t nargs) {
+    Matrix g, out;
+    PyObject *hold = NULL;
+    void *ws, *status, *stream;
+    int64_t lead, r, c, batch, steps, need, ws_bytes;
+    double coef[4];
+    int f32, j;
+    dg_status st;
+    CHECK(nargs == 10);
+    f32 = is_dtype(arg[0], dtypes[F32]);
+    CHECK(sizes_of(arg[0], &lead, &r, &c) && matrix_of(arg[0], dtypes[f32 ? F32 : BF16], lead, r, c, &g));
+    CHECK(matrix_of(arg[1], dtypes[BF16], lead, r, c, &out));
+    steps = PyLong_AsLongLong(arg[2]);
+    for (j = 0; j < 4; ++j) coef[j] = PyFloat_AsDouble(arg[3 + j]);
+    CHECK(!PyErr_Occurred() && steps >= INT32_MIN && steps <= INT32_MAX);
+    batch = lead < 0 ? 1 : lead;
+    CHECK(status_of(arg[8], &status));
+    need = ((SchulzBytesFn)fns[SCHULZ_BYTES])((int)batch, (int)r, (int)c);
+    if (steps < 1 || !(coef[3] >= 0)) need = -1;   /* (refused) */
+    PyObject *const on_device[] = {arg[0], arg[1], arg[8]};
+    CHECK(device_side(on_device, 3, arg[7], need, arg[0], arg[9], &hold, &ws, &ws_bytes, &stream));
+    Py_BEGIN_ALLOW_THREADS
+    st = ((SchulzFn)fns[SCHULZ])(g.p, f32 ? DG_VALUES_F32 : DG_VALUES_BF16, g.ld, g.batch, out.p, out.ld, out.batch,
+                                 (int)batch, (int)r, (int)c, (int)steps, (float)coef[0], (float)coef[1], (float)coef[2],
+                                 (float)coef[3], ws, ws_bytes, (int32_t *)status, stream);
+    Py_END_ALLOW_THREADS
+    Py_XDECREF(hold);
+    return PyLong_FromLong(st);
+fail:
+    Py_XDECREF(hold);
+    return NULL;
+}
+
 /* setup(addresses of the entry points, dtypes, raw stream of a device, current device, workspace maker) */
 static PyObject *setup(PyObject *self, PyObject *args) {
     PyObject *addresses, *types;
@@ -319,6 +557,11 @@ static PyMethodDef methods[] = {
     {"gemv", (PyCFunction)(void (*)(void))gemv, METH_FASTCALL, NULL},
     {"route", (PyCFunction)(void (*)(void))route, METH_FASTCALL, NULL},
     {"layer", (PyCFunction)(void (*)(void))layer, METH_FASTCALL, NULL},
+    {"gated", (PyCFunction)(void (*)(void))gated, METH_FASTCALL, NULL},
+    {"gated_backward", (PyCFunction)(void (*)(void))gated_backward, METH_FASTCALL, NULL},
+    {"quantize", (PyCFunction)(void (*)(void))quantize, METH_FASTCALL, NULL},
+    {"quantize_blocks", (PyCFunction)(void (*)(void))quantize_blocks, METH_FASTCALL, NULL},
+    {"newton_schulz", (PyCFunction)(void (*)(void))newton_schulz, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL},
 };
 

@@ -8,6 +8,8 @@
 // so a row's amax is 4 shuffles, and a thread's rows are 16 apart, so a column's amax is a maximum
 // over the thread's own rows, one shuffle, and one pass through shared memory.  Each value is read
 // once whatever is written.
+#include <cuda_bf16.h>
+
 #include "dg_internal.h"
 #include "quant.cuh"
 
@@ -15,34 +17,77 @@ namespace dg {
 namespace {
 
 constexpr int kQThreads = 256;
+constexpr uint32_t kInf = 0x7F800000u;
 
-// 8 consecutive values of a row, zero past the columns
+// 8 consecutive values of a row as they lie: 4 words of bf16 pairs, or 8 FP32 words
 template <bool BF16>
-__device__ __forceinline__ void load8(const QuantParams &p, const char *row, int col, float (&v)[8]) {
+constexpr int kWords = BF16 ? 4 : 8;
+
+// The values of a row from col on; zero past the columns
+template <bool BF16>
+__device__ __forceinline__ void load8(const QuantParams &p, const char *row, int col, uint32_t (&w)[kWords<BF16>]) {
     if (col + 8 <= p.cols) {
-        if constexpr (BF16) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(row + 2 * static_cast<int64_t>(col)));
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        const uint4 *q = reinterpret_cast<const uint4 *>(row + (BF16 ? 2 : 4) * static_cast<int64_t>(col));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(x[i] << 16);
-                v[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
-            }
-        } else {
-            const float4 *q = reinterpret_cast<const float4 *>(row + 4 * static_cast<int64_t>(col));
-            const float4 a = __ldg(q), b = __ldg(q + 1);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        for (int i = 0; i < kWords<BF16> / 4; ++i) {
+            const uint4 x = __ldcs(q + i);   // (read once)
+            w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] = 0.f;
-            if (col + i < p.cols)
-                v[i] = BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[col + i]) << 16)
-                            : reinterpret_cast<const float *>(row)[col + i];
-        }
+        for (int i = 0; i < kWords<BF16>; ++i) w[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i < p.cols) {
+                if constexpr (BF16)
+                    w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[col + i]) << (16 * (i & 1));
+                else
+                    w[i] = reinterpret_cast<const uint32_t *>(row)[col + i];
+            }
     }
+}
+
+// Value i of the 8
+template <bool BF16>
+__device__ __forceinline__ float value(const uint32_t (&w)[kWords<BF16>], int i) {
+    if constexpr (BF16) return __uint_as_float((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    else return __uint_as_float(w[i]);
+}
+
+// max(m, |w|), element by element of a word (m not negative).  A NaN never wins; an infinity does.
+template <bool BF16>
+__device__ __forceinline__ uint32_t amax_word(uint32_t m, uint32_t w) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&m),
+                                         __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w)));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    } else {
+        return __float_as_uint(fmaxf(__uint_as_float(m), fabsf(__uint_as_float(w))));
+    }
+}
+
+// A word's larger element as FP32 bits
+template <bool BF16>
+__device__ __forceinline__ uint32_t amax_bits_of(uint32_t m) {
+    if constexpr (BF16) return max(m & 0xFFFF0000u, m << 16);
+    else return m;
+}
+
+// Infinities become NaN, so that they do not count and get the NaN code.
+template <bool BF16, int N>
+__device__ __forceinline__ void drop_infinities(uint32_t (&v)[N][kWords<BF16>]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < kWords<BF16>; ++j) {
+            const uint32_t w = v[i][j];
+            if constexpr (BF16) {
+                if ((w & 0x7FFF0000u) == kInf) v[i][j] = (v[i][j] & 0xFFFFu) | 0x7FC00000u;
+                if ((w & 0x7FFFu) == 0x7F80u) v[i][j] = (v[i][j] & 0xFFFF0000u) | 0x7FC0u;
+            } else {
+                if ((w & 0x7FFFFFFFu) == kInf) v[i][j] = 0x7FC00000u;
+            }
+        }
 }
 
 __device__ __forceinline__ void store8(const QuantParams &p, uint8_t *row, int col, uint32_t lo, uint32_t hi) {
@@ -53,6 +98,23 @@ __device__ __forceinline__ void store8(const QuantParams &p, uint8_t *row, int c
         for (int i = 0; i < 8; ++i)
             if (col + i < p.cols) row[col + i] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
     }
+}
+
+// The 8 values over one scale, or over their columns' scales, to the codes of a row
+template <bool BF16>
+__device__ __forceinline__ void put_codes(const QuantParams &p, uint8_t *row, int col, const uint32_t (&w)[kWords<BF16>],
+                                          const float (&inv)[8]) {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        o[j] = cvt_e4m3x2(value<BF16>(w, 2 * j) * inv[2 * j], value<BF16>(w, 2 * j + 1) * inv[2 * j + 1]);
+    store8(p, row, col, o[0] | o[1] << 16, o[2] | o[3] << 16);
+}
+template <bool BF16>
+__device__ __forceinline__ void put_codes(const QuantParams &p, uint8_t *row, int col, const uint32_t (&w)[kWords<BF16>],
+                                          float inv) {
+    const float all[8] = {inv, inv, inv, inv, inv, inv, inv, inv};
+    put_codes<BF16>(p, row, col, w, all);
 }
 
 // Row j of the packed words that 128-row block `block` belongs to, its byte, and whether it is the
@@ -83,11 +145,14 @@ __device__ __forceinline__ void put_byte(uint8_t *word, int byte, uint32_t v, bo
 
 // MODE: 1 rows, 2 columns, 3 both, 4 blocks.  TR: rows of a tile (128 but for rows alone).
 template <bool BF16, int MODE, int TR>
-__global__ void __launch_bounds__(kQThreads) dg_quantize_kernel(const __grid_constant__ QuantParams p,
-                                                                const __grid_constant__ KGroupRows t) {
+__global__ void __launch_bounds__(kQThreads, BF16 ? 4 : 2) dg_quantize_kernel(const __grid_constant__ QuantParams p,
+                                                                              const __grid_constant__ KGroupRows t) {
     static_assert(TR == 128 || MODE == 1, "columns and blocks have 128 rows");
-    constexpr int N = TR / 16;   // rows of a thread
-    __shared__ uint32_t s_col[MODE == 2 || MODE == 3 ? 8 : 1][128];
+    constexpr int N = TR / 16;          // rows of a thread
+    constexpr int W = kWords<BF16>;
+    constexpr bool COLS = MODE == 2 || MODE == 3;
+    __shared__ uint32_t s_col[COLS ? 8 : 1][16 * W];   // a warp's column amax
+    __shared__ float s_inv[COLS ? 128 : 1];
     __shared__ uint32_t s_block[8];
     grid_launch_dependents();
     grid_dependency_wait();
@@ -99,7 +164,7 @@ __global__ void __launch_bounds__(kQThreads) dg_quantize_kernel(const __grid_con
     const int tiles_y = (p.rows + TR - 1) / TR;
     for (int ty = blockIdx.y; ty < tiles_y; ty += gridDim.y) {
         const int row0 = ty * TR + rl;
-        float v[N][8];
+        uint32_t v[N][W];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int row = row0 + 16 * i;
@@ -107,90 +172,93 @@ __global__ void __launch_bounds__(kQThreads) dg_quantize_kernel(const __grid_con
                 load8<BF16>(p, x + static_cast<int64_t>(row) * p.ldx * (BF16 ? 2 : 4), col, v[i]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+                for (int j = 0; j < W; ++j) v[i][j] = 0u;
             }
+        }
+        // the thread's amax by column, which also says whether there is an infinity
+        uint32_t cm[W], any = 0u;
+        auto columns = [&]() {
+            any = 0u;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                cm[j] = 0u;
+#pragma unroll
+                for (int i = 0; i < N; ++i) cm[j] = amax_word<BF16>(cm[j], v[i][j]);
+                any = max(any, amax_bits_of<BF16>(cm[j]));
+            }
+        };
+        columns();
+        if (any == kInf) {
+            drop_infinities<BF16, N>(v);
+            columns();
         }
         if constexpr (MODE == 1 || MODE == 3) {
             const int gi = blockIdx.x;
             const bool last = col0 + 128 >= p.cols;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                uint32_t amax = 0;
+                uint32_t m = 0u;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) amax = max(amax, amax_bits(v[i][j]));
+                for (int j = 0; j < W; ++j) m = amax_word<BF16>(m, v[i][j]);
+                uint32_t amax = amax_bits_of<BF16>(m);
 #pragma unroll
                 for (int o = 1; o < 16; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
                 const int row = row0 + 16 * i;
                 const uint32_t byte = ue8m0_of_amax(amax);
-                if (row < p.rows) {
-                    const float inv = inv_scale(byte);
-                    store8(p, p.q + static_cast<int64_t>(row) * p.ldq, col, e4m3x4(v[i][0], v[i][1], v[i][2], v[i][3], inv),
-                           e4m3x4(v[i][4], v[i][5], v[i][6], v[i][7], inv));
-                }
+                if (row < p.rows) put_codes<BF16>(p, p.q + static_cast<int64_t>(row) * p.ldq, col, v[i], inv_scale(byte));
                 if (cl == 0 && row < p.sf_ld)   // (rows that pad the words to a multiple of 4: zero)
                     put_byte(p.sf + (static_cast<int64_t>(gi >> 2) * p.sf_ld + row) * 4, gi & 3, row < p.rows ? byte : 0u, last);
             }
         }
-        if constexpr (MODE == 2 || MODE == 3) {
+        if constexpr (COLS) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < N; ++i) m = max(m, amax_bits(v[i][j]));
-                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-                if (lane < 16) s_col[warp][cl * 8 + j] = m;
+            for (int j = 0; j < W; ++j) {
+                cm[j] = amax_word<BF16>(cm[j], __shfl_xor_sync(0xFFFFFFFFu, cm[j], 16));
+                if (lane < 16) s_col[warp][cl * W + j] = cm[j];
             }
             __syncthreads();
-            if (threadIdx.x < 128) {
-                uint32_t m = 0;
+            if (threadIdx.x < 16 * W) {
+                uint32_t m = 0u;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) m = max(m, s_col[w][threadIdx.x]);
-                const uint32_t byte = ue8m0_of_amax(m);
-                s_col[0][threadIdx.x] = byte;   // (only this thread reads the column's entries)
-                const int c = col0 + threadIdx.x;
-                if (c < p.sfk_ld) {
-                    int word, at;
-                    bool last;
-                    packed_row(p, t, ty, word, at, last);
-                    put_byte(p.sfk + (static_cast<int64_t>(word) * p.sfk_ld + c) * 4, at, c < p.cols ? byte : 0u, last);
+                for (int w = 0; w < 8; ++w) m = amax_word<BF16>(m, s_col[w][threadIdx.x]);
+#pragma unroll
+                for (int e = 0; e < (BF16 ? 2 : 1); ++e) {
+                    const int lc = static_cast<int>(threadIdx.x) * (BF16 ? 2 : 1) + e, c = col0 + lc;
+                    const uint32_t byte = ue8m0_of_amax(BF16 ? (e ? m & 0xFFFF0000u : m << 16) : m);
+                    s_inv[lc] = inv_scale(byte);
+                    if (c < p.sfk_ld) {
+                        int word, at;
+                        bool last;
+                        packed_row(p, t, ty, word, at, last);
+                        put_byte(p.sfk + (static_cast<int64_t>(word) * p.sfk_ld + c) * 4, at, c < p.cols ? byte : 0u, last);
+                    }
                 }
             }
             __syncthreads();
             float inv[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) inv[j] = inv_scale(s_col[0][cl * 8 + j]);
+            for (int j = 0; j < 8; ++j) inv[j] = s_inv[cl * 8 + j];
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int row = row0 + 16 * i;
-                if (row >= p.rows) break;
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = e4m3x2(v[i][2 * j], v[i][2 * j + 1], inv[2 * j], inv[2 * j + 1]);
-                store8(p, p.qk + static_cast<int64_t>(row) * p.ldqk, col, o[0] | o[1] << 16, o[2] | o[3] << 16);
+                if (row < p.rows) put_codes<BF16>(p, p.qk + static_cast<int64_t>(row) * p.ldqk, col, v[i], inv);
             }
-            if (gridDim.y < tiles_y) __syncthreads();   // s_col is free for the next tile
+            // (the next tile's writes to s_col and s_inv come after its own first barrier, or, s_col,
+            // after every thread has passed this tile's second)
         }
         if constexpr (MODE == 4) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m = max(m, amax_bits(v[i][j]));
-            m = __reduce_max_sync(0xFFFFFFFFu, m);
+            uint32_t m = __reduce_max_sync(0xFFFFFFFFu, any);
             if (lane == 0) s_block[warp] = m;
             __syncthreads();
             m = s_block[0];
 #pragma unroll
             for (int w = 1; w < 8; ++w) m = max(m, s_block[w]);
             const uint32_t byte = ue8m0_of_amax(m);
-            const float inv = inv_scale(byte);
             uint8_t *q = p.q + batch * p.q_batch;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int row = row0 + 16 * i;
-                if (row >= p.rows) break;
-                store8(p, q + static_cast<int64_t>(row) * p.ldq, col, e4m3x4(v[i][0], v[i][1], v[i][2], v[i][3], inv),
-                       e4m3x4(v[i][4], v[i][5], v[i][6], v[i][7], inv));
+                if (row < p.rows) put_codes<BF16>(p, q + static_cast<int64_t>(row) * p.ldq, col, v[i], inv_scale(byte));
             }
             // one byte a row (products along the columns), one a column (along the rows)
             const int i = threadIdx.x & 127;
