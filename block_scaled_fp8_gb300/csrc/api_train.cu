@@ -142,9 +142,7 @@ dg_status gated(const GatedArgs &g) {
         p.h = static_cast<uint16_t *>(g.h);
         p.ldh = g.ldh;
         ok &= encode_fp8(&maps.b, g.b, inner, b_rows, g.ldb, kBlockK);
-        ok &= encode_out(&maps.d, g.dgu, 2 * static_cast<uint64_t>(inner), m, g.lddgu);
-        if (g.h) ok &= encode_out(&maps.c, g.h, inner, m, g.ldh);
-        else maps.c = maps.d;   // not used
+        maps.d = maps.c = maps.a;   // not used
     } else {
         p.d = static_cast<uint16_t *>(g.h);
         p.ldd = g.ldh;

@@ -186,12 +186,16 @@ struct Bs2Config {
 // stage fewer where that is their price (that epilogue, not the MMAs, sets the pace
 // of the FP32-output GEMMs).
 constexpr int kF32StageBufs = 4;
+// The gated backward epilogue: five boxes of 32 rows x 32 bf16 columns per warp (two of gate and up,
+// one of h), two operand stages fewer.
+constexpr int kGatedBwdBufs = 10;
 // The bf16 C epilogue keeps its C tile in shared memory where the tile's columns
 // are whole 32-column boxes.
 template <int BN, int MP, bool WITH_C, bool F32>
 constexpr bool kCTile = WITH_C && !F32 && MP == 256 && BN % 32 == 0 && BN <= 256;
 template <int BN, int MP, int LAY, bool F32, bool WITH_C = false>
-using Bs2Cfg = Bs2Config<BN, MP, (LAY & 2) != 0, (LAY & 4) != 0, F32 ? kF32StageBufs : 0, (LAY & 8) != 0,
+using Bs2Cfg = Bs2Config<BN, MP, (LAY & 2) != 0, (LAY & 4) != 0,
+                         (LAY & kLayGatedBwd) ? kGatedBwdBufs : F32 ? kF32StageBufs : 0, (LAY & 8) != 0,
                          kCTile<BN, MP, WITH_C, F32>>;
 
 struct PairTile {
@@ -507,11 +511,51 @@ __device__ __forceinline__ void pack_bf16_32(const uint32_t (&a)[16], const uint
 }
 
 // 1 / (1 + e^-x) by the hardware's 2^x and 1/x: within 2^-21 + 2^-23 |x| of the value
-// (e^-x = inf gives 0), far below the bf16 or E4M3 rounding of what it enters.
-__device__ __forceinline__ float sigmoid_approx(float x) {
-    float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-x)));
+// (0 where it is below 2^-126), far below the bf16 or E4M3 rounding of what it enters.  Two at
+// a time, the sums and products as packed pairs (the gated epilogues' arithmetic is bound by issue
+// slots: flushing forms and pairs take 19 instructions less for two values).
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
     return r;
+}
+__device__ __forceinline__ void f32x2_parts(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t x) {
+    constexpr float kNegLog2e = -1.4426950408889634f;
+    float a, b;
+    f32x2_parts(mul2(x, f32x2(kNegLog2e, kNegLog2e)), a, b);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    f32x2_parts(add2(f32x2(a, b), f32x2(1.0f, 1.0f)), a, b);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return f32x2(a, b);
+}
+__device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
+    float lo, hi;
+    f32x2_parts(v, lo, hi);
+    return pack_bf16(lo, hi);
+}
+// The two values of a bf16 pair.
+__device__ __forceinline__ uint64_t bf16x2_values(uint32_t w) {
+    return f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
 template <int BN, bool WITH_C, int MP, bool F32 = false, int LAY = 0>
@@ -1082,19 +1126,26 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
             __syncwarp();
             c_pending = true;
         };
-        // gated backward: 32 columns of this thread's row of gate (off 0) or up (off p.n); zero
-        // outside the matrix
-        auto load_gu = [&](uint32_t (&dst)[16], int row, int col, int off) {
+        // gated backward: unit h (16 bytes, 8 columns) of row r of a 32 x 32 box; lanes that take one
+        // unit of all rows, and lanes that take the units of 8 rows in order, both reach all banks
+        auto unit = [](uint8_t *box, uint32_t r, uint32_t h) { return box + r * 64 + ((h ^ ((r >> 1) & 3)) << 4); };
+        constexpr int kBox = 2 * Cfg::kStageBufBytes;
+        // Chunk j (32 columns of this warp's rows) of gate and up into boxes 2 (j & 1) and the next, by
+        // asynchronous copies whose lanes take rows' 64 bytes in order; zero outside the matrix.  One
+        // group per call, whether anything is copied or not.
+        auto load_gu = [&](const PairTile &tl, bool any, int j) {
+            uint8_t *const g_box = stage_out + (j & 1) * 2 * kBox;
+            const int c = tl.n0 + static_cast<int>(half) * (BN / 2) + 32 * j + 8 * static_cast<int>(lane & 3);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (row < p.rows && col + 8 * h < p.n)
-                    v = __ldcg(reinterpret_cast<const uint4 *>(p.gu + static_cast<int64_t>(row) * p.ldgu + off + col + 8 * h));
-                dst[4 * h + 0] = v.x;
-                dst[4 * h + 1] = v.y;
-                dst[4 * h + 2] = v.z;
-                dst[4 * h + 3] = v.w;
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t r = 8 * i + (lane >> 2);
+                const int row = tl.d_row0 + row_off + static_cast<int>(r);
+                const bool in = any && tl.valid_rows > 0 && row < p.rows && c < p.n;
+                const uint16_t *src = in ? p.gu + static_cast<int64_t>(row) * p.ldgu + c : p.gu;
+                cp_async_16(smem_u32(unit(g_box, r, lane & 3)), src, in ? 16u : 0u);
+                cp_async_16(smem_u32(unit(g_box + kBox, r, lane & 3)), in ? src + p.n : src, in ? 16u : 0u);
             }
+            cp_async_commit();
         };
         // this tile's rows of gate (first warp of a quadrant) or up (second) to L2
         auto prefetch_gu = [&](const PairTile &tl) {
@@ -1110,7 +1161,11 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
             get_pair_tile<BN, MP, LAY>(p, prefix, pinfo, num_units, psf_k, pair_id, rank, tile);
             if constexpr (WITH_C && !F32) prefetch_c(tile);
             if (c_tma) load_ctile(tile);
-            if constexpr ((LAY & kLayGatedBwd) != 0) prefetch_gu(tile);
+            if constexpr ((LAY & kLayGatedBwd) != 0) {
+                load_gu(tile, true, 0);
+                load_gu(tile, true, 1);
+                prefetch_gu(tile);
+            }
             if constexpr (WITH_C && F32) {
                 prefetch_d32(tile);
                 if (!p.c_in_place) {
@@ -1322,17 +1377,34 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                     }
                 }
                 // h = silu(gate) up, in place of gate
-                uint32_t amax = 0u;
+                float amax_f = 0.f;   // (fmaxf passes NaN over)
 #pragma unroll
                 for (int j = 0; j < HC / 16; ++j)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float gv = __uint_as_float(g[j][i]);
-                        const float h = gv * sigmoid_approx(gv) * __uint_as_float(u[j][i]);
-                        g[j][i] = __float_as_uint(h);
-                        const uint32_t b = col0 + 16 * j < p.n ? amax_bits(h) : 0u;   // (p.n is whole chunks)
-                        amax = b > amax ? b : amax;
+                    for (int i = 0; i < 16; i += 2) {
+                        const uint64_t gv = f32x2(__uint_as_float(g[j][i]), __uint_as_float(g[j][i + 1]));
+                        const uint64_t uv = f32x2(__uint_as_float(u[j][i]), __uint_as_float(u[j][i + 1]));
+                        float a, b;
+                        f32x2_parts(mul2(mul2(gv, sigmoid2(gv)), uv), a, b);
+                        g[j][i] = __float_as_uint(a);
+                        g[j][i + 1] = __float_as_uint(b);
+                        if (col0 + 16 * j < p.n) amax_f = fmaxf(amax_f, fmaxf(fabsf(a), fabsf(b)));   // (p.n is whole chunks)
                     }
+                uint32_t amax = __float_as_uint(amax_f);
+                if (amax == 0x7F800000u) {
+                    // an infinite product: it does not count, and becomes NaN
+                    amax = 0u;
+#pragma unroll
+                    for (int j = 0; j < HC / 16; ++j)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if ((g[j][i] & 0x7FFFFFFFu) == 0x7F800000u) {
+                                if (p.hq != nullptr) g[j][i] = 0x7FC00000u;
+                            } else if (col0 + 16 * j < p.n) {
+                                amax = max(amax, amax_bits(__uint_as_float(g[j][i])));
+                            }
+                        }
+                }
                 if (p.hq != nullptr) {
                     // a row's group of 128 columns is this thread's 64 and its partner's (the other
                     // warp of the quadrant): its scale is the larger of the halves', which meet in
@@ -1382,8 +1454,12 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                 }
             } else if constexpr ((LAY & kLayGatedBwd) != 0) {
                 // gated backward: the accumulator is dh.  This warp's 128 columns of its 32 rows go
-                // to registers and the accumulator is released; gate and up are read 32 columns at a
-                // time (their lines were fetched to L2 a tile ahead)
+                // to registers and the accumulator is released.  Then chunks of 32 columns, whose gate and
+                // up were copied to shared memory two chunks ahead (their lines fetched to L2 a
+                // tile ahead): a lane takes a row, the gradients take the places of gate and up, h a
+                // box of its own, and the warp stores whole row segments with plain stores, which nothing
+                // waits for.  (With TMA boxes in and out, a chunk's load, arithmetic and store
+                // followed one another: 4096x7168, K = 2048: 102 us against the 49 of the product alone.)
                 constexpr int HC = BN / 2;
                 uint32_t dh[HC / 16][16];
                 const uint32_t tcol = tmem_base + ((quad * 32) << 16) + acc * ACC + half * HC;
@@ -1397,38 +1473,53 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(leader_tempty + acc * 8);
                 if (++acc == NUM_ACC) { acc = 0; acc_phase ^= 1; }
-                const int row = tile.d_row0 + row_off + static_cast<int>(lane);
-                if (tile.valid_rows > 0) {
 #pragma unroll
-                    for (int j = 0; j < HC / 16; j += 2) {
-                        const int col0 = tile.n0 + static_cast<int>(half) * HC + 16 * j;
-                        uint32_t gv[16], uv[16], og[16], ou[16], oh[16];
-                        load_gu(gv, row, col0, 0);
-                        load_gu(uv, row, col0, p.n);
+                for (int j = 0; j < HC / 32; ++j) {
+                    uint8_t *const g_box = stage_out + (j & 1) * 2 * kBox, *const u_box = g_box + kBox;
+                    uint8_t *const h_box = stage_out + 4 * kBox;
+                    cp_async_wait<1>();   // this lane's copies of chunk j, and so, all lanes'
+                    __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint32_t *d2 = dh[j + i / 8] + 2 * (i & 7);
-                            float r[2][3];
+                    for (int h = 0; h < 4; ++h) {
+                        uint4 *const gp = reinterpret_cast<uint4 *>(unit(g_box, lane, h));
+                        uint4 *const up = reinterpret_cast<uint4 *>(unit(u_box, lane, h));
+                        const uint4 g4 = *gp, u4 = *up;
+                        const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+                        uint32_t og[4], ou[4], oh[4];
 #pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const float gt = __uint_as_float(q ? gv[i] & 0xFFFF0000u : gv[i] << 16);
-                                const float up = __uint_as_float(q ? uv[i] & 0xFFFF0000u : uv[i] << 16);
-                                const float d = __uint_as_float(d2[q]);
-                                // s = sigmoid(g), silu = g s, silu' = s + silu (1 - s)
-                                const float sg = sigmoid_approx(gt);
-                                const float si = gt * sg;
-                                r[q][0] = d * up * fmaf(si, 1.0f - sg, sg);
-                                r[q][1] = d * si;
-                                r[q][2] = si * up;
-                            }
-                            og[i] = pack_bf16(r[0][0], r[1][0]);
-                            ou[i] = pack_bf16(r[0][1], r[1][1]);
-                            oh[i] = pack_bf16(r[0][2], r[1][2]);
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t *d2 = dh[2 * j + h / 2] + 8 * (h & 1) + 2 * i;
+                            const uint64_t d = f32x2(__uint_as_float(d2[0]), __uint_as_float(d2[1]));
+                            const uint64_t gt = bf16x2_values(gw[i]), uv = bf16x2_values(uw[i]);
+                            // s = sigmoid(g), silu = g s, silu' = s + silu (1 - s)
+                            const uint64_t sg = sigmoid2(gt), si = mul2(gt, sg);
+                            const uint64_t rest = fma2(sg, f32x2(-1.0f, -1.0f), f32x2(1.0f, 1.0f));
+                            og[i] = pack_bf16(mul2(mul2(d, uv), fma2(si, rest, sg)));
+                            ou[i] = pack_bf16(mul2(d, si));
+                            oh[i] = pack_bf16(mul2(si, uv));
                         }
-                        store_pair(&tm_d, p.d, p.ldd, og, col0, 0);
-                        store_pair(&tm_d, p.d, p.ldd, ou, col0, p.n);
-                        if (p.h != nullptr) store_pair(&tm_c, p.h, p.ldh, oh, col0, 0);
+                        *gp = make_uint4(og[0], og[1], og[2], og[3]);
+                        *up = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+                        *reinterpret_cast<uint4 *>(unit(h_box, lane, h)) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
                     }
+                    __syncwarp();
+                    const int c = tile.n0 + static_cast<int>(half) * HC + 32 * j + 8 * static_cast<int>(lane & 3);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t r = 8 * i + (lane >> 2);
+                        const int row = tile.d_row0 + row_off + static_cast<int>(r);
+                        if (tile.valid_rows > 0 && row < p.rows && c < p.n) {
+                            uint16_t *dr = p.d + static_cast<int64_t>(row) * p.ldd + c;
+                            *reinterpret_cast<uint4 *>(dr) = *reinterpret_cast<const uint4 *>(unit(g_box, r, lane & 3));
+                            *reinterpret_cast<uint4 *>(dr + p.n) = *reinterpret_cast<const uint4 *>(unit(u_box, r, lane & 3));
+                            if (p.h != nullptr)
+                                *reinterpret_cast<uint4 *>(p.h + static_cast<int64_t>(row) * p.ldh + c) =
+                                    *reinterpret_cast<const uint4 *>(unit(h_box, r, lane & 3));
+                        }
+                    }
+                    __syncwarp();   // the boxes have been read
+                    if (j + 2 < HC / 32) load_gu(tile, true, j + 2);
+                    else load_gu(next_tile, has_next, j + 2 - HC / 32);
                 }
             } else if constexpr (F32) {
                 // FP32 D (and FP32 C): each chunk goes TMEM -> registers (+ C) -> one
@@ -1635,6 +1726,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
         }
         // (an aborted loop leaves no C load landing in shared memory after the CTA is gone)
         if (c_pending && lane == 0) mbar_wait_drain(&cfull_bar[ew], c_phase, ctl);
+        if constexpr ((LAY & kLayGatedBwd) != 0) cp_async_wait<0>();
         if (lane == 0) bulk_wait_group<0>();
         __syncwarp();
     }

@@ -31,17 +31,9 @@ __device__ __forceinline__ uint32_t ue8m0_of_amax(uint32_t bits) {
 // 1 / scale; the byte is at most 247, so this is a normal number.
 __device__ __forceinline__ float inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// A value over its scale: |v inv| <= 448, so only infinities would saturate, and they become NaN.
-__device__ __forceinline__ float over_scale(float v, float inv) {
-    return (__float_as_uint(v) & 0x7FFFFFFFu) == 0x7F800000u ? __uint_as_float(0x7FC00000u) : v * inv;
-}
-
-// E4M3 codes of two values over their own scales, of four over one; the first in the low byte.
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b, float inv_a, float inv_b) {
-    return cvt_e4m3x2(over_scale(a, inv_a), over_scale(b, inv_b));
-}
+// E4M3 codes of four values (none infinite) over one scale, the first in the low byte.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float inv) {
-    return e4m3x2(a, b, inv, inv) | (e4m3x2(c, d, inv, inv) << 16);
+    return cvt_e4m3x2(a * inv, b * inv) | (cvt_e4m3x2(c * inv, d * inv) << 16);
 }
 
 }  // namespace dg
