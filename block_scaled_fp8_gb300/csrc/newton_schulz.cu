@@ -119,6 +119,8 @@ __device__ __forceinline__ void norm_factors(const NsParams &p, int64_t batch, f
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         if (threadIdx.x == 0) sum = s;
     }
+    // (the products' grid counter and abort word, which follow in the stream)
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 2) p.sync[threadIdx.x] = 0u;
     __syncthreads();
     const double norm = sqrt(sum) + static_cast<double>(p.eps);
     int e = 0;
@@ -249,15 +251,305 @@ __device__ __forceinline__ float2 half2_values(uint32_t w) { return __half22floa
 //
 // The epilogue's own operands (A; the planes of X) come by TMA into the boxes that the results go
 // out from, two chunks ahead.
+//
+// All products of all steps are one cooperative launch: each is a phase, and between phases the
+// grid waits for all CTAs' results (one arrival a CTA on a counter in the workspace, polled by the
+// producer warps, with a limit).  As launches of their own they cost 7.5 us each however small
+// (64x64, five steps: 127 us).
+struct NsMaps {
+    CUtensorMap xk[2], xn[2];   // X's high planes along K, and as [K][N]
+    CUtensorMap a, b;           // A, B along K
+    CUtensorMap xh[2], xl, ea, eb, out;   // boxes of the epilogue
+};
+
+// What a phase works on.
+struct NsPhase {
+    int mode, step, cols, tm, tn, per, num_tiles, nkb;
+};
+
+__device__ __forceinline__ NsPhase ns_phase(const NsParams &p, int i) {
+    NsPhase f;
+    f.step = i / 3;
+    f.mode = i % 3;
+    if (f.mode == kNsUpdate && f.step + 1 == p.steps) f.mode = kNsLast;
+    const bool sym = f.mode < kNsUpdate;
+    f.cols = sym ? p.lo : p.hi;
+    f.tm = (p.lo + kTile - 1) / kTile;
+    f.tn = (f.cols + kTile - 1) / kTile;
+    f.per = sym ? f.tm * (f.tm + 1) / 2 : f.tm * f.tn;
+    f.num_tiles = f.per * p.batch;
+    f.nkb = ((f.mode == kNsGram ? p.hi : p.lo) + kKBlock - 1) / kKBlock;
+    return f;
+}
+
+// Tile t of a phase: (batch, m, n), the m tiles of a column of tiles first; symmetric: column n has
+// tiles 0..n
+__device__ __forceinline__ void ns_locate(const NsPhase &f, int t, int &b, int &m0, int &n0) {
+    b = t / f.per;
+    const int r = t - b * f.per;
+    if (f.mode < kNsUpdate) {
+        int n = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
+        while (n * (n + 1) / 2 > r) --n;
+        while ((n + 1) * (n + 2) / 2 <= r) ++n;
+        m0 = (r - n * (n + 1) / 2) * kTile;
+        n0 = n * kTile;
+    } else {
+        m0 = (r % f.tm) * kTile;
+        n0 = (r / f.tm) * kTile;
+    }
+}
+
+// State that an epilogue warp keeps over the phases.
+struct NsEpilogue {
+    const NsParams &p;
+    const WaitCtl &ctl;
+    uint32_t ew, quad, half, lane, tmem_base, leader_tempty;
+    int rank, pair_id, num_pairs;
+    uint8_t *slots;
+    uint64_t *landed, *tfull_bar;
+    int acc, pending;   // pending: slots (bits) whose loads have not been waited for
+    uint32_t acc_phase, in_phase;
+};
+
+// One phase of an epilogue warp; false if the CTA is aborting.
 template <int MODE>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
-    dg_ns_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                      const __grid_constant__ CUtensorMap tm_in0, const __grid_constant__ CUtensorMap tm_in1,
-                      const __grid_constant__ CUtensorMap tm_out0, const __grid_constant__ CUtensorMap tm_out1,
-                      const __grid_constant__ NsParams p, const int k) {
-    constexpr bool B_MN = MODE >= kNsUpdate;
+__device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, const CUtensorMap *tm_in0,
+                                            const CUtensorMap *tm_in1, const CUtensorMap *tm_out0,
+                                            const CUtensorMap *tm_out1) {
     constexpr bool SYM = MODE < kNsUpdate;
     constexpr int kLoads = MODE == kNsGram ? 0 : MODE == kNsPoly ? 1 : 2;   // boxes a chunk reads
+    const NsParams &p = st.p;
+    const WaitCtl &ctl = st.ctl;
+    const uint32_t lane = st.lane, quad = st.quad, half = st.half;
+    const int num_tiles = ph.num_tiles, num_pairs = st.num_pairs, pair_id = st.pair_id;
+    const int rows = p.lo, cols = ph.cols;
+            uint8_t *const slots = st.slots;
+            uint64_t *const landed = st.landed;
+            int &acc = st.acc, &pending = st.pending;
+            uint32_t &acc_phase = st.acc_phase, &in_phase = st.in_phase;
+            const int rank = st.rank;
+            const int row_off = rank * 128 + static_cast<int>(quad) * 32, col_off = static_cast<int>(half) * 128;
+            // 16-byte unit h of row r of a box (64-byte swizzle)
+            auto unit = [](uint8_t *box, int r, int h) { return reinterpret_cast<uint4 *>(box + r * 64 + ((h ^ ((r >> 1) & 3)) << 4)); };
+            // chunk j of tile t: the epilogue's operands, into slot j & 1 (j counts on over the tiles)
+            auto load_chunk = [&](int t, int j) {
+                if constexpr (kLoads > 0) {
+                    if (t >= num_tiles) return;
+                    int b, m0, n0;
+                    ns_locate(ph, t, b, m0, n0);
+                    uint8_t *box = slots + (j & 1) * kSlotBytes;
+                    const int x = n0 + col_off + 32 * (j & 3), y = m0 + row_off;
+                    mbar_arrive_expect_tx(&landed[j & 1], kLoads * kBoxBytes);
+                    tma_load_3d(box, tm_in0, &landed[j & 1], x, y, b);
+                    if constexpr (kLoads > 1) tma_load_3d(box + kBoxBytes, tm_in1, &landed[j & 1], x, y, b);
+                }
+            };
+            if (kLoads > 0 && pair_id < num_tiles) {
+                if (lane == 0) {
+                    load_chunk(pair_id, 0);
+                    load_chunk(pair_id, 1);
+                }
+                pending = 3;
+            }
+            for (int t = pair_id; t < num_tiles; t += num_pairs) {
+                int b, m0, n0;
+                ns_locate(ph, t, b, m0, n0);
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&st.tfull_bar[acc], acc_phase, ctl, DG_DEV_TIMEOUT))) return false;
+                tc_fence_after_sync();
+                const int row0 = m0 + row_off, row = row0 + static_cast<int>(lane);
+                const bool mirror = SYM && m0 != n0;
+                // the row's entry of A's or B's diagonal
+                float diag = 0.f;
+                if (MODE != kNsGram && row < rows) diag = __ldcg((MODE == kNsPoly ? p.da : p.db) + static_cast<int64_t>(b) * p.lo + row);
+    #pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
+                    const int s = j & 1, col = n0 + col_off + 32 * j;
+                    uint8_t *box0 = slots + s * kSlotBytes, *box1 = box0 + kBoxBytes;
+                    uint32_t v[2][16];
+                    const uint32_t at = st.tmem_base + ((quad * 32) << 16) + acc * kTile + half * 128 + 32 * j;
+                    tmem_ld_32x32b_x16(at, v[0]);
+                    tmem_ld_32x32b_x16(at + 16, v[1]);
+                    if constexpr (kLoads > 0) {
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&landed[s], (in_phase >> s) & 1u, ctl, DG_DEV_TIMEOUT)))
+                            return false;
+                        in_phase ^= 1u << s;
+                        pending &= ~(1 << s);
+                    }
+                    tmem_ld_wait();
+                    reg_fence16(v[0]);
+                    reg_fence16(v[1]);
+                    if (j == 3) {   // the accumulator has been read
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(st.leader_tempty + acc * 8);
+                    }
+                    const bool in = row0 < rows && col < cols;   // (else nothing of the chunk is stored)
+                    if constexpr (kLoads == 0) {
+                        // the slot's stores have read it (the other slot's may still run)
+                        if (lane == 0) bulk_wait_group_read<1>();
+                        __syncwarp();
+                    }
+                    // 8 columns at a time, in place: f in units of 2^-12
+    #pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const uint32_t *x = v[h >> 1] + 8 * (h & 1);
+                        float f[8];
+                        uint32_t w0[4], w1[4];
+                        if constexpr (kLoads > 0) {
+                            const uint4 q = *unit(box0, lane, h);
+                            w0[0] = q.x; w0[1] = q.y; w0[2] = q.z; w0[3] = q.w;
+                        }
+                        if constexpr (kLoads > 1) {
+                            const uint4 q = *unit(box1, lane, h);
+                            w1[0] = q.x; w1[1] = q.y; w1[2] = q.z; w1[3] = q.w;
+                        }
+                        if constexpr (MODE == kNsGram) {
+    #pragma unroll
+                            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(x[i]) * (1.0f / kScale);
+                        } else if constexpr (MODE == kNsPoly) {
+                            float dc[8];
+                            const float *d = p.da + static_cast<int64_t>(b) * p.lo + col + 8 * h;
+    #pragma unroll
+                            for (int i = 0; i < 8; ++i) dc[i] = col + 8 * h + i < cols ? __ldcg(d + i) : 0.f;
+    #pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 r = half2_values(w0[i]);
+                                f[2 * i] = fmaf(fmaf(p.cc, diag + dc[2 * i], p.cb), r.x, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i]));
+                                f[2 * i + 1] = fmaf(fmaf(p.cc, diag + dc[2 * i + 1], p.cb), r.y, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
+                            }
+                        } else {
+    #pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 hi = half2_values(w0[i]), lo = half2_values(w1[i]);
+                                f[2 * i] = fmaf(p.ca + diag, hi.x + lo.x, (1.0f / kScale) * __uint_as_float(x[2 * i]));
+                                f[2 * i + 1] = fmaf(p.ca + diag, hi.y + lo.y, (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
+                            }
+                        }
+                        if constexpr (SYM) {
+                            // the diagonal goes out in FP32 (as it is, not scaled)
+                            const int on = row - (col + 8 * h);
+                            if (m0 == n0 && on >= 0 && on < 8) {
+    #pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    if (i == on) {
+                                        const float dv = f[i] * (1.0f / kScale);
+                                        if (row < rows)
+                                            (MODE == kNsGram ? p.da : p.db)[static_cast<int64_t>(b) * p.lo + row] =
+                                                MODE == kNsGram ? dv : fmaf(diag, fmaf(p.cc, diag, p.cb), dv);
+                                        f[i] = 0.f;
+                                    }
+                            }
+                        }
+                        if constexpr (MODE == kNsLast) {
+    #pragma unroll
+                            for (int i = 0; i < 8; ++i) f[i] *= 1.0f / kScale;
+                            if (!p.out_tma) {
+                                // rows that TMA cannot address: element by element
+                                uint16_t *out = p.out + b * p.out_batch;
+                                const bool tall = p.rows > p.cols;
+    #pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const int c = col + 8 * h + i;
+                                    if (row >= rows || c >= cols) continue;
+                                    const __nv_bfloat16 o = __float2bfloat16_rn(f[i]);
+                                    out[tall ? static_cast<int64_t>(c) * p.ldo + row : static_cast<int64_t>(row) * p.ldo + c] =
+                                        *reinterpret_cast<const uint16_t *>(&o);
+                                }
+                            } else if (p.rows > p.cols) {
+                                // (box1: every lane has read its own unit h of the low plane, the others not;
+                                // the transposed box is written once all have, below)
+    #pragma unroll
+                                for (int i = 0; i < 8; ++i) v[h >> 1][8 * (h & 1) + i] = __float_as_uint(f[i]);
+                            } else {
+                                uint32_t o[4];
+    #pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                                    o[i] = *reinterpret_cast<const uint32_t *>(&b2);
+                                }
+                                *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
+                            }
+                        } else if constexpr (MODE == kNsUpdate) {
+                            uint32_t o[4], l[4];
+    #pragma unroll
+                            for (int i = 0; i < 4; ++i) split2(f[2 * i], f[2 * i + 1], o[i], l[i]);
+                            *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *unit(box1, lane, h) = make_uint4(l[0], l[1], l[2], l[3]);
+                        } else {
+                            uint32_t o[4];
+    #pragma unroll
+                            for (int i = 0; i < 4; ++i) o[i] = half2_bits(f[2 * i], f[2 * i + 1]);
+                            *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
+                            if (mirror) {
+    #pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const uint16_t e = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+                                    *reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(unit(box1, 8 * h + i, lane >> 3)) + 2 * (lane & 7)) = e;
+                                }
+                            }
+                        }
+                    }
+                    if constexpr (MODE == kNsLast) {
+                        if (p.out_tma && p.rows > p.cols) {
+                            __syncwarp();
+    #pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(v[c >> 4][c & 15]));
+                                *reinterpret_cast<__nv_bfloat16 *>(reinterpret_cast<uint8_t *>(unit(box0, c, lane >> 3)) + 2 * (lane & 7)) = o;
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (in && (MODE != kNsLast || p.out_tma)) {
+                            if (MODE == kNsLast && p.rows > p.cols) {
+                                tma_store_3d(tm_out0, box0, row0, col, b);
+                            } else {
+                                tma_store_3d(tm_out0, box0, col, row0, b);
+                                if (MODE == kNsUpdate) tma_store_3d(tm_out1, box1, col, row0, b);
+                                if (mirror) tma_store_3d(tm_out0, box1, row0, col, b);
+                            }
+                        }
+                        bulk_commit_group();
+                        if constexpr (kLoads > 0) {
+                            bulk_wait_group_read<0>();
+                            // two chunks on: of this tile, or of this pair's next
+                            load_chunk(j < 2 ? t : t + num_pairs, j < 2 ? j + 2 : j - 2);
+                        }
+                    }
+                    if (kLoads > 0 && (j < 2 || t + num_pairs < num_tiles)) pending |= 1 << s;
+                    __syncwarp();
+                }
+                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+            }
+            // the phase's results are in memory before its arrival
+            if (lane == 0) bulk_wait_group<0>();
+            __syncwarp();
+            return true;
+}
+
+// Waits until the counter has come to `target` (all CTAs' arrivals of the phases before); false if
+// it does not within the limit or some CTA has given up.
+__device__ __noinline__ bool ns_grid_wait(const NsParams &p, uint32_t target, const WaitCtl &ctl) {
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        uint32_t seen, gone;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(p.sync) : "memory");
+        if (static_cast<int32_t>(seen - target) >= 0) return true;
+        asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(gone) : "l"(p.sync + 1) : "memory");
+        const bool late = global_timer_ns() - t0 > ctl.timeout_ns;
+        if (late && ctl.status) atomicOr(ctl.status, DG_DEV_TIMEOUT);
+        if (gone != 0u || late || *ctl.abort) {
+            *ctl.abort = 1;
+            return false;
+        }
+        __nanosleep(32);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    dg_ns_products_kernel(const __grid_constant__ NsMaps maps, const __grid_constant__ NsParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -269,32 +561,34 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint64_t *tfull_bar = empty_bar + kStages;   // [2] both: accumulator complete
     uint64_t *tempty_bar = tfull_bar + 2;        // [2] leader: both epilogues drained
     uint64_t *drain_bar = tempty_bar + 2;
-    uint64_t *in_bar = drain_bar + 1;            // [kEpiWarps][2] an epilogue warp's boxes landed
+    uint64_t *phase_bar = drain_bar + 1;         // the grid has finished the phase before
+    uint64_t *in_bar = phase_bar + 1;            // [kEpiWarps][2] an epilogue warp's boxes landed
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(in_bar + 2 * kEpiWarps);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    uint32_t *done = tmem_holder + 2;            // epilogue warps that have finished phases
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
+    const WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
     const int rank = static_cast<int>(cluster_ctarank());
     const bool leader = rank == 0;
     const int pair_id = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
-    const int rows = p.lo, cols = MODE >= kNsUpdate ? p.hi : p.lo;
-    const int tm = (rows + kTile - 1) / kTile, tn = (cols + kTile - 1) / kTile;
-    const int per = SYM ? tm * (tm + 1) / 2 : tm * tn, num_tiles = per * p.batch;
-    const int nkb = (k + kKBlock - 1) / kKBlock;
+    const int phases = 3 * p.steps;
 
     if (warp == 0) {
         for (uint64_t *b = bars + lane; b < in_bar + 2 * kEpiWarps; b += 32)
             mbar_init(b, b >= tempty_bar && b < tempty_bar + 2 ? 2 * kEpiWarps : 1);
-        if (lane == 0) *abort_flag = 0;
+        if (lane == 0) {
+            *abort_flag = 0;
+            *done = 0u;
+        }
         fence_mbar_init();
         if (lane == 0) {
-            tma_prefetch_desc(&tm_a);
-            tma_prefetch_desc(&tm_b);
+            tma_prefetch_desc(&maps.xk[0]);
+            tma_prefetch_desc(&maps.a);
+            tma_prefetch_desc(&maps.b);
+            tma_prefetch_desc(&maps.xn[0]);
         }
     }
-    grid_launch_dependents();
-    grid_dependency_wait();
     __syncthreads();
     cluster_sync();
     if (warp == 1) {
@@ -306,51 +600,52 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_holder;
 
-    // tile t: (batch, m, n), the m tiles of a column of tiles first; symmetric: column n has tiles 0..n
-    auto locate = [&](int t, int &b, int &m0, int &n0) {
-        b = t / per;
-        const int r = t - b * per;
-        if constexpr (SYM) {
-            int n = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
-            while (n * (n + 1) / 2 > r) --n;
-            while ((n + 1) * (n + 2) / 2 <= r) ++n;
-            m0 = (r - n * (n + 1) / 2) * kTile;
-            n0 = n * kTile;
-        } else {
-            m0 = (r % tm) * kTile;
-            n0 = (r / tm) * kTile;
-        }
-    };
-
     if (warp == 0) {
         const uint32_t leader_full = mapa_shared(smem_u32(full_bar), 0);
         int slot = 0;
         uint32_t phase = 0, issued = 0;
-        bool drop = (p.debug_flags & DG_DEBUG_DROP_ONE_LOAD) && pair_id == 0 && MODE == kNsGram;
-        for (int t = pair_id; t < num_tiles; t += num_pairs) {
-            int b, m0, n0;
-            locate(t, b, m0, n0);
-            for (int kb = 0; kb < nkb; ++kb) {
-                if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto prod_done;
-                if (drop) {
-                    drop = false;   // diagnostic: leave this stage empty
-                } else {
-                    if (elect_one()) {
-                        const uint32_t fb = leader_full + slot * 8;
-                        if (leader) mbar_arrive_expect_tx(&full_bar[slot], 2 * kStageBytes);
-                        tma_load_3d_pair(smem_a + slot * 16384, &tm_a, fb, kb * kKBlock, m0 + rank * 128, b);
-                        if constexpr (B_MN) {
-                            // 64 columns (one swizzle atom) x 64 K rows a box
-                            tma_load_3d_pair(smem_b + slot * 16384, &tm_b, fb, n0 + rank * 128, kb * kKBlock, b);
-                            tma_load_3d_pair(smem_b + slot * 16384 + 8192, &tm_b, fb, n0 + rank * 128 + 64, kb * kKBlock, b);
-                        } else {
-                            tma_load_3d_pair(smem_b + slot * 16384, &tm_b, fb, kb * kKBlock, n0 + rank * 128, b);
-                        }
-                    }
-                    __syncwarp();
-                    issued |= 1u << slot;
+        bool drop = (p.debug_flags & DG_DEBUG_DROP_ONE_LOAD) && pair_id == 0;
+        for (int i = 0; i < phases; ++i) {
+            const NsPhase f = ns_phase(p, i);
+            if (i > 0) {
+                bool ok = true;
+                if (lane == 0) {
+                    ok = ns_grid_wait(p, static_cast<uint32_t>(i) * gridDim.x, ctl);
+                    // the other CTAs' results, written by TMA and plain stores, are read by TMA
+                    asm volatile("fence.proxy.async.global;" ::: "memory");
+                    if (ok) mbar_arrive(phase_bar);
                 }
-                if (++slot == kStages) { slot = 0; phase ^= 1; }
+                if (!__all_sync(0xFFFFFFFFu, ok)) goto prod_done;
+            }
+            const CUtensorMap *ta = f.mode == kNsGram ? &maps.xk[f.step & 1] : f.mode == kNsPoly ? &maps.a : &maps.b;
+            const CUtensorMap *tb = f.mode == kNsGram ? ta : f.mode == kNsPoly ? ta : &maps.xn[f.step & 1];
+            const bool b_mn = f.mode >= kNsUpdate;
+            for (int t = pair_id; t < f.num_tiles; t += num_pairs) {
+                int b, m0, n0;
+                ns_locate(f, t, b, m0, n0);
+                for (int kb = 0; kb < f.nkb; ++kb) {
+                    if (!mbar_wait_warp(&empty_bar[slot], phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto prod_done;
+                    if (drop) {
+                        drop = false;   // diagnostic: leave this stage empty
+                    } else {
+                        if (elect_one()) {
+                            const uint32_t fb = leader_full + slot * 8;
+                            uint8_t *sa = smem_a + slot * 16384, *sb = smem_b + slot * 16384;
+                            if (leader) mbar_arrive_expect_tx(&full_bar[slot], 2 * kStageBytes);
+                            tma_load_3d_pair(sa, ta, fb, kb * kKBlock, m0 + rank * 128, b);
+                            if (b_mn) {
+                                // 64 columns (one swizzle atom) x 64 K rows a box
+                                tma_load_3d_pair(sb, tb, fb, n0 + rank * 128, kb * kKBlock, b);
+                                tma_load_3d_pair(sb + 8192, tb, fb, n0 + rank * 128 + 64, kb * kKBlock, b);
+                            } else {
+                                tma_load_3d_pair(sb, tb, fb, kb * kKBlock, n0 + rank * 128, b);
+                            }
+                        }
+                        __syncwarp();
+                        issued |= 1u << slot;
+                    }
+                    if (++slot == kStages) { slot = 0; phase ^= 1; }
+                }
             }
         }
     prod_done:
@@ -362,32 +657,39 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (leader) {
             int slot = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            // FP16 x FP16 -> FP32, M = 256, N = 256, B MN-major where X is
-            constexpr uint32_t idesc = (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24) | (B_MN ? 1u << 16 : 0u);
+            // FP16 x FP16 -> FP32, M = 256, N = 256 (bit 16: B MN-major)
+            constexpr uint32_t idesc_k = (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
             const uint64_t a0 = make_desc_kmajor_sw128(smem_u32(smem_a));
-            // (MN-major: the two 64-column atoms 8192 bytes apart, 8 K rows 1024)
-            const uint64_t b0 = B_MN ? make_smem_desc(smem_u32(smem_b), 8192, 1024, kSwizzle128B)
-                                     : make_desc_kmajor_sw128(smem_u32(smem_b));
-            constexpr uint64_t kStepB = B_MN ? (2048 >> 4) : 2;   // 16 K: 16 rows, or 32 bytes along a row
-            for (int t = pair_id; t < num_tiles; t += num_pairs) {
-                if (!mbar_wait_cluster_warp(&tempty_bar[acc], acc_phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto mma_done;
-                tc_fence_after_sync();
-                const uint32_t d = tmem_base + acc * kTile;
-                for (int kb = 0; kb < nkb; ++kb) {
-                    if (!mbar_wait_warp(&full_bar[slot], phase, ctl, DG_DEV_TIMEOUT)) goto mma_done;
+            for (int i = 0; i < phases; ++i) {
+                const NsPhase f = ns_phase(p, i);
+                const bool b_mn = f.mode >= kNsUpdate;
+                const uint32_t idesc = idesc_k | (b_mn ? 1u << 16 : 0u);
+                // (MN-major: the two 64-column atoms 8192 bytes apart, 8 K rows 1024)
+                const uint64_t b0 = b_mn ? make_smem_desc(smem_u32(smem_b), 8192, 1024, kSwizzle128B)
+                                         : make_desc_kmajor_sw128(smem_u32(smem_b));
+                const uint64_t step_b = b_mn ? (2048 >> 4) : 2;   // 16 K: 16 rows, or 32 bytes along a row
+                for (int t = pair_id; t < f.num_tiles; t += num_pairs) {
+                    if (!mbar_wait_cluster_warp(&tempty_bar[acc], acc_phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto mma_done;
                     tc_fence_after_sync();
-                    if (elect_one()) {
-                        const uint64_t a = a0 + slot * (16384 >> 4), b = b0 + slot * (16384 >> 4);
+                    const uint32_t d = tmem_base + acc * kTile;
+                    for (int kb = 0; kb < f.nkb; ++kb) {
+                        // (a tile's first stage may follow phases that have no tile for this pair: the
+                        // limit is far above a phase)
+                        if (!mbar_wait_warp(&full_bar[slot], phase, ctl, DG_DEV_TIMEOUT)) goto mma_done;
+                        tc_fence_after_sync();
+                        if (elect_one()) {
+                            const uint64_t a = a0 + slot * (16384 >> 4), b = b0 + slot * (16384 >> 4);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) mma_f16_pair(d, a + 2 * s, b + kStepB * s, idesc, (kb | s) != 0);
-                        tc_commit_pair(&empty_bar[slot], 0x3);
+                            for (int s = 0; s < 4; ++s) mma_f16_pair(d, a + 2 * s, b + step_b * s, idesc, (kb | s) != 0);
+                            tc_commit_pair(&empty_bar[slot], 0x3);
+                        }
+                        __syncwarp();
+                        if (++slot == kStages) { slot = 0; phase ^= 1; }
                     }
+                    if (elect_one()) tc_commit_pair(&tfull_bar[acc], 0x3);
                     __syncwarp();
-                    if (++slot == kStages) { slot = 0; phase ^= 1; }
+                    if (++acc == 2) { acc = 0; acc_phase ^= 1; }
                 }
-                if (elect_one()) tc_commit_pair(&tfull_bar[acc], 0x3);
-                __syncwarp();
-                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
             }
         mma_done:
             if (elect_one()) {
@@ -397,218 +699,41 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
         }
     } else {
-        const uint32_t ew = warp - 2, quad = warp & 3, half = ew >> 2;
-        const uint32_t leader_tempty = mapa_shared(smem_u32(tempty_bar), 0);
-        uint8_t *const slots = smem_epi + ew * 2 * kSlotBytes;
-        uint64_t *const landed = in_bar + 2 * ew;
-        const int row_off = rank * 128 + static_cast<int>(quad) * 32, col_off = static_cast<int>(half) * 128;
-        // 16-byte unit h of row r of a box (64-byte swizzle)
-        auto unit = [](uint8_t *box, int r, int h) { return reinterpret_cast<uint4 *>(box + r * 64 + ((h ^ ((r >> 1) & 3)) << 4)); };
-        // chunk j of tile t: the epilogue's operands, into slot j & 1 (j counts on over the tiles)
-        auto load_chunk = [&](int t, int j) {
-            if constexpr (kLoads > 0) {
-                if (t >= num_tiles) return;
-                int b, m0, n0;
-                locate(t, b, m0, n0);
-                uint8_t *box = slots + (j & 1) * kSlotBytes;
-                const int x = n0 + col_off + 32 * (j & 3), y = m0 + row_off;
-                mbar_arrive_expect_tx(&landed[j & 1], kLoads * kBoxBytes);
-                tma_load_3d(box, &tm_in0, &landed[j & 1], x, y, b);
-                if constexpr (kLoads > 1) tma_load_3d(box + kBoxBytes, &tm_in1, &landed[j & 1], x, y, b);
+        const uint32_t ew = warp - 2;
+        NsEpilogue st{p, ctl, ew, warp & 3, ew >> 2, lane, tmem_base, mapa_shared(smem_u32(tempty_bar), 0), rank, pair_id,
+                      num_pairs, smem_epi + ew * 2 * kSlotBytes, in_bar + 2 * ew, tfull_bar, 0, 0, 0u, 0u};
+        for (int i = 0; i < phases; ++i) {
+            const NsPhase f = ns_phase(p, i);
+            if (i > 0 && !mbar_wait_warp(phase_bar, (i - 1) & 1, ctl, DG_DEV_TIMEOUT)) break;
+            const CUtensorMap *xh = &maps.xh[f.step & 1], *next = &maps.xh[(f.step & 1) ^ 1];
+            bool ok;
+            if (f.mode == kNsGram) ok = ns_epilogue<kNsGram>(st, f, nullptr, nullptr, &maps.ea, nullptr);
+            else if (f.mode == kNsPoly) ok = ns_epilogue<kNsPoly>(st, f, &maps.ea, nullptr, &maps.eb, nullptr);
+            else if (f.mode == kNsUpdate) ok = ns_epilogue<kNsUpdate>(st, f, xh, &maps.xl, next, &maps.xl);
+            else ok = ns_epilogue<kNsLast>(st, f, xh, &maps.xl, &maps.out, nullptr);
+            if (!ok) break;
+            // the warp's results are visible to the grid (all lanes' plain stores, lane 0's boxes);
+            // the CTA's last warp to finish the phase arrives for it
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            __threadfence();
+            __syncwarp();
+            if (lane == 0 && i + 1 < phases) {
+                if (atomicAdd(done, 1u) % kEpiWarps == kEpiWarps - 1) {
+                    __threadfence();
+                    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.sync) : "memory");
+                }
             }
-        };
-        int acc = 0, pending = 0;   // pending: slots (bits) whose loads have not been waited for
-        uint32_t acc_phase = 0, in_phase = 0;
-        if (kLoads > 0 && pair_id < num_tiles) {
-            if (lane == 0) {
-                load_chunk(pair_id, 0);
-                load_chunk(pair_id, 1);
-            }
-            pending = 3;
-        }
-        bool alive = true;
-        for (int t = pair_id; t < num_tiles && alive; t += num_pairs) {
-            int b, m0, n0;
-            locate(t, b, m0, n0);
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull_bar[acc], acc_phase, ctl, DG_DEV_TIMEOUT))) break;
-            tc_fence_after_sync();
-            const int row0 = m0 + row_off, row = row0 + static_cast<int>(lane);
-            const bool mirror = SYM && m0 != n0;
-            // the row's entry of A's or B's diagonal
-            float diag = 0.f;
-            if (MODE != kNsGram && row < rows) diag = __ldcg((MODE == kNsPoly ? p.da : p.db) + static_cast<int64_t>(b) * p.lo + row);
-#pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-                const int s = j & 1, col = n0 + col_off + 32 * j;
-                uint8_t *box0 = slots + s * kSlotBytes, *box1 = box0 + kBoxBytes;
-                uint32_t v[2][16];
-                const uint32_t at = tmem_base + ((quad * 32) << 16) + acc * kTile + half * 128 + 32 * j;
-                tmem_ld_32x32b_x16(at, v[0]);
-                tmem_ld_32x32b_x16(at + 16, v[1]);
-                if constexpr (kLoads > 0) {
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&landed[s], (in_phase >> s) & 1u, ctl, DG_DEV_TIMEOUT))) {
-                        alive = false;
-                        break;
-                    }
-                    in_phase ^= 1u << s;
-                    pending &= ~(1 << s);
-                }
-                tmem_ld_wait();
-                reg_fence16(v[0]);
-                reg_fence16(v[1]);
-                if (j == 3) {   // the accumulator has been read
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(leader_tempty + acc * 8);
-                }
-                const bool in = row0 < rows && col < cols;   // (else nothing of the chunk is stored)
-                if constexpr (kLoads == 0) {
-                    // the slot's stores have read it (the other slot's may still run)
-                    if (lane == 0) bulk_wait_group_read<1>();
-                    __syncwarp();
-                }
-                // 8 columns at a time, in place: f in units of 2^-12
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const uint32_t *x = v[h >> 1] + 8 * (h & 1);
-                    float f[8];
-                    uint32_t w0[4], w1[4];
-                    if constexpr (kLoads > 0) {
-                        const uint4 q = *unit(box0, lane, h);
-                        w0[0] = q.x; w0[1] = q.y; w0[2] = q.z; w0[3] = q.w;
-                    }
-                    if constexpr (kLoads > 1) {
-                        const uint4 q = *unit(box1, lane, h);
-                        w1[0] = q.x; w1[1] = q.y; w1[2] = q.z; w1[3] = q.w;
-                    }
-                    if constexpr (MODE == kNsGram) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(x[i]) * (1.0f / kScale);
-                    } else if constexpr (MODE == kNsPoly) {
-                        float dc[8];
-                        const float *d = p.da + static_cast<int64_t>(b) * p.lo + col + 8 * h;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dc[i] = col + 8 * h + i < cols ? __ldcg(d + i) : 0.f;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 r = half2_values(w0[i]);
-                            f[2 * i] = fmaf(fmaf(p.cc, diag + dc[2 * i], p.cb), r.x, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i]));
-                            f[2 * i + 1] = fmaf(fmaf(p.cc, diag + dc[2 * i + 1], p.cb), r.y, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 hi = half2_values(w0[i]), lo = half2_values(w1[i]);
-                            f[2 * i] = fmaf(p.ca + diag, hi.x + lo.x, (1.0f / kScale) * __uint_as_float(x[2 * i]));
-                            f[2 * i + 1] = fmaf(p.ca + diag, hi.y + lo.y, (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
-                        }
-                    }
-                    if constexpr (SYM) {
-                        // the diagonal goes out in FP32 (as it is, not scaled)
-                        const int on = row - (col + 8 * h);
-                        if (m0 == n0 && on >= 0 && on < 8) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (i == on) {
-                                    const float dv = f[i] * (1.0f / kScale);
-                                    if (row < rows)
-                                        (MODE == kNsGram ? p.da : p.db)[static_cast<int64_t>(b) * p.lo + row] =
-                                            MODE == kNsGram ? dv : fmaf(diag, fmaf(p.cc, diag, p.cb), dv);
-                                    f[i] = 0.f;
-                                }
-                        }
-                    }
-                    if constexpr (MODE == kNsLast) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] *= 1.0f / kScale;
-                        if (!p.out_tma) {
-                            // rows that TMA cannot address: element by element
-                            uint16_t *out = p.out + b * p.out_batch;
-                            const bool tall = p.rows > p.cols;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int c = col + 8 * h + i;
-                                if (row >= rows || c >= cols) continue;
-                                const __nv_bfloat16 o = __float2bfloat16_rn(f[i]);
-                                out[tall ? static_cast<int64_t>(c) * p.ldo + row : static_cast<int64_t>(row) * p.ldo + c] =
-                                    *reinterpret_cast<const uint16_t *>(&o);
-                            }
-                        } else if (p.rows > p.cols) {
-                            // (box1: every lane has read its own unit h of the low plane, the others not;
-                            // the transposed box is written once all have, below)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) v[h >> 1][8 * (h & 1) + i] = __float_as_uint(f[i]);
-                        } else {
-                            uint32_t o[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                                o[i] = *reinterpret_cast<const uint32_t *>(&b2);
-                            }
-                            *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
-                        }
-                    } else if constexpr (MODE == kNsUpdate) {
-                        uint32_t o[4], l[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) split2(f[2 * i], f[2 * i + 1], o[i], l[i]);
-                        *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *unit(box1, lane, h) = make_uint4(l[0], l[1], l[2], l[3]);
-                    } else {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[i] = half2_bits(f[2 * i], f[2 * i + 1]);
-                        *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (mirror) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const uint16_t e = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
-                                *reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(unit(box1, 8 * h + i, lane >> 3)) + 2 * (lane & 7)) = e;
-                            }
-                        }
-                    }
-                }
-                if constexpr (MODE == kNsLast) {
-                    if (p.out_tma && p.rows > p.cols) {
-                        __syncwarp();
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(v[c >> 4][c & 15]));
-                            *reinterpret_cast<__nv_bfloat16 *>(reinterpret_cast<uint8_t *>(unit(box0, c, lane >> 3)) + 2 * (lane & 7)) = o;
-                        }
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (in && (MODE != kNsLast || p.out_tma)) {
-                        if (MODE == kNsLast && p.rows > p.cols) {
-                            tma_store_3d(&tm_out0, box0, row0, col, b);
-                        } else {
-                            tma_store_3d(&tm_out0, box0, col, row0, b);
-                            if (MODE == kNsUpdate) tma_store_3d(&tm_out1, box1, col, row0, b);
-                            if (mirror) tma_store_3d(&tm_out0, box1, row0, col, b);
-                        }
-                    }
-                    bulk_commit_group();
-                    if constexpr (kLoads > 0) {
-                        bulk_wait_group_read<0>();
-                        // two chunks on: of this tile, or of this pair's next
-                        load_chunk(j < 2 ? t : t + num_pairs, j < 2 ? j + 2 : j - 2);
-                    }
-                }
-                if (kLoads > 0 && (j < 2 || t + num_pairs < num_tiles)) pending |= 1 << s;
-                __syncwarp();
-            }
-            if (++acc == 2) { acc = 0; acc_phase ^= 1; }
         }
         // (an aborted loop leaves no load landing in shared memory after the CTA is gone)
         if (lane == 0) {
             for (int s = 0; s < 2; ++s)
-                if (pending & (1 << s)) mbar_wait_drain(&landed[s], (in_phase >> s) & 1u, ctl);
+                if (st.pending & (1 << s)) mbar_wait_drain(&st.landed[s], (st.in_phase >> s) & 1u, ctl);
             bulk_wait_group<0>();
         }
         __syncwarp();
     }
+    // a CTA that gave up tells the others
+    if (lane == 0 && *abort_flag) atomicOr(p.sync + 1, 1u);
     tc_fence_before_sync();
     __syncthreads();
     cluster_sync();
@@ -638,7 +763,6 @@ bool encode_plane(CUtensorMap *map, const uint16_t *base, int64_t cols, int64_t 
 }
 
 // Co-resident CTA pairs on the current device, at most num_sms / 2.
-template <int MODE>
 int max_pairs(int num_sms) {
     static std::mutex mu;
     static int cache[64];
@@ -647,6 +771,8 @@ int max_pairs(int num_sms) {
     std::lock_guard<std::mutex> lock(mu);
     int &v = cache[dev];
     if (v == 0) {
+        if (cudaFuncSetAttribute(dg_ns_products_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+            return 0;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -658,32 +784,9 @@ int max_pairs(int num_sms) {
         cfg.dynamicSmemBytes = kSmem;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&v, dg_ns_gemm_kernel<MODE>, &cfg) != cudaSuccess) v = 0;
+        if (cudaOccupancyMaxActiveClusters(&v, dg_ns_products_kernel, &cfg) != cudaSuccess) v = 0;
     }
     return v * 2 > num_sms ? num_sms / 2 : v;
-}
-
-template <int MODE>
-cudaError_t launch_product(const NsParams &p, const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &in0,
-                           const CUtensorMap &in1, const CUtensorMap &out0, const CUtensorMap &out1, int k, int num_sms,
-                           cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(dg_ns_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    const int64_t tm = up(p.lo, kTile) / kTile, tn = up(p.hi, kTile) / kTile;
-    const int64_t tiles = (MODE >= kNsUpdate ? tm * tn : tm * (tm + 1) / 2) * p.batch;
-    const int pairs = max_pairs<MODE>(num_sms);
-    if (pairs <= 0) return cudaErrorInvalidConfiguration;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(2 * static_cast<int>(tiles < pairs ? tiles : pairs));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dg_ns_gemm_kernel<MODE>, a, b, in0, in1, out0, out1, p, k);
 }
 
 cudaError_t launch_simple(void (*kernel)(NsParams), dim3 grid, const NsParams &p, cudaStream_t stream) {
@@ -703,11 +806,11 @@ constexpr int kMaxPartial = 304;
 
 }  // namespace
 
-// Two high planes, the low plane, A and B, their diagonals, the norm's partial sums; rows of whole 64-element
+// Two high planes, the low plane, A and B, their diagonals, the norm's partial sums, the grid's counter; rows of whole 64-element
 // (128-byte) lines.
 int64_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
     const int64_t lo = rows < cols ? rows : cols, hi = rows < cols ? cols : rows;
-    return batch * (2 * lo * (3 * up(hi, 64) + 2 * up(lo, 64)) + 8 * kMaxPartial + 8 * up(lo, 4));
+    return batch * (2 * lo * (3 * up(hi, 64) + 2 * up(lo, 64)) + 8 * kMaxPartial + 8 * up(lo, 4)) + 128;
 }
 
 cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, cudaStream_t stream, int *launches) {
@@ -723,6 +826,7 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
     p.xl = take(plane);
     p.a = take(square);
     p.b = take(square);
+    p.sync = reinterpret_cast<uint32_t *>(take(128));
     p.partial = reinterpret_cast<double *>(take(8ll * kMaxPartial * p.batch));
     p.da = reinterpret_cast<float *>(take(4 * up(p.lo, 4) * p.batch));
     p.db = reinterpret_cast<float *>(w);
@@ -738,40 +842,42 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
     else
         e = launch_simple(bf16 ? dg_ns_split_kernel<true, false> : dg_ns_split_kernel<false, false>,
                           dim3((p.cols + 2047) / 2048, (p.rows + 7) / 8, p.batch), p, stream);
-    *launches = 2 + 3 * steps;
+    if (e != cudaSuccess) return e;
+    *launches = 3;
     // operands: X along K (Gram), X as [K][N], A and B; epilogue boxes of the planes, A, B and the output
-    CUtensorMap xk[2], xn[2], a, b, xh[2], xl, ea, eb, eo;
+    NsMaps maps;
     const int64_t px = p.lo * p.ldx, pa = p.lo * p.lda;
     bool ok = true;
     for (int i = 0; i < 2; ++i)
-        ok &= encode_plane(&xk[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, 128) &&
-              encode_plane(&xn[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, kKBlock) &&
-              encode_plane(&xh[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, 32);
-    ok &= encode_plane(&xl, p.xl, p.hi, p.lo, p.ldx, px, p.batch, 32) &&
-          encode_plane(&a, p.a, p.lo, p.lo, p.lda, pa, p.batch, 128) &&
-          encode_plane(&b, p.b, p.lo, p.lo, p.lda, pa, p.batch, 128) &&
-          encode_plane(&ea, p.a, p.lo, p.lo, p.lda, pa, p.batch, 32) &&
-          encode_plane(&eb, p.b, p.lo, p.lo, p.lda, pa, p.batch, 32);
+        ok &= encode_plane(&maps.xk[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, 128) &&
+              encode_plane(&maps.xn[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, kKBlock) &&
+              encode_plane(&maps.xh[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, 32);
+    ok &= encode_plane(&maps.xl, p.xl, p.hi, p.lo, p.ldx, px, p.batch, 32) &&
+          encode_plane(&maps.a, p.a, p.lo, p.lo, p.lda, pa, p.batch, 128) &&
+          encode_plane(&maps.b, p.b, p.lo, p.lo, p.lda, pa, p.batch, 128) &&
+          encode_plane(&maps.ea, p.a, p.lo, p.lo, p.lda, pa, p.batch, 32) &&
+          encode_plane(&maps.eb, p.b, p.lo, p.lo, p.lda, pa, p.batch, 32);
     if (!ok) return cudaErrorInvalidValue;
     // the output by TMA where its rows (and matrices) start on 16 bytes
     p.out_tma = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && p.ldo % 8 == 0 && (p.batch == 1 || p.out_batch % 8 == 0) &&
-                encode_plane(&eo, p.out, p.cols, p.rows, p.ldo, p.batch == 1 ? p.ldo * p.rows : p.out_batch, p.batch, 32);
-    if (!p.out_tma) eo = ea;   // not used
-    int cur = 0;
-    uint16_t *planes[2] = {p.xh[0], p.xh[1]};
-    for (int s = 0; s < steps && e == cudaSuccess; ++s) {
-        p.xh[0] = planes[cur];
-        p.xh[1] = planes[cur ^ 1];
-        e = launch_product<kNsGram>(p, xk[cur], xk[cur], ea, ea, ea, ea, p.hi, num_sms, stream);
-        if (e == cudaSuccess) e = launch_product<kNsPoly>(p, a, a, ea, ea, eb, eb, p.lo, num_sms, stream);
-        if (e == cudaSuccess)
-            e = s + 1 < steps
-                    ? launch_product<kNsUpdate>(p, b, xn[cur], xh[cur], xl, xh[cur ^ 1], xl, p.lo, num_sms, stream)
-                    : launch_product<kNsLast>(p, b, xn[cur], xh[cur], xl, eo, eo, p.lo, num_sms, stream);
-        p.debug_flags = 0;
-        cur ^= 1;
-    }
-    return e;
+                encode_plane(&maps.out, p.out, p.cols, p.rows, p.ldo, p.batch == 1 ? p.ldo * p.rows : p.out_batch, p.batch, 32);
+    if (!p.out_tma) maps.out = maps.ea;   // not used
+    p.steps = steps;
+    // tiles of the phase that has most: no more pairs than that
+    const int64_t tm = up(p.lo, kTile) / kTile, tiles = tm * (up(p.hi, kTile) / kTile) * p.batch;
+    const int pairs = max_pairs(num_sms);
+    if (pairs <= 0) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;   // the CTAs wait for one another
+    attr[0].val.cooperative = 1;
+    cfg.gridDim = dim3(2 * static_cast<int>(tiles < pairs ? tiles : pairs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, dg_ns_products_kernel, maps, p);
 }
 
 }  // namespace dg

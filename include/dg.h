@@ -641,7 +641,7 @@ dg_status dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(const void *dy, int
  *   workspace   device memory, 128-byte aligned, dg_newton_schulz_workspace_bytes(batch, rows,
  *         cols) bytes (-1 for sizes that the call refuses); needs no initialisation and
  *         does not outlive the call.  Calls that may run at the same time need one each.
- *   2 + 3 steps launches.
+ *   Three launches, the last a cooperative one over as many SMs as the products have tiles for.
  */
 int64_t dg_newton_schulz_workspace_bytes(int batch, int rows, int cols);
 dg_status dg_newton_schulz(const void *g, int g_fmt, int64_t ldg, int64_t g_batch, void *out, int64_t ldo,
