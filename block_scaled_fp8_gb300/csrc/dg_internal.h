@@ -163,6 +163,7 @@ struct NsParams {
     int lo, hi;             // short and long side: X is [lo][hi]
     int64_t ldx, lda;
     int steps;
+    int bn_sym, bn_update;  // columns of the products' tiles
     uint16_t *xh[2];        // FP16 high planes of X, used in turns
     uint16_t *xl;           // low plane
     uint16_t *a, *b;        // FP16 [batch][lo][lda], 0 on the diagonal

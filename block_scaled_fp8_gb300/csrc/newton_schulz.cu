@@ -257,14 +257,15 @@ __device__ __forceinline__ float2 half2_values(uint32_t w) { return __half22floa
 // producer warps, with a limit).  As launches of their own they cost 7.5 us each however small
 // (64x64, five steps: 127 us).
 struct NsMaps {
-    CUtensorMap xk[2], xn[2];   // X's high planes along K, and as [K][N]
+    CUtensorMap xk[2], xn[2];   // X's high planes along K (128 rows a box), and as [K][N]
     CUtensorMap a, b;           // A, B along K
+    CUtensorMap xkb[2], ab;     // X and A as the second operand of a symmetric product: bn_sym / 2 rows a box
     CUtensorMap xh[2], xl, ea, eb, out;   // boxes of the epilogue
 };
 
 // What a phase works on.
 struct NsPhase {
-    int mode, step, cols, tm, tn, per, num_tiles, nkb;
+    int mode, step, cols, bn, tm, tn, per, num_tiles, nkb;
 };
 
 __device__ __forceinline__ NsPhase ns_phase(const NsParams &p, int i) {
@@ -274,28 +275,32 @@ __device__ __forceinline__ NsPhase ns_phase(const NsParams &p, int i) {
     if (f.mode == kNsUpdate && f.step + 1 == p.steps) f.mode = kNsLast;
     const bool sym = f.mode < kNsUpdate;
     f.cols = sym ? p.lo : p.hi;
+    f.bn = sym ? p.bn_sym : p.bn_update;
     f.tm = (p.lo + kTile - 1) / kTile;
-    f.tn = (f.cols + kTile - 1) / kTile;
-    f.per = sym ? f.tm * (f.tm + 1) / 2 : f.tm * f.tn;
+    f.tn = (f.cols + f.bn - 1) / f.bn;
+    // symmetric: the column tiles of diagonal block q (kTile / bn of them) have row tiles 0..q
+    const int r = kTile / f.bn, q = f.tn / r;
+    f.per = sym ? r * (q * (q + 1) / 2) + (f.tn - r * q) * (q + 1) : f.tm * f.tn;
     f.num_tiles = f.per * p.batch;
     f.nkb = ((f.mode == kNsGram ? p.hi : p.lo) + kKBlock - 1) / kKBlock;
     return f;
 }
 
-// Tile t of a phase: (batch, m, n), the m tiles of a column of tiles first; symmetric: column n has
-// tiles 0..n
+// Tile t of a phase: (batch, m, n), the m tiles of a column of tiles first
 __device__ __forceinline__ void ns_locate(const NsPhase &f, int t, int &b, int &m0, int &n0) {
     b = t / f.per;
-    const int r = t - b * f.per;
+    const int i = t - b * f.per;
     if (f.mode < kNsUpdate) {
-        int n = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
-        while (n * (n + 1) / 2 > r) --n;
-        while ((n + 1) * (n + 2) / 2 <= r) ++n;
-        m0 = (r - n * (n + 1) / 2) * kTile;
-        n0 = n * kTile;
+        const int r = kTile / f.bn, h = i / r;   // q(q+1)/2 <= h < (q+1)(q+2)/2
+        int q = static_cast<int>((sqrtf(8.0f * static_cast<float>(h) + 1.0f) - 1.0f) * 0.5f);
+        while (q * (q + 1) / 2 > h) --q;
+        while ((q + 1) * (q + 2) / 2 <= h) ++q;
+        const int in = i - r * (q * (q + 1) / 2);
+        m0 = in % (q + 1) * kTile;
+        n0 = (r * q + in / (q + 1)) * f.bn;
     } else {
-        m0 = (r % f.tm) * kTile;
-        n0 = (r / f.tm) * kTile;
+        m0 = i % f.tm * kTile;
+        n0 = i / f.tm * f.bn;
     }
 }
 
@@ -323,210 +328,213 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
     const uint32_t lane = st.lane, quad = st.quad, half = st.half;
     const int num_tiles = ph.num_tiles, num_pairs = st.num_pairs, pair_id = st.pair_id;
     const int rows = p.lo, cols = ph.cols;
-            uint8_t *const slots = st.slots;
-            uint64_t *const landed = st.landed;
-            int &acc = st.acc, &pending = st.pending;
-            uint32_t &acc_phase = st.acc_phase, &in_phase = st.in_phase;
-            const int rank = st.rank;
-            const int row_off = rank * 128 + static_cast<int>(quad) * 32, col_off = static_cast<int>(half) * 128;
-            // 16-byte unit h of row r of a box (64-byte swizzle)
-            auto unit = [](uint8_t *box, int r, int h) { return reinterpret_cast<uint4 *>(box + r * 64 + ((h ^ ((r >> 1) & 3)) << 4)); };
-            // chunk j of tile t: the epilogue's operands, into slot j & 1 (j counts on over the tiles)
-            auto load_chunk = [&](int t, int j) {
-                if constexpr (kLoads > 0) {
-                    if (t >= num_tiles) return;
-                    int b, m0, n0;
-                    ns_locate(ph, t, b, m0, n0);
-                    uint8_t *box = slots + (j & 1) * kSlotBytes;
-                    const int x = n0 + col_off + 32 * (j & 3), y = m0 + row_off;
-                    mbar_arrive_expect_tx(&landed[j & 1], kLoads * kBoxBytes);
-                    tma_load_3d(box, tm_in0, &landed[j & 1], x, y, b);
-                    if constexpr (kLoads > 1) tma_load_3d(box + kBoxBytes, tm_in1, &landed[j & 1], x, y, b);
-                }
-            };
-            if (kLoads > 0 && pair_id < num_tiles) {
-                if (lane == 0) {
-                    load_chunk(pair_id, 0);
-                    load_chunk(pair_id, 1);
-                }
-                pending = 3;
-            }
-            for (int t = pair_id; t < num_tiles; t += num_pairs) {
-                int b, m0, n0;
-                ns_locate(ph, t, b, m0, n0);
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&st.tfull_bar[acc], acc_phase, ctl, DG_DEV_TIMEOUT))) return false;
-                tc_fence_after_sync();
-                const int row0 = m0 + row_off, row = row0 + static_cast<int>(lane);
-                const bool mirror = SYM && m0 != n0;
-                // the row's entry of A's or B's diagonal
-                float diag = 0.f;
-                if (MODE != kNsGram && row < rows) diag = __ldcg((MODE == kNsPoly ? p.da : p.db) + static_cast<int64_t>(b) * p.lo + row);
+    uint8_t *const slots = st.slots;
+    uint64_t *const landed = st.landed;
+    int &acc = st.acc, &pending = st.pending;
+    uint32_t &acc_phase = st.acc_phase, &in_phase = st.in_phase;
+    const int rank = st.rank;
+    const int row_off = rank * 128 + static_cast<int>(quad) * 32, col_off = static_cast<int>(half) * (ph.bn / 2);
+    const int chunks = ph.bn / 64;   // of 32 columns, a tile and warp
+    // 16-byte unit h of row r of a box (64-byte swizzle)
+    auto unit = [](uint8_t *box, int r, int h) { return reinterpret_cast<uint4 *>(box + r * 64 + ((h ^ ((r >> 1) & 3)) << 4)); };
+    // chunk c of this pair in this phase (chunk c % chunks of its tile c / chunks): the epilogue's operands, into
+    // slot c & 1; nothing past the last
+    const int my_chunks = pair_id < num_tiles ? (num_tiles - pair_id + num_pairs - 1) / num_pairs * chunks : 0;
+    auto load_chunk = [&](int c) {
+        if constexpr (kLoads > 0) {
+            if (c >= my_chunks) return;
+            int b, m0, n0;
+            ns_locate(ph, pair_id + c / chunks * num_pairs, b, m0, n0);
+            uint8_t *box = slots + (c & 1) * kSlotBytes;
+            const int x = n0 + col_off + 32 * (c % chunks), y = m0 + row_off;
+            mbar_arrive_expect_tx(&landed[c & 1], kLoads * kBoxBytes);
+            tma_load_3d(box, tm_in0, &landed[c & 1], x, y, b);
+            if constexpr (kLoads > 1) tma_load_3d(box + kBoxBytes, tm_in1, &landed[c & 1], x, y, b);
+        }
+    };
+    if (kLoads > 0) {
+        if (lane == 0) {
+            load_chunk(0);
+            load_chunk(1);
+        }
+        pending = my_chunks >= 2 ? 3 : my_chunks;
+    }
+    int c = 0;
+    for (int t = pair_id; t < num_tiles; t += num_pairs) {
+        int b, m0, n0;
+        ns_locate(ph, t, b, m0, n0);
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&st.tfull_bar[acc], acc_phase, ctl, DG_DEV_TIMEOUT))) return false;
+        tc_fence_after_sync();
+        const int row0 = m0 + row_off, row = row0 + static_cast<int>(lane);
+        const bool mirror = SYM && n0 >= m0 + kTile;   // (beside the diagonal's block of rows)
+        // the row's entry of A's or B's diagonal
+        float diag = 0.f;
+        if (MODE != kNsGram && row < rows) diag = __ldcg((MODE == kNsPoly ? p.da : p.db) + static_cast<int64_t>(b) * p.lo + row);
     #pragma unroll 1
-                for (int j = 0; j < 4; ++j) {
-                    const int s = j & 1, col = n0 + col_off + 32 * j;
-                    uint8_t *box0 = slots + s * kSlotBytes, *box1 = box0 + kBoxBytes;
-                    uint32_t v[2][16];
-                    const uint32_t at = st.tmem_base + ((quad * 32) << 16) + acc * kTile + half * 128 + 32 * j;
-                    tmem_ld_32x32b_x16(at, v[0]);
-                    tmem_ld_32x32b_x16(at + 16, v[1]);
-                    if constexpr (kLoads > 0) {
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&landed[s], (in_phase >> s) & 1u, ctl, DG_DEV_TIMEOUT)))
-                            return false;
-                        in_phase ^= 1u << s;
-                        pending &= ~(1 << s);
-                    }
-                    tmem_ld_wait();
-                    reg_fence16(v[0]);
-                    reg_fence16(v[1]);
-                    if (j == 3) {   // the accumulator has been read
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_remote(st.leader_tempty + acc * 8);
-                    }
-                    const bool in = row0 < rows && col < cols;   // (else nothing of the chunk is stored)
-                    if constexpr (kLoads == 0) {
-                        // the slot's stores have read it (the other slot's may still run)
-                        if (lane == 0) bulk_wait_group_read<1>();
-                        __syncwarp();
-                    }
-                    // 8 columns at a time, in place: f in units of 2^-12
-    #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const uint32_t *x = v[h >> 1] + 8 * (h & 1);
-                        float f[8];
-                        uint32_t w0[4], w1[4];
-                        if constexpr (kLoads > 0) {
-                            const uint4 q = *unit(box0, lane, h);
-                            w0[0] = q.x; w0[1] = q.y; w0[2] = q.z; w0[3] = q.w;
-                        }
-                        if constexpr (kLoads > 1) {
-                            const uint4 q = *unit(box1, lane, h);
-                            w1[0] = q.x; w1[1] = q.y; w1[2] = q.z; w1[3] = q.w;
-                        }
-                        if constexpr (MODE == kNsGram) {
-    #pragma unroll
-                            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(x[i]) * (1.0f / kScale);
-                        } else if constexpr (MODE == kNsPoly) {
-                            float dc[8];
-                            const float *d = p.da + static_cast<int64_t>(b) * p.lo + col + 8 * h;
-    #pragma unroll
-                            for (int i = 0; i < 8; ++i) dc[i] = col + 8 * h + i < cols ? __ldcg(d + i) : 0.f;
-    #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 r = half2_values(w0[i]);
-                                f[2 * i] = fmaf(fmaf(p.cc, diag + dc[2 * i], p.cb), r.x, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i]));
-                                f[2 * i + 1] = fmaf(fmaf(p.cc, diag + dc[2 * i + 1], p.cb), r.y, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
-                            }
-                        } else {
-    #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 hi = half2_values(w0[i]), lo = half2_values(w1[i]);
-                                f[2 * i] = fmaf(p.ca + diag, hi.x + lo.x, (1.0f / kScale) * __uint_as_float(x[2 * i]));
-                                f[2 * i + 1] = fmaf(p.ca + diag, hi.y + lo.y, (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
-                            }
-                        }
-                        if constexpr (SYM) {
-                            // the diagonal goes out in FP32 (as it is, not scaled)
-                            const int on = row - (col + 8 * h);
-                            if (m0 == n0 && on >= 0 && on < 8) {
-    #pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    if (i == on) {
-                                        const float dv = f[i] * (1.0f / kScale);
-                                        if (row < rows)
-                                            (MODE == kNsGram ? p.da : p.db)[static_cast<int64_t>(b) * p.lo + row] =
-                                                MODE == kNsGram ? dv : fmaf(diag, fmaf(p.cc, diag, p.cb), dv);
-                                        f[i] = 0.f;
-                                    }
-                            }
-                        }
-                        if constexpr (MODE == kNsLast) {
-    #pragma unroll
-                            for (int i = 0; i < 8; ++i) f[i] *= 1.0f / kScale;
-                            if (!p.out_tma) {
-                                // rows that TMA cannot address: element by element
-                                uint16_t *out = p.out + b * p.out_batch;
-                                const bool tall = p.rows > p.cols;
-    #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const int c = col + 8 * h + i;
-                                    if (row >= rows || c >= cols) continue;
-                                    const __nv_bfloat16 o = __float2bfloat16_rn(f[i]);
-                                    out[tall ? static_cast<int64_t>(c) * p.ldo + row : static_cast<int64_t>(row) * p.ldo + c] =
-                                        *reinterpret_cast<const uint16_t *>(&o);
-                                }
-                            } else if (p.rows > p.cols) {
-                                // (box1: every lane has read its own unit h of the low plane, the others not;
-                                // the transposed box is written once all have, below)
-    #pragma unroll
-                                for (int i = 0; i < 8; ++i) v[h >> 1][8 * (h & 1) + i] = __float_as_uint(f[i]);
-                            } else {
-                                uint32_t o[4];
-    #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                                    o[i] = *reinterpret_cast<const uint32_t *>(&b2);
-                                }
-                                *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
-                            }
-                        } else if constexpr (MODE == kNsUpdate) {
-                            uint32_t o[4], l[4];
-    #pragma unroll
-                            for (int i = 0; i < 4; ++i) split2(f[2 * i], f[2 * i + 1], o[i], l[i]);
-                            *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *unit(box1, lane, h) = make_uint4(l[0], l[1], l[2], l[3]);
-                        } else {
-                            uint32_t o[4];
-    #pragma unroll
-                            for (int i = 0; i < 4; ++i) o[i] = half2_bits(f[2 * i], f[2 * i + 1]);
-                            *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
-                            if (mirror) {
-    #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const uint16_t e = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
-                                    *reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(unit(box1, 8 * h + i, lane >> 3)) + 2 * (lane & 7)) = e;
-                                }
-                            }
-                        }
-                    }
-                    if constexpr (MODE == kNsLast) {
-                        if (p.out_tma && p.rows > p.cols) {
-                            __syncwarp();
-    #pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(v[c >> 4][c & 15]));
-                                *reinterpret_cast<__nv_bfloat16 *>(reinterpret_cast<uint8_t *>(unit(box0, c, lane >> 3)) + 2 * (lane & 7)) = o;
-                            }
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (in && (MODE != kNsLast || p.out_tma)) {
-                            if (MODE == kNsLast && p.rows > p.cols) {
-                                tma_store_3d(tm_out0, box0, row0, col, b);
-                            } else {
-                                tma_store_3d(tm_out0, box0, col, row0, b);
-                                if (MODE == kNsUpdate) tma_store_3d(tm_out1, box1, col, row0, b);
-                                if (mirror) tma_store_3d(tm_out0, box1, row0, col, b);
-                            }
-                        }
-                        bulk_commit_group();
-                        if constexpr (kLoads > 0) {
-                            bulk_wait_group_read<0>();
-                            // two chunks on: of this tile, or of this pair's next
-                            load_chunk(j < 2 ? t : t + num_pairs, j < 2 ? j + 2 : j - 2);
-                        }
-                    }
-                    if (kLoads > 0 && (j < 2 || t + num_pairs < num_tiles)) pending |= 1 << s;
-                    __syncwarp();
-                }
-                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+        for (int j = 0; j < chunks; ++j, ++c) {
+            const int s = c & 1, col = n0 + col_off + 32 * j;
+            uint8_t *box0 = slots + s * kSlotBytes, *box1 = box0 + kBoxBytes;
+            uint32_t v[2][16];
+            const uint32_t at = st.tmem_base + ((quad * 32) << 16) + acc * kTile + col_off + 32 * j;
+            tmem_ld_32x32b_x16(at, v[0]);
+            tmem_ld_32x32b_x16(at + 16, v[1]);
+            if constexpr (kLoads > 0) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(&landed[s], (in_phase >> s) & 1u, ctl, DG_DEV_TIMEOUT)))
+                    return false;
+                in_phase ^= 1u << s;
+                pending &= ~(1 << s);
             }
-            // the phase's results are in memory before its arrival
-            if (lane == 0) bulk_wait_group<0>();
+            tmem_ld_wait();
+            reg_fence16(v[0]);
+            reg_fence16(v[1]);
+            if (j == chunks - 1) {   // the accumulator has been read
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(st.leader_tempty + acc * 8);
+            }
+            const bool in = row0 < rows && col < cols;   // (else nothing of the chunk is stored)
+            if constexpr (kLoads == 0) {
+                // the slot's stores have read it (the other slot's may still run)
+                if (lane == 0) bulk_wait_group_read<1>();
+                __syncwarp();
+            }
+            // 8 columns at a time, in place: f in units of 2^-12
+    #pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const uint32_t *x = v[h >> 1] + 8 * (h & 1);
+                float f[8];
+                uint32_t w0[4], w1[4];
+                if constexpr (kLoads > 0) {
+                    const uint4 q = *unit(box0, lane, h);
+                    w0[0] = q.x; w0[1] = q.y; w0[2] = q.z; w0[3] = q.w;
+                }
+                if constexpr (kLoads > 1) {
+                    const uint4 q = *unit(box1, lane, h);
+                    w1[0] = q.x; w1[1] = q.y; w1[2] = q.z; w1[3] = q.w;
+                }
+                if constexpr (MODE == kNsGram) {
+    #pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(x[i]) * (1.0f / kScale);
+                } else if constexpr (MODE == kNsPoly) {
+                    float dc[8];
+                    const float *d = p.da + static_cast<int64_t>(b) * p.lo + col + 8 * h;
+    #pragma unroll
+                    for (int i = 0; i < 8; ++i) dc[i] = col + 8 * h + i < cols ? __ldcg(d + i) : 0.f;
+    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 r = half2_values(w0[i]);
+                        f[2 * i] = fmaf(fmaf(p.cc, diag + dc[2 * i], p.cb), r.x, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i]));
+                        f[2 * i + 1] = fmaf(fmaf(p.cc, diag + dc[2 * i + 1], p.cb), r.y, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
+                    }
+                } else {
+    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 hi = half2_values(w0[i]), lo = half2_values(w1[i]);
+                        f[2 * i] = fmaf(p.ca + diag, hi.x + lo.x, (1.0f / kScale) * __uint_as_float(x[2 * i]));
+                        f[2 * i + 1] = fmaf(p.ca + diag, hi.y + lo.y, (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
+                    }
+                }
+                if constexpr (SYM) {
+                    // the diagonal goes out in FP32 (as it is, not scaled)
+                    const int on = row - (col + 8 * h);
+                    if (!mirror && on >= 0 && on < 8) {
+    #pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i == on) {
+                                const float dv = f[i] * (1.0f / kScale);
+                                if (row < rows)
+                                    (MODE == kNsGram ? p.da : p.db)[static_cast<int64_t>(b) * p.lo + row] =
+                                        MODE == kNsGram ? dv : fmaf(diag, fmaf(p.cc, diag, p.cb), dv);
+                                f[i] = 0.f;
+                            }
+                    }
+                }
+                if constexpr (MODE == kNsLast) {
+    #pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] *= 1.0f / kScale;
+                    if (!p.out_tma) {
+                        // rows that TMA cannot address: element by element
+                        uint16_t *out = p.out + b * p.out_batch;
+                        const bool tall = p.rows > p.cols;
+    #pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int cc = col + 8 * h + i;
+                            if (row >= rows || cc >= cols) continue;
+                            const __nv_bfloat16 o = __float2bfloat16_rn(f[i]);
+                            out[tall ? static_cast<int64_t>(cc) * p.ldo + row : static_cast<int64_t>(row) * p.ldo + cc] =
+                                *reinterpret_cast<const uint16_t *>(&o);
+                        }
+                    } else if (p.rows > p.cols) {
+                        // (box1: every lane has read its own unit h of the low plane, the others not;
+                        // the transposed box is written once all have, below)
+    #pragma unroll
+                        for (int i = 0; i < 8; ++i) v[h >> 1][8 * (h & 1) + i] = __float_as_uint(f[i]);
+                    } else {
+                        uint32_t o[4];
+    #pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                            o[i] = *reinterpret_cast<const uint32_t *>(&b2);
+                        }
+                        *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                } else if constexpr (MODE == kNsUpdate) {
+                    uint32_t o[4], l[4];
+    #pragma unroll
+                    for (int i = 0; i < 4; ++i) split2(f[2 * i], f[2 * i + 1], o[i], l[i]);
+                    *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *unit(box1, lane, h) = make_uint4(l[0], l[1], l[2], l[3]);
+                } else {
+                    uint32_t o[4];
+    #pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = half2_bits(f[2 * i], f[2 * i + 1]);
+                    *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
+                    if (mirror) {
+    #pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint16_t e = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+                            *reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(unit(box1, 8 * h + i, lane >> 3)) + 2 * (lane & 7)) = e;
+                        }
+                    }
+                }
+            }
+            if constexpr (MODE == kNsLast) {
+                if (p.out_tma && p.rows > p.cols) {
+                    __syncwarp();
+    #pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(v[e >> 4][e & 15]));
+                        *reinterpret_cast<__nv_bfloat16 *>(reinterpret_cast<uint8_t *>(unit(box0, e, lane >> 3)) + 2 * (lane & 7)) = o;
+                    }
+                }
+            }
+            fence_proxy_async_smem();
             __syncwarp();
-            return true;
+            if (lane == 0) {
+                if (in && (MODE != kNsLast || p.out_tma)) {
+                    if (MODE == kNsLast && p.rows > p.cols) {
+                        tma_store_3d(tm_out0, box0, row0, col, b);
+                    } else {
+                        tma_store_3d(tm_out0, box0, col, row0, b);
+                        if (MODE == kNsUpdate) tma_store_3d(tm_out1, box1, col, row0, b);
+                        if (mirror) tma_store_3d(tm_out0, box1, row0, col, b);
+                    }
+                }
+                bulk_commit_group();
+                if constexpr (kLoads > 0) {
+                    bulk_wait_group_read<0>();
+                    load_chunk(c + 2);
+                }
+            }
+            if (kLoads > 0 && c + 2 < my_chunks) pending |= 1 << s;
+            __syncwarp();
+        }
+        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+    }
+    // the phase's results are in memory before its arrival
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+    return true;
 }
 
 // Waits until the counter has come to `target` (all CTAs' arrivals of the phases before); false if
@@ -618,8 +626,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (!__all_sync(0xFFFFFFFFu, ok)) goto prod_done;
             }
             const CUtensorMap *ta = f.mode == kNsGram ? &maps.xk[f.step & 1] : f.mode == kNsPoly ? &maps.a : &maps.b;
-            const CUtensorMap *tb = f.mode == kNsGram ? ta : f.mode == kNsPoly ? ta : &maps.xn[f.step & 1];
+            const CUtensorMap *tb = f.mode == kNsGram ? &maps.xkb[f.step & 1] : f.mode == kNsPoly ? &maps.ab : &maps.xn[f.step & 1];
             const bool b_mn = f.mode >= kNsUpdate;
+            // this CTA's half of the columns: bn / 2 rows of 64 K, or boxes of 64 columns (one swizzle
+            // atom, of which the MMA reads bn / 2 where that is less) x 64 K rows
+            const uint32_t stage = 16384u + (b_mn ? (f.bn == kTile ? 16384u : 8192u) : static_cast<uint32_t>(f.bn) * 64u);
             for (int t = pair_id; t < f.num_tiles; t += num_pairs) {
                 int b, m0, n0;
                 ns_locate(f, t, b, m0, n0);
@@ -631,14 +642,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         if (elect_one()) {
                             const uint32_t fb = leader_full + slot * 8;
                             uint8_t *sa = smem_a + slot * 16384, *sb = smem_b + slot * 16384;
-                            if (leader) mbar_arrive_expect_tx(&full_bar[slot], 2 * kStageBytes);
+                            const int n = n0 + rank * (f.bn / 2);
+                            if (leader) mbar_arrive_expect_tx(&full_bar[slot], 2 * stage);
                             tma_load_3d_pair(sa, ta, fb, kb * kKBlock, m0 + rank * 128, b);
                             if (b_mn) {
-                                // 64 columns (one swizzle atom) x 64 K rows a box
-                                tma_load_3d_pair(sb, tb, fb, n0 + rank * 128, kb * kKBlock, b);
-                                tma_load_3d_pair(sb + 8192, tb, fb, n0 + rank * 128 + 64, kb * kKBlock, b);
+                                tma_load_3d_pair(sb, tb, fb, n, kb * kKBlock, b);
+                                if (f.bn == kTile) tma_load_3d_pair(sb + 8192, tb, fb, n + 64, kb * kKBlock, b);
                             } else {
-                                tma_load_3d_pair(sb, tb, fb, kb * kKBlock, n0 + rank * 128, b);
+                                tma_load_3d_pair(sb, tb, fb, kb * kKBlock, n, b);
                             }
                         }
                         __syncwarp();
@@ -657,13 +668,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (leader) {
             int slot = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            // FP16 x FP16 -> FP32, M = 256, N = 256 (bit 16: B MN-major)
-            constexpr uint32_t idesc_k = (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
             const uint64_t a0 = make_desc_kmajor_sw128(smem_u32(smem_a));
             for (int i = 0; i < phases; ++i) {
                 const NsPhase f = ns_phase(p, i);
                 const bool b_mn = f.mode >= kNsUpdate;
-                const uint32_t idesc = idesc_k | (b_mn ? 1u << 16 : 0u);
+                // FP16 x FP16 -> FP32, M = 256, N = bn (bit 16: B MN-major)
+                const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(f.bn >> 3) << 17) | ((kTile >> 4) << 24) |
+                                       (b_mn ? 1u << 16 : 0u);
                 // (MN-major: the two 64-column atoms 8192 bytes apart, 8 K rows 1024)
                 const uint64_t b0 = b_mn ? make_smem_desc(smem_u32(smem_b), 8192, 1024, kSwizzle128B)
                                          : make_desc_kmajor_sw128(smem_u32(smem_b));
@@ -748,12 +759,11 @@ int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 // 3-D map of planes [batch][rows][ld] of 16-bit values: boxes of 64 elements (128 bytes) x box_rows as
 // operands, of 32 x 32 elements for the epilogue.
 bool encode_plane(CUtensorMap *map, const uint16_t *base, int64_t cols, int64_t rows, int64_t ld, int64_t batch_stride,
-                  int64_t batch, uint32_t box_rows) {
+                  int64_t batch, uint32_t box_rows, bool epi = false) {
     TensorMapEncodeFn fn = host_encode();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(batch_stride) * 2};
-    const bool epi = box_rows == 32;
     const cuuint32_t box[3] = {epi ? 32u : kKBlock, box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<uint16_t *>(base), dims, strides, box, estr,
@@ -787,6 +797,28 @@ int max_pairs(int num_sms) {
         if (cudaOccupancyMaxActiveClusters(&v, dg_ns_products_kernel, &cfg) != cudaSuccess) v = 0;
     }
     return v * 2 > num_sms ? num_sms / 2 : v;
+}
+
+// Columns of a product's tiles: 256, or where those are few, 128 or 64.  A tile's time is modelled as its
+// K-blocks times the cycles of one (the operands' loads set them: 16 KB of rows and 64 bytes
+// a column at about 55 bytes a cycle) and its epilogue (a chunk of 32 columns after another,
+// about 1500 cycles each), which only the last tile of a pair does not hide.
+int choose_bn(const NsParams &p, bool sym, int pairs, int64_t *tiles) {
+    int best = 256;
+    double least = 0.0;
+    for (int bn : {256, 128, 64}) {
+        const int64_t tm = up(p.lo, kTile) / kTile, tn = up(sym ? p.lo : p.hi, bn) / bn, r = kTile / bn, q = tn / r;
+        const int64_t n = (sym ? r * (q * (q + 1) / 2) + (tn - r * q) * (q + 1) : tm * tn) * p.batch;
+        // (symmetric: the mean of the products along the long side and the short)
+        const int64_t nkb = sym ? (up(p.hi, kKBlock) + up(p.lo, kKBlock)) / kKBlock / 2 + 1 : up(p.lo, kKBlock) / kKBlock;
+        const double t = static_cast<double>((n + pairs - 1) / pairs) * nkb * (16384 + 64 * bn) / 55.0 + 1500.0 * (bn / 64);
+        if (bn == 256 || t < 0.95 * least) {
+            best = bn;
+            least = t;
+            *tiles = n;
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_simple(void (*kernel)(NsParams), dim3 grid, const NsParams &p, cudaStream_t stream) {
@@ -845,28 +877,32 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
     if (e != cudaSuccess) return e;
     *launches = 3;
     // operands: X along K (Gram), X as [K][N], A and B; epilogue boxes of the planes, A, B and the output
+    const int pairs = max_pairs(num_sms);
+    if (pairs <= 0) return cudaErrorInvalidConfiguration;
+    int64_t tiles_sym, tiles;
+    p.bn_sym = choose_bn(p, true, pairs, &tiles_sym);
+    p.bn_update = choose_bn(p, false, pairs, &tiles);
+    if (tiles_sym > tiles) tiles = tiles_sym;   // (no more pairs than the phase that has most tiles)
     NsMaps maps;
     const int64_t px = p.lo * p.ldx, pa = p.lo * p.lda;
     bool ok = true;
     for (int i = 0; i < 2; ++i)
         ok &= encode_plane(&maps.xk[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, 128) &&
               encode_plane(&maps.xn[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, kKBlock) &&
-              encode_plane(&maps.xh[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, 32);
-    ok &= encode_plane(&maps.xl, p.xl, p.hi, p.lo, p.ldx, px, p.batch, 32) &&
+              encode_plane(&maps.xkb[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, p.bn_sym / 2) &&
+              encode_plane(&maps.xh[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, 32, true);
+    ok &= encode_plane(&maps.xl, p.xl, p.hi, p.lo, p.ldx, px, p.batch, 32, true) &&
           encode_plane(&maps.a, p.a, p.lo, p.lo, p.lda, pa, p.batch, 128) &&
+          encode_plane(&maps.ab, p.a, p.lo, p.lo, p.lda, pa, p.batch, p.bn_sym / 2) &&
           encode_plane(&maps.b, p.b, p.lo, p.lo, p.lda, pa, p.batch, 128) &&
-          encode_plane(&maps.ea, p.a, p.lo, p.lo, p.lda, pa, p.batch, 32) &&
-          encode_plane(&maps.eb, p.b, p.lo, p.lo, p.lda, pa, p.batch, 32);
+          encode_plane(&maps.ea, p.a, p.lo, p.lo, p.lda, pa, p.batch, 32, true) &&
+          encode_plane(&maps.eb, p.b, p.lo, p.lo, p.lda, pa, p.batch, 32, true);
     if (!ok) return cudaErrorInvalidValue;
     // the output by TMA where its rows (and matrices) start on 16 bytes
     p.out_tma = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && p.ldo % 8 == 0 && (p.batch == 1 || p.out_batch % 8 == 0) &&
-                encode_plane(&maps.out, p.out, p.cols, p.rows, p.ldo, p.batch == 1 ? p.ldo * p.rows : p.out_batch, p.batch, 32);
+                encode_plane(&maps.out, p.out, p.cols, p.rows, p.ldo, p.batch == 1 ? p.ldo * p.rows : p.out_batch, p.batch, 32, true);
     if (!p.out_tma) maps.out = maps.ea;   // not used
     p.steps = steps;
-    // tiles of the phase that has most: no more pairs than that
-    const int64_t tm = up(p.lo, kTile) / kTile, tiles = tm * (up(p.hi, kTile) / kTile) * p.batch;
-    const int pairs = max_pairs(num_sms);
-    if (pairs <= 0) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;   // the CTAs wait for one another
