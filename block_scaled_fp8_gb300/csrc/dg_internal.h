@@ -161,17 +161,17 @@ struct NsParams {
     uint32_t debug_flags;
     // ----
     int lo, hi;             // short and long side: X is [lo][hi]
-    int64_t ldx, lda;
+    int64_t ldx, lda, ldd;
     int steps;
     int bn_sym, bn_update;  // columns of the products' tiles
     uint16_t *xh[2];        // FP16 high planes of X, used in turns
     uint16_t *xl;           // low plane
     uint16_t *a, *b;        // FP16 [batch][lo][lda], 0 on the diagonal
-    float *da, *db;         // their diagonals, FP32 [batch][lo]
+    float *da, *db;         // their diagonals, FP32 [batch][ldd]
     int out_tma;            // the output's rows can be stored by TMA
     double *partial;        // [batch][num_partial] sums of squares
     int num_partial;
-    uint32_t *sync;         // the products' grid counter, and a word that a CTA that gives up sets
+    uint64_t *sync;         // low half: the products' grid counter; high half: set by a CTA that gives up
     int dense;              // a matrix's rows of G follow one another
 };
 int64_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);

@@ -38,7 +38,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kBoxBytes = 32 * 64;
 constexpr int kSlotBytes = 2 * kBoxBytes;
 constexpr int kEpiBytes = kEpiWarps * 2 * kSlotBytes;
-constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiBytes + 512;
+constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiBytes + 128 * kEpiWarps + 512;
 
 // ------------------------------------------------------------------ norm and split
 
@@ -120,7 +120,7 @@ __device__ __forceinline__ void norm_factors(const NsParams &p, int64_t batch, f
         if (threadIdx.x == 0) sum = s;
     }
     // (the products' grid counter and abort word, which follow in the stream)
-    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 2) p.sync[threadIdx.x] = 0u;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.sync = 0u;
     __syncthreads();
     const double norm = sqrt(sum) + static_cast<double>(p.eps);
     int e = 0;
@@ -198,23 +198,53 @@ __global__ void __launch_bounds__(256) dg_ns_split_kernel(const __grid_constant_
             *reinterpret_cast<uint4 *>(p.xl + to) = make_uint4(l[0], l[1], l[2], l[3]);
         }
     } else {
-        const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;   // of G
-#pragma unroll 8
-        for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-            const int r = r0 + i / 64, c = c0 + i % 64;
-            tile[i / 64][i % 64] =
-                r < p.rows && c < p.cols ? g_value<BF16>(g, static_cast<int64_t>(r) * p.ldg + c) * f1 * f2 : 0.f;
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-            const int r = i / 8, c = 8 * (i % 8);               // of X's tile
-            if (c0 + r >= p.lo || r0 + c >= p.hi) continue;
-            uint32_t h[4], l[4];
+        // kTiles tiles of 64x64 down a column of tiles: the factors are worked out once a CTA
+        constexpr int kTiles = 4, V = BF16 ? 8 : 4;
+        const int c0 = blockIdx.x * 64;                         // of G
+        const bool vec = (reinterpret_cast<uintptr_t>(g) & 15u) == 0 && p.ldg % V == 0 && c0 + 64 <= p.cols;
+        for (int i = 0; i < kTiles; ++i) {
+            const int r0 = (static_cast<int>(blockIdx.y) * kTiles + i) * 64;
+            if (r0 >= p.rows) break;
+            if (vec) {
+                constexpr int kPer = 64 / V;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) split2(tile[c + 2 * j][r], tile[c + 2 * j + 1][r], h[j], l[j]);
-            const int64_t to = (batch * p.lo + c0 + r) * p.ldx + r0 + c;
-            *reinterpret_cast<uint4 *>(p.xh[0] + to) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4 *>(p.xl + to) = make_uint4(l[0], l[1], l[2], l[3]);
+                for (int q = threadIdx.x; q < 64 * kPer; q += 256) {
+                    const int r = q / kPer, c = q % kPer * V;
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (r0 + r < p.rows)
+                        x = __ldg(reinterpret_cast<const uint4 *>(g + (static_cast<int64_t>(r0 + r) * p.ldg + c0 + c) * (BF16 ? 2 : 4)));
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (BF16) {
+                            tile[r][c + 2 * j] = __uint_as_float(w[j] << 16) * f1 * f2;
+                            tile[r][c + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * f1 * f2;
+                        } else {
+                            tile[r][c + j] = __uint_as_float(w[j]) * f1 * f2;
+                        }
+                    }
+                }
+            } else {
+#pragma unroll 8
+                for (int q = threadIdx.x; q < 64 * 64; q += 256) {
+                    const int r = r0 + q / 64, c = c0 + q % 64;
+                    tile[q / 64][q % 64] =
+                        r < p.rows && c < p.cols ? g_value<BF16>(g, static_cast<int64_t>(r) * p.ldg + c) * f1 * f2 : 0.f;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int q = threadIdx.x; q < 64 * 8; q += 256) {
+                const int r = q / 8, c = 8 * (q % 8);           // of X's tile
+                if (c0 + r >= p.lo || r0 + c >= p.hi) continue;
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) split2(tile[c + 2 * j][r], tile[c + 2 * j + 1][r], h[j], l[j]);
+                const int64_t to = (batch * p.lo + c0 + r) * p.ldx + r0 + c;
+                *reinterpret_cast<uint4 *>(p.xh[0] + to) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(p.xl + to) = make_uint4(l[0], l[1], l[2], l[3]);
+            }
+            __syncthreads();
         }
     }
 }
@@ -311,6 +341,7 @@ struct NsEpilogue {
     uint32_t ew, quad, half, lane, tmem_base, leader_tempty;
     int rank, pair_id, num_pairs;
     uint8_t *slots;
+    float *diag;        // 32 values on their way out
     uint64_t *landed, *tfull_bar;
     int acc, pending;   // pending: slots (bits) whose loads have not been waited for
     uint32_t acc_phase, in_phase;
@@ -363,14 +394,21 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
     for (int t = pair_id; t < num_tiles; t += num_pairs) {
         int b, m0, n0;
         ns_locate(ph, t, b, m0, n0);
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&st.tfull_bar[acc], acc_phase, ctl, DG_DEV_TIMEOUT))) return false;
-        tc_fence_after_sync();
         const int row0 = m0 + row_off, row = row0 + static_cast<int>(lane);
         const bool mirror = SYM && n0 >= m0 + kTile;   // (beside the diagonal's block of rows)
-        // the row's entry of A's or B's diagonal
-        float diag = 0.f;
-        if (MODE != kNsGram && row < rows) diag = __ldcg((MODE == kNsPoly ? p.da : p.db) + static_cast<int64_t>(b) * p.lo + row);
-    #pragma unroll 1
+        // the row's entry of A's or B's diagonal, and (polynomial) a column's of each chunk by lane
+        float diag = 0.f, dcol[4];
+        if (MODE != kNsGram && row < rows) diag = __ldcg((MODE == kNsPoly ? p.da : p.db) + static_cast<int64_t>(b) * p.ldd + row);
+        if constexpr (MODE == kNsPoly) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int cc = n0 + col_off + 32 * j + static_cast<int>(lane);
+                dcol[j] = j < chunks && cc < cols ? __ldcg(p.da + static_cast<int64_t>(b) * p.ldd + cc) : 0.f;
+            }
+        }
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&st.tfull_bar[acc], acc_phase, ctl, DG_DEV_TIMEOUT))) return false;
+        tc_fence_after_sync();
+#pragma unroll 1
         for (int j = 0; j < chunks; ++j, ++c) {
             const int s = c & 1, col = n0 + col_off + 32 * j;
             uint8_t *box0 = slots + s * kSlotBytes, *box1 = box0 + kBoxBytes;
@@ -392,12 +430,20 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(st.leader_tempty + acc * 8);
             }
+            if constexpr (MODE == kNsPoly) {
+                if (j > 0) {   // (this chunk's columns in the first place)
+                    dcol[0] = dcol[1];
+                    dcol[1] = dcol[2];
+                    dcol[2] = dcol[3];
+                }
+            }
             const bool in = row0 < rows && col < cols;   // (else nothing of the chunk is stored)
             if constexpr (kLoads == 0) {
                 // the slot's stores have read it (the other slot's may still run)
                 if (lane == 0) bulk_wait_group_read<1>();
                 __syncwarp();
             }
+            float on_diag = 0.f;
             // 8 columns at a time, in place: f in units of 2^-12
     #pragma unroll
             for (int h = 0; h < 4; ++h) {
@@ -417,9 +463,8 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
                     for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(x[i]) * (1.0f / kScale);
                 } else if constexpr (MODE == kNsPoly) {
                     float dc[8];
-                    const float *d = p.da + static_cast<int64_t>(b) * p.lo + col + 8 * h;
-    #pragma unroll
-                    for (int i = 0; i < 8; ++i) dc[i] = col + 8 * h + i < cols ? __ldcg(d + i) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dc[i] = __shfl_sync(0xFFFFFFFFu, dcol[0], 8 * h + i);
     #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 r = half2_values(w0[i]);
@@ -435,18 +480,13 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
                     }
                 }
                 if constexpr (SYM) {
-                    // the diagonal goes out in FP32 (as it is, not scaled)
-                    const int on = row - (col + 8 * h);
-                    if (!mirror && on >= 0 && on < 8) {
-    #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (i == on) {
-                                const float dv = f[i] * (1.0f / kScale);
-                                if (row < rows)
-                                    (MODE == kNsGram ? p.da : p.db)[static_cast<int64_t>(b) * p.lo + row] =
-                                        MODE == kNsGram ? dv : fmaf(diag, fmaf(p.cc, diag, p.cb), dv);
-                                f[i] = 0.f;
-                            }
+                    // the diagonal goes out in FP32: the chunk whose columns are the warp's rows has all
+                    // of the warp's, one a lane (taken by selects: branches cost a microsecond here)
+                    const int on = col == row0 ? static_cast<int>(lane) - 8 * h : -1;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        on_diag = i == on ? f[i] : on_diag;
+                        f[i] = i == on ? 0.f : f[i];
                     }
                 }
                 if constexpr (MODE == kNsLast) {
@@ -498,6 +538,10 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
                     }
                 }
             }
+            if constexpr (SYM) {
+                on_diag *= 1.0f / kScale;   // (as it is, not scaled)
+                if (col == row0) st.diag[lane] = MODE == kNsGram ? on_diag : fmaf(diag, fmaf(p.cc, diag, p.cb), on_diag);
+            }
             if constexpr (MODE == kNsLast) {
                 if (p.out_tma && p.rows > p.cols) {
                     __syncwarp();
@@ -518,6 +562,8 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
                         tma_store_3d(tm_out0, box0, col, row0, b);
                         if (MODE == kNsUpdate) tma_store_3d(tm_out1, box1, col, row0, b);
                         if (mirror) tma_store_3d(tm_out0, box1, row0, col, b);
+                        if (SYM && col == row0)   // (rows past lo are padding there)
+                            bulk_store((MODE == kNsGram ? p.da : p.db) + static_cast<int64_t>(b) * p.ldd + row0, st.diag, 128);
                     }
                 }
                 bulk_commit_group();
@@ -537,22 +583,26 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
     return true;
 }
 
-// Waits until the counter has come to `target` (all CTAs' arrivals of the phases before); false if
-// it does not within the limit or some CTA has given up.
+// Waits until the counter (the low half of the word) has come to `target`, all CTAs' arrivals of the
+// phases before; false if it does not within the limit or some CTA has given up (the high half).
 __device__ __noinline__ bool ns_grid_wait(const NsParams &p, uint32_t target, const WaitCtl &ctl) {
     const uint64_t t0 = global_timer_ns();
     while (true) {
-        uint32_t seen, gone;
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(p.sync) : "memory");
-        if (static_cast<int32_t>(seen - target) >= 0) return true;
-        asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(gone) : "l"(p.sync + 1) : "memory");
-        const bool late = global_timer_ns() - t0 > ctl.timeout_ns;
-        if (late && ctl.status) atomicOr(ctl.status, DG_DEV_TIMEOUT);
-        if (gone != 0u || late || *ctl.abort) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i) {
+            uint64_t w;
+            asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(p.sync) : "memory");
+            if (static_cast<int32_t>(static_cast<uint32_t>(w) - target) >= 0) return true;
+            if ((w >> 32) != 0 || *ctl.abort) {
+                *ctl.abort = 1;
+                return false;
+            }
+        }
+        if (global_timer_ns() - t0 > ctl.timeout_ns) {
+            if (ctl.status) atomicOr(ctl.status, DG_DEV_TIMEOUT);
             *ctl.abort = 1;
             return false;
         }
-        __nanosleep(32);
     }
 }
 
@@ -563,7 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                                 ~static_cast<uintptr_t>(1023));
     uint8_t *smem_a = smem, *smem_b = smem + kStages * 16384;
     uint8_t *smem_epi = smem + kStages * kStageBytes;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem_epi + kEpiBytes);
+    float *diag_out = reinterpret_cast<float *>(smem_epi + kEpiBytes);   // 32 an epilogue warp
+    uint64_t *bars = reinterpret_cast<uint64_t *>(diag_out + 32 * kEpiWarps);
     uint64_t *full_bar = bars;                   // [kStages] leader: both CTAs' stages landed
     uint64_t *empty_bar = full_bar + kStages;    // [kStages] both: MMAs done with the stage
     uint64_t *tfull_bar = empty_bar + kStages;   // [2] both: accumulator complete
@@ -591,10 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         fence_mbar_init();
         if (lane == 0) {
-            tma_prefetch_desc(&maps.xk[0]);
-            tma_prefetch_desc(&maps.a);
-            tma_prefetch_desc(&maps.b);
-            tma_prefetch_desc(&maps.xn[0]);
+            const CUtensorMap *m = reinterpret_cast<const CUtensorMap *>(&maps);
+            for (unsigned i = 0; i < sizeof(maps) / sizeof(CUtensorMap); ++i) tma_prefetch_desc(m + i);
         }
     }
     __syncthreads();
@@ -712,10 +761,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     } else {
         const uint32_t ew = warp - 2;
         NsEpilogue st{p, ctl, ew, warp & 3, ew >> 2, lane, tmem_base, mapa_shared(smem_u32(tempty_bar), 0), rank, pair_id,
-                      num_pairs, smem_epi + ew * 2 * kSlotBytes, in_bar + 2 * ew, tfull_bar, 0, 0, 0u, 0u};
+                      num_pairs, smem_epi + ew * 2 * kSlotBytes, diag_out + 32 * ew, in_bar + 2 * ew, tfull_bar, 0, 0, 0u, 0u};
         for (int i = 0; i < phases; ++i) {
             const NsPhase f = ns_phase(p, i);
-            if (i > 0 && !mbar_wait_warp(phase_bar, (i - 1) & 1, ctl, DG_DEV_TIMEOUT)) break;
+            if (i > 0) {
+                if (!mbar_wait_warp(phase_bar, (i - 1) & 1, ctl, DG_DEV_TIMEOUT)) break;
+                asm volatile("fence.proxy.async.global;" ::: "memory");   // (as the producer's)
+            }
             const CUtensorMap *xh = &maps.xh[f.step & 1], *next = &maps.xh[(f.step & 1) ^ 1];
             bool ok;
             if (f.mode == kNsGram) ok = ns_epilogue<kNsGram>(st, f, nullptr, nullptr, &maps.ea, nullptr);
@@ -723,16 +775,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             else if (f.mode == kNsUpdate) ok = ns_epilogue<kNsUpdate>(st, f, xh, &maps.xl, next, &maps.xl);
             else ok = ns_epilogue<kNsLast>(st, f, xh, &maps.xl, &maps.out, nullptr);
             if (!ok) break;
-            // the warp's results are visible to the grid (all lanes' plain stores, lane 0's boxes);
-            // the CTA's last warp to finish the phase arrives for it
-            asm volatile("fence.proxy.async.global;" ::: "memory");
-            __threadfence();
+            // The CTA's last warp to finish the phase arrives for it.  A warp's results (its boxes, complete
+            // since the wait for them, and the lanes' plain stores) are released to the CTA by its count,
+            // and by the last warp's arrival, which has acquired all counts, to the grid: one release
+            // at the grid's scope, which costs about a microsecond, instead of one a warp and another.
             __syncwarp();
             if (lane == 0 && i + 1 < phases) {
-                if (atomicAdd(done, 1u) % kEpiWarps == kEpiWarps - 1) {
-                    __threadfence();
-                    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.sync) : "memory");
-                }
+                uint32_t before;
+                asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(done)) : "memory");
+                if (before % kEpiWarps == kEpiWarps - 1)
+                    asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(p.sync) : "memory");
             }
         }
         // (an aborted loop leaves no load landing in shared memory after the CTA is gone)
@@ -744,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         __syncwarp();
     }
     // a CTA that gave up tells the others
-    if (lane == 0 && *abort_flag) atomicOr(p.sync + 1, 1u);
+    if (lane == 0 && *abort_flag) atomicOr(reinterpret_cast<uint32_t *>(p.sync) + 1, 1u);
     tc_fence_before_sync();
     __syncthreads();
     cluster_sync();
@@ -842,7 +894,7 @@ constexpr int kMaxPartial = 304;
 // (128-byte) lines.
 int64_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
     const int64_t lo = rows < cols ? rows : cols, hi = rows < cols ? cols : rows;
-    return batch * (2 * lo * (3 * up(hi, 64) + 2 * up(lo, 64)) + 8 * kMaxPartial + 8 * up(lo, 4)) + 128;
+    return batch * (2 * lo * (3 * up(hi, 64) + 2 * up(lo, 64)) + 8 * kMaxPartial + 8 * up(lo, 32)) + 128;
 }
 
 cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, cudaStream_t stream, int *launches) {
@@ -858,9 +910,10 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
     p.xl = take(plane);
     p.a = take(square);
     p.b = take(square);
-    p.sync = reinterpret_cast<uint32_t *>(take(128));
+    p.sync = reinterpret_cast<uint64_t *>(take(128));
     p.partial = reinterpret_cast<double *>(take(8ll * kMaxPartial * p.batch));
-    p.da = reinterpret_cast<float *>(take(4 * up(p.lo, 4) * p.batch));
+    p.ldd = up(p.lo, 32);
+    p.da = reinterpret_cast<float *>(take(4 * p.ldd * p.batch));
     p.db = reinterpret_cast<float *>(w);
     p.dense = p.ldg == p.cols;
     const int64_t segs = p.dense ? (static_cast<int64_t>(p.rows) * p.cols + 8191) / 8192 : p.rows * ((p.cols + 8191ll) / 8192);
@@ -870,7 +923,7 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
     const bool tall = p.rows > p.cols;
     if (tall)
         e = launch_simple(bf16 ? dg_ns_split_kernel<true, true> : dg_ns_split_kernel<false, true>,
-                          dim3((p.cols + 63) / 64, (p.rows + 63) / 64, p.batch), p, stream);
+                          dim3((p.cols + 63) / 64, (p.rows + 255) / 256, p.batch), p, stream);
     else
         e = launch_simple(bf16 ? dg_ns_split_kernel<true, false> : dg_ns_split_kernel<false, false>,
                           dim3((p.cols + 2047) / 2048, (p.rows + 7) / 8, p.batch), p, stream);

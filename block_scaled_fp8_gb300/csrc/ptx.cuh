@@ -322,6 +322,14 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
         : "memory");
 }
 
+// Untiled bulk copy from shared to global memory of `bytes` (a multiple of 16, both addresses 16-byte
+// aligned), in the thread's bulk group.
+__device__ __forceinline__ void bulk_store(void *dst, const void *smem_src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+                 "r"(smem_u32(smem_src)), "r"(bytes)
+                 : "memory");
+}
+
 // TMA reduce: the box in shared memory is added element-wise to the tensor in
 // global memory (the addition is done at L2, in the tensor map's type; FP32
 // adds round to nearest even).
