@@ -39,16 +39,43 @@ bool encode_out(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows
                   CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
-// Co-resident CTA pairs of a gated kernel on the current device.
-int gated_pairs(int lay, int num_sms) {
+// Co-resident clusters of a gated kernel on the current device, in num_sms SMs (the cluster's size
+// is that of the kernel: a pair, or forward the pairs that share a group of 128 columns).
+int gated_clusters(int bn, bool backward, int num_sms) {
     static std::mutex mu;
-    static int cache[64][2];
+    static int cache[64][2][3];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     std::lock_guard<std::mutex> lock(mu);
-    int &v = cache[dev][lay == kLayGated ? 0 : 1];
-    if (v == 0) v = bs2_max_active_pairs(256, false, 256, false, lay);
-    return v * 2 > num_sms ? num_sms / 2 : v;
+    int &v = cache[dev][backward ? 1 : 0][bn == 256 ? 0 : bn == 128 ? 1 : 2];
+    if (v == 0) v = bs2_max_active_pairs(bn, false, 256, false, backward ? (kLayGatedBwd | 2) : kLayGated);
+    const int cluster = backward ? 2 : 512 / bn;
+    return v * cluster > num_sms ? num_sms / cluster : v;
+}
+
+// Columns of the tiles.  Forward: 256 (128 gate, 128 up), or where that leaves pairs without a tile 128 or
+// 64, with 2 or 4 pairs to a group of 128 columns of h; a K-block takes what its loads take, 16 KB
+// of rows and 64 bytes a column at about 55 bytes a cycle (64 columns: 0.62 of 256).  Backward: a K-block
+// of B is loaded whole whatever the tile's columns, so 128 only where all its tiles run at once
+// (half the epilogue).
+int gated_block_n(bool backward, int64_t units, int inner, int num_sms) {
+    if (backward) {
+        const int64_t tiles = units * cdiv(inner, 128);
+        return tiles <= gated_clusters(128, true, num_sms) ? 128 : 256;
+    }
+    int best = 256;
+    double least = 0.0;
+    const int64_t groups = units * cdiv(inner, kGran);
+    for (int bn : {256, 128, 64}) {
+        const int clusters = gated_clusters(bn, false, num_sms);
+        if (clusters <= 0) continue;
+        const double t = static_cast<double>(cdiv(groups, clusters)) * (16384 + 64 * bn);
+        if (bn == 256 || t < 0.97 * least) {
+            best = bn;
+            least = t;
+        }
+    }
+    return best;
 }
 
 struct GatedArgs {
@@ -83,10 +110,9 @@ dg_status gated(const GatedArgs &g) {
     if (m == 0 || inner == 0) return DG_OK;
     if (k == 0 || m > kMaxFewSize || inner > kMaxFewSize / 2 || k > kMaxFewSize) return DG_ERR_UNSUPPORTED;
     const int64_t units = cdiv(m, 2 * kBlockM);
-    const int cols = g.backward ? 256 : 128;   // output columns of a tile
-    const int64_t tiles = (g.grouped ? m / kBlockM : units) * cdiv(inner, cols);
+    const int64_t max_units = g.grouped ? m / kBlockM : units;
     const int64_t b_rows = static_cast<int64_t>(g.groups) * (g.backward ? k : 2 * inner);
-    if (tiles > INT32_MAX / 2 || b_rows > INT32_MAX) return DG_ERR_UNSUPPORTED;
+    if (max_units * cdiv(inner, 128) > INT32_MAX / 8 || b_rows > INT32_MAX) return DG_ERR_UNSUPPORTED;
     if (g.grouped && (units > kMaxPairPrefix || g.groups >= 32768)) return DG_ERR_UNSUPPORTED;
     // pointers
     if (!g.a || !g.b || !g.sfa || !g.sfb || (g.grouped && !g.layout)) return DG_ERR_INVALID_ARG;
@@ -120,7 +146,8 @@ dg_status gated(const GatedArgs &g) {
     p.status = g.status;
     p.layout = g.backward ? (kLayGatedBwd | 2) : kLayGated;
     p.num_m_blocks = static_cast<int>(units);
-    p.num_n_blocks = static_cast<int>(cdiv(inner, cols));
+    const int bn = gated_block_n(g.backward, units, inner, sms);
+    p.num_n_blocks = static_cast<int>(cdiv(inner, g.backward ? bn : kGran));
     p.num_k_blocks = static_cast<int>(cdiv(k, kBlockK));
     p.group_m = 8;
     p.timeout_ns = host_timeout_ns();
@@ -150,7 +177,7 @@ dg_status gated(const GatedArgs &g) {
         p.ldhq = g.ldhq;
         p.sfh = static_cast<uint8_t *>(g.sfh);
         p.sfh_ld = static_cast<int>(align4(m));
-        ok &= encode_fp8(&maps.b, g.b, k, b_rows, g.ldb, kBlockM);
+        ok &= encode_fp8(&maps.b, g.b, k, b_rows, g.ldb, static_cast<uint32_t>(bn / 2));
         if (g.h) ok &= encode_out(&maps.d, g.h, inner, m, g.ldh);
         if (g.gu) ok &= encode_out(&maps.c, g.gu, 2 * static_cast<uint64_t>(inner), m, g.ldgu);
         if (!g.h) maps.d = g.gu ? maps.c : maps.a;   // not used
@@ -159,11 +186,12 @@ dg_status gated(const GatedArgs &g) {
     maps.b2 = maps.b;   // not used
     if (!ok) return DG_ERR_CUDA;
     KernelInfo info;
-    const int pairs = gated_pairs(p.layout, sms);
-    if (pairs <= 0 || !get_bs2_kernel_info(256, false, 256, &info, false, p.layout)) return DG_ERR_UNSUPPORTED;
-    const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
-    host_set_last_config(256, 256, info.stages, grid, 2, 1);
-    const cudaError_t e = launch_bs2_gemm(256, 256, maps, p, grid, static_cast<cudaStream_t>(g.stream));
+    const int clusters = gated_clusters(bn, g.backward, sms), cluster = g.backward ? 2 : 512 / bn;
+    if (clusters <= 0 || !get_bs2_kernel_info(bn, false, 256, &info, false, p.layout)) return DG_ERR_UNSUPPORTED;
+    const int64_t tiles = max_units * p.num_n_blocks;
+    const int grid = cluster * static_cast<int>(tiles < clusters ? tiles : clusters);
+    host_set_last_config(256, bn, info.stages, grid, 2, 1);
+    const cudaError_t e = launch_bs2_gemm(bn, 256, maps, p, grid, static_cast<cudaStream_t>(g.stream));
     return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 

@@ -189,13 +189,18 @@ constexpr int kF32StageBufs = 4;
 // The gated backward epilogue: five boxes of 32 rows x 32 bf16 columns per warp (two of gate and up,
 // one of h), two operand stages fewer.
 constexpr int kGatedBwdBufs = 10;
+// The gated forward epilogue: one box of 32 columns per warp.
+constexpr int kGatedBufs = 2;
+// CTAs of a cluster: a pair; gated forward: the pairs whose tiles make up a group of 128 columns of h.
+template <int BN, int LAY>
+constexpr int kBs2Cluster = (LAY & kLayGated) ? 512 / BN : 2;
 // The bf16 C epilogue keeps its C tile in shared memory where the tile's columns
 // are whole 32-column boxes.
 template <int BN, int MP, bool WITH_C, bool F32>
 constexpr bool kCTile = WITH_C && !F32 && MP == 256 && BN % 32 == 0 && BN <= 256;
 template <int BN, int MP, int LAY, bool F32, bool WITH_C = false>
 using Bs2Cfg = Bs2Config<BN, MP, (LAY & 2) != 0, (LAY & 4) != 0,
-                         (LAY & kLayGatedBwd) ? kGatedBwdBufs : F32 ? kF32StageBufs : 0, (LAY & 8) != 0,
+                         (LAY & kLayGatedBwd) ? kGatedBwdBufs : (LAY & kLayGated) ? kGatedBufs : F32 ? kF32StageBufs : 0, (LAY & 8) != 0,
                          kCTile<BN, MP, WITH_C, F32>>;
 
 struct PairTile {
@@ -405,8 +410,10 @@ __device__ __forceinline__ void get_pair_tile(const GemmParams &p, const int *pr
     const int r = t - g * per_group;
     const int u = first + r % gsize;
     const int nb = r / gsize;
-    // (gated: a tile is BN/2 output columns, the gate rows of B and then the up rows)
-    tile.n0 = nb * ((LAY & kLayGated) ? BN / 2 : BN);
+    // (gated: a tile is BN/2 output columns, the gate rows of B and then the up rows; an n-block is the
+    // 128 columns of a cluster's pairs)
+    tile.n0 = nb * ((LAY & kLayGated) ? kGran : BN);
+    if constexpr ((LAY & kLayGated) != 0 && BN < 256) tile.n0 += static_cast<int>(cluster_ctarank() >> 1) * (BN / 2);
     int group = 0;
     tile.zero_tail = 0;
     tile.kb0 = 0;
@@ -559,7 +566,7 @@ __device__ __forceinline__ uint64_t bf16x2_values(uint32_t w) {
 }
 
 template <int BN, bool WITH_C, int MP, bool F32 = false, int LAY = 0>
-__global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims__(kBs2Cluster<BN, LAY>, 1, 1)
     dg_bs2_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
                        const __grid_constant__ CUtensorMap tm_b,
                        const __grid_constant__ CUtensorMap tm_b2,
@@ -579,9 +586,11 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
     constexpr int MMA_M = MP;
     constexpr int ACC = Cfg::kAccCols;
 
-    // gated forward: two tiles' half-row scales (0: zeros) of each epilogue warp's rows, and the
-    // quadrants' barriers
-    __shared__ uint8_t s_scale[(LAY & kLayGated) ? 512 : 1];
+    // gated forward: two tiles' scales (0: zeros) of the rows' parts, a part for each of the warps and
+    // pairs that share a group, and the quadrants' barriers
+    constexpr int kParts = kBs2Cluster<BN, LAY>;
+    __shared__ uint8_t s_scale[(LAY & kLayGated) ? 2 * kParts * 128 : 1];
+    static_assert(!(LAY & kLayGated) || Cfg::kSmemBytes + 2 * kParts * 128 + 64 <= Cfg::kSmemLimit, "static shared memory");
     __shared__ uint64_t s_xbar[(LAY & kLayGated) ? 4 : 1];
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -609,10 +618,16 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
     const uint32_t warp = threadIdx.x >> 5;
     const uint32_t lane = threadIdx.x & 31;
     WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
-    const int rank = static_cast<int>(cluster_ctarank());   // 0 = leader
+    // Pairs of a cluster work on their own, but for the gated forward epilogue's exchange; pair_id counts
+    // clusters then, whose pairs take tiles side by side.
+    constexpr int CL = kBs2Cluster<BN, LAY>;
+    const int cta = static_cast<int>(cluster_ctarank());
+    const int rank = cta & 1;   // 0 = leader
+    const uint32_t pair_base = CL > 2 ? static_cast<uint32_t>(cta & ~1) : 0u;
+    const uint16_t kBoth = static_cast<uint16_t>(0x3u << pair_base), kLeader = static_cast<uint16_t>(0x1u << pair_base);
     const bool leader = rank == 0;
-    const int pair_id = blockIdx.x >> 1;
-    const int num_pairs = gridDim.x >> 1;
+    const int pair_id = blockIdx.x / CL;
+    const int num_pairs = gridDim.x / CL;
     const int groups_per_tile = (p.num_k_blocks + 3) >> 2;
     const int psf_k = groups_per_tile;
 
@@ -625,7 +640,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
             mbar_init(b, b >= tempty_bar && b < tempty_bar + NUM_ACC ? 2 * Cfg::kEpiWarps : 1);
         }
         if constexpr ((LAY & kLayGated) != 0)
-            if (lane < 4) mbar_init(&s_xbar[lane], 2);
+            if (lane < 4) mbar_init(&s_xbar[lane], CL);
         if (lane == 0) *abort_flag = 0;
         fence_mbar_init();
     }
@@ -662,7 +677,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer (both CTAs, whole warp)
-        const uint32_t leader_full = mapa_shared(smem_u32(full_bar), 0);
+        const uint32_t leader_full = mapa_shared(smem_u32(full_bar), pair_base);
         int slot = 0;
         uint32_t phase = 0;
         uint32_t issued = 0;
@@ -832,20 +847,20 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                         } else {
                             for (int j = 0; j < nk; ++j) mma_kb(j);
                         }
-                        tc_commit_pair(&empty_bar[slot], 0x3);
-                        if (group_end) tc_commit_pair(&sf_tfree_bar[sslot], 0x1);
+                        tc_commit_pair(&empty_bar[slot], kBoth);
+                        if (group_end) tc_commit_pair(&sf_tfree_bar[sslot], kLeader);
                     }
                     __syncwarp();
                     if (group_end) ++g;
                     if (++slot == R) { slot = 0; phase ^= 1; }
                 }
-                if (elect_one()) tc_commit_pair(&tfull_bar[acc], 0x3);
+                if (elect_one()) tc_commit_pair(&tfull_bar[acc], kBoth);
                 __syncwarp();
                 if (++acc == NUM_ACC) { acc = 0; acc_phase ^= 1; }
             }
         mma_done:
             if (elect_one()) {
-                tc_commit_pair(&drain_bar[0], 0x1);
+                tc_commit_pair(&drain_bar[0], kLeader);
                 mbar_wait(&drain_bar[0], 0, ctl, DG_DEV_TIMEOUT);
             }
             __syncwarp();
@@ -866,7 +881,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
         constexpr int NW = Cfg::kSfWarps;
         static_assert(NSF % NW == 0, "scale slots per warp");
         const int sw = static_cast<int>(warp) - Cfg::kSfWarp;
-        const uint32_t leader_peer = mapa_shared(smem_u32(sf_peer_bar), 0);
+        const uint32_t leader_peer = mapa_shared(smem_u32(sf_peer_bar), pair_base);
         // groups of 4 K-blocks in tile t: the same for every tile, except in the
         // K-grouped layout, where a tile has its group's K-blocks (maybe none)
         auto tile_groups = [&](int t) -> int {
@@ -931,10 +946,11 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                         for (int c = 0; c < Cfg::kSfbChunks; ++c)
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
-                                // (gated: chunk 0 is the gate rows, chunk 1 the up rows, p.n on)
+                                // (gated: the first half of the columns are gate rows, the second the up
+                                // rows, p.n on)
                                 copy_word(p.sfb_words, p.sfb_ld, p.sfb_slices,
-                                          st.n0 + ((LAY & kLayGated) ? c * p.n : 128 * c) + 32 * q +
-                                              static_cast<int>(lane),
+                                          st.n0 + 128 * c + 32 * q + static_cast<int>(lane) +
+                                              ((LAY & kLayGated) && 128 * c + 32 * q >= BN / 2 ? p.n - BN / 2 : 0),
                                           (B4 || S32) ? st.sfb_y0 + 4 * lj + jj : yb,
                                           128 * Cfg::kSfaKb + 128 * (jj * Cfg::kSfbChunks + c) + 4 * lane + q);
                 } else {
@@ -995,8 +1011,8 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                             tc_cp_64x128b_warpx2_01_23_pair(sfa_tmem + 4 + 4 * jj,
                                                             make_desc_sf_32x128b(smem_u32(sfb_buf + 256 * jj)));
                     }
-                    tc_commit_pair(&sf_ready_bar[tslot], 0x1);
-                    tc_commit_pair(&sf_sfree_bar[slot], 0x3);   // both CTAs may refill the slot
+                    tc_commit_pair(&sf_ready_bar[tslot], kLeader);
+                    tc_commit_pair(&sf_sfree_bar[slot], kBoth);   // both CTAs may refill the slot
                     copied = true;
                 }
             }
@@ -1005,7 +1021,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
     sf_done:
         cp_async_wait<0>();
         if (lane == 0 && leader && copied) {
-            tc_commit_pair(&drain_bar[1 + sw], 0x1);
+            tc_commit_pair(&drain_bar[1 + sw], kLeader);
             mbar_wait(&drain_bar[1 + sw], 0, ctl, DG_DEV_TIMEOUT);
         }
         __syncwarp();
@@ -1017,7 +1033,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
         // the quadrant's 32 rows (offset in this CTA's rows) and D-column offset of its TMEM columns
         const int row_off = MP == 256 ? static_cast<int>(quad) * 32 : static_cast<int>(quad & 1) * 32;
         const int col_off = MP == 256 ? 0 : static_cast<int>(quad >> 1) * (BN / 2);
-        const uint32_t leader_tempty = mapa_shared(smem_u32(tempty_bar), 0);
+        const uint32_t leader_tempty = mapa_shared(smem_u32(tempty_bar), pair_base);
         int acc = 0;
         uint32_t acc_phase = 0;
         uint32_t buf = 0;
@@ -1265,6 +1281,27 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                 }
                 buf = buf + 1 == NB2 ? 0 : buf + 1;
             };
+            // FP32 chunks of 16 columns from `col` on as bf16: in boxes of two, or a lone chunk directly
+            auto store_plane = [&](const CUtensorMap *map, uint16_t *base, int64_t ld, const auto &v, int col, int off) {
+                constexpr int kChunks = static_cast<int>(sizeof(v) / sizeof(v[0]));
+                if constexpr (kChunks == 1) {
+                    const int drow = tile.d_row0 + row_off + static_cast<int>(lane);
+                    if (col < p.n && drow < p.rows) {
+                        uint32_t o[16];
+                        pack_bf16_32(v[0], v[0], o);
+                        uint4 *dp = reinterpret_cast<uint4 *>(base + static_cast<int64_t>(drow) * ld + off + col);
+                        dp[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                        dp[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kChunks; j += 2) {
+                        uint32_t o[16];
+                        pack_bf16_32(v[j], v[j + 1], o);
+                        store_pair(map, base, ld, o, col + 16 * j, off);
+                    }
+                }
+            };
             // bf16 C of this tile into registers (the first tile's once its accumulator is
             // complete, so that its loads do not compete with the first operand loads)
             if constexpr (WITH_C && !F32) {
@@ -1343,7 +1380,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                 }
             }
             if constexpr ((LAY & kLayGated) != 0) {
-                // gated forward: this warp's 64 gate and 64 up columns of its 32 rows, in the
+                // gated forward: this warp's BN/4 gate and BN/4 up columns of its 32 rows, in the
                 // two halves of the accumulator, to registers; the accumulator is released
                 // before any arithmetic, so that the next tile's MMAs wait for the reads alone
                 constexpr int HC = BN / 4;
@@ -1367,14 +1404,8 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                 const int col0 = tile.n0 + static_cast<int>(half) * HC;
                 const bool stores = tile.valid_rows > 0;   // (all rows of a block, or none)
                 if (p.gu != nullptr && stores) {
-#pragma unroll
-                    for (int j = 0; j < HC / 16; j += 2) {
-                        uint32_t o[16];
-                        pack_bf16_32(g[j], g[j + 1], o);
-                        store_pair(&tm_c, p.gu, p.ldgu, o, col0 + 16 * j, 0);
-                        pack_bf16_32(u[j], u[j + 1], o);
-                        store_pair(&tm_c, p.gu, p.ldgu, o, col0 + 16 * j, p.n);
-                    }
+                    store_plane(&tm_c, p.gu, p.ldgu, g, col0, 0);
+                    store_plane(&tm_c, p.gu, p.ldgu, u, col0, p.n);
                 }
                 // h = silu(gate) up, in place of gate
                 float amax_f = 0.f;   // (fmaxf passes NaN over)
@@ -1406,19 +1437,34 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                         }
                 }
                 if (p.hq != nullptr) {
-                    // a row's group of 128 columns is this thread's 64 and its partner's (the other
-                    // warp of the quadrant): its scale is the larger of the halves', which meet in
-                    // shared memory, in slots that alternate by tile, so that one arrival a warp and
-                    // tile is enough
-                    const uint32_t slot = xphase * 256u;
+                    // a row's group of 128 columns is this thread's BN/4 and those of the other warp
+                    // of the quadrant, here and in the cluster's other pairs: its scale is the largest of
+                    // theirs, which meet in each CTA's shared memory, in slots that alternate by tile, so
+                    // that one arrival a warp and tile is enough
+                    const uint32_t row_at = xphase * (kParts * 128u) + quad * 32u + lane;
                     const uint32_t mine = amax == 0u ? 0u : ue8m0_of_amax(amax);
-                    s_scale[slot + ew * 32u + lane] = static_cast<uint8_t>(mine);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_xbar[quad]);
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s_xbar[quad], xphase, ctl, DG_DEV_TIMEOUT))) break;
-                    const uint32_t other = s_scale[slot + (ew ^ 4u) * 32u + lane];
+                    uint32_t larger = mine;
+                    if constexpr (CL == 2) {
+                        s_scale[row_at + half * 128u] = static_cast<uint8_t>(mine);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s_xbar[quad]);
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s_xbar[quad], xphase, ctl, DG_DEV_TIMEOUT))) break;
+                    } else {
+                        const uint32_t part = smem_u32(s_scale + row_at + ((pair_base >> 1) * 2u + half) * 128u);
+#pragma unroll
+                        for (int q = 0; q < CL / 2; ++q)
+                            st_cluster_u8(mapa_shared(part, 2u * q + static_cast<uint32_t>(rank)), mine);
+                        __syncwarp();
+                        if (lane < CL / 2)
+                            mbar_arrive_cluster(mapa_shared(smem_u32(&s_xbar[quad]), 2u * lane + static_cast<uint32_t>(rank)));
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&s_xbar[quad], xphase, ctl, DG_DEV_TIMEOUT))) break;
+                    }
+#pragma unroll
+                    for (int q = 0; q < kParts; ++q) {
+                        const uint32_t b = s_scale[row_at + q * 128u];
+                        larger = b > larger ? b : larger;
+                    }
                     xphase ^= 1u;
-                    const uint32_t larger = mine > other ? mine : other;
                     const uint32_t byte = larger == 0u ? 127u : larger;
                     const float inv = inv_scale(byte);
                     const int row = tile.d_row0 + row_off + static_cast<int>(lane);
@@ -1437,20 +1483,15 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                     }
                     // the group's byte of the row's scale word; the last tile's threads also clear the
                     // word's unused bytes, and those of the rows that pad the words to a multiple of 4
-                    if (half == 0 && stores && row < p.sfh_ld) {
+                    if (half == 0 && pair_base == 0 && stores && row < p.sfh_ld) {
                         const int gi = tile.n0 / kGran;
                         uint8_t *w = p.sfh + (static_cast<int64_t>(gi >> 2) * p.sfh_ld + row) * 4;
                         w[gi & 3] = row < p.rows ? static_cast<uint8_t>(byte) : 0;
-                        if (tile.n0 + BN / 2 >= p.n)
+                        if (tile.n0 + kGran >= p.n)
                             for (int b = (gi & 3) + 1; b < 4; ++b) w[b] = 0;
                     }
                 } else if (stores) {
-#pragma unroll
-                    for (int j = 0; j < HC / 16; j += 2) {
-                        uint32_t o[16];
-                        pack_bf16_32(g[j], g[j + 1], o);
-                        store_pair(&tm_d, p.d, p.ldd, o, col0 + 16 * j, 0);
-                    }
+                    store_plane(&tm_d, p.d, p.ldd, g, col0, 0);
                 }
             } else if constexpr ((LAY & kLayGatedBwd) != 0) {
                 // gated backward: the accumulator is dh.  This warp's 128 columns of its 32 rows go
@@ -1774,10 +1815,10 @@ int max_active_pairs_impl() {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = kBs2Cluster<BN, LAY>;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(2);
+    cfg.gridDim = dim3(kBs2Cluster<BN, LAY>);
     cfg.blockDim = dim3(Cfg::kThreads);
     cfg.dynamicSmemBytes = Cfg::kSmemBytes;
     cfg.attrs = attr;

@@ -32,8 +32,11 @@
     X(256, false, 256, false, 4) X(128, false, 256, false, 4) X(128, true, 256, false, 4)          \
     X(32, false, 128, false, 4) X(96, false, 128, false, 4) X(128, false, 128, false, 4)
 
-// Gated feed-forward: forward (layout bit 4, NT), backward (bit 5, NN)
-#define DG_BS2_LIST_GATED(X) X(256, false, 256, false, 16) X(256, false, 256, false, 34)
+// Gated feed-forward: forward (layout bit 4, NT; 256, 128 or 64 columns: gate and up of 128 columns
+// by 1, 2 or 4 pairs), backward (bit 5, NN)
+#define DG_BS2_LIST_GATED(X)                                                                       \
+    X(256, false, 256, false, 16) X(128, false, 256, false, 16) X(64, false, 256, false, 16)       \
+    X(256, false, 256, false, 34) X(128, false, 256, false, 34)
 
 #define DG_BS2_LIST(X) \
     DG_BS2_LIST_BF16(X) DG_BS2_LIST_F32(X) DG_BS2_LIST_MN(X) DG_BS2_LIST_FP4(X) DG_BS2_LIST_GATED(X)

@@ -356,6 +356,15 @@ __device__ __forceinline__ void bulk_wait_group() {
     asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// A byte to another CTA's shared memory (cluster address from mapa_shared), and an arrival on a barrier
+// there that releases this thread's writes to the cluster.
+__device__ __forceinline__ void st_cluster_u8(uint32_t cluster_addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // FP32 word to another CTA's shared memory, and its 4 bytes to the transaction count of a
 // barrier there (cluster addresses from mapa_shared).
 __device__ __forceinline__ void st_async_cluster_f32(uint32_t cluster_addr, float v, uint32_t cluster_bar) {

@@ -56,7 +56,7 @@ def check_quantised(hq, sfh, h, tol, what):
 # (rows, inner width, K): one row, whole and ragged tiles, widths and K that end inside a block
 # of 128 and inside a word of 4 blocks, several K ring turns, more tiles than CTA pairs
 SIZES = [(1, 16, 16), (256, 128, 128), (129, 144, 80), (7, 1408, 2048), (515, 272, 400), (300, 640, 1040),
-         (2300, 1296, 384)]
+         (600, 1408, 384), (2300, 1296, 384)]
 
 
 @pytest.mark.parametrize("m,i,k", SIZES)
@@ -338,3 +338,34 @@ def test_lost_load_is_reported(backward):
     assert int(status) == dg.DG_DEV_TIMEOUT
     status.zero_()
     assert torch.equal(call(), want) and int(status) == 0
+
+
+def test_tiles_of_every_width():
+    """A row's bits are the same in tiles of 64, 128 and 256 columns."""
+    torch.manual_seed(19)
+    i, k = 1296, 640
+    a, sfa, _ = rows_operand(torch.randn(4096, k))
+    b, sfb, _ = block_operand(torch.randn(2 * i, k) * k ** -0.5)
+    c, sfc, _ = block_operand(torch.randn(k, i), along_rows=True)
+    gu = torch.randn(4096, 2 * i).to(BF16)
+    a, sfa, b, sfb, c, sfc, gu = cuda(a, sfa, b, sfb, c, sfc, gu)
+    seen, back, want = set(), set(), None
+    for m in (4096, 700, 256, 3):
+        hq = torch.empty(m, i, dtype=E4M3, device="cuda")
+        sfh = torch.empty(cdiv(i, 512), cdiv(m, 4) * 4, dtype=torch.int32, device="cuda")
+        words = torch.zeros(sfa.shape[0], cdiv(m, 4) * 4, dtype=torch.int32, device="cuda")
+        words[:, :m] = sfa[:, :m]
+        g = torch.empty(m, 2 * i, dtype=BF16, device="cuda")
+        h = torch.empty(m, i, dtype=BF16, device="cuda")
+        dg.dg_fp8_gated_gemm_nt(a[:m], words, b, sfb, hq=hq, sfh=sfh, gu=g)
+        dg.dg_fp8_gated_gemm_nt(a[:m], words, b, sfb, h=h)
+        seen.add(dg.last_config()["block_n"])
+        d = torch.empty(m, 2 * i, dtype=BF16, device="cuda")
+        dg.dg_fp8_gated_gemm_nn_backward(a[:m], words, c, sfc, gu[:m], d)
+        back.add(dg.last_config()["block_n"])
+        got = (hq.view(torch.uint8), sfh[:, :m].t(), g, h, d)
+        if want is None:
+            want = got
+        for x, y in zip(got, want):
+            assert torch.equal(x, y[:m])
+    assert seen == {64, 128, 256} and back == {128, 256}
