@@ -21,11 +21,11 @@ __device__ __forceinline__ uint32_t amax_bits(float v) {
     return b < 0x7F800000u ? b : 0u;
 }
 
-// Biased exponent (the UE8M0 byte) of the scale of a group with these amax bits.
+// Biased exponent (the UE8M0 byte) of the scale of a group with these amax bits: a fraction above
+// 0.75 carries into the exponent.  127 for 0, and for a NaN (a group without a finite value).
 __device__ __forceinline__ uint32_t ue8m0_of_amax(uint32_t bits) {
-    if (bits == 0u) return 127u;
-    const int e = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return static_cast<uint32_t>(e < 1 ? 1 : e);   // (at most 254 - 7)
+    const int e = static_cast<int>((bits + 0x1FFFFFu) >> 23) - 8;
+    return bits - 1u >= 0x7F800000u ? 127u : static_cast<uint32_t>(max(e, 1));   // (at most 254 - 7)
 }
 
 // 1 / scale; the byte is at most 247, so this is a normal number.

@@ -23,11 +23,11 @@ constexpr uint32_t kInf = 0x7F800000u;
 template <bool BF16>
 constexpr int kWords = BF16 ? 4 : 8;
 
-// The values of a row from col on; zero past the columns
-template <bool BF16>
-__device__ __forceinline__ void load8(const QuantParams &p, const char *row, int col, uint32_t (&w)[kWords<BF16>]) {
-    if (col + 8 <= p.cols) {
-        const uint4 *q = reinterpret_cast<const uint4 *>(row + (BF16 ? 2 : 4) * static_cast<int64_t>(col));
+// The values of a row from col on; zero past the columns (FULL: there are none past them)
+template <bool BF16, bool FULL>
+__device__ __forceinline__ void load8(const QuantParams &p, const char *at, int col, uint32_t (&w)[kWords<BF16>]) {
+    if (FULL || col + 8 <= p.cols) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(at);
 #pragma unroll
         for (int i = 0; i < kWords<BF16> / 4; ++i) {
             const uint4 x = __ldcs(q + i);   // (read once)
@@ -40,37 +40,28 @@ __device__ __forceinline__ void load8(const QuantParams &p, const char *row, int
         for (int i = 0; i < 8; ++i)
             if (col + i < p.cols) {
                 if constexpr (BF16)
-                    w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[col + i]) << (16 * (i & 1));
+                    w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(at)[i]) << (16 * (i & 1));
                 else
-                    w[i] = reinterpret_cast<const uint32_t *>(row)[col + i];
+                    w[i] = reinterpret_cast<const uint32_t *>(at)[i];
             }
     }
 }
 
-// Value i of the 8
+// The larger magnitude of two words, element by element, with some sign (one instruction; masked
+// where it is used).  A NaN never wins; an infinity does.
 template <bool BF16>
-__device__ __forceinline__ float value(const uint32_t (&w)[kWords<BF16>], int i) {
-    if constexpr (BF16) return __uint_as_float((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-    else return __uint_as_float(w[i]);
+__device__ __forceinline__ uint32_t amax2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (BF16) asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.xorsign.abs.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// max(m, |w|), element by element of a word (m not negative).  A NaN never wins; an infinity does.
+// A word's larger magnitude as FP32 bits (a NaN only where all of it is)
 template <bool BF16>
-__device__ __forceinline__ uint32_t amax_word(uint32_t m, uint32_t w) {
-    if constexpr (BF16) {
-        const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&m),
-                                         __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w)));
-        return *reinterpret_cast<const uint32_t *>(&r);
-    } else {
-        return __float_as_uint(fmaxf(__uint_as_float(m), fabsf(__uint_as_float(w))));
-    }
-}
-
-// A word's larger element as FP32 bits
-template <bool BF16>
-__device__ __forceinline__ uint32_t amax_bits_of(uint32_t m) {
-    if constexpr (BF16) return max(m & 0xFFFF0000u, m << 16);
-    else return m;
+__device__ __forceinline__ uint32_t magnitude(uint32_t m) {
+    if constexpr (BF16) return (amax2<true>(m, __byte_perm(m, m, 0x1032)) & 0x7FFFu) << 16;
+    else return m & 0x7FFFFFFFu;
 }
 
 // Infinities become NaN, so that they do not count and get the NaN code.
@@ -90,31 +81,44 @@ __device__ __forceinline__ void drop_infinities(uint32_t (&v)[N][kWords<BF16>]) 
         }
 }
 
-__device__ __forceinline__ void store8(const QuantParams &p, uint8_t *row, int col, uint32_t lo, uint32_t hi) {
-    if (col + 8 <= p.cols) {
-        *reinterpret_cast<uint2 *>(row + col) = make_uint2(lo, hi);
+// 1 / scale of a byte as a factor of the words' elements: FP32, or bf16 twice (a power of two in
+// bf16's range: products are exact, or so small that their code is 0)
+template <bool BF16>
+__device__ __forceinline__ uint32_t factor(uint32_t byte) {
+    return BF16 ? (254u - byte) * 0x00800080u : (254u - byte) << 23;
+}
+
+// Codes of the 8 values over their scales: word j (or value j) times factor f(j)
+template <bool BF16, bool FULL, typename F>
+__device__ __forceinline__ void put_codes(const QuantParams &p, uint8_t *at, int col, const uint32_t (&w)[kWords<BF16>], F f) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < kWords<BF16>; ++j) {
+        if constexpr (BF16) {
+            uint32_t x;
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w[j]), "r"(f(j)));
+            v[2 * j] = __uint_as_float(x << 16);
+            v[2 * j + 1] = __uint_as_float(x & 0xFFFF0000u);
+        } else {
+            v[j] = __uint_as_float(w[j]) * __uint_as_float(f(j));
+        }
+    }
+    uint32_t o[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        asm("{\n\t.reg .b16 a, b;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+            "mov.b32 %0, {a, b};\n\t}"
+            : "=r"(o[j])
+            : "f"(v[4 * j]), "f"(v[4 * j + 1]), "f"(v[4 * j + 2]), "f"(v[4 * j + 3]));
+    if (FULL || col + 8 <= p.cols) {
+        *reinterpret_cast<uint2 *>(at) = make_uint2(o[0], o[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (col + i < p.cols) row[col + i] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
+            if (col + i < p.cols) at[i] = static_cast<uint8_t>(o[i / 4] >> (8 * (i & 3)));
     }
-}
-
-// The 8 values over one scale, or over their columns' scales, to the codes of a row
-template <bool BF16>
-__device__ __forceinline__ void put_codes(const QuantParams &p, uint8_t *row, int col, const uint32_t (&w)[kWords<BF16>],
-                                          const float (&inv)[8]) {
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        o[j] = cvt_e4m3x2(value<BF16>(w, 2 * j) * inv[2 * j], value<BF16>(w, 2 * j + 1) * inv[2 * j + 1]);
-    store8(p, row, col, o[0] | o[1] << 16, o[2] | o[3] << 16);
-}
-template <bool BF16>
-__device__ __forceinline__ void put_codes(const QuantParams &p, uint8_t *row, int col, const uint32_t (&w)[kWords<BF16>],
-                                          float inv) {
-    const float all[8] = {inv, inv, inv, inv, inv, inv, inv, inv};
-    put_codes<BF16>(p, row, col, w, all);
 }
 
 // Row j of the packed words that 128-row block `block` belongs to, its byte, and whether it is the
@@ -143,154 +147,208 @@ __device__ __forceinline__ void put_byte(uint8_t *word, int byte, uint32_t v, bo
         for (int b = byte + 1; b < 4; ++b) word[b] = 0;
 }
 
-// MODE: 1 rows, 2 columns, 3 both, 4 blocks.  TR: rows of a tile (128 but for rows alone).
-template <bool BF16, int MODE, int TR>
-__global__ void __launch_bounds__(kQThreads, BF16 ? 4 : 2) dg_quantize_kernel(const __grid_constant__ QuantParams p,
-                                                                              const __grid_constant__ KGroupRows t) {
-    static_assert(TR == 128 || MODE == 1, "columns and blocks have 128 rows");
-    constexpr int N = TR / 16;          // rows of a thread
-    constexpr int W = kWords<BF16>;
-    constexpr bool COLS = MODE == 2 || MODE == 3;
-    __shared__ uint32_t s_col[COLS ? 8 : 1][16 * W];   // a warp's column amax
-    __shared__ float s_inv[COLS ? 128 : 1];
-    __shared__ uint32_t s_block[8];
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
-    const int col0 = blockIdx.x * 128, col = col0 + cl * 8;
-    const int64_t batch = blockIdx.z;
-    const char *x = static_cast<const char *>(p.x) + batch * p.x_batch * (BF16 ? 2 : 4);
-    const int tiles_y = (p.rows + TR - 1) / TR;
-    for (int ty = blockIdx.y; ty < tiles_y; ty += gridDim.y) {
-        const int row0 = ty * TR + rl;
-        uint32_t v[N][W];
+// Largest magnitudes of N rows over the 16 lanes that hold a row's 128 values, as FP32 bits, from each
+// lane's own.  bf16: two rows to a word.
+template <bool BF16, int N>
+__device__ __forceinline__ void row_amax(const uint32_t (&m)[N], uint32_t (&out)[N]) {
+    if constexpr (BF16 && N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            // both rows' low halves, both rows' high halves
+            uint32_t x = amax2<true>(__byte_perm(m[i], m[i + 1], 0x5410), __byte_perm(m[i], m[i + 1], 0x7632));
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) x = amax2<true>(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+            out[i] = (x & 0x7FFFu) << 16;
+            out[i + 1] = x & 0x7FFF0000u;
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int row = row0 + 16 * i;
-            if (row < p.rows) {
-                load8<BF16>(p, x + static_cast<int64_t>(row) * p.ldx * (BF16 ? 2 : 4), col, v[i]);
+            uint32_t x = magnitude<BF16>(m[i]);
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) x = amax2<false>(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+            out[i] = x & 0x7FFFFFFFu;
+        }
+    }
+}
+
+struct QuantShared {
+    uint32_t col[8][128];    // a warp's column amax (bf16: pairs)
+    uint32_t inv[128];       // the columns' factors (bf16: pairs)
+    uint32_t block[8];
+};
+
+// One tile of TR rows x TC columns, 128 x 128 but for rows alone.  MODE: 1 rows, 2 columns, 3 both,
+// 4 blocks.  FULL: the tile lies inside the matrix.
+template <bool BF16, int MODE, int TR, int TC, bool FULL>
+__device__ __forceinline__ void quantize_tile(const QuantParams &p, const KGroupRows &t, QuantShared &s, int ty) {
+    constexpr int kLanes = TC / 8, kPass = kQThreads / kLanes;   // threads of a row, rows at a time
+    constexpr int N = TR / kPass;       // rows of a thread
+    constexpr int W = kWords<BF16>;
+    constexpr bool ROWS = MODE == 1 || MODE == 3, COLS = MODE == 2 || MODE == 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cl = threadIdx.x % kLanes, rl = threadIdx.x / kLanes;
+    const int col0 = blockIdx.x * TC, col = col0 + cl * 8, row0 = ty * TR + rl;
+    const int64_t batch = blockIdx.z;
+    uint32_t v[N][W];
+    {
+        constexpr int kSize = BF16 ? 2 : 4;
+        const char *x = static_cast<const char *>(p.x) + (batch * p.x_batch + static_cast<int64_t>(row0) * p.ldx + col) * kSize;
+        const int64_t step = static_cast<int64_t>(kPass * kSize) * p.ldx;
+#pragma unroll
+        for (int i = 0; i < N; ++i, x += step) {
+            if (FULL || row0 + kPass * i < p.rows) {
+                load8<BF16, FULL>(p, x, col, v[i]);
             } else {
 #pragma unroll
                 for (int j = 0; j < W; ++j) v[i][j] = 0u;
             }
         }
-        // the thread's amax by column, which also says whether there is an infinity
-        uint32_t cm[W], any = 0u;
-        auto columns = [&]() {
-            any = 0u;
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                cm[j] = 0u;
-#pragma unroll
-                for (int i = 0; i < N; ++i) cm[j] = amax_word<BF16>(cm[j], v[i][j]);
-                any = max(any, amax_bits_of<BF16>(cm[j]));
-            }
-        };
-        columns();
-        if (any == kInf) {
-            drop_infinities<BF16, N>(v);
-            columns();
-        }
-        if constexpr (MODE == 1 || MODE == 3) {
-            const int gi = blockIdx.x;
-            const bool last = col0 + 128 >= p.cols;
+    }
+    // the thread's amax by row or by column, either of which also says whether there is an infinity
+    uint32_t rm[N], cm[W], any;
+    auto maxima = [&]() {
+        any = 0u;
+        if constexpr (ROWS) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                uint32_t m = 0u;
+                rm[i] = v[i][0];
 #pragma unroll
-                for (int j = 0; j < W; ++j) m = amax_word<BF16>(m, v[i][j]);
-                uint32_t amax = amax_bits_of<BF16>(m);
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-                const int row = row0 + 16 * i;
-                const uint32_t byte = ue8m0_of_amax(amax);
-                if (row < p.rows) put_codes<BF16>(p, p.q + static_cast<int64_t>(row) * p.ldq, col, v[i], inv_scale(byte));
-                if (cl == 0 && row < p.sf_ld)   // (rows that pad the words to a multiple of 4: zero)
-                    put_byte(p.sf + (static_cast<int64_t>(gi >> 2) * p.sf_ld + row) * 4, gi & 3, row < p.rows ? byte : 0u, last);
+                for (int j = 1; j < W; ++j) rm[i] = amax2<BF16>(rm[i], v[i][j]);
+                if constexpr (MODE == 1) any = i == 0 ? rm[0] : amax2<BF16>(any, rm[i]);
             }
         }
-        if constexpr (COLS) {
+        if constexpr (MODE != 1) {
 #pragma unroll
             for (int j = 0; j < W; ++j) {
-                cm[j] = amax_word<BF16>(cm[j], __shfl_xor_sync(0xFFFFFFFFu, cm[j], 16));
-                if (lane < 16) s_col[warp][cl * W + j] = cm[j];
+                cm[j] = v[0][j];
+#pragma unroll
+                for (int i = 1; i < N; ++i) cm[j] = amax2<BF16>(cm[j], v[i][j]);
+                any = j == 0 ? cm[0] : amax2<BF16>(any, cm[j]);
             }
-            __syncthreads();
-            if (threadIdx.x < 16 * W) {
-                uint32_t m = 0u;
+        }
+        any = magnitude<BF16>(any);
+    };
+    maxima();
+    if (any == kInf) {
+        drop_infinities<BF16, N>(v);
+        maxima();
+    }
+    if constexpr (ROWS) {
+        const int gi = blockIdx.x * (TC / 128) + cl / 16;
+        const bool last = (gi + 1) * 128 >= p.cols;
+        uint32_t amax[N];
+        row_amax<BF16, N>(rm, amax);
+        uint8_t *q = p.q + static_cast<int64_t>(row0) * p.ldq + col;
+        uint8_t *sf = p.sf + (static_cast<int64_t>(gi >> 2) * p.sf_ld + row0) * 4;
+        const int64_t step = kPass * p.ldq;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) m = amax_word<BF16>(m, s_col[w][threadIdx.x]);
+        for (int i = 0; i < N; ++i, q += step) {
+            const int row = row0 + kPass * i;
+            const uint32_t byte = ue8m0_of_amax(amax[i]), f = factor<BF16>(byte);
+            if (FULL || row < p.rows) put_codes<BF16, FULL>(p, q, col, v[i], [f](int) { return f; });
+            // (rows that pad the words to a multiple of 4: zero)
+            if (cl % 16 == 0 && (FULL || (row < p.sf_ld && (TC == 128 || col < p.cols))))
+                put_byte(sf + 4 * kPass * i, gi & 3, FULL || row < p.rows ? byte : 0u, last);
+        }
+    }
+    if constexpr (COLS) {
 #pragma unroll
-                for (int e = 0; e < (BF16 ? 2 : 1); ++e) {
-                    const int lc = static_cast<int>(threadIdx.x) * (BF16 ? 2 : 1) + e, c = col0 + lc;
-                    const uint32_t byte = ue8m0_of_amax(BF16 ? (e ? m & 0xFFFF0000u : m << 16) : m);
-                    s_inv[lc] = inv_scale(byte);
-                    if (c < p.sfk_ld) {
-                        int word, at;
-                        bool last;
-                        packed_row(p, t, ty, word, at, last);
-                        put_byte(p.sfk + (static_cast<int64_t>(word) * p.sfk_ld + c) * 4, at, c < p.cols ? byte : 0u, last);
-                    }
+        for (int j = 0; j < W; ++j) {
+            cm[j] = amax2<BF16>(cm[j], __shfl_xor_sync(0xFFFFFFFFu, cm[j], 16));
+            if (lane < 16) s.col[warp][cl * W + j] = cm[j];
+        }
+        __syncthreads();
+        if (threadIdx.x < 16 * W) {
+            uint32_t m = s.col[0][threadIdx.x], inv = 0u;
+#pragma unroll
+            for (int w = 1; w < 8; ++w) m = amax2<BF16>(m, s.col[w][threadIdx.x]);
+#pragma unroll
+            for (int e = 0; e < (BF16 ? 2 : 1); ++e) {
+                const int c = col0 + static_cast<int>(threadIdx.x) * (BF16 ? 2 : 1) + e;
+                const uint32_t byte = ue8m0_of_amax(BF16 ? (e ? m & 0x7FFF0000u : (m & 0x7FFFu) << 16) : m & 0x7FFFFFFFu);
+                const uint32_t f = factor<BF16>(byte);
+                inv = !BF16 ? f : e ? (inv & 0xFFFFu) | (f & 0xFFFF0000u) : f;
+                if (c < p.sfk_ld) {
+                    int word, at;
+                    bool last;
+                    packed_row(p, t, ty, word, at, last);
+                    put_byte(p.sfk + (static_cast<int64_t>(word) * p.sfk_ld + c) * 4, at, c < p.cols ? byte : 0u, last);
                 }
             }
-            __syncthreads();
-            float inv[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) inv[j] = s_inv[cl * 8 + j];
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int row = row0 + 16 * i;
-                if (row < p.rows) put_codes<BF16>(p, p.qk + static_cast<int64_t>(row) * p.ldqk, col, v[i], inv);
-            }
-            // (the next tile's writes to s_col and s_inv come after its own first barrier, or, s_col,
-            // after every thread has passed this tile's second)
+            s.inv[threadIdx.x] = inv;
         }
-        if constexpr (MODE == 4) {
-            uint32_t m = __reduce_max_sync(0xFFFFFFFFu, any);
-            if (lane == 0) s_block[warp] = m;
-            __syncthreads();
-            m = s_block[0];
+        __syncthreads();
+        uint32_t inv[W];
 #pragma unroll
-            for (int w = 1; w < 8; ++w) m = max(m, s_block[w]);
-            const uint32_t byte = ue8m0_of_amax(m);
-            uint8_t *q = p.q + batch * p.q_batch;
+        for (int j = 0; j < W; ++j) inv[j] = s.inv[cl * W + j];
+        uint8_t *q = p.qk + static_cast<int64_t>(row0) * p.ldqk + col;
+        const int64_t step = kPass * p.ldqk;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int row = row0 + 16 * i;
-                if (row < p.rows) put_codes<BF16>(p, q + static_cast<int64_t>(row) * p.ldq, col, v[i], inv_scale(byte));
-            }
-            // one byte a row (products along the columns), one a column (along the rows)
-            const int i = threadIdx.x & 127;
-            if (threadIdx.x < 128) {
-                const int gi = blockIdx.x, row = ty * 128 + i;
-                if (p.sf != nullptr && row < p.sf_ld)
-                    put_byte(p.sf + ((batch * ((p.cols + 511) / 512) + (gi >> 2)) * p.sf_ld + row) * 4, gi & 3,
-                             row < p.rows ? byte : 0u, col0 + 128 >= p.cols);
-            } else {
-                const int c = col0 + i;
-                if (p.sfk != nullptr && c < p.sfk_ld)
-                    put_byte(p.sfk + ((batch * ((p.rows + 511) / 512) + (ty >> 2)) * p.sfk_ld + c) * 4, ty & 3,
-                             c < p.cols ? byte : 0u, (ty + 1) * 128 >= p.rows);
-            }
-            if (gridDim.y < tiles_y) __syncthreads();   // s_block is free for the next tile
+        for (int i = 0; i < N; ++i, q += step)
+            if (FULL || row0 + kPass * i < p.rows) put_codes<BF16, FULL>(p, q, col, v[i], [&inv](int j) { return inv[j]; });
+        // (the next tile's writes to s.inv come after its own first barrier, and those to s.col after
+        // every thread has passed this tile's second)
+    }
+    if constexpr (MODE == 4) {
+        uint32_t m = __reduce_max_sync(0xFFFFFFFFu, any > kInf ? 0u : any);
+        if (lane == 0) s.block[warp] = m;
+        __syncthreads();
+        m = s.block[0];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) m = max(m, s.block[w]);
+        const uint32_t byte = ue8m0_of_amax(m), f = factor<BF16>(byte);
+        uint8_t *q = p.q + batch * p.q_batch + static_cast<int64_t>(row0) * p.ldq + col;
+        const int64_t step = kPass * p.ldq;
+#pragma unroll
+        for (int i = 0; i < N; ++i, q += step)
+            if (FULL || row0 + kPass * i < p.rows) put_codes<BF16, FULL>(p, q, col, v[i], [f](int) { return f; });
+        // one byte a row (products along the columns), one a column (along the rows)
+        const int i = threadIdx.x & 127;
+        if (threadIdx.x < 128) {
+            const int gi = blockIdx.x, row = ty * 128 + i;
+            if (p.sf != nullptr && row < p.sf_ld)
+                put_byte(p.sf + ((batch * ((p.cols + 511) / 512) + (gi >> 2)) * p.sf_ld + row) * 4, gi & 3,
+                         row < p.rows ? byte : 0u, col0 + 128 >= p.cols);
+        } else {
+            const int c = col0 + i;
+            if (p.sfk != nullptr && c < p.sfk_ld)
+                put_byte(p.sfk + ((batch * ((p.rows + 511) / 512) + (ty >> 2)) * p.sfk_ld + c) * 4, ty & 3,
+                         c < p.cols ? byte : 0u, (ty + 1) * 128 >= p.rows);
         }
+        __syncthreads();   // s.block is free for the next tile
     }
 }
 
-template <bool BF16, int MODE, int TR>
+template <bool BF16, int MODE, int TR, int TC = 128>
+__global__ void __launch_bounds__(kQThreads, MODE == 1 ? (BF16 ? 6 : 4) : BF16 ? 4 : 2) dg_quantize_kernel(
+    const __grid_constant__ QuantParams p, const __grid_constant__ KGroupRows t) {
+    static_assert((TR == 128 && TC == 128) || MODE == 1, "columns and blocks have 128 rows and columns");
+    __shared__ QuantShared s;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int tiles_y = (p.rows + TR - 1) / TR;
+    for (int ty = blockIdx.y; ty < tiles_y; ty += gridDim.y) {
+        if ((ty + 1) * static_cast<int64_t>(TR) <= p.rows && (blockIdx.x + 1) * static_cast<int64_t>(TC) <= p.cols)
+            quantize_tile<BF16, MODE, TR, TC, true>(p, t, s, ty);
+        else
+            quantize_tile<BF16, MODE, TR, TC, false>(p, t, s, ty);
+    }
+}
+
+template <bool BF16, int MODE, int TR, int TC = 128>
 cudaError_t launch_one(const QuantParams &p, const KGroupRows &t, int batch, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     const int ty = (p.rows + TR - 1) / TR;
-    cfg.gridDim = dim3((p.cols + 127) / 128, ty < 65535 ? ty : 65535, batch);
+    cfg.gridDim = dim3((p.cols + TC - 1) / TC, ty < 65535 ? ty : 65535, batch);
     cfg.blockDim = dim3(kQThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dg_quantize_kernel<BF16, MODE, TR>, p, t);
+    return cudaLaunchKernelEx(&cfg, dg_quantize_kernel<BF16, MODE, TR, TC>, p, t);
 }
 
 template <bool BF16>
@@ -301,7 +359,7 @@ cudaError_t launch_typed(const QuantParams &p, const KGroupRows &t, int batch, i
             // two an SM, tiles of 16 rows
             const int64_t tiles = static_cast<int64_t>((p.cols + 127) / 128) * ((p.rows + 127) / 128);
             if (tiles < 2 * num_sms) return launch_one<BF16, 1, 16>(p, t, batch, stream);
-            return launch_one<BF16, 1, 128>(p, t, batch, stream);
+            return launch_one<BF16, 1, 16, 512>(p, t, batch, stream);
         }
         case 2: return launch_one<BF16, 2, 128>(p, t, batch, stream);
         case 3: return launch_one<BF16, 3, 128>(p, t, batch, stream);

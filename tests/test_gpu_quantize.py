@@ -183,3 +183,25 @@ def test_captured_and_on_another_stream():
     wq, wsf = rows_form(x.cpu())
     wqk, wsfk = cols_form(x.cpu())
     assert same(q, wq) and torch.equal(sf.cpu(), wsf) and same(qk, wqk) and torch.equal(sfk.cpu(), wsfk)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_nothing_finite(dtype):
+    """Groups without a finite value, and NaN in all values of one place beside an infinity in another."""
+    nan, inf = float("nan"), float("inf")
+    x = torch.randn(256, 512, generator=torch.Generator().manual_seed(5))
+    x[:128, :128] = nan
+    x[3, 128:256] = inf
+    x[:128, 130] = -inf
+    x[128:, 0:512:2] = nan
+    x[200, 1] = inf
+    x = x.to(dtype)
+    q, qk = (torch.empty(256, 512, dtype=E4M3, device="cuda") for _ in range(2))
+    sf, sfk = torch.empty(1, 256, dtype=torch.int32, device="cuda"), torch.empty(1, 512, dtype=torch.int32, device="cuda")
+    dg.dg_quantize_fp8(x.cuda(), q=q, sf=sf, qk=qk, sfk=sfk)
+    (wq, wsf), (wqk, wsfk) = rows_form(x), cols_form(x)
+    assert same(q, wq) and torch.equal(sf.cpu(), wsf) and same(qk, wqk) and torch.equal(sfk.cpu(), wsfk)
+    sft = torch.empty_like(sfk)
+    dg.dg_quantize_fp8_blocks(x.cuda(), q, sf=sf, sft=sft)
+    wq, wsf, wsft = blocks_form(x)
+    assert same(q, wq) and torch.equal(sf.cpu(), wsf) and torch.equal(sft.cpu(), wsft)
