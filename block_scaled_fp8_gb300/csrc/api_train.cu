@@ -1,6 +1,8 @@
 // Host side of the feed-forward training entry points of include/dg.h: the gated
 // block and its backward pass, the FP8 quantiser, Newton-Schulz orthogonalisation.
 // Validation order as in api.cu: sizes, pointers, alignment, then the device.
+#include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 
@@ -191,6 +193,9 @@ dg_status gated(const GatedArgs &g) {
     const int64_t tiles = max_units * p.num_n_blocks;
     const int grid = cluster * static_cast<int>(tiles < clusters ? tiles : clusters);
     host_set_last_config(256, bn, info.stages, grid, 2, 1);
+    if ((p.debug_flags & DG_DEBUG_PRINT_CONFIGS) || std::getenv("DG_PRINT_CONFIGS"))
+        std::fprintf(stderr, "[dg] gated %s rows=%d inner=%d k=%d -> BLOCK_M=256 BLOCK_N=%d stages=%d smem=%d grid=%d\n",
+                     g.backward ? "backward" : "forward", m, inner, k, bn, info.stages, info.smem_bytes, grid);
     const cudaError_t e = launch_bs2_gemm(bn, 256, maps, p, grid, static_cast<cudaStream_t>(g.stream));
     return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
@@ -347,7 +352,7 @@ dg_status dg_newton_schulz(const void *g, int g_fmt, int64_t ldg, int64_t g_batc
     if (batch < 0 || rows < 0 || cols < 0 || steps < 1 || !(eps >= 0.0f)) return DG_ERR_INVALID_ARG;
     if (g_fmt != DG_VALUES_F32 && g_fmt != DG_VALUES_BF16) return DG_ERR_INVALID_ARG;
     if (batch == 0 || rows == 0 || cols == 0) return DG_OK;
-    if (ns_unsupported(batch, rows, cols)) return DG_ERR_UNSUPPORTED;
+    if (ns_unsupported(batch, rows, cols) || steps > kMaxNsSteps) return DG_ERR_UNSUPPORTED;
     if (!g || !out || !workspace || ldg < cols || ldo < cols) return DG_ERR_INVALID_ARG;
     if (g_batch < 0 || (batch > 1 && out_batch < (rows - 1) * ldo + cols)) return DG_ERR_INVALID_ARG;
     if (workspace_bytes < ns_workspace_bytes(batch, rows, cols)) return DG_ERR_INVALID_ARG;

@@ -201,6 +201,7 @@ constexpr int kMaxLayerExperts = 1024;
 constexpr int kMaxLayerWidth = 1 << 24;
 constexpr int kMaxNsSide = 1 << 20;             // sides and elements of a matrix to orthogonalise
 constexpr int64_t kMaxNsElements = 1ll << 31;
+constexpr int kMaxNsSteps = 1000;
 constexpr int kMaxRouteExperts = 1024;
 constexpr int kMaxRouteTopk = 32;
 

@@ -1163,14 +1163,6 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
             }
             cp_async_commit();
         };
-        // this tile's rows of gate (first warp of a quadrant) or up (second) to L2
-        auto prefetch_gu = [&](const PairTile &tl) {
-            const int row = tl.d_row0 + row_off + static_cast<int>(lane);
-            const int cols = p.n - tl.n0 < BN ? p.n - tl.n0 : BN;
-            if (tl.valid_rows > 0 && row < p.rows && cols > 0)
-                prefetch_l2_bulk(p.gu + static_cast<int64_t>(row) * p.ldgu + (half ? p.n : 0) + tl.n0,
-                                 static_cast<uint32_t>(cols) * 2u);
-        };
         uint32_t xphase = 0;   // gated forward: the exchange of the halves' amax
         PairTile tile;
         if (pair_id < num_tiles) {
@@ -1180,7 +1172,6 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
             if constexpr ((LAY & kLayGatedBwd) != 0) {
                 load_gu(tile, true, 0);
                 load_gu(tile, true, 1);
-                prefetch_gu(tile);
             }
             if constexpr (WITH_C && F32) {
                 prefetch_d32(tile);
@@ -1496,15 +1487,15 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
             } else if constexpr ((LAY & kLayGatedBwd) != 0) {
                 // gated backward: the accumulator is dh.  This warp's 128 columns of its 32 rows go
                 // to registers and the accumulator is released.  Then chunks of 32 columns, whose gate and
-                // up were copied to shared memory two chunks ahead (their lines fetched to L2 a
-                // tile ahead): a lane takes a row, the gradients take the places of gate and up, h a
-                // box of its own, and the warp stores whole row segments with plain stores, which nothing
-                // waits for.  (With TMA boxes in and out, a chunk's load, arithmetic and store
-                // followed one another: 4096x7168, K = 2048: 102 us against the 49 of the product alone.)
+                // up were copied to shared memory two chunks ahead: a lane takes a row, the gradients take
+                // the places of gate and up, h a box of its own, and the warp stores whole row
+                // segments with plain stores, which nothing waits for.  (With TMA boxes in and out, a
+                // chunk's load, arithmetic and store followed one another: 4096x7168, K = 2048: 102 us
+                // against 77; the product alone takes 48.  What is left is the 294 MB of gate, up and
+                // results, 43 us of HBM time, which a tile's epilogue draws at about 5 TB/s.)
                 constexpr int HC = BN / 2;
                 uint32_t dh[HC / 16][16];
                 const uint32_t tcol = tmem_base + ((quad * 32) << 16) + acc * ACC + half * HC;
-                if (has_next) prefetch_gu(next_tile);
 #pragma unroll
                 for (int j = 0; j < HC / 16; ++j) tmem_ld_32x32b_x16(tcol + 16 * j, dh[j]);
                 tmem_ld_wait();

@@ -516,7 +516,7 @@ static PyObject *newton_schulz(PyObject *self, PyObject *const *arg, Py_ssize_t 
     batch = lead < 0 ? 1 : lead;
     CHECK(status_of(arg[8], &status));
     need = ((SchulzBytesFn)fns[SCHULZ_BYTES])((int)batch, (int)r, (int)c);
-    if (steps < 1 || !(coef[3] >= 0)) need = -1;   /* (refused) */
+    if (steps < 1 || steps > 1000 || !(coef[3] >= 0)) need = -1;   /* (refused) */
     PyObject *const on_device[] = {arg[0], arg[1], arg[8]};
     CHECK(device_side(on_device, 3, arg[7], need, arg[0], arg[9], &hold, &ws, &ws_bytes, &stream));
     Py_BEGIN_ALLOW_THREADS

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256) dg_ns_norm_kernel(const __grid_constant__
             const int64_t nv = n / V;
 #pragma unroll 4
             for (int64_t i = threadIdx.x; i < nv; i += 256) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(at) + i);
+                const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(at) + i);
                 const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(256) dg_ns_split_kernel(const __grid_constant_
             float v[8];
             if (vec) {
                 const uint4 *q = reinterpret_cast<const uint4 *>(g + at * (BF16 ? 2 : 4));
-                const uint4 a = __ldg(q);
+                const uint4 a = __ldcg(q);
                 const uint32_t x[4] = {a.x, a.y, a.z, a.w};
                 if constexpr (BF16) {
 #pragma unroll
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(256) dg_ns_split_kernel(const __grid_constant_
                         v[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
                     }
                 } else {
-                    const uint4 b = __ldg(q + 1);
+                    const uint4 b = __ldcg(q + 1);
                     const uint32_t y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(256) dg_ns_split_kernel(const __grid_constant_
                     const int r = q / kPer, c = q % kPer * V;
                     uint4 x = make_uint4(0u, 0u, 0u, 0u);
                     if (r0 + r < p.rows)
-                        x = __ldg(reinterpret_cast<const uint4 *>(g + (static_cast<int64_t>(r0 + r) * p.ldg + c0 + c) * (BF16 ? 2 : 4)));
+                        x = __ldcg(reinterpret_cast<const uint4 *>(g + (static_cast<int64_t>(r0 + r) * p.ldg + c0 + c) * (BF16 ? 2 : 4)));
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {

@@ -629,7 +629,7 @@ dg_status dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(const void *dy, int
  *   g     FP32 or bf16 (dg_values_format) [rows][ldg] at g + i * g_batch elements.
  *   out   bf16 [rows][ldo] at out + i * out_batch elements (matrices apart from one another);
  *         may be g itself where g is bf16 of the same strides.
- *   steps >= 1; a, b, c the polynomial (3.4445, -4.7750, 2.0315 brings singular values from
+ *   1 <= steps <= 1000; a, b, c the polynomial (3.4445, -4.7750, 2.0315 brings singular values from
  *         above 0.003 to 0.7 .. 1.2 in five steps); eps >= 0.  A polynomial or a G that
  *         makes an element of X or A or of b A + c A A 16 or more gives infinities or NaN.
  *   The operands of the products are rounded to 11 bits, X itself is kept to 22; sums are FP32.  The result
