@@ -164,7 +164,8 @@ dg_status gated(const GatedArgs &g) {
     p.gu = static_cast<uint16_t *>(g.gu);
     p.ldgu = g.ldgu;
     TensorMaps maps;
-    bool ok = encode_fp8(&maps.a, g.a, k, m, g.lda, kBlockM);
+    p.few_rows = !g.grouped && m <= kBlockM ? (m + 7) / 8 * 8 : 0;
+    bool ok = encode_fp8(&maps.a, g.a, k, m, g.lda, p.few_rows > 0 ? p.few_rows : kBlockM);
     if (g.backward) {
         p.d = static_cast<uint16_t *>(g.dgu);
         p.ldd = g.lddgu;

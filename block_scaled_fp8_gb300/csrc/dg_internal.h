@@ -66,6 +66,7 @@ struct GemmParams {
     int sfh_ld;
     uint16_t *h;
     int64_t ldh;
+    int few_rows;        // gated, dense with at most 128 rows: rows of A's boxes, else 0
     // packed UE8M0 scale words, [slices][ld] int32 with ld = align4(mn); the
     // block-scaled kernels' scale warps read them with cp.async
     const uint32_t *sfa_words;

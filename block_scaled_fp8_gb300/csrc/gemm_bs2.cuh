@@ -682,6 +682,11 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
         uint32_t phase = 0;
         uint32_t issued = 0;
         bool drop = (p.debug_flags & DG_DEBUG_DROP_ONE_LOAD) && pair_id == 0;
+        // gated, at most 128 rows in all: A's boxes have just those rows (few_rows, in whole 8s), and the
+        // peer none; the rows of shared memory past them hold anything, as do their rows of D, which
+        // nothing reads (boxes that lie outside the matrix take longer than the rows' own bytes)
+        const bool few = (LAY & (kLayGated | kLayGatedBwd)) != 0 && p.few_rows > 0;
+        const int few_bytes = p.few_rows * kBlockK;
         for (int t = pair_id; t < num_tiles; t += num_pairs) {
             PairTile tile;
             get_pair_tile<BN, MP, LAY>(p, prefix, pinfo, num_units, psf_k, t, rank, tile);
@@ -698,12 +703,14 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                         // slot; the K-major one: G boxes (K-blocks past K are out of bounds,
                         // zero-filled, and still count their bytes)
                         if (elect_one()) {
-                            if (leader) mbar_arrive_expect_tx(&full_bar[slot], 2 * G * Cfg::kStageBytes);
+                            if (leader)
+                                mbar_arrive_expect_tx(&full_bar[slot], few ? G * (few_bytes + 2 * Cfg::kBBytes)
+                                                                           : 2 * G * Cfg::kStageBytes);
                             uint8_t *a_slot = smem_a + slot * G * Cfg::kABytes;
                             uint8_t *b_slot = smem_b + slot * G * Cfg::kBBytes;
                             if constexpr (A_MN) {
                                 tma_load_2d_pair(a_slot, &tm_a, fb, tile.a_row0, kg0 * kBlockK);
-                            } else {
+                            } else if (!few || leader) {
 #pragma unroll
                                 for (int j = 0; j < G; ++j)
                                     tma_load_2d_pair(a_slot + j * Cfg::kABytes, &tm_a, fb, (kg0 + j) * kBlockK,
@@ -732,14 +739,18 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                         }
                     } else if (elect_one()) {
                         // the leader expects both CTAs' bytes; each CTA's loads count there
-                        if (leader) mbar_arrive_expect_tx(&full_bar[slot], 2 * nk * Cfg::kTxBytes);
+                        if (leader)
+                            mbar_arrive_expect_tx(&full_bar[slot],
+                                                  few ? nk * (few_bytes + 2 * (Cfg::kTxBytes - Cfg::kABytes))
+                                                      : 2 * nk * Cfg::kTxBytes);
                         // a slot's B: the G K-blocks of the first MMA's rows, then the G
                         // K-blocks of the second's
                         auto load_kb = [&](int j) {
                             const int kb = kg0 + j;
                             uint8_t *b_slot = smem_b + slot * G * Cfg::kBBytes;
-                            tma_load_2d_pair(smem_a + (slot * G + j) * Cfg::kABytes, &tm_a, fb, kb * kBlockK,
-                                             tile.a_row0);
+                            if (!few || leader)
+                                tma_load_2d_pair(smem_a + (slot * G + j) * Cfg::kABytes, &tm_a, fb, kb * kBlockK,
+                                                 tile.a_row0);
                             tma_load_2d_pair(b_slot + j * Cfg::kB1Bytes, &tm_b, fb, kb * kBlockK, tile.b_row0);
                             if constexpr (Cfg::kBN2 > 0)
                                 tma_load_2d_pair(b_slot + G * Cfg::kB1Bytes + j * Cfg::kB2Bytes, &tm_b2, fb,
