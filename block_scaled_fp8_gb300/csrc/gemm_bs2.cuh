@@ -57,8 +57,9 @@ namespace dg {
 // CT: the bf16 C epilogue of a dense GEMM keeps this CTA's whole C tile in shared
 // memory (loaded by TMA a tile ahead, summed in place, stored by TMA from there);
 // the region doubles as the output staging of the register C path.
+// GK: K-blocks of a ring slot, 0 for the rule below.
 template <int BN, int MP = 256, bool B_ATOM = false, bool B4 = false, int SB = 0, bool S32 = false,
-          bool CT = false>
+          bool CT = false, int GK = 0>
 struct Bs2Config {
     // BN/2 rows of B per CTA fill whole 8-row swizzle atoms; pair MMAs take N % 16 == 0, N <= 256;
     // with MP=128 each half of N is whole 16-column epilogue chunks
@@ -160,7 +161,7 @@ struct Bs2Config {
     static constexpr int kStagesCap = kStagesBySmem > kMaxStages ? kMaxStages : kStagesBySmem;
     // (128-row pairs at 32 columns: four small MMAs per K-block, so the MMA warp's
     // per-slot waits and commits set the pace and slots of 4 K-blocks go faster)
-    static constexpr int kGroupKb = MP == 128 ? (BN == 32 ? 4 : 2) : (kStagesCap >= 12 ? 4 : 1);
+    static constexpr int kGroupKb = GK > 0 ? GK : MP == 128 ? (BN == 32 ? 4 : 2) : (kStagesCap >= 12 ? 4 : 1);
     // the MMA warp waits for a scale group at slot starts and releases it at the
     // group's last K-block: a slot must not span two 4-K-block scale groups
     static_assert(kGroupKb == 1 || kGroupKb == 2 || kGroupKb == 4, "ring slots divide a scale group");
@@ -191,6 +192,9 @@ constexpr int kF32StageBufs = 4;
 constexpr int kGatedBwdBufs = 10;
 // The gated forward epilogue: one box of 32 columns per warp.
 constexpr int kGatedBufs = 2;
+// Its narrow tiles, whose K-blocks are short: ring slots of two (128 rows, inner 2048, K = 7168: 14.0 us
+// against 18.0 with one and 15.4 with four, which leave a ring of two).
+constexpr int kGatedFewKb = 2;
 // CTAs of a cluster: a pair; gated forward: the pairs whose tiles make up a group of 128 columns of h.
 template <int BN, int LAY>
 constexpr int kBs2Cluster = (LAY & kLayGated) ? 512 / BN : 2;
@@ -201,7 +205,7 @@ constexpr bool kCTile = WITH_C && !F32 && MP == 256 && BN % 32 == 0 && BN <= 256
 template <int BN, int MP, int LAY, bool F32, bool WITH_C = false>
 using Bs2Cfg = Bs2Config<BN, MP, (LAY & 2) != 0, (LAY & 4) != 0,
                          (LAY & kLayGatedBwd) ? kGatedBwdBufs : (LAY & kLayGated) ? kGatedBufs : F32 ? kF32StageBufs : 0, (LAY & 8) != 0,
-                         kCTile<BN, MP, WITH_C, F32>>;
+                         kCTile<BN, MP, WITH_C, F32>, (LAY & kLayGated) && BN < 256 ? kGatedFewKb : 0>;
 
 struct PairTile {
     int a_row0;      // this CTA's first row in the 2-D view of A (and D)
