@@ -29,8 +29,10 @@ namespace {
 constexpr float kScale = 4096.0f;          // of all FP16 planes
 constexpr int kTile = 256;                 // rows and columns of a pair tile
 constexpr int kKBlock = 64;                // K of a stage: 128 bytes
-constexpr int kStages = 5;
-constexpr int kStageBytes = 2 * 128 * 128; // A and B: 128 rows of 128 bytes each
+// Ring: stages of 128 rows of A and up to as much of B; as many as fit, 5 of 32 KB with tiles of 256
+// columns, 6 of 24 KB with narrower ones, whose K-blocks are bound by the bytes in flight
+constexpr int kMaxStages = 6;
+constexpr int kRingBytes = 5 * 32768;
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 // Epilogue: an epilogue warp's 32 rows x 128 columns of a tile in chunks of 32 columns; a chunk
@@ -38,12 +40,21 @@ constexpr int kEpiWarps = 8;
 constexpr int kBoxBytes = 32 * 64;
 constexpr int kSlotBytes = 2 * kBoxBytes;
 constexpr int kEpiBytes = kEpiWarps * 2 * kSlotBytes;
-constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiBytes + 128 * kEpiWarps + 512;
+constexpr int kSmem = 1024 + kRingBytes + kEpiBytes + 128 * kEpiWarps + 512;
 
 // ------------------------------------------------------------------ norm and split
 
-// Sum of squares of a matrix, as partial sums of CTAs: three FP32 accumulators (values below 2^-40,
-// above 2^40, between, the outer ones scaled), so that no square over- or underflows, then FP64.
+template <bool BF16>
+__device__ __forceinline__ float g_value(const char *g, int64_t at) {
+    return BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(g)[at]) << 16)
+                : reinterpret_cast<const float *>(g)[at];
+}
+
+// Sum of squares of a matrix, as partial sums of CTAs.  A thread adds the squares of its 32 values of a segment
+// in FP32, beside their largest magnitude; where that lies outside 2^-40 .. 2^40 (0 aside), the
+// segment is added again with its values scaled into the range, so that no square over- or
+// underflows.  The segments' sums are FP32 for 32 of them, then FP64 (64-bit sums throughout
+// would take most of the kernel's time: a few a clock and SM).
 template <bool BF16>
 __global__ void __launch_bounds__(256) dg_ns_norm_kernel(const __grid_constant__ NsParams p) {
     grid_launch_dependents();
@@ -51,84 +62,99 @@ __global__ void __launch_bounds__(256) dg_ns_norm_kernel(const __grid_constant__
     const int64_t batch = blockIdx.y;
     const char *g = static_cast<const char *>(p.g) + batch * p.g_batch * (BF16 ? 2 : 4);
     double total = 0.0;
-    float mid = 0.f, big = 0.f, small = 0.f;
-    auto add = [&](float v) {
-        const float m = fabsf(v);
-        if (m >= 0x1p-40f && m <= 0x1p40f) mid = fmaf(v, v, mid);
-        else if (m < 0x1p-40f) { const float s = v * 0x1p80f; small = fmaf(s, s, small); }
-        else { const float s = v * 0x1p-70f; big = fmaf(s, s, big); }   // (NaN here too)
-    };
-    auto flush = [&]() {
-        total += static_cast<double>(mid) + static_cast<double>(small) * 0x1p-160 + static_cast<double>(big) * 0x1p140;
-        mid = big = small = 0.f;
-    };
+    float run = 0.f;
     // dense matrices are one long row; a CTA takes segments of a row
     const int64_t len = p.dense ? static_cast<int64_t>(p.rows) * p.cols : p.cols;
     const int64_t rows = p.dense ? 1 : p.rows;
-    constexpr int64_t kSeg = 8192;
+    constexpr int kSeg = 8192, V = BF16 ? 8 : 4;
     const int64_t segs = (len + kSeg - 1) / kSeg;
+    int since = 0;
     for (int64_t s = blockIdx.x; s < rows * segs; s += gridDim.x) {
-        const int64_t row = s / segs, c0 = (s - row * segs) * kSeg;
-        const int64_t n = len - c0 < kSeg ? len - c0 : kSeg;
+        const int64_t row = segs == 1 ? s : s / segs, c0 = (s - row * segs) * kSeg;
+        const int n = static_cast<int>(len - c0 < kSeg ? len - c0 : kSeg);
         const char *at = g + (row * p.ldg + c0) * (BF16 ? 2 : 4);
-        constexpr int V = BF16 ? 8 : 4;
-        if ((reinterpret_cast<uintptr_t>(at) & 15u) == 0) {
-            const int64_t nv = n / V;
-#pragma unroll 4
-            for (int64_t i = threadIdx.x; i < nv; i += 256) {
-                const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(at) + i);
-                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        const bool vec = (reinterpret_cast<uintptr_t>(at) & 15u) == 0;
+        float sum, amax;
+        auto segment = [&](float scale) {
+            sum = amax = 0.f;
+            auto add = [&](float v) {
+                v *= scale;
+                sum = fmaf(v, v, sum);
+                amax = fmaxf(amax, fabsf(v));
+            };
+            int i = threadIdx.x;
+            if (vec) {
+#pragma unroll 8
+                for (; i < n / V; i += 256) {
+                    const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(at) + i);
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (BF16) {
-                        add(__uint_as_float(x[j] << 16));
-                        add(__uint_as_float(x[j] & 0xFFFF0000u));
-                    } else {
-                        add(__uint_as_float(x[j]));
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (BF16) {
+                            add(__uint_as_float(x[j] << 16));
+                            add(__uint_as_float(x[j] & 0xFFFF0000u));
+                        } else {
+                            add(__uint_as_float(x[j]));
+                        }
                     }
                 }
+                i = n / V * V + threadIdx.x;
             }
-            const int64_t i = nv * V + threadIdx.x;
-            if (i < n)
-                add(BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(at)[i]) << 16)
-                         : reinterpret_cast<const float *>(at)[i]);
+            for (; i < n; i += 256) add(g_value<BF16>(at, i));
+        };
+        segment(1.0f);
+        if (amax > 0x1p40f) {
+            segment(0x1p-70f);
+            total += static_cast<double>(sum) * 0x1p140;
+        } else if (amax < 0x1p-40f && amax > 0.f) {
+            segment(0x1p80f);
+            total += static_cast<double>(sum) * 0x1p-160;
         } else {
-            for (int64_t i = threadIdx.x; i < n; i += 256)
-                add(BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(at)[i]) << 16)
-                         : reinterpret_cast<const float *>(at)[i]);
+            run += sum;   // (a NaN stays one)
         }
-        flush();
+        if (++since == 32) {
+            total += run;
+            run = 0.f;
+            since = 0;
+        }
     }
     __shared__ double part[8];
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = total;
+    // (FP32 over a warp: five more roundings of 2^-24)
+    for (int o = 16; o > 0; o >>= 1) run += __shfl_xor_sync(0xFFFFFFFFu, run, o);
+    if (__any_sync(0xFFFFFFFFu, total != 0.0))
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = total + run;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < 8; ++w) total += part[w];
+        total = 0.0;
+        for (int w = 0; w < 8; ++w) total += part[w];
         p.partial[batch * p.num_partial + blockIdx.x] = total;
     }
 }
 
 // 2^12 / (norm + eps) in two factors, so that neither leaves FP32's range.  Every CTA adds the
-// partial sums in the same order.
+// partial sums in the same order; one thread does the 64-bit arithmetic.
 __device__ __forceinline__ void norm_factors(const NsParams &p, int64_t batch, float &f1, float &f2) {
-    __shared__ double sum;
+    __shared__ float factors[2];
     if (threadIdx.x < 32) {
         double s = 0.0;
         for (int i = threadIdx.x; i < p.num_partial; i += 32) s += p.partial[batch * p.num_partial + i];
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        if (threadIdx.x == 0) sum = s;
+        if (threadIdx.x == 0) {
+            const double norm = sqrt(s) + static_cast<double>(p.eps);
+            int e = 0;
+            // (not norm > 0: a NaN stays one)
+            const double mant = norm == 0.0 ? 0.0 : frexp(static_cast<double>(kScale) / norm, &e);
+            const int e1 = e / 2;
+            factors[0] = static_cast<float>(ldexp(1.0, e1));
+            factors[1] = static_cast<float>(ldexp(mant, e - e1));
+        }
     }
     // (the products' grid counter and abort word, which follow in the stream)
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.sync = 0u;
     __syncthreads();
-    const double norm = sqrt(sum) + static_cast<double>(p.eps);
-    int e = 0;
-    // (not norm > 0: a NaN stays one)
-    const double mant = norm == 0.0 ? 0.0 : frexp(static_cast<double>(kScale) / norm, &e);
-    const int e1 = e / 2;
-    f1 = static_cast<float>(ldexp(1.0, e1));
-    f2 = static_cast<float>(ldexp(mant, e - e1));
+    f1 = factors[0];
+    f2 = factors[1];
 }
 
 // Two values as high and low FP16 pairs.
@@ -137,12 +163,6 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
     const __half2 l = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&l);
-}
-
-template <bool BF16>
-__device__ __forceinline__ float g_value(const char *g, int64_t at) {
-    return BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(g)[at]) << 16)
-                : reinterpret_cast<const float *>(g)[at];
 }
 
 // X0 as high and low planes [lo][ldx].  A wide G row by row, 8 values a thread (16-byte loads where
@@ -567,7 +587,8 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
                     }
                 }
                 bulk_commit_group();
-                if constexpr (kLoads > 0) {
+                // two chunks on: of this tile, or of this pair's next (a phase ends with a wait for all stores)
+                if (kLoads > 0 && c + 2 < my_chunks) {
                     bulk_wait_group_read<0>();
                     load_chunk(c + 2);
                 }
@@ -611,13 +632,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    uint8_t *smem_a = smem, *smem_b = smem + kStages * 16384;
-    uint8_t *smem_epi = smem + kStages * kStageBytes;
+    // a stage: A's 16 KB, then B's largest part
+    const int b_sym = p.bn_sym * 64, b_update = p.bn_update == kTile ? 16384 : 8192;
+    const int stage_bytes = 16384 + (b_sym > b_update ? b_sym : b_update);
+    const int stages = kRingBytes / stage_bytes < kMaxStages ? kRingBytes / stage_bytes : kMaxStages;
+    uint8_t *smem_epi = smem + kRingBytes;
     float *diag_out = reinterpret_cast<float *>(smem_epi + kEpiBytes);   // 32 an epilogue warp
     uint64_t *bars = reinterpret_cast<uint64_t *>(diag_out + 32 * kEpiWarps);
-    uint64_t *full_bar = bars;                   // [kStages] leader: both CTAs' stages landed
-    uint64_t *empty_bar = full_bar + kStages;    // [kStages] both: MMAs done with the stage
-    uint64_t *tfull_bar = empty_bar + kStages;   // [2] both: accumulator complete
+    uint64_t *full_bar = bars;                   // [stages] leader: both CTAs' stages landed
+    uint64_t *empty_bar = full_bar + kMaxStages; // [stages] both: MMAs done with the stage
+    uint64_t *tfull_bar = empty_bar + kMaxStages;   // [2] both: accumulator complete
     uint64_t *tempty_bar = tfull_bar + 2;        // [2] leader: both epilogues drained
     uint64_t *drain_bar = tempty_bar + 2;
     uint64_t *phase_bar = drain_bar + 1;         // the grid has finished the phase before
@@ -690,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     } else {
                         if (elect_one()) {
                             const uint32_t fb = leader_full + slot * 8;
-                            uint8_t *sa = smem_a + slot * 16384, *sb = smem_b + slot * 16384;
+                            uint8_t *sa = smem + slot * stage_bytes, *sb = sa + 16384;
                             const int n = n0 + rank * (f.bn / 2);
                             if (leader) mbar_arrive_expect_tx(&full_bar[slot], 2 * stage);
                             tma_load_3d_pair(sa, ta, fb, kb * kKBlock, m0 + rank * 128, b);
@@ -704,20 +728,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         __syncwarp();
                         issued |= 1u << slot;
                     }
-                    if (++slot == kStages) { slot = 0; phase ^= 1; }
+                    if (++slot == stages) { slot = 0; phase ^= 1; }
                 }
             }
         }
     prod_done:
         if (lane == 0 && leader)
-            for (int s = 0; s < kStages; ++s)
+            for (int s = 0; s < stages; ++s)
                 if (issued & (1u << s)) mbar_wait_drain(&full_bar[s], s < slot ? phase : phase ^ 1, ctl);
         __syncwarp();
     } else if (warp == 1) {
         if (leader) {
             int slot = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            const uint64_t a0 = make_desc_kmajor_sw128(smem_u32(smem_a));
+            const uint64_t a0 = make_desc_kmajor_sw128(smem_u32(smem));
             for (int i = 0; i < phases; ++i) {
                 const NsPhase f = ns_phase(p, i);
                 const bool b_mn = f.mode >= kNsUpdate;
@@ -725,8 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(f.bn >> 3) << 17) | ((kTile >> 4) << 24) |
                                        (b_mn ? 1u << 16 : 0u);
                 // (MN-major: the two 64-column atoms 8192 bytes apart, 8 K rows 1024)
-                const uint64_t b0 = b_mn ? make_smem_desc(smem_u32(smem_b), 8192, 1024, kSwizzle128B)
-                                         : make_desc_kmajor_sw128(smem_u32(smem_b));
+                const uint64_t b0 = b_mn ? make_smem_desc(smem_u32(smem) + 16384, 8192, 1024, kSwizzle128B)
+                                         : make_desc_kmajor_sw128(smem_u32(smem) + 16384);
                 const uint64_t step_b = b_mn ? (2048 >> 4) : 2;   // 16 K: 16 rows, or 32 bytes along a row
                 for (int t = pair_id; t < f.num_tiles; t += num_pairs) {
                     if (!mbar_wait_cluster_warp(&tempty_bar[acc], acc_phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto mma_done;
@@ -738,13 +762,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         if (!mbar_wait_warp(&full_bar[slot], phase, ctl, DG_DEV_TIMEOUT)) goto mma_done;
                         tc_fence_after_sync();
                         if (elect_one()) {
-                            const uint64_t a = a0 + slot * (16384 >> 4), b = b0 + slot * (16384 >> 4);
+                            const uint64_t a = a0 + slot * (stage_bytes >> 4), b = b0 + slot * (stage_bytes >> 4);
 #pragma unroll
                             for (int s = 0; s < 4; ++s) mma_f16_pair(d, a + 2 * s, b + step_b * s, idesc, (kb | s) != 0);
                             tc_commit_pair(&empty_bar[slot], 0x3);
                         }
                         __syncwarp();
-                        if (++slot == kStages) { slot = 0; phase ^= 1; }
+                        if (++slot == stages) { slot = 0; phase ^= 1; }
                     }
                     if (elect_one()) tc_commit_pair(&tfull_bar[acc], 0x3);
                     __syncwarp();
