@@ -560,7 +560,12 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
             }
             if constexpr (SYM) {
                 on_diag *= 1.0f / kScale;   // (as it is, not scaled)
-                if (col == row0) st.diag[lane] = MODE == kNsGram ? on_diag : fmaf(diag, fmaf(p.cc, diag, p.cb), on_diag);
+                if (col == row0) {
+                    // (the copy of the diagonal chunk before, which may be the chunk before, has read it)
+                    if (lane == 0) bulk_wait_group_read<0>();
+                    __syncwarp();
+                    st.diag[lane] = MODE == kNsGram ? on_diag : fmaf(diag, fmaf(p.cc, diag, p.cb), on_diag);
+                }
             }
             if constexpr (MODE == kNsLast) {
                 if (p.out_tma && p.rows > p.cols) {

@@ -189,3 +189,17 @@ def test_lost_load_is_reported():
     dg.dg_newton_schulz(g, out, status=status)
     close(out, plain(g.cpu()))
     assert int(status) == 0
+
+
+@pytest.mark.parametrize("b,r,c", [(700, 40, 64), (300, 20, 33), (200, 130, 70)])
+def test_many_small_matrices(b, r, c):
+    """More matrices than CTA pairs, so that a pair goes from one diagonal tile to the next."""
+    g = torch.stack([gradient(r, c, j) * 2.0 ** (j % 7) for j in range(b)])
+    out = torch.empty(b, r, c, dtype=torch.bfloat16, device="cuda")
+    dg.dg_newton_schulz(g.cuda(), out)
+    for j in range(0, b, 7):
+        close(out[j], plain(g[j]), what=f"matrix {j}")
+    one = torch.empty(r, c, dtype=torch.bfloat16, device="cuda")
+    for j in (0, 75, 76, 152, b - 1):
+        dg.dg_newton_schulz(g[j].cuda(), one)
+        assert torch.equal(one, out[j])
