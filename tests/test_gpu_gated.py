@@ -7,10 +7,11 @@ the |g| < 32 of these inputs (2^-21 + 2^-23 |g|, and three more FP32 roundings).
 import pytest
 import torch
 
-from _ffn import block_operand, cdiv, gated64, gated_backward64, pack, rows_operand, scale64
+from tests._ffn import block_operand, cdiv, gated64, gated_backward64, pack, rows_operand, scale64
 from block_scaled_fp8_gb300 import binding as dg
 
-pytestmark = pytest.mark.gpu
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
 BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
 
 

@@ -14,7 +14,8 @@ import torch
 
 from block_scaled_fp8_gb300 import binding as dg
 
-pytestmark = pytest.mark.gpu
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
 COEF, EPS = (3.4445, -4.7750, 2.0315), 1e-7
 
 

@@ -5,10 +5,11 @@ so nothing here has a tolerance.  The comparison's own rounding is torch's CPU c
 import pytest
 import torch
 
-from _ffn import cdiv, pack, scale64
+from tests._ffn import cdiv, pack, scale64
 from block_scaled_fp8_gb300 import binding as dg
 
-pytestmark = pytest.mark.gpu
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
 E4M3 = torch.float8_e4m3fn
 
 

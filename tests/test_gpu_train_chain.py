@@ -9,10 +9,11 @@ W2, dy, dgu), whose errors are independent: sqrt(6) 2^-4 / sqrt(3) = 0.089 of it
 import pytest
 import torch
 
-from _ffn import cdiv
+from tests._ffn import cdiv
 from block_scaled_fp8_gb300 import binding as dg
 
-pytestmark = pytest.mark.gpu
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
 BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
 E, I, K = 4, 272, 384
 COUNTS = [130, 0, 256, 77]                       # rows of each expert, padded with zeros to whole blocks
