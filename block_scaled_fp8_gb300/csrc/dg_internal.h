@@ -172,7 +172,8 @@ struct NsParams {
     int out_tma;            // the output's rows can be stored by TMA
     double *partial;        // [batch][num_partial] sums of squares
     int num_partial;
-    uint64_t *sync;         // low half: the products' grid counter; high half: set by a CTA that gives up
+    int group0;             // matrices of the first group; the rest, if any, make a second
+    uint64_t *sync;         // [2] low half: a group's grid counter; high half: set by a CTA that gives up
     int dense;              // a matrix's rows of G follow one another
 };
 int64_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);

@@ -151,7 +151,7 @@ __device__ __forceinline__ void norm_factors(const NsParams &p, int64_t batch, f
         }
     }
     // (the products' grid counter and abort word, which follow in the stream)
-    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.sync = 0u;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 2) p.sync[threadIdx.x] = 0u;
     __syncthreads();
     f1 = factors[0];
     f2 = factors[1];
@@ -302,10 +302,13 @@ __device__ __forceinline__ float2 half2_values(uint32_t w) { return __half22floa
 // The epilogue's own operands (A; the planes of X) come by TMA into the boxes that the results go
 // out from, two chunks ahead.
 //
-// All products of all steps are one cooperative launch: each is a phase, and between phases the
-// grid waits for all CTAs' results (one arrival a CTA on a counter in the workspace, polled by the
-// producer warps, with a limit).  As launches of their own they cost 7.5 us each however small
+// All products of all steps are one cooperative launch: each is a phase, and a phase's tiles wait for all
+// tiles of the one before (a counter of finished tiles in the workspace, polled by the producer
+// warps, with a limit).  As launches of their own they cost 7.5 us each however small
 // (64x64, five steps: 127 us).
+// Several large matrices go in two groups with a counter each, the second a phase behind: while one
+// group waits for its phase's last tiles, the other has work, and the few tiles of a symmetric
+// product run beside the many of an update.
 struct NsMaps {
     CUtensorMap xk[2], xn[2];   // X's high planes along K (128 rows a box), and as [K][N]
     CUtensorMap a, b;           // A, B along K
@@ -316,9 +319,12 @@ struct NsMaps {
 // What a phase works on.
 struct NsPhase {
     int mode, step, cols, bn, tm, tn, per, num_tiles, nkb;
+    int b0;      // the group's first matrix
+    int first;   // this pair's first tile
 };
 
-__device__ __forceinline__ NsPhase ns_phase(const NsParams &p, int i) {
+// Phase i of group g, or of no tiles where it has no such phase.
+__device__ __forceinline__ NsPhase ns_shape(const NsParams &p, int i, int g) {
     NsPhase f;
     f.step = i / 3;
     f.mode = i % 3;
@@ -331,15 +337,36 @@ __device__ __forceinline__ NsPhase ns_phase(const NsParams &p, int i) {
     // symmetric: the column tiles of diagonal block q (kTile / bn of them) have row tiles 0..q
     const int r = kTile / f.bn, q = f.tn / r;
     f.per = sym ? r * (q * (q + 1) / 2) + (f.tn - r * q) * (q + 1) : f.tm * f.tn;
-    f.num_tiles = f.per * p.batch;
+    f.b0 = g == 0 ? 0 : p.group0;
+    f.num_tiles = i < 0 || i >= 3 * p.steps ? 0 : f.per * (g == 0 ? p.group0 : p.batch - p.group0);
     f.nkb = ((f.mode == kNsGram ? p.hi : p.lo) + kKBlock - 1) / kKBlock;
     return f;
+}
+
+// The phase that group g has in turn `turn`: its phase turn - g.  The second group's tiles go on from
+// the pair after the first group's last.
+__device__ __forceinline__ NsPhase ns_phase(const NsParams &p, int turn, int g, int pair_id, int num_pairs) {
+    NsPhase f = ns_shape(p, turn - g, g);
+    f.first = pair_id;
+    if (g > 0) {
+        f.first = pair_id - ns_shape(p, turn, 0).num_tiles % num_pairs;
+        if (f.first < 0) f.first += num_pairs;
+    }
+    return f;
+}
+
+// What group g's counter has come to when its phases before phase i are finished: both CTAs of a
+// tile's pair count it.
+__device__ __forceinline__ uint32_t ns_finished(const NsParams &p, int i, int g) {
+    const uint32_t sym = ns_shape(p, 0, g).num_tiles, update = ns_shape(p, 2, g).num_tiles, r = i % 3;
+    return 2u * (i / 3 * (2u * sym + update) + r * sym);
 }
 
 // Tile t of a phase: (batch, m, n), the m tiles of a column of tiles first
 __device__ __forceinline__ void ns_locate(const NsPhase &f, int t, int &b, int &m0, int &n0) {
     b = t / f.per;
     const int i = t - b * f.per;
+    b += f.b0;
     if (f.mode < kNsUpdate) {
         const int r = kTile / f.bn, h = i / r;   // q(q+1)/2 <= h < (q+1)(q+2)/2
         int q = static_cast<int>((sqrtf(8.0f * static_cast<float>(h) + 1.0f) - 1.0f) * 0.5f);
@@ -359,7 +386,7 @@ struct NsEpilogue {
     const NsParams &p;
     const WaitCtl &ctl;
     uint32_t ew, quad, half, lane, tmem_base, leader_tempty;
-    int rank, pair_id, num_pairs;
+    int rank, num_pairs;
     uint8_t *slots;
     float *diag;        // 32 values on their way out
     uint64_t *landed, *tfull_bar;
@@ -377,7 +404,7 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
     const NsParams &p = st.p;
     const WaitCtl &ctl = st.ctl;
     const uint32_t lane = st.lane, quad = st.quad, half = st.half;
-    const int num_tiles = ph.num_tiles, num_pairs = st.num_pairs, pair_id = st.pair_id;
+    const int num_tiles = ph.num_tiles, num_pairs = st.num_pairs, first = ph.first;
     const int rows = p.lo, cols = ph.cols;
     uint8_t *const slots = st.slots;
     uint64_t *const landed = st.landed;
@@ -390,12 +417,12 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
     auto unit = [](uint8_t *box, int r, int h) { return reinterpret_cast<uint4 *>(box + r * 64 + ((h ^ ((r >> 1) & 3)) << 4)); };
     // chunk c of this pair in this phase (chunk c % chunks of its tile c / chunks): the epilogue's operands, into
     // slot c & 1; nothing past the last
-    const int my_chunks = pair_id < num_tiles ? (num_tiles - pair_id + num_pairs - 1) / num_pairs * chunks : 0;
+    const int my_chunks = first < num_tiles ? (num_tiles - first + num_pairs - 1) / num_pairs * chunks : 0;
     auto load_chunk = [&](int c) {
         if constexpr (kLoads > 0) {
             if (c >= my_chunks) return;
             int b, m0, n0;
-            ns_locate(ph, pair_id + c / chunks * num_pairs, b, m0, n0);
+            ns_locate(ph, first + c / chunks * num_pairs, b, m0, n0);
             uint8_t *box = slots + (c & 1) * kSlotBytes;
             const int x = n0 + col_off + 32 * (c % chunks), y = m0 + row_off;
             mbar_arrive_expect_tx(&landed[c & 1], kLoads * kBoxBytes);
@@ -411,7 +438,7 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
         pending = my_chunks >= 2 ? 3 : my_chunks;
     }
     int c = 0;
-    for (int t = pair_id; t < num_tiles; t += num_pairs) {
+    for (int t = first; t < num_tiles; t += num_pairs) {
         int b, m0, n0;
         ns_locate(ph, t, b, m0, n0);
         const int row0 = m0 + row_off, row = row0 + static_cast<int>(lane);
@@ -609,15 +636,14 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
     return true;
 }
 
-// Waits until the counter (the low half of the word) has come to `target`, all CTAs' arrivals of the
-// phases before; false if it does not within the limit or some CTA has given up (the high half).
-__device__ __noinline__ bool ns_grid_wait(const NsParams &p, uint32_t target, const WaitCtl &ctl) {
+// Waits until a group's counter (the low half of its word) has come to `target`; false if it does not within the limit or some CTA has given up (the high half).
+__device__ __noinline__ bool ns_grid_wait(const uint64_t *counter, uint32_t target, const WaitCtl &ctl) {
     const uint64_t t0 = global_timer_ns();
     while (true) {
 #pragma unroll 1
         for (int i = 0; i < 64; ++i) {
             uint64_t w;
-            asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(p.sync) : "memory");
+            asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(w) : "l"(counter) : "memory");
             if (static_cast<int32_t>(static_cast<uint32_t>(w) - target) >= 0) return true;
             if ((w >> 32) != 0 || *ctl.abort) {
                 *ctl.abort = 1;
@@ -649,25 +675,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint64_t *tfull_bar = empty_bar + kMaxStages;   // [2] both: accumulator complete
     uint64_t *tempty_bar = tfull_bar + 2;        // [2] leader: both epilogues drained
     uint64_t *drain_bar = tempty_bar + 2;
-    uint64_t *phase_bar = drain_bar + 1;         // the grid has finished the phase before
-    uint64_t *in_bar = phase_bar + 1;            // [kEpiWarps][2] an epilogue warp's boxes landed
+    uint64_t *phase_bar = drain_bar + 1;         // [2] the grid has finished the group's phase before
+    uint64_t *in_bar = phase_bar + 2;            // [kEpiWarps][2] an epilogue warp's boxes landed
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(in_bar + 2 * kEpiWarps);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    uint32_t *done = tmem_holder + 2;            // epilogue warps that have finished phases
+    uint32_t *done = tmem_holder + 2;            // [2] epilogue warps that have finished a group's phases
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
     const int rank = static_cast<int>(cluster_ctarank());
     const bool leader = rank == 0;
     const int pair_id = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
-    const int phases = 3 * p.steps;
+    const int phases = 3 * p.steps, groups = p.group0 < p.batch ? 2 : 1, turns = phases + groups - 1;
 
     if (warp == 0) {
         for (uint64_t *b = bars + lane; b < in_bar + 2 * kEpiWarps; b += 32)
             mbar_init(b, b >= tempty_bar && b < tempty_bar + 2 ? 2 * kEpiWarps : 1);
         if (lane == 0) {
             *abort_flag = 0;
-            *done = 0u;
+            done[0] = done[1] = 0u;
         }
         fence_mbar_init();
         if (lane == 0) {
@@ -691,15 +717,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         int slot = 0;
         uint32_t phase = 0, issued = 0;
         bool drop = (p.debug_flags & DG_DEBUG_DROP_ONE_LOAD) && pair_id == 0;
-        for (int i = 0; i < phases; ++i) {
-            const NsPhase f = ns_phase(p, i);
+        for (int turn = 0; turn < turns; ++turn)
+        for (int g = 0; g < groups; ++g) {
+            const int i = turn - g;
+            const NsPhase f = ns_phase(p, turn, g, pair_id, num_pairs);
+            if (f.first >= f.num_tiles) continue;   // (nothing to do: nothing to wait for)
             if (i > 0) {
                 bool ok = true;
                 if (lane == 0) {
-                    ok = ns_grid_wait(p, static_cast<uint32_t>(i) * gridDim.x, ctl);
+                    ok = ns_grid_wait(p.sync + g, ns_finished(p, i, g), ctl);
                     // the other CTAs' results, written by TMA and plain stores, are read by TMA
                     asm volatile("fence.proxy.async.global;" ::: "memory");
-                    if (ok) mbar_arrive(phase_bar);
+                    if (ok) mbar_arrive(phase_bar + g);
                 }
                 if (!__all_sync(0xFFFFFFFFu, ok)) goto prod_done;
             }
@@ -709,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             // this CTA's half of the columns: bn / 2 rows of 64 K, or boxes of 64 columns (one swizzle
             // atom, of which the MMA reads bn / 2 where that is less) x 64 K rows
             const uint32_t stage = 16384u + (b_mn ? (f.bn == kTile ? 16384u : 8192u) : static_cast<uint32_t>(f.bn) * 64u);
-            for (int t = pair_id; t < f.num_tiles; t += num_pairs) {
+            for (int t = f.first; t < f.num_tiles; t += num_pairs) {
                 int b, m0, n0;
                 ns_locate(f, t, b, m0, n0);
                 for (int kb = 0; kb < f.nkb; ++kb) {
@@ -747,8 +776,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             int slot = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             const uint64_t a0 = make_desc_kmajor_sw128(smem_u32(smem));
-            for (int i = 0; i < phases; ++i) {
-                const NsPhase f = ns_phase(p, i);
+            for (int turn = 0; turn < turns; ++turn)
+            for (int g = 0; g < groups; ++g) {
+                const NsPhase f = ns_phase(p, turn, g, pair_id, num_pairs);
                 const bool b_mn = f.mode >= kNsUpdate;
                 // FP16 x FP16 -> FP32, M = 256, N = bn (bit 16: B MN-major)
                 const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(f.bn >> 3) << 17) | ((kTile >> 4) << 24) |
@@ -757,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const uint64_t b0 = b_mn ? make_smem_desc(smem_u32(smem) + 16384, 8192, 1024, kSwizzle128B)
                                          : make_desc_kmajor_sw128(smem_u32(smem) + 16384);
                 const uint64_t step_b = b_mn ? (2048 >> 4) : 2;   // 16 K: 16 rows, or 32 bytes along a row
-                for (int t = pair_id; t < f.num_tiles; t += num_pairs) {
+                for (int t = f.first; t < f.num_tiles; t += num_pairs) {
                     if (!mbar_wait_cluster_warp(&tempty_bar[acc], acc_phase ^ 1, ctl, DG_DEV_TIMEOUT)) goto mma_done;
                     tc_fence_after_sync();
                     const uint32_t d = tmem_base + acc * kTile;
@@ -789,31 +819,39 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else {
         const uint32_t ew = warp - 2;
-        NsEpilogue st{p, ctl, ew, warp & 3, ew >> 2, lane, tmem_base, mapa_shared(smem_u32(tempty_bar), 0), rank, pair_id,
-                      num_pairs, smem_epi + ew * 2 * kSlotBytes, diag_out + 32 * ew, in_bar + 2 * ew, tfull_bar, 0, 0, 0u, 0u};
-        for (int i = 0; i < phases; ++i) {
-            const NsPhase f = ns_phase(p, i);
+        NsEpilogue st{p, ctl, ew, warp & 3, ew >> 2, lane, tmem_base, mapa_shared(smem_u32(tempty_bar), 0), rank, num_pairs,
+                      smem_epi + ew * 2 * kSlotBytes, diag_out + 32 * ew, in_bar + 2 * ew, tfull_bar, 0, 0, 0u, 0u};
+        bool ok = true;
+        uint32_t waited = 0;   // parities of phase_bar
+        for (int turn = 0; turn < turns && ok; ++turn)
+        for (int g = 0; g < groups && ok; ++g) {
+            const int i = turn - g;
+            const NsPhase f = ns_phase(p, turn, g, pair_id, num_pairs);
+            if (f.first >= f.num_tiles) continue;
             if (i > 0) {
-                if (!mbar_wait_warp(phase_bar, (i - 1) & 1, ctl, DG_DEV_TIMEOUT)) break;
+                ok = mbar_wait_warp(phase_bar + g, (waited >> g) & 1u, ctl, DG_DEV_TIMEOUT);
+                waited ^= 1u << g;
+                if (!ok) break;
                 asm volatile("fence.proxy.async.global;" ::: "memory");   // (as the producer's)
             }
             const CUtensorMap *xh = &maps.xh[f.step & 1], *next = &maps.xh[(f.step & 1) ^ 1];
-            bool ok;
             if (f.mode == kNsGram) ok = ns_epilogue<kNsGram>(st, f, nullptr, nullptr, &maps.ea, nullptr);
             else if (f.mode == kNsPoly) ok = ns_epilogue<kNsPoly>(st, f, &maps.ea, nullptr, &maps.eb, nullptr);
             else if (f.mode == kNsUpdate) ok = ns_epilogue<kNsUpdate>(st, f, xh, &maps.xl, next, &maps.xl);
             else ok = ns_epilogue<kNsLast>(st, f, xh, &maps.xl, &maps.out, nullptr);
             if (!ok) break;
-            // The CTA's last warp to finish the phase arrives for it.  A warp's results (its boxes, complete
-            // since the wait for them, and the lanes' plain stores) are released to the CTA by its count,
-            // and by the last warp's arrival, which has acquired all counts, to the grid: one release
-            // at the grid's scope, which costs about a microsecond, instead of one a warp and another.
+            // The CTA's last warp to finish the phase counts its tiles.  A warp's results (its boxes,
+            // complete since the wait for them) are released to the CTA by its count, and by the last
+            // warp's, which has acquired the others', to the grid: one release at the grid's scope,
+            // which costs about a microsecond, instead of one a warp and another.
             __syncwarp();
             if (lane == 0 && i + 1 < phases) {
                 uint32_t before;
-                asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(done)) : "memory");
+                asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(done + g)) : "memory");
                 if (before % kEpiWarps == kEpiWarps - 1)
-                    asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(p.sync) : "memory");
+                    asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(p.sync + g),
+                                 "l"(static_cast<uint64_t>((f.num_tiles - f.first + num_pairs - 1) / num_pairs))
+                                 : "memory");
             }
         }
         // (an aborted loop leaves no load landing in shared memory after the CTA is gone)
@@ -825,7 +863,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         __syncwarp();
     }
     // a CTA that gave up tells the others
-    if (lane == 0 && *abort_flag) atomicOr(reinterpret_cast<uint32_t *>(p.sync) + 1, 1u);
+    if (lane == 0 && *abort_flag)
+        for (int g = 0; g < groups; ++g) atomicOr(reinterpret_cast<uint32_t *>(p.sync + g) + 1, 1u);
     tc_fence_before_sync();
     __syncthreads();
     cluster_sync();
@@ -985,6 +1024,11 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
                 encode_plane(&maps.out, p.out, p.cols, p.rows, p.ldo, p.batch == 1 ? p.ldo * p.rows : p.out_batch, p.batch, 32, true);
     if (!p.out_tma) maps.out = maps.ea;   // not used
     p.steps = steps;
+    // Two groups where the symmetric products have more than a wave of tiles, whose last wave the other
+    // group's tiles fill, and K enough to be worth the longer chain (3x2048x7168: 1293 us against 1379,
+    // 4x2048x7168: 1414 / 1463, 16x1024x4096: 1329 / 1346); else one (2x2048x7168: 777 us against 822 with
+    // two, 3x1408x2048: 320 / 367, 700x40x64: 294 / 305).
+    p.group0 = tiles_sym > pairs && p.hi >= 2048 ? p.batch - p.batch / 2 : p.batch;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;   // the CTAs wait for one another

@@ -204,3 +204,24 @@ def test_many_small_matrices(b, r, c):
     for j in (0, 75, 76, 152, b - 1):
         dg.dg_newton_schulz(g[j].cuda(), one)
         assert torch.equal(one, out[j])
+
+
+@pytest.mark.parametrize("b", [9, 10])
+def test_two_groups(b):
+    """Enough large matrices for two groups of phases, of equal and of unequal numbers."""
+    r, c = 1024, 2064
+    g = torch.randn(b, r, c, generator=torch.Generator().manual_seed(b)).cuda()
+    out = torch.empty(b, r, c, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dg.dg_newton_schulz(g, out, steps=3, status=status)
+    assert int(status) == 0
+    one = torch.empty(r, c, dtype=torch.bfloat16, device="cuda")
+    for j in (0, b // 2, b - 1):
+        dg.dg_newton_schulz(g[j], one, steps=3)
+        assert torch.equal(one, out[j])
+    x = g[b - 1].double()
+    x = x / (x.norm() + EPS)
+    for _ in range(3):
+        p = x @ x.t()
+        x = COEF[0] * x + (COEF[1] * p + COEF[2] * (p @ p)) @ x
+    close(out[b - 1], x.cpu())
