@@ -4,9 +4,12 @@
 // for X with the short side as its rows (a tall G is transposed on the way in and out).
 //
 // All three products are FP16 x FP16 -> FP32 on CTA pairs (tcgen05 cta_group::2, kind::f16):
-// 256x256 tiles, operands by TMA with 128-byte swizzle in stages of 64 K, two accumulators in
-// TMEM, so that a tile's epilogue runs beside the next tile's MMAs.  Roles: warp 0 producer,
-// warp 1 MMA issuer (leader), warps 2-9 epilogue.
+// 256x256 tiles (or 128 or 64 columns where tiles are few), operands by TMA with 128-byte swizzle in
+// stages of 64 K, two accumulators in TMEM, so that a tile's epilogue runs beside the next tile's
+// MMAs.  Roles: warp 0 producer, warp 1 MMA issuer (leader), warps 2-9 epilogue.
+// Bound by: large matrices, the card's power limit (4x2048x7168: 1.42 ms, 1.46 PFLOP/s of the products that
+// are run, at 1.55 GHz when repeated; the update's planes, 470 MB a step, add 0.05 ms a step); small
+// ones, the chain of a phase, 3.3 us and 0.2 us a K-block (64x64: 4 us a phase).
 //
 // Numbers: the operands are FP16 (11 bits) scaled by 2^12, which keeps the iteration's values
 // (|X| <= 1.3, |A| <= 1.5, |B| <= 3 with the usual coefficients) below 2^14 and their small ones
@@ -14,7 +17,7 @@
 // is the operand, and a X + B X is formed from both.  With X rounded to 11 bits in each step its
 // error is multiplied by a = 3.4 a step in every direction that G hardly has, and comes to 4e-2 of
 // the result for a gradient with a decaying spectrum; with the low plane it is 1e-3 or less
-// (bf16's own rounding of the result: 1.7e-3).  Sums are FP32, the norm FP64.
+// (bf16's own rounding of the result: 1.7e-3).  Sums are FP32, the norm's partial sums FP64.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -296,8 +299,9 @@ __device__ __forceinline__ float2 half2_values(uint32_t w) { return __half22floa
 //
 // The diagonals of A and B are kept apart in FP32 and are 0 in the FP16 matrices: with A = D + R,
 // A A = D D + D R + R D + R R, and B X = diag(B) X + (rest) X.  Near convergence X X^T is close to
-// the identity, so that the diagonal holds most of A and B, and its rounding to 11 bits most of the error: with it
-// in FP32 the result's error is about half (noise 512x512: 7e-4 against 1.5e-3 of its norm).
+// the identity, so that the diagonal holds most of A and B, and its rounding to 11 bits most of
+// the error: with it in FP32 the result's error is about half (noise 512x512: 7e-4 against 1.5e-3
+// of its norm).
 //
 // The epilogue's own operands (A; the planes of X) come by TMA into the boxes that the results go
 // out from, two chunks ahead.
@@ -492,7 +496,7 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
             }
             float on_diag = 0.f;
             // 8 columns at a time, in place: f in units of 2^-12
-    #pragma unroll
+#pragma unroll
             for (int h = 0; h < 4; ++h) {
                 const uint32_t *x = v[h >> 1] + 8 * (h & 1);
                 float f[8];
@@ -506,20 +510,20 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
                     w1[0] = q.x; w1[1] = q.y; w1[2] = q.z; w1[3] = q.w;
                 }
                 if constexpr (MODE == kNsGram) {
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(x[i]) * (1.0f / kScale);
                 } else if constexpr (MODE == kNsPoly) {
                     float dc[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) dc[i] = __shfl_sync(0xFFFFFFFFu, dcol[0], 8 * h + i);
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 r = half2_values(w0[i]);
                         f[2 * i] = fmaf(fmaf(p.cc, diag + dc[2 * i], p.cb), r.x, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i]));
                         f[2 * i + 1] = fmaf(fmaf(p.cc, diag + dc[2 * i + 1], p.cb), r.y, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
                     }
                 } else {
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 hi = half2_values(w0[i]), lo = half2_values(w1[i]);
                         f[2 * i] = fmaf(p.ca + diag, hi.x + lo.x, (1.0f / kScale) * __uint_as_float(x[2 * i]));
@@ -537,13 +541,13 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
                     }
                 }
                 if constexpr (MODE == kNsLast) {
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 8; ++i) f[i] *= 1.0f / kScale;
                     if (!p.out_tma) {
                         // rows that TMA cannot address: element by element
                         uint16_t *out = p.out + b * p.out_batch;
                         const bool tall = p.rows > p.cols;
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int cc = col + 8 * h + i;
                             if (row >= rows || cc >= cols) continue;
@@ -554,11 +558,11 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
                     } else if (p.rows > p.cols) {
                         // (box1: every lane has read its own unit h of the low plane, the others not;
                         // the transposed box is written once all have, below)
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 8; ++i) v[h >> 1][8 * (h & 1) + i] = __float_as_uint(f[i]);
                     } else {
                         uint32_t o[4];
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
                             o[i] = *reinterpret_cast<const uint32_t *>(&b2);
@@ -567,17 +571,17 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
                     }
                 } else if constexpr (MODE == kNsUpdate) {
                     uint32_t o[4], l[4];
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 4; ++i) split2(f[2 * i], f[2 * i + 1], o[i], l[i]);
                     *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
                     *unit(box1, lane, h) = make_uint4(l[0], l[1], l[2], l[3]);
                 } else {
                     uint32_t o[4];
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 4; ++i) o[i] = half2_bits(f[2 * i], f[2 * i + 1]);
                     *unit(box0, lane, h) = make_uint4(o[0], o[1], o[2], o[3]);
                     if (mirror) {
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const uint16_t e = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
                             *reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(unit(box1, 8 * h + i, lane >> 3)) + 2 * (lane & 7)) = e;
@@ -597,7 +601,7 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
             if constexpr (MODE == kNsLast) {
                 if (p.out_tma && p.rows > p.cols) {
                     __syncwarp();
-    #pragma unroll
+#pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(v[e >> 4][e & 15]));
                         *reinterpret_cast<__nv_bfloat16 *>(reinterpret_cast<uint8_t *>(unit(box0, e, lane >> 3)) + 2 * (lane & 7)) = o;
@@ -636,7 +640,8 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
     return true;
 }
 
-// Waits until a group's counter (the low half of its word) has come to `target`; false if it does not within the limit or some CTA has given up (the high half).
+// Waits until a group's counter (the low half of its word) has come to `target`; false if it does not
+// within the limit or some CTA has given up (the high half).
 __device__ __noinline__ bool ns_grid_wait(const uint64_t *counter, uint32_t target, const WaitCtl &ctl) {
     const uint64_t t0 = global_timer_ns();
     while (true) {
