@@ -281,7 +281,7 @@ dg_status dg_quantize_fp8(const void *x, int x_fmt, int64_t ldx, void *q, int64_
         if (cols % 4 != 0 || static_cast<int64_t>(t.srow[num_groups]) * kBlockK != rows) return DG_ERR_LAYOUT;
     }
     if (rows == 0 || cols == 0) return DG_OK;
-    if (rows > kMaxFewSize || cols > kMaxFewSize) return DG_ERR_UNSUPPORTED;
+    if (rows > kMaxQuantSize || cols > kMaxQuantSize) return DG_ERR_UNSUPPORTED;
     if (!x || (q && !sf) || (qk && !sfk)) return DG_ERR_INVALID_ARG;
     if (ldx < cols || (q && ldq < cols) || (qk && ldqk < cols)) return DG_ERR_INVALID_ARG;
     if (bad_values(x, ldx, x_fmt) || (q && (!aligned(q, 16) || ldq % 16 != 0 || !aligned(sf, 16))) ||
@@ -313,7 +313,7 @@ dg_status dg_quantize_fp8_blocks(const void *x, int x_fmt, int64_t ldx, int64_t 
     if (batch < 0 || rows < 0 || cols < 0) return DG_ERR_INVALID_ARG;
     if (x_fmt != DG_VALUES_F32 && x_fmt != DG_VALUES_BF16) return DG_ERR_INVALID_ARG;
     if (batch == 0 || rows == 0 || cols == 0) return DG_OK;
-    if (rows > kMaxFewSize || cols > kMaxFewSize || batch > 65535) return DG_ERR_UNSUPPORTED;
+    if (rows > kMaxQuantSize || cols > kMaxQuantSize || batch > 65535) return DG_ERR_UNSUPPORTED;
     if (!x || !q || (!sf && !sft)) return DG_ERR_INVALID_ARG;
     if (ldx < cols || ldq < cols || x_batch < 0) return DG_ERR_INVALID_ARG;
     if (batch > 1 && q_batch < (rows - 1) * ldq + cols) return DG_ERR_INVALID_ARG;   // (the matrices' codes are apart)

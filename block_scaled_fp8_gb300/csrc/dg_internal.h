@@ -198,6 +198,7 @@ cudaError_t launch_fill_d(const void *c, int64_t ldc, void *d, int64_t ldd, int 
 
 constexpr int kMaxFewRows = 64;         // rows of a few-row product, tokens of a MoE layer call
 constexpr int kMaxFewSize = 0x7FFFFFFF - 255;   // n and k of a product, tokens to route: rounded up to tiles they fit an int
+constexpr int kMaxQuantSize = 0x7FFFFFFF - 1023;   // rows and columns to quantise: a tile past them is an int still
 constexpr int kMaxLayerTopk = 16;
 constexpr int kMaxLayerExperts = 1024;
 constexpr int kMaxLayerWidth = 1 << 24;

@@ -538,11 +538,12 @@ dg_status dg_moe_fp8_layer(const void *x, int64_t ldx, const int32_t *ids, const
  *   Unused bytes of a word and words that pad a row of them are 0.  A NaN or infinite value
  *   becomes the NaN code and does not count for its group's scale.
  *   Pointers 16-byte aligned; ldx a multiple of 4 (FP32) or 8 (bf16), ldq and ldqk of 16.
- *   rows == 0 or cols == 0 is a no-op.  No output may overlap x.
+ *   rows == 0 or cols == 0 is a no-op, more than 2^31 - 1024 of either DG_ERR_UNSUPPORTED.  No output
+ *   may overlap x.
  * dg_quantize_fp8_blocks -- the same with a scale for each 128x128 block of each of `batch`
  *   matrices (weights): x at x + b * x_batch elements, q at q + b * q_batch (multiples of 16
- *   bytes; the matrices' codes apart from one another).  sf: words int32 [batch][ceil(cols/512)][align4(rows)], for the matrix as B of the NT
- *   calls; sft: [batch][ceil(rows/512)][align4(cols)], for the matrix as it lies there as B of
+ *   bytes; the matrices' codes apart from one another).  sf: words int32
+ *   [batch][ceil(cols/512)][align4(rows)], for the matrix as B of the NT calls; sft: [batch][ceil(rows/512)][align4(cols)], for the matrix as it lies there as B of
  *   the NN calls (products along its rows).  Either may be NULL.  batch <= 65535.
  */
 typedef enum { DG_VALUES_F32 = 0, DG_VALUES_BF16 = 1 } dg_values_format;

@@ -87,6 +87,16 @@ def test_newton_schulz_workspace(lib):
     assert binding.newton_schulz_workspace_bytes(1, 1000, 250) == a
 
 
+@pytest.mark.parametrize("over", [254, 512, 1022])
+def test_quantize_sizes_near_the_int_range(lib, over):
+    """A tile's columns and rows past the matrix still have to be ints: 512 of them, and 8 beside."""
+    n = TOP - over
+    assert quantize(lib, cols=n, ldx=2 ** 32, ldq=2 ** 32) == UNSUPPORTED
+    assert quantize(lib, rows=n) == UNSUPPORTED
+    assert blocks(lib, rows=n, qb=2 ** 40, batch=1) == UNSUPPORTED
+    assert blocks(lib, cols=n, ldx=2 ** 32, ldq=2 ** 32, batch=1) == UNSUPPORTED
+
+
 def f8(*s):
     return torch.zeros(*s, dtype=torch.uint8).view(torch.float8_e4m3fn)
 
