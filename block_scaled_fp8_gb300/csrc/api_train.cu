@@ -205,6 +205,13 @@ bool ns_unsupported(int batch, int rows, int cols) {
     return batch > 4096 || rows > kMaxNsSide || cols > kMaxNsSide || static_cast<int64_t>(rows) * cols > kMaxNsElements;
 }
 
+// The products' grid counters, 32 bits whose differences are signed, count both CTAs of each finished
+// tile: at most 6 a step and tile of 256 x 64, the narrowest.
+bool ns_too_many_tiles(int batch, int rows, int cols, int steps) {
+    const int64_t lo = rows < cols ? rows : cols, hi = rows < cols ? cols : rows;
+    return 6ll * steps * batch * cdiv(lo, 256) * cdiv(hi, 64) > INT32_MAX;
+}
+
 bool bad_values(const void *x, int64_t ldx, int fmt) {
     return !aligned(x, 16) || ldx % (fmt == DG_VALUES_BF16 ? 8 : 4) != 0;
 }
@@ -353,7 +360,8 @@ dg_status dg_newton_schulz(const void *g, int g_fmt, int64_t ldg, int64_t g_batc
     if (batch < 0 || rows < 0 || cols < 0 || steps < 1 || !(eps >= 0.0f)) return DG_ERR_INVALID_ARG;
     if (g_fmt != DG_VALUES_F32 && g_fmt != DG_VALUES_BF16) return DG_ERR_INVALID_ARG;
     if (batch == 0 || rows == 0 || cols == 0) return DG_OK;
-    if (ns_unsupported(batch, rows, cols) || steps > kMaxNsSteps) return DG_ERR_UNSUPPORTED;
+    if (ns_unsupported(batch, rows, cols) || steps > kMaxNsSteps || ns_too_many_tiles(batch, rows, cols, steps))
+        return DG_ERR_UNSUPPORTED;
     if (!g || !out || !workspace || ldg < cols || ldo < cols) return DG_ERR_INVALID_ARG;
     if (g_batch < 0 || (batch > 1 && out_batch < (rows - 1) * ldo + cols)) return DG_ERR_INVALID_ARG;
     if (workspace_bytes < ns_workspace_bytes(batch, rows, cols)) return DG_ERR_INVALID_ARG;

@@ -543,8 +543,9 @@ dg_status dg_moe_fp8_layer(const void *x, int64_t ldx, const int32_t *ids, const
  * dg_quantize_fp8_blocks -- the same with a scale for each 128x128 block of each of `batch`
  *   matrices (weights): x at x + b * x_batch elements, q at q + b * q_batch (multiples of 16
  *   bytes; the matrices' codes apart from one another).  sf: words int32
- *   [batch][ceil(cols/512)][align4(rows)], for the matrix as B of the NT calls; sft: [batch][ceil(rows/512)][align4(cols)], for the matrix as it lies there as B of
- *   the NN calls (products along its rows).  Either may be NULL.  batch <= 65535.
+ *   [batch][ceil(cols/512)][align4(rows)], for the matrix as B of the NT calls; sft:
+ *   [batch][ceil(rows/512)][align4(cols)], for the matrix as it lies there as B of the NN calls
+ *   (products along its rows).  Either may be NULL.  batch <= 65535.
  */
 typedef enum { DG_VALUES_F32 = 0, DG_VALUES_BF16 = 1 } dg_values_format;
 dg_status dg_quantize_fp8(const void *x, int x_fmt, int64_t ldx, void *q, int64_t ldq, void *sf, void *qk, int64_t ldqk,
@@ -638,11 +639,13 @@ dg_status dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(const void *dy, int
  *   A zero matrix gives zeros; a NaN or infinite value makes its matrix NaN, no other.
  *   A matrix's result does not depend on the others, nor on batch.
  *   No alignment beyond the elements' own; rows, cols <= 2^20 and rows * cols <= 2^31, batch <=
- *   4096 (DG_ERR_UNSUPPORTED).  batch, rows or cols 0 is a no-op.
+ *   4096, and 6 steps batch ceil(short side / 256) ceil(long side / 64) < 2^31 (else
+ *   DG_ERR_UNSUPPORTED).  batch, rows or cols 0 is a no-op.
  *   workspace   device memory, 128-byte aligned, dg_newton_schulz_workspace_bytes(batch, rows,
  *         cols) bytes (-1 for sizes that the call refuses); needs no initialisation and
  *         does not outlive the call.  Calls that may run at the same time need one each.
- *   Three launches, the last a cooperative one over as many SMs as the products have tiles for.
+ *   Three launches, the last a cooperative one over as many SMs as the products have tiles for; its
+ *   CTAs wait for one product after another, each within the limit of dg_set_wait_timeout_ms.
  */
 int64_t dg_newton_schulz_workspace_bytes(int batch, int rows, int cols);
 dg_status dg_newton_schulz(const void *g, int g_fmt, int64_t ldg, int64_t g_batch, void *out, int64_t ldo,

@@ -97,6 +97,17 @@ def test_quantize_sizes_near_the_int_range(lib, over):
     assert blocks(lib, cols=n, ldx=2 ** 32, ldq=2 ** 32, batch=1) == UNSUPPORTED
 
 
+def test_newton_schulz_tiles_and_steps(lib):
+    """The finished tiles of a call are counted in 31 bits: 6 a step and tile of 256 x 64."""
+    one = dict(batch=4096, rows=1, cols=2 ** 20, ldg=2 ** 20, gb=2 ** 20, ldo=2 ** 20, ob=2 ** 20, ws=128, bytes=2 ** 50)
+    assert schulz(lib, steps=6, **one) == UNSUPPORTED                  # 6 * 6 * 4096 * 2^14 tiles: 2.4e9
+    assert schulz(lib, steps=5, **{**one, "ws": 64}) == ALIGN          # 2.0e9: refused for its workspace alone
+    assert schulz(lib, steps=1000, rows=4096, cols=4096, ldg=4096, ldo=4096, gb=2 ** 24, ob=2 ** 24, bytes=2 ** 50,
+                  ws=64) == ALIGN
+    tall = dict(one, rows=2 ** 20, cols=1, ldg=8, ldo=8, gb=2 ** 23, ob=2 ** 23)
+    assert schulz(lib, steps=6, **tall) == UNSUPPORTED and schulz(lib, steps=5, **{**tall, "ws": 64}) == ALIGN
+
+
 def f8(*s):
     return torch.zeros(*s, dtype=torch.uint8).view(torch.float8_e4m3fn)
 
