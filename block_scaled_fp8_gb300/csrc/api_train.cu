@@ -57,9 +57,11 @@ int gated_clusters(int bn, bool backward, int num_sms) {
 
 // Columns of the tiles.  Forward: 256 (128 gate, 128 up), or where that leaves pairs without a tile 128 or
 // 64, with 2 or 4 pairs to a group of 128 columns of h; a K-block takes what its loads take, 16 KB
-// of rows and 64 bytes a column at about 55 bytes a cycle (64 columns: 0.62 of 256).  Backward: a K-block
-// of B is loaded whole whatever the tile's columns, so 128 only where all its tiles run at once
-// (half the epilogue).
+// of rows and 64 bytes a column at about 55 bytes a cycle (64 columns: 0.62 of 256).  7 rows, inner 1408,
+// k 2048: 8.8 us with 64 columns, 9.8 with 256; 128 rows, inner 2048, k 7168: 18.0 against 20.8 (14.0
+// with ring slots of two K-blocks).  Backward: a K-block of B is loaded whole whatever the tile's
+// columns, so 128 only where all its tiles run at once, with half the epilogue (515 rows, inner 1360,
+// k 2048: 12.2 us against 16.8 with 256; 1 row, inner 2048, k 7168: 18.3 against 23.8).
 int gated_block_n(bool backward, int64_t units, int inner, int num_sms) {
     if (backward) {
         const int64_t tiles = units * cdiv(inner, 128);

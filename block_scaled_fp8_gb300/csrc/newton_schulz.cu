@@ -7,8 +7,9 @@
 // 256x256 tiles (or 128 or 64 columns where tiles are few), operands by TMA with 128-byte swizzle in
 // stages of 64 K, two accumulators in TMEM, so that a tile's epilogue runs beside the next tile's
 // MMAs.  Roles: warp 0 producer, warp 1 MMA issuer (leader), warps 2-9 epilogue.
-// Bound by: large matrices, the card's power limit (4x2048x7168: 1.42 ms, 1.46 PFLOP/s of the products that
-// are run, at 1.55 GHz when repeated; the update's planes, 470 MB a step, add 0.05 ms a step); small
+// Bound by: large matrices, the card's power limit (4x2048x7168: 1.41 ms in bursts of ten calls, 1.46
+// PFLOP/s of the products that are run, and 1.62 ms when repeated for long, at 1.55 GHz; the update's
+// planes, 470 MB a step, add 0.05 ms a step); small
 // ones, the chain of a phase, 3.3 us and 0.2 us a K-block (64x64: 4 us a phase).
 //
 // Numbers: the operands are FP16 (11 bits) scaled by 2^12, which keeps the iteration's values
@@ -53,8 +54,8 @@ __device__ __forceinline__ float g_value(const char *g, int64_t at) {
                 : reinterpret_cast<const float *>(g)[at];
 }
 
-// Sum of squares of a matrix, as partial sums of CTAs.  A thread adds the squares of its 32 values of a segment
-// in FP32, beside their largest magnitude; where that lies outside 2^-40 .. 2^40 (0 aside), the
+// Sum of squares of a matrix, as partial sums of CTAs.  A thread adds the squares of its 32 values of
+// a segment in FP32, beside their largest magnitude; where that lies outside 2^-40 .. 2^40 (0 aside), the
 // segment is added again with its values scaled into the range, so that no square over- or
 // underflows.  The segments' sums are FP32 for 32 of them, then FP64 (64-bit sums throughout
 // would take most of the kernel's time: a few a clock and SM).
@@ -235,7 +236,8 @@ __global__ void __launch_bounds__(256) dg_ns_split_kernel(const __grid_constant_
                     const int r = q / kPer, c = q % kPer * V;
                     uint4 x = make_uint4(0u, 0u, 0u, 0u);
                     if (r0 + r < p.rows)
-                        x = __ldcg(reinterpret_cast<const uint4 *>(g + (static_cast<int64_t>(r0 + r) * p.ldg + c0 + c) * (BF16 ? 2 : 4)));
+                        x = __ldcg(reinterpret_cast<const uint4 *>(
+                            g + (static_cast<int64_t>(r0 + r) * p.ldg + c0 + c) * (BF16 ? 2 : 4)));
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -290,7 +292,9 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ float2 half2_values(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+__device__ __forceinline__ float2 half2_values(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
 
 // MODE kNsGram: D = A; kNsPoly: D = b A + c A A; kNsUpdate: X planes of a X + B X; kNsLast: the same
 // to the bf16 output.  The first two are [lo][lo] products of K-major operands and symmetric: the
@@ -308,8 +312,8 @@ __device__ __forceinline__ float2 half2_values(uint32_t w) { return __half22floa
 //
 // All products of all steps are one cooperative launch: each is a phase, and a phase's tiles wait for all
 // tiles of the one before (a counter of finished tiles in the workspace, polled by the producer
-// warps, with a limit).  As launches of their own they cost 7.5 us each however small
-// (64x64, five steps: 127 us).
+// warps, with a limit).  As launches of their own they cost 7.5 us each however small (64x64, five
+// steps: 127 us against 67).
 // Several large matrices go in two groups with a counter each, the second a phase behind: while one
 // group waits for its phase's last tiles, the other has work, and the few tiles of a symmetric
 // product run beside the many of an update.
@@ -418,7 +422,9 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
     const int row_off = rank * 128 + static_cast<int>(quad) * 32, col_off = static_cast<int>(half) * (ph.bn / 2);
     const int chunks = ph.bn / 64;   // of 32 columns, a tile and warp
     // 16-byte unit h of row r of a box (64-byte swizzle)
-    auto unit = [](uint8_t *box, int r, int h) { return reinterpret_cast<uint4 *>(box + r * 64 + ((h ^ ((r >> 1) & 3)) << 4)); };
+    auto unit = [](uint8_t *box, int r, int h) {
+        return reinterpret_cast<uint4 *>(box + r * 64 + ((h ^ ((r >> 1) & 3)) << 4));
+    };
     // chunk c of this pair in this phase (chunk c % chunks of its tile c / chunks): the epilogue's operands, into
     // slot c & 1; nothing past the last
     const int my_chunks = first < num_tiles ? (num_tiles - first + num_pairs - 1) / num_pairs * chunks : 0;
@@ -449,7 +455,8 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
         const bool mirror = SYM && n0 >= m0 + kTile;   // (beside the diagonal's block of rows)
         // the row's entry of A's or B's diagonal, and (polynomial) a column's of each chunk by lane
         float diag = 0.f, dcol[4];
-        if (MODE != kNsGram && row < rows) diag = __ldcg((MODE == kNsPoly ? p.da : p.db) + static_cast<int64_t>(b) * p.ldd + row);
+        if (MODE != kNsGram && row < rows)
+            diag = __ldcg((MODE == kNsPoly ? p.da : p.db) + static_cast<int64_t>(b) * p.ldd + row);
         if constexpr (MODE == kNsPoly) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -519,8 +526,10 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 r = half2_values(w0[i]);
-                        f[2 * i] = fmaf(fmaf(p.cc, diag + dc[2 * i], p.cb), r.x, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i]));
-                        f[2 * i + 1] = fmaf(fmaf(p.cc, diag + dc[2 * i + 1], p.cb), r.y, p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
+                        f[2 * i] = fmaf(fmaf(p.cc, diag + dc[2 * i], p.cb), r.x,
+                                        p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i]));
+                        f[2 * i + 1] = fmaf(fmaf(p.cc, diag + dc[2 * i + 1], p.cb), r.y,
+                                            p.cc * (1.0f / kScale) * __uint_as_float(x[2 * i + 1]));
                     }
                 } else {
 #pragma unroll
@@ -584,7 +593,8 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const uint16_t e = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
-                            *reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(unit(box1, 8 * h + i, lane >> 3)) + 2 * (lane & 7)) = e;
+                            uint8_t *const at_unit = reinterpret_cast<uint8_t *>(unit(box1, 8 * h + i, lane >> 3));
+                            *reinterpret_cast<uint16_t *>(at_unit + 2 * (lane & 7)) = e;
                         }
                     }
                 }
@@ -604,7 +614,8 @@ __device__ __forceinline__ bool ns_epilogue(NsEpilogue &st, const NsPhase &ph, c
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(v[e >> 4][e & 15]));
-                        *reinterpret_cast<__nv_bfloat16 *>(reinterpret_cast<uint8_t *>(unit(box0, e, lane >> 3)) + 2 * (lane & 7)) = o;
+                        uint8_t *const at_unit = reinterpret_cast<uint8_t *>(unit(box0, e, lane >> 3));
+                        *reinterpret_cast<__nv_bfloat16 *>(at_unit + 2 * (lane & 7)) = o;
                     }
                 }
             }
@@ -738,7 +749,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (!__all_sync(0xFFFFFFFFu, ok)) goto prod_done;
             }
             const CUtensorMap *ta = f.mode == kNsGram ? &maps.xk[f.step & 1] : f.mode == kNsPoly ? &maps.a : &maps.b;
-            const CUtensorMap *tb = f.mode == kNsGram ? &maps.xkb[f.step & 1] : f.mode == kNsPoly ? &maps.ab : &maps.xn[f.step & 1];
+            const CUtensorMap *tb = f.mode == kNsGram   ? &maps.xkb[f.step & 1]
+                                    : f.mode == kNsPoly ? &maps.ab
+                                                        : &maps.xn[f.step & 1];
             const bool b_mn = f.mode >= kNsUpdate;
             // this CTA's half of the columns: bn / 2 rows of 64 K, or boxes of 64 columns (one swizzle
             // atom, of which the MMA reads bn / 2 where that is less) x 64 K rows
@@ -847,12 +860,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (!ok) break;
             // The CTA's last warp to finish the phase counts its tiles.  A warp's results (its boxes,
             // complete since the wait for them) are released to the CTA by its count, and by the last
-            // warp's, which has acquired the others', to the grid: one release at the grid's scope,
-            // which costs about a microsecond, instead of one a warp and another.
+            // warp's, which has acquired the others', to the grid: one release at the grid's scope
+            // (one a warp and no count in the CTA: 0.15 to 0.4 us more a phase).
             __syncwarp();
             if (lane == 0 && i + 1 < phases) {
                 uint32_t before;
-                asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(done + g)) : "memory");
+                asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;"
+                             : "=r"(before)
+                             : "r"(smem_u32(done + g))
+                             : "memory");
                 if (before % kEpiWarps == kEpiWarps - 1)
                     asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(p.sync + g),
                                  "l"(static_cast<uint64_t>((f.num_tiles - f.first + num_pairs - 1) / num_pairs))
@@ -927,7 +943,8 @@ int max_pairs(int num_sms) {
 // Columns of a product's tiles: 256, or where those are few, 128 or 64.  A tile's time is modelled as its
 // K-blocks times the cycles of one (the operands' loads set them: 16 KB of rows and 64 bytes
 // a column at about 55 bytes a cycle) and its epilogue (a chunk of 32 columns after another,
-// about 1500 cycles each), which only the last tile of a pair does not hide.
+// about 1500 cycles each), which only the last tile of a pair does not hide.  Measured, chosen against 256
+// throughout: 250x1000 127 us and 168, 1024x1024 149 and 217.
 int choose_bn(const NsParams &p, bool sym, int pairs, int64_t *tiles) {
     int best = 256;
     double least = 0.0;
@@ -963,8 +980,8 @@ constexpr int kMaxPartial = 304;
 
 }  // namespace
 
-// Two high planes, the low plane, A and B, their diagonals, the norm's partial sums, the grid's counter; rows of whole 64-element
-// (128-byte) lines.
+// Two high planes, the low plane, A and B, their diagonals, the norm's partial sums, the grid's counter;
+// rows of whole 64-element (128-byte) lines.
 int64_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
     const int64_t lo = rows < cols ? rows : cols, hi = rows < cols ? cols : rows;
     return batch * (2 * lo * (3 * up(hi, 64) + 2 * up(lo, 64)) + 8 * kMaxPartial + 8 * up(lo, 32)) + 128;
@@ -989,9 +1006,12 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
     p.da = reinterpret_cast<float *>(take(4 * p.ldd * p.batch));
     p.db = reinterpret_cast<float *>(w);
     p.dense = p.ldg == p.cols;
-    const int64_t segs = p.dense ? (static_cast<int64_t>(p.rows) * p.cols + 8191) / 8192 : p.rows * ((p.cols + 8191ll) / 8192);
-    p.num_partial = static_cast<int>(segs < kMaxPartial ? segs : kMaxPartial);   // (by the matrix alone, as its sum's order)
-    cudaError_t e = launch_simple(bf16 ? dg_ns_norm_kernel<true> : dg_ns_norm_kernel<false>, dim3(p.num_partial, p.batch), p, stream);
+    const int64_t segs = p.dense ? (static_cast<int64_t>(p.rows) * p.cols + 8191) / 8192
+                                 : p.rows * ((p.cols + 8191ll) / 8192);
+    // (by the matrix alone, as its sum's order)
+    p.num_partial = static_cast<int>(segs < kMaxPartial ? segs : kMaxPartial);
+    cudaError_t e = launch_simple(bf16 ? dg_ns_norm_kernel<true> : dg_ns_norm_kernel<false>,
+                                  dim3(p.num_partial, p.batch), p, stream);
     if (e != cudaSuccess) return e;
     const bool tall = p.rows > p.cols;
     if (tall)
@@ -1025,8 +1045,10 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
           encode_plane(&maps.eb, p.b, p.lo, p.lo, p.lda, pa, p.batch, 32, true);
     if (!ok) return cudaErrorInvalidValue;
     // the output by TMA where its rows (and matrices) start on 16 bytes
-    p.out_tma = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && p.ldo % 8 == 0 && (p.batch == 1 || p.out_batch % 8 == 0) &&
-                encode_plane(&maps.out, p.out, p.cols, p.rows, p.ldo, p.batch == 1 ? p.ldo * p.rows : p.out_batch, p.batch, 32, true);
+    p.out_tma = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && p.ldo % 8 == 0 &&
+                (p.batch == 1 || p.out_batch % 8 == 0) &&
+                encode_plane(&maps.out, p.out, p.cols, p.rows, p.ldo, p.batch == 1 ? p.ldo * p.rows : p.out_batch,
+                             p.batch, 32, true);
     if (!p.out_tma) maps.out = maps.ea;   // not used
     p.steps = steps;
     // Two groups where the symmetric products have more than a wave of tiles, whose last wave the other

@@ -225,3 +225,14 @@ def test_two_groups(b):
         p = x @ x.t()
         x = COEF[0] * x + (COEF[1] * p + COEF[2] * (p @ p)) @ x
     close(out[b - 1], x.cpu())
+
+
+@pytest.mark.parametrize("r,c", [(1, 24), (24, 1), (1, 20), (1, 1)])
+def test_batch_of_single_rows_and_columns(r, c):
+    """Matrices closer to one another than the row stride that a single row stands for."""
+    g = torch.stack([gradient(r, c, 40 + j) for j in range(5)])
+    out = torch.full((7, r, c), 9.0, dtype=torch.bfloat16, device="cuda")
+    dg.dg_newton_schulz(g.cuda(), out[1:6])
+    assert bool((out[0] == 9.0).all()) and bool((out[6] == 9.0).all())
+    for j in range(5):
+        close(out[1 + j], plain(g[j]), what=f"matrix {j}")
