@@ -2,9 +2,9 @@
 
 Every translation unit under csrc/ is compiled for sm_103a only, in parallel,
 then linked into one shared library against the shared CUDA runtime.  The
-marshalling of the binding's decode calls (csrc/marshal.c, a Python extension
-without CUDA) is built beside it where Python's headers are installed; without
-them the library is whole, and only the binding's decode calls are missing.
+marshalling of the binding's decode and training calls (csrc/marshal.c, a Python
+extension without CUDA) is built beside it where Python's headers are installed;
+without them the library is whole, and only those calls of the binding are missing.
 """
 from __future__ import annotations
 
