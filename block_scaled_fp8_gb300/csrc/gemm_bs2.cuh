@@ -187,9 +187,10 @@ struct Bs2Config {
 // stage fewer where that is their price (that epilogue, not the MMAs, sets the pace
 // of the FP32-output GEMMs).
 constexpr int kF32StageBufs = 4;
-// The gated backward epilogue: five boxes of 32 rows x 32 bf16 columns per warp (two of gate and up,
-// one of h), two operand stages fewer.
-constexpr int kGatedBwdBufs = 10;
+// The gated backward epilogue.  256 columns: five boxes of 32 rows x 32 bf16 columns per warp (two of gate
+// and up, one of h), two operand stages fewer; 128 columns: one of 32 x 32 FP32.
+template <int BN>
+constexpr int kGatedBwdBufs = BN == 128 ? 4 : 10;
 // The gated forward epilogue: one box of 32 columns per warp.
 constexpr int kGatedBufs = 2;
 // Its narrow tiles, whose K-blocks are short: ring slots of two (128 rows, inner 2048, K = 7168: 14.0 us
@@ -204,7 +205,7 @@ template <int BN, int MP, bool WITH_C, bool F32>
 constexpr bool kCTile = WITH_C && !F32 && MP == 256 && BN % 32 == 0 && BN <= 256;
 template <int BN, int MP, int LAY, bool F32, bool WITH_C = false>
 using Bs2Cfg = Bs2Config<BN, MP, (LAY & 2) != 0, (LAY & 4) != 0,
-                         (LAY & kLayGatedBwd) ? kGatedBwdBufs
+                         (LAY & kLayGatedBwd) ? kGatedBwdBufs<BN>
                                               : (LAY & kLayGated) ? kGatedBufs : F32 ? kF32StageBufs : 0,
                          (LAY & 8) != 0, kCTile<BN, MP, WITH_C, F32>, (LAY & kLayGated) && BN < 256 ? kGatedFewKb : 0>;
 
@@ -565,9 +566,29 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
     f32x2_parts(v, lo, hi);
     return pack_bf16(lo, hi);
 }
+// 16 bytes of global memory, past L1, loaded where it stands.
+__device__ __forceinline__ uint4 load16(const uint16_t *at) {
+    uint4 v;
+    asm volatile("ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(at)
+                 : "memory");
+    return v;
+}
 // The two values of a bf16 pair.
 __device__ __forceinline__ uint64_t bf16x2_values(uint32_t w) {
     return f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Gradients of gate and up, and h, for two values: s = sigmoid(g), silu = g s, silu' = s + silu (1 - s)
+__device__ __forceinline__ void gated_gradient(uint64_t dh, uint32_t gw, uint32_t uw, uint32_t &dg, uint32_t &du,
+                                               uint32_t &h) {
+    const uint64_t g = bf16x2_values(gw), u = bf16x2_values(uw);
+    const uint64_t s = sigmoid2(g), silu = mul2(g, s);
+    const uint64_t rest = fma2(s, f32x2(-1.0f, -1.0f), f32x2(1.0f, 1.0f));
+    dg = pack_bf16(mul2(mul2(dh, u), fma2(silu, rest, s)));
+    du = pack_bf16(mul2(dh, silu));
+    h = pack_bf16(mul2(silu, u));
 }
 
 template <int BN, bool WITH_C, int MP, bool F32 = false, int LAY = 0>
@@ -1179,13 +1200,34 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
             }
             cp_async_commit();
         };
+        // 128 columns: a tile's gate and up (two chunks) in registers, 16 bytes of rows 8 i + lane / 4
+        constexpr int kGuRegs = (LAY & kLayGatedBwd) && BN == 128 ? 2 : 1;
+        uint4 gate[kGuRegs][4], up[kGuRegs][4];
+        auto load_gu_regs = [&](const PairTile &tl) {
+            const int row0 = tl.d_row0 + row_off + static_cast<int>(lane >> 2);
+#pragma unroll
+            for (int j = 0; j < kGuRegs; ++j) {
+                const int c = tl.n0 + static_cast<int>(half) * (BN / 2) + 32 * j + 8 * static_cast<int>(lane & 3);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    gate[j][i] = up[j][i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (tl.valid_rows > 0 && row0 + 8 * i < p.rows && c < p.n) {
+                        const uint16_t *src = p.gu + static_cast<int64_t>(row0 + 8 * i) * p.ldgu + c;
+                        gate[j][i] = load16(src);
+                        up[j][i] = load16(src + p.n);
+                    }
+                }
+            }
+        };
         uint32_t xphase = 0;   // gated forward: the exchange of the halves' amax
         PairTile tile;
         if (pair_id < num_tiles) {
             get_pair_tile<BN, MP, LAY>(p, prefix, pinfo, num_units, psf_k, pair_id, rank, tile);
             if constexpr (WITH_C && !F32) prefetch_c(tile);
             if (c_tma) load_ctile(tile);
-            if constexpr ((LAY & kLayGatedBwd) != 0) {
+            if constexpr ((LAY & kLayGatedBwd) != 0 && BN == 128) {
+                load_gu_regs(tile);
+            } else if constexpr ((LAY & kLayGatedBwd) != 0) {
                 load_gu(tile, true, 0);
                 load_gu(tile, true, 1);
             }
@@ -1503,15 +1545,74 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                 } else if (stores) {
                     store_plane(&tm_d, p.d, p.ldd, g, col0, 0);
                 }
+            } else if constexpr ((LAY & kLayGatedBwd) != 0 && BN == 128) {
+                // gated backward with narrow tiles, one a pair as a rule, where the chain counts: gate and up
+                // have been in registers since the tile began, as lanes load and store whole 64-byte
+                // row segments, and dh, which TMEM gives a row a lane, changes to that order through
+                // shared memory (515x1360, K = 2048: 11.1 us against 12.3 in the form below, which
+                // also has a ring stage less).
+                constexpr int HC = BN / 2;
+                const uint32_t tcol = tmem_base + ((quad * 32) << 16) + acc * ACC + half * HC;
+                // 16-byte unit h (4 columns) of row r
+                auto dh_unit = [&](uint32_t r, uint32_t h) {
+                    return reinterpret_cast<uint4 *>(stage_out + r * 128 + ((h ^ (r & 7)) << 4));
+                };
+#pragma unroll
+                for (int j = 0; j < HC / 32; ++j) {
+                    uint32_t dh[2][16];
+                    tmem_ld_32x32b_x16(tcol + 32 * j, dh[0]);
+                    tmem_ld_32x32b_x16(tcol + 32 * j + 16, dh[1]);
+                    tmem_ld_wait();
+                    reg_fence16(dh[0]);
+                    reg_fence16(dh[1]);
+                    if (j == HC / 32 - 1) {
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(leader_tempty + acc * 8);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 8; ++h) {
+                        const uint32_t *v = dh[h >> 2] + 4 * (h & 3);
+                        *dh_unit(lane, h) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                    __syncwarp();
+                    const int row0 = tile.d_row0 + row_off + static_cast<int>(lane >> 2);
+                    const int c = tile.n0 + static_cast<int>(half) * HC + 32 * j + 8 * static_cast<int>(lane & 3);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = row0 + 8 * i;
+                        const uint32_t r = 8 * i + (lane >> 2), u = 2 * (lane & 3);
+                        const uint4 d0 = *dh_unit(r, u), d1 = *dh_unit(r, u + 1), g4 = gate[j][i], u4 = up[j][i];
+                        const uint32_t dw[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+                        const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+                        uint32_t og[4], ou[4], oh[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            gated_gradient(f32x2(__uint_as_float(dw[2 * q]), __uint_as_float(dw[2 * q + 1])), gw[q], uw[q],
+                                           og[q], ou[q], oh[q]);
+                        if (tile.valid_rows > 0 && row < p.rows && c < p.n) {
+                            uint16_t *dr = p.d + static_cast<int64_t>(row) * p.ldd + c;
+                            *reinterpret_cast<uint4 *>(dr) = make_uint4(og[0], og[1], og[2], og[3]);
+                            *reinterpret_cast<uint4 *>(dr + p.n) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+                            if (p.h != nullptr)
+                                *reinterpret_cast<uint4 *>(p.h + static_cast<int64_t>(row) * p.ldh + c) =
+                                    make_uint4(oh[0], oh[1], oh[2], oh[3]);
+                        }
+                    }
+                    __syncwarp();   // dh's box has been read
+                }
+                if (++acc == NUM_ACC) { acc = 0; acc_phase ^= 1; }
+                if (has_next) load_gu_regs(next_tile);
             } else if constexpr ((LAY & kLayGatedBwd) != 0) {
                 // gated backward: the accumulator is dh.  This warp's 128 columns of its 32 rows go
                 // to registers and the accumulator is released.  Then chunks of 32 columns, whose gate and
                 // up were copied to shared memory two chunks ahead: a lane takes a row, the gradients take
                 // the places of gate and up, h a box of its own, and the warp stores whole row
                 // segments with plain stores, which nothing waits for.  (With TMA boxes in and out, a
-                // chunk's load, arithmetic and store followed one another: 4096x7168, K = 2048: 102 us
-                // against 77; the product alone takes 49.  What is left is the 294 MB of gate, up and
-                // results, 43 us of HBM time, which a tile's epilogue draws at about 5 TB/s.)
+                // chunk's load, arithmetic and store followed one another: 4096x7168, K = 2048, without
+                // h: 102 us against 77.  As nodes of a graph: 66 us, 74 with h, the product alone 40;
+                // the 235 MB of gate, up and their gradients, 294 with h, take 35 and 43 us of HBM time.
+                // More of gate and up in flight, up to the whole tile in registers: 82 to 113 us.)
                 constexpr int HC = BN / 2;
                 uint32_t dh[HC / 16][16];
                 const uint32_t tcol = tmem_base + ((quad * 32) << 16) + acc * ACC + half * HC;
@@ -1540,14 +1641,8 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t *d2 = dh[2 * j + h / 2] + 8 * (h & 1) + 2 * i;
-                            const uint64_t d = f32x2(__uint_as_float(d2[0]), __uint_as_float(d2[1]));
-                            const uint64_t gt = bf16x2_values(gw[i]), uv = bf16x2_values(uw[i]);
-                            // s = sigmoid(g), silu = g s, silu' = s + silu (1 - s)
-                            const uint64_t sg = sigmoid2(gt), si = mul2(gt, sg);
-                            const uint64_t rest = fma2(sg, f32x2(-1.0f, -1.0f), f32x2(1.0f, 1.0f));
-                            og[i] = pack_bf16(mul2(mul2(d, uv), fma2(si, rest, sg)));
-                            ou[i] = pack_bf16(mul2(d, si));
-                            oh[i] = pack_bf16(mul2(si, uv));
+                            gated_gradient(f32x2(__uint_as_float(d2[0]), __uint_as_float(d2[1])), gw[i], uw[i], og[i],
+                                           ou[i], oh[i]);
                         }
                         *gp = make_uint4(og[0], og[1], og[2], og[3]);
                         *up = make_uint4(ou[0], ou[1], ou[2], ou[3]);

@@ -370,3 +370,29 @@ def test_tiles_of_every_width():
         for x, y in zip(got, want):
             assert torch.equal(x, y[:m])
     assert seen == {64, 128, 256} and back == {128, 256}
+
+
+def test_more_narrow_tiles_than_pairs():
+    """Experts of 128 rows: each is a tile of its own, so that narrow tiles, chosen for the rows alone, are
+    more than the CTA pairs, and a pair goes from one to the next."""
+    e, i, k = 8, 2048, 256
+    m = 128 * e
+    g = torch.Generator().manual_seed(31)
+
+    def codes(*s):
+        return torch.randn(*s, generator=g).to(torch.float8_e4m3fn).cuda()
+
+    def words(*s):
+        return (torch.randint(124, 130, (*s, 4), generator=g, dtype=torch.uint8).view(torch.int32).view(*s)).cuda()
+    dy, w2 = codes(m, k), codes(e, k, i)
+    sfdy, sfw2 = words(1, m), words(e, 1, i)
+    gu = torch.randn(m, 2 * i, generator=g).to(torch.bfloat16).cuda()
+    layout = torch.arange(e, dtype=torch.int32).repeat_interleave(128).cuda()
+    dgu, h = torch.empty_like(gu), torch.empty(m, i, dtype=torch.bfloat16, device="cuda")
+    dg.dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(dy, sfdy, w2, sfw2, layout, gu, dgu, h=h)
+    assert dg.last_config()["block_n"] == 128
+    want, want_h = torch.empty(128, 2 * i, dtype=torch.bfloat16, device="cuda"), torch.empty_like(h[:128])
+    for j in range(e):
+        r = slice(128 * j, 128 * j + 128)
+        dg.dg_fp8_gated_gemm_nn_backward(dy[r], sfdy[:, r].contiguous(), w2[j], sfw2[j], gu[r], want, h=want_h)
+        assert torch.equal(dgu[r], want) and torch.equal(h[r], want_h), j
