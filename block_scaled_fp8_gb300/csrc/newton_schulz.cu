@@ -314,9 +314,9 @@ __device__ __forceinline__ float2 half2_values(uint32_t w) {
 // tiles of the one before (a counter of finished tiles in the workspace, polled by the producer
 // warps, with a limit).  As launches of their own they cost 7.5 us each however small (64x64, five
 // steps: 127 us against 67).
-// Several large matrices go in two groups with a counter each, the second a phase behind: while one
+// Several matrices may go in two groups with a counter each, the second a phase behind: while one
 // group waits for its phase's last tiles, the other has work, and the few tiles of a symmetric
-// product run beside the many of an update.
+// product run beside the many of an update (choose_tiles).
 struct NsMaps {
     CUtensorMap xk[2], xn[2];   // X's high planes along K (128 rows a box), and as [K][N]
     CUtensorMap a, b;           // A, B along K
@@ -940,27 +940,101 @@ int max_pairs(int num_sms) {
     return v * 2 > num_sms ? num_sms / 2 : v;
 }
 
+// Tiles of a matrix's product with tiles of bn columns (as ns_shape counts them).
+int64_t count_tiles(const NsParams &p, bool sym, int bn) {
+    const int64_t tm = up(p.lo, kTile) / kTile, tn = up(sym ? p.lo : p.hi, bn) / bn, r = kTile / bn, q = tn / r;
+    return sym ? r * (q * (q + 1) / 2) + (tn - r * q) * (q + 1) : tm * tn;
+}
+
 // Columns of a product's tiles: 256, or where those are few, 128 or 64.  A tile's time is modelled as its
 // K-blocks times the cycles of one (the operands' loads set them: 16 KB of rows and 64 bytes
 // a column at about 55 bytes a cycle) and its epilogue (a chunk of 32 columns after another,
 // about 1500 cycles each), which only the last tile of a pair does not hide.  Measured, chosen against 256
 // throughout: 250x1000 127 us and 168, 1024x1024 149 and 217.
-int choose_bn(const NsParams &p, bool sym, int pairs, int64_t *tiles) {
+int choose_bn(const NsParams &p, bool sym, int pairs) {
     int best = 256;
     double least = 0.0;
     for (int bn : {256, 128, 64}) {
-        const int64_t tm = up(p.lo, kTile) / kTile, tn = up(sym ? p.lo : p.hi, bn) / bn, r = kTile / bn, q = tn / r;
-        const int64_t n = (sym ? r * (q * (q + 1) / 2) + (tn - r * q) * (q + 1) : tm * tn) * p.batch;
+        const int64_t n = count_tiles(p, sym, bn) * p.batch;
         // (symmetric: the mean of the products along the long side and the short)
         const int64_t nkb = sym ? (up(p.hi, kKBlock) + up(p.lo, kKBlock)) / kKBlock / 2 + 1 : up(p.lo, kKBlock) / kKBlock;
-        const double t = static_cast<double>((n + pairs - 1) / pairs) * nkb * (16384 + 64 * bn) / 55.0 + 1500.0 * (bn / 64);
+        const double t = static_cast<double>((n + pairs - 1) / pairs) * nkb * (16384 + 64 * bn) / 55.0 +
+                         1500.0 * (bn / 64);
         if (bn == 256 || t < 0.95 * least) {
             best = bn;
             least = t;
-            *tiles = n;
         }
     }
     return best;
+}
+
+// Modelled time in us of `steps` steps with tiles of these columns, in one group or in two: each pair's
+// tiles one after another in turn order (ns_phase), the phase's no sooner than 3.3 us (the chain of counter,
+// load, epilogue and store, of which a tile's columns past 64 add their epilogue) after the
+// last tile of the group's phase before.  Tiles cost as in choose_bn, at 1.9 GHz.  The second group's waits and
+// its tiles' loads beside the first's: 1.2 us a phase.
+double model_time(const NsParams &p, int steps, int bn_sym, int bn_update, int groups, int pairs) {
+    constexpr int kMax = 128;
+    if (pairs > kMax) pairs = kMax;
+    float busy[kMax] = {}, done[2] = {};
+    float cost[3], tail[3];
+    int64_t tiles[3];
+    for (int m = 0; m < 3; ++m) {
+        const int bn = m < kNsUpdate ? bn_sym : bn_update;
+        const int64_t nkb = up(m == kNsGram ? p.hi : p.lo, kKBlock) / kKBlock;
+        const float epilogue = 0.79f * (bn / 64), loads = nkb * (16384 + 64 * bn) / 104500.0f;
+        cost[m] = loads > epilogue ? loads : epilogue;
+        tail[m] = 3.3f + epilogue - 0.79f;
+        tiles[m] = count_tiles(p, m < kNsUpdate, bn);
+    }
+    const int phases = 3 * (steps < 3 ? steps : 3);
+    for (int turn = 0; turn < phases + groups - 1; ++turn) {
+        int first = 0;
+        for (int g = 0; g < groups; ++g) {
+            const int i = turn - g;
+            if (i < 0 || i >= phases) continue;
+            const int64_t n = tiles[i % 3] * (groups == 1 ? p.batch : g == 0 ? p.batch - p.batch / 2 : p.batch / 2);
+            const int64_t each = n / pairs;
+            const int more = static_cast<int>(n % pairs);   // pairs from `first` on that have one more
+            float end = done[g];
+            for (int q = 0; q < pairs; ++q) {
+                const int at = q >= first ? q - first : q - first + pairs;
+                const int64_t mine = each + (at < more ? 1 : 0);
+                if (mine == 0) continue;
+                const float t = (busy[q] > done[g] ? busy[q] : done[g]) + mine * cost[i % 3];
+                busy[q] = t;
+                end = t > end ? t : end;
+            }
+            done[g] = end + tail[i % 3];
+            if (g == 0) first = more;
+        }
+    }
+    return (done[0] > done[1] ? done[0] : done[1]) + (groups > 1 ? 1.2 * phases : 0.0);
+}
+
+// Columns of the products' tiles and the matrices of the first group.  Two groups let one have tiles
+// while the other waits for its phase's last, and let a symmetric product's few tiles run beside an
+// update's many; they cost where a phase alone fills the pairs.  The model decides, between tiles of 256 and 128
+// columns (64, two groups against one: 8x512x512 125 us and 115, 700x40x64 305 and 294).  Measured, two
+// against one: 2x2112x1536 286 us and 300, 4x1024x1024 196 and 207, 8x1024x1024 293 and 319, 4x2048x2048
+// 533 and 583, 16x512x1024 213 and 224, 3x2048x7168 1165 and 1252, 4x2048x7168 1414 and 1463; left as one
+// group: 2x1536x1536 246 and 244, 2x1024x4096 310 and 257, 3x1408x2048 367 and 320, 2x2048x7168 822 and 777.
+void choose_tiles(NsParams &p, int steps, int pairs) {
+    p.bn_sym = choose_bn(p, true, pairs);
+    p.bn_update = choose_bn(p, false, pairs);
+    p.group0 = p.batch;
+    if (p.batch < 2) return;
+    double least = model_time(p, steps, p.bn_sym, p.bn_update, 1, pairs);
+    for (int s : {256, 128})
+        for (int u : {256, 128}) {
+            const double t = model_time(p, steps, s, u, 2, pairs);
+            if (t < least) {
+                least = t;
+                p.bn_sym = s;
+                p.bn_update = u;
+                p.group0 = p.batch - p.batch / 2;
+            }
+        }
 }
 
 cudaError_t launch_simple(void (*kernel)(NsParams), dim3 grid, const NsParams &p, cudaStream_t stream) {
@@ -1025,10 +1099,11 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
     // operands: X along K (Gram), X as [K][N], A and B; epilogue boxes of the planes, A, B and the output
     const int pairs = max_pairs(num_sms);
     if (pairs <= 0) return cudaErrorInvalidConfiguration;
-    int64_t tiles_sym, tiles;
-    p.bn_sym = choose_bn(p, true, pairs, &tiles_sym);
-    p.bn_update = choose_bn(p, false, pairs, &tiles);
-    if (tiles_sym > tiles) tiles = tiles_sym;   // (no more pairs than the phase that has most tiles)
+    choose_tiles(p, steps, pairs);
+    // (no more pairs than the phase that has most tiles)
+    const int64_t tiles_sym = count_tiles(p, true, p.bn_sym) * p.batch;
+    int64_t tiles = count_tiles(p, false, p.bn_update) * p.batch;
+    if (tiles_sym > tiles) tiles = tiles_sym;
     NsMaps maps;
     const int64_t px = p.lo * p.ldx, pa = p.lo * p.lda;
     bool ok = true;
@@ -1051,11 +1126,6 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
                              p.batch, 32, true);
     if (!p.out_tma) maps.out = maps.ea;   // not used
     p.steps = steps;
-    // Two groups where the symmetric products have more than a wave of tiles, whose last wave the other
-    // group's tiles fill, and K enough to be worth the longer chain (3x2048x7168: 1293 us against 1379,
-    // 4x2048x7168: 1414 / 1463, 16x1024x4096: 1329 / 1346); else one (2x2048x7168: 777 us against 822 with
-    // two, 3x1408x2048: 320 / 367, 700x40x64: 294 / 305).
-    p.group0 = tiles_sym > pairs && p.hi >= 2048 ? p.batch - p.batch / 2 : p.batch;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;   // the CTAs wait for one another

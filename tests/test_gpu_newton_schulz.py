@@ -236,3 +236,17 @@ def test_batch_of_single_rows_and_columns(r, c):
     assert bool((out[0] == 9.0).all()) and bool((out[6] == 9.0).all())
     for j in range(5):
         close(out[1 + j], plain(g[j]), what=f"matrix {j}")
+
+
+@pytest.mark.parametrize("b,r,c", [(4, 1024, 1024), (6, 1024, 1024), (8, 1000, 1024), (2, 2112, 1536), (5, 1536, 1536)])
+def test_groups_and_tiles_leave_the_bits(b, r, c):
+    """A matrix's result does not depend on batch, and so not on the tiles and groups that a batch makes
+    the call choose: narrow and wide tiles, two groups, equal and unequal."""
+    g = torch.randn(b, r, c, generator=torch.Generator().manual_seed(b + r)).cuda()
+    out, one = (torch.empty(*s, r, c, dtype=torch.bfloat16, device="cuda") for s in ((b,), ()))
+    for steps in (1, 5):
+        dg.dg_newton_schulz(g, out, steps=steps)
+        for j in range(b):
+            dg.dg_newton_schulz(g[j], one, steps=steps)
+            assert torch.equal(one, out[j]), (steps, j)
+    close(out[b - 1], plain(g[b - 1].cpu()))
