@@ -136,23 +136,45 @@ __global__ void __launch_bounds__(256) dg_ns_norm_kernel(const __grid_constant__
     }
 }
 
-// 2^12 / (norm + eps) in two factors, so that neither leaves FP32's range.  Every CTA adds the
-// partial sums in the same order; one thread does the 64-bit arithmetic.
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// 2^12 / (sqrt(s) + eps) in two factors, so that neither leaves FP32's range: FP32 arithmetic on
+// significands beside integer exponents (a few roundings of 2^-24, all of X alike).  With a 64-bit square
+// root and division, a chain of its own in every CTA of the split, a call took 1 us more (250x1000:
+// 92.0 us against 90.9).  s: 0, 2^-298 .. 2^300, infinite or NaN.
+__device__ __forceinline__ void inverse_norm(double s, float eps, float &f1, float &f2) {
+    const uint32_t hi = static_cast<uint32_t>(__double2hiint(s));
+    if (!(hi < 0x7FF00000u)) {   // infinite: 0, NaN: NaN
+        f1 = 1.0f;
+        f2 = kScale / static_cast<float>(s);
+        return;
+    }
+    // sqrt(s) = r 2^es, eps = q 2^ee, r and q in [1, 2) or 0
+    const int k = static_cast<int>(hi >> 20) - 1023, es = s == 0.0 ? -1000 : k >> 1;
+    const int top = static_cast<int>((hi & 0xFFFFFu) | static_cast<uint32_t>(1023 + (k & 1)) << 20);
+    const float r = s == 0.0 ? 0.0f : sqrtf(static_cast<float>(__hiloint2double(top, __double2loint(s))));
+    const int ee = eps == 0.0f ? -1000 : eps < 0x1p-126f ? -126 : static_cast<int>(__float_as_uint(eps) >> 23) - 127;
+    if (es < -500 && ee < -500) {   // 0: X is 0
+        f1 = f2 = 0.0f;
+        return;
+    }
+    const int e = es > ee ? es : ee;   // (eps infinite: 128, and 1 / norm 0)
+    const float norm = (es - e > -64 ? r * pow2(es - e) : 0.0f) +
+                       (ee - e > -64 ? eps * pow2(-(ee >> 1)) * pow2((ee >> 1) - e) : 0.0f);
+    const int to = 12 - e, e1 = to >> 1;
+    f1 = pow2(e1);
+    f2 = pow2(to - e1) / norm;
+}
+
+// The factors of a matrix.  Every CTA adds the partial sums in the same order.
 __device__ __forceinline__ void norm_factors(const NsParams &p, int64_t batch, float &f1, float &f2) {
     __shared__ float factors[2];
     if (threadIdx.x < 32) {
         double s = 0.0;
         for (int i = threadIdx.x; i < p.num_partial; i += 32) s += p.partial[batch * p.num_partial + i];
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        if (threadIdx.x == 0) {
-            const double norm = sqrt(s) + static_cast<double>(p.eps);
-            int e = 0;
-            // (not norm > 0: a NaN stays one)
-            const double mant = norm == 0.0 ? 0.0 : frexp(static_cast<double>(kScale) / norm, &e);
-            const int e1 = e / 2;
-            factors[0] = static_cast<float>(ldexp(1.0, e1));
-            factors[1] = static_cast<float>(ldexp(mant, e - e1));
-        }
+        if (threadIdx.x == 0) inverse_norm(s, p.eps, factors[0], factors[1]);
     }
     // (the products' grid counter and abort word, which follow in the stream)
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 2) p.sync[threadIdx.x] = 0u;

@@ -250,3 +250,17 @@ def test_groups_and_tiles_leave_the_bits(b, r, c):
             dg.dg_newton_schulz(g[j], one, steps=steps)
             assert torch.equal(one, out[j]), (steps, j)
     close(out[b - 1], plain(g[b - 1].cpu()))
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -140, 2.0 ** -126, 2.0 ** -75, 1.0, 2.0 ** 64, 2.0 ** 126])
+def test_norm_and_eps_of_any_magnitude(scale):
+    """eps beside, below and above the norm, up to FP32's ends (values below 2^-126 have few bits left,
+    which the definition is given as well)."""
+    g = (torch.tensor([[1.0, -0.5, 0.25], [0.5, 1.0, 0.75]]) * scale).float()
+    out = torch.empty(2, 3, dtype=torch.bfloat16, device="cuda")
+    for ratio in (0.0, 2.0 ** -20, 0.5, 1.0, 4.0):
+        eps = float(torch.tensor(scale * ratio).float())     # as the call takes it
+        dg.dg_newton_schulz(g.cuda(), out, steps=1, eps=eps)
+        close(out, plain(g, steps=1, eps=eps), what=f"{scale} {ratio}")
+    dg.dg_newton_schulz(g.cuda(), out, steps=1, eps=float("inf"))
+    assert not bool(out.any())
