@@ -281,17 +281,15 @@ dg_status dg_quantize_fp8(const void *x, int x_fmt, int64_t ldx, void *q, int64_
                           void *sfk, int rows, int cols, const int *ks, int num_groups, void *stream) {
     if (rows < 0 || cols < 0 || num_groups < 0) return DG_ERR_INVALID_ARG;
     if (x_fmt != DG_VALUES_F32 && x_fmt != DG_VALUES_BF16) return DG_ERR_INVALID_ARG;
-    if (!q && !qk) return DG_ERR_INVALID_ARG;
     KGroupRows t;
     t.num_groups = 0;
     if (ks != nullptr) {
-        if (!qk) return DG_ERR_INVALID_ARG;
         if (host_k_grouped_rows(ks, num_groups, &t) < 0) return DG_ERR_INVALID_ARG;
         if (cols % 4 != 0 || static_cast<int64_t>(t.srow[num_groups]) * kBlockK != rows) return DG_ERR_LAYOUT;
     }
     if (rows == 0 || cols == 0) return DG_OK;
     if (rows > kMaxQuantSize || cols > kMaxQuantSize) return DG_ERR_UNSUPPORTED;
-    if (!x || (q && !sf) || (qk && !sfk)) return DG_ERR_INVALID_ARG;
+    if (!x || (!q && !qk) || (ks && !qk) || (q && !sf) || (qk && !sfk)) return DG_ERR_INVALID_ARG;
     if (ldx < cols || (q && ldq < cols) || (qk && ldqk < cols)) return DG_ERR_INVALID_ARG;
     if (bad_values(x, ldx, x_fmt) || (q && (!aligned(q, 16) || ldq % 16 != 0 || !aligned(sf, 16))) ||
         (qk && (!aligned(qk, 16) || ldqk % 16 != 0 || !aligned(sfk, 16))))

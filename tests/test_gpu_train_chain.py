@@ -141,3 +141,28 @@ def test_captured():
     for n in ("y", "dx", "dw1", "dw2", "up1", "up2", "w1", "w2"):
         assert torch.equal(getattr(a, n), getattr(b, n)), n
     assert int(a.status) == 0 and int(b.status) == 0
+
+
+def test_nothing_to_do():
+    """Tensors of no rows, columns or matrices: no error, and nothing is written."""
+    def e4m3(*s):
+        return torch.empty(*s, dtype=torch.float8_e4m3fn, device="cuda")
+
+    def words(*s):
+        return torch.empty(*s, dtype=torch.int32, device="cuda")
+    bf16 = dict(dtype=torch.bfloat16, device="cuda")
+    x = torch.empty(0, 256, **bf16)
+    dg.dg_quantize_fp8(x, q=e4m3(0, 256), sf=words(1, 0))
+    dg.dg_quantize_fp8(x, qk=e4m3(0, 256), sfk=words(0, 256))
+    dg.dg_quantize_fp8(x, qk=e4m3(0, 256), sfk=words(0, 256), ks=[0, 0])
+    dg.dg_quantize_fp8(torch.empty(4, 0, **bf16), q=e4m3(4, 0), sf=words(0, 4))
+    dg.dg_quantize_fp8_blocks(torch.empty(0, 8, 16, **bf16), e4m3(0, 8, 16), sf=words(0, 1, 8))
+    dg.dg_newton_schulz(torch.empty(0, 8, 16, **bf16), torch.empty(0, 8, 16, **bf16))
+    dg.dg_newton_schulz(torch.empty(8, 0, **bf16), torch.empty(8, 0, **bf16))
+    dg.dg_fp8_gated_gemm_nt(e4m3(0, 128), words(1, 0), e4m3(64, 128), words(1, 64), h=torch.empty(0, 32, **bf16))
+    dg.dg_fp8_gated_gemm_nt(e4m3(0, 128), words(1, 0), e4m3(64, 128), words(1, 64), hq=e4m3(0, 32), sfh=words(1, 0))
+    dg.dg_fp8_gated_gemm_nn_backward(e4m3(0, 128), words(1, 0), e4m3(128, 32), words(1, 32), torch.empty(0, 64, **bf16),
+                                     torch.empty(0, 64, **bf16), h=torch.empty(0, 32, **bf16))
+    dg.dg_m_grouped_fp8_gated_gemm_nt_contiguous(e4m3(0, 128), words(1, 0), e4m3(2, 64, 128), words(2, 1, 64), words(0),
+                                                 h=torch.empty(0, 32, **bf16))
+    torch.cuda.synchronize()

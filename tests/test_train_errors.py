@@ -97,6 +97,16 @@ def test_quantize_sizes_near_the_int_range(lib, over):
     assert blocks(lib, cols=n, ldx=2 ** 32, ldq=2 ** 32, batch=1) == UNSUPPORTED
 
 
+def test_nothing_to_do_needs_no_pointers(lib):
+    """Tensors without elements have null pointers."""
+    none = dict(x=None, q=None, sf=None, qk=None, sfk=None)
+    assert quantize(lib, rows=0, **none) == OK and quantize(lib, cols=0, ldx=0, ldq=0, ldqk=0, **none) == OK
+    assert quantize(lib, rows=0, ks=[0, 0], **none) == OK
+    assert quantize(lib, rows=0, ks=[128], **none) == LAYOUT      # (the sizes are checked all the same)
+    assert blocks(lib, batch=0, x=None, q=None, sf=None, sft=None) == OK
+    assert schulz(lib, batch=0, g=None, out=None, ws=None, bytes=0) == OK
+
+
 def test_newton_schulz_tiles_and_steps(lib):
     """The finished tiles of a call are counted in 31 bits: 6 a step and tile of 256 x 64."""
     one = dict(batch=4096, rows=1, cols=2 ** 20, ldg=2 ** 20, gb=2 ** 20, ldo=2 ** 20, ob=2 ** 20, ws=128, bytes=2 ** 50)
