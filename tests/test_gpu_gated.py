@@ -396,3 +396,31 @@ def test_more_narrow_tiles_than_pairs():
         r = slice(128 * j, 128 * j + 128)
         dg.dg_fp8_gated_gemm_nn_backward(dy[r], sfdy[:, r].contiguous(), w2[j], sfw2[j], gu[r], want, h=want_h)
         assert torch.equal(dgu[r], want) and torch.equal(h[r], want_h), j
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 elements of gate and up: rows at both ends and past 2^31 elements have the bits of a
+    small call."""
+    m, i, k = 263168, 8192, 128
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def codes(*s):
+        return torch.randn(*s, generator=g, device="cuda").to(torch.float8_e4m3fn)
+
+    def words(*s):
+        return torch.randint(124, 130, (*s, 4), generator=g, device="cuda", dtype=torch.uint8).view(torch.int32).view(*s)
+    x, sfx, w1, sf1, w2, sf2 = codes(m, k), words(1, m), codes(2 * i, k), words(1, 2 * i), codes(k, i), words(1, i)
+    bf16 = dict(dtype=torch.bfloat16, device="cuda")
+    gu, h = torch.empty(m, 2 * i, **bf16), torch.empty(m, i, **bf16)
+    small, small_h = torch.empty(256, 2 * i, **bf16), torch.empty(256, i, **bf16)
+    assert gu.numel() > 2 ** 32
+    rows = [slice(r, r + 256) for r in (0, 131072, m - 256)]
+    dg.dg_fp8_gated_gemm_nt(x, sfx, w1, sf1, h=h, gu=gu)
+    for r in rows:
+        dg.dg_fp8_gated_gemm_nt(x[r], sfx[:, r].contiguous(), w1, sf1, h=small_h, gu=small)
+        assert torch.equal(small, gu[r]) and torch.equal(small_h, h[r]), r
+    kept = [gu[r].clone() for r in rows]
+    dg.dg_fp8_gated_gemm_nn_backward(x, sfx, w2, sf2, gu, gu, h=h)
+    for r, before in zip(rows, kept):
+        dg.dg_fp8_gated_gemm_nn_backward(x[r], sfx[:, r].contiguous(), w2, sf2, before, small, h=small_h)
+        assert torch.equal(small, gu[r]) and torch.equal(small_h, h[r]), r
