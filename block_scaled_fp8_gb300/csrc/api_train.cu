@@ -388,10 +388,10 @@ dg_status dg_newton_schulz(const void *g, int g_fmt, int64_t ldg, int64_t g_batc
     p.status = status_dev;
     p.timeout_ns = host_timeout_ns();
     p.debug_flags = host_take_debug_flags();
-    int launches = 0;
+    int config[4] = {};
     const cudaError_t e = launch_newton_schulz(p, steps, g_fmt == DG_VALUES_BF16, sms, static_cast<cudaStream_t>(stream),
-                                               &launches);
-    host_set_last_config(256, 256, 0, 0, 6, launches);
+                                               config);
+    host_set_last_config(256, config[0], config[1], config[2], 6, config[3]);
     return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 

@@ -46,6 +46,16 @@ constexpr int kSlotBytes = 2 * kBoxBytes;
 constexpr int kEpiBytes = kEpiWarps * 2 * kSlotBytes;
 constexpr int kSmem = 1024 + kRingBytes + kEpiBytes + 128 * kEpiWarps + 512;
 
+// A stage: A's 16 KB, then B's largest part.
+__host__ __device__ constexpr int ring_stage_bytes(int bn_sym, int bn_update) {
+    const int b_sym = bn_sym * 64, b_update = bn_update == kTile ? 16384 : 8192;
+    return 16384 + (b_sym > b_update ? b_sym : b_update);
+}
+__host__ __device__ constexpr int ring_stages(int bn_sym, int bn_update) {
+    const int n = kRingBytes / ring_stage_bytes(bn_sym, bn_update);
+    return n < kMaxStages ? n : kMaxStages;
+}
+
 // ------------------------------------------------------------------ norm and split
 
 template <bool BF16>
@@ -701,10 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    // a stage: A's 16 KB, then B's largest part
-    const int b_sym = p.bn_sym * 64, b_update = p.bn_update == kTile ? 16384 : 8192;
-    const int stage_bytes = 16384 + (b_sym > b_update ? b_sym : b_update);
-    const int stages = kRingBytes / stage_bytes < kMaxStages ? kRingBytes / stage_bytes : kMaxStages;
+    const int stage_bytes = ring_stage_bytes(p.bn_sym, p.bn_update), stages = ring_stages(p.bn_sym, p.bn_update);
     uint8_t *smem_epi = smem + kRingBytes;
     float *diag_out = reinterpret_cast<float *>(smem_epi + kEpiBytes);   // 32 an epilogue warp
     uint64_t *bars = reinterpret_cast<uint64_t *>(diag_out + 32 * kEpiWarps);
@@ -1083,7 +1090,7 @@ int64_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
     return batch * (2 * lo * (3 * up(hi, 64) + 2 * up(lo, 64)) + 8 * kMaxPartial + 8 * up(lo, 32)) + 128;
 }
 
-cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, cudaStream_t stream, int *launches) {
+cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, cudaStream_t stream, int (&config)[4]) {
     p.lo = p.rows < p.cols ? p.rows : p.cols;
     p.hi = p.rows < p.cols ? p.cols : p.rows;
     p.ldx = up(p.hi, 64);
@@ -1117,7 +1124,6 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
         e = launch_simple(bf16 ? dg_ns_split_kernel<true, false> : dg_ns_split_kernel<false, false>,
                           dim3((p.cols + 2047) / 2048, (p.rows + 7) / 8, p.batch), p, stream);
     if (e != cudaSuccess) return e;
-    *launches = 3;
     // operands: X along K (Gram), X as [K][N], A and B; epilogue boxes of the planes, A, B and the output
     const int pairs = max_pairs(num_sms);
     if (pairs <= 0) return cudaErrorInvalidConfiguration;
@@ -1153,6 +1159,10 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
     attr[0].id = cudaLaunchAttributeCooperative;   // the CTAs wait for one another
     attr[0].val.cooperative = 1;
     cfg.gridDim = dim3(2 * static_cast<int>(tiles < pairs ? tiles : pairs));
+    config[0] = p.bn_update;
+    config[1] = ring_stages(p.bn_sym, p.bn_update);
+    config[2] = static_cast<int>(cfg.gridDim.x);
+    config[3] = 3;
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;

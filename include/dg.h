@@ -690,7 +690,7 @@ const char *dg_status_string(int status);
 
 /* Tile configuration the last GEMM call on this thread launched:
  * out[0]=BLOCK_M, out[1]=BLOCK_N (kinds 3 and 5: rows of the narrow operand in
- * shared memory), out[2]=stages, out[3]=grid size,
+ * shared memory; kind 6: of the products with X), out[2]=stages, out[3]=grid size,
  * out[4]=kernel kind (0 block-scaled, 1 FP32-promotion, 2 block-scaled on
  * CTA pairs, 3 few-row product, 5 MoE layer for few tokens, 6 Newton-Schulz products), out[5]=number of
  * kernel launches of that call. */

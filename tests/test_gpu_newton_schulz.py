@@ -264,3 +264,13 @@ def test_norm_and_eps_of_any_magnitude(scale):
         close(out, plain(g, steps=1, eps=eps), what=f"{scale} {ratio}")
     dg.dg_newton_schulz(g.cuda(), out, steps=1, eps=float("inf"))
     assert not bool(out.any())
+
+
+def test_last_config():
+    """The products' tiles and grid as they were chosen."""
+    for (b, r, c), (bn, stages, grid) in (((1, 64, 64), (64, 6, 2)), ((1, 250, 1000), (64, 6, 32)), ((4, 4096, 1024), (256, 5, None))):
+        g = torch.randn(b, r, c, device="cuda")
+        dg.dg_newton_schulz(g, torch.empty(b, r, c, dtype=torch.bfloat16, device="cuda"), steps=1)
+        v = dg.last_config()
+        assert (v["block_m"], v["block_n"], v["stages"], v["launches"]) == (256, bn, stages, 3)
+        assert v["grid"] == (grid or torch.cuda.get_device_properties(0).multi_processor_count)
