@@ -8,7 +8,7 @@
 // so a row's amax is 4 shuffles, and a thread's rows are 16 apart, so a column's amax is a maximum
 // over the thread's own rows, one shuffle, and one pass through shared memory.  Each value is read
 // once whatever is written.  For rows alone a tile is 16 rows x 128 or 512 columns.
-// Measured, bf16 8192x7168 both ways: 36.6 us, 6.4 TB/s of the 236 MB, with 55 % of the issue slots in
+// Measured, bf16 8192x7168 both ways: 36.6 us, 6.4 TB/s of the 236 MB, with 57 % of the issue slots in
 // use (49 us with twice the instructions, before maxima and products went two values at a time);
 // blocks of 8 FP32 matrices 4096x7168: 165 us, 7.1 TB/s; rows of 96x7168: 5.2 us, a launch.
 #include <cuda_bf16.h>
