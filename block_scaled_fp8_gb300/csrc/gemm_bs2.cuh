@@ -613,11 +613,11 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
     constexpr int ACC = Cfg::kAccCols;
 
     // gated forward: two tiles' scales (0: zeros) of the rows' parts, a part for each of the warps and
-    // pairs that share a group, and the quadrants' barriers
+    // pairs that share a group, and two tiles' barriers of the quadrants
     constexpr int kParts = kBs2Cluster<BN, LAY>;
     __shared__ uint8_t s_scale[(LAY & kLayGated) ? 2 * kParts * 128 : 1];
     static_assert(!(LAY & kLayGated) || Cfg::kSmemBytes + 2 * kParts * 128 + 64 <= Cfg::kSmemLimit, "static shared memory");
-    __shared__ uint64_t s_xbar[(LAY & kLayGated) ? 4 : 1];
+    __shared__ uint64_t s_xbar[(LAY & kLayGated) ? 8 : 1];
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
             mbar_init(b, b >= tempty_bar && b < tempty_bar + NUM_ACC ? 2 * Cfg::kEpiWarps : 1);
         }
         if constexpr ((LAY & kLayGated) != 0)
-            if (lane < 4) mbar_init(&s_xbar[lane], CL);
+            if (lane < 8) mbar_init(&s_xbar[lane], CL);
         if (lane == 0) *abort_flag = 0;
         fence_mbar_init();
     }
@@ -1219,7 +1219,7 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                 }
             }
         };
-        uint32_t xphase = 0;   // gated forward: the exchange of the halves' amax
+        uint32_t xtile = 0;   // gated forward: tiles whose scales were exchanged
         PairTile tile;
         if (pair_id < num_tiles) {
             get_pair_tile<BN, MP, LAY>(p, prefix, pinfo, num_units, psf_k, pair_id, rank, tile);
@@ -1491,16 +1491,21 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                 if (p.hq != nullptr) {
                     // a row's group of 128 columns is this thread's BN/4 and those of the other warp
                     // of the quadrant, here and in the cluster's other pairs: its scale is the largest of
-                    // theirs, which meet in each CTA's shared memory, in slots that alternate by tile, so
-                    // that one arrival a warp and tile is enough
-                    const uint32_t row_at = xphase * (kParts * 128u) + quad * 32u + lane;
+                    // theirs, which meet in each CTA's shared memory.  Slots and barriers alternate by tile, so
+                    // that one arrival a warp and tile is enough: a warp arrives for tile t + 2 once its own
+                    // CTA's barrier of t + 1 is complete, and so once every CTA has passed tile t.  (Slots
+                    // alone are not enough: a warp's arrivals at the CTAs are not ordered with another's, so
+                    // that on one barrier its arrival for t + 1 could stand in for a slower warp's for t.)
+                    const uint32_t xslot = xtile & 1u, xparity = (xtile >> 1) & 1u;
+                    uint64_t *const xbar = &s_xbar[4 * xslot + quad];
+                    const uint32_t row_at = xslot * (kParts * 128u) + quad * 32u + lane;
                     const uint32_t mine = amax == 0u ? 0u : ue8m0_of_amax(amax);
                     uint32_t larger = mine;
                     if constexpr (CL == 2) {
                         s_scale[row_at + half * 128u] = static_cast<uint8_t>(mine);
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&s_xbar[quad]);
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s_xbar[quad], xphase, ctl, DG_DEV_TIMEOUT))) break;
+                        if (lane == 0) mbar_arrive(xbar);
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(xbar, xparity, ctl, DG_DEV_TIMEOUT))) break;
                     } else {
                         const uint32_t part = smem_u32(s_scale + row_at + ((pair_base >> 1) * 2u + half) * 128u);
 #pragma unroll
@@ -1508,15 +1513,15 @@ __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims
                             st_cluster_u8(mapa_shared(part, 2u * q + static_cast<uint32_t>(rank)), mine);
                         __syncwarp();
                         if (lane < CL / 2)
-                            mbar_arrive_cluster(mapa_shared(smem_u32(&s_xbar[quad]), 2u * lane + static_cast<uint32_t>(rank)));
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&s_xbar[quad], xphase, ctl, DG_DEV_TIMEOUT))) break;
+                            mbar_arrive_cluster(mapa_shared(smem_u32(xbar), 2u * lane + static_cast<uint32_t>(rank)));
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(xbar, xparity, ctl, DG_DEV_TIMEOUT))) break;
                     }
 #pragma unroll
                     for (int q = 0; q < kParts; ++q) {
                         const uint32_t b = s_scale[row_at + q * 128u];
                         larger = b > larger ? b : larger;
                     }
-                    xphase ^= 1u;
+                    ++xtile;
                     const uint32_t byte = larger == 0u ? 127u : larger;
                     const float inv = inv_scale(byte);
                     const int row = tile.d_row0 + row_off + static_cast<int>(lane);
