@@ -96,10 +96,10 @@ __global__ void __launch_bounds__(256) dg_ns_norm_kernel(const __grid_constant__
                 sum = fmaf(v, v, sum);
                 amax = fmaxf(amax, fabsf(v));
             };
-            int i = threadIdx.x;
+            // (V values a thread in their order, whether the address allows a load of 16 bytes or not)
             if (vec) {
 #pragma unroll 8
-                for (; i < n / V; i += 256) {
+                for (int i = threadIdx.x; i < n / V; i += 256) {
                     const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(at) + i);
                     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -112,9 +112,13 @@ __global__ void __launch_bounds__(256) dg_ns_norm_kernel(const __grid_constant__
                         }
                     }
                 }
-                i = n / V * V + threadIdx.x;
+            } else {
+#pragma unroll 4
+                for (int i = threadIdx.x; i < n / V; i += 256)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) add(g_value<BF16>(at, i * V + j));
             }
-            for (; i < n; i += 256) add(g_value<BF16>(at, i));
+            for (int i = n / V * V + threadIdx.x; i < n; i += 256) add(g_value<BF16>(at, i));
         };
         segment(1.0f);
         if (amax > 0x1p40f) {
