@@ -17,8 +17,14 @@
 // normal down to 2^-26.  X itself is kept as two FP16 planes, high and low (22 bits): the high plane
 // is the operand, and a X + B X is formed from both.  With X rounded to 11 bits in each step its
 // error is multiplied by a = 3.4 a step in every direction that G hardly has, and comes to 4e-2 of
-// the result for a gradient with a decaying spectrum; with the low plane it is 1e-3 or less
-// (bf16's own rounding of the result: 1.7e-3).  Sums are FP32, the norm's partial sums FP64.
+// the result for a gradient with a decaying spectrum; with the low plane it is 1e-3 or less where the
+// short side is 250 or more (bf16's own rounding of the result: 1.7e-3).  B times what the high plane leaves
+// out of X, strong directions mixed into weak ones, falls with the square root of the short side, so that
+// small matrices need it: up to a short side of 192 the update's product takes the low plane too, twice its
+// K-blocks (error with 8 strong directions, 64x64: 3.4e-3 without, 7e-4 with; 200x200: 1.1e-3 without; singular
+// values over four decades, 4x4: 2.2e-2 and 1.5e-3.  64x64: 63.3 us without, 64.0 with; 700x40x64: 287 and
+// 292; 128x2048: 103 and 105; 250x1000, which goes without: 93 and 97).
+// Sums are FP32, the norm's partial sums FP64.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -355,10 +361,22 @@ __device__ __forceinline__ float2 half2_values(uint32_t w) {
 // product run beside the many of an update (choose_tiles).
 struct NsMaps {
     CUtensorMap xk[2], xn[2];   // X's high planes along K (128 rows a box), and as [K][N]
+    CUtensorMap xln;            // the low plane as [K][N]
     CUtensorMap a, b;           // A, B along K
     CUtensorMap xkb[2], ab;     // X and A as the second operand of a symmetric product: bn_sym / 2 rows a box
     CUtensorMap xh[2], xl, ea, eb, out;   // boxes of the epilogue
 };
+
+// Short side up to which an update's product goes over both planes of X.  (Its tiles have one row then: the pair
+// that computes a tile is the only one that reads these columns of the low plane, which its epilogue replaces.)
+constexpr int kLowPlaneSide = 192;
+static_assert(kLowPlaneSide <= kTile, "the low plane is read and replaced by the same pair");
+
+// K-blocks of a product.
+__host__ __device__ inline int ns_kblocks(int mode, int lo, int hi) {
+    const int n = ((mode == kNsGram ? hi : lo) + kKBlock - 1) / kKBlock;
+    return mode >= kNsUpdate && lo <= kLowPlaneSide ? 2 * n : n;
+}
 
 // What a phase works on.
 struct NsPhase {
@@ -383,7 +401,7 @@ __device__ __forceinline__ NsPhase ns_shape(const NsParams &p, int i, int g) {
     f.per = sym ? r * (q * (q + 1) / 2) + (f.tn - r * q) * (q + 1) : f.tm * f.tn;
     f.b0 = g == 0 ? 0 : p.group0;
     f.num_tiles = i < 0 || i >= 3 * p.steps ? 0 : f.per * (g == 0 ? p.group0 : p.batch - p.group0);
-    f.nkb = ((f.mode == kNsGram ? p.hi : p.lo) + kKBlock - 1) / kKBlock;
+    f.nkb = ns_kblocks(f.mode, p.lo, p.hi);
     return f;
 }
 
@@ -786,6 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                     : f.mode == kNsPoly ? &maps.ab
                                                         : &maps.xn[f.step & 1];
             const bool b_mn = f.mode >= kNsUpdate;
+            const int plane = b_mn ? ns_kblocks(kNsPoly, p.lo, p.hi) : f.nkb;   // K-blocks of X's high plane
             // this CTA's half of the columns: bn / 2 rows of 64 K, or boxes of 64 columns (one swizzle
             // atom, of which the MMA reads bn / 2 where that is less) x 64 K rows
             const uint32_t stage = 16384u + (b_mn ? (f.bn == kTile ? 16384u : 8192u) : static_cast<uint32_t>(f.bn) * 64u);
@@ -800,14 +819,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         if (elect_one()) {
                             const uint32_t fb = leader_full + slot * 8;
                             uint8_t *sa = smem + slot * stage_bytes, *sb = sa + 16384;
-                            const int n = n0 + rank * (f.bn / 2);
+                            const int n = n0 + rank * (f.bn / 2), k = (kb < plane ? kb : kb - plane) * kKBlock;
                             if (leader) mbar_arrive_expect_tx(&full_bar[slot], 2 * stage);
-                            tma_load_3d_pair(sa, ta, fb, kb * kKBlock, m0 + rank * 128, b);
+                            tma_load_3d_pair(sa, ta, fb, k, m0 + rank * 128, b);
                             if (b_mn) {
-                                tma_load_3d_pair(sb, tb, fb, n, kb * kKBlock, b);
-                                if (f.bn == kTile) tma_load_3d_pair(sb + 8192, tb, fb, n + 64, kb * kKBlock, b);
+                                const CUtensorMap *tp = kb < plane ? tb : &maps.xln;
+                                tma_load_3d_pair(sb, tp, fb, n, k, b);
+                                if (f.bn == kTile) tma_load_3d_pair(sb + 8192, tp, fb, n + 64, k, b);
                             } else {
-                                tma_load_3d_pair(sb, tb, fb, kb * kKBlock, n, b);
+                                tma_load_3d_pair(sb, tb, fb, k, n, b);
                             }
                         }
                         __syncwarp();
@@ -990,7 +1010,7 @@ int choose_bn(const NsParams &p, bool sym, int pairs) {
     for (int bn : {256, 128, 64}) {
         const int64_t n = count_tiles(p, sym, bn) * p.batch;
         // (symmetric: the mean of the products along the long side and the short)
-        const int64_t nkb = sym ? (up(p.hi, kKBlock) + up(p.lo, kKBlock)) / kKBlock / 2 + 1 : up(p.lo, kKBlock) / kKBlock;
+        const int64_t nkb = sym ? (up(p.hi, kKBlock) + up(p.lo, kKBlock)) / kKBlock / 2 + 1 : ns_kblocks(kNsUpdate, p.lo, p.hi);
         const double t = static_cast<double>((n + pairs - 1) / pairs) * nkb * (16384 + 64 * bn) / 55.0 +
                          1500.0 * (bn / 64);
         if (bn == 256 || t < 0.95 * least) {
@@ -1014,7 +1034,7 @@ double model_time(const NsParams &p, int steps, int bn_sym, int bn_update, int g
     int64_t tiles[3];
     for (int m = 0; m < 3; ++m) {
         const int bn = m < kNsUpdate ? bn_sym : bn_update;
-        const int64_t nkb = up(m == kNsGram ? p.hi : p.lo, kKBlock) / kKBlock;
+        const int64_t nkb = ns_kblocks(m, p.lo, p.hi);
         const float epilogue = 0.79f * (bn / 64), loads = nkb * (16384 + 64 * bn) / 104500.0f;
         cost[m] = loads > epilogue ? loads : epilogue;
         tail[m] = 3.3f + epilogue - 0.79f;
@@ -1145,6 +1165,7 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
               encode_plane(&maps.xkb[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, p.bn_sym / 2) &&
               encode_plane(&maps.xh[i], p.xh[i], p.hi, p.lo, p.ldx, px, p.batch, 32, true);
     ok &= encode_plane(&maps.xl, p.xl, p.hi, p.lo, p.ldx, px, p.batch, 32, true) &&
+          encode_plane(&maps.xln, p.xl, p.hi, p.lo, p.ldx, px, p.batch, kKBlock) &&
           encode_plane(&maps.a, p.a, p.lo, p.lo, p.lda, pa, p.batch, 128) &&
           encode_plane(&maps.ab, p.a, p.lo, p.lo, p.lda, pa, p.batch, p.bn_sym / 2) &&
           encode_plane(&maps.b, p.b, p.lo, p.lo, p.lda, pa, p.batch, 128) &&

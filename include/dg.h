@@ -634,8 +634,9 @@ dg_status dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(const void *dy, int
  *   1 <= steps <= 1000; a, b, c the polynomial (3.4445, -4.7750, 2.0315 brings singular values from
  *         above 0.003 to 0.7 .. 1.2 in five steps); eps >= 0.  A polynomial or a G that
  *         makes an element of X or A or of b A + c A A 16 or more gives infinities or NaN.
- *   The operands of the products are rounded to 11 bits, X itself is kept to 22; sums are FP32.  The result
- *   differs from the definition's by about 1e-3 of its RMS before its rounding to bf16.
+ *   The operands of the products are rounded to 11 bits, X itself is kept to 22; sums are FP32.  Before its
+ *   rounding to bf16 the result differs from the definition's by at most about 1e-3 of its RMS where the short
+ *   side is 250 or more, 1.5e-3 from 24 on, 5e-3 below (five steps of the coefficients above).
  *   A zero matrix gives zeros; a NaN or infinite value makes its matrix NaN, no other.
  *   A matrix's result does not depend on the others, nor on batch.
  *   No alignment beyond the elements' own; rows, cols <= 2^20 and rows * cols <= 2^31, batch <=
