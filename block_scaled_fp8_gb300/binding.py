@@ -501,13 +501,15 @@ def _fail(fn: str, status: int):
 
 _kept = threading.local()   # .workspaces: {(device, stream): buffer}
 _MAX_KEPT = 8
+_MAX_KEPT_BYTES = 128 << 20   # of one buffer: 64 tokens, 16 of 1024 experts, 7168 x 2048 take 120 MB
 
 
 def _workspace(nbytes: int, t, stream):
     """Device memory for a call whose caller gave none.  On the current stream: a buffer kept
     for this stream by this host thread (calls there run one after another), as long as the thread
-    lives and uses no more than _MAX_KEPT streams after it.  In a graph capture:
-    one of its own, which the allocator keeps from other use as long as the capture needs it.
+    lives and uses no more than _MAX_KEPT streams after it; of more than _MAX_KEPT_BYTES, one that goes back
+    to the allocator with the call (which gives it to nothing but later work on this stream).  In a graph
+    capture: one of its own, which the allocator keeps from other use as long as the capture needs it.
     On a stream that the caller names: the same there, so that the call waits for nothing on the
     current stream."""
     if stream is not None:
@@ -515,7 +517,7 @@ def _workspace(nbytes: int, t, stream):
             stream = torch.cuda.ExternalStream(stream.cuda_stream, device=t.device)
         with torch.cuda.stream(stream):
             return _workspace(nbytes, t, None)
-    if torch._C._cuda_isCurrentStreamCapturing():
+    if nbytes > _MAX_KEPT_BYTES or torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
     i = t.get_device()
     key = (i, torch._C._cuda_getCurrentRawStream(i))
