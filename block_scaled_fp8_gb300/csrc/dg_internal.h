@@ -177,8 +177,13 @@ struct NsParams {
     int dense;              // a matrix's rows of G follow one another
 };
 int64_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
-// config: columns of the update's tiles, ring stages, grid of the products, launches
-cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, cudaStream_t stream, int (&config)[4]);
+// What a call chose.
+struct NsConfig {
+    int bn_sym, bn_update;   // columns of the products' tiles
+    int stages, grid, launches;
+    int group0;              // matrices of the first group
+};
+cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, cudaStream_t stream, NsConfig *config);
 
 // Host state and helpers of api.cu that the few-row entry points (api_few.cu) share.
 typedef CUresult (*TensorMapEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,

@@ -1114,7 +1114,7 @@ int64_t ns_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
     return batch * (2 * lo * (3 * up(hi, 64) + 2 * up(lo, 64)) + 8 * kMaxPartial + 8 * up(lo, 32)) + 128;
 }
 
-cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, cudaStream_t stream, int (&config)[4]) {
+cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, cudaStream_t stream, NsConfig *config) {
     p.lo = p.rows < p.cols ? p.rows : p.cols;
     p.hi = p.rows < p.cols ? p.cols : p.rows;
     p.ldx = up(p.hi, 64);
@@ -1184,10 +1184,7 @@ cudaError_t launch_newton_schulz(NsParams p, int steps, bool bf16, int num_sms, 
     attr[0].id = cudaLaunchAttributeCooperative;   // the CTAs wait for one another
     attr[0].val.cooperative = 1;
     cfg.gridDim = dim3(2 * static_cast<int>(tiles < pairs ? tiles : pairs));
-    config[0] = p.bn_update;
-    config[1] = ring_stages(p.bn_sym, p.bn_update);
-    config[2] = static_cast<int>(cfg.gridDim.x);
-    config[3] = 3;
+    *config = {p.bn_sym, p.bn_update, ring_stages(p.bn_sym, p.bn_update), static_cast<int>(cfg.gridDim.x), 3, p.group0};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
