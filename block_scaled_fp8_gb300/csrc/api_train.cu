@@ -388,11 +388,11 @@ dg_status dg_newton_schulz(const void *g, int g_fmt, int64_t ldg, int64_t g_batc
     p.status = status_dev;
     p.timeout_ns = host_timeout_ns();
     p.debug_flags = host_take_debug_flags();
-    NsConfig v = {};
+    NsConfig v;
     const cudaError_t e = launch_newton_schulz(p, steps, g_fmt == DG_VALUES_BF16, sms, static_cast<cudaStream_t>(stream),
                                                &v);
-    host_set_last_config(256, v.bn_update, v.stages, v.grid, 6, v.launches);
     if (e != cudaSuccess) return DG_ERR_CUDA;
+    host_set_last_config(256, v.bn_update, v.stages, v.grid, 6, v.launches);
     if ((p.debug_flags & DG_DEBUG_PRINT_CONFIGS) || std::getenv("DG_PRINT_CONFIGS"))
         std::fprintf(stderr,
                      "[dg] newton-schulz batch=%d rows=%d cols=%d -> BLOCK_M=256 BLOCK_N=%d (symmetric) %d (update) "
