@@ -483,7 +483,7 @@ __device__ __forceinline__ void get_pair_tile(const GemmParams &p, const int *pr
     if constexpr ((LAY & kLayGated) != 0) {
         // the leader's half of B: gate rows of the expert; the peer's: its up rows
         tile.b_row0 = (2 * group + rank) * p.n + tile.n0;
-        tile.sfb_y0 = group * ((LAY & 4) ? p.num_k_blocks : psf_k);
+        tile.sfb_y0 = group * psf_k;
         tile.d_row0 = tile.a_row0;
         return;
     }
@@ -502,14 +502,6 @@ __device__ __forceinline__ void get_pair_tile(const GemmParams &p, const int *pr
     if (p.mode != kModeKGrouped) tile.d_row0 = tile.a_row0;
 }
 
-// LAY: operand layouts, bit 0 = A MN-major (stored [K][M]), bit 1 = B MN-major
-// (stored [K][N]), bit 2 = B is FP4 (E2M1, K-major, one scale per 32 K); 0 is
-// the NT layout (both K-major FP8).  An MN-major operand's
-// stage is a TMA box of 128 MN-bytes x 128 K-rows with 128-byte swizzle: one
-// swizzle atom along MN (MP=256; an MN-major B half of BN/2 <= 128 columns,
-// the rest of the atom unread), 8-row groups 1024 bytes apart, and a 32-K step
-// of the MMA 4096 bytes on; the instruction descriptor's transpose bits (15:
-// A, 16: B) select the layout.
 // Two chunks of 16 FP32 values as 32 bf16, and two values as one word.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
@@ -591,6 +583,16 @@ __device__ __forceinline__ void gated_gradient(uint64_t dh, uint32_t gw, uint32_
     h = pack_bf16(mul2(silu, u));
 }
 
+// LAY: operand layouts, bit 0 = A MN-major (stored [K][M]), bit 1 = B MN-major
+// (stored [K][N]), bit 2 = B is FP4 (E2M1, K-major, one scale per 32 K), bit 3 =
+// A and B with a scale per 32 K (K-grouped); 0 is the NT layout (both K-major FP8).
+// kLayGated (16): NT, B an expert's gate rows and up rows, D the activation's
+// product; kLayGatedBwd (32, with bit 1): NN, D the gradient of gate and up.  An MN-major operand's
+// stage is a TMA box of 128 MN-bytes x 128 K-rows with 128-byte swizzle: one
+// swizzle atom along MN (MP=256; an MN-major B half of BN/2 <= 128 columns,
+// the rest of the atom unread), 8-row groups 1024 bytes apart, and a 32-K step
+// of the MMA 4096 bytes on; the instruction descriptor's transpose bits (15:
+// A, 16: B) select the layout.
 template <int BN, bool WITH_C, int MP, bool F32 = false, int LAY = 0>
 __global__ void __launch_bounds__(Bs2Config<BN, MP>::kThreads, 1) __cluster_dims__(kBs2Cluster<BN, LAY>, 1, 1)
     dg_bs2_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
