@@ -502,7 +502,7 @@ static PyObject *newton_schulz(PyObject *self, PyObject *const *arg, Py_ssize_t 
     Matrix g, out;
     PyObject *hold = NULL;
     void *ws, *status, *stream;
-    int64_t lead, r, c, batch, steps, need, ws_bytes;
+    int64_t lead, r, c, lo, hi, batch, steps, need, ws_bytes;
     double coef[4];
     int f32, j;
     dg_status st;
@@ -516,7 +516,12 @@ static PyObject *newton_schulz(PyObject *self, PyObject *const *arg, Py_ssize_t 
     batch = lead < 0 ? 1 : lead;
     CHECK(status_of(arg[8], &status));
     need = ((SchulzBytesFn)fns[SCHULZ_BYTES])((int)batch, (int)r, (int)c);
-    if (steps < 1 || steps > 1000 || !(coef[3] >= 0)) need = -1;   /* (refused) */
+    lo = r < c ? r : c;
+    hi = r < c ? c : r;
+    /* (refused; the last: more tiles than the kernels count) */
+    if (steps < 1 || steps > 1000 || !(coef[3] >= 0) ||
+        (need >= 0 && 6 * steps * batch * ((lo + 255) / 256) * ((hi + 63) / 64) > INT32_MAX))
+        need = -1;
     PyObject *const on_device[] = {arg[0], arg[1], arg[8]};
     CHECK(device_side(on_device, 3, arg[7], need, arg[0], arg[9], &hold, &ws, &ws_bytes, &stream));
     Py_BEGIN_ALLOW_THREADS
