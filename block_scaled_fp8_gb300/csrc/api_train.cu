@@ -62,6 +62,9 @@ int gated_clusters(int bn, bool backward, int num_sms) {
 // with ring slots of two K-blocks).  Backward: a K-block of B is loaded whole whatever the tile's
 // columns, so 128 only where all its tiles run at once, with half the epilogue (515 rows, inner 1360,
 // k 2048: 12.2 us against 16.8 with 256; 1 row, inner 2048, k 7168: 18.3 against 23.8).
+// units: grouped, the least there can be, as if every block of 128 rows had another of its expert beside it (where
+// the experts' rows lie is known to the device alone).  Experts of a single block make up to twice as many, and a
+// call with tiles chosen for one wave then takes two.
 int gated_block_n(bool backward, int64_t units, int inner, int num_sms) {
     if (backward) {
         const int64_t tiles = units * cdiv(inner, 128);

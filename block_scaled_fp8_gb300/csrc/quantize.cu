@@ -33,7 +33,7 @@ __device__ __forceinline__ void load8(const QuantParams &p, const char *at, int 
         const uint4 *q = reinterpret_cast<const uint4 *>(at);
 #pragma unroll
         for (int i = 0; i < kWords<BF16> / 4; ++i) {
-            const uint4 x = __ldcg(q + i);   // (read once; past L1, which a kernel before may have filled)
+            const uint4 x = __ldcg(q + i);   // (read once, so past L1)
             w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
         }
     } else {

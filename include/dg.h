@@ -645,7 +645,8 @@ dg_status dg_m_grouped_fp8_gated_gemm_nn_backward_contiguous(const void *dy, int
  *   workspace   device memory, 128-byte aligned, dg_newton_schulz_workspace_bytes(batch, rows,
  *         cols) bytes (-1 for sizes that the call refuses); needs no initialisation and
  *         does not outlive the call.  Calls that may run at the same time need one each.
- *   Three launches, the last a cooperative one over as many SMs as the products have tiles for; its
+ *   Three launches, the last a cooperative one over as many SMs as the products have tiles for, two at least
+ *   (dg_set_num_sms(1): DG_ERR_UNSUPPORTED, as for the gated calls); its
  *   CTAs wait for one product after another, each within the limit of dg_set_wait_timeout_ms.
  */
 int64_t dg_newton_schulz_workspace_bytes(int batch, int rows, int cols);
