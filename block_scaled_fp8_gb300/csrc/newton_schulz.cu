@@ -7,9 +7,10 @@
 // 256x256 tiles (or 128 or 64 columns where tiles are few), operands by TMA with 128-byte swizzle in
 // stages of 64 K, two accumulators in TMEM, so that a tile's epilogue runs beside the next tile's
 // MMAs.  Roles: warp 0 producer, warp 1 MMA issuer (leader), warps 2-9 epilogue.
-// Bound by: large matrices, the card's power limit (4x2048x7168: 1.41 ms in bursts of ten calls, 1.46
-// PFLOP/s of the products that are run, and 1.62 ms when repeated for long, at 1.55 GHz; the update's
-// planes, 470 MB a step, add 0.05 ms a step); small
+// Bound by: large matrices, the card's power limit (4x2048x7168: 1.42 ms in bursts of ten calls, 1.46
+// PFLOP/s of the products that are run, and 1.61 to 1.67 ms when repeated for long, at 1.45 GHz; the update's
+// planes, 470 MB a step, add 0.05 ms a step); middle ones, the pairs that a product's tiles leave idle
+// (2x2112x1536: a step's 42, 42 and 108 tiles on 76 pairs take 105 K-block times where an even share is 66); small
 // ones, the chain of a phase, 3.3 us and 0.2 us a K-block (64x64: 4 us a phase).
 //
 // Numbers: the operands are FP16 (11 bits) scaled by 2^12, which keeps the iteration's values
